@@ -69,7 +69,9 @@ typedef enum {
   FM_ERR_UNSUPPORTED = 2,  /* d not in {64,128}, N < 1, H % Hm != 0, ...           */
   FM_ERR_CUDA = 3,         /* a CUDA runtime call or kernel launch failed          */
   FM_ERR_TIMEOUT = 4,      /* a kernel wait gave up (see flashmask_check_status)   */
-  FM_ERR_WORKSPACE = 5     /* workspace null, misaligned or smaller than required  */
+  FM_ERR_WORKSPACE = 5,    /* workspace null, misaligned or smaller than required  */
+  FM_ERR_PAGE = 6          /* a page table entry, length or start on the device was
+                              out of range (see flashmask_check_status)            */
 } fm_status;
 
 /* Tile edge (rows and columns) of the classification. */
@@ -305,6 +307,124 @@ fm_status flashmask_localize(const fm_mask* mask, int B, int N, int row0, int ro
                              int32_t* lte, int32_t* uts, int32_t* ute, int32_t* inexact,
                              void* stream);
 
+/* ------------------------------------------------------------------ rotary positions
+ * Rotates the leading `rot_dim` elements of every head of Q and K by their
+ * token's position. They form n = rot_dim / 2 pairs, (i, i + n) in the half
+ * layout and (2i, 2i + 1) when `interleaved`; pair i of a token at position t
+ * turns by the angle a = t * freqs[i] and is multiplied by `mscale`:
+ *     (x, y) -> mscale * (x cos a - y sin a, y cos a + x sin a)
+ * and the other d - rot_dim elements are copied. `inverse` turns by -a instead:
+ * the map is linear, so the same call with inverse = 1 is its gradient (dX
+ * from dY), and with mscale = 1 it undoes the rotation.
+ *   t[0], t[1]  one or two tensors that share B, N, d, the positions and one
+ *               launch (Q and K, which may differ in heads); n_tensors 1 or 2.
+ *               x and y are [B, H, N, d] of `dtype` with strides in elements
+ *               for batch, head and token (the last dimension is contiguous),
+ *               so a slice of a fused projection is read in place. y may be x
+ *               with the same strides; otherwise they must not overlap, and the
+ *               rows of one y must not overlap each other.
+ *   positions   int32 [B, N] with `pos_stride` elements between batches (0:
+ *               one row for all), any value; NULL: token n sits at position n.
+ *   freqs       fp64 [rot_dim / 2], radians per position, on the device. Any
+ *               scaling for long contexts is in them and in mscale.
+ * The angle is taken in turns modulo one with 64-bit integers, so its error
+ * does not grow with the position; sums are fp32 and rounded once. A frequency
+ * that is not finite gives NaN. d >= 1, 0 <= rot_dim <= d and even; B * N <
+ * 2^31. B, N or H zero is FM_ERR_UNSUPPORTED. Asynchronous on `stream`; needs
+ * no workspace. */
+typedef enum { FM_BF16 = 0, FM_F16 = 1, FM_F32 = 2 } fm_dtype;
+typedef struct {
+  const void* x;
+  void* y;
+  int H;
+  int64_t xs[3]; /* strides of x: batch, head, token (elements) */
+  int64_t ys[3]; /* strides of y                                */
+} fm_heads;
+fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positions,
+                         int64_t pos_stride, const double* freqs, int B, int N, int d, int rot_dim,
+                         int interleaved, int dtype, float mscale, int inverse, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit paged cache
+ * Keys and values of running sequences as e4m3 codes in pages of FM_PAGE
+ * tokens, one scale for each page and head (the block scaling of the FP8
+ * forward, with its 128-row block cut to a page). All arrays are the caller's:
+ *   k8      e4m3 [pages, Hk, FM_PAGE, d]
+ *   v8      e4m3 [pages, Hk, d, FM_PAGE]  (transposed: the tokens of one column
+ *                                          lie together, as P V reads them)
+ *   kscale, vscale  fp32 [pages, Hk]      a value is its code times the scale
+ * page_table is int32 [B, max_pages]: entry i of a row is the page holding the
+ * sequence's tokens [64 i, 64 i + 64). Only the entries of pages that a call
+ * needs are read; the rest may hold anything. d in {64, 128}; FM_PAGE *
+ * max_pages <= FM_MAX_SEQLEN. Entries, lengths and starts live on the device:
+ * the kernels check each one they use, leave the access out when it is out of
+ * range and record it, so that flashmask_check_status() returns FM_ERR_PAGE
+ * (the outputs of that sequence are then undefined). */
+#define FM_PAGE 64
+typedef struct {
+  void* k8;
+  void* v8;
+  float* kscale;
+  float* vscale;
+  int pages, Hk, d;
+} fm_cache;
+
+/* Workspace of the two calls below for these sizes (H query heads, N new or
+ * query tokens a sequence); 0 for an unsupported shape. 256-byte aligned and
+ * zeroed before its first use, as at the top of this file; not to be shared by
+ * calls that may run at the same time. Its first 16 bytes are the status word. */
+size_t flashmask_cache_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages);
+
+/* Writes N new tokens of each sequence behind the start[b] it holds: K and V
+ * bf16 [B, Hk, N, d] with strides in elements for batch, head and token
+ * (multiples of 8; the last dimension contiguous, 16-byte aligned). count (int32
+ * [B], may be NULL: N) says how many of a sequence's N rows are real; the
+ * others are not read. Codes are rounded to nearest even.
+ *   Scales are powers of two: the smallest 2^k, k >= -100, with absmax <=
+ *   448 * 2^k over the tokens of the page and head. While a page fills, its
+ *   scale only grows; the codes already there are then rounded again to the
+ *   larger scale (exact unless they fall into e4m3's subnormal range). A page
+ *   whose first token is written here is begun: its old scales do not count
+ *   and the slots behind the last new token are set to zero. Slots behind the
+ *   last new token of a page begun earlier are left as they are.
+ *   A token with a value that is not finite, in K or in V of a head, does not
+ *   count for that head's scales and is stored so that every query that sees
+ *   it, and no other, gets NaN: its K codes are NaN, its V codes zero.
+ *   The pages written by one call must be distinct (a page shared by two
+ *   sequences is copied by the caller before either appends to it). A start
+ *   below 0 or a sequence that would outgrow max_pages is left alone and
+ *   recorded. Asynchronous on `stream`; uses only the status word of `ws`. */
+fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_table, int max_pages,
+                                 const void* k, const int64_t ks[3], const void* v,
+                                 const int64_t vs[3], const int32_t* start, const int32_t* count,
+                                 int B, int N, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of N query tokens of each sequence over its cached keys and values:
+ * one token while a sequence runs, several when drafted tokens are checked, a
+ * chunk of a prompt. lens (int32 [B]) is the number of cached tokens, the query
+ * tokens' own among them; q_lens (int32 [B], may be NULL: N) how many of the N
+ * rows are real. Row t of sequence b sits at position i = lens[b] - q_lens[b] +
+ * t; rows t >= q_lens[b] are neither read nor written. Key j < lens[b] is
+ * masked when
+ *     (causal && j > i) || (LTS[j] <= i < LTE[j]) || (UTS[j] <= i < UTE[j])
+ * with the vectors [B, Hm, max_pages * FM_PAGE] of `mask`, whose lts and lte
+ * may both be NULL too (no lower interval); mask NULL: causal, no intervals.
+ * Head h reads mask head h / (H / Hm) and cache head h / (H / Hk); H % Hk ==
+ * 0, H % Hm == 0. O, LSE and rows without a visible key are as at the top of
+ * this file: O bf16 [B, H, N, d], LSE fp32 [B, H, N] (contiguous).
+ * Keys and values count as their codes times their scales; scores, softmax
+ * statistics and sums are fp32. What masked keys, and codes behind a sequence's
+ * end, hold has no influence, NaN included. A query row with a value that is
+ * not finite gives NaN.
+ *   qs, os: strides of Q and O in elements for batch, head and token (multiples
+ *   of 8; the last dimension contiguous, 16-byte aligned).
+ * Results do not depend on the order in which CTAs run. Asynchronous on
+ * `stream`. */
+fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache* cache,
+                              const int32_t* page_table, int max_pages, const int32_t* lens,
+                              const int32_t* q_lens, const fm_mask* mask, int B, int H, int N,
+                              float scale, void* o, const int64_t os[3], float* lse, void* ws,
+                              size_t ws_bytes, void* stream);
+
 /* Self-test of the failure path (no counterpart in the pages). Launches `ctas`
  * (1..1024) one-warp CTAs whose mbarrier wait can never complete, bounded the
  * way every wait of the library is: CTA 0 gives up after `limit_ns` (1e6..2e9)
@@ -320,6 +440,7 @@ fm_status flashmask_selftest_timeout(void* ws, size_t ws_bytes, long long limit_
 
 /* Synchronises `stream`, then reads and clears the workspace status word.
  * Returns FM_ERR_TIMEOUT if a kernel wait gave up since the last check,
+ * FM_ERR_PAGE if a cache call met a page, length or start out of range,
  * FM_ERR_CUDA if the stream reports an error, FM_OK otherwise. If detail is
  * not NULL it receives the recorded failure site (0 if none). */
 fm_status flashmask_check_status(void* ws, void* stream, int* detail);

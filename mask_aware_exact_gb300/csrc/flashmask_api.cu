@@ -596,7 +596,7 @@ fm_status flashmask_check_status(void* ws, void* stream, int* detail) {
   if (h[0] == 0) return FM_OK;
   if (detail) *detail = h[1];
   if (cudaMemset(ws, 0, sizeof(h)) != cudaSuccess) return FM_ERR_CUDA;
-  return FM_ERR_TIMEOUT;
+  return h[0] == fm::kStatusPage ? FM_ERR_PAGE : FM_ERR_TIMEOUT;
 }
 
 const char* flashmask_status_string(fm_status s) {
@@ -607,6 +607,7 @@ const char* flashmask_status_string(fm_status s) {
     case FM_ERR_CUDA: return "CUDA error";
     case FM_ERR_TIMEOUT: return "a kernel wait timed out";
     case FM_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case FM_ERR_PAGE: return "a page, length or start of the cache was out of range";
   }
   return "unknown status";
 }

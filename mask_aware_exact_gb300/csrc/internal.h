@@ -9,9 +9,9 @@ namespace fm {
 constexpr int kTile = 128;
 
 // Device status word layout (int32[4] at the start of the workspace):
-//   [0] bit mask of failures (kStatusTimeout, kStatusLayout)
+//   [0] bit mask of failures (kStatusTimeout, kStatusLayout, kStatusPage)
 //   [1] first failure site (one of the Site codes below), 0 if none
-enum : int { kStatusTimeout = 1, kStatusLayout = 2 };
+enum : int { kStatusTimeout = 1, kStatusLayout = 2, kStatusPage = 4 };
 enum Site : int {
   kSiteNone = 0,
   kSiteFwdQ = 101, kSiteFwdK, kSiteFwdV, kSiteFwdS, kSiteFwdP, kSiteFwdO, kSiteFwdKEmpty,
@@ -19,6 +19,7 @@ enum Site : int {
   kSiteBwdKV = 201, kSiteBwdQ, kSiteBwdQEmpty, kSiteBwdS, kSiteBwdDP, kSiteBwdPT, kSiteBwdDS,
   kSiteBwdDV, kSiteBwdDQ, kSiteBwdDrained, kSiteBwdDone, kSiteBwdSmemAlign, kSiteBwdSplit,
   kSiteSelftest = 301,
+  kSiteAppendRange = 401, kSiteAppendPage, kSiteCacheLen, kSiteCachePage, kSiteCacheWait,
 };
 
 // Backward load balance: among the split_blocks(Tc) longest key blocks of

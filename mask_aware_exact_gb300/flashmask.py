@@ -9,6 +9,7 @@ binding still works but the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -21,7 +22,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflashmask.so")
 
 FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA, FM_ERR_TIMEOUT, FM_ERR_WORKSPACE = range(6)
+FM_ERR_PAGE = 6
 FM_TILE = 128
+FM_PAGE = 64
+FM_BF16, FM_F16, FM_F32 = range(3)
 FM_TILE_NONE, FM_TILE_PARTIAL, FM_TILE_FULL = 0, 1, 2
 
 
@@ -42,12 +46,24 @@ class FmFp8Layout(ctypes.Structure):
                 ("fwd_total", "q8", "k8", "vt8", "qscale", "kscale", "vscale", "total")]
 
 
+class _FmHeads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("xs", ctypes.c_int64 * 3), ("ys", ctypes.c_int64 * 3)]
+
+
+class _FmCache(ctypes.Structure):
+    _fields_ = [("k8", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("kscale", ctypes.c_void_p),
+                ("vscale", ctypes.c_void_p), ("pages", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int)]
+
+
 EXPORTED = ("flashmask_workspace_bytes", "flashmask_workspace_layout", "flashmask_classify",
             "flashmask_fwd", "flashmask_bwd", "flashmask_bwd_preprocess", "flashmask_bwd_main",
             "flashmask_bwd_finalize", "flashmask_fwd_noalloc", "flashmask_host_workspace_bytes",
             "flashmask_fwd_bwd_host", "flashmask_localize", "flashmask_selftest_timeout",
             "flashmask_fwd_fp8_workspace_bytes", "flashmask_fwd_fp8_layout", "flashmask_fwd_fp8",
-            "flashmask_check_status", "flashmask_status_string")
+            "flashmask_check_status", "flashmask_status_string", "flashmask_rope",
+            "flashmask_cache_workspace_bytes", "flashmask_cache_append", "flashmask_fwd_cache")
 
 _lib = None
 
@@ -103,6 +119,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.flashmask_check_status.restype = i
     L.flashmask_status_string.argtypes = [i]
     L.flashmask_status_string.restype = ctypes.c_char_p
+    i64, i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
+    L.flashmask_rope.argtypes = [ctypes.POINTER(_FmHeads), i, vp, i64, vp, i, i, i, i, i, i, f, i, vp]
+    L.flashmask_rope.restype = i
+    L.flashmask_cache_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    L.flashmask_cache_workspace_bytes.restype = sz
+    L.flashmask_cache_append.argtypes = [ctypes.POINTER(_FmCache), vp, i, vp, i64p, vp, i64p, vp, vp,
+                                         i, i, vp, sz, vp]
+    L.flashmask_cache_append.restype = i
+    L.flashmask_fwd_cache.argtypes = [vp, i64p, ctypes.POINTER(_FmCache), vp, i, vp, vp,
+                                      ctypes.POINTER(_FmMask), i, i, i, f, vp, i64p, vp, vp, sz, vp]
+    L.flashmask_fwd_cache.restype = i
     _lib = L
     return L
 
@@ -449,3 +476,260 @@ def flashmask_selftest_timeout(ws: torch.Tensor, limit_ns: int, ctas: int = 1, s
     """Queues the bounded-wait self-test (see include/flashmask.h)."""
     _check(load().flashmask_selftest_timeout(ws.data_ptr(), ws.numel(), int(limit_ns), int(ctas),
                                              _stream_ptr(stream)), "flashmask_selftest_timeout")
+
+
+# ---------------------------------------------------------------- rotary positions
+_ROPE_DTYPES = {torch.bfloat16: FM_BF16, torch.float16: FM_F16, torch.float32: FM_F32}
+_Strides = ctypes.c_int64 * 3
+
+
+@contextlib.contextmanager
+def _on(device, stream, *inputs):
+    """The raw stream to launch on: `stream`, or the current one of `device`. With
+    a stream of its own the call's outputs are allocated for that stream and its
+    inputs are kept until it has passed the call."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.device(device):
+                yield torch.cuda.current_stream(device).cuda_stream
+    else:
+        if stream.device != device:
+            raise ValueError("stream and tensors must be on the same device")
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _want(t, name, dtype, device, shape=None, contiguous=True):
+    if t.dtype != dtype or t.device != device or (shape is not None and t.shape != shape) or \
+            (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name} must be a{' contiguous' if contiguous else ''} {dtype} tensor"
+                         f"{'' if shape is None else ' ' + str(list(shape))} on {device}")
+
+
+def _rows(t, name, dtype, device):
+    """[B, H, N, d] with any strides but a contiguous last dimension."""
+    if t.dim() != 4 or t.dtype != dtype or t.device != device or not t.is_cuda or \
+            (t.stride(3) != 1 and t.shape[3] != 1):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor [B, H, N, d] on {device} with a "
+                         "contiguous last dimension")
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original: int = 8192, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Frequencies (fp64 [rot_dim / 2], radians per position) and the factor on the
+    rotated values for flashmask_rope. Pair i turns by base^(-2 i / rot_dim) a
+    position. scaling: "none"; "linear" divides every frequency by `factor`;
+    "parts" keeps pairs that turn at least `fast` times within `original`
+    positions, divides those that turn at most `slow` times by `factor`, mixes
+    the two linearly between, and multiplies the rotated values by
+    0.1 ln(factor) + 1."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and not negative")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    f = base ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / max(rot_dim, 1))
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if not fast > slow:
+            raise ValueError("fast must be above slow")
+        keep = np.clip((original * f / (2 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
+        f = keep * f + (1.0 - keep) * f / factor
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling != "none":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.from_numpy(f).to(device), mscale
+
+
+def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, where):
+    if q.dtype not in _ROPE_DTYPES:
+        raise ValueError("q must be bf16, fp16 or fp32")
+    dev = q.device
+    xs = (q,) if k is None else (q, k)
+    for t, n in zip(xs, "qk"):
+        _rows(t, n, q.dtype, dev)
+    B, _, N, d = q.shape
+    if k is not None and (k.shape[0] != B or k.shape[2] != N or k.shape[3] != d):
+        raise ValueError("q and k must share B, N and d")
+    rot = 2 * freqs.numel()
+    _want(freqs, "freqs", torch.float64, dev)
+    if freqs.dim() != 1 or rot > d:
+        raise ValueError("freqs must be [rot_dim / 2] with rot_dim <= d")
+    pos_stride = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.device != dev or positions.dim() != 2 or \
+                positions.shape[0] not in (1, B) or positions.shape[1] != N or \
+                (N > 1 and positions.stride(1) != 1):
+            raise ValueError(f"positions must be int32 [{B}, {N}] or [1, {N}] on {dev}, rows contiguous")
+        pos_stride = positions.stride(0) if positions.shape[0] == B and B > 1 else 0
+    with _on(dev, stream, q, k, freqs, positions) as raw:
+        if out is None:
+            ys = tuple(torch.empty(t.shape, dtype=t.dtype, device=dev) for t in xs)
+        else:
+            ys = tuple(out)[:len(xs)]
+            for t, x in zip(ys, xs):
+                _rows(t, "out", q.dtype, dev)
+                if t.shape != x.shape:
+                    raise ValueError("out must have the shapes of q and k")
+                if stream is not None:
+                    t.record_stream(stream)
+        if B * N * d > 0:
+            heads = (_FmHeads * len(xs))(*[
+                _FmHeads(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride()[:3], y.stride()[:3])
+                for x, y in zip(xs, ys)])
+            _check(load().flashmask_rope(heads, len(xs),
+                                         None if positions is None else positions.data_ptr(),
+                                         pos_stride, freqs.data_ptr(), B, N, d, rot,
+                                         int(bool(interleaved)), _ROPE_DTYPES[q.dtype],
+                                         float(mscale), inverse, raw), where)
+    return ys[0], (ys[1] if k is not None else None)
+
+
+def flashmask_rope(q, k, freqs, positions=None, interleaved=False, mscale=1.0, out=None,
+                   stream=None):
+    """Q and K [B, H, N, d] (bf16, fp16 or fp32; any strides with a contiguous last
+    dimension; k may be None) with the first 2 * len(freqs) elements of every
+    head rotated by their token's position; returns (Q', K'). freqs and mscale
+    as rope_frequencies gives them. positions: int32 [B, N] or [1, N] (None:
+    token n sits at n). out: a pair to write into, (q, k) itself to rotate in
+    place."""
+    return _rope(q, k, freqs, positions, interleaved, mscale, out, stream, 0, "flashmask_rope")
+
+
+def flashmask_rope_bwd(dq, dk, freqs, positions=None, interleaved=False, mscale=1.0, out=None,
+                       stream=None):
+    """Gradients of flashmask_rope's inputs from those of its outputs, same arguments."""
+    return _rope(dq, dk, freqs, positions, interleaved, mscale, out, stream, 1,
+                 "flashmask_rope_bwd")
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+@dataclass
+class KVCache:
+    """Keys and values as e4m3 codes in pages of FM_PAGE tokens with one scale per
+    page and head: k8 [pages, Hk, 64, d], v8 [pages, Hk, d, 64] (float8_e4m3fn,
+    V transposed), kscale, vscale fp32 [pages, Hk]."""
+
+    k8: torch.Tensor
+    v8: torch.Tensor
+    kscale: torch.Tensor
+    vscale: torch.Tensor
+
+    @staticmethod
+    def empty(pages: int, Hk: int, d: int, device="cuda") -> "KVCache":
+        f8 = dict(dtype=torch.float8_e4m3fn, device=device)
+        return KVCache(torch.zeros((pages, Hk, FM_PAGE, d), **f8),
+                       torch.zeros((pages, Hk, d, FM_PAGE), **f8),
+                       torch.ones((pages, Hk), device=device), torch.ones((pages, Hk), device=device))
+
+    def c_struct(self) -> _FmCache:
+        k8, v8 = self.k8, self.v8
+        if k8.dim() != 4 or k8.shape[2] != FM_PAGE or not k8.is_cuda:
+            raise ValueError("k8 must be a CUDA tensor [pages, Hk, 64, d]")
+        pages, Hk, _, d = k8.shape
+        _want(k8, "k8", torch.float8_e4m3fn, k8.device)
+        _want(v8, "v8", torch.float8_e4m3fn, k8.device, (pages, Hk, d, FM_PAGE))
+        _want(self.kscale, "kscale", torch.float32, k8.device, (pages, Hk))
+        _want(self.vscale, "vscale", torch.float32, k8.device, (pages, Hk))
+        return _FmCache(k8.data_ptr(), v8.data_ptr(), self.kscale.data_ptr(), self.vscale.data_ptr(),
+                        pages, Hk, d)
+
+
+def flashmask_cache_workspace_bytes(B, H, Hk, N, d, max_pages) -> int:
+    return int(load().flashmask_cache_workspace_bytes(B, H, Hk, N, d, max_pages))
+
+
+def alloc_cache_workspace(B, H, Hk, N, d, max_pages, device="cuda") -> torch.Tensor:
+    """Zeroed workspace of flashmask_cache_append and flashmask_fwd_cache."""
+    n = flashmask_cache_workspace_bytes(B, H, Hk, N, d, max_pages)
+    if n == 0:
+        raise FlashMaskError(FM_ERR_UNSUPPORTED, "flashmask_cache_workspace_bytes")
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+def _per_sequence(t, name, B, device):
+    if t is not None:
+        _want(t, name, torch.int32, device, (B,))
+    return None if t is None else t.data_ptr()
+
+
+def _page_table(t, B, device):
+    if t.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    _want(t, "page_table", torch.int32, device, (B, t.shape[1]))
+    return t.shape[1]
+
+
+def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=None, stream=None):
+    """Writes K and V (bf16 [B, Hk, N, d], last dimension contiguous) behind the
+    start[b] tokens that sequence b holds; count[b] <= N of its rows are real.
+    page_table int32 [B, max_pages]; start, count int32 [B]. See
+    include/flashmask.h for scales and rounding."""
+    c = cache.c_struct()
+    dev = cache.k8.device
+    _rows(k, "k", torch.bfloat16, dev)
+    _rows(v, "v", torch.bfloat16, dev)
+    B, Hk, N, d = k.shape
+    if v.shape != k.shape or Hk != c.Hk or d != c.d:
+        raise ValueError("k and v must be [B, Hk, N, d] with the cache's Hk and d")
+    max_pages = _page_table(page_table, B, dev)
+    st, ct = _per_sequence(start, "start", B, dev), _per_sequence(count, "count", B, dev)
+    _want(ws, "ws", torch.uint8, dev)
+    with _on(dev, stream, cache.k8, cache.v8, cache.kscale, cache.vscale, page_table, k, v, start,
+             count, ws) as raw:
+        _check(load().flashmask_cache_append(ctypes.byref(c), page_table.data_ptr(), max_pages,
+                                             k.data_ptr(), _Strides(*k.stride()[:3]), v.data_ptr(),
+                                             _Strides(*v.stride()[:3]), st, ct, B, N, ws.data_ptr(),
+                                             ws.numel(), raw), "flashmask_cache_append")
+
+
+def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMask | None = None,
+                        q_lens=None, scale=None, o=None, lse=None, stream=None):
+    """Attention of the N query tokens of each sequence (q bf16 [B, H, N, d], last
+    dimension contiguous) over its lens[b] cached tokens, the query tokens' own
+    among them; q_lens[b] <= N of its rows are real. mask: causal when None,
+    else a DeviceMask whose vectors are [B, Hm, 64 * max_pages] (lts and lte may
+    be None). Returns (O bf16 like q, LSE fp32 [B, H, N]); rows behind q_lens[b]
+    of `o` and `lse` are left as they were."""
+    c = cache.c_struct()
+    dev = cache.k8.device
+    _rows(q, "q", torch.bfloat16, dev)
+    B, H, N, d = q.shape
+    if d != c.d:
+        raise ValueError("q must have the cache's d")
+    max_pages = _page_table(page_table, B, dev)
+    ln, ql = _per_sequence(lens, "lens", B, dev), _per_sequence(q_lens, "q_lens", B, dev)
+    _want(ws, "ws", torch.uint8, dev)
+    vectors = () if mask is None else (mask.lts, mask.lte, mask.uts, mask.ute)
+    m = None
+    if mask is not None:
+        given = [t for t in vectors if t is not None]
+        Hm = given[0].shape[1] if given and given[0].dim() == 3 else 1
+        for t in given:
+            _want(t, "mask vectors", torch.int32, dev, (B, Hm, max_pages * FM_PAGE))
+        m = _FmMask(*[None if t is None else t.data_ptr() for t in vectors], Hm, int(mask.causal))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with _on(dev, stream, q, cache.k8, cache.v8, cache.kscale, cache.vscale, page_table, lens, q_lens,
+             ws, o, lse, *vectors) as raw:
+        if o is None:
+            o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+        _rows(o, "o", torch.bfloat16, dev)
+        _want(lse, "lse", torch.float32, dev, (B, H, N))
+        if o.shape != q.shape:
+            raise ValueError("o must have q's shape")
+        _check(load().flashmask_fwd_cache(q.data_ptr(), _Strides(*q.stride()[:3]), ctypes.byref(c),
+                                          page_table.data_ptr(), max_pages, ln, ql,
+                                          None if m is None else ctypes.byref(m), B, H, N, scale,
+                                          o.data_ptr(), _Strides(*o.stride()[:3]), lse.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), raw), "flashmask_fwd_cache")
+    return o, lse
