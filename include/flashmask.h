@@ -408,6 +408,7 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  *     (causal && j > i) || (LTS[j] <= i < LTE[j]) || (UTS[j] <= i < UTE[j])
  * with the vectors [B, Hm, max_pages * FM_PAGE] of `mask`, whose lts and lte
  * may both be NULL too (no lower interval); mask NULL: causal, no intervals.
+ * The vectors are 16-byte aligned; entries behind a sequence's length may hold anything.
  * Head h reads mask head h / (H / Hm) and cache head h / (H / Hk); H % Hk ==
  * 0, H % Hm == 0. O, LSE and rows without a visible key are as at the top of
  * this file: O bf16 [B, H, N, d], LSE fp32 [B, H, N] (contiguous).
@@ -417,8 +418,9 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * not finite gives NaN.
  *   qs, os: strides of Q and O in elements for batch, head and token (multiples
  *   of 8; the last dimension contiguous, 16-byte aligned).
- * Results do not depend on the order in which CTAs run. Asynchronous on
- * `stream`. */
+ * Results do not depend on the order in which CTAs run (the same call gives the
+ * same bits); how a sequence's sum is split depends on the whole batch, so its
+ * last bits may differ beside other sequences. Asynchronous on `stream`. */
 fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache* cache,
                               const int32_t* page_table, int max_pages, const int32_t* lens,
                               const int32_t* q_lens, const fm_mask* mask, int B, int H, int N,

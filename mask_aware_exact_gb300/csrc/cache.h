@@ -62,7 +62,20 @@ struct CacheFwdParams {
   int64_t os[3];
   float* lse;
   int32_t* status;
+  // workspace (see CacheWs)
+  int32_t* arrived;     // [segments]: partial results that have arrived (0 between calls)
+  int32_t* class_done;  // [row tiles]: words classified (0 between calls)
+  float* partial;       // [CTAs][2] partial results
+  uint32_t* vis;        // [row tiles][words]: pages that some row sees
+  uint32_t* part;       // [row tiles][words]: pages where intervals hide some key from some row
+  int32_t* prefix;      // [row tiles][words + 1]: running count of visible pages
 };
-cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, cudaStream_t s);
+// Byte offsets of the workspace regions.
+struct CacheWs {
+  size_t arrived, class_done, partial, vis, part, prefix, total;
+};
+constexpr int kCacheMaxCtas = 256;  // partial results are kept for at most this many CTAs
+CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages);
+cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s);
 
 }  // namespace fm

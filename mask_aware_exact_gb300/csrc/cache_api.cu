@@ -33,6 +33,12 @@ bool strides_ok(const int64_t* s) {
   return true;
 }
 
+// The mask's vectors are read 16 bytes at a time.
+bool vectors_ok(const fm_mask* m) {
+  return (m->lts == nullptr) == (m->lte == nullptr) && (m->uts == nullptr) == (m->ute == nullptr) &&
+         aligned16(m->lts) && aligned16(m->lte) && aligned16(m->uts) && aligned16(m->ute);
+}
+
 bool cache_shape_ok(int B, int H, int Hk, int N, int d, int max_pages) {
   if (B <= 0 || H <= 0 || Hk <= 0 || N <= 0 || max_pages <= 0) return false;
   if (d != 64 && d != 128) return false;
@@ -118,7 +124,7 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
 
 size_t flashmask_cache_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages) {
   if (!cache_shape_ok(B, H, Hk, N, d, max_pages)) return 0;
-  return 256;
+  return fm::cache_ws_layout(B, H, Hk, N, d, max_pages).total;
 }
 
 fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_table, int max_pages,
@@ -162,13 +168,12 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   if (!q || !qs || !page_table || !lens || !o || !os || !lse) return FM_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !strides_ok(qs) || !strides_ok(os)) return FM_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FM_ERR_INVALID_ARG;
-  if (mask && ((mask->lts == nullptr) != (mask->lte == nullptr) ||
-               (mask->uts == nullptr) != (mask->ute == nullptr)))
-    return FM_ERR_INVALID_ARG;
+  if (mask && !vectors_ok(mask)) return FM_ERR_INVALID_ARG;
   if (!cache_shape_ok(B, H, cache->Hk, N, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
+  if (B > 65535) return FM_ERR_UNSUPPORTED;
   if (mask && (mask->Hm <= 0 || H % mask->Hm != 0)) return FM_ERR_UNSUPPORTED;
-  const fm_status st =
-      check_ws(ws, ws_bytes, flashmask_cache_workspace_bytes(B, H, cache->Hk, N, cache->d, max_pages));
+  const fm::CacheWs L = fm::cache_ws_layout(B, H, cache->Hk, N, cache->d, max_pages);
+  const fm_status st = check_ws(ws, ws_bytes, L.total);
   if (st != FM_OK) return st;
   fm::CacheFwdParams p;
   p.q = static_cast<const uint16_t*>(q);
@@ -198,8 +203,17 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
     p.os[i] = os[i];
   }
   p.lse = lse;
-  p.status = static_cast<int32_t*>(ws);
-  return fm::launch_cache_fwd(cache->d, p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  char* w = static_cast<char*>(ws);
+  p.status = reinterpret_cast<int32_t*>(w);
+  p.arrived = reinterpret_cast<int32_t*>(w + L.arrived);
+  p.class_done = reinterpret_cast<int32_t*>(w + L.class_done);
+  p.partial = reinterpret_cast<float*>(w + L.partial);
+  p.vis = reinterpret_cast<uint32_t*>(w + L.vis);
+  p.part = reinterpret_cast<uint32_t*>(w + L.part);
+  p.prefix = reinterpret_cast<int32_t*>(w + L.prefix);
+  const int sms = sm_count();
+  if (sms <= 0) return FM_ERR_CUDA;
+  return fm::launch_cache_fwd(cache->d, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FM_OK
              : FM_ERR_CUDA;
 }

@@ -1,83 +1,955 @@
-// Attention over the 8-bit paged cache. Simple form: one warp per query row and
-// head, keys one after another, running maximum and sum.
+// Attention over the 8-bit paged cache: a few query rows per cache head against
+// long sequences (one token of each running sequence, drafted tokens), where
+// reading the codes once bounds the call.
+//
+// Rows. The G = H / Hk query heads that share a cache head and the sequence's
+// query tokens form one list of rows, r = t * G + g, cut into tiles of 16 (the M
+// of a matrix instruction). A segment is one (sequence, cache head, row tile); its
+// work is the list of pages that some row of it sees.
+//
+// Split. All pages of all segments form one line, cut into equal runs, one run
+// per CTA (one CTA per SM), whatever the lengths of the sequences. A run covers
+// pieces of one or more segments; a segment cut by a run border leaves partial
+// results in the workspace and the CTA that finishes last adds them in order, so
+// results do not depend on timing. With a column-wise mask a first kernel marks
+// the pages that are visible to a row tile, and only those are on the line.
+//
+// One producer warp walks the run and loads pages (K codes, V codes: 64 * d bytes
+// each, contiguous) with bulk copies into a ring of three slots for each of seven
+// consumer warps; tile i of the run goes to warp i mod 7. The warps keep separate
+// softmax states and merge them when a piece ends; the producer is then already
+// loading the next piece.
+//
+// Arithmetic. Codes become fp16 (exact) and enter m16n8k16 instructions with fp32
+// accumulators; tcgen05 would need 128 rows. The query row is scaled by a power of
+// two so that its largest element lies in [2^14, 2^15): fp16 then holds every bf16
+// element down to 2^-30 of the largest exactly. P is rounded to fp16 (2^-12
+// relative) after scaling by the page's V scale, relative to the row's largest such
+// product: a second running maximum, mv of log2(P * scale), beside m of the scores,
+// so that neither the weights of pages with small values (in l) nor the values of
+// pages with small weights are lost. m, mv, l and O are fp32.
+//
+// Layout of a fragment. Lane = 4 g + c holds of a row tile the rows g and g + 8 and
+// of a page the keys 16 c .. 16 c + 15: the columns of the eight S instructions are
+// keys in the order that leaves each lane with 16 consecutive ones, so that its
+// 16-byte load of a V column is exactly the operand that meets its P. The summed
+// index d of S is permuted in the same way: a lane reads 16 consecutive codes of a
+// key, and the query is laid out to match.
 #include "cache.h"
+#include "flashmask.h"
 #include "ptx_fp8.cuh"
 
 namespace fm {
 namespace {
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-  float f;
-  asm("{.reg .f16 a, b; mov.b32 {a, b}, %1; cvt.f32.f16 %0, a;}" : "=f"(f) : "r"(h));
-  return f;
+constexpr int kConsumers = 7;  // with the producer 8 warps: two for each scheduler, 255 registers a thread
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kRows = 16;      // rows of a tile
+constexpr int kSlots = 3;      // ring slots of a consumer warp
+constexpr int kPieceRing = 4;  // piece descriptors in flight
+// Pages a run has at least: one for each consumer warp. Shorter runs only
+// add partial results.
+constexpr int kMinRun = kConsumers;
+constexpr float kPShift = 14.f;  // P is stored as 2^14 P
+
+// ---------------------------------------------------------------- geometry
+struct Geometry {
+  int G, RT, classes, words;  // query heads per cache head, row tiles, mask classes, bit words
+};
+
+// Row tile `rt` of sequence b: its query tokens [t_lo, t_hi] at positions t + shift,
+// none when t_hi < t_lo; len is the sequence's length, cut to what the table holds.
+struct RowTile {
+  int len, live, shift, t_lo, t_hi;
+};
+__device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, int G, int b, int rt, bool record) {
+  RowTile r;
+  r.live = p.q_lens ? min(max(p.q_lens[b], 0), p.N) : p.N;
+  r.len = p.lens[b];
+  const int most = p.max_pages * kPage;
+  if (r.len < 0 || r.len > most) {
+    if (record) record_failure(p.status, kStatusPage, kSiteCacheLen);
+    r.len = min(max(r.len, 0), most);
+  }
+  r.shift = r.len - r.live;
+  const long long rows = static_cast<long long>(G) * r.live, r0 = static_cast<long long>(rt) * kRows;
+  r.t_lo = static_cast<int>(r0 / G);
+  r.t_hi = r0 < rows ? static_cast<int>(min(r0 + kRows - 1, rows - 1) / G) : r.t_lo - 1;
+  return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) cache_fwd_simple(const CacheFwdParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.H * p.N) return;
-  const int t = row % p.N, h = (row / p.N) % p.H, b = row / (static_cast<long long>(p.N) * p.H);
-  const int qn = p.q_lens ? min(max(p.q_lens[b], 0), p.N) : p.N;
-  if (t >= qn) return;
-  int len = p.lens[b];
-  const int most = p.max_pages * kPage;
-  if (len < 0 || len > most) {
-    if (lane == 0) record_failure(p.status, kStatusPage, kSiteCacheLen);
-    len = min(max(len, 0), most);
-  }
-  const int pos = len - qn + t, hk = h / (p.H / p.c.Hk);
-  const size_t mrow = (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) * most;
-  float q[D / 32], acc[D / 32];
-  for (int i = 0; i < D / 32; ++i) {
-    q[i] = __uint_as_float(static_cast<uint32_t>(p.q[b * p.qs[0] + h * p.qs[1] + t * p.qs[2] + lane + 32 * i]) << 16);
-    acc[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int end = p.mask.causal ? min(len, pos + 1) : len;
-  for (int j = 0; j < end; ++j) {
-    if (p.mask.lts && p.mask.lts[mrow + j] <= pos && pos < p.mask.lte[mrow + j]) continue;
-    if (p.mask.uts && p.mask.uts[mrow + j] <= pos && pos < p.mask.ute[mrow + j]) continue;
-    const int page = p.table[static_cast<size_t>(b) * p.max_pages + j / kPage];
-    if (page < 0 || page >= p.c.pages) {
-      if (lane == 0) record_failure(p.status, kStatusPage, kSiteCachePage);
-      continue;
-    }
-    const size_t ph = static_cast<size_t>(page) * p.c.Hk + hk;
-    float s = 0.f;
-    for (int i = 0; i < D / 32; ++i)
-      s += q[i] * e4m3_value(p.c.k8[ph * (kPage * D) + (j % kPage) * D + lane + 32 * i]);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.scale_log2 * p.c.kscale[ph];
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float w = exp2f(s - (mn == -INFINITY ? 0.f : mn));
-    m = mn;
-    l = l * f + w;
-    const float vs = p.c.vscale[ph];
-    for (int i = 0; i < D / 32; ++i)
-      acc[i] = acc[i] * f + w * vs * e4m3_value(p.c.v8[ph * (kPage * D) + (lane + 32 * i) * kPage + j % kPage]);
-  }
-  const bool none = l == 0.f;
-  for (int i = 0; i < D / 32; ++i)
-    p.o[b * p.os[0] + h * p.os[1] + t * p.os[2] + lane + 32 * i] =
-        static_cast<uint16_t>(pack_bf16x2(none ? 0.f : acc[i] / l, 0.f));
-  if (lane == 0)
-    p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+__device__ __forceinline__ int mask_class(const CacheFwdParams& p, const Geometry& geo, int hk) {
+  return geo.classes == p.c.Hk ? hk : hk / (p.c.Hk / geo.classes);
 }
+
+// Pages on a segment's line.
+template <bool kVec>
+__device__ __forceinline__ int pages_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
+  const int rt = seg % geo.RT, bh = seg / geo.RT;
+  const int b = bh / p.c.Hk;
+  if constexpr (kVec) {
+    const int cls = mask_class(p, geo, bh - b * p.c.Hk);
+    const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
+    return p.prefix[at * (geo.words + 1) + geo.words];
+  } else {
+    const RowTile r = row_tile(p, geo.G, b, rt, false);
+    if (r.t_hi < r.t_lo) return 0;
+    const int lim = p.mask.causal ? min(r.len, r.shift + r.t_hi + 1) : r.len;
+    return lim > 0 ? (lim + kPage - 1) / kPage : 0;
+  }
+}
+
+// ---------------------------------------------------------------- visible pages
+// Bits of the pages that some row of a row tile sees (vis), of those where an
+// interval hides some key from some row (part), and the running count of the
+// former per word (prefix; its last entry is the total). A CTA takes one word, 32
+// pages; a key hides the positions [lo, hi] of the tile if the union of its
+// intervals covers them. The CTA that finishes a row tile last sums its words.
+__global__ void __launch_bounds__(256) cache_classify(const CacheFwdParams p, const Geometry geo) {
+  __shared__ uint32_t bits[2];
+  __shared__ int last;
+  const int w = blockIdx.x, b = blockIdx.z;
+  const int cls = blockIdx.y / geo.RT, rt = blockIdx.y % geo.RT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowTile r = row_tile(p, geo.G, b, rt, w == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  const int lo = r.shift + r.t_lo, hi = r.shift + r.t_hi;
+  int m0 = cls, m1 = cls;  // mask heads of the class
+  if (geo.classes != p.mask.Hm) {
+    const int each = p.H / p.mask.Hm;
+    m0 = cls * geo.G / each;
+    m1 = (cls * geo.G + geo.G - 1) / each;
+  }
+  if (threadIdx.x < 2) bits[threadIdx.x] = 0;
+  __syncthreads();
+  const int L = p.max_pages * kPage;
+  uint32_t vis = 0, part = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int page = 32 * w + 4 * warp + i;
+    bool see = false, cut = false;
+    for (int half = 0; half < 2; ++half) {
+      const int j = page * kPage + 32 * half + lane;
+      if (j >= r.len || hi < lo || (p.mask.causal && j > hi)) continue;
+      for (int m = m0; m <= m1; ++m) {
+        const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j;
+        const int s0 = p.mask.lts ? p.mask.lts[at] : 0, e0 = p.mask.lts ? p.mask.lte[at] : 0;
+        const int s1 = p.mask.uts ? p.mask.uts[at] : 0, e1 = p.mask.uts ? p.mask.ute[at] : 0;
+        cut |= max(s0, lo) < min(e0, hi + 1) || max(s1, lo) < min(e1, hi + 1);
+        int reach = p.mask.causal ? max(lo, j) : lo;  // first position not known to be hidden
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (s0 <= reach && reach < e0) reach = e0;
+          if (s1 <= reach && reach < e1) reach = e1;
+        }
+        see |= reach <= hi;
+      }
+    }
+    if (__any_sync(0xffffffffu, see)) vis |= 1u << (4 * warp + i);
+    if (__any_sync(0xffffffffu, cut)) part |= 1u << (4 * warp + i);
+  }
+  if (lane == 0) {
+    atomicOr(&bits[0], vis);
+    atomicOr(&bits[1], part);
+  }
+  __syncthreads();
+  const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
+  if (threadIdx.x == 0) {
+    p.vis[at * geo.words + w] = bits[0];
+    p.part[at * geo.words + w] = bits[1];
+    __threadfence();
+    last = atomicAdd(&p.class_done[at], 1) == geo.words - 1;
+  }
+  __syncthreads();
+  if (!last || warp != 0) return;
+  __threadfence();
+  int sum = 0;
+  int32_t* out = p.prefix + at * (geo.words + 1);
+  for (int w0 = 0; w0 < geo.words; w0 += 32) {
+    const int n = w0 + lane < geo.words ? __popc(__ldcg(&p.vis[at * geo.words + w0 + lane])) : 0;
+    int c = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += x;
+    }
+    if (w0 + lane < geo.words) out[w0 + lane] = sum + c - n;
+    sum += __shfl_sync(0xffffffffu, c, 31);
+  }
+  if (lane == 0) {
+    out[geo.words] = sum;
+    p.class_done[at] = 0;
+  }
+}
+
+// Index of the k-th set bit of x (k < popc(x)).
+__device__ __forceinline__ int nth_bit(uint32_t x, int k) {
+  int at = 0;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const int n = __popc((x >> at) & ((1u << s) - 1u));
+    if (k >= n) {
+      k -= n;
+      at += s;
+    }
+  }
+  return at;
+}
+
+// ---------------------------------------------------------------- instructions
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four codes -> two fp16 pairs.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Bounded wait: gives up after the library's limit, or when another wait has (a
+// page error alone does not end waits).
+__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_t* status) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
+    if (global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
+      record_failure(status, kStatusTimeout, kSiteCacheWait);
+      return false;
+    }
+  }
+  return true;
+}
+// 2^(a - b) where either may be -inf (then a is, or both are).
+__device__ __forceinline__ float ex2_diff(float a, float b) { return a == b ? 1.f : ex2(a - b); }
+
+template <int D>
+struct Smem {
+  static constexpr int kHalf = kPage * D;  // bytes of a page's K or V
+  static constexpr int kRing = 0;          // [consumer][slot]
+  static constexpr int kMerge = kRing + kConsumers * kSlots * kHalf;  // fp32 [4][D / 8][32][4]
+  static constexpr int kStats = kMerge + 4 * kRows * D * 4;          // float [4][16][3]: m, mv, l
+  static constexpr int kMeta = kStats + 4 * kRows * 3 * 4;  // int4 [consumer][slot]
+  static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8]
+  static constexpr int kBars = kPiece + kPieceRing * 32;
+  static constexpr int kNumBars = 2 * kConsumers * kSlots + 2 * kPieceRing + 1;
+  static constexpr int kScan = kBars + kNumBars * 8;  // long long [16]
+  static constexpr int kBytes = kScan + 16 * 8;
+};
+static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(Smem<128>::kScan % 8 == 0 && Smem<64>::kScan % 8 == 0, "alignment");
+
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t full(int w, int s) const { return base + 8 * (w * kSlots + s); }
+  __device__ uint32_t empty(int w, int s) const { return base + 8 * ((kConsumers + w) * kSlots + s); }
+  __device__ uint32_t piece_full(int s) const { return base + 8 * (2 * kConsumers * kSlots + s); }
+  __device__ uint32_t piece_empty(int s) const { return base + 8 * (2 * kConsumers * kSlots + kPieceRing + s); }
+  __device__ uint32_t merge() const { return base + 8 * (2 * kConsumers * kSlots + 2 * kPieceRing); }
+};
+
+// One piece of a segment: tiles [first, first + count) of the CTA's run.
+struct Piece {
+  int seg, first, count, whole, slot, cta0, parts, pad;
+};
+
+// Floats of one partial result in the workspace: O [16][D], then m, mv, l [16] each.
+__host__ __device__ constexpr int part_floats(int D) { return kRows * D + 3 * kRows; }
+
+// Consumer state of one warp: two rows of the tile per lane.
+template <int D>
+struct State {
+  float acc[D / 8][4];
+  float m[2], mv[2], l[2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m[i] = mv[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+  }
+};
+
+// Writes rows of O and LSE from sums relative to m and mv.
+__device__ __forceinline__ float out_factor(float m, float mv, float l) {
+  // acc = 2^(14 - mv) sum P V and l = 2^-m sum P
+  const float f = mv == -INFINITY ? 0.f : ex2(mv - (m == -INFINITY ? 0.f : m) - kPShift);
+  return l == 0.f ? 0.f : f / l;
+}
+__device__ __forceinline__ float out_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+template <int D, bool kVec>
+__global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdParams p, const Geometry geo) {
+  using S = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nseg = p.B * p.c.Hk * geo.RT;
+  const Bars bar{smem_u32(smem + S::kBars)};
+  long long* scan = reinterpret_cast<long long*>(smem + S::kScan);
+
+  if (tid == 0) {
+    for (int w = 0; w < kConsumers; ++w)
+      for (int s = 0; s < kSlots; ++s) {
+        mbar_init(bar.full(w, s), 1);
+        mbar_init(bar.empty(w, s), 1);
+      }
+    for (int s = 0; s < kPieceRing; ++s) {
+      mbar_init(bar.piece_full(s), 1);
+      mbar_init(bar.piece_empty(s), kConsumers);
+    }
+    mbar_init(bar.merge(), kConsumers);
+    fence_barrier_init();
+  }
+
+  // the line's length and the segment where this CTA's run begins
+  const int each = (nseg + kThreads - 1) / kThreads;
+  const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
+  long long mine = 0;
+  for (int s = seg_lo; s < seg_hi; ++s) mine += pages_of<kVec>(p, geo, s);
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) scan[warp] = before;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w <= kConsumers; ++w) {
+    const long long x = scan[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  before -= mine;
+  const long long ctas = gridDim.x;
+  const long long run = max(static_cast<long long>(kMinRun), (total + ctas - 1) / ctas);
+  const long long run_lo = min(run * blockIdx.x, total), run_hi = min(run_lo + run, total);
+  if (run_lo < run_hi && before <= run_lo && run_lo < before + mine) {
+    int s = seg_lo;
+    for (;; ++s) {
+      const int n = pages_of<kVec>(p, geo, s);
+      if (run_lo < before + n) break;
+      before += n;
+    }
+    scan[12] = s;
+    scan[13] = run_lo - before;
+  }
+  __syncthreads();
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    int seg = static_cast<int>(scan[12]), k = static_cast<int>(scan[13]);
+    const int tiles = static_cast<int>(run_hi - run_lo);
+    bool ok = true;
+    int pieces = 0;
+    auto publish = [&](const Piece& d) {
+      const int e = pieces % kPieceRing;
+      if (pieces >= kPieceRing)
+        ok = __all_sync(0xffffffffu, ok && cache_wait(bar.piece_empty(e), (pieces / kPieceRing - 1) & 1, p.status));
+      ++pieces;
+      if (lane == 0 && ok) {
+        int* at = reinterpret_cast<int*>(smem + S::kPiece) + 8 * e;
+        at[0] = d.seg, at[1] = d.first, at[2] = d.count, at[3] = d.whole;
+        at[4] = d.slot, at[5] = d.cta0, at[6] = d.parts;
+        mbar_arrive(bar.piece_full(e));
+      }
+      __syncwarp();
+    };
+    int done = 0;
+    while (ok && done < tiles) {
+      // the next 32 tiles of the run, one per lane, over the next 32 segments
+      const int s_l = seg + lane;
+      int n = s_l < nseg ? pages_of<kVec>(p, geo, s_l) : 0;
+      const int n_all = n;
+      if (lane == 0) n -= k;
+      int c = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, c, o);
+        // sums past 2^30 are only compared with tile numbers below 32
+        if (lane >= o) c = min(c + x, 1 << 30);
+      }
+      const int avail = min(min(__shfl_sync(0xffffffffu, c, 31), 32), tiles - done);
+      int j = 0;  // segments that end at or before this lane's tile
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        const int x = __shfl_sync(0xffffffffu, c, j + s - 1);
+        if (x <= lane) j += s;
+      }
+      const int c_j = __shfl_sync(0xffffffffu, c, j), n_j = __shfl_sync(0xffffffffu, n_all, j);
+      const int my_seg = seg + j;
+      const int my_k = n_j - (c_j - lane);  // the tile's number in its segment
+      const bool live = lane < avail;
+      int page = -1, logical = 0, cut = 0;
+      float ks = 0.f, lvs = 0.f;
+      if (live) {
+        const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+        logical = my_k;
+        if constexpr (kVec) {
+          const size_t at = (static_cast<size_t>(b) * geo.classes + mask_class(p, geo, hk)) * geo.RT + rt;
+          const int32_t* pre = p.prefix + at * (geo.words + 1);
+          int lo = 0, hi = geo.words;  // pre[lo] <= my_k < pre[hi]
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= my_k) lo = mid; else hi = mid;
+          }
+          const int bit = nth_bit(p.vis[at * geo.words + lo], my_k - pre[lo]);
+          logical = 32 * lo + bit;
+          cut = (p.part[at * geo.words + lo] >> bit) & 1u;
+        }
+        page = p.table[static_cast<size_t>(b) * p.max_pages + logical];
+        if (page < 0 || page >= p.c.pages) {
+          record_failure(p.status, kStatusPage, kSiteCachePage);
+          page = -1;
+        } else {
+          const size_t ph = static_cast<size_t>(page) * p.c.Hk + hk;
+          ks = p.c.kscale[ph];
+          lvs = log2f(p.c.vscale[ph]);
+        }
+      }
+      for (int t = 0; ok && t < avail; ++t) {
+        const int sg = __shfl_sync(0xffffffffu, my_seg, t), kk = __shfl_sync(0xffffffffu, my_k, t);
+        const int nn = __shfl_sync(0xffffffffu, n_j, t);
+        if (done == 0 || kk == 0) {
+          Piece d;
+          d.seg = sg;
+          d.first = done;
+          d.count = min(nn - kk, tiles - done);
+          d.whole = kk == 0 && d.count == nn;
+          d.slot = kk == 0 ? 1 : 0;
+          const long long s0 = run_lo + done - kk;
+          d.cta0 = static_cast<int>(s0 / run);
+          d.parts = static_cast<int>((s0 + nn - 1) / run) - d.cta0 + 1;
+          publish(d);
+        }
+        const int pg = __shfl_sync(0xffffffffu, page, t);
+        const int w = done % kConsumers, q = 2 * (done / kConsumers);
+        const int lg = __shfl_sync(0xffffffffu, logical, t), ct = __shfl_sync(0xffffffffu, cut, t);
+        const float k_s = __shfl_sync(0xffffffffu, ks, t), v_s = __shfl_sync(0xffffffffu, lvs, t);
+        if (lane == 0 && ok) {
+          const int hk = (sg / geo.RT) % p.c.Hk;
+          const size_t off = (static_cast<size_t>(max(pg, 0)) * p.c.Hk + hk) * S::kHalf;
+#pragma unroll
+          for (int half = 0; half < 2 && ok; ++half) {
+            const int seq = q + half, slot = seq % kSlots;
+            if (seq >= kSlots) ok = cache_wait(bar.empty(w, slot), (seq / kSlots - 1) & 1, p.status);
+            if (!ok) break;
+            int4* meta = reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot;
+            *meta = make_int4(pg < 0 ? -1 : lg, ct, __float_as_int(half ? v_s : k_s), __float_as_int(v_s));
+            if (pg >= 0) {
+              mbar_arrive_expect_tx(bar.full(w, slot), S::kHalf);
+              bulk_load(smem_u32(smem + S::kRing + (w * kSlots + slot) * S::kHalf),
+                        (half ? p.c.v8 : p.c.k8) + off, S::kHalf, bar.full(w, slot));
+            } else {
+              mbar_arrive(bar.full(w, slot));
+            }
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        ++done;
+      }
+      // the tile behind the last one taken
+      if (avail > 0) {
+        seg = __shfl_sync(0xffffffffu, my_seg, avail - 1);
+        k = __shfl_sync(0xffffffffu, my_k, avail - 1) + 1;
+      } else {
+        seg += 32;
+        k = 0;
+      }
+    }
+    Piece end = {};
+    if (ok) publish(end);
+    if (!ok && lane == 0) {
+      // copies in flight land before the CTA's shared memory is given up
+      for (int w = 0; w < kConsumers; ++w)
+        for (int s = 0; s < kSlots; ++s) {
+          const int issued = (done + kConsumers - 1 - w) / kConsumers * 2;  // at most, of warp w
+          for (int seq = max(0, issued - kSlots); seq < issued; ++seq)
+            if (seq % kSlots == s) mbar_wait_for(bar.full(w, s), (seq / kSlots) & 1, nullptr, 1000000ull);
+        }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(smem + S::kRing) + warp * kSlots * S::kHalf;
+  float4* merge = reinterpret_cast<float4*>(smem + S::kMerge);
+  float* stats = reinterpret_cast<float*>(smem + S::kStats);
+  uint32_t merge_phase = 0;
+  bool ok = true;
+  // all consumer warps; false when a wait gave up
+  auto sync_warps = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.merge());
+    ok = __all_sync(0xffffffffu, cache_wait(bar.merge(), merge_phase & 1, p.status));
+    ++merge_phase;
+    return ok;
+  };
+  int seq = 0;  // ring position of this warp
+
+  for (int piece = 0; ok; ++piece) {
+    const int e = piece % kPieceRing;
+    ok = __all_sync(0xffffffffu, cache_wait(bar.piece_full(e), (piece / kPieceRing) & 1, p.status));
+    if (!ok) break;
+    const int* d = reinterpret_cast<const int*>(smem + S::kPiece) + 8 * e;
+    const int seg = d[0], first = d[1], count = d[2], whole = d[3], slot_id = d[4], cta0 = d[5], parts = d[6];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.piece_empty(e));
+    if (count == 0) break;
+
+    const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const RowTile r = row_tile(p, geo.G, b, rt, lane == 0 && warp == 0);
+    const int rows = geo.G * r.live;
+    State<D> st;
+    st.clear();
+    uint32_t qf[D / 16][4];
+    float crow[2];
+    int lim[2], pos[2];
+    size_t mrow[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int rr = rt * kRows + g + 8 * i;
+      const bool live = rr < rows;
+      const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+      pos[i] = r.shift + t;
+      lim[i] = live && p.mask.causal ? min(r.len, pos[i] + 1) : r.len;
+      if constexpr (kVec)
+        mrow[i] = (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) *
+                  static_cast<size_t>(p.max_pages * kPage);
+      // this lane's 16 elements of each half: d = 64 half + 16 c ..
+      uint4 x[D / 64][2];
+      const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + t * p.qs[2] + 16 * c;
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          x[hf][u] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t top = 0;
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t mk = 0x7fff7fffu;
+          const uint32_t a = __vmaxu2(__vmaxu2(x[hf][u].x & mk, x[hf][u].y & mk), __vmaxu2(x[hf][u].z & mk, x[hf][u].w & mk));
+          top = max(top, max(a & 0xffffu, a >> 16));
+        }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest element's exponent becomes 14; rows that are not finite become NaN
+      const bool bad = top >= 0x7f80u;
+      const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+      const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
+      crow[i] = p.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4& v = x[hf][u >> 1];
+          const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
+          qf[4 * hf + u][i] = pack_f16x2(__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f);
+          qf[4 * hf + u][2 + i] = pack_f16x2(__uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f);
+        }
+    }
+    // keys that every row of the tile sees as far as causality and length go
+    int all_lim = min(lim[0], lim[1]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) all_lim = min(all_lim, __shfl_xor_sync(0xffffffffu, all_lim, o));
+
+    const int t0 = first + ((warp - first) % kConsumers + kConsumers) % kConsumers;
+    for (int tile = t0; ok && tile < first + count; tile += kConsumers) {
+      const int sk = seq % kSlots, sv = (seq + 1) % kSlots;
+      ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sk), (seq / kSlots) & 1, p.status));
+      if (!ok) break;
+      const int4 meta = *(reinterpret_cast<const int4*>(smem + S::kMeta) + warp * kSlots + sk);
+      const float lvs = __int_as_float(meta.w);
+      const int j0 = meta.x * kPage;
+      float s[8][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+      const uint32_t kbase = ring + sk * S::kHalf + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const uint4 w = lds128(kbase + 2 * n * D + 64 * hf);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t b0, b1;
+            codes_to_f16(ww[u], b0, b1);
+            mma16816(s[n], qf[4 * hf + u], b0, b1);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.empty(warp, sk));
+
+      // scores in log2 units, masked
+      const float ck[2] = {crow[0] * __int_as_float(meta.z), crow[1] * __int_as_float(meta.z)};
+      float top[2] = {-INFINITY, -INFINITY};
+      uint32_t see[2] = {0xffffu, 0xffffu};  // bit 2 n + i: key j0 + 16 c + 2 n + i
+      const bool tail = meta.x < 0 || j0 + kPage > all_lim;
+      if (tail || meta.y) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = meta.x < 0 ? 0 : min(max(lim[i] - (j0 + 16 * c), 0), 16);
+          see[i] = (1u << n) - 1u;
+        }
+        if constexpr (kVec) {
+          if (meta.y) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const size_t at = mrow[i] + j0 + 16 * c;
+              uint32_t hid = 0;
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                if (p.mask.lts) {
+                  const int4 a = *reinterpret_cast<const int4*>(p.mask.lts + at + 4 * q4);
+                  const int4 z = *reinterpret_cast<const int4*>(p.mask.lte + at + 4 * q4);
+                  hid |= (static_cast<uint32_t>(a.x <= pos[i] && pos[i] < z.x) |
+                          static_cast<uint32_t>(a.y <= pos[i] && pos[i] < z.y) << 1 |
+                          static_cast<uint32_t>(a.z <= pos[i] && pos[i] < z.z) << 2 |
+                          static_cast<uint32_t>(a.w <= pos[i] && pos[i] < z.w) << 3) << (4 * q4);
+                }
+                if (p.mask.uts) {
+                  const int4 a = *reinterpret_cast<const int4*>(p.mask.uts + at + 4 * q4);
+                  const int4 z = *reinterpret_cast<const int4*>(p.mask.ute + at + 4 * q4);
+                  hid |= (static_cast<uint32_t>(a.x <= pos[i] && pos[i] < z.x) |
+                          static_cast<uint32_t>(a.y <= pos[i] && pos[i] < z.y) << 1 |
+                          static_cast<uint32_t>(a.z <= pos[i] && pos[i] < z.z) << 2 |
+                          static_cast<uint32_t>(a.w <= pos[i] && pos[i] < z.w) << 3) << (4 * q4);
+                }
+              }
+              see[i] &= ~hid;
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = s[n][i] * ck[i >> 1];
+            s[n][i] = (see[i >> 1] >> (2 * n + (i & 1))) & 1u ? x : -INFINITY;
+          }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][i] *= ck[i >> 1];
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top[i] = fmax3(top[i], s[n][2 * i], s[n][2 * i + 1]);
+      uint32_t pf[4][4];
+      bool moved = false;
+      float av[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        const float m_new = fmaxf(st.m[i], top[i]), mv_new = fmaxf(st.mv[i], top[i] + lvs);
+        const float al = ex2_diff(st.m[i], m_new);
+        av[i] = ex2_diff(st.mv[i], mv_new);
+        moved |= av[i] != 1.f;
+        st.m[i] = m_new;
+        st.mv[i] = mv_new;
+        const float mu = m_new == -INFINITY ? 0.f : m_new, mvu = mv_new == -INFINITY ? 0.f : mv_new;
+        const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float p0 = ex2(s[n][2 * i] - mu), p1 = ex2(s[n][2 * i + 1] - mu);
+          sum0 += p0;
+          sum1 += p1;
+          pf[n >> 1][2 * (n & 1) + i] = pack_f16x2(p0 * f, p1 * f);
+        }
+        st.l[i] = st.l[i] * al + (sum0 + sum1);
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.acc[n][i] *= av[i >> 1];
+      }
+
+      ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sv), ((seq + 1) / kSlots) & 1, p.status));
+      if (!ok) break;
+      const uint32_t vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
+      if (!tail) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          const uint4 w = lds128(vbase + 8 * n * kPage);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t b0, b1;
+            codes_to_f16(ww[u], b0, b1);
+            mma16816(st.acc[n], pf[u], b0, b1);
+          }
+        }
+      } else if (meta.x >= 0) {
+        // codes behind the sequence's end may be anything, NaN too: they become 0
+        const int n_ok = min(max(r.len - (j0 + 16 * c), 0), 16);
+        uint32_t keep[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int nb = min(max(n_ok - 4 * u, 0), 4);
+          keep[u] = nb == 4 ? 0xffffffffu : (1u << (8 * nb)) - 1u;
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          const uint4 w = lds128(vbase + 8 * n * kPage);
+          const uint32_t ww[4] = {w.x & keep[0], w.y & keep[1], w.z & keep[2], w.w & keep[3]};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t b0, b1;
+            codes_to_f16(ww[u], b0, b1);
+            mma16816(st.acc[n], pf[u], b0, b1);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.empty(warp, sv));
+      seq += 2;
+    }
+    if (!ok) break;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 1);
+      st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 2);
+    }
+
+    // ---- the warps' states become warp 0's: 4-6 into 0-2, 2-3 into 0-1, 1 into 0
+    auto put = [&](int buf) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        merge[(buf * (D / 8) + n) * 32 + lane] =
+            make_float4(st.acc[n][0], st.acc[n][1], st.acc[n][2], st.acc[n][3]);
+      if (c == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* x = stats + (buf * kRows + g + 8 * i) * 3;
+          x[0] = st.m[i], x[1] = st.mv[i], x[2] = st.l[i];
+        }
+      }
+    };
+    auto take = [&](int buf) {
+      float fa[2], fb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* x = stats + (buf * kRows + g + 8 * i) * 3;
+        const float m = fmaxf(st.m[i], x[0]), mv = fmaxf(st.mv[i], x[1]);
+        st.l[i] = st.l[i] * ex2_diff(st.m[i], m) + x[2] * ex2_diff(x[0], m);
+        fa[i] = ex2_diff(st.mv[i], mv);
+        fb[i] = ex2_diff(x[1], mv);
+        st.m[i] = m;
+        st.mv[i] = mv;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const float4 x = merge[(buf * (D / 8) + n) * 32 + lane];
+        st.acc[n][0] = st.acc[n][0] * fa[0] + x.x * fb[0];
+        st.acc[n][1] = st.acc[n][1] * fa[0] + x.y * fb[0];
+        st.acc[n][2] = st.acc[n][2] * fa[1] + x.z * fb[1];
+        st.acc[n][3] = st.acc[n][3] * fa[1] + x.w * fb[1];
+      }
+    };
+    if (!sync_warps()) break;  // the last piece's states have been read
+    if (warp >= 4) put(warp - 4);
+    if (!sync_warps()) break;
+    if (warp + 4 < kConsumers) take(warp);
+    if (warp == 2 || warp == 3) put(warp);
+    if (!sync_warps()) break;
+    if (warp < 2) take(warp + 2);
+    if (warp == 1) put(1);
+    if (!sync_warps()) break;
+    if (warp == 0) {
+      take(1);
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int rr = rt * kRows + g + 8 * i;
+          if (rr >= rows) continue;
+          const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+          const float f = out_factor(st.m[i], st.mv[i], st.l[i]);
+          uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + 2 * c;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<uint32_t*>(o + 8 * n) = pack_bf16x2(st.acc[n][2 * i] * f, st.acc[n][2 * i + 1] * f);
+          if (c == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(st.m[i], st.l[i]);
+        }
+      } else {
+        float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(out + (g + 8 * i) * D + 8 * n + 2 * c) =
+                make_float2(st.acc[n][2 * i], st.acc[n][2 * i + 1]);
+          if (c == 0) {
+            float* x = out + kRows * D + g + 8 * i;
+            x[0] = st.m[i], x[kRows] = st.mv[i], x[2 * kRows] = st.l[i];
+          }
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          const int n = atomicAdd(&p.arrived[seg], 1);
+          if (n == parts - 1) p.arrived[seg] = 0;  // every part is there: ready for the next call
+          stats[0] = __int_as_float(n == parts - 1);
+          __threadfence();
+        }
+      }
+    }
+    if (!whole) {
+      if (!sync_warps()) break;
+      const bool finish = __float_as_int(stats[0]) != 0;
+      if (finish) {
+        // every part, in the order of the keys: 16 threads a row, D / 16 columns each
+        __threadfence();
+        constexpr int kCols = D / 16;
+        const int col = (tid & 15) * kCols;
+        auto part_at = [&](int i) {
+          return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
+        };
+        for (int row = tid >> 4; row < kRows; row += 2 * kConsumers) {
+          float m = -INFINITY, mv = -INFINITY, l = 0.f;
+          for (int i = 0; i < parts; ++i) {
+            const float* x = part_at(i) + kRows * D + row;
+            m = fmaxf(m, __ldcg(x));
+            mv = fmaxf(mv, __ldcg(x + kRows));
+          }
+          float sum[kCols];
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) sum[k] = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < parts; ++i) {
+            const float* x = part_at(i);
+            l += __ldcg(x + kRows * D + 2 * kRows + row) * ex2_diff(__ldcg(x + kRows * D + row), m);
+            const float f = ex2_diff(__ldcg(x + kRows * D + kRows + row), mv);
+#pragma unroll
+            for (int k = 0; k < kCols; k += 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(x + row * D + col + k));
+              sum[k] += v.x * f;
+              sum[k + 1] += v.y * f;
+              sum[k + 2] += v.z * f;
+              sum[k + 3] += v.w * f;
+            }
+          }
+          const int rr = rt * kRows + row;
+          if (rr < rows) {
+            const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+            const float f = out_factor(m, mv, l);
+            uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + col;
+#pragma unroll
+            for (int k = 0; k < kCols; k += 2)
+              *reinterpret_cast<uint32_t*>(o + k) = pack_bf16x2(sum[k] * f, sum[k + 1] * f);
+            if ((tid & 15) == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(m, l);
+          }
+        }
+      }
+      if (!sync_warps()) break;  // stats[0] has been read
+    }
+  }
+
+  // segments without a visible page: O = 0, LSE = -inf
+  for (int seg = blockIdx.x + gridDim.x * warp; ok && seg < nseg; seg += gridDim.x * kConsumers) {
+    if (pages_of<kVec>(p, geo, seg) != 0) continue;
+    const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const RowTile r = row_tile(p, geo.G, b, rt, lane == 0);
+    const int row_hi = min(geo.G * r.live, (rt + 1) * kRows);
+    for (int rr = rt * kRows; rr < row_hi; ++rr) {
+      const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2];
+      for (int k = lane; k < D / 2; k += 32) *reinterpret_cast<uint32_t*>(o + 2 * k) = 0u;
+      if (lane == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = -INFINITY;
+    }
+  }
+}
+
+template <int D, bool kVec>
+cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  if (kVec) {
+    const dim3 grid(static_cast<unsigned>(geo.words), static_cast<unsigned>(geo.classes * geo.RT),
+                    static_cast<unsigned>(p.B));
+    cache_classify<<<grid, 256, 0, s>>>(p, geo);
+  }
+  const cudaError_t e = cudaFuncSetAttribute(cache_fwd_kernel<D, kVec>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
+  cache_fwd_kernel<D, kVec><<<grid, kThreads, Smem<D>::kBytes, s>>>(p, geo);
+  return cudaGetLastError();
+}
+
+Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
+  Geometry g;
+  g.G = H / Hk;
+  g.RT = static_cast<int>((static_cast<long long>(g.G) * N + kRows - 1) / kRows);
+  g.classes = Hk % Hm == 0 ? Hm : Hk;
+  g.words = (max_pages + 31) / 32;
+  return g;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.B) * p.H * p.N;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
+  const Geometry g = geometry(H, Hk, Hk, N, max_pages);
+  const size_t tiles = static_cast<size_t>(B) * Hk * g.RT;
+  CacheWs w;
+  size_t off = 256;  // the status word
+  w.arrived = off;
+  off = up256(off + tiles * 4);
+  w.class_done = off;
+  off = up256(off + tiles * 4);
+  w.partial = off;
+  off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 * part_floats(d) * 4);
+  w.vis = off;
+  off = up256(off + tiles * g.words * 4);
+  w.part = off;
+  off = up256(off + tiles * g.words * 4);
+  w.prefix = off;
+  off = up256(off + tiles * (g.words + 1) * 4);
+  w.total = off;
+  return w;
+}
+
+cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s) {
+  const Geometry geo = geometry(p.H, p.c.Hk, p.mask.Hm, p.N, p.max_pages);
+  const bool vec = p.mask.lts != nullptr || p.mask.uts != nullptr;
   if (d == 64)
-    cache_fwd_simple<64><<<grid, 128, 0, s>>>(p);
-  else
-    cache_fwd_simple<128><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+    return vec ? launch_t<64, true>(p, geo, num_sms, s) : launch_t<64, false>(p, geo, num_sms, s);
+  return vec ? launch_t<128, true>(p, geo, num_sms, s) : launch_t<128, false>(p, geo, num_sms, s);
 }
 
 }  // namespace fm

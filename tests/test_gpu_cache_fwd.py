@@ -354,7 +354,9 @@ def test_out_of_range_is_recorded(N):
         ld = torch.tensor([n, 200], dtype=torch.int32, device="cuda")
         o, lse = fm.flashmask_fwd_cache(q, cache, table.clamp(max=cache.k8.shape[0] - 1), ld, ws)
         assert fm.flashmask_check_status(ws) == (fm.FM_ERR_PAGE, 403)
-        assert torch.equal(o[1], want[0][1])
+        # sequence 1 is right; its bits may differ, because the line of pages is
+        # cut elsewhere when another sequence's length changes
+        check(o[1:], lse[1:], q[1:], cache, table[1:], lens[1:])
 
 
 @pytest.fixture(scope="module")
