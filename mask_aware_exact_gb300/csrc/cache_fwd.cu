@@ -35,6 +35,8 @@
 // 16-byte load of a V column is exactly the operand that meets its P. The summed
 // index d of S is permuted in the same way: a lane reads 16 consecutive codes of a
 // key, and the query is laid out to match.
+#include <atomic>
+
 #include "cache.h"
 #include "flashmask.h"
 #include "ptx_fp8.cuh"
@@ -46,7 +48,8 @@ constexpr int kConsumers = 7;  // with the producer 8 warps: two for each schedu
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kRows = 16;      // rows of a tile
 constexpr int kSlots = 3;      // ring slots of a consumer warp
-constexpr int kPieceRing = 4;  // piece descriptors in flight
+constexpr int kPieceRing = 16;  // piece descriptors in flight: more than twice what a group can start
+constexpr int kBatch = 4 * kConsumers;  // tiles looked up at a time, one per lane
 // Pages a run has at least: one for each consumer warp. Shorter runs only
 // add partial results.
 constexpr int kMinRun = kConsumers;
@@ -248,7 +251,7 @@ struct Smem {
   static constexpr int kMerge = kRing + kConsumers * kSlots * kHalf;  // fp32 [4][D / 8][32][4]
   static constexpr int kStats = kMerge + 4 * kRows * D * 4;          // float [4][16][3]: m, mv, l
   static constexpr int kMeta = kStats + 4 * kRows * 3 * 4;  // int4 [consumer][slot]
-  static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8]
+  static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8], see below
   static constexpr int kBars = kPiece + kPieceRing * 32;
   static constexpr int kNumBars = 2 * kConsumers * kSlots + 2 * kPieceRing + 1;
   static constexpr int kScan = kBars + kNumBars * 8;  // long long [16]
@@ -266,10 +269,9 @@ struct Bars {
   __device__ uint32_t merge() const { return base + 8 * (2 * kConsumers * kSlots + 2 * kPieceRing); }
 };
 
-// One piece of a segment: tiles [first, first + count) of the CTA's run.
-struct Piece {
-  int seg, first, count, whole, slot, cta0, parts, pad;
-};
+// A piece descriptor, int[8]: segment, first tile in the CTA's run, tiles (0: the
+// end), whole segment?, slot of its partial result, first CTA and number of the
+// segment's parts.
 
 // Floats of one partial result in the workspace: O [16][D], then m, mv, l [16] each.
 __host__ __device__ constexpr int part_floats(int D) { return kRows * D + 3 * kRows; }
@@ -366,23 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     int seg = static_cast<int>(scan[12]), k = static_cast<int>(scan[13]);
     const int tiles = static_cast<int>(run_hi - run_lo);
     bool ok = true;
-    int pieces = 0;
-    auto publish = [&](const Piece& d) {
-      const int e = pieces % kPieceRing;
-      if (pieces >= kPieceRing)
-        ok = __all_sync(0xffffffffu, ok && cache_wait(bar.piece_empty(e), (pieces / kPieceRing - 1) & 1, p.status));
-      ++pieces;
-      if (lane == 0 && ok) {
-        int* at = reinterpret_cast<int*>(smem + S::kPiece) + 8 * e;
-        at[0] = d.seg, at[1] = d.first, at[2] = d.count, at[3] = d.whole;
-        at[4] = d.slot, at[5] = d.cta0, at[6] = d.parts;
-        mbar_arrive(bar.piece_full(e));
-      }
-      __syncwarp();
-    };
+    int pieces = 0;  // published so far
     int done = 0;
     while (ok && done < tiles) {
-      // the next 32 tiles of the run, one per lane, over the next 32 segments
+      // the next tiles of the run, one per lane, over the next 32 segments
       const int s_l = seg + lane;
       int n = s_l < nseg ? pages_of<kVec>(p, geo, s_l) : 0;
       const int n_all = n;
@@ -394,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
         // sums past 2^30 are only compared with tile numbers below 32
         if (lane >= o) c = min(c + x, 1 << 30);
       }
-      const int avail = min(min(__shfl_sync(0xffffffffu, c, 31), 32), tiles - done);
+      const int avail = min(min(__shfl_sync(0xffffffffu, c, 31), kBatch), tiles - done);
       int j = 0;  // segments that end at or before this lane's tile
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) {
@@ -432,35 +421,46 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
           lvs = log2f(p.c.vscale[ph]);
         }
       }
-      for (int t = 0; ok && t < avail; ++t) {
-        const int sg = __shfl_sync(0xffffffffu, my_seg, t), kk = __shfl_sync(0xffffffffu, my_k, t);
-        const int nn = __shfl_sync(0xffffffffu, n_j, t);
-        if (done == 0 || kk == 0) {
-          Piece d;
-          d.seg = sg;
-          d.first = done;
-          d.count = min(nn - kk, tiles - done);
-          d.whole = kk == 0 && d.count == nn;
-          d.slot = kk == 0 ? 1 : 0;
-          const long long s0 = run_lo + done - kk;
-          d.cta0 = static_cast<int>(s0 / run);
-          d.parts = static_cast<int>((s0 + nn - 1) / run) - d.cta0 + 1;
-          publish(d);
+      // one tile for each consumer warp at a time, issued by as many lanes. A lane
+      // waits only for slots that tiles of earlier groups leave, and for piece
+      // entries of earlier groups, so the lanes never wait for one another.
+      for (int base = 0; ok && base < avail; base += kConsumers) {
+        const int in_group = min(kConsumers, avail - base), src = min(base + lane, 31);
+        const int sg = __shfl_sync(0xffffffffu, my_seg, src), kk = __shfl_sync(0xffffffffu, my_k, src);
+        const int nn = __shfl_sync(0xffffffffu, n_j, src), pg = __shfl_sync(0xffffffffu, page, src);
+        const int lg = __shfl_sync(0xffffffffu, logical, src), ct = __shfl_sync(0xffffffffu, cut, src);
+        const float k_s = __shfl_sync(0xffffffffu, ks, src), v_s = __shfl_sync(0xffffffffu, lvs, src);
+        const int at = done + lane;  // number of the tile in the run
+        const bool mine_too = lane < in_group;
+        const bool starts = mine_too && (at == 0 || kk == 0);
+        const uint32_t who = __ballot_sync(0xffffffffu, starts);
+        if (starts) {
+          const int n = pieces + __popc(who & ((1u << lane) - 1u)), e = n % kPieceRing;
+          if (n >= kPieceRing) ok = cache_wait(bar.piece_empty(e), (n / kPieceRing - 1) & 1, p.status);
+          if (ok) {
+            const int count = min(nn - kk, tiles - at);
+            const long long s0 = run_lo + at - kk;
+            const int cta0 = static_cast<int>(s0 / run);
+            int* d = reinterpret_cast<int*>(smem + S::kPiece) + 8 * e;
+            d[0] = sg, d[1] = at, d[2] = count, d[3] = kk == 0 && count == nn;
+            d[4] = kk == 0 ? 1 : 0, d[5] = cta0;
+            d[6] = static_cast<int>((s0 + nn - 1) / run) - cta0 + 1;
+            mbar_arrive(bar.piece_full(e));
+          }
         }
-        const int pg = __shfl_sync(0xffffffffu, page, t);
-        const int w = done % kConsumers, q = 2 * (done / kConsumers);
-        const int lg = __shfl_sync(0xffffffffu, logical, t), ct = __shfl_sync(0xffffffffu, cut, t);
-        const float k_s = __shfl_sync(0xffffffffu, ks, t), v_s = __shfl_sync(0xffffffffu, lvs, t);
-        if (lane == 0 && ok) {
+        pieces += __popc(who);
+        if (mine_too && ok) {
+          const int w = at % kConsumers, q = 2 * (at / kConsumers);
           const int hk = (sg / geo.RT) % p.c.Hk;
           const size_t off = (static_cast<size_t>(max(pg, 0)) * p.c.Hk + hk) * S::kHalf;
 #pragma unroll
-          for (int half = 0; half < 2 && ok; ++half) {
+          for (int half = 0; half < 2; ++half) {
             const int seq = q + half, slot = seq % kSlots;
-            if (seq >= kSlots) ok = cache_wait(bar.empty(w, slot), (seq / kSlots - 1) & 1, p.status);
+            if (seq >= kSlots) ok = ok && cache_wait(bar.empty(w, slot), (seq / kSlots - 1) & 1, p.status);
             if (!ok) break;
-            int4* meta = reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot;
-            *meta = make_int4(pg < 0 ? -1 : lg, ct, __float_as_int(half ? v_s : k_s), __float_as_int(v_s));
+            if (half == 0)
+              *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot) =
+                  make_int4(pg < 0 ? -1 : lg, ct, __float_as_int(k_s), __float_as_int(v_s));
             if (pg >= 0) {
               mbar_arrive_expect_tx(bar.full(w, slot), S::kHalf);
               bulk_load(smem_u32(smem + S::kRing + (w * kSlots + slot) * S::kHalf),
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
           }
         }
         ok = __all_sync(0xffffffffu, ok);
-        ++done;
+        done += in_group;
       }
       // the tile behind the last one taken
       if (avail > 0) {
@@ -482,8 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
         k = 0;
       }
     }
-    Piece end = {};
-    if (ok) publish(end);
+    if (ok && lane == 0) {  // the end: an empty piece
+      const int e = pieces % kPieceRing;
+      if (pieces >= kPieceRing) ok = cache_wait(bar.piece_empty(e), (pieces / kPieceRing - 1) & 1, p.status);
+      if (ok) {
+        (reinterpret_cast<int*>(smem + S::kPiece) + 8 * e)[2] = 0;
+        mbar_arrive(bar.piece_full(e));
+      }
+    }
     if (!ok && lane == 0) {
       // copies in flight land before the CTA's shared memory is given up
       for (int w = 0; w < kConsumers; ++w)
@@ -895,6 +901,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   }
 }
 
+// Lets the kernel have its shared memory, once for each device.
+template <int D, bool kVec>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done[4];  // devices 0 .. 255
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev > 255) return cudaErrorInvalidDevice;
+  if (done[dev >> 6].load(std::memory_order_relaxed) >> (dev & 63) & 1) return cudaSuccess;
+  e = cudaFuncSetAttribute(cache_fwd_kernel<D, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<D>::kBytes);
+  if (e == cudaSuccess) done[dev >> 6].fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  return e;
+}
+
 template <int D, bool kVec>
 cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
   if (kVec) {
@@ -902,8 +923,7 @@ cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, 
                     static_cast<unsigned>(p.B));
     cache_classify<<<grid, 256, 0, s>>>(p, geo);
   }
-  const cudaError_t e = cudaFuncSetAttribute(cache_fwd_kernel<D, kVec>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  const cudaError_t e = allow_smem<D, kVec>();
   if (e != cudaSuccess) return e;
   const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
   cache_fwd_kernel<D, kVec><<<grid, kThreads, Smem<D>::kBytes, s>>>(p, geo);

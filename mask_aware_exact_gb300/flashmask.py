@@ -9,8 +9,8 @@ binding still works but the first call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -481,42 +481,38 @@ def flashmask_selftest_timeout(ws: torch.Tensor, limit_ns: int, ctas: int = 1, s
 # ---------------------------------------------------------------- rotary positions
 _ROPE_DTYPES = {torch.bfloat16: FM_BF16, torch.float16: FM_F16, torch.float32: FM_F32}
 _Strides = ctypes.c_int64 * 3
+_HeadsPair = _FmHeads * 2
 
 
-@contextlib.contextmanager
-def _on(device, stream, *inputs):
-    """The raw stream to launch on: `stream`, or the current one of `device`. With
-    a stream of its own the call's outputs are allocated for that stream and its
-    inputs are kept until it has passed the call."""
+def _launch(index, stream, tensors, call):
+    """call(raw stream) on device `index`: on `stream`, or on that device's current
+    one. With a stream of its own the call's outputs are allocated for that stream
+    and its inputs are kept until it has passed the call."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.device(device):
-                yield torch.cuda.current_stream(device).cuda_stream
-    else:
-        if stream.device != device:
-            raise ValueError("stream and tensors must be on the same device")
-        for t in inputs:
-            if t is not None:
-                t.record_stream(stream)
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+        if index == torch._C._cuda_getDevice():
+            return call(torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    if stream.device.index != index:
+        raise ValueError("stream and tensors must be on the same device")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-def _want(t, name, dtype, device, shape=None, contiguous=True):
-    if t.dtype != dtype or t.device != device or (shape is not None and t.shape != shape) or \
-            (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name} must be a{' contiguous' if contiguous else ''} {dtype} tensor"
-                         f"{'' if shape is None else ' ' + str(list(shape))} on {device}")
+def _want(t, name, dtype, index, shape):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
 
 
-def _rows(t, name, dtype, device):
+def _rows(t, name, dtype, index):
     """[B, H, N, d] with any strides but a contiguous last dimension."""
-    if t.dim() != 4 or t.dtype != dtype or t.device != device or not t.is_cuda or \
+    if t.dtype is not dtype or t.get_device() != index or index < 0 or t.dim() != 4 or \
             (t.stride(3) != 1 and t.shape[3] != 1):
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor [B, H, N, d] on {device} with a "
-                         "contiguous last dimension")
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor [B, H, N, d] with a contiguous last "
+                         f"dimension, on the same device as the others")
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -548,47 +544,52 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
 
 
 def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, where):
-    if q.dtype not in _ROPE_DTYPES:
+    dtype = _ROPE_DTYPES.get(q.dtype)
+    if dtype is None:
         raise ValueError("q must be bf16, fp16 or fp32")
-    dev = q.device
-    xs = (q,) if k is None else (q, k)
-    for t, n in zip(xs, "qk"):
-        _rows(t, n, q.dtype, dev)
-    B, _, N, d = q.shape
-    if k is not None and (k.shape[0] != B or k.shape[2] != N or k.shape[3] != d):
-        raise ValueError("q and k must share B, N and d")
+    index = q.get_device()
+    _rows(q, "q", q.dtype, index)
+    B, Hq, N, d = q.shape
+    xs = (q,)
+    if k is not None:
+        _rows(k, "k", q.dtype, index)
+        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+            raise ValueError("q and k must share B, N and d")
+        xs = (q, k)
     rot = 2 * freqs.numel()
-    _want(freqs, "freqs", torch.float64, dev)
-    if freqs.dim() != 1 or rot > d:
+    _want(freqs, "freqs", torch.float64, index, (rot // 2,))
+    if rot > d:
         raise ValueError("freqs must be [rot_dim / 2] with rot_dim <= d")
-    pos_stride = 0
+    pos, pos_stride = None, 0
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.device != dev or positions.dim() != 2 or \
-                positions.shape[0] not in (1, B) or positions.shape[1] != N or \
-                (N > 1 and positions.stride(1) != 1):
-            raise ValueError(f"positions must be int32 [{B}, {N}] or [1, {N}] on {dev}, rows contiguous")
-        pos_stride = positions.stride(0) if positions.shape[0] == B and B > 1 else 0
-    with _on(dev, stream, q, k, freqs, positions) as raw:
-        if out is None:
-            ys = tuple(torch.empty(t.shape, dtype=t.dtype, device=dev) for t in xs)
-        else:
-            ys = tuple(out)[:len(xs)]
-            for t, x in zip(ys, xs):
-                _rows(t, "out", q.dtype, dev)
-                if t.shape != x.shape:
-                    raise ValueError("out must have the shapes of q and k")
-                if stream is not None:
-                    t.record_stream(stream)
+        if positions.dtype is not torch.int32 or positions.get_device() != index or \
+                positions.dim() != 2 or positions.shape[1] != N or \
+                positions.shape[0] not in (1, B) or (N > 1 and positions.stride(1) != 1):
+            raise ValueError(f"positions must be int32 [{B}, {N}] or [1, {N}] on cuda:{index}, rows "
+                             "contiguous")
+        pos = positions.data_ptr()
+        pos_stride = positions.stride(0) if positions.shape[0] > 1 else 0
+    if out is not None:
+        out = tuple(out)[:len(xs)]
+        for t, x in zip(out, xs):
+            _rows(t, "out", q.dtype, index)
+            if t.shape != x.shape:
+                raise ValueError("out must have the shapes of q and k")
+
+    def call(raw):
+        ys = out or [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
         if B * N * d > 0:
-            heads = (_FmHeads * len(xs))(*[
-                _FmHeads(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride()[:3], y.stride()[:3])
-                for x, y in zip(xs, ys)])
-            _check(load().flashmask_rope(heads, len(xs),
-                                         None if positions is None else positions.data_ptr(),
-                                         pos_stride, freqs.data_ptr(), B, N, d, rot,
-                                         int(bool(interleaved)), _ROPE_DTYPES[q.dtype],
-                                         float(mscale), inverse, raw), where)
-    return ys[0], (ys[1] if k is not None else None)
+            heads = _HeadsPair()
+            for h, x, y in zip(heads, xs, ys):
+                h.x, h.y, h.H = x.data_ptr(), y.data_ptr(), x.shape[1]
+                h.xs[:], h.ys[:] = x.stride()[:3], y.stride()[:3]
+            st = load().flashmask_rope(heads, len(xs), pos, pos_stride, freqs.data_ptr(), B, N, d, rot,
+                                       bool(interleaved), dtype, mscale, inverse, raw)
+            if st:
+                raise FlashMaskError(st, where)
+        return ys[0], (ys[1] if k is not None else None)
+
+    return _launch(index, stream, (*xs, freqs, positions, *(out or ())), call)
 
 
 def flashmask_rope(q, k, freqs, positions=None, interleaved=False, mscale=1.0, out=None,
@@ -610,11 +611,12 @@ def flashmask_rope_bwd(dq, dk, freqs, positions=None, interleaved=False, mscale=
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
     """Keys and values as e4m3 codes in pages of FM_PAGE tokens with one scale per
     page and head: k8 [pages, Hk, 64, d], v8 [pages, Hk, d, 64] (float8_e4m3fn,
-    V transposed), kscale, vscale fp32 [pages, Hk]."""
+    V transposed), kscale, vscale fp32 [pages, Hk]. A handle: its tensors are
+    checked once, at its first use."""
 
     k8: torch.Tensor
     v8: torch.Tensor
@@ -628,17 +630,27 @@ class KVCache:
                        torch.zeros((pages, Hk, d, FM_PAGE), **f8),
                        torch.ones((pages, Hk), device=device), torch.ones((pages, Hk), device=device))
 
-    def c_struct(self) -> _FmCache:
-        k8, v8 = self.k8, self.v8
-        if k8.dim() != 4 or k8.shape[2] != FM_PAGE or not k8.is_cuda:
+    @property
+    def tensors(self):
+        return self.k8, self.v8, self.kscale, self.vscale
+
+    @functools.cached_property
+    def _handle(self):
+        """(C struct, Hk, d, device index)"""
+        k8 = self.k8
+        index = k8.get_device()
+        if k8.dim() != 4 or k8.shape[2] != FM_PAGE or index < 0:
             raise ValueError("k8 must be a CUDA tensor [pages, Hk, 64, d]")
         pages, Hk, _, d = k8.shape
-        _want(k8, "k8", torch.float8_e4m3fn, k8.device)
-        _want(v8, "v8", torch.float8_e4m3fn, k8.device, (pages, Hk, d, FM_PAGE))
-        _want(self.kscale, "kscale", torch.float32, k8.device, (pages, Hk))
-        _want(self.vscale, "vscale", torch.float32, k8.device, (pages, Hk))
-        return _FmCache(k8.data_ptr(), v8.data_ptr(), self.kscale.data_ptr(), self.vscale.data_ptr(),
-                        pages, Hk, d)
+        _want(k8, "k8", torch.float8_e4m3fn, index, k8.shape)
+        _want(self.v8, "v8", torch.float8_e4m3fn, index, (pages, Hk, d, FM_PAGE))
+        _want(self.kscale, "kscale", torch.float32, index, (pages, Hk))
+        _want(self.vscale, "vscale", torch.float32, index, (pages, Hk))
+        return _FmCache(k8.data_ptr(), self.v8.data_ptr(), self.kscale.data_ptr(),
+                        self.vscale.data_ptr(), pages, Hk, d), Hk, d, index
+
+    def c_struct(self) -> _FmCache:
+        return self._handle[0]
 
 
 def flashmask_cache_workspace_bytes(B, H, Hk, N, d, max_pages) -> int:
@@ -655,16 +667,17 @@ def alloc_cache_workspace(B, H, Hk, N, d, max_pages, device="cuda") -> torch.Ten
     return ws
 
 
-def _per_sequence(t, name, B, device):
-    if t is not None:
-        _want(t, name, torch.int32, device, (B,))
-    return None if t is None else t.data_ptr()
+def _per_sequence(t, name, B, index):
+    if t is None:
+        return None
+    _want(t, name, torch.int32, index, (B,))
+    return t.data_ptr()
 
 
-def _page_table(t, B, device):
+def _page_table(t, B, index):
     if t.dim() != 2:
         raise ValueError("page_table must be int32 [B, max_pages]")
-    _want(t, "page_table", torch.int32, device, (B, t.shape[1]))
+    _want(t, "page_table", torch.int32, index, (B, t.shape[1]))
     return t.shape[1]
 
 
@@ -673,22 +686,25 @@ def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=No
     start[b] tokens that sequence b holds; count[b] <= N of its rows are real.
     page_table int32 [B, max_pages]; start, count int32 [B]. See
     include/flashmask.h for scales and rounding."""
-    c = cache.c_struct()
-    dev = cache.k8.device
-    _rows(k, "k", torch.bfloat16, dev)
-    _rows(v, "v", torch.bfloat16, dev)
-    B, Hk, N, d = k.shape
-    if v.shape != k.shape or Hk != c.Hk or d != c.d:
+    c, Hk, d, index = cache._handle
+    _rows(k, "k", torch.bfloat16, index)
+    _rows(v, "v", torch.bfloat16, index)
+    B, _, N, _ = k.shape
+    if v.shape != k.shape or k.shape[1] != Hk or k.shape[3] != d:
         raise ValueError("k and v must be [B, Hk, N, d] with the cache's Hk and d")
-    max_pages = _page_table(page_table, B, dev)
-    st, ct = _per_sequence(start, "start", B, dev), _per_sequence(count, "count", B, dev)
-    _want(ws, "ws", torch.uint8, dev)
-    with _on(dev, stream, cache.k8, cache.v8, cache.kscale, cache.vscale, page_table, k, v, start,
-             count, ws) as raw:
-        _check(load().flashmask_cache_append(ctypes.byref(c), page_table.data_ptr(), max_pages,
-                                             k.data_ptr(), _Strides(*k.stride()[:3]), v.data_ptr(),
+    max_pages = _page_table(page_table, B, index)
+    st, ct = _per_sequence(start, "start", B, index), _per_sequence(count, "count", B, index)
+    _want(ws, "ws", torch.uint8, index, (ws.numel(),))
+
+    def call(raw):
+        code = load().flashmask_cache_append(c, page_table.data_ptr(), max_pages, k.data_ptr(),
+                                             _Strides(*k.stride()[:3]), v.data_ptr(),
                                              _Strides(*v.stride()[:3]), st, ct, B, N, ws.data_ptr(),
-                                             ws.numel(), raw), "flashmask_cache_append")
+                                             ws.numel(), raw)
+        if code:
+            raise FlashMaskError(code, "flashmask_cache_append")
+
+    _launch(index, stream, (*cache.tensors, page_table, k, v, start, count, ws), call)
 
 
 def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMask | None = None,
@@ -699,37 +715,45 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
     else a DeviceMask whose vectors are [B, Hm, 64 * max_pages] (lts and lte may
     be None). Returns (O bf16 like q, LSE fp32 [B, H, N]); rows behind q_lens[b]
     of `o` and `lse` are left as they were."""
-    c = cache.c_struct()
-    dev = cache.k8.device
-    _rows(q, "q", torch.bfloat16, dev)
-    B, H, N, d = q.shape
-    if d != c.d:
+    c, _, d, index = cache._handle
+    _rows(q, "q", torch.bfloat16, index)
+    B, H, N, _ = q.shape
+    if q.shape[3] != d:
         raise ValueError("q must have the cache's d")
-    max_pages = _page_table(page_table, B, dev)
-    ln, ql = _per_sequence(lens, "lens", B, dev), _per_sequence(q_lens, "q_lens", B, dev)
-    _want(ws, "ws", torch.uint8, dev)
-    vectors = () if mask is None else (mask.lts, mask.lte, mask.uts, mask.ute)
-    m = None
+    max_pages = _page_table(page_table, B, index)
+    ln, ql = _per_sequence(lens, "lens", B, index), _per_sequence(q_lens, "q_lens", B, index)
+    _want(ws, "ws", torch.uint8, index, (ws.numel(),))
+    vectors, m = (), None
     if mask is not None:
-        given = [t for t in vectors if t is not None]
-        Hm = given[0].shape[1] if given and given[0].dim() == 3 else 1
-        for t in given:
-            _want(t, "mask vectors", torch.int32, dev, (B, Hm, max_pages * FM_PAGE))
-        m = _FmMask(*[None if t is None else t.data_ptr() for t in vectors], Hm, int(mask.causal))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with _on(dev, stream, q, cache.k8, cache.v8, cache.kscale, cache.vscale, page_table, lens, q_lens,
-             ws, o, lse, *vectors) as raw:
-        if o is None:
-            o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-        _rows(o, "o", torch.bfloat16, dev)
-        _want(lse, "lse", torch.float32, dev, (B, H, N))
+        vectors = (mask.lts, mask.lte, mask.uts, mask.ute)
+        Hm, ptrs = 1, []
+        for t in vectors:
+            if t is not None:
+                Hm = t.shape[1] if t.dim() == 3 else -1
+        for t in vectors:
+            if t is not None:
+                _want(t, "mask vectors", torch.int32, index, (B, Hm, max_pages * FM_PAGE))
+            ptrs.append(None if t is None else t.data_ptr())
+        m = _FmMask(*ptrs, Hm, bool(mask.causal))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if o is not None:
+        _rows(o, "o", torch.bfloat16, index)
         if o.shape != q.shape:
             raise ValueError("o must have q's shape")
-        _check(load().flashmask_fwd_cache(q.data_ptr(), _Strides(*q.stride()[:3]), ctypes.byref(c),
-                                          page_table.data_ptr(), max_pages, ln, ql,
-                                          None if m is None else ctypes.byref(m), B, H, N, scale,
-                                          o.data_ptr(), _Strides(*o.stride()[:3]), lse.data_ptr(),
-                                          ws.data_ptr(), ws.numel(), raw), "flashmask_fwd_cache")
-    return o, lse
+    if lse is not None:
+        _want(lse, "lse", torch.float32, index, (B, H, N))
+
+    def call(raw):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        norm = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
+        code = load().flashmask_fwd_cache(q.data_ptr(), _Strides(*q.stride()[:3]), c,
+                                          page_table.data_ptr(), max_pages, ln, ql, m, B, H, N, scale,
+                                          out.data_ptr(), _Strides(*out.stride()[:3]), norm.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), raw)
+        if code:
+            raise FlashMaskError(code, "flashmask_fwd_cache")
+        return out, norm
+
+    return _launch(index, stream, (q, *cache.tensors, page_table, lens, q_lens, ws, o, lse, *vectors),
+                   call)
