@@ -75,6 +75,8 @@ struct CacheWs {
   size_t arrived, class_done, partial, vis, part, prefix, total;
 };
 constexpr int kCacheMaxCtas = 256;  // partial results are kept for at most this many CTAs
+// Whether the pages of all row tiles can be counted in 32 bits.
+bool cache_line_ok(int B, int H, int Hk, int N, int max_pages);
 CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages);
 cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s);
 

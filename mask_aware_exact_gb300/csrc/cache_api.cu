@@ -44,7 +44,8 @@ bool cache_shape_ok(int B, int H, int Hk, int N, int d, int max_pages) {
   if (d != 64 && d != 128) return false;
   if (H % Hk != 0 || Hk > 65535) return false;
   if (max_pages > FM_MAX_SEQLEN / FM_PAGE || N > FM_MAX_SEQLEN) return false;
-  return static_cast<long long>(B) * H <= 0x7fffffffLL / N;
+  if (static_cast<long long>(B) * H > 0x7fffffffLL / N) return false;
+  return fm::cache_line_ok(B, H, Hk, N, max_pages);
 }
 
 fm_status cache_ok(const fm_cache* c) {

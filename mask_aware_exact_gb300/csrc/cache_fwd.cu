@@ -11,14 +11,16 @@
 // per CTA (one CTA per SM), whatever the lengths of the sequences. A run covers
 // pieces of one or more segments; a segment cut by a run border leaves partial
 // results in the workspace and the CTA that finishes last adds them in order, so
-// results do not depend on timing. With a column-wise mask a first kernel marks
+// results do not depend on timing. Where every segment is short (32 pages or an
+// eighth of a run) the borders move to segment ends: nothing is cut, and the
+// imbalance costs less than the joins. With a column-wise mask a first kernel marks
 // the pages that are visible to a row tile, and only those are on the line.
 //
 // One producer warp walks the run and loads pages (K codes, V codes: 64 * d bytes
 // each, contiguous) with bulk copies into a ring of three slots for each of seven
 // consumer warps; tile i of the run goes to warp i mod 7. The warps keep separate
-// softmax states and merge them when a piece ends; the producer is then already
-// loading the next piece.
+// softmax states. When a piece ends each leaves its state in shared memory and goes
+// on with the next piece; the last to arrive adds them up.
 //
 // Arithmetic. Codes become fp16 (exact) and enter m16n8k16 instructions with fp32
 // accumulators; tcgen05 would need 128 rows. The query row is scaled by a power of
@@ -53,6 +55,7 @@ constexpr int kBatch = 4 * kConsumers;  // tiles looked up at a time, one per la
 // Pages a run has at least: one for each consumer warp. Shorter runs only
 // add partial results.
 constexpr int kMinRun = kConsumers;
+constexpr int kUncut = 32;  // segments up to this many pages are not cut
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 
 // ---------------------------------------------------------------- geometry
@@ -199,7 +202,7 @@ __device__ __forceinline__ int nth_bit(uint32_t x, int k) {
 
 // ---------------------------------------------------------------- instructions
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -211,15 +214,13 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
   return r;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -241,6 +242,20 @@ __device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_
   }
   return true;
 }
+// The same for a counter in shared memory that only grows.
+__device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* status) {
+  const volatile int* at = count;
+  const uint64_t t0 = global_timer_ns();
+  while (*at < want) {
+    if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
+    if (global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
+      record_failure(status, kStatusTimeout, kSiteCacheWait);
+      return false;
+    }
+  }
+  __threadfence_block();
+  return true;
+}
 // 2^(a - b) where either may be -inf (then a is, or both are).
 __device__ __forceinline__ float ex2_diff(float a, float b) { return a == b ? 1.f : ex2(a - b); }
 
@@ -248,14 +263,14 @@ template <int D>
 struct Smem {
   static constexpr int kHalf = kPage * D;  // bytes of a page's K or V
   static constexpr int kRing = 0;          // [consumer][slot]
-  static constexpr int kMerge = kRing + kConsumers * kSlots * kHalf;  // fp32 [4][D / 8][32][4]
-  static constexpr int kStats = kMerge + 4 * kRows * D * 4;          // float [4][16][3]: m, mv, l
-  static constexpr int kMeta = kStats + 4 * kRows * 3 * 4;  // int4 [consumer][slot]
+  static constexpr int kMerge = kRing + kConsumers * kSlots * kHalf;  // float4 [consumer][D / 8][32]
+  static constexpr int kStats = kMerge + kConsumers * kRows * D * 4;  // float [consumer][3][16]: m, mv, l
+  static constexpr int kMeta = kStats + kConsumers * kRows * 3 * 4;   // int4 [consumer][slot]
   static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8], see below
   static constexpr int kBars = kPiece + kPieceRing * 32;
   static constexpr int kNumBars = 2 * kConsumers * kSlots + 2 * kPieceRing + 1;
-  static constexpr int kScan = kBars + kNumBars * 8;  // long long [16]
-  static constexpr int kBytes = kScan + 16 * 8;
+  static constexpr int kScan = kBars + kNumBars * 8;  // int [32], see the kernel
+  static constexpr int kBytes = kScan + 32 * 4;
 };
 static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory per CTA");
 static_assert(Smem<128>::kScan % 8 == 0 && Smem<64>::kScan % 8 == 0, "alignment");
@@ -266,14 +281,15 @@ struct Bars {
   __device__ uint32_t empty(int w, int s) const { return base + 8 * ((kConsumers + w) * kSlots + s); }
   __device__ uint32_t piece_full(int s) const { return base + 8 * (2 * kConsumers * kSlots + s); }
   __device__ uint32_t piece_empty(int s) const { return base + 8 * (2 * kConsumers * kSlots + kPieceRing + s); }
-  __device__ uint32_t merge() const { return base + 8 * (2 * kConsumers * kSlots + 2 * kPieceRing); }
+  __device__ uint32_t done() const { return base + 8 * (2 * kConsumers * kSlots + 2 * kPieceRing); }
 };
 
 // A piece descriptor, int[8]: segment, first tile in the CTA's run, tiles (0: the
 // end), whole segment?, slot of its partial result, first CTA and number of the
 // segment's parts.
 
-// Floats of one partial result in the workspace: O [16][D], then m, mv, l [16] each.
+// Floats of one partial result in the workspace: O as its fragments (float4 [D / 8]
+// [lane]), then m, mv, l [16] each.
 __host__ __device__ constexpr int part_floats(int D) { return kRows * D + 3 * kRows; }
 
 // Consumer state of one warp: two rows of the tile per lane.
@@ -311,62 +327,75 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nseg = p.B * p.c.Hk * geo.RT;
   const Bars bar{smem_u32(smem + S::kBars)};
-  long long* scan = reinterpret_cast<long long*>(smem + S::kScan);
+  int* scan = reinterpret_cast<int*>(smem + S::kScan);  // see the words below
+  enum { kWSum = 0, kWMax = 8, kSeg = 16, kFirst, kLo, kHi, kCount, kJobs, kMerged, kJob0 = 24 };
 
-  if (tid == 0) {
-    for (int w = 0; w < kConsumers; ++w)
-      for (int s = 0; s < kSlots; ++s) {
-        mbar_init(bar.full(w, s), 1);
-        mbar_init(bar.empty(w, s), 1);
-      }
-    for (int s = 0; s < kPieceRing; ++s) {
-      mbar_init(bar.piece_full(s), 1);
-      mbar_init(bar.piece_empty(s), kConsumers);
-    }
-    mbar_init(bar.merge(), kConsumers);
+  if (tid < S::kNumBars) {
+    // one arrival each, but of piece_empty and done, where every consumer warp arrives
+    const bool all = tid >= 2 * kConsumers * kSlots + kPieceRing;
+    mbar_init(bar.base + 8 * tid, all ? kConsumers : 1);
     fence_barrier_init();
   }
+  if (tid >= kCount && tid <= kMerged) scan[tid] = 0;
 
-  // the line's length and the segment where this CTA's run begins
+  // the line's length, its longest segment, and where this CTA's run begins and ends
   const int each = (nseg + kThreads - 1) / kThreads;
   const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
-  long long mine = 0;
-  for (int s = seg_lo; s < seg_hi; ++s) mine += pages_of<kVec>(p, geo, s);
-  long long before = mine;
+  int mine = 0, longest = 0;
+  bool empty = false;
+  for (int s = seg_lo; s < seg_hi; ++s) {
+    const int n = pages_of<kVec>(p, geo, s);
+    mine += n;
+    longest = max(longest, n);
+    empty |= n == 0;
+  }
+  int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += x;
   }
-  if (lane == 31) scan[warp] = before;
-  __syncthreads();
-  long long total = 0;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    scan[kWSum + warp] = before;
+    scan[kWMax + warp] = longest;
+  }
+  const bool any_empty = __syncthreads_or(empty);
+  int total = 0;
 #pragma unroll
-  for (int w = 0; w <= kConsumers; ++w) {
-    const long long x = scan[w];
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int x = scan[kWSum + w];
     if (w < warp) before += x;
     total += x;
+    longest = max(longest, scan[kWMax + w]);
   }
   before -= mine;
-  const long long ctas = gridDim.x;
-  const long long run = max(static_cast<long long>(kMinRun), (total + ctas - 1) / ctas);
-  const long long run_lo = min(run * blockIdx.x, total), run_hi = min(run_lo + run, total);
-  if (run_lo < run_hi && before <= run_lo && run_lo < before + mine) {
-    int s = seg_lo;
-    for (;; ++s) {
-      const int n = pages_of<kVec>(p, geo, s);
-      if (run_lo < before + n) break;
-      before += n;
+  const int run = max(kMinRun, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const bool uncut = longest <= max(kUncut, run / 8);
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const long long x_wide = static_cast<long long>(run) * (blockIdx.x + side);
+    const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
+    if (x == total) {
+      if (tid == 0) scan[kLo + side] = total;
+    } else if (before <= x && x < before + mine) {
+      int s = seg_lo, at = before, n;
+      while (x >= at + (n = pages_of<kVec>(p, geo, s))) at += n, ++s;
+      const bool next = uncut && x != at;  // on to the segment's end
+      scan[kLo + side] = next ? at + n : x;
+      if (side == 0) {
+        scan[kSeg] = next ? s + 1 : s;
+        scan[kFirst] = next || uncut ? 0 : x - at;
+      }
     }
-    scan[12] = s;
-    scan[13] = run_lo - before;
   }
   __syncthreads();
+  const int run_lo = scan[kLo], run_hi = scan[kHi];
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
-    int seg = static_cast<int>(scan[12]), k = static_cast<int>(scan[13]);
-    const int tiles = static_cast<int>(run_hi - run_lo);
+    int seg = scan[kSeg], k = scan[kFirst];
+    const int tiles = run_hi - run_lo;
     bool ok = true;
     int pieces = 0;  // published so far
     int done = 0;
@@ -395,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       const int my_k = n_j - (c_j - lane);  // the tile's number in its segment
       const bool live = lane < avail;
       int page = -1, logical = 0, cut = 0;
-      float ks = 0.f, lvs = 0.f;
+      size_t ph = 0;
       if (live) {
         const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
         logical = my_k;
@@ -416,11 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
           record_failure(p.status, kStatusPage, kSiteCachePage);
           page = -1;
         } else {
-          const size_t ph = static_cast<size_t>(page) * p.c.Hk + hk;
-          ks = p.c.kscale[ph];
-          lvs = log2f(p.c.vscale[ph]);
+          ph = static_cast<size_t>(page) * p.c.Hk + hk;
         }
       }
+      const float ks = page >= 0 ? p.c.kscale[ph] : 0.f, vs = page >= 0 ? p.c.vscale[ph] : 1.f;
       // one tile for each consumer warp at a time, issued by as many lanes. A lane
       // waits only for slots that tiles of earlier groups leave, and for piece
       // entries of earlier groups, so the lanes never wait for one another.
@@ -429,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
         const int sg = __shfl_sync(0xffffffffu, my_seg, src), kk = __shfl_sync(0xffffffffu, my_k, src);
         const int nn = __shfl_sync(0xffffffffu, n_j, src), pg = __shfl_sync(0xffffffffu, page, src);
         const int lg = __shfl_sync(0xffffffffu, logical, src), ct = __shfl_sync(0xffffffffu, cut, src);
-        const float k_s = __shfl_sync(0xffffffffu, ks, src), v_s = __shfl_sync(0xffffffffu, lvs, src);
+        const unsigned long long off =
+            __shfl_sync(0xffffffffu, static_cast<unsigned long long>(ph) * S::kHalf, src);
         const int at = done + lane;  // number of the tile in the run
         const bool mine_too = lane < in_group;
         const bool starts = mine_too && (at == 0 || kk == 0);
@@ -439,35 +468,34 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
           if (n >= kPieceRing) ok = cache_wait(bar.piece_empty(e), (n / kPieceRing - 1) & 1, p.status);
           if (ok) {
             const int count = min(nn - kk, tiles - at);
-            const long long s0 = run_lo + at - kk;
-            const int cta0 = static_cast<int>(s0 / run);
+            const int s0 = run_lo + at - kk;  // where the segment begins on the line
+            const int cta0 = s0 / run;
             int* d = reinterpret_cast<int*>(smem + S::kPiece) + 8 * e;
             d[0] = sg, d[1] = at, d[2] = count, d[3] = kk == 0 && count == nn;
             d[4] = kk == 0 ? 1 : 0, d[5] = cta0;
-            d[6] = static_cast<int>((s0 + nn - 1) / run) - cta0 + 1;
+            d[6] = (s0 + nn - 1) / run - cta0 + 1;
             mbar_arrive(bar.piece_full(e));
           }
         }
         pieces += __popc(who);
+        const int w = at % kConsumers, q = 2 * (at / kConsumers);
+        const int slot_k = q % kSlots, slot_v = (q + 1) % kSlots;
+        const uint32_t dst = smem_u32(smem + S::kRing + w * kSlots * S::kHalf);
+        // K's copy is on its way before the scales are waited for: a barrier counts
+        // bytes that land before they are expected
         if (mine_too && ok) {
-          const int w = at % kConsumers, q = 2 * (at / kConsumers);
-          const int hk = (sg / geo.RT) % p.c.Hk;
-          const size_t off = (static_cast<size_t>(max(pg, 0)) * p.c.Hk + hk) * S::kHalf;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int seq = q + half, slot = seq % kSlots;
-            if (seq >= kSlots) ok = ok && cache_wait(bar.empty(w, slot), (seq / kSlots - 1) & 1, p.status);
-            if (!ok) break;
-            if (half == 0)
-              *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot) =
-                  make_int4(pg < 0 ? -1 : lg, ct, __float_as_int(k_s), __float_as_int(v_s));
-            if (pg >= 0) {
-              mbar_arrive_expect_tx(bar.full(w, slot), S::kHalf);
-              bulk_load(smem_u32(smem + S::kRing + (w * kSlots + slot) * S::kHalf),
-                        (half ? p.c.v8 : p.c.k8) + off, S::kHalf, bar.full(w, slot));
-            } else {
-              mbar_arrive(bar.full(w, slot));
-            }
+          if (q >= kSlots) ok = cache_wait(bar.empty(w, slot_k), (q / kSlots - 1) & 1, p.status);
+          if (ok && pg >= 0) bulk_load(dst + slot_k * S::kHalf, p.c.k8 + off, S::kHalf, bar.full(w, slot_k));
+        }
+        const float k_s = __shfl_sync(0xffffffffu, ks, src), v_s = __shfl_sync(0xffffffffu, vs, src);
+        if (mine_too && ok) {
+          *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot_k) =
+              make_int4(pg < 0 ? -1 : lg, ct, __float_as_int(k_s), __float_as_int(v_s));
+          mbar_arrive_expect_tx(bar.full(w, slot_k), pg >= 0 ? S::kHalf : 0);
+          if (q + 1 >= kSlots) ok = cache_wait(bar.empty(w, slot_v), ((q + 1) / kSlots - 1) & 1, p.status);
+          if (ok) {
+            mbar_arrive_expect_tx(bar.full(w, slot_v), pg >= 0 ? S::kHalf : 0);
+            if (pg >= 0) bulk_load(dst + slot_v * S::kHalf, p.c.v8 + off, S::kHalf, bar.full(w, slot_v));
           }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -504,20 +532,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t ring = smem_u32(smem + S::kRing) + warp * kSlots * S::kHalf;
+  const uint8_t* ring = smem + S::kRing + warp * kSlots * S::kHalf;
   float4* merge = reinterpret_cast<float4*>(smem + S::kMerge);
   float* stats = reinterpret_cast<float*>(smem + S::kStats);
-  uint32_t merge_phase = 0;
   bool ok = true;
-  // all consumer warps; false when a wait gave up
-  auto sync_warps = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar.merge());
-    ok = __all_sync(0xffffffffu, cache_wait(bar.merge(), merge_phase & 1, p.status));
-    ++merge_phase;
-    return ok;
-  };
-  int seq = 0;  // ring position of this warp
+  int seq = 0;      // ring position of this warp
+  int merges = 0;   // pieces so far whose states were merged in shared memory
 
   for (int piece = 0; ok; ++piece) {
     const int e = piece % kPieceRing;
@@ -593,27 +613,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sk), (seq / kSlots) & 1, p.status));
       if (!ok) break;
       const int4 meta = *(reinterpret_cast<const int4*>(smem + S::kMeta) + warp * kSlots + sk);
-      const float lvs = __int_as_float(meta.w);
+      const float lvs = __log2f(__int_as_float(meta.w));
       const int j0 = meta.x * kPage;
       float s[8][4];
 #pragma unroll
       for (int n = 0; n < 8; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-      const uint32_t kbase = ring + sk * S::kHalf + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
+      const uint8_t* kbase = ring + sk * S::kHalf + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
 #pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf)
+      for (int hf = 0; hf < D / 64; ++hf) {
+        uint4 w[8];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const uint4 w = lds128(kbase + 2 * n * D + 64 * hf);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint4*>(kbase + 2 * n * D + 64 * hf);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
             uint32_t b0, b1;
-            codes_to_f16(ww[u], b0, b1);
+            codes_to_f16(word(w[n], u), b0, b1);
             mma16816(s[n], qf[4 * hf + u], b0, b1);
           }
-        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.empty(warp, sk));
 
@@ -708,39 +729,30 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
 
       ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sv), ((seq + 1) / kSlots) & 1, p.status));
       if (!ok) break;
-      const uint32_t vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
-      if (!tail) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const uint4 w = lds128(vbase + 8 * n * kPage);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t b0, b1;
-            codes_to_f16(ww[u], b0, b1);
-            mma16816(st.acc[n], pf[u], b0, b1);
-          }
-        }
-      } else if (meta.x >= 0) {
-        // codes behind the sequence's end may be anything, NaN too: they become 0
-        const int n_ok = min(max(r.len - (j0 + 16 * c), 0), 16);
-        uint32_t keep[4];
+      const uint8_t* vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
+      // codes behind the sequence's end may be anything, NaN too: they become 0
+      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+      if (tail) {
+        const int n_ok = meta.x < 0 ? 0 : min(max(r.len - (j0 + 16 * c), 0), 16);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int nb = min(max(n_ok - 4 * u, 0), 4);
-          keep[u] = nb == 4 ? 0xffffffffu : (1u << (8 * nb)) - 1u;
+          keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
         }
+      }
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const uint4 w = lds128(vbase + 8 * n * kPage);
-          const uint32_t ww[4] = {w.x & keep[0], w.y & keep[1], w.z & keep[2], w.w & keep[3]};
+      for (int n0 = 0; n0 < D / 8; n0 += 8) {
+        uint4 w[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint4*>(vbase + 8 * (n0 + n) * kPage);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
             uint32_t b0, b1;
-            codes_to_f16(ww[u], b0, b1);
-            mma16816(st.acc[n], pf[u], b0, b1);
+            codes_to_f16(word(w[n], u) & keep[u], b0, b1);
+            mma16816(st.acc[n0 + n], pf[u], b0, b1);
           }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.empty(warp, sv));
@@ -753,141 +765,182 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 2);
     }
 
-    // ---- the warps' states become warp 0's: 4-6 into 0-2, 2-3 into 0-1, 1 into 0
-    auto put = [&](int buf) {
+    const int writers = min(count, kConsumers);  // warps that had tiles, from first % 7 on
+    const int mine = (warp - first % kConsumers + kConsumers) % kConsumers;
+    if (mine >= writers) {
+      merges += writers > 1;
+      continue;
+    }
+    if (writers > 1) {
+      // leave the state, once the pieces before have been added up
+      ok = __all_sync(0xffffffffu, count_wait(&scan[kMerged], merges, p.status));
+      ++merges;
+      if (!ok) break;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
-        merge[(buf * (D / 8) + n) * 32 + lane] =
+        merge[(warp * (D / 8) + n) * 32 + lane] =
             make_float4(st.acc[n][0], st.acc[n][1], st.acc[n][2], st.acc[n][3]);
       if (c == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float* x = stats + (buf * kRows + g + 8 * i) * 3;
-          x[0] = st.m[i], x[1] = st.mv[i], x[2] = st.l[i];
+          float* x = stats + 3 * kRows * warp + g + 8 * i;
+          x[0] = st.m[i], x[kRows] = st.mv[i], x[2 * kRows] = st.l[i];
         }
       }
-    };
-    auto take = [&](int buf) {
-      float fa[2], fb[2];
+      __threadfence_block();
+      __syncwarp();
+      int came = 0;
+      if (lane == 0) came = atomicAdd(&scan[kCount], 1);
+      if (__shfl_sync(0xffffffffu, came, 0) != writers - 1) continue;
+      __threadfence_block();
+      // the last warp adds the states up, in the order of their first tiles
+      float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
+      for (int k = 0; k < writers; ++k) {
+        const float* x = stats + 3 * kRows * ((first + k) % kConsumers) + g;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          m[i] = fmaxf(m[i], x[8 * i]);
+          mv[i] = fmaxf(mv[i], x[kRows + 8 * i]);
+        }
+      }
+      st.clear();
+      for (int k = 0; k < writers; ++k) {
+        const int w = (first + k) % kConsumers;
+        const float* x = stats + 3 * kRows * w + g;
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          st.l[i] += x[2 * kRows + 8 * i] * ex2_diff(x[8 * i], m[i]);
+          f[i] = ex2_diff(x[kRows + 8 * i], mv[i]);
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          const float4 v = merge[(w * (D / 8) + n) * 32 + lane];
+          st.acc[n][0] += v.x * f[0];
+          st.acc[n][1] += v.y * f[0];
+          st.acc[n][2] += v.z * f[1];
+          st.acc[n][3] += v.w * f[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) st.m[i] = m[i], st.mv[i] = mv[i];
+      __syncwarp();
+      if (lane == 0) {
+        scan[kCount] = 0;
+        __threadfence_block();
+        *reinterpret_cast<volatile int*>(&scan[kMerged]) = merges;
+      }
+    }
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float* x = stats + (buf * kRows + g + 8 * i) * 3;
-        const float m = fmaxf(st.m[i], x[0]), mv = fmaxf(st.mv[i], x[1]);
-        st.l[i] = st.l[i] * ex2_diff(st.m[i], m) + x[2] * ex2_diff(x[0], m);
-        fa[i] = ex2_diff(st.mv[i], mv);
-        fb[i] = ex2_diff(x[1], mv);
-        st.m[i] = m;
-        st.mv[i] = mv;
-      }
+        const int rr = rt * kRows + g + 8 * i;
+        if (rr >= rows) continue;
+        const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+        const float f = out_factor(st.m[i], st.mv[i], st.l[i]);
+        uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + 2 * c;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        const float4 x = merge[(buf * (D / 8) + n) * 32 + lane];
-        st.acc[n][0] = st.acc[n][0] * fa[0] + x.x * fb[0];
-        st.acc[n][1] = st.acc[n][1] * fa[0] + x.y * fb[0];
-        st.acc[n][2] = st.acc[n][2] * fa[1] + x.z * fb[1];
-        st.acc[n][3] = st.acc[n][3] * fa[1] + x.w * fb[1];
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<uint32_t*>(o + 8 * n) = pack_bf16x2(st.acc[n][2 * i] * f, st.acc[n][2 * i + 1] * f);
+        if (c == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(st.m[i], st.l[i]);
       }
+    } else {
+      float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float4*>(out + (n * 32 + lane) * 4) =
+            make_float4(st.acc[n][0], st.acc[n][1], st.acc[n][2], st.acc[n][3]);
+      if (c == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* x = out + kRows * D + g + 8 * i;
+          x[0] = st.m[i], x[kRows] = st.mv[i], x[2 * kRows] = st.l[i];
+        }
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0 && atomicAdd(&p.arrived[seg], 1) == parts - 1) {
+        p.arrived[seg] = 0;  // every part is there: ready for the next call
+        // joined at the end of the run, by all warps
+        int* job = scan + kJob0 + 4 * (slot_id == 0 ? 0 : 1);
+        job[0] = seg, job[1] = cta0, job[2] = parts;
+        atomicOr(&scan[kJobs], slot_id == 0 ? 1 : 2);
+      }
+    }
+  }
+
+  // segments of which this CTA's part came last: every part, in the order of the
+  // keys; a warp takes every seventh group of 8 columns, lanes as in a fragment
+  if (ok) {
+    __syncwarp();
+    __threadfence();
+    if (lane == 0) mbar_arrive(bar.done());
+    ok = __all_sync(0xffffffffu, cache_wait(bar.done(), 0, p.status));
+  }
+  for (int j = 0; ok && j < 2; ++j) {
+    if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
+    const int seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
+    const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const RowTile r = row_tile(p, geo.G, b, rt, false);
+    auto part_at = [&](int i) {
+      return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
     };
-    if (!sync_warps()) break;  // the last piece's states have been read
-    if (warp >= 4) put(warp - 4);
-    if (!sync_warps()) break;
-    if (warp + 4 < kConsumers) take(warp);
-    if (warp == 2 || warp == 3) put(warp);
-    if (!sync_warps()) break;
-    if (warp < 2) take(warp + 2);
-    if (warp == 1) put(1);
-    if (!sync_warps()) break;
-    if (warp == 0) {
-      take(1);
-      if (whole) {
+    float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float* x = part_at(i) + kRows * D + g;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rr = rt * kRows + g + 8 * i;
-          if (rr >= rows) continue;
-          const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
-          const float f = out_factor(st.m[i], st.mv[i], st.l[i]);
-          uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + 2 * c;
+      for (int k = 0; k < 2; ++k) {
+        m[k] = fmaxf(m[k], __ldcg(x + 8 * k));
+        mv[k] = fmaxf(mv[k], __ldcg(x + kRows + 8 * k));
+      }
+    }
+    constexpr int kMine = (D / 8 + kConsumers - 1) / kConsumers;
+    float sum[kMine][4];
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<uint32_t*>(o + 8 * n) = pack_bf16x2(st.acc[n][2 * i] * f, st.acc[n][2 * i + 1] * f);
-          if (c == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(st.m[i], st.l[i]);
-        }
-      } else {
-        float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D);
+    for (int n = 0; n < kMine; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < 4; ++k) sum[n][k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float* x = part_at(i);
+      float f[2];
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2*>(out + (g + 8 * i) * D + 8 * n + 2 * c) =
-                make_float2(st.acc[n][2 * i], st.acc[n][2 * i + 1]);
-          if (c == 0) {
-            float* x = out + kRows * D + g + 8 * i;
-            x[0] = st.m[i], x[kRows] = st.mv[i], x[2 * kRows] = st.l[i];
-          }
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) {
-          const int n = atomicAdd(&p.arrived[seg], 1);
-          if (n == parts - 1) p.arrived[seg] = 0;  // every part is there: ready for the next call
-          stats[0] = __int_as_float(n == parts - 1);
-          __threadfence();
+      for (int k = 0; k < 2; ++k) {
+        l[k] += __ldcg(x + kRows * D + 2 * kRows + g + 8 * k) * ex2_diff(__ldcg(x + kRows * D + g + 8 * k), m[k]);
+        f[k] = ex2_diff(__ldcg(x + kRows * D + kRows + g + 8 * k), mv[k]);
+      }
+#pragma unroll
+      for (int n = 0; n < kMine; ++n) {
+        const int col = warp + kConsumers * n;
+        if (col < D / 8) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(x + (col * 32 + lane) * 4));
+          sum[n][0] += v.x * f[0];
+          sum[n][1] += v.y * f[0];
+          sum[n][2] += v.z * f[1];
+          sum[n][3] += v.w * f[1];
         }
       }
     }
-    if (!whole) {
-      if (!sync_warps()) break;
-      const bool finish = __float_as_int(stats[0]) != 0;
-      if (finish) {
-        // every part, in the order of the keys: 16 threads a row, D / 16 columns each
-        __threadfence();
-        constexpr int kCols = D / 16;
-        const int col = (tid & 15) * kCols;
-        auto part_at = [&](int i) {
-          return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
-        };
-        for (int row = tid >> 4; row < kRows; row += 2 * kConsumers) {
-          float m = -INFINITY, mv = -INFINITY, l = 0.f;
-          for (int i = 0; i < parts; ++i) {
-            const float* x = part_at(i) + kRows * D + row;
-            m = fmaxf(m, __ldcg(x));
-            mv = fmaxf(mv, __ldcg(x + kRows));
-          }
-          float sum[kCols];
 #pragma unroll
-          for (int k = 0; k < kCols; ++k) sum[k] = 0.f;
-#pragma unroll 4
-          for (int i = 0; i < parts; ++i) {
-            const float* x = part_at(i);
-            l += __ldcg(x + kRows * D + 2 * kRows + row) * ex2_diff(__ldcg(x + kRows * D + row), m);
-            const float f = ex2_diff(__ldcg(x + kRows * D + kRows + row), mv);
+    for (int k = 0; k < 2; ++k) {
+      const int rr = rt * kRows + g + 8 * k;
+      if (rr >= geo.G * r.live) continue;
+      const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+      const float f = out_factor(m[k], mv[k], l[k]);
+      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + 2 * c;
 #pragma unroll
-            for (int k = 0; k < kCols; k += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(x + row * D + col + k));
-              sum[k] += v.x * f;
-              sum[k + 1] += v.y * f;
-              sum[k + 2] += v.z * f;
-              sum[k + 3] += v.w * f;
-            }
-          }
-          const int rr = rt * kRows + row;
-          if (rr < rows) {
-            const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
-            const float f = out_factor(m, mv, l);
-            uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + col;
-#pragma unroll
-            for (int k = 0; k < kCols; k += 2)
-              *reinterpret_cast<uint32_t*>(o + k) = pack_bf16x2(sum[k] * f, sum[k + 1] * f);
-            if ((tid & 15) == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(m, l);
-          }
-        }
+      for (int n = 0; n < kMine; ++n) {
+        const int col = warp + kConsumers * n;
+        if (col < D / 8)
+          *reinterpret_cast<uint32_t*>(o + 8 * col) = pack_bf16x2(sum[n][2 * k] * f, sum[n][2 * k + 1] * f);
       }
-      if (!sync_warps()) break;  // stats[0] has been read
+      if (warp == 0 && c == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(m[k], l[k]);
     }
   }
 
   // segments without a visible page: O = 0, LSE = -inf
-  for (int seg = blockIdx.x + gridDim.x * warp; ok && seg < nseg; seg += gridDim.x * kConsumers) {
+  for (int seg = blockIdx.x + gridDim.x * warp; ok && any_empty && seg < nseg; seg += gridDim.x * kConsumers) {
     if (pages_of<kVec>(p, geo, seg) != 0) continue;
     const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
     const RowTile r = row_tile(p, geo.G, b, rt, lane == 0);
@@ -942,6 +995,11 @@ Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
+
+bool cache_line_ok(int B, int H, int Hk, int N, int max_pages) {
+  const long long tiles = (static_cast<long long>(H / Hk) * N + kRows - 1) / kRows;
+  return static_cast<double>(B) * Hk * tiles * max_pages < 2147483648.0;
+}
 
 CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   const Geometry g = geometry(H, Hk, Hk, N, max_pages);
