@@ -3,9 +3,9 @@
 // reading the codes once bounds the call.
 //
 // Rows. The G = H / Hk query heads that share a cache head and the sequence's
-// query tokens form one list of rows, r = t * G + g, cut into tiles of 16 (the M
-// of a matrix instruction). A segment is one (sequence, cache head, row tile); its
-// work is the list of pages that some row of it sees.
+// query tokens form one list of rows, r = t * G + g, cut into tiles of 8, 16 or 32.
+// A segment is one (sequence, cache head, row tile); its work is the list of pages
+// that some row of it sees.
 //
 // Split. All pages of all segments form one line, cut into equal runs, one run
 // per CTA (one CTA per SM), whatever the lengths of the sequences. A run covers
@@ -23,20 +23,23 @@
 // on with the next piece; the last to arrive adds them up.
 //
 // Arithmetic. Codes become fp16 (exact) and enter m16n8k16 instructions with fp32
-// accumulators; tcgen05 would need 128 rows. The query row is scaled by a power of
-// two so that its largest element lies in [2^14, 2^15): fp16 then holds every bf16
-// element down to 2^-30 of the largest exactly. P is rounded to fp16 (2^-12
-// relative) after scaling by the page's V scale, relative to the row's largest such
-// product: a second running maximum, mv of log2(P * scale), beside m of the scores,
-// so that neither the weights of pages with small values (in l) nor the values of
-// pages with small weights are lost. m, mv, l and O are fp32.
+// accumulators; tcgen05 would need 128 rows. The products are taken transposed,
+// S^T = K Q^T and O^T = V^T P^T, so that keys and columns of V fill the 16 rows of
+// an instruction and the query rows its 8 columns: with 8 rows nothing is wasted,
+// and a code is converted once for all row groups of the tile. A query row is
+// scaled by a power of two so that its largest element lies in [2^14, 2^15): fp16
+// then holds every bf16 element down to 2^-30 of the largest exactly. P is rounded
+// to fp16 (2^-12 relative) after scaling by the page's V scale, relative to the
+// row's largest such product: a second running maximum, mv of log2(P * scale),
+// beside m of the scores, so that neither the weights of pages with small values
+// (in l) nor the values of pages with small weights are lost. m, mv, l and O are
+// fp32.
 //
-// Layout of a fragment. Lane = 4 g + c holds of a row tile the rows g and g + 8 and
-// of a page the keys 16 c .. 16 c + 15: the columns of the eight S instructions are
-// keys in the order that leaves each lane with 16 consecutive ones, so that its
-// 16-byte load of a V column is exactly the operand that meets its P. The summed
-// index d of S is permuted in the same way: a lane reads 16 consecutive codes of a
-// key, and the query is laid out to match.
+// Layout of a fragment. Lane = 4 g + c. The summed index of S^T is permuted so that
+// a lane reads 16 consecutive codes of a key (d = 64 half + 16 c ..), the query laid
+// out to match. The keys of an S^T instruction u are ordered so that after the 8x8
+// transposes that turn P into the second operand a lane holds the keys 16 c + 4 u ..
+// + 3, which are the codes of word u of its 16-byte load of a V column.
 #include <atomic>
 
 #include "cache.h"
@@ -48,7 +51,6 @@ namespace {
 
 constexpr int kConsumers = 7;  // with the producer 8 warps: two for each scheduler, 255 registers a thread
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kRows = 16;      // rows of a tile
 constexpr int kSlots = 3;      // ring slots of a consumer warp
 constexpr int kPieceRing = 16;  // piece descriptors in flight: more than twice what a group can start
 constexpr int kBatch = 4 * kConsumers;  // tiles looked up at a time, one per lane
@@ -60,7 +62,8 @@ constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 
 // ---------------------------------------------------------------- geometry
 struct Geometry {
-  int G, RT, classes, words;  // query heads per cache head, row tiles, mask classes, bit words
+  int G, rows, RT, classes, words;  // query heads per cache head, rows of a tile, row tiles, mask
+                                    // classes, words of page bits
 };
 
 // Row tile `rt` of sequence b: its query tokens [t_lo, t_hi] at positions t + shift,
@@ -68,7 +71,8 @@ struct Geometry {
 struct RowTile {
   int len, live, shift, t_lo, t_hi;
 };
-__device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, int G, int b, int rt, bool record) {
+__device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, const Geometry& geo, int b, int rt,
+                                            bool record) {
   RowTile r;
   r.live = p.q_lens ? min(max(p.q_lens[b], 0), p.N) : p.N;
   r.len = p.lens[b];
@@ -78,9 +82,9 @@ __device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, int G, int 
     r.len = min(max(r.len, 0), most);
   }
   r.shift = r.len - r.live;
-  const long long rows = static_cast<long long>(G) * r.live, r0 = static_cast<long long>(rt) * kRows;
+  const uint32_t G = geo.G, rows = G * r.live, r0 = static_cast<uint32_t>(rt) * geo.rows;
   r.t_lo = static_cast<int>(r0 / G);
-  r.t_hi = r0 < rows ? static_cast<int>(min(r0 + kRows - 1, rows - 1) / G) : r.t_lo - 1;
+  r.t_hi = r0 < rows ? static_cast<int>(min(r0 + geo.rows - 1, rows - 1) / G) : r.t_lo - 1;
   return r;
 }
 
@@ -98,7 +102,7 @@ __device__ __forceinline__ int pages_of(const CacheFwdParams& p, const Geometry&
     const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
     return p.prefix[at * (geo.words + 1) + geo.words];
   } else {
-    const RowTile r = row_tile(p, geo.G, b, rt, false);
+    const RowTile r = row_tile(p, geo, b, rt, false);
     if (r.t_hi < r.t_lo) return 0;
     const int lim = p.mask.causal ? min(r.len, r.shift + r.t_hi + 1) : r.len;
     return lim > 0 ? (lim + kPage - 1) / kPage : 0;
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(256) cache_classify(const CacheFwdParams p, co
   const int w = blockIdx.x, b = blockIdx.z;
   const int cls = blockIdx.y / geo.RT, rt = blockIdx.y % geo.RT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RowTile r = row_tile(p, geo.G, b, rt, w == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  const RowTile r = row_tile(p, geo, b, rt, w == 0 && blockIdx.y == 0 && threadIdx.x == 0);
   const int lo = r.shift + r.t_lo, hi = r.shift + r.t_hi;
   int m0 = cls, m1 = cls;  // mask heads of the class
   if (geo.classes != p.mask.Hm) {
@@ -259,12 +263,14 @@ __device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* 
 // 2^(a - b) where either may be -inf (then a is, or both are).
 __device__ __forceinline__ float ex2_diff(float a, float b) { return a == b ? 1.f : ex2(a - b); }
 
-template <int D>
+template <int D, int NT>
 struct Smem {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kFrags = D / 16 * NT;  // accumulator fragments (four floats a lane) of a warp
   static constexpr int kHalf = kPage * D;  // bytes of a page's K or V
   static constexpr int kRing = 0;          // [consumer][slot]
-  static constexpr int kMerge = kRing + kConsumers * kSlots * kHalf;  // float4 [consumer][D / 8][32]
-  static constexpr int kStats = kMerge + kConsumers * kRows * D * 4;  // float [consumer][3][16]: m, mv, l
+  static constexpr int kMerge = kRing + kConsumers * kSlots * kHalf;  // float4 [consumer][frag][32]
+  static constexpr int kStats = kMerge + kConsumers * kRows * D * 4;  // float [consumer][3][rows]: m, mv, l
   static constexpr int kMeta = kStats + kConsumers * kRows * 3 * 4;   // int4 [consumer][slot]
   static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8], see below
   static constexpr int kBars = kPiece + kPieceRing * 32;
@@ -272,8 +278,7 @@ struct Smem {
   static constexpr int kScan = kBars + kNumBars * 8;  // int [32], see the kernel
   static constexpr int kBytes = kScan + 32 * 4;
 };
-static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory per CTA");
-static_assert(Smem<128>::kScan % 8 == 0 && Smem<64>::kScan % 8 == 0, "alignment");
+static_assert(Smem<128, 2>::kBytes <= 227 * 1024 && Smem<64, 4>::kBytes <= 227 * 1024, "shared memory per CTA");
 
 struct Bars {
   uint32_t base;
@@ -288,24 +293,55 @@ struct Bars {
 // end), whole segment?, slot of its partial result, first CTA and number of the
 // segment's parts.
 
-// Floats of one partial result in the workspace: O as its fragments (float4 [D / 8]
-// [lane]), then m, mv, l [16] each.
-__host__ __device__ constexpr int part_floats(int D) { return kRows * D + 3 * kRows; }
+// Floats of one partial result in the workspace: O as its fragments (float4 [frag]
+// [lane]), then m, mv, l of the tile's rows.
+__host__ __device__ constexpr int part_floats(int D, int rows) { return rows * D + 3 * rows; }
 
-// Consumer state of one warp: two rows of the tile per lane.
-template <int D>
+// Transposes an 8 x 8 matrix of 16-bit elements held as a fragment (row g, columns
+// 2 c and 2 c + 1 in lane 4 g + c).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// State of one consumer warp. A lane's rows are 8 t + 2 c + e (m, mv and l are the
+// same in all lanes of a row, l once the piece has ended); acc[mt][t]: columns
+// 16 mt + g (and + 8) of rows 2 c, 2 c + 1.
+template <int D, int NT>
 struct State {
-  float acc[D / 8][4];
-  float m[2], mv[2], l[2];
+  float acc[D / 16][NT][4];
+  float m[NT][2], mv[NT][2], l[NT][2];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[i] = mv[i] = -INFINITY;
-      l[i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = mv[t][e] = -INFINITY;
+        l[t][e] = 0.f;
+      }
+  }
+  // Fragments to frags [frag][lane], m, mv, l of the rows to stats [3][8 NT].
+  __device__ __forceinline__ void put(float4* frags, float* stats, int lane) const {
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        frags[(n * NT + t) * 32 + lane] = make_float4(acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
+    if (lane < 4) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* x = stats + 8 * t + 2 * lane + e;
+          x[0] = m[t][e], x[8 * NT] = mv[t][e], x[16 * NT] = l[t][e];
+        }
     }
   }
 };
@@ -320,9 +356,33 @@ __device__ __forceinline__ float out_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
-template <int D, bool kVec>
+// LSE of the rows r0 and r0 + 1 of a lane.
+__device__ __forceinline__ void store_lse(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0,
+                                          int rows, bool mine, const float (&m)[2], const float (&l)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int tok = (r0 + e) / geo.G, h = hk * geo.G + r0 + e - tok * geo.G;
+    if (mine && r0 + e < rows)
+      p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(m[e], l[e]);
+  }
+}
+
+// Bits of the keys at[i], at[i + 2], .. at[i + 14] (i = odd) with s <= pos < e.
+__device__ __forceinline__ uint32_t hidden8(const int32_t* s, const int32_t* e, int pos, int odd) {
+  uint32_t hid = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int4 a = *reinterpret_cast<const int4*>(s + 4 * q), z = *reinterpret_cast<const int4*>(e + 4 * q);
+    const int a0 = odd ? a.y : a.x, z0 = odd ? z.y : z.x, a1 = odd ? a.w : a.z, z1 = odd ? z.w : z.z;
+    hid |= (static_cast<uint32_t>(a0 <= pos && pos < z0) | static_cast<uint32_t>(a1 <= pos && pos < z1) << 1) << (2 * q);
+  }
+  return hid;
+}
+
+template <int D, int NT, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdParams p, const Geometry geo) {
-  using S = Smem<D>;
+  using S = Smem<D, NT>;
+  constexpr int kRows = S::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nseg = p.B * p.c.Hk * geo.RT;
@@ -550,27 +610,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     if (count == 0) break;
 
     const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-    const RowTile r = row_tile(p, geo.G, b, rt, lane == 0 && warp == 0);
+    const RowTile r = row_tile(p, geo, b, rt, lane == 0 && warp == 0);
     const int rows = geo.G * r.live;
-    State<D> st;
+    State<D, NT> st;
     st.clear();
-    uint32_t qf[D / 16][4];
-    float crow[2];
-    int lim[2], pos[2];
-    size_t mrow[2] = {0, 0};
+    uint32_t qf[NT][D / 16][2];
+    float crow[NT][2];
+    int lim[NT][2], pos[NT][2];
+    size_t mrow[NT][2];
+    int all_lim = r.len;  // keys that every row of the tile sees as far as causality and length go
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = rt * kRows + g + 8 * i;
+    for (int t = 0; t < NT; ++t) {
+      // the query row that this lane brings in, 16 elements of each half: d = 64 half + 16 c ..
+      const int rr = rt * kRows + 8 * t + g;
       const bool live = rr < rows;
-      const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
-      pos[i] = r.shift + t;
-      lim[i] = live && p.mask.causal ? min(r.len, pos[i] + 1) : r.len;
-      if constexpr (kVec)
-        mrow[i] = (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) *
-                  static_cast<size_t>(p.max_pages * kPage);
-      // this lane's 16 elements of each half: d = 64 half + 16 c ..
+      const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
       uint4 x[D / 64][2];
-      const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + t * p.qs[2] + 16 * c;
+      const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
@@ -591,21 +647,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       const bool bad = top >= 0x7f80u;
       const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
       const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
-      crow[i] = p.scale_log2 * __int_as_float((127 - up) << 23);
+      const float back = p.scale_log2 * __int_as_float((127 - up) << 23);
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint4& v = x[hf][u >> 1];
           const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
-          qf[4 * hf + u][i] = pack_f16x2(__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f);
-          qf[4 * hf + u][2 + i] = pack_f16x2(__uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f);
+          qf[t][4 * hf + u][0] = pack_f16x2(__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f);
+          qf[t][4 * hf + u][1] = pack_f16x2(__uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f);
         }
-    }
-    // keys that every row of the tile sees as far as causality and length go
-    int all_lim = min(lim[0], lim[1]);
+      // the rows whose scores this lane holds
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) all_lim = min(all_lim, __shfl_xor_sync(0xffffffffu, all_lim, o));
+      for (int e = 0; e < 2; ++e) {
+        crow[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
+        const int r2 = rt * kRows + 8 * t + 2 * c + e;
+        const int tok2 = r2 / geo.G, h2 = hk * geo.G + r2 - tok2 * geo.G;
+        pos[t][e] = r.shift + tok2;
+        lim[t][e] = r2 < rows && p.mask.causal ? min(r.len, pos[t][e] + 1) : r.len;
+        all_lim = min(all_lim, lim[t][e]);
+        mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + min(h2, p.H - 1) / (p.H / p.mask.Hm)) *
+                                static_cast<size_t>(p.max_pages * kPage)
+                          : 0;
+      }
+    }
+    all_lim = __reduce_min_sync(0xffffffffu, all_lim);
 
     const int t0 = first + ((warp - first) % kConsumers + kConsumers) % kConsumers;
     for (int tile = t0; ok && tile < first + count; tile += kConsumers) {
@@ -615,116 +681,112 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       const int4 meta = *(reinterpret_cast<const int4*>(smem + S::kMeta) + warp * kSlots + sk);
       const float lvs = __log2f(__int_as_float(meta.w));
       const int j0 = meta.x * kPage;
-      float s[8][4];
+      // S^T: instruction u holds the keys kb + 4 u and kb + 4 u + 2 of this lane
+      const int kb = 16 * (g >> 1) + (g & 1);
+      float s[4][NT][4];
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-      const uint8_t* kbase = ring + sk * S::kHalf + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][t][i] = 0.f;
+      const uint8_t* kbase = ring + sk * S::kHalf + kb * D + 16 * c;
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf) {
-        uint4 w[8];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint4*>(kbase + 2 * n * D + 64 * hf);
+        uint4 w[4][2];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            uint32_t b0, b1;
-            codes_to_f16(word(w[n], u), b0, b1);
-            mma16816(s[n], qf[4 * hf + u], b0, b1);
+          for (int x = 0; x < 2; ++x)
+            w[u][x] = *reinterpret_cast<const uint4*>(kbase + (4 * u + 2 * x) * D + 64 * hf);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t a[4];
+            codes_to_f16(word(w[u][0], k), a[0], a[2]);
+            codes_to_f16(word(w[u][1], k), a[1], a[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(s[u][t], a, qf[t][4 * hf + k][0], qf[t][4 * hf + k][1]);
           }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.empty(warp, sk));
 
-      // scores in log2 units, masked
-      const float ck[2] = {crow[0] * __int_as_float(meta.z), crow[1] * __int_as_float(meta.z)};
-      float top[2] = {-INFINITY, -INFINITY};
-      uint32_t see[2] = {0xffffu, 0xffffu};  // bit 2 n + i: key j0 + 16 c + 2 n + i
+      // scores in log2 units, masked; s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e
+      const float kscale = __int_as_float(meta.z);
       const bool tail = meta.x < 0 || j0 + kPage > all_lim;
-      if (tail || meta.y) {
+      uint32_t pf[4][NT][2];
+      bool moved = false;
+      float av[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int n = meta.x < 0 ? 0 : min(max(lim[i] - (j0 + 16 * c), 0), 16);
-          see[i] = (1u << n) - 1u;
-        }
-        if constexpr (kVec) {
-          if (meta.y) {
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const size_t at = mrow[i] + j0 + 16 * c;
-              uint32_t hid = 0;
-#pragma unroll
-              for (int q4 = 0; q4 < 4; ++q4) {
-                if (p.mask.lts) {
-                  const int4 a = *reinterpret_cast<const int4*>(p.mask.lts + at + 4 * q4);
-                  const int4 z = *reinterpret_cast<const int4*>(p.mask.lte + at + 4 * q4);
-                  hid |= (static_cast<uint32_t>(a.x <= pos[i] && pos[i] < z.x) |
-                          static_cast<uint32_t>(a.y <= pos[i] && pos[i] < z.y) << 1 |
-                          static_cast<uint32_t>(a.z <= pos[i] && pos[i] < z.z) << 2 |
-                          static_cast<uint32_t>(a.w <= pos[i] && pos[i] < z.w) << 3) << (4 * q4);
-                }
-                if (p.mask.uts) {
-                  const int4 a = *reinterpret_cast<const int4*>(p.mask.uts + at + 4 * q4);
-                  const int4 z = *reinterpret_cast<const int4*>(p.mask.ute + at + 4 * q4);
-                  hid |= (static_cast<uint32_t>(a.x <= pos[i] && pos[i] < z.x) |
-                          static_cast<uint32_t>(a.y <= pos[i] && pos[i] < z.y) << 1 |
-                          static_cast<uint32_t>(a.z <= pos[i] && pos[i] < z.z) << 2 |
-                          static_cast<uint32_t>(a.w <= pos[i] && pos[i] < z.w) << 3) << (4 * q4);
-                }
+        for (int e = 0; e < 2; ++e) {
+          const float ck = crow[t][e] * kscale;
+          float top = -INFINITY;
+          if (tail || meta.y) {
+            // bit 2 u + x: key kb + 4 u + 2 x is visible
+            const int n = meta.x < 0 ? 0 : min(max(lim[t][e] - (j0 + kb), 0), 16);
+            uint32_t see = (1u << ((n + 1) >> 1)) - 1u;
+            if constexpr (kVec) {
+              if (meta.y && meta.x >= 0) {
+                const size_t at = mrow[t][e] + j0 + (kb & ~1);
+                if (p.mask.lts) see &= ~hidden8(p.mask.lts + at, p.mask.lte + at, pos[t][e], g & 1);
+                if (p.mask.uts) see &= ~hidden8(p.mask.uts + at, p.mask.ute + at, pos[t][e], g & 1);
               }
-              see[i] &= ~hid;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float& v = s[u][t][2 * x + e];
+                v = (see >> (2 * u + x)) & 1u ? v * ck : -INFINITY;
+                top = fmaxf(top, v);
+              }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              s[u][t][e] *= ck;
+              s[u][t][2 + e] *= ck;
+              top = fmax3(top, s[u][t][e], s[u][t][2 + e]);
             }
           }
-        }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float m_new = fmaxf(st.m[t][e], top), mv_new = fmaxf(st.mv[t][e], top + lvs);
+          const float al = ex2_diff(st.m[t][e], m_new);
+          av[t][e] = ex2_diff(st.mv[t][e], mv_new);
+          moved |= av[t][e] != 1.f;
+          st.m[t][e] = m_new;
+          st.mv[t][e] = mv_new;
+          const float mu = m_new == -INFINITY ? 0.f : m_new, mvu = mv_new == -INFINITY ? 0.f : mv_new;
+          const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
+          float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = s[n][i] * ck[i >> 1];
-            s[n][i] = (see[i >> 1] >> (2 * n + (i & 1))) & 1u ? x : -INFINITY;
+          for (int u = 0; u < 4; ++u) {
+            const float p0 = ex2(s[u][t][e] - mu), p1 = ex2(s[u][t][2 + e] - mu);
+            sum0 += p0;
+            sum1 += p1;
+            s[u][t][e] = p0 * f;
+            s[u][t][2 + e] = p1 * f;
           }
-      } else {
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][i] *= ck[i >> 1];
-      }
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) top[i] = fmax3(top[i], s[n][2 * i], s[n][2 * i + 1]);
-      uint32_t pf[4][4];
-      bool moved = false;
-      float av[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-        const float m_new = fmaxf(st.m[i], top[i]), mv_new = fmaxf(st.mv[i], top[i] + lvs);
-        const float al = ex2_diff(st.m[i], m_new);
-        av[i] = ex2_diff(st.mv[i], mv_new);
-        moved |= av[i] != 1.f;
-        st.m[i] = m_new;
-        st.mv[i] = mv_new;
-        const float mu = m_new == -INFINITY ? 0.f : m_new, mvu = mv_new == -INFINITY ? 0.f : mv_new;
-        const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
-        float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const float p0 = ex2(s[n][2 * i] - mu), p1 = ex2(s[n][2 * i + 1] - mu);
-          sum0 += p0;
-          sum1 += p1;
-          pf[n >> 1][2 * (n & 1) + i] = pack_f16x2(p0 * f, p1 * f);
+          st.l[t][e] = st.l[t][e] * al + (sum0 + sum1);
         }
-        st.l[i] = st.l[i] * al + (sum0 + sum1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          pf[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
+          pf[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
+        }
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+        for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st.acc[n][i] *= av[i >> 1];
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.acc[n][t][i] *= av[t][i & 1];
       }
 
       ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sv), ((seq + 1) / kSlots) & 1, p.status));
@@ -741,17 +803,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
         }
       }
 #pragma unroll
-      for (int n0 = 0; n0 < D / 8; n0 += 8) {
-        uint4 w[8];
+      for (int n0 = 0; n0 < D / 16; n0 += 4) {
+        uint4 w[4][2];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint4*>(vbase + 8 * (n0 + n) * kPage);
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            w[n][x] = *reinterpret_cast<const uint4*>(vbase + (16 * (n0 + n) + 8 * x) * kPage);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            uint32_t b0, b1;
-            codes_to_f16(word(w[n], u) & keep[u], b0, b1);
-            mma16816(st.acc[n0 + n], pf[u], b0, b1);
+          for (int n = 0; n < 4; ++n) {
+            uint32_t a[4];
+            codes_to_f16(word(w[n][0], u) & keep[u], a[0], a[2]);
+            codes_to_f16(word(w[n][1], u) & keep[u], a[1], a[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(st.acc[n0 + n][t], a, pf[u][t][0], pf[u][t][1]);
           }
       }
       __syncwarp();
@@ -760,10 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     }
     if (!ok) break;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 1);
-      st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 2);
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) st.l[t][e] += __shfl_xor_sync(0xffffffffu, st.l[t][e], o);
 
     const int writers = min(count, kConsumers);  // warps that had tiles, from first % 7 on
     const int mine = (warp - first % kConsumers + kConsumers) % kConsumers;
@@ -776,17 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       ok = __all_sync(0xffffffffu, count_wait(&scan[kMerged], merges, p.status));
       ++merges;
       if (!ok) break;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-        merge[(warp * (D / 8) + n) * 32 + lane] =
-            make_float4(st.acc[n][0], st.acc[n][1], st.acc[n][2], st.acc[n][3]);
-      if (c == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float* x = stats + 3 * kRows * warp + g + 8 * i;
-          x[0] = st.m[i], x[kRows] = st.mv[i], x[2 * kRows] = st.l[i];
-        }
-      }
+      st.put(merge + warp * S::kFrags * 32, stats + 3 * kRows * warp, lane);
       __threadfence_block();
       __syncwarp();
       int came = 0;
@@ -794,36 +852,39 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       if (__shfl_sync(0xffffffffu, came, 0) != writers - 1) continue;
       __threadfence_block();
       // the last warp adds the states up, in the order of their first tiles
-      float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
-      for (int k = 0; k < writers; ++k) {
-        const float* x = stats + 3 * kRows * ((first + k) % kConsumers) + g;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          m[i] = fmaxf(m[i], x[8 * i]);
-          mv[i] = fmaxf(mv[i], x[kRows + 8 * i]);
-        }
-      }
       st.clear();
       for (int k = 0; k < writers; ++k) {
-        const int w = (first + k) % kConsumers;
-        const float* x = stats + 3 * kRows * w + g;
-        float f[2];
+        const float* x = stats + 3 * kRows * ((first + k) % kConsumers) + 2 * c;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          st.l[i] += x[2 * kRows + 8 * i] * ex2_diff(x[8 * i], m[i]);
-          f[i] = ex2_diff(x[kRows + 8 * i], mv[i]);
-        }
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const float4 v = merge[(w * (D / 8) + n) * 32 + lane];
-          st.acc[n][0] += v.x * f[0];
-          st.acc[n][1] += v.y * f[0];
-          st.acc[n][2] += v.z * f[1];
-          st.acc[n][3] += v.w * f[1];
-        }
+          for (int e = 0; e < 2; ++e) {
+            st.m[t][e] = fmaxf(st.m[t][e], x[8 * t + e]);
+            st.mv[t][e] = fmaxf(st.mv[t][e], x[kRows + 8 * t + e]);
+          }
       }
+      for (int k = 0; k < writers; ++k) {
+        const int w = (first + k) % kConsumers;
+        const float* x = stats + 3 * kRows * w + 2 * c;
+        float f[NT][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) st.m[i] = m[i], st.mv[i] = mv[i];
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            st.l[t][e] += x[2 * kRows + 8 * t + e] * ex2_diff(x[8 * t + e], st.m[t][e]);
+            f[t][e] = ex2_diff(x[kRows + 8 * t + e], st.mv[t][e]);
+          }
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float4 v = merge[(w * S::kFrags + n * NT + t) * 32 + lane];
+            st.acc[n][t][0] += v.x * f[t][0];
+            st.acc[n][t][1] += v.y * f[t][1];
+            st.acc[n][t][2] += v.z * f[t][0];
+            st.acc[n][t][3] += v.w * f[t][1];
+          }
+      }
       __syncwarp();
       if (lane == 0) {
         scan[kCount] = 0;
@@ -833,30 +894,24 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     }
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = rt * kRows + g + 8 * i;
-        if (rr >= rows) continue;
-        const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
-        const float f = out_factor(st.m[i], st.mv[i], st.l[i]);
-        uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + 2 * c;
+      for (int t = 0; t < NT; ++t) {
+        const float f0 = out_factor(st.m[t][0], st.mv[t][0], st.l[t][0]);
+        const float f1 = out_factor(st.m[t][1], st.mv[t][1], st.l[t][1]);
+        const int rr = rt * kRows + 8 * t + g;  // the row this lane holds after the transposes
+        const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+        uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<uint32_t*>(o + 8 * n) = pack_bf16x2(st.acc[n][2 * i] * f, st.acc[n][2 * i + 1] * f);
-        if (c == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(st.m[i], st.l[i]);
+        for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t v = transpose8x8(pack_bf16x2(st.acc[n][t][2 * x] * f0, st.acc[n][t][2 * x + 1] * f1));
+            if (rr < rows) *reinterpret_cast<uint32_t*>(o + 16 * n + 8 * x) = v;
+          }
+        store_lse(p, geo, b, hk, rt * kRows + 8 * t + 2 * c, rows, g == 0, st.m[t], st.l[t]);
       }
     } else {
-      float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D);
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<float4*>(out + (n * 32 + lane) * 4) =
-            make_float4(st.acc[n][0], st.acc[n][1], st.acc[n][2], st.acc[n][3]);
-      if (c == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float* x = out + kRows * D + g + 8 * i;
-          x[0] = st.m[i], x[kRows] = st.mv[i], x[2 * kRows] = st.l[i];
-        }
-      }
+      float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D, kRows);
+      st.put(reinterpret_cast<float4*>(out), out + kRows * D, lane);
       __threadfence();
       __syncwarp();
       if (lane == 0 && atomicAdd(&p.arrived[seg], 1) == parts - 1) {
@@ -870,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   }
 
   // segments of which this CTA's part came last: every part, in the order of the
-  // keys; a warp takes every seventh group of 8 columns, lanes as in a fragment
+  // keys; a warp takes every seventh fragment
   if (ok) {
     __syncwarp();
     __threadfence();
@@ -881,61 +936,50 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
     const int seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
     const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-    const RowTile r = row_tile(p, geo.G, b, rt, false);
+    const RowTile r = row_tile(p, geo, b, rt, false);
+    const int rows = geo.G * r.live;
     auto part_at = [&](int i) {
-      return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
+      return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D, kRows);
     };
-    float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int fr = warp; fr < S::kFrags; fr += kConsumers) {
+      const int n = fr / NT, t = fr % NT;
+      float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float* x = part_at(i) + kRows * D + g;
+      for (int i = 0; i < parts; ++i) {
+        const float* x = part_at(i) + kRows * D + 8 * t + 2 * c;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        m[k] = fmaxf(m[k], __ldcg(x + 8 * k));
-        mv[k] = fmaxf(mv[k], __ldcg(x + kRows + 8 * k));
-      }
-    }
-    constexpr int kMine = (D / 8 + kConsumers - 1) / kConsumers;
-    float sum[kMine][4];
-#pragma unroll
-    for (int n = 0; n < kMine; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum[n][k] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float* x = part_at(i);
-      float f[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        l[k] += __ldcg(x + kRows * D + 2 * kRows + g + 8 * k) * ex2_diff(__ldcg(x + kRows * D + g + 8 * k), m[k]);
-        f[k] = ex2_diff(__ldcg(x + kRows * D + kRows + g + 8 * k), mv[k]);
-      }
-#pragma unroll
-      for (int n = 0; n < kMine; ++n) {
-        const int col = warp + kConsumers * n;
-        if (col < D / 8) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(x + (col * 32 + lane) * 4));
-          sum[n][0] += v.x * f[0];
-          sum[n][1] += v.y * f[0];
-          sum[n][2] += v.z * f[1];
-          sum[n][3] += v.w * f[1];
+        for (int e = 0; e < 2; ++e) {
+          m[e] = fmaxf(m[e], __ldcg(x + e));
+          mv[e] = fmaxf(mv[e], __ldcg(x + kRows + e));
         }
       }
-    }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        const float* x = part_at(i);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(x) + fr * 32 + lane);
+        x += kRows * D + 8 * t + 2 * c;
+        float f[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int rr = rt * kRows + g + 8 * k;
-      if (rr >= geo.G * r.live) continue;
-      const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
-      const float f = out_factor(m[k], mv[k], l[k]);
-      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2] + 2 * c;
-#pragma unroll
-      for (int n = 0; n < kMine; ++n) {
-        const int col = warp + kConsumers * n;
-        if (col < D / 8)
-          *reinterpret_cast<uint32_t*>(o + 8 * col) = pack_bf16x2(sum[n][2 * k] * f, sum[n][2 * k + 1] * f);
+        for (int e = 0; e < 2; ++e) {
+          l[e] += __ldcg(x + 2 * kRows + e) * ex2_diff(__ldcg(x + e), m[e]);
+          f[e] = ex2_diff(__ldcg(x + kRows + e), mv[e]);
+        }
+        sum[0] += v.x * f[0];
+        sum[1] += v.y * f[1];
+        sum[2] += v.z * f[0];
+        sum[3] += v.w * f[1];
       }
-      if (warp == 0 && c == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = out_lse(m[k], l[k]);
+      const float f0 = out_factor(m[0], mv[0], l[0]), f1 = out_factor(m[1], mv[1], l[1]);
+      const int rr = rt * kRows + 8 * t + g;
+      const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 16 * n + 2 * c;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t v = transpose8x8(pack_bf16x2(sum[2 * x] * f0, sum[2 * x + 1] * f1));
+        if (rr < rows) *reinterpret_cast<uint32_t*>(o + 8 * x) = v;
+      }
+      if (n == 0) store_lse(p, geo, b, hk, rt * kRows + 8 * t + 2 * c, rows, g == 0, m, l);
     }
   }
 
@@ -943,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   for (int seg = blockIdx.x + gridDim.x * warp; ok && any_empty && seg < nseg; seg += gridDim.x * kConsumers) {
     if (pages_of<kVec>(p, geo, seg) != 0) continue;
     const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-    const RowTile r = row_tile(p, geo.G, b, rt, lane == 0);
+    const RowTile r = row_tile(p, geo, b, rt, lane == 0);
     const int row_hi = min(geo.G * r.live, (rt + 1) * kRows);
     for (int rr = rt * kRows; rr < row_hi; ++rr) {
       const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
@@ -955,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
 }
 
 // Lets the kernel have its shared memory, once for each device.
-template <int D, bool kVec>
+template <int D, int NT, bool kVec>
 cudaError_t allow_smem() {
   static std::atomic<uint64_t> done[4];  // devices 0 .. 255
   int dev = 0;
@@ -963,30 +1007,42 @@ cudaError_t allow_smem() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev > 255) return cudaErrorInvalidDevice;
   if (done[dev >> 6].load(std::memory_order_relaxed) >> (dev & 63) & 1) return cudaSuccess;
-  e = cudaFuncSetAttribute(cache_fwd_kernel<D, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Smem<D>::kBytes);
+  e = cudaFuncSetAttribute(cache_fwd_kernel<D, NT, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<D, NT>::kBytes);
   if (e == cudaSuccess) done[dev >> 6].fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
   return e;
 }
 
-template <int D, bool kVec>
+template <int D, int NT, bool kVec>
 cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
   if (kVec) {
     const dim3 grid(static_cast<unsigned>(geo.words), static_cast<unsigned>(geo.classes * geo.RT),
                     static_cast<unsigned>(p.B));
     cache_classify<<<grid, 256, 0, s>>>(p, geo);
   }
-  const cudaError_t e = allow_smem<D, kVec>();
+  const cudaError_t e = allow_smem<D, NT, kVec>();
   if (e != cudaSuccess) return e;
   const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
-  cache_fwd_kernel<D, kVec><<<grid, kThreads, Smem<D>::kBytes, s>>>(p, geo);
+  cache_fwd_kernel<D, NT, kVec><<<grid, kThreads, Smem<D, NT>::kBytes, s>>>(p, geo);
   return cudaGetLastError();
 }
 
-Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
+template <int D, int NT>
+cudaError_t launch_nt(const CacheFwdParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  return p.mask.lts != nullptr || p.mask.uts != nullptr ? launch_t<D, NT, true>(p, geo, num_sms, s)
+                                                        : launch_t<D, NT, false>(p, geo, num_sms, s);
+}
+
+// Rows of a tile: as few as hold all rows, so that no columns of an instruction are
+// empty, up to what the accumulators leave registers for.
+int rows_of_tile(int rows, int d) { return rows <= 8 ? 8 : rows <= 16 || d == 128 ? 16 : 32; }
+
+Geometry geometry(int H, int Hk, int Hm, int N, int d, int max_pages) {
   Geometry g;
   g.G = H / Hk;
-  g.RT = static_cast<int>((static_cast<long long>(g.G) * N + kRows - 1) / kRows);
+  const int rows = g.G * N;  // below 2^31: B * H * N is
+  g.rows = rows_of_tile(rows, d);
+  g.RT = (rows - 1) / g.rows + 1;
   g.classes = Hk % Hm == 0 ? Hm : Hk;
   g.words = (max_pages + 31) / 32;
   return g;
@@ -997,12 +1053,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 bool cache_line_ok(int B, int H, int Hk, int N, int max_pages) {
-  const long long tiles = (static_cast<long long>(H / Hk) * N + kRows - 1) / kRows;
+  const long long tiles = (static_cast<long long>(H / Hk) * N + 7) / 8;
   return static_cast<double>(B) * Hk * tiles * max_pages < 2147483648.0;
 }
 
 CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
-  const Geometry g = geometry(H, Hk, Hk, N, max_pages);
+  const Geometry g = geometry(H, Hk, Hk, N, d, max_pages);
   const size_t tiles = static_cast<size_t>(B) * Hk * g.RT;
   CacheWs w;
   size_t off = 256;  // the status word
@@ -1011,7 +1067,7 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   w.class_done = off;
   off = up256(off + tiles * 4);
   w.partial = off;
-  off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 * part_floats(d) * 4);
+  off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 * part_floats(d, g.rows) * 4);
   w.vis = off;
   off = up256(off + tiles * g.words * 4);
   w.part = off;
@@ -1023,11 +1079,12 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
 }
 
 cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s) {
-  const Geometry geo = geometry(p.H, p.c.Hk, p.mask.Hm, p.N, p.max_pages);
-  const bool vec = p.mask.lts != nullptr || p.mask.uts != nullptr;
+  const Geometry geo = geometry(p.H, p.c.Hk, p.mask.Hm, p.N, d, p.max_pages);
   if (d == 64)
-    return vec ? launch_t<64, true>(p, geo, num_sms, s) : launch_t<64, false>(p, geo, num_sms, s);
-  return vec ? launch_t<128, true>(p, geo, num_sms, s) : launch_t<128, false>(p, geo, num_sms, s);
+    return geo.rows == 8    ? launch_nt<64, 1>(p, geo, num_sms, s)
+           : geo.rows == 16 ? launch_nt<64, 2>(p, geo, num_sms, s)
+                            : launch_nt<64, 4>(p, geo, num_sms, s);
+  return geo.rows == 8 ? launch_nt<128, 1>(p, geo, num_sms, s) : launch_nt<128, 2>(p, geo, num_sms, s);
 }
 
 }  // namespace fm
