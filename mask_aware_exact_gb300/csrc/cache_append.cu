@@ -60,12 +60,13 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
 }
 
+// A thread holds one 16-byte chunk (8 columns) of kEach consecutive slots of the
+// page, for K and for V, so that the codes of a V column leave it as one word.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  constexpr int kRowChunks = D / 8;                                   // 16-byte chunks of a row
-  constexpr int kRowsPerPass = kAppendThreads / kRowChunks;           // 16 or 32
-  constexpr int kPasses = kPage / kRowsPerPass;                       // 4 or 2
-  constexpr int kVRow = kPage + 4;                                    // bytes; word stride 17: no bank conflicts
+  constexpr int kRowChunks = D / 8;                             // 16-byte chunks of a row
+  constexpr int kEach = kPage * kRowChunks / kAppendThreads;    // 4 or 2
+  constexpr int kVRow = kPage + 4;  // bytes of a column in shared memory: a word stride of 17
   __shared__ uint32_t kmax[kPage], vmax[kPage];
   __shared__ int exps[2];
   __shared__ __align__(16) uint8_t vt[D * kVRow];
@@ -79,25 +80,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     return;
   }
   const int page_i = start / kPage + static_cast<int>(blockIdx.z);
-  const int first = page_i * kPage;              // position of slot 0
-  const int lo = max(start - first, 0);          // first new slot
+  const int first = page_i * kPage;                // position of slot 0
+  const int lo = max(start - first, 0);            // first new slot
   const int hi = min(start + cnt - first, kPage);  // behind the last new slot
   if (lo >= hi) return;
-  const int tok0 = first + lo - start;           // new token of slot lo
 
-  // the new rows: slot lo + r holds token tok0 + r
-  uint4 kr[kPasses], vr[kPasses];
-  const int c = tid % kRowChunks, r0 = tid / kRowChunks;
-  const int rows = hi - lo;
-  const uint16_t* ksrc = p.k + b * p.ks[0] + h * p.ks[1] + static_cast<int64_t>(tok0) * p.ks[2] + 8 * c;
-  const uint16_t* vsrc = p.v + b * p.vs[0] + h * p.vs[1] + static_cast<int64_t>(tok0) * p.vs[2] + 8 * c;
+  // the new rows: slot s holds token first + s - start
+  uint4 kr[kEach], vr[kEach];
+  const int c = tid % kRowChunks, s0 = tid / kRowChunks * kEach;
+  const uint16_t* ksrc = p.k + b * p.ks[0] + h * p.ks[1] + 8 * c;
+  const uint16_t* vsrc = p.v + b * p.vs[0] + h * p.vs[1] + 8 * c;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = r0 + i * kRowsPerPass;
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t tok = first + s0 + i - start;
     kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) {
-      kr[i] = *reinterpret_cast<const uint4*>(ksrc + r * p.ks[2]);
-      vr[i] = *reinterpret_cast<const uint4*>(vsrc + r * p.vs[2]);
+    if (s0 + i >= lo && s0 + i < hi) {
+      kr[i] = __ldcs(reinterpret_cast<const uint4*>(ksrc + tok * p.ks[2]));
+      vr[i] = __ldcs(reinterpret_cast<const uint4*>(vsrc + tok * p.vs[2]));
     }
   }
   const int page = p.table[static_cast<size_t>(b) * p.max_pages + page_i];
@@ -115,16 +114,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 
   // largest magnitude of every new token
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    uint32_t a = absbits8(kr[i]), e = absbits8(vr[i]);
+  for (int i = 0; i < kEach; ++i) {
+    uint32_t a = absbits8(kr[i]) << 16 | absbits8(vr[i]);
 #pragma unroll
-    for (int o = kRowChunks / 2; o > 0; o >>= 1) {
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-    }
+    for (int o = kRowChunks / 2; o > 0; o >>= 1) a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, o));
     if (c == 0) {
-      kmax[r0 + i * kRowsPerPass] = a;
-      vmax[r0 + i * kRowsPerPass] = e;
+      kmax[s0 + i] = a >> 16;
+      vmax[s0 + i] = a & 0xffffu;
     }
   }
   __syncthreads();
@@ -156,26 +152,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     p.c.vscale[ph] = vs;
   }
 
-  // K: rows of codes; V: bytes of the transposed tile, slot-major in a column
+  // K: rows of codes, zeros behind the last token of a page begun here; V: the
+  // codes of each column into shared memory
+  uint2 vc[kEach];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = r0 + i * kRowsPerPass;
-    const int slot = lo + r;
-    if (r < rows) {
-      const bool bad = kmax[r] >= 0x7f80u || vmax[r] >= 0x7f80u;
-      const uint2 kc = bad ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : codes8(kr[i], kinv);
-      *reinterpret_cast<uint2*>(kp + slot * D + 8 * c) = kc;
-      const uint2 vc = bad ? make_uint2(0u, 0u) : codes8(vr[i], vinv);
+  for (int i = 0; i < kEach; ++i) {
+    const int slot = s0 + i;
+    const bool bad = kmax[slot] >= 0x7f80u || vmax[slot] >= 0x7f80u;
+    vc[i] = bad ? make_uint2(0u, 0u) : codes8(vr[i], vinv);
+    if ((slot >= lo && slot < hi) || !begun)
+      *reinterpret_cast<uint2*>(kp + slot * D + 8 * c) =
+          bad ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : codes8(kr[i], kinv);
+  }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        vt[(8 * c + j) * kVRow + slot] = static_cast<uint8_t>(vc.x >> (8 * j));
-        vt[(8 * c + 4 + j) * kVRow + slot] = static_cast<uint8_t>(vc.y >> (8 * j));
-      }
-    } else if (!begun) {
-      *reinterpret_cast<uint2*>(kp + slot * D + 8 * c) = make_uint2(0u, 0u);
+  for (int j = 0; j < 8; ++j) {
+    // byte j of each slot's codes, slots in order
+    uint32_t w = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) vt[(8 * c + j) * kVRow + slot] = 0;
-    }
+    for (int i = 0; i < kEach; ++i) w |= ((j < 4 ? vc[i].x : vc[i].y) >> (8 * (j & 3)) & 0xffu) << (8 * i);
+    if constexpr (kEach == 4)
+      *reinterpret_cast<uint32_t*>(vt + (8 * c + j) * kVRow + s0) = w;
+    else
+      *reinterpret_cast<uint16_t*>(vt + (8 * c + j) * kVRow + s0) = static_cast<uint16_t>(w);
   }
   // older codes of a page whose scale has grown
   if (begun && ks > kold) {
@@ -191,6 +189,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       reinterpret_cast<uint4*>(vp)[i] = make_uint4(src[0], src[1], src[2], src[3]);
     }
   } else {
+    const int rows = hi - lo;
     for (int i = tid; i < D * rows; i += kAppendThreads) {
       const int col = i / rows, slot = lo + i - col * rows;
       vp[col * kPage + slot] = vt[col * kVRow + slot];

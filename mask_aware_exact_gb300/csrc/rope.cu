@@ -11,10 +11,13 @@
 //
 // HBM-bound: every element is read and written once. A thread owns kVec pairs
 // of one token and walks over heads of Q and K with the same sine and cosine,
-// so their cost (about 25 instructions a pair) is spread over the heads and
-// hides behind the loads. It handles kUnroll heads at a time, all loads before
-// the first store, which keeps 2 * kUnroll 16-byte loads in flight per thread
-// and makes the call correct in place.
+// so their cost (about 50 instructions a pair) is spread over the heads. Its
+// 16-byte pieces of the next kStages heads are always on their way into its own
+// slots of shared memory (asynchronous copies, no registers held, no thread waits
+// for another). A head's pieces are read before they are written and no other
+// thread touches them, so the call is correct in place.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,7 +28,8 @@ namespace fm {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kBlocksPerSm = 16;
+constexpr int kStages = 4;  // heads in flight per thread
 
 // f / (2 pi) modulo one turn as a 64-bit fraction, from the bits of the fp64
 // f: mantissa times the first 64 bits of 2 / pi, shifted by the exponent. The
@@ -71,33 +75,69 @@ struct alignas(V * sizeof(T)) Vec {
   T e[V];
 };
 
-// kVec elements per access. A chunk of a token's head is kVec pairs: in the half
-// layout two accesses, at i and i + n; interleaved, two accesses side by side.
-// Chunks behind the rotated ones copy 2 * kVec elements.
+// This thread's copy of 16 bytes into shared memory, in the current group.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void copy_wait() {  // all but the last n groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// kVec elements per access. A chunk of a token's head is kVec pairs in two accesses
+// half the rotated part apart, whatever the layout, so that each access of a warp
+// is contiguous (16-byte halves of a sector would each fetch the whole one); one
+// pair when kVec is 1. Chunks behind the rotated ones copy two accesses.
 template <typename T, int kVec, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int heads_each) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p, int heads_each) {
   using V = Vec<T, kVec>;
+  constexpr bool kAsync = sizeof(V) == 16;
+  __shared__ V slots[kAsync ? kStages : 1][2][kAsync ? kRopeThreads : 1];
   const int n = p.rot / 2;
   const int rot_chunks = n / kVec;
-  const int chunks = rot_chunks + (p.d - p.rot + 2 * kVec - 1) / (2 * kVec);
+  const int copy_chunks = (p.d - p.rot + 2 * kVec - 1) / (2 * kVec);
+  const int chunks = rot_chunks + copy_chunks;
   const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const long long token = id / chunks;
   if (token >= static_cast<long long>(p.B) * p.N) return;
   const int chunk = static_cast<int>(id - token * chunks);
-  const int b = static_cast<int>(token / p.N), t = static_cast<int>(token - static_cast<long long>(b) * p.N);
+  const int b = static_cast<int>(token) / p.N, t = static_cast<int>(token) - b * p.N;
   const bool rotated = chunk < rot_chunks;
 
   // element offsets of the chunk's two accesses within a head
   int e0, e1;
   bool two = true;
   if (rotated) {
-    e0 = kInterleaved ? 2 * kVec * chunk : kVec * chunk;
-    e1 = kInterleaved ? e0 + kVec : e0 + n;
+    e0 = kInterleaved && kVec == 1 ? 2 * chunk : kVec * chunk;
+    e1 = kInterleaved && kVec == 1 ? e0 + 1 : e0 + n;
   } else {
-    e0 = p.rot + 2 * kVec * (chunk - rot_chunks);
-    e1 = e0 + kVec;
+    e0 = p.rot + kVec * (chunk - rot_chunks);
+    e1 = e0 + kVec * copy_chunks;
     two = e1 < p.d;
   }
+
+  const int H = p.t[0].H + p.t[1].H;
+  const int h0 = blockIdx.y * heads_each, h1 = min(H, h0 + heads_each);
+  auto source = [&](int h) {
+    const bool first = h < p.t[0].H;
+    const RopeTensor& r = p.t[first ? 0 : 1];
+    return static_cast<const T*>(r.x) + b * r.xs[0] + (first ? h : h - p.t[0].H) * r.xs[1] + t * r.xs[2];
+  };
+  auto fetch = [&](int h, int slot) {
+    if constexpr (kAsync) {
+      if (h < h1) {
+        const T* src = source(h);
+        copy16(&slots[slot][0][threadIdx.x], src + e0);
+        if (two) copy16(&slots[slot][1][threadIdx.x], src + e1);
+      }
+      copy_commit();
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) fetch(h0 + i, i);
 
   float cs[kVec], sn[kVec];
 #pragma unroll
@@ -107,7 +147,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       bool finite;
-      const uint64_t f = turns_per_position(p.freqs[kVec * chunk + i], finite);
+      // interleaved: the first access holds pairs e0 / 2 .., the second pairs e1 / 2 ..
+      const int pair = !kInterleaved || kVec == 1 ? kVec * chunk + i
+                                                  : (i < kVec / 2 ? e0 : e1 - kVec) / 2 + i;
+      const uint64_t f = turns_per_position(p.freqs[pair], finite);
       const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * f;
       // the top 32 bits in units of half turns, in [-1, 1)
       const float half_turns =
@@ -119,58 +162,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
     }
   }
 
-  const int H = p.t[0].H + p.t[1].H;
-  const int h0 = blockIdx.y * heads_each, h1 = min(H, h0 + heads_each);
-  for (int h = h0; h < h1; h += kUnroll) {
-    V x0[kUnroll], x1[kUnroll];
-    T* dst[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int hh = h + u;
-      const bool live = hh < h1;
-      const RopeTensor& r = p.t[hh < p.t[0].H ? 0 : 1];
-      const int hl = hh < p.t[0].H ? hh : hh - p.t[0].H;
-      dst[u] = nullptr;
-      if (live) {
-        const T* src = static_cast<const T*>(r.x) + b * r.xs[0] + hl * r.xs[1] + t * r.xs[2];
-        dst[u] = static_cast<T*>(r.y) + b * r.ys[0] + hl * r.ys[1] + t * r.ys[2];
-        x0[u] = *reinterpret_cast<const V*>(src + e0);
-        if (two) x1[u] = *reinterpret_cast<const V*>(src + e1);
-      }
+  int slot = 0;
+  for (int h = h0; h < h1; ++h) {
+    V x0, x1;
+    if constexpr (kAsync) {
+      copy_wait<kStages - 1>();
+      x0 = slots[slot][0][threadIdx.x];
+      if (two) x1 = slots[slot][1][threadIdx.x];
+    } else {
+      const T* src = source(h);
+      x0 = *reinterpret_cast<const V*>(src + e0);
+      if (two) x1 = *reinterpret_cast<const V*>(src + e1);
     }
+    const bool first = h < p.t[0].H;
+    const RopeTensor& r = p.t[first ? 0 : 1];
+    T* dst = static_cast<T*>(r.y) + b * r.ys[0] + (first ? h : h - p.t[0].H) * r.ys[1] + t * r.ys[2];
+    if (rotated) {
+      V y0, y1;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (dst[u] == nullptr) continue;
-      if (rotated) {
-        V y0, y1;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          // pair i: elements (i, i + n) or (2i, 2i + 1)
-          float a, c;
-          if constexpr (!kInterleaved) {
-            a = to_f<T>(x0[u].e[i]);
-            c = to_f<T>(x1[u].e[i]);
-          } else {
-            a = to_f<T>(2 * i < kVec ? x0[u].e[(2 * i) % kVec] : x1[u].e[(2 * i) % kVec]);
-            c = to_f<T>(2 * i + 1 < kVec ? x0[u].e[(2 * i + 1) % kVec] : x1[u].e[(2 * i + 1) % kVec]);
-          }
-          const T ya = from_f<T>(a * cs[i] - c * sn[i]);
-          const T yc = from_f<T>(c * cs[i] + a * sn[i]);
-          if constexpr (!kInterleaved) {
-            y0.e[i] = ya;
-            y1.e[i] = yc;
-          } else {
-            if (2 * i < kVec) y0.e[(2 * i) % kVec] = ya; else y1.e[(2 * i) % kVec] = ya;
-            if (2 * i + 1 < kVec) y0.e[(2 * i + 1) % kVec] = yc; else y1.e[(2 * i + 1) % kVec] = yc;
-          }
+      for (int i = 0; i < kVec; ++i) {
+        // pair i: element i of both accesses, or elements 2 i and 2 i + 1 of the two in a row
+        float a, c;
+        if constexpr (!kInterleaved) {
+          a = to_f<T>(x0.e[i]);
+          c = to_f<T>(x1.e[i]);
+        } else {
+          a = to_f<T>(2 * i < kVec ? x0.e[(2 * i) % kVec] : x1.e[(2 * i) % kVec]);
+          c = to_f<T>(2 * i + 1 < kVec ? x0.e[(2 * i + 1) % kVec] : x1.e[(2 * i + 1) % kVec]);
         }
-        *reinterpret_cast<V*>(dst[u] + e0) = y0;
-        *reinterpret_cast<V*>(dst[u] + e1) = y1;
-      } else {
-        *reinterpret_cast<V*>(dst[u] + e0) = x0[u];
-        if (two) *reinterpret_cast<V*>(dst[u] + e1) = x1[u];
+        const T ya = from_f<T>(a * cs[i] - c * sn[i]);
+        const T yc = from_f<T>(c * cs[i] + a * sn[i]);
+        if constexpr (!kInterleaved) {
+          y0.e[i] = ya;
+          y1.e[i] = yc;
+        } else {
+          if (2 * i < kVec) y0.e[(2 * i) % kVec] = ya; else y1.e[(2 * i) % kVec] = ya;
+          if (2 * i + 1 < kVec) y0.e[(2 * i + 1) % kVec] = yc; else y1.e[(2 * i + 1) % kVec] = yc;
+        }
       }
+      x0 = y0;
+      x1 = y1;
     }
+    *reinterpret_cast<V*>(dst + e0) = x0;
+    if (two) *reinterpret_cast<V*>(dst + e1) = x1;
+    fetch(h + kStages, slot);
+    slot = slot + 1 == kStages ? 0 : slot + 1;
   }
 }
 
@@ -181,14 +217,12 @@ cudaError_t launch_rope_t(const RopeParams& p, int num_sms, cudaStream_t s) {
   const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int H = p.t[0].H + p.t[1].H;
-  // Heads per thread: as many as leave four blocks for every SM, so that long
-  // calls share the sines over all heads and short ones spread over the GPU.
-  int groups = static_cast<int>((4LL * num_sms + blocks - 1) / blocks);
-  const int most = (H + kUnroll - 1) / kUnroll;
-  if (groups > most) groups = most;
-  int each = (H + groups - 1) / groups;
-  each = (each + kUnroll - 1) / kUnroll * kUnroll;
-  groups = (H + each - 1) / each;
+  // Heads per thread: as many as leave kBlocksPerSm blocks for every SM, so that
+  // long calls share the sines over many heads and short ones spread over the GPU.
+  int each = H;
+  const long long want = static_cast<long long>(kBlocksPerSm) * num_sms;
+  if (blocks < want) each = static_cast<int>(std::max(1LL, H * blocks / want));
+  const int groups = (H + each - 1) / each;
   if (groups > 65535) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
   if (p.interleaved)

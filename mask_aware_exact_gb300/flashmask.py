@@ -13,6 +13,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -120,7 +121,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.flashmask_status_string.argtypes = [i]
     L.flashmask_status_string.restype = ctypes.c_char_p
     i64, i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
-    L.flashmask_rope.argtypes = [ctypes.POINTER(_FmHeads), i, vp, i64, vp, i, i, i, i, i, i, f, i, vp]
+    L.flashmask_rope.argtypes = [vp, i, vp, i64, vp, i, i, i, i, i, i, f, i, vp]
     L.flashmask_rope.restype = i
     L.flashmask_cache_workspace_bytes.argtypes = [i, i, i, i, i, i]
     L.flashmask_cache_workspace_bytes.restype = sz
@@ -481,7 +482,8 @@ def flashmask_selftest_timeout(ws: torch.Tensor, limit_ns: int, ctas: int = 1, s
 # ---------------------------------------------------------------- rotary positions
 _ROPE_DTYPES = {torch.bfloat16: FM_BF16, torch.float16: FM_F16, torch.float32: FM_F32}
 _Strides = ctypes.c_int64 * 3
-_HeadsPair = _FmHeads * 2
+_HEADS = struct.Struct("@PPi6q")  # an _FmHeads: x, y, H, strides of x and y
+assert _HEADS.size == ctypes.sizeof(_FmHeads)
 
 
 def _launch(index, stream, tensors, call):
@@ -579,10 +581,8 @@ def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, whe
     def call(raw):
         ys = out or [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
         if B * N * d > 0:
-            heads = _HeadsPair()
-            for h, x, y in zip(heads, xs, ys):
-                h.x, h.y, h.H = x.data_ptr(), y.data_ptr(), x.shape[1]
-                h.xs[:], h.ys[:] = x.stride()[:3], y.stride()[:3]
+            heads = b"".join([_HEADS.pack(x.data_ptr(), y.data_ptr(), x.shape[1], *x.stride()[:3],
+                                          *y.stride()[:3]) for x, y in zip(xs, ys)])
             st = load().flashmask_rope(heads, len(xs), pos, pos_stride, freqs.data_ptr(), B, N, d, rot,
                                        bool(interleaved), dtype, mscale, inverse, raw)
             if st:
