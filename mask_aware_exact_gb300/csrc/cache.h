@@ -70,6 +70,13 @@ struct CacheFwdParams {
   uint32_t* part;       // [row tiles][words]: pages where intervals hide some key from some row
   int32_t* prefix;      // [row tiles][words + 1]: running count of visible pages
 };
+// Rows of the attention's work. The G = H / Hk query heads of a cache head and a
+// sequence's query tokens form one list of rows, r = t * G + g, cut into RT tiles.
+struct Geometry {
+  int G, rows, RT;  // query heads per cache head, rows of a tile, row tiles
+  int classes;      // mask classes: cache heads whose rows see the same masks share one
+  int words;        // 32-bit words of page bits
+};
 // Byte offsets of the workspace regions.
 struct CacheWs {
   size_t arrived, class_done, partial, vis, part, prefix, total;
@@ -78,6 +85,12 @@ constexpr int kCacheMaxCtas = 256;  // partial results are kept for at most this
 // Whether the pages of all row tiles can be counted in 32 bits.
 bool cache_line_ok(int B, int H, int Hk, int N, int max_pages);
 CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages);
+cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s);
+// Many query rows per cache head: tiles of 128 rows on the 5th-generation tensor cores.
+constexpr int kManyRows = 128;
+size_t cache_fwd_rows_part_floats(int d);  // of one partial result
+cudaError_t launch_cache_fwd_rows(int d, const CacheFwdParams& p, const Geometry& geo, int num_sms,
+                                  cudaStream_t s);
 cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s);
 
 }  // namespace fm

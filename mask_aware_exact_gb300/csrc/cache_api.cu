@@ -42,9 +42,9 @@ bool vectors_ok(const fm_mask* m) {
 bool cache_shape_ok(int B, int H, int Hk, int N, int d, int max_pages) {
   if (B <= 0 || H <= 0 || Hk <= 0 || N <= 0 || max_pages <= 0) return false;
   if (d != 64 && d != 128) return false;
-  if (H % Hk != 0 || Hk > 65535) return false;
+  if (H % Hk != 0 || Hk > 65535 || B > 65535) return false;
   if (max_pages > FM_MAX_SEQLEN / FM_PAGE || N > FM_MAX_SEQLEN) return false;
-  if (static_cast<long long>(B) * H > 0x7fffffffLL / N) return false;
+  if (static_cast<long long>(B) * H > 0x7fffffffLL / N) return false;  // rows fit 32 bits
   return fm::cache_line_ok(B, H, Hk, N, max_pages);
 }
 
@@ -171,7 +171,6 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   if (!std::isfinite(scale) || !(scale > 0.f)) return FM_ERR_INVALID_ARG;
   if (mask && !vectors_ok(mask)) return FM_ERR_INVALID_ARG;
   if (!cache_shape_ok(B, H, cache->Hk, N, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
-  if (B > 65535) return FM_ERR_UNSUPPORTED;
   if (mask && (mask->Hm <= 0 || H % mask->Hm != 0)) return FM_ERR_UNSUPPORTED;
   const fm::CacheWs L = fm::cache_ws_layout(B, H, cache->Hk, N, cache->d, max_pages);
   const fm_status st = check_ws(ws, ws_bytes, L.total);

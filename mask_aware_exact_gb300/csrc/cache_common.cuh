@@ -1,0 +1,258 @@
+// Parts shared by the two kernels of the attention over the paged cache: rows and
+// pages, the cut of the line of pages into runs, waits and conversions.
+#pragma once
+#include "cache.h"
+#include "ptx_fp8.cuh"
+
+namespace fm {
+
+// ---------------------------------------------------------------- geometry
+
+// Row tile `rt` of sequence b: its query tokens [t_lo, t_hi] at positions t + shift,
+// none when t_hi < t_lo; len is the sequence's length, cut to what the table holds.
+struct RowTile {
+  int len, live, shift, t_lo, t_hi;
+};
+__device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, const Geometry& geo, int b, int rt,
+                                            bool record) {
+  RowTile r;
+  r.live = p.q_lens ? min(max(p.q_lens[b], 0), p.N) : p.N;
+  r.len = p.lens[b];
+  const int most = p.max_pages * kPage;
+  if (r.len < 0 || r.len > most) {
+    if (record) record_failure(p.status, kStatusPage, kSiteCacheLen);
+    r.len = min(max(r.len, 0), most);
+  }
+  r.shift = r.len - r.live;
+  const uint32_t G = geo.G, rows = G * r.live, r0 = static_cast<uint32_t>(rt) * geo.rows;
+  r.t_lo = static_cast<int>(r0 / G);
+  r.t_hi = r0 < rows ? static_cast<int>(min(r0 + geo.rows - 1, rows - 1) / G) : r.t_lo - 1;
+  return r;
+}
+
+__device__ __forceinline__ int mask_class(const CacheFwdParams& p, const Geometry& geo, int hk) {
+  return geo.classes == p.c.Hk ? hk : hk / (p.c.Hk / geo.classes);
+}
+
+// Pages on a segment's line.
+template <bool kVec>
+__device__ __forceinline__ int pages_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
+  const int rt = seg % geo.RT, bh = seg / geo.RT;
+  const int b = bh / p.c.Hk;
+  if constexpr (kVec) {
+    const int cls = mask_class(p, geo, bh - b * p.c.Hk);
+    const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
+    return p.prefix[at * (geo.words + 1) + geo.words];
+  } else {
+    const RowTile r = row_tile(p, geo, b, rt, false);
+    if (r.t_hi < r.t_lo) return 0;
+    const int lim = p.mask.causal ? min(r.len, r.shift + r.t_hi + 1) : r.len;
+    return lim > 0 ? (lim + kPage - 1) / kPage : 0;
+  }
+}
+
+// Index of the k-th set bit of x (k < popc(x)).
+__device__ __forceinline__ int nth_bit(uint32_t x, int k) {
+  int at = 0;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const int n = __popc((x >> at) & ((1u << s) - 1u));
+    if (k >= n) {
+      k -= n;
+      at += s;
+    }
+  }
+  return at;
+}
+
+// The k-th page on the line of row tile rt of (b, hk), and whether intervals hide
+// some of its keys from some row.
+template <bool kVec>
+__device__ __forceinline__ int page_on_line(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int rt,
+                                            int k, int& cut) {
+  cut = 0;
+  if constexpr (!kVec) return k;
+  const size_t at = (static_cast<size_t>(b) * geo.classes + mask_class(p, geo, hk)) * geo.RT + rt;
+  const int32_t* pre = p.prefix + at * (geo.words + 1);
+  int lo = 0, hi = geo.words;  // pre[lo] <= k < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= k) lo = mid; else hi = mid;
+  }
+  const int bit = nth_bit(p.vis[at * geo.words + lo], k - pre[lo]);
+  cut = (p.part[at * geo.words + lo] >> bit) & 1u;
+  return 32 * lo + bit;
+}
+
+// A CTA's run on the line of units (pages, or pairs of them) of all segments.
+struct Line {
+  int run;         // units of a full run
+  int lo, hi;      // this CTA's run
+  int seg, first;  // segment of its first unit, and that unit's number in it
+  bool any_empty;  // some segment has no unit
+};
+constexpr int kLineWords = 40;  // ints of shared memory for find_run
+// Segments of up to this many pages are not cut.
+constexpr int kUncut = 32;
+
+// Called by all kThreads threads of every CTA; units(s) is the number of units of
+// segment s, `pages` the pages of a unit.
+template <int kThreads, typename F>
+__device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* words, F units) {
+  constexpr int kWarps = kThreads / 32;
+  static_assert(2 * kWarps + 4 <= kLineWords, "shared words");
+  int* const wsum = words;
+  int* const wmax = words + kWarps;
+  int* const found = words + 2 * kWarps;  // lo, hi, segment, first
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int each = (nseg + kThreads - 1) / kThreads;
+  const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
+  int mine = 0, longest = 0;
+  bool empty = false;
+  for (int s = seg_lo; s < seg_hi; ++s) {
+    const int n = units(s);
+    mine += n;
+    longest = max(longest, n);
+    empty |= n == 0;
+  }
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    wsum[warp] = before;
+    wmax[warp] = longest;
+  }
+  Line r;
+  r.any_empty = __syncthreads_or(empty);
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int x = wsum[w];
+    if (w < warp) before += x;
+    total += x;
+    longest = max(longest, wmax[w]);
+  }
+  before -= mine;
+  r.run = max(min_run, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const bool uncut = longest <= max(kUncut / pages, r.run / 8);
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const long long x_wide = static_cast<long long>(r.run) * (blockIdx.x + side);
+    const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
+    if (x == total) {
+      if (tid == 0) found[side] = total;
+    } else if (before <= x && x < before + mine) {
+      int s = seg_lo, at = before, n;
+      while (x >= at + (n = units(s))) at += n, ++s;
+      const bool next = uncut && x != at;  // on to the segment's end
+      found[side] = next ? at + n : x;
+      if (side == 0) {
+        found[2] = next ? s + 1 : s;
+        found[3] = uncut ? 0 : x - at;
+      }
+    }
+  }
+  __syncthreads();
+  r.lo = found[0];
+  r.hi = found[1];
+  r.seg = found[2];
+  r.first = found[3];
+  return r;
+}
+
+// Units run_at .. + 31 of a CTA's run, one per lane: unit k of segment seg is lane
+// 0's. Returns how many there are within 32 segments (at most `most`); a lane gets
+// its segment, the unit's number in it and the segment's units.
+template <typename F>
+__device__ __forceinline__ int next_units(int seg, int k, int nseg, int most, F units, int& my_seg, int& my_k,
+                                          int& my_n) {
+  const int lane = threadIdx.x & 31;
+  const int s = seg + lane;
+  const int n_all = s < nseg ? units(s) : 0;
+  int c = n_all - (lane == 0 ? k : 0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, c, o);
+    // sums past 2^30 are only compared with lane numbers
+    if (lane >= o) c = min(c + x, 1 << 30);
+  }
+  int j = 0;  // segments that end at or before this lane's unit
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) {
+    const int x = __shfl_sync(0xffffffffu, c, j + i - 1);
+    if (x <= lane) j += i;
+  }
+  const int c_j = __shfl_sync(0xffffffffu, c, j);
+  my_n = __shfl_sync(0xffffffffu, n_all, j);
+  my_seg = seg + j;
+  my_k = my_n - (c_j - lane);
+  return min(__shfl_sync(0xffffffffu, c, 31), most);
+}
+
+// Four codes -> two fp16 pairs.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Bounded wait: gives up after the library's limit, or when another wait has (a
+// page error alone does not end waits).
+__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_t* status) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
+    if (global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
+      record_failure(status, kStatusTimeout, kSiteCacheWait);
+      return false;
+    }
+  }
+  return true;
+}
+// The same for a counter in shared memory that only grows.
+__device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* status) {
+  const volatile int* at = count;
+  const uint64_t t0 = global_timer_ns();
+  while (*at < want) {
+    if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
+    if (global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
+      record_failure(status, kStatusTimeout, kSiteCacheWait);
+      return false;
+    }
+  }
+  __threadfence_block();
+  return true;
+}
+// 2^(a - b) where either may be -inf (then a is, or both are).
+__device__ __forceinline__ float ex2_diff(float a, float b) { return a == b ? 1.f : ex2(a - b); }
+
+// O and LSE of a row from sums relative to m and mv.
+__device__ __forceinline__ float out_factor(float m, float mv, float l, float shift) {
+  // acc = 2^(shift - mv) sum P V and l = 2^-m sum P
+  const float f = mv == -INFINITY ? 0.f : ex2(mv - (m == -INFINITY ? 0.f : m) - shift);
+  return l == 0.f ? 0.f : f / l;
+}
+__device__ __forceinline__ float out_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+
+}  // namespace fm

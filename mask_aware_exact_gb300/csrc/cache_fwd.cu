@@ -3,7 +3,7 @@
 // reading the codes once bounds the call.
 //
 // Rows. The G = H / Hk query heads that share a cache head and the sequence's
-// query tokens form one list of rows, r = t * G + g, cut into tiles of 8, 16 or 32.
+// query tokens form one list of rows, r = t * G + g, here one tile of 8 or 16.
 // A segment is one (sequence, cache head, row tile); its work is the list of pages
 // that some row of it sees.
 //
@@ -42,9 +42,8 @@
 // + 3, which are the codes of word u of its 16-byte load of a V column.
 #include <atomic>
 
-#include "cache.h"
+#include "cache_common.cuh"
 #include "flashmask.h"
-#include "ptx_fp8.cuh"
 
 namespace fm {
 namespace {
@@ -57,152 +56,7 @@ constexpr int kBatch = 4 * kConsumers;  // tiles looked up at a time, one per la
 // Pages a run has at least: one for each consumer warp. Shorter runs only
 // add partial results.
 constexpr int kMinRun = kConsumers;
-constexpr int kUncut = 32;  // segments up to this many pages are not cut
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
-
-// ---------------------------------------------------------------- geometry
-struct Geometry {
-  int G, rows, RT, classes, words;  // query heads per cache head, rows of a tile, row tiles, mask
-                                    // classes, words of page bits
-};
-
-// Row tile `rt` of sequence b: its query tokens [t_lo, t_hi] at positions t + shift,
-// none when t_hi < t_lo; len is the sequence's length, cut to what the table holds.
-struct RowTile {
-  int len, live, shift, t_lo, t_hi;
-};
-__device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, const Geometry& geo, int b, int rt,
-                                            bool record) {
-  RowTile r;
-  r.live = p.q_lens ? min(max(p.q_lens[b], 0), p.N) : p.N;
-  r.len = p.lens[b];
-  const int most = p.max_pages * kPage;
-  if (r.len < 0 || r.len > most) {
-    if (record) record_failure(p.status, kStatusPage, kSiteCacheLen);
-    r.len = min(max(r.len, 0), most);
-  }
-  r.shift = r.len - r.live;
-  const uint32_t G = geo.G, rows = G * r.live, r0 = static_cast<uint32_t>(rt) * geo.rows;
-  r.t_lo = static_cast<int>(r0 / G);
-  r.t_hi = r0 < rows ? static_cast<int>(min(r0 + geo.rows - 1, rows - 1) / G) : r.t_lo - 1;
-  return r;
-}
-
-__device__ __forceinline__ int mask_class(const CacheFwdParams& p, const Geometry& geo, int hk) {
-  return geo.classes == p.c.Hk ? hk : hk / (p.c.Hk / geo.classes);
-}
-
-// Pages on a segment's line.
-template <bool kVec>
-__device__ __forceinline__ int pages_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
-  const int rt = seg % geo.RT, bh = seg / geo.RT;
-  const int b = bh / p.c.Hk;
-  if constexpr (kVec) {
-    const int cls = mask_class(p, geo, bh - b * p.c.Hk);
-    const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
-    return p.prefix[at * (geo.words + 1) + geo.words];
-  } else {
-    const RowTile r = row_tile(p, geo, b, rt, false);
-    if (r.t_hi < r.t_lo) return 0;
-    const int lim = p.mask.causal ? min(r.len, r.shift + r.t_hi + 1) : r.len;
-    return lim > 0 ? (lim + kPage - 1) / kPage : 0;
-  }
-}
-
-// ---------------------------------------------------------------- visible pages
-// Bits of the pages that some row of a row tile sees (vis), of those where an
-// interval hides some key from some row (part), and the running count of the
-// former per word (prefix; its last entry is the total). A CTA takes one word, 32
-// pages; a key hides the positions [lo, hi] of the tile if the union of its
-// intervals covers them. The CTA that finishes a row tile last sums its words.
-__global__ void __launch_bounds__(256) cache_classify(const CacheFwdParams p, const Geometry geo) {
-  __shared__ uint32_t bits[2];
-  __shared__ int last;
-  const int w = blockIdx.x, b = blockIdx.z;
-  const int cls = blockIdx.y / geo.RT, rt = blockIdx.y % geo.RT;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RowTile r = row_tile(p, geo, b, rt, w == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-  const int lo = r.shift + r.t_lo, hi = r.shift + r.t_hi;
-  int m0 = cls, m1 = cls;  // mask heads of the class
-  if (geo.classes != p.mask.Hm) {
-    const int each = p.H / p.mask.Hm;
-    m0 = cls * geo.G / each;
-    m1 = (cls * geo.G + geo.G - 1) / each;
-  }
-  if (threadIdx.x < 2) bits[threadIdx.x] = 0;
-  __syncthreads();
-  const int L = p.max_pages * kPage;
-  uint32_t vis = 0, part = 0;
-  for (int i = 0; i < 4; ++i) {
-    const int page = 32 * w + 4 * warp + i;
-    bool see = false, cut = false;
-    for (int half = 0; half < 2; ++half) {
-      const int j = page * kPage + 32 * half + lane;
-      if (j >= r.len || hi < lo || (p.mask.causal && j > hi)) continue;
-      for (int m = m0; m <= m1; ++m) {
-        const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j;
-        const int s0 = p.mask.lts ? p.mask.lts[at] : 0, e0 = p.mask.lts ? p.mask.lte[at] : 0;
-        const int s1 = p.mask.uts ? p.mask.uts[at] : 0, e1 = p.mask.uts ? p.mask.ute[at] : 0;
-        cut |= max(s0, lo) < min(e0, hi + 1) || max(s1, lo) < min(e1, hi + 1);
-        int reach = p.mask.causal ? max(lo, j) : lo;  // first position not known to be hidden
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (s0 <= reach && reach < e0) reach = e0;
-          if (s1 <= reach && reach < e1) reach = e1;
-        }
-        see |= reach <= hi;
-      }
-    }
-    if (__any_sync(0xffffffffu, see)) vis |= 1u << (4 * warp + i);
-    if (__any_sync(0xffffffffu, cut)) part |= 1u << (4 * warp + i);
-  }
-  if (lane == 0) {
-    atomicOr(&bits[0], vis);
-    atomicOr(&bits[1], part);
-  }
-  __syncthreads();
-  const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
-  if (threadIdx.x == 0) {
-    p.vis[at * geo.words + w] = bits[0];
-    p.part[at * geo.words + w] = bits[1];
-    __threadfence();
-    last = atomicAdd(&p.class_done[at], 1) == geo.words - 1;
-  }
-  __syncthreads();
-  if (!last || warp != 0) return;
-  __threadfence();
-  int sum = 0;
-  int32_t* out = p.prefix + at * (geo.words + 1);
-  for (int w0 = 0; w0 < geo.words; w0 += 32) {
-    const int n = w0 + lane < geo.words ? __popc(__ldcg(&p.vis[at * geo.words + w0 + lane])) : 0;
-    int c = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += x;
-    }
-    if (w0 + lane < geo.words) out[w0 + lane] = sum + c - n;
-    sum += __shfl_sync(0xffffffffu, c, 31);
-  }
-  if (lane == 0) {
-    out[geo.words] = sum;
-    p.class_done[at] = 0;
-  }
-}
-
-// Index of the k-th set bit of x (k < popc(x)).
-__device__ __forceinline__ int nth_bit(uint32_t x, int k) {
-  int at = 0;
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    const int n = __popc((x >> at) & ((1u << s) - 1u));
-    if (k >= n) {
-      k -= n;
-      at += s;
-    }
-  }
-  return at;
-}
 
 // ---------------------------------------------------------------- instructions
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -212,57 +66,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four codes -> two fp16 pairs.
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-// Bounded wait: gives up after the library's limit, or when another wait has (a
-// page error alone does not end waits).
-__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_t* status) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
-    if (global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
-      record_failure(status, kStatusTimeout, kSiteCacheWait);
-      return false;
-    }
-  }
-  return true;
-}
-// The same for a counter in shared memory that only grows.
-__device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* status) {
-  const volatile int* at = count;
-  const uint64_t t0 = global_timer_ns();
-  while (*at < want) {
-    if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
-    if (global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
-      record_failure(status, kStatusTimeout, kSiteCacheWait);
-      return false;
-    }
-  }
-  __threadfence_block();
-  return true;
-}
-// 2^(a - b) where either may be -inf (then a is, or both are).
-__device__ __forceinline__ float ex2_diff(float a, float b) { return a == b ? 1.f : ex2(a - b); }
-
 template <int D, int NT>
 struct Smem {
   static constexpr int kRows = 8 * NT;
@@ -275,10 +78,10 @@ struct Smem {
   static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8], see below
   static constexpr int kBars = kPiece + kPieceRing * 32;
   static constexpr int kNumBars = 2 * kConsumers * kSlots + 2 * kPieceRing + 1;
-  static constexpr int kScan = kBars + kNumBars * 8;  // int [32], see the kernel
-  static constexpr int kBytes = kScan + 32 * 4;
+  static constexpr int kScan = kBars + kNumBars * 8;  // int [kLineWords + 12], see the kernel
+  static constexpr int kBytes = kScan + (kLineWords + 12) * 4;
 };
-static_assert(Smem<128, 2>::kBytes <= 227 * 1024 && Smem<64, 4>::kBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(Smem<128, 2>::kBytes <= 227 * 1024 && Smem<64, 2>::kBytes <= 227 * 1024, "shared memory per CTA");
 
 struct Bars {
   uint32_t base;
@@ -346,16 +149,6 @@ struct State {
   }
 };
 
-// Writes rows of O and LSE from sums relative to m and mv.
-__device__ __forceinline__ float out_factor(float m, float mv, float l) {
-  // acc = 2^(14 - mv) sum P V and l = 2^-m sum P
-  const float f = mv == -INFINITY ? 0.f : ex2(mv - (m == -INFINITY ? 0.f : m) - kPShift);
-  return l == 0.f ? 0.f : f / l;
-}
-__device__ __forceinline__ float out_lse(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
-}
-
 // LSE of the rows r0 and r0 + 1 of a lane.
 __device__ __forceinline__ void store_lse(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0,
                                           int rows, bool mine, const float (&m)[2], const float (&l)[2]) {
@@ -388,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   const int nseg = p.B * p.c.Hk * geo.RT;
   const Bars bar{smem_u32(smem + S::kBars)};
   int* scan = reinterpret_cast<int*>(smem + S::kScan);  // see the words below
-  enum { kWSum = 0, kWMax = 8, kSeg = 16, kFirst, kLo, kHi, kCount, kJobs, kMerged, kJob0 = 24 };
+  enum { kCount = kLineWords, kJobs, kMerged, kJob0 };
 
   if (tid < S::kNumBars) {
     // one arrival each, but of piece_empty and done, where every consumer warp arrives
@@ -398,108 +191,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   }
   if (tid >= kCount && tid <= kMerged) scan[tid] = 0;
 
-  // the line's length, its longest segment, and where this CTA's run begins and ends
-  const int each = (nseg + kThreads - 1) / kThreads;
-  const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
-  int mine = 0, longest = 0;
-  bool empty = false;
-  for (int s = seg_lo; s < seg_hi; ++s) {
-    const int n = pages_of<kVec>(p, geo, s);
-    mine += n;
-    longest = max(longest, n);
-    empty |= n == 0;
-  }
-  int before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    scan[kWSum + warp] = before;
-    scan[kWMax + warp] = longest;
-  }
-  const bool any_empty = __syncthreads_or(empty);
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int x = scan[kWSum + w];
-    if (w < warp) before += x;
-    total += x;
-    longest = max(longest, scan[kWMax + w]);
-  }
-  before -= mine;
-  const int run = max(kMinRun, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  const bool uncut = longest <= max(kUncut, run / 8);
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const long long x_wide = static_cast<long long>(run) * (blockIdx.x + side);
-    const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
-    if (x == total) {
-      if (tid == 0) scan[kLo + side] = total;
-    } else if (before <= x && x < before + mine) {
-      int s = seg_lo, at = before, n;
-      while (x >= at + (n = pages_of<kVec>(p, geo, s))) at += n, ++s;
-      const bool next = uncut && x != at;  // on to the segment's end
-      scan[kLo + side] = next ? at + n : x;
-      if (side == 0) {
-        scan[kSeg] = next ? s + 1 : s;
-        scan[kFirst] = next || uncut ? 0 : x - at;
-      }
-    }
-  }
-  __syncthreads();
-  const int run_lo = scan[kLo], run_hi = scan[kHi];
+  const Line line = find_run<kThreads>(nseg, kMinRun, 1, scan, [&](int seg) { return pages_of<kVec>(p, geo, seg); });
+  const int run = line.run, run_lo = line.lo, run_hi = line.hi;
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
-    int seg = scan[kSeg], k = scan[kFirst];
+    int seg = line.seg, k = line.first;
     const int tiles = run_hi - run_lo;
     bool ok = true;
     int pieces = 0;  // published so far
     int done = 0;
     while (ok && done < tiles) {
       // the next tiles of the run, one per lane, over the next 32 segments
-      const int s_l = seg + lane;
-      int n = s_l < nseg ? pages_of<kVec>(p, geo, s_l) : 0;
-      const int n_all = n;
-      if (lane == 0) n -= k;
-      int c = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, c, o);
-        // sums past 2^30 are only compared with tile numbers below 32
-        if (lane >= o) c = min(c + x, 1 << 30);
-      }
-      const int avail = min(min(__shfl_sync(0xffffffffu, c, 31), kBatch), tiles - done);
-      int j = 0;  // segments that end at or before this lane's tile
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) {
-        const int x = __shfl_sync(0xffffffffu, c, j + s - 1);
-        if (x <= lane) j += s;
-      }
-      const int c_j = __shfl_sync(0xffffffffu, c, j), n_j = __shfl_sync(0xffffffffu, n_all, j);
-      const int my_seg = seg + j;
-      const int my_k = n_j - (c_j - lane);  // the tile's number in its segment
+      int my_seg, my_k, n_j;
+      const int avail = next_units(
+          seg, k, nseg, min(kBatch, tiles - done), [&](int sg) { return pages_of<kVec>(p, geo, sg); }, my_seg, my_k, n_j);
       const bool live = lane < avail;
       int page = -1, logical = 0, cut = 0;
       size_t ph = 0;
       if (live) {
         const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-        logical = my_k;
-        if constexpr (kVec) {
-          const size_t at = (static_cast<size_t>(b) * geo.classes + mask_class(p, geo, hk)) * geo.RT + rt;
-          const int32_t* pre = p.prefix + at * (geo.words + 1);
-          int lo = 0, hi = geo.words;  // pre[lo] <= my_k < pre[hi]
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= my_k) lo = mid; else hi = mid;
-          }
-          const int bit = nth_bit(p.vis[at * geo.words + lo], my_k - pre[lo]);
-          logical = 32 * lo + bit;
-          cut = (p.part[at * geo.words + lo] >> bit) & 1u;
-        }
+        logical = page_on_line<kVec>(p, geo, b, hk, rt, my_k, cut);
         page = p.table[static_cast<size_t>(b) * p.max_pages + logical];
         if (page < 0 || page >= p.c.pages) {
           record_failure(p.status, kStatusPage, kSiteCachePage);
@@ -895,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     if (whole) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float f0 = out_factor(st.m[t][0], st.mv[t][0], st.l[t][0]);
-        const float f1 = out_factor(st.m[t][1], st.mv[t][1], st.l[t][1]);
+        const float f0 = out_factor(st.m[t][0], st.mv[t][0], st.l[t][0], kPShift);
+        const float f1 = out_factor(st.m[t][1], st.mv[t][1], st.l[t][1], kPShift);
         const int rr = rt * kRows + 8 * t + g;  // the row this lane holds after the transposes
         const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
         uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;
@@ -970,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
         sum[2] += v.z * f[0];
         sum[3] += v.w * f[1];
       }
-      const float f0 = out_factor(m[0], mv[0], l[0]), f1 = out_factor(m[1], mv[1], l[1]);
+      const float f0 = out_factor(m[0], mv[0], l[0], kPShift), f1 = out_factor(m[1], mv[1], l[1], kPShift);
       const int rr = rt * kRows + 8 * t + g;
       const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
       uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 16 * n + 2 * c;
@@ -984,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   }
 
   // segments without a visible page: O = 0, LSE = -inf
-  for (int seg = blockIdx.x + gridDim.x * warp; ok && any_empty && seg < nseg; seg += gridDim.x * kConsumers) {
+  for (int seg = blockIdx.x + gridDim.x * warp; ok && line.any_empty && seg < nseg; seg += gridDim.x * kConsumers) {
     if (pages_of<kVec>(p, geo, seg) != 0) continue;
     const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
     const RowTile r = row_tile(p, geo, b, rt, lane == 0);
@@ -1016,9 +728,8 @@ cudaError_t allow_smem() {
 template <int D, int NT, bool kVec>
 cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
   if (kVec) {
-    const dim3 grid(static_cast<unsigned>(geo.words), static_cast<unsigned>(geo.classes * geo.RT),
-                    static_cast<unsigned>(p.B));
-    cache_classify<<<grid, 256, 0, s>>>(p, geo);
+    const cudaError_t c = launch_cache_classify(p, geo, s);
+    if (c != cudaSuccess) return c;
   }
   const cudaError_t e = allow_smem<D, NT, kVec>();
   if (e != cudaSuccess) return e;
@@ -1034,14 +745,14 @@ cudaError_t launch_nt(const CacheFwdParams& p, const Geometry& geo, int num_sms,
 }
 
 // Rows of a tile: as few as hold all rows, so that no columns of an instruction are
-// empty, up to what the accumulators leave registers for.
-int rows_of_tile(int rows, int d) { return rows <= 8 ? 8 : rows <= 16 || d == 128 ? 16 : 32; }
+// empty; above 16 rows the kernel for many rows takes over.
+int rows_of_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kManyRows; }
 
-Geometry geometry(int H, int Hk, int Hm, int N, int d, int max_pages) {
+Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
   Geometry g;
   g.G = H / Hk;
   const int rows = g.G * N;  // below 2^31: B * H * N is
-  g.rows = rows_of_tile(rows, d);
+  g.rows = rows_of_tile(rows);
   g.RT = (rows - 1) / g.rows + 1;
   g.classes = Hk % Hm == 0 ? Hm : Hk;
   g.words = (max_pages + 31) / 32;
@@ -1053,12 +764,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 bool cache_line_ok(int B, int H, int Hk, int N, int max_pages) {
-  const long long tiles = (static_cast<long long>(H / Hk) * N + 7) / 8;
-  return static_cast<double>(B) * Hk * tiles * max_pages < 2147483648.0;
+  const Geometry g = geometry(H, Hk, Hk, N, max_pages);
+  return static_cast<double>(B) * Hk * g.RT * max_pages < 2147483648.0;
 }
 
 CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
-  const Geometry g = geometry(H, Hk, Hk, N, d, max_pages);
+  const Geometry g = geometry(H, Hk, Hk, N, max_pages);
   const size_t tiles = static_cast<size_t>(B) * Hk * g.RT;
   CacheWs w;
   size_t off = 256;  // the status word
@@ -1067,7 +778,8 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   w.class_done = off;
   off = up256(off + tiles * 4);
   w.partial = off;
-  off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 * part_floats(d, g.rows) * 4);
+  off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 *
+                    (g.rows == kManyRows ? cache_fwd_rows_part_floats(d) : part_floats(d, g.rows)) * 4);
   w.vis = off;
   off = up256(off + tiles * g.words * 4);
   w.part = off;
@@ -1079,11 +791,9 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
 }
 
 cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s) {
-  const Geometry geo = geometry(p.H, p.c.Hk, p.mask.Hm, p.N, d, p.max_pages);
-  if (d == 64)
-    return geo.rows == 8    ? launch_nt<64, 1>(p, geo, num_sms, s)
-           : geo.rows == 16 ? launch_nt<64, 2>(p, geo, num_sms, s)
-                            : launch_nt<64, 4>(p, geo, num_sms, s);
+  const Geometry geo = geometry(p.H, p.c.Hk, p.mask.Hm, p.N, p.max_pages);
+  if (geo.rows == kManyRows) return launch_cache_fwd_rows(d, p, geo, num_sms, s);
+  if (d == 64) return geo.rows == 8 ? launch_nt<64, 1>(p, geo, num_sms, s) : launch_nt<64, 2>(p, geo, num_sms, s);
   return geo.rows == 8 ? launch_nt<128, 1>(p, geo, num_sms, s) : launch_nt<128, 2>(p, geo, num_sms, s);
 }
 

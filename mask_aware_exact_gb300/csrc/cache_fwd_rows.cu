@@ -1,0 +1,726 @@
+// Attention over the 8-bit paged cache for many query rows per cache head (chunks
+// of prompts, drafted tokens of large groups): tiles of 128 rows on tcgen05.
+//
+// The line of pages, its cut into equal runs and the joins are those of the kernel
+// for few rows; a unit of the line is a step of two pages, 128 keys. The codes of a
+// step arrive by bulk copies and four warps turn them into fp16 operands in shared
+// memory (exact), K as [key][d] and V as [d][key], both K-major and 128-byte
+// swizzled; S = Q K^T and O += P V then run as kind::f16 with P in TMEM. Taking Q and
+// P as several e4m3 parts would need no conversion, but four parts of Q and two of
+// P to keep their precision: more tensor work than fp16 and the same operand reads.
+//
+// As in the forward on bf16 tensors two softmax warpgroups split the keys of a step,
+// warpgroup w taking page w, with states and accumulators O_w of their own, merged
+// when a piece ends. So a warpgroup meets one K scale and one V scale a step: the
+// first goes into the exponent, the second into P, relative to the row's largest
+// P * scale so far (mv, beside m of the scores), so that neither the weights of
+// pages with small values nor the values of pages with small weights are lost. P is
+// stored as fp16(2^7 P * scale / 2^mv) and O_w rescaled only when mv grows by more
+// than 2^8.
+//
+// Warp roles (512 threads):
+//   0-7    softmax: thread (w, r) owns row r (= TMEM lane) and the 64 keys of page w;
+//          also bring in Q at the start of a piece and write the results at its end.
+//   8      S issuer, 9 P V issuer (one thread each).
+//   10     walks the run, looks pages up, issues the copies, publishes a step's
+//          description to all roles (ring of kMetaRing).
+//   12-15  conversion.
+// TMEM: S regions [0,128) [128,256), O_0 [256, 256+d), O_1 [384, 384+d); P over S.
+//
+// What bounds it: shared memory. A step with d = 128 writes 32 KB of codes and 64 KB of
+// fp16 operands and reads 32 KB and 96 KB, 224 KB at 128 bytes a clock: 1 750 cycles,
+// about the softmax warps' latency chain (1 550).
+#include <atomic>
+
+#include "cache_common.cuh"
+#include "flashmask.h"
+
+namespace fm {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = kManyRows;
+constexpr int kMetaRing = 8;
+constexpr int kStages = 4;  // staged code tiles: K and V of two steps
+constexpr int kMetaInts = 16;
+constexpr int kMinRun = 4;  // steps
+constexpr float kPShift = 7.f;
+constexpr float kLag = 8.f;  // mv may lag the row's largest product by this much (log2)
+
+enum MetaWord { kSeg, kFlags, kJ0, kKs = kJ0 + 2, kVs = kKs + 2, kValid = kVs + 2, kCut = kValid + 2, kCta0, kParts };
+enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16 };
+
+template <int D>
+struct Layout {
+  static constexpr int kTile = 128 * D * 2;  // fp16 operand tile
+  static constexpr int kCodes = 128 * D;     // codes of a step, K or V
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kTile;
+  static constexpr int kV = kK + 2 * kTile;
+  static constexpr int kStage = kV + 2 * kTile;
+  static constexpr int kMeta = kStage + kStages * kCodes;
+  static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
+  static constexpr int kBar = kWords + (kLineWords + 4) * 4;
+  static constexpr int kNumBars = 2 * kStages + kMetaRing + 4 * 3 + 3;
+  static constexpr int kTmemSlot = kBar + kNumBars * 8;
+  static constexpr int kBytes = kTmemSlot + 16;
+};
+static_assert(Layout<128>::kBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(Layout<128>::kBar % 8 == 0 && Layout<64>::kBar % 8 == 0, "barriers are 8-byte aligned");
+
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t at(int i) const { return base + 8 * i; }
+  __device__ uint32_t stage_full(int s) const { return at(s); }                // bytes
+  __device__ uint32_t stage_empty(int s) const { return at(kStages + s); }     // 4 conversion warps
+  __device__ uint32_t meta(int s) const { return at(2 * kStages + s); }        // 1
+  __device__ uint32_t k_ready(int s) const { return at(2 * kStages + kMetaRing + s); }       // 4
+  __device__ uint32_t v_ready(int s) const { return at(2 * kStages + kMetaRing + 2 + s); }   // 4
+  __device__ uint32_t s_full(int g) const { return at(2 * kStages + kMetaRing + 4 + g); }    // commit
+  __device__ uint32_t p_full(int g) const { return at(2 * kStages + kMetaRing + 6 + g); }    // 8
+  __device__ uint32_t pv_done(int g) const { return at(2 * kStages + kMetaRing + 8 + g); }   // commit
+  __device__ uint32_t q_full() const { return at(2 * kStages + kMetaRing + 10); }            // 8
+  __device__ uint32_t o_free() const { return at(2 * kStages + kMetaRing + 11); }            // 8
+  __device__ uint32_t softmax() const { return at(2 * kStages + kMetaRing + 12); }           // 8
+};
+
+__device__ __forceinline__ uint32_t col_o(int w) { return 256u + 128u * static_cast<uint32_t>(w); }
+
+// Instruction descriptor, kind::f16 with fp16 A and B (format code 0), both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Steps on a segment's line.
+template <bool kVec>
+__device__ __forceinline__ int steps_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
+  return (pages_of<kVec>(p, geo, seg) + 1) >> 1;
+}
+
+// Bits of the keys j .. j + 63 with s <= pos < e.
+__device__ __forceinline__ uint64_t hidden64(const int32_t* s, const int32_t* e, int pos) {
+  uint64_t hid = 0;
+#pragma unroll 4
+  for (int q = 0; q < 16; ++q) {
+    const int4 a = *reinterpret_cast<const int4*>(s + 4 * q), z = *reinterpret_cast<const int4*>(e + 4 * q);
+    const uint32_t b = static_cast<uint32_t>(a.x <= pos && pos < z.x) | static_cast<uint32_t>(a.y <= pos && pos < z.y) << 1 |
+                       static_cast<uint32_t>(a.z <= pos && pos < z.z) << 2 | static_cast<uint32_t>(a.w <= pos && pos < z.w) << 3;
+    hid |= static_cast<uint64_t>(b) << (4 * q);
+  }
+  return hid;
+}
+
+// Scales n (32) TMEM columns of this warp's lanes by f.
+__device__ __forceinline__ void tmem_scale32(uint32_t taddr, float f) {
+  uint32_t v[32];
+  tmem_ld32(taddr, v);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+  tmem_st32(taddr, v);
+}
+
+// 16 codes -> 16 fp16 as two 16-byte units of a swizzled row; `odd` stores the second
+// one first, which keeps the eight lanes of a store on different banks.
+__device__ __forceinline__ void put_units(uint32_t tile, int row, int unit, const uint4& w, bool odd) {
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) codes_to_f16(word(w, i), h[2 * i], h[2 * i + 1]);
+  const uint32_t a0 = tile + sw128_offset(row, unit), a1 = tile + sw128_offset(row, unit + 1);
+  if (odd) {
+    st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+    st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+  } else {
+    st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+    st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+  }
+}
+
+// Floats of one partial result: O as float4 [D / 4][128 rows], then m, mv, l [128].
+constexpr __host__ __device__ int part_floats(int D) { return kRows * D + 3 * kRows; }
+
+template <int D, bool kVec>
+__global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const CacheFwdParams p, const Geometry geo) {
+  using L = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nseg = p.B * p.c.Hk * geo.RT;
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) record_failure(p.status, kStatusLayout, kSiteCacheWait);
+    return;
+  }
+  const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+  const Bars bar{smem_u32(smem + L::kBar)};
+  int* words = reinterpret_cast<int*>(smem + L::kWords);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  const int* meta_at = reinterpret_cast<const int*>(smem + L::kMeta);
+
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (tid < L::kNumBars) {
+    // arrivals: stage_full 1, stage_empty 4, meta 1, k_ready and v_ready 4, s_full 1,
+    // p_full 8, pv_done 1, q_full, o_free and softmax 8
+    const int i = tid - 2 * kStages - kMetaRing;
+    int n = 1;
+    if (tid >= kStages && tid < 2 * kStages) n = 4;
+    if (i >= 0 && i < 4) n = 4;
+    if (i == 6 || i == 7 || i >= 10) n = 8;
+    mbar_init(bar.at(tid), n);
+    fence_barrier_init();
+  }
+  const Line line = find_run<kThreads>(nseg, kMinRun, 2, words, [&](int s) { return steps_of<kVec>(p, geo, s); });
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Waits for the description of step J; false when the wait gave up.
+  auto step = [&](int J, int (&m)[kMetaInts]) -> bool {
+    if (!cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status)) return false;
+    const int4* at = reinterpret_cast<const int4*>(meta_at + (J % kMetaRing) * kMetaInts);
+#pragma unroll
+    for (int i = 0; i < kMetaInts / 4; ++i) {
+      const int4 v = at[i];
+      m[4 * i] = v.x, m[4 * i + 1] = v.y, m[4 * i + 2] = v.z, m[4 * i + 3] = v.w;
+    }
+    return true;
+  };
+
+  if (warp == 10) {
+    // ------------------------------------------------------------ run, pages, copies
+    int seg = line.seg, k = line.first, done = 0;
+    const int steps = line.hi - line.lo;
+    bool ok = true;
+    auto slot_free = [&](int seq) {
+      return seq < kStages || cache_wait(bar.stage_empty(seq % kStages), (seq / kStages - 1) & 1, p.status);
+    };
+    while (ok && done < steps) {
+      int my_seg, my_k, my_n;
+      const int avail = next_units(
+          seg, k, nseg, min(32, steps - done), [&](int s) { return steps_of<kVec>(p, geo, s); }, my_seg, my_k, my_n);
+      int page[2] = {-1, -1}, j0[2] = {-1, -1}, valid[2] = {0, 0}, cut[2] = {0, 0};
+      float ks[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};
+      if (lane < avail) {
+        const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+        const int pages = pages_of<kVec>(p, geo, my_seg);
+        const RowTile r = row_tile(p, geo, b, rt, true);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (2 * my_k + x >= pages) continue;
+          const int logical = page_on_line<kVec>(p, geo, b, hk, rt, 2 * my_k + x, cut[x]);
+          const int pg = p.table[static_cast<size_t>(b) * p.max_pages + logical];
+          if (pg < 0 || pg >= p.c.pages) {
+            record_failure(p.status, kStatusPage, kSiteCachePage);
+            continue;
+          }
+          const size_t ph = static_cast<size_t>(pg) * p.c.Hk + hk;
+          page[x] = pg;
+          j0[x] = logical * kPage;
+          valid[x] = min(r.len - j0[x], kPage);
+          ks[x] = p.c.kscale[ph];
+          vs[x] = p.c.vscale[ph];
+        }
+      }
+      for (int t = 0; ok && t < avail; ++t, ++done) {
+        const int sg = __shfl_sync(0xffffffffu, my_seg, t), kk = __shfl_sync(0xffffffffu, my_k, t);
+        const int nn = __shfl_sync(0xffffffffu, my_n, t);
+        int m[kMetaInts] = {};
+        int pg[2];
+        m[kSeg] = sg;
+        m[kCut] = __shfl_sync(0xffffffffu, cut[0] | cut[1] << 1, t);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          pg[x] = __shfl_sync(0xffffffffu, page[x], t);
+          m[kJ0 + x] = __shfl_sync(0xffffffffu, j0[x], t);
+          m[kKs + x] = __shfl_sync(0xffffffffu, __float_as_int(ks[x]), t);
+          m[kVs + x] = __shfl_sync(0xffffffffu, __float_as_int(vs[x]), t);
+          m[kValid + x] = __shfl_sync(0xffffffffu, valid[x], t);
+        }
+        if (lane == 0) {
+          const bool first = done == 0 || kk == 0, last = kk == nn - 1 || done == steps - 1;
+          const int s0 = line.lo + done - kk, cta0 = s0 / line.run;  // s0: where the segment begins on the line
+          const int parts = (s0 + nn - 1) / line.run - cta0 + 1;
+          // a segment that ends and begins in this run is whole: it starts here (its
+          // first step does) and ends before the run's end
+          const bool starts_here = s0 >= line.lo, ends_here = s0 + nn <= line.hi;
+          m[kFlags] = (first ? kFirstStep : 0) | (last ? kLastStep : 0) | (starts_here && ends_here ? kWhole : 0) |
+                      (starts_here ? kTailSlot : 0);
+          m[kCta0] = cta0;
+          m[kParts] = parts;
+          ok = slot_free(2 * done);
+          if (ok) {
+            // entry J % 8 was last read for step J - 8, which every role has left once the
+            // K codes of step J - 2 are converted
+            int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + (done % kMetaRing) * (kMetaInts / 4);
+#pragma unroll
+            for (int i = 0; i < kMetaInts / 4; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+            mbar_arrive(bar.meta(done % kMetaRing));
+          }
+          const int hk = (sg / geo.RT) % p.c.Hk;
+          const uint32_t bytes = (pg[0] >= 0 ? L::kCodes / 2 : 0) + (pg[1] >= 0 ? L::kCodes / 2 : 0);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int seq = 2 * done + kv, slot = seq % kStages;
+            if (kv == 1 && ok) ok = slot_free(seq);
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar.stage_full(slot), bytes);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (pg[x] >= 0)
+                bulk_load(smem_u32(smem + L::kStage + slot * L::kCodes + x * (L::kCodes / 2)),
+                          (kv ? p.c.v8 : p.c.k8) + (static_cast<size_t>(pg[x]) * p.c.Hk + hk) * (kPage * D), L::kCodes / 2,
+                          bar.stage_full(slot));
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (avail > 0) {
+        seg = __shfl_sync(0xffffffffu, my_seg, avail - 1);
+        k = __shfl_sync(0xffffffffu, my_k, avail - 1) + 1;
+      } else {
+        seg += 32;
+        k = 0;
+      }
+    }
+    if (lane == 0) {
+      if (ok && slot_free(2 * done)) {
+        (reinterpret_cast<int*>(smem + L::kMeta) + (done % kMetaRing) * kMetaInts)[kFlags] = kEnd;
+        mbar_arrive(bar.meta(done % kMetaRing));
+      } else {
+        // copies in flight land before the CTA's shared memory is given up
+        for (int seq = max(0, 2 * done - kStages); seq < 2 * done; ++seq)
+          mbar_wait_for(bar.stage_full(seq % kStages), (seq / kStages) & 1, nullptr, 1000000ull);
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ S issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16(128, 128);
+      const uint64_t dq = sdesc_sw128(sQ, 16, 1024), dk = sdesc_sw128(sK, 16, 1024);
+      int pieces = 0;
+      for (int J = 0;; ++J) {
+        int m[kMetaInts];
+        if (!step(J, m) || (m[kFlags] & kEnd)) break;
+        const int g = J & 1;
+        // Q of the piece; the products of step J - 2, which read this region; K
+        if ((m[kFlags] & kFirstStep) && !cache_wait(bar.q_full(), pieces++ & 1, p.status)) break;
+        if (J >= 2 && !cache_wait(bar.pv_done(g), ((J >> 1) - 1) & 1, p.status)) break;
+        if (!cache_wait(bar.k_ready(g), (J >> 1) & 1, p.status)) break;
+        tc_fence_after();
+        const uint64_t kd = dk + static_cast<uint64_t>((g * L::kTile) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+          mma_ss(tmem + 128 * g, dq + off, kd + off, idesc, kk > 0);
+        }
+        mma_commit(bar.s_full(g));
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ P V issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16(128, D);
+      const uint64_t dv = sdesc_sw128(sV, 16, 1024);
+      int pieces = 0;
+      for (int J = 0;; ++J) {
+        int m[kMetaInts];
+        if (!step(J, m) || (m[kFlags] & kEnd)) break;
+        const int g = J & 1;
+        const bool first = m[kFlags] & kFirstStep;
+        if (!cache_wait(bar.v_ready(g), (J >> 1) & 1, p.status)) break;
+        // the piece's first products overwrite the accumulators of the piece before
+        if (first && pieces > 0 && !cache_wait(bar.o_free(), (pieces - 1) & 1, p.status)) break;
+        pieces += first;
+        if (!cache_wait(bar.p_full(g), (J >> 1) & 1, p.status)) break;
+        tc_fence_after();
+        const uint64_t vd = dv + static_cast<uint64_t>((g * L::kTile) >> 4);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem + col_o(w), tmem + 128 * g + 64 * w + 8 * kk,
+                   vd + static_cast<uint64_t>((w * D * 128 + kk * 32) >> 4), idesc, !first || kk > 0);
+        mma_commit(bar.pv_done(g));
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ conversion
+    const int ct = tid - 12 * 32;
+    bool ok = true;
+    for (int J = 0; ok; ++J) {
+      int m[kMetaInts];
+      ok = __all_sync(0xffffffffu, step(J, m));
+      if (!ok || (m[kFlags] & kEnd)) break;
+      const int g = J & 1;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int seq = 2 * J + kv, slot = seq % kStages;
+        // the operand slot is free once the products of step J - 2 have read it
+        const uint32_t freed = kv ? bar.pv_done(g) : bar.s_full(g);
+        ok = cache_wait(bar.stage_full(slot), (seq / kStages) & 1, p.status) &&
+             (J < 2 || cache_wait(freed, ((J >> 1) - 1) & 1, p.status));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* codes = smem + L::kStage + slot * L::kCodes;
+        if (kv == 0) {
+          // K: 16 codes of a key become two units of its row of fp16
+          const uint32_t tile = sK + g * L::kTile;
+          constexpr int kPer = D / 16;  // pieces of 16 codes of a key
+#pragma unroll 4
+          for (int i = ct; i < 128 * kPer; i += 128) {
+            const int row = i / kPer, pc = i % kPer;
+            if ((row < 64 ? m[kValid] : m[kValid + 1]) == 0) continue;
+            put_units(tile + (pc >> 2) * 16384, row, 2 * (pc & 3), *reinterpret_cast<const uint4*>(codes + i * 16),
+                      pc & 4);
+          }
+        } else {
+          // V: 16 keys of a column; codes behind the sequence's end become 0
+          const uint32_t tile = sV + g * L::kTile;
+#pragma unroll 4
+          for (int i = ct; i < 2 * D * 4; i += 128) {
+            const int x = i / (D * 4), row = (i >> 2) % D, pc = i & 3;
+            const int left = (x == 0 ? m[kValid] : m[kValid + 1]) - 16 * pc;
+            uint4 w = left > 0 ? *reinterpret_cast<const uint4*>(codes + i * 16) : make_uint4(0u, 0u, 0u, 0u);
+            if (left < 16) {
+              auto keep = [&](int u) {
+                const int nb = min(max(left - 4 * u, 0), 4);
+                return nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
+              };
+              w.x &= keep(0), w.y &= keep(1), w.z &= keep(2), w.w &= keep(3);
+            }
+            put_units(tile + x * D * 128, row, 2 * pc, w, false);
+          }
+        }
+        fence_proxy_async_smem();  // the operands are read by the tensor cores
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv ? bar.v_ready(g) : bar.k_ready(g));
+          mbar_arrive(bar.stage_empty(slot));
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int w = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float* red = reinterpret_cast<float*>(smem + L::kQ);  // [w][m, mv, l][128], between pieces
+    bool ok = true;
+    int syncs = 0;
+    auto sync_softmax = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.softmax());
+      ok = __all_sync(0xffffffffu, cache_wait(bar.softmax(), syncs & 1, p.status));
+      ++syncs;
+      return ok;
+    };
+    float m_ = -INFINITY, mv = -INFINITY, l = 0.f, crow = 0.f;
+    int lim = 0, pos = 0, b = 0, hk = 0, rt = 0, rows = 0, tok = 0, h = 0;
+    size_t mrow = 0;
+    bool live = false, warp_live = false;
+    for (int J = 0; ok; ++J) {
+      int mt[kMetaInts];
+      ok = __all_sync(0xffffffffu, step(J, mt));
+      if (!ok || (mt[kFlags] & kEnd)) break;
+      const int g = J & 1;
+      const bool first = mt[kFlags] & kFirstStep;
+      if (first) {
+        // this thread's row, and Q: columns [w D/2, w D/2 + D/2) of it
+        const int seg = mt[kSeg], bh = seg / geo.RT;
+        rt = seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+        const RowTile r = row_tile(p, geo, b, rt, tid == 0);
+        rows = geo.G * r.live;
+        const int rr = rt * kRows + row;
+        live = rr < rows;
+        warp_live = __any_sync(0xffffffffu, live);
+        tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+        pos = r.shift + tok;
+        lim = live && p.mask.causal ? min(r.len, pos + 1) : r.len;
+        if constexpr (kVec)
+          mrow = (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) * static_cast<size_t>(p.max_pages * kPage);
+        uint4 x[D / 16];
+        const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + w * (D / 2);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          x[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t mk = 0x7fff7fffu;
+          const uint32_t a = __vmaxu2(__vmaxu2(x[i].x & mk, x[i].y & mk), __vmaxu2(x[i].z & mk, x[i].w & mk));
+          top = max(top, max(a & 0xffffu, a >> 16));
+        }
+        // the last S of the piece before has been read: Q's place is free
+        reinterpret_cast<uint32_t*>(red)[w * kRows + row] = top;
+        if (!sync_softmax()) break;
+        top = max(top, reinterpret_cast<uint32_t*>(red)[(w ^ 1) * kRows + row]);
+        if (!sync_softmax()) break;
+        const bool bad = top >= 0x7f80u;
+        const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+        const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
+        crow = p.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            y[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
+          const int unit = w * (D / 16) + i;  // 16-byte unit of the row
+          st_shared_v4(sQ + (unit >> 3) * 16384 + sw128_offset(row, unit & 7), y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.q_full());
+        m_ = mv = -INFINITY;
+        l = 0.f;
+      }
+
+      const int j0 = w == 0 ? mt[kJ0] : mt[kJ0 + 1];
+      // a score is S times c; c > 0 keeps masked scores at -inf
+      const float c = fmaxf(crow * __int_as_float(w == 0 ? mt[kKs] : mt[kKs + 1]), 1.17549435e-38f);
+      const float lvs = __log2f(__int_as_float(w == 0 ? mt[kVs] : mt[kVs + 1]));
+      const bool tail = __any_sync(0xffffffffu, j0 < 0 || j0 + kPage > lim);
+      const bool cut = (mt[kCut] >> w) & 1;
+      uint64_t hid = 0;  // keys this row does not see
+      if (warp_live && (tail || cut)) {
+        const int n = j0 < 0 ? 0 : min(max(lim - j0, 0), kPage);
+        hid = n == kPage ? 0ull : ~0ull << n;
+        if constexpr (kVec) {
+          if (cut && j0 >= 0) {
+            if (p.mask.lts) hid |= hidden64(p.mask.lts + mrow + j0, p.mask.lte + mrow + j0, pos);
+            if (p.mask.uts) hid |= hidden64(p.mask.uts + mrow + j0, p.mask.ute + mrow + j0, pos);
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J >> 1) & 1, p.status));
+      if (!ok) break;
+      if (warp_live) {
+        tc_fence_after();
+        uint32_t sv[64];
+        const uint32_t s_addr = tmem + lane_base + 128 * g + 64 * w;
+        tmem_ld64(s_addr, s_addr + 32, sv);
+        if (tail || cut) {
+          const uint32_t hlo = static_cast<uint32_t>(hid), hhi = static_cast<uint32_t>(hid >> 32);
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : sv[j];
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 64; j += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = fmax3(mx[i], __uint_as_float(sv[j + 2 * i]), __uint_as_float(sv[j + 2 * i + 1]));
+        const float pm = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
+        const float m_new = fmaxf(m_, pm);
+        l *= ex2_diff(m_, m_new);
+        m_ = m_new;
+        const float mv_new = fmaxf(mv, pm + lvs);
+        const bool rescale = mv_new > mv + kLag;
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = ex2(mv - mv_new);
+          mv = mv_new;
+        }
+        const float mu = m_ == -INFINITY ? 0.f : m_, mvu = mv == -INFINITY ? 0.f : mv;
+        const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
+        const uint64_t c2 = f2_make(c, c), nm2 = f2_make(-mu, -mu), f2 = f2_make(f, f);
+        uint64_t l2 = f2_make(0.f, 0.f);
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float x0, x1, p0, p1;
+          f2_split(f2_fma(f2_make(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, nm2), x0, x1);
+          const uint64_t pp = f2_make(ex2(x0), ex2(x1));
+          l2 = f2_add(l2, pp);
+          f2_split(f2_mul(pp, f2), p0, p1);
+          pk[i] = pack_f16x2(p0, p1);
+        }
+        float l0, l1;
+        f2_split(l2, l0, l1);
+        l += l0 + l1;
+        tmem_st32p(tmem + lane_base + 128 * g + 64 * w, pk);
+        if (!first && __any_sync(0xffffffffu, rescale)) {
+          // O_w is rescaled once the products of step J - 1 have completed
+          ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g ^ 1), ((J - 1) >> 1) & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) tmem_scale32(tmem + lane_base + col_o(w) + 32 * ch, alpha);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.p_full(g));
+      if (!(mt[kFlags] & kLastStep)) continue;
+
+      // ---- the piece's end: the two halves' states are merged
+      ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g), (J >> 1) & 1, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      red[w * 3 * kRows + row] = m_;
+      red[(w * 3 + 1) * kRows + row] = mv;
+      red[(w * 3 + 2) * kRows + row] = l;
+      if (!sync_softmax()) break;
+      const float* other = red + (w ^ 1) * 3 * kRows + row;
+      const float m = fmaxf(m_, other[0]), mva = fmaxf(mv, other[kRows]);
+      // the sum in the same order in both warpgroups, so that they agree to the bit
+      const float la = l * ex2_diff(m_, m), lb = other[2 * kRows] * ex2_diff(other[0], m);
+      const float lsum = w == 0 ? la + lb : lb + la;
+      const float fs = ex2_diff(mv, mva), fo = ex2_diff(other[kRows], mva);
+      const bool whole = mt[kFlags] & kWhole;
+      const float out = whole ? out_factor(m, mva, lsum, kPShift) : 1.f;
+      const float f0 = (w == 0 ? fs : fo) * out, f1 = (w == 0 ? fo : fs) * out;
+      const int slot = (mt[kFlags] & kTailSlot) ? 1 : 0;
+      float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot) * part_floats(D);
+      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + w * (D / 2);
+      if (warp_live) {
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t va[32], vb[32];
+          const uint32_t col = w * (D / 2) + 32 * ch;
+          tmem_ld32(tmem + lane_base + col_o(0) + col, va);
+          tmem_ld32(tmem + lane_base + col_o(1) + col, vb);
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(va[i]) * f0 + __uint_as_float(vb[i]) * f1;
+          if (whole) {
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(o + 32 * ch + 8 * i) =
+                    make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                               pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(part)[(col / 4 + i) * kRows + row] =
+                  make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.o_free());
+      if (whole) {
+        if (live && w == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(m, lsum);
+      } else {
+        if (w == 0) {
+          float* x = part + kRows * D + row;
+          x[0] = m, x[kRows] = mva, x[2 * kRows] = lsum;
+        }
+        __threadfence();
+        if (!sync_softmax()) break;  // all of the partial result is written
+        if (tid == 0) {
+          const bool all = atomicAdd(&p.arrived[mt[kSeg]], 1) == mt[kParts] - 1;
+          if (all) p.arrived[mt[kSeg]] = 0;  // ready for the next call
+          words[kLineWords] = all;
+          __threadfence();
+        }
+        if (!sync_softmax()) break;
+        if (words[kLineWords] && warp_live) {
+          // every part, in the order of the keys: this thread's row and half of its columns
+          __threadfence();
+          auto part_at = [&](int i) {
+            return p.partial + (static_cast<size_t>(mt[kCta0] + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
+          };
+          float jm = -INFINITY, jmv = -INFINITY, jl = 0.f;
+          for (int i = 0; i < mt[kParts]; ++i) {
+            const float* x = part_at(i) + kRows * D + row;
+            jm = fmaxf(jm, __ldcg(x));
+            jmv = fmaxf(jmv, __ldcg(x + kRows));
+          }
+          for (int i = 0; i < mt[kParts]; ++i) {
+            const float* x = part_at(i) + kRows * D + row;
+            jl += __ldcg(x + 2 * kRows) * ex2_diff(__ldcg(x), jm);
+          }
+          const float fin = out_factor(jm, jmv, jl, kPShift);
+#pragma unroll
+          for (int ch = 0; ch < D / 64; ++ch) {
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = 0.f;
+            for (int i = 0; i < mt[kParts]; ++i) {
+              const float* x = part_at(i);
+              const float fx = ex2_diff(__ldcg(x + kRows * D + kRows + row), jmv);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(x) + ((w * (D / 2) + 32 * ch) / 4 + j) * kRows + row);
+                y[4 * j] += v.x * fx;
+                y[4 * j + 1] += v.y * fx;
+                y[4 * j + 2] += v.z * fx;
+                y[4 * j + 3] += v.w * fx;
+              }
+            }
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(o + 32 * ch + 8 * i) = make_uint4(
+                    pack_bf16x2(y[8 * i] * fin, y[8 * i + 1] * fin), pack_bf16x2(y[8 * i + 2] * fin, y[8 * i + 3] * fin),
+                    pack_bf16x2(y[8 * i + 4] * fin, y[8 * i + 5] * fin), pack_bf16x2(y[8 * i + 6] * fin, y[8 * i + 7] * fin));
+            }
+          }
+          if (live && w == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(jm, jl);
+        }
+      }
+      if (!sync_softmax()) break;  // red (Q's place) and the word have been read
+    }
+
+    // segments without a visible page: O = 0, LSE = -inf
+    for (int sg = blockIdx.x; ok && line.any_empty && sg < nseg; sg += gridDim.x) {
+      if (steps_of<kVec>(p, geo, sg) != 0) continue;
+      const int rt2 = sg % geo.RT, bh = sg / geo.RT, b2 = bh / p.c.Hk, hk2 = bh - b2 * p.c.Hk;
+      const RowTile r = row_tile(p, geo, b2, rt2, tid == 0);
+      const int row_hi = min(geo.G * r.live, (rt2 + 1) * kRows);
+      for (int rr = rt2 * kRows + warp; rr < row_hi; rr += 8) {
+        const int t = rr / geo.G, hh = hk2 * geo.G + rr - t * geo.G;
+        uint16_t* o = p.o + b2 * p.os[0] + hh * p.os[1] + t * p.os[2];
+        for (int i = lane; i < D / 2; i += 32) *reinterpret_cast<uint32_t*>(o + 2 * i) = 0u;
+        if (lane == 0) p.lse[(static_cast<size_t>(b2) * p.H + hh) * p.N + t] = -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool kVec>
+cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> done[4];  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev > 255) return cudaErrorInvalidDevice;
+  if (!(done[dev >> 6].load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(cache_fwd_rows_kernel<D, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    done[dev >> 6].fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  if (kVec) {
+    e = launch_cache_classify(p, geo, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
+  cache_fwd_rows_kernel<D, kVec><<<grid, kThreads, Layout<D>::kBytes, s>>>(p, geo);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_fwd_rows_part_floats(int d) { return part_floats(d); }
+
+cudaError_t launch_cache_fwd_rows(int d, const CacheFwdParams& p, const Geometry& geo, int num_sms,
+                                  cudaStream_t s) {
+  const bool vec = p.mask.lts != nullptr || p.mask.uts != nullptr;
+  if (d == 64) return vec ? launch_t<64, true>(p, geo, num_sms, s) : launch_t<64, false>(p, geo, num_sms, s);
+  return vec ? launch_t<128, true>(p, geo, num_sms, s) : launch_t<128, false>(p, geo, num_sms, s);
+}
+
+}  // namespace fm
