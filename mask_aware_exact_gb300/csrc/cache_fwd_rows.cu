@@ -24,7 +24,7 @@
 //   8      S issuer, 9 P V issuer (one thread each).
 //   10     walks the run, looks pages up, issues the copies, publishes a step's
 //          description to all roles (ring of kMetaRing).
-//   12-15  conversion.
+//   12, 13 conversion of K; 14, 15 of V.
 // TMEM: S regions [0,128) [128,256), O_0 [256, 256+d), O_1 [384, 384+d); P over S.
 //
 // What bounds it: shared memory. A step with d = 128 writes 32 KB of codes and 64 KB of
@@ -72,10 +72,10 @@ struct Bars {
   uint32_t base;
   __device__ uint32_t at(int i) const { return base + 8 * i; }
   __device__ uint32_t stage_full(int s) const { return at(s); }                // bytes
-  __device__ uint32_t stage_empty(int s) const { return at(kStages + s); }     // 4 conversion warps
+  __device__ uint32_t stage_empty(int s) const { return at(kStages + s); }     // 2 conversion warps
   __device__ uint32_t meta(int s) const { return at(2 * kStages + s); }        // 1
-  __device__ uint32_t k_ready(int s) const { return at(2 * kStages + kMetaRing + s); }       // 4
-  __device__ uint32_t v_ready(int s) const { return at(2 * kStages + kMetaRing + 2 + s); }   // 4
+  __device__ uint32_t k_ready(int s) const { return at(2 * kStages + kMetaRing + s); }       // 2
+  __device__ uint32_t v_ready(int s) const { return at(2 * kStages + kMetaRing + 2 + s); }   // 2
   __device__ uint32_t s_full(int g) const { return at(2 * kStages + kMetaRing + 4 + g); }    // commit
   __device__ uint32_t p_full(int g) const { return at(2 * kStages + kMetaRing + 6 + g); }    // 8
   __device__ uint32_t pv_done(int g) const { return at(2 * kStages + kMetaRing + 8 + g); }   // commit
@@ -119,22 +119,6 @@ __device__ __forceinline__ void tmem_scale32(uint32_t taddr, float f) {
   tmem_st32(taddr, v);
 }
 
-// 16 codes -> 16 fp16 as two 16-byte units of a swizzled row; `odd` stores the second
-// one first, which keeps the eight lanes of a store on different banks.
-__device__ __forceinline__ void put_units(uint32_t tile, int row, int unit, const uint4& w, bool odd) {
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) codes_to_f16(word(w, i), h[2 * i], h[2 * i + 1]);
-  const uint32_t a0 = tile + sw128_offset(row, unit), a1 = tile + sw128_offset(row, unit + 1);
-  if (odd) {
-    st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-    st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-  } else {
-    st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-    st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-  }
-}
-
 // Floats of one partial result: O as float4 [D / 4][128 rows], then m, mv, l [128].
 constexpr __host__ __device__ int part_floats(int D) { return kRows * D + 3 * kRows; }
 
@@ -159,12 +143,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
     tmem_relinquish();
   }
   if (tid < L::kNumBars) {
-    // arrivals: stage_full 1, stage_empty 4, meta 1, k_ready and v_ready 4, s_full 1,
+    // arrivals: stage_full 1, stage_empty 2, meta 1, k_ready and v_ready 2, s_full 1,
     // p_full 8, pv_done 1, q_full, o_free and softmax 8
     const int i = tid - 2 * kStages - kMetaRing;
     int n = 1;
-    if (tid >= kStages && tid < 2 * kStages) n = 4;
-    if (i >= 0 && i < 4) n = 4;
+    if (tid >= kStages && tid < 2 * kStages) n = 2;
+    if (i >= 0 && i < 4) n = 2;
     if (i == 6 || i == 7 || i >= 10) n = 8;
     mbar_init(bar.at(tid), n);
     fence_barrier_init();
@@ -175,6 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // Waits for the description of step J; its flags, kEnd when the wait gave up.
+  auto step_flags = [&](int J) -> int {
+    if (!cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status)) return kEnd;
+    return meta_at[(J % kMetaRing) * kMetaInts + kFlags];
+  };
   // Waits for the description of step J; false when the wait gave up.
   auto step = [&](int J, int (&m)[kMetaInts]) -> bool {
     if (!cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status)) return false;
@@ -250,8 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           m[kParts] = parts;
           ok = slot_free(2 * done);
           if (ok) {
-            // entry J % 8 was last read for step J - 8, which every role has left once the
-            // K codes of step J - 2 are converted
+            // entry J % 8 was last read for step J - 8, which every role has left: the K codes
+            // of step J - 2 are converted, so S of step J - 4 and P V of step J - 6 are done,
+            // and V of step J - 6 with them
             int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + (done % kMetaRing) * (kMetaInts / 4);
 #pragma unroll
             for (int i = 0; i < kMetaInts / 4; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
@@ -300,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       const uint64_t dq = sdesc_sw128(sQ, 16, 1024), dk = sdesc_sw128(sK, 16, 1024);
       int pieces = 0;
       for (int J = 0;; ++J) {
-        int m[kMetaInts];
-        if (!step(J, m) || (m[kFlags] & kEnd)) break;
+        const int flags = step_flags(J);
+        if (flags & kEnd) break;
         const int g = J & 1;
         // Q of the piece; the products of step J - 2, which read this region; K
-        if ((m[kFlags] & kFirstStep) && !cache_wait(bar.q_full(), pieces++ & 1, p.status)) break;
+        if ((flags & kFirstStep) && !cache_wait(bar.q_full(), pieces++ & 1, p.status)) break;
         if (J >= 2 && !cache_wait(bar.pv_done(g), ((J >> 1) - 1) & 1, p.status)) break;
         if (!cache_wait(bar.k_ready(g), (J >> 1) & 1, p.status)) break;
         tc_fence_after();
@@ -324,10 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       const uint64_t dv = sdesc_sw128(sV, 16, 1024);
       int pieces = 0;
       for (int J = 0;; ++J) {
-        int m[kMetaInts];
-        if (!step(J, m) || (m[kFlags] & kEnd)) break;
+        const int flags = step_flags(J);
+        if (flags & kEnd) break;
         const int g = J & 1;
-        const bool first = m[kFlags] & kFirstStep;
+        const bool first = flags & kFirstStep;
         if (!cache_wait(bar.v_ready(g), (J >> 1) & 1, p.status)) break;
         // the piece's first products overwrite the accumulators of the piece before
         if (first && pieces > 0 && !cache_wait(bar.o_free(), (pieces - 1) & 1, p.status)) break;
@@ -346,58 +336,62 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ conversion
-    const int ct = tid - 12 * 32;
+    // warps 12, 13: K; warps 14, 15: V. Both tiles are blocks of rows of 64 codes: K two
+    // halves (d = 128) of 128 keys, V the columns of two pages. A thread's piece of 16
+    // codes lies at the same place of every 16th row, so its swizzled units do too. The
+    // loop stays short on purpose: with it unrolled the roles' code overflowed the
+    // instruction cache, which cost more than anything else here.
+    const int kv = (warp - 12) >> 1, ct = tid & 63, pc = ct & 3, row0 = ct >> 2;
+    const int blocks = kv ? 2 : D / 64, block_rows = kv ? D : 128, row_bytes = kv ? 64 : D;
+    const uint32_t u0 = ((2 * pc) ^ (row0 & 7)) << 4, u1 = ((2 * pc + 1) ^ (row0 & 7)) << 4;
     bool ok = true;
     for (int J = 0; ok; ++J) {
-      int m[kMetaInts];
-      ok = __all_sync(0xffffffffu, step(J, m));
-      if (!ok || (m[kFlags] & kEnd)) break;
-      const int g = J & 1;
+      ok = __all_sync(0xffffffffu, cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status));
+      if (!ok) break;
+      const int* m = meta_at + (J % kMetaRing) * kMetaInts;
+      if (m[kFlags] & kEnd) break;
+      const int valid[2] = {m[kValid], m[kValid + 1]};
+      const int g = J & 1, slot = (2 * J + kv) % kStages;
+      // the operand slot is free once the products of step J - 2 have read it
+      const uint32_t freed = kv ? bar.pv_done(g) : bar.s_full(g);
+      ok = cache_wait(bar.stage_full(slot), ((2 * J + kv) / kStages) & 1, p.status) &&
+           (J < 2 || cache_wait(freed, ((J >> 1) - 1) & 1, p.status));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint8_t* codes = smem + L::kStage + slot * L::kCodes + row0 * row_bytes + 16 * pc;
+      uint32_t dst = (kv ? sV : sK) + g * L::kTile + row0 * 128;
+      for (int x = 0; x < blocks; ++x) {
+        // V: codes behind the sequence's end (or of an absent page) become 0
+        const int left = kv == 0 ? 16 : (x == 0 ? valid[0] : valid[1]) - 16 * pc;
+        uint32_t keep[4];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int seq = 2 * J + kv, slot = seq % kStages;
-        // the operand slot is free once the products of step J - 2 have read it
-        const uint32_t freed = kv ? bar.pv_done(g) : bar.s_full(g);
-        ok = cache_wait(bar.stage_full(slot), (seq / kStages) & 1, p.status) &&
-             (J < 2 || cache_wait(freed, ((J >> 1) - 1) & 1, p.status));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* codes = smem + L::kStage + slot * L::kCodes;
-        if (kv == 0) {
-          // K: 16 codes of a key become two units of its row of fp16
-          const uint32_t tile = sK + g * L::kTile;
-          constexpr int kPer = D / 16;  // pieces of 16 codes of a key
-#pragma unroll 4
-          for (int i = ct; i < 128 * kPer; i += 128) {
-            const int row = i / kPer, pc = i % kPer;
-            if ((row < 64 ? m[kValid] : m[kValid + 1]) == 0) continue;
-            put_units(tile + (pc >> 2) * 16384, row, 2 * (pc & 3), *reinterpret_cast<const uint4*>(codes + i * 16),
-                      pc & 4);
-          }
-        } else {
-          // V: 16 keys of a column; codes behind the sequence's end become 0
-          const uint32_t tile = sV + g * L::kTile;
-#pragma unroll 4
-          for (int i = ct; i < 2 * D * 4; i += 128) {
-            const int x = i / (D * 4), row = (i >> 2) % D, pc = i & 3;
-            const int left = (x == 0 ? m[kValid] : m[kValid + 1]) - 16 * pc;
-            uint4 w = left > 0 ? *reinterpret_cast<const uint4*>(codes + i * 16) : make_uint4(0u, 0u, 0u, 0u);
-            if (left < 16) {
-              auto keep = [&](int u) {
-                const int nb = min(max(left - 4 * u, 0), 4);
-                return nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
-              };
-              w.x &= keep(0), w.y &= keep(1), w.z &= keep(2), w.w &= keep(3);
-            }
-            put_units(tile + x * D * 128, row, 2 * pc, w, false);
+        for (int u = 0; u < 4; ++u) {
+          const int nb = min(max(left - 4 * u, 0), 4);
+          keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
+        }
+        const uint8_t* src = codes + x * (kv ? kPage * D : 64);
+#pragma unroll 1
+        for (int row = 0; row < block_rows; row += 64) {
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (row + 16 * i) * row_bytes);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) codes_to_f16(word(w[i], u) & keep[u], h[2 * u], h[2 * u + 1]);
+            const uint32_t at = dst + (row + 16 * i) * 128;
+            st_shared_v4(at + u0, h[0], h[1], h[2], h[3]);
+            st_shared_v4(at + u1, h[4], h[5], h[6], h[7]);
           }
         }
-        fence_proxy_async_smem();  // the operands are read by the tensor cores
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(kv ? bar.v_ready(g) : bar.k_ready(g));
-          mbar_arrive(bar.stage_empty(slot));
-        }
+        dst += block_rows * 128;
+      }
+      fence_proxy_async_smem();  // the operands are read by the tensor cores
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(kv ? bar.v_ready(g) : bar.k_ready(g));
+        mbar_arrive(bar.stage_empty(slot));
       }
     }
   } else if (warp < 8) {
