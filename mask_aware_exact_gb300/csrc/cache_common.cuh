@@ -214,9 +214,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 // Bounded wait: gives up after the library's limit, or when another wait has (a
-// page error alone does not end waits).
-__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_t* status) {
-  if (mbar_test_wait(bar, parity)) return true;
+// page error alone does not end waits). Only the first test is inline: the roles'
+// loops have to stay small for the instruction cache.
+static __device__ __noinline__ bool cache_wait_slow(uint32_t bar, uint32_t parity, int32_t* status) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if ((*reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout) != 0) return false;
@@ -226,6 +226,9 @@ __device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_
     }
   }
   return true;
+}
+__device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_t* status) {
+  return mbar_test_wait(bar, parity) || cache_wait_slow(bar, parity, status);
 }
 // The same for a counter in shared memory that only grows.
 __device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* status) {

@@ -47,8 +47,10 @@ constexpr int kMinRun = 4;  // steps
 constexpr float kPShift = 7.f;
 constexpr float kLag = 8.f;  // mv may lag the row's largest product by this much (log2)
 
-enum MetaWord { kSeg, kFlags, kJ0, kKs = kJ0 + 2, kVs = kKs + 2, kValid = kVs + 2, kCut = kValid + 2, kCta0, kParts };
-enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16 };
+// A step's description, int[16]: the step, then four words for each of its two pages
+// (first key, or -1 for none; K scale; log2 of the V scale; keys before the end).
+enum MetaWord { kFlags, kSeg, kCta0, kParts, kPageWords, kJ0 = 0, kKs, kLvs, kValid };
+enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16, kCut = 32 };  // kCut << page
 
 template <int D>
 struct Layout {
@@ -164,18 +166,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
     if (!cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status)) return kEnd;
     return meta_at[(J % kMetaRing) * kMetaInts + kFlags];
   };
-  // Waits for the description of step J; false when the wait gave up.
-  auto step = [&](int J, int (&m)[kMetaInts]) -> bool {
-    if (!cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status)) return false;
-    const int4* at = reinterpret_cast<const int4*>(meta_at + (J % kMetaRing) * kMetaInts);
-#pragma unroll
-    for (int i = 0; i < kMetaInts / 4; ++i) {
-      const int4 v = at[i];
-      m[4 * i] = v.x, m[4 * i + 1] = v.y, m[4 * i + 2] = v.z, m[4 * i + 3] = v.w;
-    }
-    return true;
-  };
-
   if (warp == 10) {
     // ------------------------------------------------------------ run, pages, copies
     int seg = line.seg, k = line.first, done = 0;
@@ -189,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       const int avail = next_units(
           seg, k, nseg, min(32, steps - done), [&](int s) { return steps_of<kVec>(p, geo, s); }, my_seg, my_k, my_n);
       int page[2] = {-1, -1}, j0[2] = {-1, -1}, valid[2] = {0, 0}, cut[2] = {0, 0};
-      float ks[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};
+      float ks[2] = {0.f, 0.f}, lvs[2] = {0.f, 0.f};
       if (lane < avail) {
         const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
         const int pages = pages_of<kVec>(p, geo, my_seg);
@@ -208,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           j0[x] = logical * kPage;
           valid[x] = min(r.len - j0[x], kPage);
           ks[x] = p.c.kscale[ph];
-          vs[x] = p.c.vscale[ph];
+          lvs[x] = __log2f(p.c.vscale[ph]);
         }
       }
       for (int t = 0; ok && t < avail; ++t, ++done) {
@@ -217,14 +207,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
         int m[kMetaInts] = {};
         int pg[2];
         m[kSeg] = sg;
-        m[kCut] = __shfl_sync(0xffffffffu, cut[0] | cut[1] << 1, t);
+        const int cuts = __shfl_sync(0xffffffffu, cut[0] | cut[1] << 1, t);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           pg[x] = __shfl_sync(0xffffffffu, page[x], t);
-          m[kJ0 + x] = __shfl_sync(0xffffffffu, j0[x], t);
-          m[kKs + x] = __shfl_sync(0xffffffffu, __float_as_int(ks[x]), t);
-          m[kVs + x] = __shfl_sync(0xffffffffu, __float_as_int(vs[x]), t);
-          m[kValid + x] = __shfl_sync(0xffffffffu, valid[x], t);
+          int* w = m + kPageWords + 4 * x;
+          w[kJ0] = __shfl_sync(0xffffffffu, j0[x], t);
+          w[kKs] = __shfl_sync(0xffffffffu, __float_as_int(ks[x]), t);
+          w[kLvs] = __shfl_sync(0xffffffffu, __float_as_int(lvs[x]), t);
+          w[kValid] = __shfl_sync(0xffffffffu, valid[x], t);
         }
         if (lane == 0) {
           const bool first = done == 0 || kk == 0, last = kk == nn - 1 || done == steps - 1;
@@ -234,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           // first step does) and ends before the run's end
           const bool starts_here = s0 >= line.lo, ends_here = s0 + nn <= line.hi;
           m[kFlags] = (first ? kFirstStep : 0) | (last ? kLastStep : 0) | (starts_here && ends_here ? kWhole : 0) |
-                      (starts_here ? kTailSlot : 0);
+                      (starts_here ? kTailSlot : 0) | kCut * cuts;
           m[kCta0] = cta0;
           m[kParts] = parts;
           ok = slot_free(2 * done);
@@ -350,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       if (!ok) break;
       const int* m = meta_at + (J % kMetaRing) * kMetaInts;
       if (m[kFlags] & kEnd) break;
-      const int valid[2] = {m[kValid], m[kValid + 1]};
+      const int valid[2] = {m[kPageWords + kValid], m[kPageWords + 4 + kValid]};
       const int g = J & 1, slot = (2 * J + kv) % kStages;
       // the operand slot is free once the products of step J - 2 have read it
       const uint32_t freed = kv ? bar.pv_done(g) : bar.s_full(g);
@@ -409,147 +400,150 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       ++syncs;
       return ok;
     };
-    float m_ = -INFINITY, mv = -INFINITY, l = 0.f, crow = 0.f;
-    int lim = 0, pos = 0, b = 0, hk = 0, rt = 0, rows = 0, tok = 0, h = 0;
-    size_t mrow = 0;
-    bool live = false, warp_live = false;
-    for (int J = 0; ok; ++J) {
-      int mt[kMetaInts];
-      ok = __all_sync(0xffffffffu, step(J, mt));
-      if (!ok || (mt[kFlags] & kEnd)) break;
-      const int g = J & 1;
-      const bool first = mt[kFlags] & kFirstStep;
-      if (first) {
-        // this thread's row, and Q: columns [w D/2, w D/2 + D/2) of it
-        const int seg = mt[kSeg], bh = seg / geo.RT;
-        rt = seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-        const RowTile r = row_tile(p, geo, b, rt, tid == 0);
-        rows = geo.G * r.live;
-        const int rr = rt * kRows + row;
-        live = rr < rows;
-        warp_live = __any_sync(0xffffffffu, live);
-        tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
-        pos = r.shift + tok;
-        lim = live && p.mask.causal ? min(r.len, pos + 1) : r.len;
-        if constexpr (kVec)
-          mrow = (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) * static_cast<size_t>(p.max_pages * kPage);
-        uint4 x[D / 16];
-        const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + w * (D / 2);
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          x[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t mk = 0x7fff7fffu;
-          const uint32_t a = __vmaxu2(__vmaxu2(x[i].x & mk, x[i].y & mk), __vmaxu2(x[i].z & mk, x[i].w & mk));
-          top = max(top, max(a & 0xffffu, a >> 16));
-        }
-        // the last S of the piece before has been read: Q's place is free
-        reinterpret_cast<uint32_t*>(red)[w * kRows + row] = top;
-        if (!sync_softmax()) break;
-        top = max(top, reinterpret_cast<uint32_t*>(red)[(w ^ 1) * kRows + row]);
-        if (!sync_softmax()) break;
-        const bool bad = top >= 0x7f80u;
-        const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
-        const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
-        crow = p.scale_log2 * __int_as_float((127 - up) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            y[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
-          const int unit = w * (D / 16) + i;  // 16-byte unit of the row
-          st_shared_v4(sQ + (unit >> 3) * 16384 + sw128_offset(row, unit & 7), y[0], y[1], y[2], y[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.q_full());
-        m_ = mv = -INFINITY;
-        l = 0.f;
-      }
-
-      const int j0 = w == 0 ? mt[kJ0] : mt[kJ0 + 1];
-      // a score is S times c; c > 0 keeps masked scores at -inf
-      const float c = fmaxf(crow * __int_as_float(w == 0 ? mt[kKs] : mt[kKs + 1]), 1.17549435e-38f);
-      const float lvs = __log2f(__int_as_float(w == 0 ? mt[kVs] : mt[kVs + 1]));
-      const bool tail = __any_sync(0xffffffffu, j0 < 0 || j0 + kPage > lim);
-      const bool cut = (mt[kCut] >> w) & 1;
-      uint64_t hid = 0;  // keys this row does not see
-      if (warp_live && (tail || cut)) {
-        const int n = j0 < 0 ? 0 : min(max(lim - j0, 0), kPage);
-        hid = n == kPage ? 0ull : ~0ull << n;
-        if constexpr (kVec) {
-          if (cut && j0 >= 0) {
-            if (p.mask.lts) hid |= hidden64(p.mask.lts + mrow + j0, p.mask.lte + mrow + j0, pos);
-            if (p.mask.uts) hid |= hidden64(p.mask.uts + mrow + j0, p.mask.ute + mrow + j0, pos);
-          }
-        }
-      }
-      ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J >> 1) & 1, p.status));
+    for (int J = 0; ok;) {
+      ok = __all_sync(0xffffffffu, cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status));
       if (!ok) break;
-      if (warp_live) {
-        tc_fence_after();
-        uint32_t sv[64];
-        const uint32_t s_addr = tmem + lane_base + 128 * g + 64 * w;
-        tmem_ld64(s_addr, s_addr + 32, sv);
-        if (tail || cut) {
-          const uint32_t hlo = static_cast<uint32_t>(hid), hhi = static_cast<uint32_t>(hid >> 32);
+      const int* head = meta_at + (J % kMetaRing) * kMetaInts;
+      if (head[kFlags] & kEnd) break;
+      const int seg = head[kSeg], cta0 = head[kCta0], parts = head[kParts];
+      const bool whole = head[kFlags] & kWhole;
+      const int slot = head[kFlags] & kTailSlot ? 1 : 0;
+      // this thread's row, and Q: columns [w D/2, w D/2 + D/2) of it
+      const int bh = seg / geo.RT, rt = seg - bh * geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+      const RowTile r = row_tile(p, geo, b, rt, tid == 0);
+      const int rows = geo.G * r.live;
+      const int rr = rt * kRows + row;
+      const bool live = rr < rows;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+      const int pos = r.shift + tok;
+      const int lim = live && p.mask.causal ? min(r.len, pos + 1) : r.len;
+      const int all_lim = __reduce_min_sync(0xffffffffu, lim);  // keys that every row of the warp sees
+      const size_t mrow =
+          kVec ? (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) * static_cast<size_t>(p.max_pages * kPage) : 0;
+      uint4 x[D / 16];
+      const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + w * (D / 2);
+      uint32_t top = 0;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : sv[j];
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 64; j += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mx[i] = fmax3(mx[i], __uint_as_float(sv[j + 2 * i]), __uint_as_float(sv[j + 2 * i + 1]));
-        const float pm = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
-        const float m_new = fmaxf(m_, pm);
-        l *= ex2_diff(m_, m_new);
-        m_ = m_new;
-        const float mv_new = fmaxf(mv, pm + lvs);
-        const bool rescale = mv_new > mv + kLag;
-        float alpha = 1.f;
-        if (rescale) {
-          alpha = ex2(mv - mv_new);
-          mv = mv_new;
-        }
-        const float mu = m_ == -INFINITY ? 0.f : m_, mvu = mv == -INFINITY ? 0.f : mv;
-        const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
-        const uint64_t c2 = f2_make(c, c), nm2 = f2_make(-mu, -mu), f2 = f2_make(f, f);
-        uint64_t l2 = f2_make(0.f, 0.f);
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x0, x1, p0, p1;
-          f2_split(f2_fma(f2_make(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, nm2), x0, x1);
-          const uint64_t pp = f2_make(ex2(x0), ex2(x1));
-          l2 = f2_add(l2, pp);
-          f2_split(f2_mul(pp, f2), p0, p1);
-          pk[i] = pack_f16x2(p0, p1);
-        }
-        float l0, l1;
-        f2_split(l2, l0, l1);
-        l += l0 + l1;
-        tmem_st32p(tmem + lane_base + 128 * g + 64 * w, pk);
-        if (!first && __any_sync(0xffffffffu, rescale)) {
-          // O_w is rescaled once the products of step J - 1 have completed
-          ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g ^ 1), ((J - 1) >> 1) & 1, p.status));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) tmem_scale32(tmem + lane_base + col_o(w) + 32 * ch, alpha);
-        }
-        tmem_st_wait();
+      for (int i = 0; i < D / 16; ++i) {
+        x[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t mk = 0x7fff7fffu;
+        const uint32_t a = __vmaxu2(__vmaxu2(x[i].x & mk, x[i].y & mk), __vmaxu2(x[i].z & mk, x[i].w & mk));
+        top = max(top, max(a & 0xffffu, a >> 16));
       }
-      tc_fence_before();
+      // the last S of the piece before has been read: Q's place is free
+      reinterpret_cast<uint32_t*>(red)[w * kRows + row] = top;
+      if (!sync_softmax()) break;
+      top = max(top, reinterpret_cast<uint32_t*>(red)[(w ^ 1) * kRows + row]);
+      if (!sync_softmax()) break;
+      const bool bad = top >= 0x7f80u;
+      const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+      const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
+      const float crow = p.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          y[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
+        const int unit = w * (D / 16) + i;  // 16-byte unit of the row
+        st_shared_v4(sQ + (unit >> 3) * 16384 + sw128_offset(row, unit & 7), y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.p_full(g));
-      if (!(mt[kFlags] & kLastStep)) continue;
+      if (lane == 0) mbar_arrive(bar.q_full());
+      float m_ = -INFINITY, mv = -INFINITY, l = 0.f;
+
+      // ---- the piece's steps; what is rare is kept out of the loop's straight line
+      int flags;
+      for (bool first = true;; first = false, ++J) {
+        if (!first) {
+          ok = __all_sync(0xffffffffu, cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status));
+          if (!ok) break;
+        }
+        const int g = J & 1;
+        flags = meta_at[(J % kMetaRing) * kMetaInts + kFlags];
+        const int4 pw = *reinterpret_cast<const int4*>(meta_at + (J % kMetaRing) * kMetaInts + kPageWords + 4 * w);
+        const int j0 = pw.x;
+        // a score is S times c; c > 0 keeps masked scores at -inf
+        const float c = fmaxf(crow * __int_as_float(pw.y), 1.17549435e-38f);
+        const float lvs = __int_as_float(pw.z);
+        const bool masked = j0 < 0 || j0 + kPage > all_lim || (flags & (kCut << w));
+        ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J >> 1) & 1, p.status));
+        if (!ok) break;
+        if (warp_live) {
+          tc_fence_after();
+          uint32_t sv[64];
+          const uint32_t s_addr = tmem + lane_base + 128 * g + 64 * w;
+          tmem_ld64(s_addr, s_addr + 32, sv);
+          if (__builtin_expect(masked, 0)) {
+            const int n = j0 < 0 ? 0 : min(max(lim - j0, 0), kPage);
+            uint64_t hid = n == kPage ? 0ull : ~0ull << n;  // keys this row does not see
+            if constexpr (kVec) {
+              if ((flags & (kCut << w)) && j0 >= 0) {
+                if (p.mask.lts) hid |= hidden64(p.mask.lts + mrow + j0, p.mask.lte + mrow + j0, pos);
+                if (p.mask.uts) hid |= hidden64(p.mask.uts + mrow + j0, p.mask.ute + mrow + j0, pos);
+              }
+            }
+            const uint32_t hlo = static_cast<uint32_t>(hid), hhi = static_cast<uint32_t>(hid >> 32);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : sv[j];
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 64; j += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mx[i] = fmax3(mx[i], __uint_as_float(sv[j + 2 * i]), __uint_as_float(sv[j + 2 * i + 1]));
+          const float pm = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
+          const float m_new = fmaxf(m_, pm);
+          l *= ex2_diff(m_, m_new);
+          m_ = m_new;
+          const float mv_new = fmaxf(mv, pm + lvs);
+          const bool rescale = mv_new > mv + kLag;
+          const float mv_old = mv;
+          if (rescale) mv = mv_new;
+          const float mu = m_ == -INFINITY ? 0.f : m_, mvu = mv == -INFINITY ? 0.f : mv;
+          const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
+          const uint64_t c2 = f2_make(c, c), nm2 = f2_make(-mu, -mu), f2 = f2_make(f, f);
+          uint64_t l2 = f2_make(0.f, 0.f);
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x0, x1, p0, p1;
+            f2_split(f2_fma(f2_make(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, nm2), x0, x1);
+            const uint64_t pp = f2_make(ex2(x0), ex2(x1));
+            l2 = f2_add(l2, pp);
+            f2_split(f2_mul(pp, f2), p0, p1);
+            pk[i] = pack_f16x2(p0, p1);
+          }
+          float l0, l1;
+          f2_split(l2, l0, l1);
+          l += l0 + l1;
+          tmem_st32p(tmem + lane_base + 128 * g + 64 * w, pk);
+          if (__builtin_expect(!first && __any_sync(0xffffffffu, rescale), 0)) {
+            // O_w is rescaled once the products of step J - 1 have completed
+            ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g ^ 1), ((J - 1) >> 1) & 1, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            const float alpha = rescale ? ex2(mv_old - mv) : 1.f;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) tmem_scale32(tmem + lane_base + col_o(w) + 32 * ch, alpha);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.p_full(g));
+        if (flags & kLastStep) break;
+      }
+      if (!ok) break;
 
       // ---- the piece's end: the two halves' states are merged
+      const int g = J & 1;
       ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g), (J >> 1) & 1, p.status));
+      ++J;
       if (!ok) break;
       tc_fence_after();
       red[w * 3 * kRows + row] = m_;
@@ -562,10 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       const float la = l * ex2_diff(m_, m), lb = other[2 * kRows] * ex2_diff(other[0], m);
       const float lsum = w == 0 ? la + lb : lb + la;
       const float fs = ex2_diff(mv, mva), fo = ex2_diff(other[kRows], mva);
-      const bool whole = mt[kFlags] & kWhole;
       const float out = whole ? out_factor(m, mva, lsum, kPShift) : 1.f;
       const float f0 = (w == 0 ? fs : fo) * out, f1 = (w == 0 ? fo : fs) * out;
-      const int slot = (mt[kFlags] & kTailSlot) ? 1 : 0;
       float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot) * part_floats(D);
       uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + w * (D / 2);
       if (warp_live) {
@@ -607,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
         __threadfence();
         if (!sync_softmax()) break;  // all of the partial result is written
         if (tid == 0) {
-          const bool all = atomicAdd(&p.arrived[mt[kSeg]], 1) == mt[kParts] - 1;
-          if (all) p.arrived[mt[kSeg]] = 0;  // ready for the next call
+          const bool all = atomicAdd(&p.arrived[seg], 1) == parts - 1;
+          if (all) p.arrived[seg] = 0;  // ready for the next call
           words[kLineWords] = all;
           __threadfence();
         }
@@ -617,15 +609,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           // every part, in the order of the keys: this thread's row and half of its columns
           __threadfence();
           auto part_at = [&](int i) {
-            return p.partial + (static_cast<size_t>(mt[kCta0] + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
+            return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
           };
           float jm = -INFINITY, jmv = -INFINITY, jl = 0.f;
-          for (int i = 0; i < mt[kParts]; ++i) {
+          for (int i = 0; i < parts; ++i) {
             const float* x = part_at(i) + kRows * D + row;
             jm = fmaxf(jm, __ldcg(x));
             jmv = fmaxf(jmv, __ldcg(x + kRows));
           }
-          for (int i = 0; i < mt[kParts]; ++i) {
+          for (int i = 0; i < parts; ++i) {
             const float* x = part_at(i) + kRows * D + row;
             jl += __ldcg(x + 2 * kRows) * ex2_diff(__ldcg(x), jm);
           }
@@ -635,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
             float y[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = 0.f;
-            for (int i = 0; i < mt[kParts]; ++i) {
+            for (int i = 0; i < parts; ++i) {
               const float* x = part_at(i);
               const float fx = ex2_diff(__ldcg(x + kRows * D + kRows + row), jmv);
 #pragma unroll
