@@ -428,16 +428,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       // scores in log2 units, masked; s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e
       const float kscale = __int_as_float(meta.z);
       const bool tail = meta.x < 0 || j0 + kPage > all_lim;
-      uint32_t pf[4][NT][2];
-      bool moved = false;
-      float av[NT][2];
+      // Each pass goes over all rows of the lane, so that their chains overlap.
+      float ck[NT][2], top[NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ck = crow[t][e] * kscale;
-          float top = -INFINITY;
-          if (tail || meta.y) {
+        for (int e = 0; e < 2; ++e) ck[t][e] = crow[t][e] * kscale;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][t][i] *= ck[t][i & 1];
+      if (__builtin_expect(tail || meta.y, 0)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             // bit 2 u + x: key kb + 4 u + 2 x is visible
             const int n = meta.x < 0 ? 0 : min(max(lim[t][e] - (j0 + kb), 0), 16);
             uint32_t see = (1u << ((n + 1) >> 1)) - 1u;
@@ -451,48 +458,53 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                float& v = s[u][t][2 * x + e];
-                v = (see >> (2 * u + x)) & 1u ? v * ck : -INFINITY;
-                top = fmaxf(top, v);
-              }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              s[u][t][e] *= ck;
-              s[u][t][2 + e] *= ck;
-              top = fmax3(top, s[u][t][e], s[u][t][2 + e]);
-            }
+              for (int x = 0; x < 2; ++x)
+                if (!((see >> (2 * u + x)) & 1u)) s[u][t][2 * x + e] = -INFINITY;
           }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const float m_new = fmaxf(st.m[t][e], top), mv_new = fmaxf(st.mv[t][e], top + lvs);
-          const float al = ex2_diff(st.m[t][e], m_new);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          top[t][e] = fmax3(fmax3(s[0][t][e], s[0][t][2 + e], s[1][t][e]), fmax3(s[1][t][2 + e], s[2][t][e], s[2][t][2 + e]),
+                            fmaxf(s[3][t][e], s[3][t][2 + e]));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top[t][e] = fmaxf(top[t][e], __shfl_xor_sync(0xffffffffu, top[t][e], o));
+      uint32_t pf[4][NT][2];
+      bool moved = false;
+      float av[NT][2], mu[NT][2], fv[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float m_new = fmaxf(st.m[t][e], top[t][e]), mv_new = fmaxf(st.mv[t][e], top[t][e] + lvs);
+          st.l[t][e] *= ex2_diff(st.m[t][e], m_new);
           av[t][e] = ex2_diff(st.mv[t][e], mv_new);
           moved |= av[t][e] != 1.f;
           st.m[t][e] = m_new;
           st.mv[t][e] = mv_new;
-          const float mu = m_new == -INFINITY ? 0.f : m_new, mvu = mv_new == -INFINITY ? 0.f : mv_new;
-          const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
-          float sum0 = 0.f, sum1 = 0.f;
+          mu[t][e] = m_new == -INFINITY ? 0.f : m_new;
+          fv[t][e] = ex2(fminf(mu[t][e] + lvs - (mv_new == -INFINITY ? 0.f : mv_new) + kPShift, 126.f));
+        }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float p0 = ex2(s[u][t][e] - mu), p1 = ex2(s[u][t][2 + e] - mu);
-            sum0 += p0;
-            sum1 += p1;
-            s[u][t][e] = p0 * f;
-            s[u][t][2 + e] = p1 * f;
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float pr[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = ex2(s[u][t][i] - mu[t][i & 1]);
+            st.l[t][i & 1] += x;
+            pr[i] = x * fv[t][i & 1];
           }
-          st.l[t][e] = st.l[t][e] * al + (sum0 + sum1);
+          pf[u][t][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
+          pf[u][t][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          pf[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
-          pf[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
-        }
-      }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, moved), 0)) {
 #pragma unroll
         for (int n = 0; n < D / 16; ++n)
 #pragma unroll
@@ -746,7 +758,7 @@ cudaError_t launch_nt(const CacheFwdParams& p, const Geometry& geo, int num_sms,
 
 // Rows of a tile: as few as hold all rows, so that no columns of an instruction are
 // empty; above 16 rows the kernel for many rows takes over.
-int rows_of_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kManyRows; }
+int rows_of_tile(int rows) { return rows <= 8 ? 8 : rows <= 32 ? 16 : kManyRows; }
 
 Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
   Geometry g;
