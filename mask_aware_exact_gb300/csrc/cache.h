@@ -68,7 +68,8 @@ struct CacheFwdParams {
   float* partial;       // [CTAs][2] partial results
   uint32_t* vis;        // [row tiles][words]: pages that some row sees
   uint32_t* part;       // [row tiles][words]: pages where intervals hide some key from some row
-  int32_t* prefix;      // [row tiles][words + 1]: running count of visible pages
+  uint16_t* list;       // [row tiles][max_pages]: the former in order, bit 15 from the latter
+  int32_t* listed;      // [row tiles]: their number
 };
 // Rows of the attention's work. The G = H / Hk query heads of a cache head and a
 // sequence's query tokens form one list of rows, r = t * G + g, cut into RT tiles.
@@ -79,7 +80,7 @@ struct Geometry {
 };
 // Byte offsets of the workspace regions.
 struct CacheWs {
-  size_t arrived, class_done, partial, vis, part, prefix, total;
+  size_t arrived, class_done, partial, vis, part, list, listed, total;
 };
 constexpr int kCacheMaxCtas = 256;  // partial results are kept for at most this many CTAs
 // Whether the pages of all row tiles can be counted in 32 bits.

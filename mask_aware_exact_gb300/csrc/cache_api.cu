@@ -210,7 +210,8 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   p.partial = reinterpret_cast<float*>(w + L.partial);
   p.vis = reinterpret_cast<uint32_t*>(w + L.vis);
   p.part = reinterpret_cast<uint32_t*>(w + L.part);
-  p.prefix = reinterpret_cast<int32_t*>(w + L.prefix);
+  p.list = reinterpret_cast<uint16_t*>(w + L.list);
+  p.listed = reinterpret_cast<int32_t*>(w + L.listed);
   const int sms = sm_count();
   if (sms <= 0) return FM_ERR_CUDA;
   return fm::launch_cache_fwd(cache->d, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess

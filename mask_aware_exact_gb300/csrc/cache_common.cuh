@@ -37,32 +37,18 @@ __device__ __forceinline__ int mask_class(const CacheFwdParams& p, const Geometr
 // Pages on a segment's line.
 template <bool kVec>
 __device__ __forceinline__ int pages_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
-  const int rt = seg % geo.RT, bh = seg / geo.RT;
+  const int bh = seg / geo.RT, rt = seg - bh * geo.RT;
   const int b = bh / p.c.Hk;
   if constexpr (kVec) {
     const int cls = mask_class(p, geo, bh - b * p.c.Hk);
     const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
-    return p.prefix[at * (geo.words + 1) + geo.words];
+    return p.listed[at];
   } else {
     const RowTile r = row_tile(p, geo, b, rt, false);
     if (r.t_hi < r.t_lo) return 0;
     const int lim = p.mask.causal ? min(r.len, r.shift + r.t_hi + 1) : r.len;
     return lim > 0 ? (lim + kPage - 1) / kPage : 0;
   }
-}
-
-// Index of the k-th set bit of x (k < popc(x)).
-__device__ __forceinline__ int nth_bit(uint32_t x, int k) {
-  int at = 0;
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    const int n = __popc((x >> at) & ((1u << s) - 1u));
-    if (k >= n) {
-      k -= n;
-      at += s;
-    }
-  }
-  return at;
 }
 
 // The k-th page on the line of row tile rt of (b, hk), and whether intervals hide
@@ -73,15 +59,9 @@ __device__ __forceinline__ int page_on_line(const CacheFwdParams& p, const Geome
   cut = 0;
   if constexpr (!kVec) return k;
   const size_t at = (static_cast<size_t>(b) * geo.classes + mask_class(p, geo, hk)) * geo.RT + rt;
-  const int32_t* pre = p.prefix + at * (geo.words + 1);
-  int lo = 0, hi = geo.words;  // pre[lo] <= k < pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= k) lo = mid; else hi = mid;
-  }
-  const int bit = nth_bit(p.vis[at * geo.words + lo], k - pre[lo]);
-  cut = (p.part[at * geo.words + lo] >> bit) & 1u;
-  return 32 * lo + bit;
+  const int v = p.list[at * p.max_pages + k];
+  cut = v >> 15;
+  return v & 0x7fff;
 }
 
 // A CTA's run on the line of units (pages, or pairs of them) of all segments.

@@ -160,6 +160,40 @@ __device__ __forceinline__ void store_lse(const CacheFwdParams& p, const Geometr
   }
 }
 
+// Sum of the same fragment of several states, in the order they are added.
+struct FragmentSum {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // x: m of the lane's two rows, then mv and l `stride` apart
+  __device__ __forceinline__ void add(const float4& v, const float* x, int stride) {
+    const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float m_new = fmaxf(m[e], x[e]), mv_new = fmaxf(mv[e], x[stride + e]);
+      l[e] = l[e] * ex2_diff(m[e], m_new) + x[2 * stride + e] * ex2_diff(x[e], m_new);
+      const float fa = ex2_diff(mv[e], mv_new), fb = ex2_diff(x[stride + e], mv_new);
+      acc[e] = acc[e] * fa + y[e] * fb;
+      acc[2 + e] = acc[2 + e] * fa + y[2 + e] * fb;
+      m[e] = m_new;
+      mv[e] = mv_new;
+    }
+  }
+  // O of rows r0 .. r0 + 7, columns col .. col + 15, and with column 0 their LSE.
+  __device__ __forceinline__ void store(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0, int rows,
+                                        int col, int lane) const {
+    const int g = lane >> 2, c = lane & 3;
+    const float f0 = out_factor(m[0], mv[0], l[0], kPShift), f1 = out_factor(m[1], mv[1], l[1], kPShift);
+    const int rr = r0 + g, tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+    uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + col + 2 * c;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t v = transpose8x8(pack_bf16x2(acc[2 * x] * f0, acc[2 * x + 1] * f1));
+      if (rr < rows) *reinterpret_cast<uint32_t*>(o + 8 * x) = v;
+    }
+    if (col == 0) store_lse(p, geo, b, hk, r0 + 2 * c, rows, g == 0, m, l);
+  }
+};
+
 // Bits of the keys at[i], at[i + 2], .. at[i + 14] (i = odd) with s <= pos < e.
 __device__ __forceinline__ uint32_t hidden8(const int32_t* s, const int32_t* e, int pos, int odd) {
   uint32_t hid = 0;
@@ -308,6 +342,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   float4* merge = reinterpret_cast<float4*>(smem + S::kMerge);
   float* stats = reinterpret_cast<float*>(smem + S::kStats);
   bool ok = true;
+  int syncs = 0;
+  // all consumer warps; false when a wait gave up
+  auto sync_warps = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.done());
+    ok = __all_sync(0xffffffffu, cache_wait(bar.done(), syncs & 1, p.status));
+    ++syncs;
+    return ok;
+  };
+  // a partial result is written: the last of its segment's notes the join, which all
+  // warps do at the end of the run
+  auto arrive = [&](int seg, int cta0, int parts, int slot_id) {
+    if (atomicAdd(&p.arrived[seg], 1) != parts - 1) return;
+    p.arrived[seg] = 0;  // every part is there: ready for the next call
+    __threadfence();
+    int* job = scan + kJob0 + 4 * slot_id;
+    job[0] = seg, job[1] = cta0, job[2] = parts;
+    atomicOr(&scan[kJobs], 1 << slot_id);
+  };
   int seq = 0;      // ring position of this warp
   int merges = 0;   // pieces so far whose states were merged in shared memory
 
@@ -559,6 +612,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
 
     const int writers = min(count, kConsumers);  // warps that had tiles, from first % 7 on
     const int mine = (warp - first % kConsumers + kConsumers) % kConsumers;
+    if (first + count == run_hi - run_lo) {
+      // the run's last piece: nothing is left to overlap with, so all warps add up,
+      // each its fragments
+      ok = __all_sync(0xffffffffu, count_wait(&scan[kMerged], merges, p.status));
+      if (!ok) break;
+      if (mine < writers) st.put(merge + warp * S::kFrags * 32, stats + 3 * kRows * warp, lane);
+      if (!sync_warps()) break;
+      float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D, kRows);
+#pragma unroll 1
+      for (int fr = warp; fr < S::kFrags; fr += kConsumers) {
+        const int n = fr / NT, t = fr % NT;
+        FragmentSum f;
+#pragma unroll 1
+        for (int k = 0; k < writers; ++k) {
+          const int w = (first + k) % kConsumers;
+          f.add(merge[(w * S::kFrags + fr) * 32 + lane], stats + 3 * kRows * w + 8 * t + 2 * c, kRows);
+        }
+        if (whole) {
+          f.store(p, geo, b, hk, rt * kRows + 8 * t, rows, 16 * n, lane);
+        } else {
+          reinterpret_cast<float4*>(part)[fr * 32 + lane] = make_float4(f.acc[0], f.acc[1], f.acc[2], f.acc[3]);
+          if (n == 0 && g == 0) {
+            float* x = part + kRows * D + 8 * t + 2 * c;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[e] = f.m[e], x[kRows + e] = f.mv[e], x[2 * kRows + e] = f.l[e];
+          }
+        }
+      }
+      if (!whole) {
+        __threadfence();
+        if (!sync_warps()) break;
+        if (tid == 0) arrive(seg, cta0, parts, slot_id);
+      }
+      break;
+    }
     if (mine >= writers) {
       merges += writers > 1;
       continue;
@@ -638,72 +726,44 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       st.put(reinterpret_cast<float4*>(out), out + kRows * D, lane);
       __threadfence();
       __syncwarp();
-      if (lane == 0 && atomicAdd(&p.arrived[seg], 1) == parts - 1) {
-        p.arrived[seg] = 0;  // every part is there: ready for the next call
-        // joined at the end of the run, by all warps
-        int* job = scan + kJob0 + 4 * (slot_id == 0 ? 0 : 1);
-        job[0] = seg, job[1] = cta0, job[2] = parts;
-        atomicOr(&scan[kJobs], slot_id == 0 ? 1 : 2);
-      }
+      if (lane == 0) arrive(seg, cta0, parts, slot_id);
     }
   }
 
   // segments of which this CTA's part came last: every part, in the order of the
   // keys; a warp takes every seventh fragment
   if (ok) {
-    __syncwarp();
     __threadfence();
-    if (lane == 0) mbar_arrive(bar.done());
-    ok = __all_sync(0xffffffffu, cache_wait(bar.done(), 0, p.status));
+    sync_warps();
   }
   for (int j = 0; ok && j < 2; ++j) {
     if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
     const int seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
-    const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-    const RowTile r = row_tile(p, geo, b, rt, false);
-    const int rows = geo.G * r.live;
-    auto part_at = [&](int i) {
-      return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D, kRows);
-    };
+    const int bh = seg / geo.RT, rt = seg - bh * geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const int rows = geo.G * row_tile(p, geo, b, rt, false).live;
+#pragma unroll 1
     for (int fr = warp; fr < S::kFrags; fr += kConsumers) {
       const int n = fr / NT, t = fr % NT;
-      float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll 4
-      for (int i = 0; i < parts; ++i) {
-        const float* x = part_at(i) + kRows * D + 8 * t + 2 * c;
+      FragmentSum f;
+#pragma unroll 1
+      for (int i0 = 0; i0 < parts; i0 += 4) {
+        // four parts on their way at a time
+        float4 v[4];
+        float x[4][6];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          m[e] = fmaxf(m[e], __ldcg(x + e));
-          mv[e] = fmaxf(mv[e], __ldcg(x + kRows + e));
+        for (int i = 0; i < 4; ++i) {
+          const int part = min(i0 + i, parts - 1);
+          const float* at = p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * part_floats(D, kRows);
+          v[i] = __ldcg(reinterpret_cast<const float4*>(at) + fr * 32 + lane);
+          at += kRows * D + 8 * t + 2 * c;
+#pragma unroll
+          for (int q = 0; q < 6; ++q) x[i][q] = __ldcg(at + (q >> 1) * kRows + (q & 1));
         }
-      }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int i = 0; i < parts; ++i) {
-        const float* x = part_at(i);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(x) + fr * 32 + lane);
-        x += kRows * D + 8 * t + 2 * c;
-        float f[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[e] += __ldcg(x + 2 * kRows + e) * ex2_diff(__ldcg(x + e), m[e]);
-          f[e] = ex2_diff(__ldcg(x + kRows + e), mv[e]);
-        }
-        sum[0] += v.x * f[0];
-        sum[1] += v.y * f[1];
-        sum[2] += v.z * f[0];
-        sum[3] += v.w * f[1];
+        for (int i = 0; i < 4; ++i)
+          if (i0 + i < parts) f.add(v[i], x[i], 2);
       }
-      const float f0 = out_factor(m[0], mv[0], l[0], kPShift), f1 = out_factor(m[1], mv[1], l[1], kPShift);
-      const int rr = rt * kRows + 8 * t + g;
-      const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
-      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 16 * n + 2 * c;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t v = transpose8x8(pack_bf16x2(sum[2 * x] * f0, sum[2 * x + 1] * f1));
-        if (rr < rows) *reinterpret_cast<uint32_t*>(o + 8 * x) = v;
-      }
-      if (n == 0) store_lse(p, geo, b, hk, rt * kRows + 8 * t + 2 * c, rows, g == 0, m, l);
+      f.store(p, geo, b, hk, rt * kRows + 8 * t, rows, 16 * n, lane);
     }
   }
 
@@ -796,8 +856,10 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   off = up256(off + tiles * g.words * 4);
   w.part = off;
   off = up256(off + tiles * g.words * 4);
-  w.prefix = off;
-  off = up256(off + tiles * (g.words + 1) * 4);
+  w.list = off;
+  off = up256(off + tiles * max_pages * 2);
+  w.listed = off;
+  off = up256(off + tiles * 4);
   w.total = off;
   return w;
 }
