@@ -127,7 +127,8 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
       if (tid == 0) found[side] = total;
     } else if (before <= x && x < before + mine) {
       int s = seg_lo, at = before, n;
-      while (x >= at + (n = units(s))) at += n, ++s;
+      // a thread with one segment knows its units
+      while (x >= at + (n = each == 1 ? mine : units(s))) at += n, ++s;
       const bool next = uncut && x != at;  // on to the segment's end
       found[side] = next ? at + n : x;
       if (side == 0) {

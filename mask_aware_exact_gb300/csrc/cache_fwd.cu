@@ -160,37 +160,115 @@ __device__ __forceinline__ void store_lse(const CacheFwdParams& p, const Geometr
   }
 }
 
-// Sum of the same fragment of several states, in the order they are added.
-struct FragmentSum {
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  // x: m of the lane's two rows, then mv and l `stride` apart
-  __device__ __forceinline__ void add(const float4& v, const float* x, int stride) {
-    const float y[4] = {v.x, v.y, v.z, v.w};
+// Sums of states, each warp its share of the fragments: warp, warp + kConsumers, ..
+template <int D, int NT>
+struct FragmentSums {
+  static constexpr int kFrags = D / 16 * NT, kMine = (kFrags + kConsumers - 1) / kConsumers;
+  float acc[kMine][4];
+  float m[NT][2], mv[NT][2], l[NT][2];  // of all rows of the lane
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float m_new = fmaxf(m[e], x[e]), mv_new = fmaxf(mv[e], x[stride + e]);
-      l[e] = l[e] * ex2_diff(m[e], m_new) + x[2 * stride + e] * ex2_diff(x[e], m_new);
-      const float fa = ex2_diff(mv[e], mv_new), fb = ex2_diff(x[stride + e], mv_new);
-      acc[e] = acc[e] * fa + y[e] * fb;
-      acc[2 + e] = acc[2 + e] * fa + y[2 + e] * fb;
-      m[e] = m_new;
-      mv[e] = mv_new;
+    for (int q = 0; q < kMine; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[t][e] = mv[t][e] = -INFINITY, l[t][e] = 0.f;
+  }
+  // Adds n (at most kMost) states in order: stats(k) points to m, mv, l [8 NT] of state
+  // k, frags(k) to this lane's part of its fragment 0. The loads of all of them are
+  // issued before the first is used.
+  template <int kMost, typename Stats, typename Frags, typename Load>
+  __device__ __forceinline__ void add(int n, int warp, Stats stats, Frags frags, int c, Load load) {
+    float x[kMost][NT][6];
+    float4 v[kMost][kMine];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const float* st = stats(min(k, n - 1)) + 2 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q < 6; ++q) x[k][t][q] = load(st + 8 * t + (q >> 1) * 8 * NT + (q & 1));
+      const float4* fr = frags(min(k, n - 1));
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) v[k][q] = load(fr + min(warp + kConsumers * q, kFrags - 1) * 32);
+    }
+    float old[NT][2], f[kMost][NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mm = m[t][e], mmv = mv[t][e];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+          if (k < n) mm = fmaxf(mm, x[k][t][e]), mmv = fmaxf(mmv, x[k][t][2 + e]);
+        }
+        old[t][e] = ex2_diff(mv[t][e], mmv);
+        l[t][e] *= ex2_diff(m[t][e], mm);
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+          f[k][t][e] = ex2_diff(x[k][t][2 + e], mmv);
+          if (k < n) l[t][e] += x[k][t][4 + e] * ex2_diff(x[k][t][e], mm);
+        }
+        m[t][e] = mm;
+        mv[t][e] = mmv;
+      }
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      // kConsumers is odd: the rows of a warp's fragments alternate when NT is 2
+      const bool t1 = NT == 2 && ((warp + kConsumers * q) & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][i] *= t1 ? old[NT - 1][i & 1] : old[0][i & 1];
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        if (k < n) {
+          const float f0 = t1 ? f[k][NT - 1][0] : f[k][0][0], f1 = t1 ? f[k][NT - 1][1] : f[k][0][1];
+          acc[q][0] += v[k][q].x * f0;
+          acc[q][1] += v[k][q].y * f1;
+          acc[q][2] += v[k][q].z * f0;
+          acc[q][3] += v[k][q].w * f1;
+        }
+      }
     }
   }
-  // O of rows r0 .. r0 + 7, columns col .. col + 15, and with column 0 their LSE.
-  __device__ __forceinline__ void store(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0, int rows,
-                                        int col, int lane) const {
-    const int g = lane >> 2, c = lane & 3;
-    const float f0 = out_factor(m[0], mv[0], l[0], kPShift), f1 = out_factor(m[1], mv[1], l[1], kPShift);
-    const int rr = r0 + g, tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
-    uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + col + 2 * c;
+  // The sums as a state (see State::put).
+  __device__ __forceinline__ void put(float4* frags, float* stats, int warp, int lane) const {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint32_t v = transpose8x8(pack_bf16x2(acc[2 * x] * f0, acc[2 * x + 1] * f1));
-      if (rr < rows) *reinterpret_cast<uint32_t*>(o + 8 * x) = v;
+    for (int q = 0; q < kMine; ++q)
+      if (warp + kConsumers * q < kFrags)
+        frags[(warp + kConsumers * q) * 32 + lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+    if (warp == 0 && lane < 4) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* x = stats + 8 * t + 2 * lane + e;
+          x[0] = m[t][e], x[8 * NT] = mv[t][e], x[16 * NT] = l[t][e];
+        }
     }
-    if (col == 0) store_lse(p, geo, b, hk, r0 + 2 * c, rows, g == 0, m, l);
+  }
+  // O and LSE of the row tile that begins at row r0.
+  __device__ __forceinline__ void store(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0, int rows,
+                                        int warp, int lane) const {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float f0 = out_factor(m[t][0], mv[t][0], l[t][0], kPShift), f1 = out_factor(m[t][1], mv[t][1], l[t][1], kPShift);
+      const int rr = r0 + 8 * t + g, tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const int fr = warp + kConsumers * q;
+        if (fr >= kFrags || fr % NT != t) continue;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t v = transpose8x8(pack_bf16x2(acc[q][2 * x] * f0, acc[q][2 * x + 1] * f1));
+          if (rr < rows) *reinterpret_cast<uint32_t*>(o + fr / NT * 16 + 8 * x) = v;
+        }
+      }
+      if (warp == 0) store_lse(p, geo, b, hk, r0 + 8 * t + 2 * c, rows, g == 0, m[t], l[t]);
+    }
   }
 };
 
@@ -620,26 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       if (mine < writers) st.put(merge + warp * S::kFrags * 32, stats + 3 * kRows * warp, lane);
       if (!sync_warps()) break;
       float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D, kRows);
-#pragma unroll 1
-      for (int fr = warp; fr < S::kFrags; fr += kConsumers) {
-        const int n = fr / NT, t = fr % NT;
-        FragmentSum f;
-#pragma unroll 1
-        for (int k = 0; k < writers; ++k) {
-          const int w = (first + k) % kConsumers;
-          f.add(merge[(w * S::kFrags + fr) * 32 + lane], stats + 3 * kRows * w + 8 * t + 2 * c, kRows);
-        }
-        if (whole) {
-          f.store(p, geo, b, hk, rt * kRows + 8 * t, rows, 16 * n, lane);
-        } else {
-          reinterpret_cast<float4*>(part)[fr * 32 + lane] = make_float4(f.acc[0], f.acc[1], f.acc[2], f.acc[3]);
-          if (n == 0 && g == 0) {
-            float* x = part + kRows * D + 8 * t + 2 * c;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[e] = f.m[e], x[kRows + e] = f.mv[e], x[2 * kRows + e] = f.l[e];
-          }
-        }
-      }
+      FragmentSums<D, NT> f;
+      f.clear();
+      f.template add<kConsumers>(
+          writers, warp, [&](int k) { return stats + 3 * kRows * ((first + k) % kConsumers); },
+          [&](int k) { return merge + ((first + k) % kConsumers) * S::kFrags * 32 + lane; }, c,
+          [](auto* at) { return *at; });
+      if (whole)
+        f.store(p, geo, b, hk, rt * kRows, rows, warp, lane);
+      else
+        f.put(reinterpret_cast<float4*>(part), part + kRows * D, warp, lane);
       if (!whole) {
         __threadfence();
         if (!sync_warps()) break;
@@ -741,30 +809,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     const int seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
     const int bh = seg / geo.RT, rt = seg - bh * geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
     const int rows = geo.G * row_tile(p, geo, b, rt, false).live;
-#pragma unroll 1
-    for (int fr = warp; fr < S::kFrags; fr += kConsumers) {
-      const int n = fr / NT, t = fr % NT;
-      FragmentSum f;
-#pragma unroll 1
-      for (int i0 = 0; i0 < parts; i0 += 4) {
-        // four parts on their way at a time
-        float4 v[4];
-        float x[4][6];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int part = min(i0 + i, parts - 1);
-          const float* at = p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * part_floats(D, kRows);
-          v[i] = __ldcg(reinterpret_cast<const float4*>(at) + fr * 32 + lane);
-          at += kRows * D + 8 * t + 2 * c;
-#pragma unroll
-          for (int q = 0; q < 6; ++q) x[i][q] = __ldcg(at + (q >> 1) * kRows + (q & 1));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i0 + i < parts) f.add(v[i], x[i], 2);
-      }
-      f.store(p, geo, b, hk, rt * kRows + 8 * t, rows, 16 * n, lane);
+    FragmentSums<D, NT> f;
+    f.clear();
+    for (int i0 = 0; i0 < parts; i0 += 4) {
+      // four parts on their way at a time
+      auto at = [&](int i) {
+        const int part = i0 + i;
+        return p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * part_floats(D, kRows);
+      };
+      f.template add<4>(
+          min(parts - i0, 4), warp, [&](int i) { return at(i) + kRows * D; },
+          [&](int i) { return reinterpret_cast<const float4*>(at(i)) + lane; }, c,
+          [](auto* at) { return __ldcg(at); });  // other CTAs wrote them: past L1
     }
+    f.store(p, geo, b, hk, rt * kRows, rows, warp, lane);
   }
 
   // segments without a visible page: O = 0, LSE = -inf

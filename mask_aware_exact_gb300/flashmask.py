@@ -120,16 +120,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.flashmask_check_status.restype = i
     L.flashmask_status_string.argtypes = [i]
     L.flashmask_status_string.restype = ctypes.c_char_p
-    i64, i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
-    L.flashmask_rope.argtypes = [vp, i, vp, i64, vp, i, i, i, i, i, i, f, i, vp]
+    L.flashmask_rope.argtypes = [vp, i, vp, ctypes.c_int64, vp, i, i, i, i, i, i, f, i, vp]
     L.flashmask_rope.restype = i
     L.flashmask_cache_workspace_bytes.argtypes = [i, i, i, i, i, i]
     L.flashmask_cache_workspace_bytes.restype = sz
-    L.flashmask_cache_append.argtypes = [ctypes.POINTER(_FmCache), vp, i, vp, i64p, vp, i64p, vp, vp,
+    L.flashmask_cache_append.argtypes = [ctypes.POINTER(_FmCache), vp, i, vp, vp, vp, vp, vp, vp,
                                          i, i, vp, sz, vp]
     L.flashmask_cache_append.restype = i
-    L.flashmask_fwd_cache.argtypes = [vp, i64p, ctypes.POINTER(_FmCache), vp, i, vp, vp,
-                                      ctypes.POINTER(_FmMask), i, i, i, f, vp, i64p, vp, vp, sz, vp]
+    L.flashmask_fwd_cache.argtypes = [vp, vp, ctypes.POINTER(_FmCache), vp, i, vp, vp,
+                                      ctypes.POINTER(_FmMask), i, i, i, f, vp, vp, vp, vp, sz, vp]
     L.flashmask_fwd_cache.restype = i
     _lib = L
     return L
@@ -481,7 +480,7 @@ def flashmask_selftest_timeout(ws: torch.Tensor, limit_ns: int, ctas: int = 1, s
 
 # ---------------------------------------------------------------- rotary positions
 _ROPE_DTYPES = {torch.bfloat16: FM_BF16, torch.float16: FM_F16, torch.float32: FM_F32}
-_Strides = ctypes.c_int64 * 3
+_STRIDES = struct.Struct("@3q")
 _HEADS = struct.Struct("@PPi6q")  # an _FmHeads: x, y, H, strides of x and y
 assert _HEADS.size == ctypes.sizeof(_FmHeads)
 
@@ -546,21 +545,20 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
 
 
 def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, where):
-    dtype = _ROPE_DTYPES.get(q.dtype)
-    if dtype is None:
+    code = _ROPE_DTYPES.get(q.dtype)
+    if code is None:
         raise ValueError("q must be bf16, fp16 or fp32")
     index = q.get_device()
     _rows(q, "q", q.dtype, index)
     B, Hq, N, d = q.shape
-    xs = (q,)
     if k is not None:
         _rows(k, "k", q.dtype, index)
-        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
             raise ValueError("q and k must share B, N and d")
-        xs = (q, k)
-    rot = 2 * freqs.numel()
-    _want(freqs, "freqs", torch.float64, index, (rot // 2,))
-    if rot > d:
+    n = freqs.numel()
+    _want(freqs, "freqs", torch.float64, index, (n,))
+    if 2 * n > d:
         raise ValueError("freqs must be [rot_dim / 2] with rot_dim <= d")
     pos, pos_stride = None, 0
     if positions is not None:
@@ -571,25 +569,34 @@ def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, whe
                              "contiguous")
         pos = positions.data_ptr()
         pos_stride = positions.stride(0) if positions.shape[0] > 1 else 0
+    yq = yk = None
     if out is not None:
-        out = tuple(out)[:len(xs)]
-        for t, x in zip(out, xs):
-            _rows(t, "out", q.dtype, index)
-            if t.shape != x.shape:
-                raise ValueError("out must have the shapes of q and k")
+        yq, yk = out[0], (out[1] if k is not None else None)
+        for t, x in ((yq, q), (yk, k)):
+            if x is not None:
+                _rows(t, "out", q.dtype, index)
+                if t.shape != x.shape:
+                    raise ValueError("out must have the shapes of q and k")
 
     def call(raw):
-        ys = out or [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
+        oq, ok = yq, yk
+        if oq is None:
+            oq = torch.empty((B, Hq, N, d), dtype=q.dtype, device=q.device)
+            if k is not None:
+                ok = torch.empty((B, Hk, N, d), dtype=q.dtype, device=q.device)
         if B * N * d > 0:
-            heads = b"".join([_HEADS.pack(x.data_ptr(), y.data_ptr(), x.shape[1], *x.stride()[:3],
-                                          *y.stride()[:3]) for x, y in zip(xs, ys)])
-            st = load().flashmask_rope(heads, len(xs), pos, pos_stride, freqs.data_ptr(), B, N, d, rot,
-                                       bool(interleaved), dtype, mscale, inverse, raw)
+            heads = _HEADS.pack(q.data_ptr(), oq.data_ptr(), Hq, *q.stride()[:3], *oq.stride()[:3])
+            if k is not None:
+                heads += _HEADS.pack(k.data_ptr(), ok.data_ptr(), Hk, *k.stride()[:3], *ok.stride()[:3])
+            st = _lib.flashmask_rope(heads, 1 if k is None else 2, pos, pos_stride, freqs.data_ptr(), B, N,
+                                     d, 2 * n, bool(interleaved), code, mscale, inverse, raw)
             if st:
                 raise FlashMaskError(st, where)
-        return ys[0], (ys[1] if k is not None else None)
+        return oq, ok
 
-    return _launch(index, stream, (*xs, freqs, positions, *(out or ())), call)
+    if _lib is None:
+        load()
+    return _launch(index, stream, (q, k, freqs, positions, yq, yk), call)
 
 
 def flashmask_rope(q, k, freqs, positions=None, interleaved=False, mscale=1.0, out=None,
@@ -698,8 +705,8 @@ def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=No
 
     def call(raw):
         code = load().flashmask_cache_append(c, page_table.data_ptr(), max_pages, k.data_ptr(),
-                                             _Strides(*k.stride()[:3]), v.data_ptr(),
-                                             _Strides(*v.stride()[:3]), st, ct, B, N, ws.data_ptr(),
+                                             _STRIDES.pack(*k.stride()[:3]), v.data_ptr(),
+                                             _STRIDES.pack(*v.stride()[:3]), st, ct, B, N, ws.data_ptr(),
                                              ws.numel(), raw)
         if code:
             raise FlashMaskError(code, "flashmask_cache_append")
@@ -747,9 +754,9 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
     def call(raw):
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
         norm = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
-        code = load().flashmask_fwd_cache(q.data_ptr(), _Strides(*q.stride()[:3]), c,
+        code = load().flashmask_fwd_cache(q.data_ptr(), _STRIDES.pack(*q.stride()[:3]), c,
                                           page_table.data_ptr(), max_pages, ln, ql, m, B, H, N, scale,
-                                          out.data_ptr(), _Strides(*out.stride()[:3]), norm.data_ptr(),
+                                          out.data_ptr(), _STRIDES.pack(*out.stride()[:3]), norm.data_ptr(),
                                           ws.data_ptr(), ws.numel(), raw)
         if code:
             raise FlashMaskError(code, "flashmask_fwd_cache")
