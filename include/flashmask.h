@@ -404,7 +404,7 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * chunk of a prompt. lens (int32 [B]) is the number of cached tokens, the query
  * tokens' own among them; q_lens (int32 [B], may be NULL: N) how many of the N
  * rows are real. Row t of sequence b sits at position i = lens[b] - q_lens[b] +
- * t; rows t >= q_lens[b] are neither read nor written. Key j < lens[b] is
+ * t; rows t >= q_lens[b] have no influence and are not written. Key j < lens[b] is
  * masked when
  *     (causal && j > i) || (LTS[j] <= i < LTE[j]) || (UTS[j] <= i < UTE[j])
  * with the vectors [B, Hm, max_pages * FM_PAGE] of `mask`, whose lts and lte

@@ -64,11 +64,9 @@ struct CacheFwdParams {
   int32_t* status;
   // workspace (see CacheWs)
   int32_t* arrived;     // [segments]: partial results that have arrived (0 between calls)
-  int32_t* class_done;  // [row tiles]: words classified (0 between calls)
   float* partial;       // [CTAs][2] partial results
-  uint32_t* vis;        // [row tiles][words]: pages that some row sees
-  uint32_t* part;       // [row tiles][words]: pages where intervals hide some key from some row
-  uint16_t* list;       // [row tiles][max_pages]: the former in order, bit 15 from the latter
+  uint16_t* list;       // [row tiles][max_pages]: pages that some row sees, in order; bit 15: intervals
+                        // hide some key of the page from some row
   int32_t* listed;      // [row tiles]: their number
 };
 // Rows of the attention's work. The G = H / Hk query heads of a cache head and a
@@ -80,7 +78,7 @@ struct Geometry {
 };
 // Byte offsets of the workspace regions.
 struct CacheWs {
-  size_t arrived, class_done, partial, vis, part, list, listed, total;
+  size_t arrived, partial, list, listed, total;
 };
 constexpr int kCacheMaxCtas = 256;  // partial results are kept for at most this many CTAs
 // Whether the pages of all row tiles can be counted in 32 bits.

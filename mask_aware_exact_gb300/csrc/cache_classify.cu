@@ -3,15 +3,32 @@
 // row tile, the list of the pages that some row sees, in order, each with a bit that
 // says whether intervals hide some of its keys from some row, and their number.
 //
-// Latency-bound: 8 or 16 bytes of bounds per cached token, spread over one CTA for
-// every 32 pages, each thread loading the bounds of 8 keys at once. The CTA that
-// finishes a row tile last makes the list from the others' page bits.
+// Latency-bound: 8 or 16 bytes of bounds per cached token. A cluster of eight CTAs
+// shares a row tile, each taking an eighth of the pages; the counts that place a CTA's
+// part of the list come from the others' shared memory. 8 sequences of 131072 tokens:
+// 8.7 us with cold caches, like one CTA for every 32 pages with a counter in global
+// memory, but without its scratch words.
 #include "cache_common.cuh"
+#include "flashmask.h"
 
 namespace fm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;
+constexpr int kCluster = 8;
+constexpr int kWordsMost = FM_MAX_SEQLEN / kPage / 32 / kCluster;  // 32-page words of a CTA
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The int at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ int of_cta(const int* at, int rank) {
+  uint32_t remote;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
   const int4 a = reinterpret_cast<const int4*>(src)[0], b = reinterpret_cast<const int4*>(src)[1];
@@ -19,120 +36,127 @@ __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
 }
 
 // A key is hidden from the whole tile, positions [lo, hi], if the union of its
-// intervals (and of the rows above it, when causal) covers them.
-__global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams p, const Geometry geo) {
-  __shared__ uint32_t bits[2][kThreads / 32];
-  __shared__ int sums[kThreads / 32 + 1];
-  __shared__ int last;
-  const int tile = blockIdx.x / geo.words, w = blockIdx.x - tile * geo.words, b = blockIdx.y;
+// intervals (and of the rows above it, when causal) covers them. A thread takes 8 keys
+// at a time, so a page is 8 lanes and a warp takes groups of 4 pages.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    cache_classify(const CacheFwdParams p, const Geometry geo) {
+  __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
+  __shared__ int before[kWordsMost];  // visible pages of this CTA before a word
+  __shared__ int count;               // visible pages of this CTA
+  const int tile = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = blockIdx.y;
   const int cls = tile / geo.RT, rt = tile - cls * geo.RT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int each = (geo.words + kCluster - 1) / kCluster;
+  const int w0 = rank * each, words = max(0, min(each, geo.words - w0));  // words [w0, w0 + words)
   const RowTile r = row_tile(p, geo, b, rt, blockIdx.x == 0 && tid == 0);
   const int lo = r.shift + r.t_lo, hi = r.shift + r.t_hi;
   int m0 = cls, m1 = cls;  // mask heads of the class
   if (geo.classes != p.mask.Hm) {
-    const int each = p.H / p.mask.Hm;
-    m0 = cls * geo.G / each;
-    m1 = (cls * geo.G + geo.G - 1) / each;
+    const int per = p.H / p.mask.Hm;
+    m0 = cls * geo.G / per;
+    m1 = (cls * geo.G + geo.G - 1) / per;
   }
   const int L = p.max_pages * kPage;
-  const int j0 = (w * kThreads + tid) * 8;  // this thread's keys j0 .. j0 + 7
   const int end = hi < lo ? 0 : p.mask.causal ? min(r.len, hi + 1) : r.len;
-  bool see = false, cut = false;
-  if (j0 < end) {
-    for (int m = m0; m <= m1; ++m) {
-      const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
-      int s0[8] = {}, e0[8] = {}, s1[8] = {}, e1[8] = {};
-      if (p.mask.lts) {
-        load8(p.mask.lts + at, s0);
-        load8(p.mask.lte + at, e0);
-      }
-      if (p.mask.uts) {
-        load8(p.mask.uts + at, s1);
-        load8(p.mask.ute + at, e1);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = j0 + i;
-        if (j >= end) continue;
-        cut |= max(s0[i], lo) < min(e0[i], hi + 1) || max(s1[i], lo) < min(e1[i], hi + 1);
-        int reach = p.mask.causal ? max(lo, j) : lo;  // first position not known to be hidden
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (s0[i] <= reach && reach < e0[i]) reach = e0[i];
-          if (s1[i] <= reach && reach < e1[i]) reach = e1[i];
+#pragma unroll 2
+  for (int i = warp; i < 8 * words; i += kThreads / 32) {
+    const int j0 = ((8 * w0 + i) * 32 + lane) * 8;  // this thread's keys j0 .. j0 + 7
+    bool see = false, cut = false;
+    if (j0 < end) {
+      for (int m = m0; m <= m1; ++m) {
+        const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
+        int s0[8] = {}, e0[8] = {};
+        if (p.mask.lts) {
+          load8(p.mask.lts + at, s0);
+          load8(p.mask.lte + at, e0);
         }
-        see |= reach <= hi;
+        if (!p.mask.uts) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const bool there = j0 + k < end;
+            const int from = p.mask.causal ? max(lo, j0 + k) : lo;  // the rows above are hidden anyway
+            cut |= there && max(s0[k], lo) < min(e0[k], hi + 1);
+            see |= there && !(s0[k] <= from && hi < e0[k]);
+          }
+        } else {
+          int s1[8], e1[8];
+          load8(p.mask.uts + at, s1);
+          load8(p.mask.ute + at, e1);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const bool there = j0 + k < end;
+            cut |= there && (max(s0[k], lo) < min(e0[k], hi + 1) || max(s1[k], lo) < min(e1[k], hi + 1));
+            int reach = p.mask.causal ? max(lo, j0 + k) : lo;  // first position not known to be hidden
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (s0[k] <= reach && reach < e0[k]) reach = e0[k];
+              if (s1[k] <= reach && reach < e1[k]) reach = e1[k];
+            }
+            see |= there && reach <= hi;
+          }
+        }
       }
     }
-  }
-  // a page is eight lanes; a warp has four pages
-  const uint32_t sees = __ballot_sync(0xffffffffu, see), cuts = __ballot_sync(0xffffffffu, cut);
-  if (lane == 0) {
-    uint32_t v = 0, c = 0;
+    const uint32_t sb = __ballot_sync(0xffffffffu, see), cb = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) {
+      uint32_t v = 0, c = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v |= static_cast<uint32_t>((sees >> (8 * i) & 0xffu) != 0) << i;
-      c |= static_cast<uint32_t>((cuts >> (8 * i) & 0xffu) != 0) << i;
+      for (int k = 0; k < 4; ++k) {
+        v |= static_cast<uint32_t>((sb >> (8 * k) & 0xffu) != 0) << k;
+        c |= static_cast<uint32_t>((cb >> (8 * k) & 0xffu) != 0) << k;
+      }
+      sees[i] = static_cast<uint8_t>(v);
+      cuts[i] = static_cast<uint8_t>(c);
     }
-    bits[0][warp] = v << (4 * warp);
-    bits[1][warp] = c << (4 * warp);
   }
   __syncthreads();
+  auto word_of = [&](int i) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v |= static_cast<uint32_t>(sees[8 * i + k]) << (4 * k);
+    return v;
+  };
+  if (warp == 0) {
+    int sum = 0;
+    for (int i0 = 0; i0 < words; i0 += 32) {
+      const int n = i0 + lane < words ? __popc(word_of(i0 + lane)) : 0;
+      int c = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
+      }
+      if (i0 + lane < words) before[i0 + lane] = sum + c - n;
+      sum += __shfl_sync(0xffffffffu, c, 31);
+    }
+    if (lane == 0) count = sum;
+  }
+  cluster_sync();
+  // this CTA's place in the list, and the whole
+  int mine = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < kCluster; ++k) {
+    const int x = of_cta(&count, k);
+    if (k < rank) mine += x;
+    total += x;
+  }
   const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
-  if (tid == 0) {
-    uint32_t v = 0, c = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      v |= bits[0][i];
-      c |= bits[1][i];
-    }
-    p.vis[at * geo.words + w] = v;
-    p.part[at * geo.words + w] = c;
-    __threadfence();
-    last = atomicAdd(&p.class_done[at], 1) == geo.words - 1;
+  uint16_t* list = p.list + at * p.max_pages + mine;
+  for (int q = tid; q < 32 * words; q += kThreads) {
+    const int i = q >> 5, bit = q & 31;
+    const uint32_t v = word_of(i);
+    if (v >> bit & 1u)
+      list[before[i] + __popc(v & ((1u << bit) - 1u))] =
+          static_cast<uint16_t>((32 * (w0 + i) + bit) | (cuts[q >> 2] >> (q & 3) & 1u) << 15);
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  uint16_t* list = p.list + at * p.max_pages;
-  int total = 0;
-  for (int w0 = 0; w0 < geo.words; w0 += kThreads) {
-    const bool mine = w0 + tid < geo.words;
-    uint32_t v = mine ? __ldcg(&p.vis[at * geo.words + w0 + tid]) : 0;
-    const uint32_t c = mine ? __ldcg(&p.part[at * geo.words + w0 + tid]) : 0;
-    int sum = __popc(v);
-    const int n = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += x;
-    }
-    if (lane == 31) sums[warp] = sum;
-    __syncthreads();
-    int before = total + sum - n;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += sums[i];
-      total += sums[i];
-    }
-    while (v) {
-      const int bit = __ffs(v) - 1;
-      v &= v - 1;
-      list[before++] = static_cast<uint16_t>((32 * (w0 + tid) + bit) | (c >> bit & 1u) << 15);
-    }
-    __syncthreads();
-  }
-  if (tid == 0) {
-    p.listed[at] = total;
-    p.class_done[at] = 0;
-  }
+  if (rank == 0 && tid == 0) p.listed[at] = total;
+  cluster_sync();  // no CTA leaves while its count may be read
 }
 
 }  // namespace
 
 cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(geo.words) * static_cast<unsigned>(geo.classes * geo.RT),
+  const dim3 grid(static_cast<unsigned>(kCluster) * static_cast<unsigned>(geo.classes * geo.RT),
                   static_cast<unsigned>(p.B));
   cache_classify<<<grid, kThreads, 0, s>>>(p, geo);
   return cudaGetLastError();

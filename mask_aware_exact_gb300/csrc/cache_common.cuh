@@ -238,5 +238,4 @@ __device__ __forceinline__ float out_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
-
 }  // namespace fm

@@ -465,8 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       // the query row that this lane brings in, 16 elements of each half: d = 64 half + 16 c ..
+      // (read whether real or not, as long as it exists: the number of real rows is
+      // still on its way)
       const int rr = rt * kRows + 8 * t + g;
-      const bool live = rr < rows;
+      const bool there = rr < geo.G * p.N, live = rr < rows;
       const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
       uint4 x[D / 64][2];
       const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
@@ -474,12 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          x[hf][u] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
+          x[hf][u] = there ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
       uint32_t top = 0;
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          if (!live) x[hf][u] = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t mk = 0x7fff7fffu;
           const uint32_t a = __vmaxu2(__vmaxu2(x[hf][u].x & mk, x[hf][u].y & mk), __vmaxu2(x[hf][u].z & mk, x[hf][u].w & mk));
           top = max(top, max(a & 0xffffu, a >> 16));
@@ -905,15 +908,9 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   size_t off = 256;  // the status word
   w.arrived = off;
   off = up256(off + tiles * 4);
-  w.class_done = off;
-  off = up256(off + tiles * 4);
   w.partial = off;
   off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 *
                     (g.rows == kManyRows ? cache_fwd_rows_part_floats(d) : part_floats(d, g.rows)) * 4);
-  w.vis = off;
-  off = up256(off + tiles * g.words * 4);
-  w.part = off;
-  off = up256(off + tiles * g.words * 4);
   w.list = off;
   off = up256(off + tiles * max_pages * 2);
   w.listed = off;
