@@ -371,8 +371,10 @@ typedef struct {
 
 /* Workspace of the two calls below for these sizes (H query heads, N new or
  * query tokens a sequence); 0 for an unsupported shape. 256-byte aligned and
- * zeroed before its first use, as at the top of this file; not to be shared by
- * calls that may run at the same time. Its first 16 bytes are the status word. */
+ * zeroed before its first use; not to be shared by calls that may run at the
+ * same time. One workspace serves these two calls in turn for all sizes that
+ * it is large enough for. Zero it again after another entry point has used it
+ * or after FM_ERR_TIMEOUT. Its first 16 bytes are the status word. */
 size_t flashmask_cache_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages);
 
 /* Writes N new tokens of each sequence behind the start[b] it holds: K and V
@@ -390,6 +392,7 @@ size_t flashmask_cache_workspace_bytes(int B, int H, int Hk, int N, int d, int m
  *   A token with a value that is not finite, in K or in V of a head, does not
  *   count for that head's scales and is stored so that every query that sees
  *   it, and no other, gets NaN: its K codes are NaN, its V codes zero.
+ *   count outside [0, N] counts as the nearer bound.
  *   The pages written by one call must be distinct (a page shared by two
  *   sequences is copied by the caller before either appends to it). A start
  *   below 0 or a sequence that would outgrow max_pages is left alone and
@@ -404,7 +407,8 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * chunk of a prompt. lens (int32 [B]) is the number of cached tokens, the query
  * tokens' own among them; q_lens (int32 [B], may be NULL: N) how many of the N
  * rows are real. Row t of sequence b sits at position i = lens[b] - q_lens[b] +
- * t; rows t >= q_lens[b] have no influence and are not written. Key j < lens[b] is
+ * t; rows t >= q_lens[b] have no influence and are not written; q_lens outside
+ * [0, N] counts as the nearer bound. Key j < lens[b] is
  * masked when
  *     (causal && j > i) || (LTS[j] <= i < LTE[j]) || (UTS[j] <= i < UTE[j])
  * with the vectors [B, Hm, max_pages * FM_PAGE] of `mask`, whose lts and lte

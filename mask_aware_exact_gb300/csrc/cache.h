@@ -63,7 +63,8 @@ struct CacheFwdParams {
   float* lse;
   int32_t* status;
   // workspace (see CacheWs)
-  int32_t* arrived;     // [segments]: partial results that have arrived (0 between calls)
+  int32_t* arrived;     // [CTAs]: partial results that have arrived of the cut segment that begins
+                        // in a CTA's run (0 between calls)
   float* partial;       // [CTAs][2] partial results
   uint16_t* list;       // [row tiles][max_pages]: pages that some row sees, in order; bit 15: intervals
                         // hide some key of the page from some row

@@ -26,6 +26,14 @@ int sm_count() {
   return n;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Whether rows written with these strides lie apart (a dimension of one size may have
+// any stride, others not zero).
+bool apart(const int64_t* s, int B, int H, int N) {
+  return (B == 1 || s[0] != 0) && (H == 1 || s[1] != 0) && (N == 1 || s[2] != 0);
+}
+
 // Rows of 8-element (16-byte) pieces need strides that keep them aligned.
 bool strides_ok(const int64_t* s) {
   for (int i = 0; i < 3; ++i)
@@ -50,7 +58,8 @@ bool cache_shape_ok(int B, int H, int Hk, int N, int d, int max_pages) {
 
 fm_status cache_ok(const fm_cache* c) {
   if (!c || !c->k8 || !c->v8 || !c->kscale || !c->vscale) return FM_ERR_INVALID_ARG;
-  if (!aligned16(c->k8) || !aligned16(c->v8)) return FM_ERR_INVALID_ARG;
+  if (!aligned16(c->k8) || !aligned16(c->v8) || !aligned4(c->kscale) || !aligned4(c->vscale))
+    return FM_ERR_INVALID_ARG;
   if (c->pages <= 0) return FM_ERR_INVALID_ARG;
   return FM_OK;
 }
@@ -106,6 +115,8 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
     }
   }
   if (heads > 65535 || static_cast<long long>(B) * N * d > (1LL << 38)) return FM_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_tensors; ++i)
+    if (!apart(t[i].ys, B, t[i].H, N)) return FM_ERR_INVALID_ARG;
   p.positions = positions;
   p.pos_stride = pos_stride;
   p.freqs = freqs;
@@ -136,6 +147,7 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
   if (cs != FM_OK) return cs;
   if (!page_table || !k || !v || !ks || !vs || !start) return FM_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !strides_ok(ks) || !strides_ok(vs)) return FM_ERR_INVALID_ARG;
+  if (!aligned4(page_table) || !aligned4(start) || !aligned4(count)) return FM_ERR_INVALID_ARG;
   if (!cache_shape_ok(B, cache->Hk, cache->Hk, N, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
   const fm_status st = check_ws(ws, ws_bytes, 16);
   if (st != FM_OK) return st;
@@ -168,6 +180,8 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   if (cs != FM_OK) return cs;
   if (!q || !qs || !page_table || !lens || !o || !os || !lse) return FM_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !strides_ok(qs) || !strides_ok(os)) return FM_ERR_INVALID_ARG;
+  if (!aligned4(page_table) || !aligned4(lens) || !aligned4(q_lens) || !aligned4(lse))
+    return FM_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FM_ERR_INVALID_ARG;
   if (mask && !vectors_ok(mask)) return FM_ERR_INVALID_ARG;
   if (!cache_shape_ok(B, H, cache->Hk, N, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
@@ -175,6 +189,7 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   const fm::CacheWs L = fm::cache_ws_layout(B, H, cache->Hk, N, cache->d, max_pages);
   const fm_status st = check_ws(ws, ws_bytes, L.total);
   if (st != FM_OK) return st;
+  if (!apart(os, B, H, N)) return FM_ERR_INVALID_ARG;
   fm::CacheFwdParams p;
   p.q = static_cast<const uint16_t*>(q);
   p.c = cache_dev(cache);

@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   // a partial result is written: the last of its segment's notes the join, which all
   // warps do at the end of the run
   auto arrive = [&](int seg, int cta0, int parts, int slot_id) {
-    if (atomicAdd(&p.arrived[seg], 1) != parts - 1) return;
-    p.arrived[seg] = 0;  // every part is there: ready for the next call
+    if (atomicAdd(&p.arrived[cta0], 1) != parts - 1) return;
+    p.arrived[cta0] = 0;  // every part is there: ready for the next call
     __threadfence();
     int* job = scan + kJob0 + 4 * slot_id;
     job[0] = seg, job[1] = cta0, job[2] = parts;
@@ -905,9 +905,11 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   const Geometry g = geometry(H, Hk, Hk, N, max_pages);
   const size_t tiles = static_cast<size_t>(B) * Hk * g.RT;
   CacheWs w;
-  size_t off = 256;  // the status word
+  // the status word and the counters, which have to be zero, lie at the same place for
+  // all sizes, so that one workspace serves them in turn
+  size_t off = 256;
   w.arrived = off;
-  off = up256(off + tiles * 4);
+  off = up256(off + kCacheMaxCtas * 4);
   w.partial = off;
   off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 *
                     (g.rows == kManyRows ? cache_fwd_rows_part_floats(d) : part_floats(d, g.rows)) * 4);

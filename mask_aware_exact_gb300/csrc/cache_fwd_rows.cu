@@ -599,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
         __threadfence();
         if (!sync_softmax()) break;  // all of the partial result is written
         if (tid == 0) {
-          const bool all = atomicAdd(&p.arrived[seg], 1) == parts - 1;
-          if (all) p.arrived[seg] = 0;  // ready for the next call
+          const bool all = atomicAdd(&p.arrived[cta0], 1) == parts - 1;
+          if (all) p.arrived[cta0] = 0;  // ready for the next call
           words[kLineWords] = all;
           __threadfence();
         }

@@ -267,6 +267,22 @@ def test_strides_streams_and_repeatability():
 
 
 @pytest.mark.gpu
+def test_one_workspace_serves_all_sizes_in_turn():
+    fm = need_gpu()
+    ws = fm.alloc_cache_workspace(8, 32, 4, 40, 128, 40)
+    g = torch.Generator().manual_seed(0)
+    for i, (B, H, Hk, N, d, L, masked) in enumerate([
+            (1, 8, 1, 1, 128, 2400, False), (8, 32, 4, 1, 64, 700, True), (2, 8, 2, 40, 128, 2000, False),
+            (1, 1, 1, 1, 64, 2500, False), (3, 16, 4, 8, 128, 900, True), (1, 8, 1, 1, 128, 2400, False),
+            (1, 32, 1, 9, 64, 2000, True)]):
+        lens = [max(N, L - 97 * b) for b in range(B)]
+        q, cache, table, _ = make(fm, B, H, Hk, N, d, lens, seed=i)
+        mask = mask_of("window_prefix", B, H, Hk, N, table.shape[1] * PAGE, g, fm) if masked else None
+        o, lse = run(fm, q, cache, table, lens, mask=mask, ws=ws)
+        check(o, lse, q, cache, table, lens, mask=mask)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("masked", [False, True])
 def test_graph_replay_with_other_lengths(masked):
     # one capture serves a growing batch: lengths and pages live on the device
@@ -380,7 +396,9 @@ def test_refusals(lib):
     upper = fm._FmMask(FAKE, FAKE, None, FAKE, 1, 1)
     for bad in (dict(q=None), dict(q=FAKE + 8), dict(qs=(0, 4, 64)), dict(k8=None), dict(pages=0),
                 dict(lens=None), dict(mask=half), dict(mask=upper), dict(scale=0.0),
-                dict(scale=float("inf")), dict(o=None), dict(o=FAKE + 2)):
+                dict(scale=float("inf")), dict(o=None), dict(o=FAKE + 2), dict(lens=FAKE + 2),
+                dict(qs=(0, 0, 64)),  # as O's strides they let heads overlap
+                dict(mask=fm._FmMask(FAKE + 4, FAKE, None, None, 1, 1))):
         assert call(lib, **bad) == fm.FM_ERR_INVALID_ARG, bad
     for bad in (dict(d=32), dict(H=3), dict(H=0), dict(N=0), dict(B=0), dict(max_pages=0),
                 dict(mask=fm._FmMask(FAKE, FAKE, None, None, 3, 1)),

@@ -172,16 +172,16 @@ def lib():
     return fm.load()
 
 
-def call(lib, x=FAKE, y=FAKE, H=2, n=1, positions=None, freqs=FAKE, B=1, N=4, d=64, rot=64,
+def call(lib, x=FAKE, y=FAKE, H=2, ys=(512, 256, 64), n=1, positions=None, freqs=FAKE, B=1, N=4, d=64, rot=64,
          dtype=fm.FM_BF16, mscale=1.0):
-    t = (fm._FmHeads * 2)(*[fm._FmHeads(x, y, H, (0, 0, 0), (0, 0, 0))] * 2)
+    t = (fm._FmHeads * 2)(*[fm._FmHeads(x, y, H, (0, 0, 0), ys)] * 2)
     return lib.flashmask_rope(t, n, positions, 0, freqs, B, N, d, rot, 0, dtype, mscale, 0, None)
 
 
 def test_refusals(lib):
     for bad in (dict(x=None), dict(y=None), dict(n=0), dict(n=3), dict(dtype=3), dict(freqs=None),
                 dict(freqs=FAKE + 4), dict(positions=FAKE + 2), dict(x=FAKE + 1),
-                dict(mscale=float("nan"))):
+                dict(mscale=float("nan")), dict(ys=(512, 0, 64)), dict(ys=(512, 256, 0))):
         assert call(lib, **bad) == fm.FM_ERR_INVALID_ARG, bad
     for bad in (dict(B=0), dict(N=0), dict(H=0), dict(d=0), dict(rot=66), dict(rot=-2), dict(rot=7),
                 dict(H=70000), dict(B=1 << 16, N=1 << 16)):
