@@ -25,7 +25,7 @@
 //   10     walks the run, looks pages up, issues the copies, publishes a step's
 //          description to all roles (ring of kMetaRing).
 //   12, 13 conversion of K; 14, 15 of V.
-// TMEM: S regions [0,128) [128,256), O_0 [256, 256+d), O_1 [384, 384+d); P over S.
+// TMEM: R = 2 S regions of 128 columns (3 with d = 64), then O_0 and O_1; P over S.
 //
 // What bounds it: shared memory. A step with d = 128 writes 32 KB of codes and 64 KB of
 // fp16 operands and reads 32 KB and 96 KB, 224 KB at 128 bytes a clock: 1 750 cycles,
@@ -40,8 +40,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kRows = kManyRows;
-constexpr int kMetaRing = 8;
-constexpr int kStages = 4;  // staged code tiles: K and V of two steps
+constexpr int kMetaRing = 16;
 constexpr int kMetaInts = 16;
 constexpr int kMinRun = 4;  // steps
 constexpr float kPShift = 7.f;
@@ -54,39 +53,51 @@ enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16,
 
 template <int D>
 struct Layout {
+  // S regions in TMEM, operand slots of K and of V: with d = 64 the accumulators leave
+  // room for a third region, and the way from a step's P over its products to the S
+  // that reuses its region is spread over three steps
+  static constexpr int R = D == 64 ? 3 : 2;
+  static constexpr int kStages = 2 * R;      // staged code tiles: K and V of R steps
   static constexpr int kTile = 128 * D * 2;  // fp16 operand tile
   static constexpr int kCodes = 128 * D;     // codes of a step, K or V
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + kTile;
-  static constexpr int kV = kK + 2 * kTile;
-  static constexpr int kStage = kV + 2 * kTile;
+  static constexpr int kV = kK + R * kTile;
+  static constexpr int kStage = kV + R * kTile;
   static constexpr int kMeta = kStage + kStages * kCodes;
   static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
   static constexpr int kBar = kWords + (kLineWords + 4) * 4;
-  static constexpr int kNumBars = 2 * kStages + kMetaRing + 4 * 3 + 3;
+  static constexpr int kNumBars = 2 * kStages + kMetaRing + 5 * R + 3;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kBytes = kTmemSlot + 16;
 };
-static_assert(Layout<128>::kBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(Layout<128>::kBytes <= 227 * 1024 && Layout<64>::kBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(kMetaRing > 3 * Layout<64>::R, "see where an entry is written");
 static_assert(Layout<128>::kBar % 8 == 0 && Layout<64>::kBar % 8 == 0, "barriers are 8-byte aligned");
 
+template <int R>
 struct Bars {
+  static constexpr int kStages = 2 * R, kFirst = 2 * kStages + kMetaRing;
   uint32_t base;
   __device__ uint32_t at(int i) const { return base + 8 * i; }
   __device__ uint32_t stage_full(int s) const { return at(s); }                // bytes
   __device__ uint32_t stage_empty(int s) const { return at(kStages + s); }     // 2 conversion warps
   __device__ uint32_t meta(int s) const { return at(2 * kStages + s); }        // 1
-  __device__ uint32_t k_ready(int s) const { return at(2 * kStages + kMetaRing + s); }       // 2
-  __device__ uint32_t v_ready(int s) const { return at(2 * kStages + kMetaRing + 2 + s); }   // 2
-  __device__ uint32_t s_full(int g) const { return at(2 * kStages + kMetaRing + 4 + g); }    // commit
-  __device__ uint32_t p_full(int g) const { return at(2 * kStages + kMetaRing + 6 + g); }    // 8
-  __device__ uint32_t pv_done(int g) const { return at(2 * kStages + kMetaRing + 8 + g); }   // commit
-  __device__ uint32_t q_full() const { return at(2 * kStages + kMetaRing + 10); }            // 8
-  __device__ uint32_t o_free() const { return at(2 * kStages + kMetaRing + 11); }            // 8
-  __device__ uint32_t softmax() const { return at(2 * kStages + kMetaRing + 12); }           // 8
+  __device__ uint32_t k_ready(int g) const { return at(kFirst + g); }          // 2
+  __device__ uint32_t v_ready(int g) const { return at(kFirst + R + g); }      // 2
+  __device__ uint32_t s_full(int g) const { return at(kFirst + 2 * R + g); }   // commit
+  __device__ uint32_t p_full(int g) const { return at(kFirst + 3 * R + g); }   // 8
+  __device__ uint32_t pv_done(int g) const { return at(kFirst + 4 * R + g); }  // commit
+  __device__ uint32_t q_full() const { return at(kFirst + 5 * R); }            // 8
+  __device__ uint32_t o_free() const { return at(kFirst + 5 * R + 1); }        // 8
+  __device__ uint32_t softmax() const { return at(kFirst + 5 * R + 2); }       // 8
 };
 
-__device__ __forceinline__ uint32_t col_o(int w) { return 256u + 128u * static_cast<uint32_t>(w); }
+// TMEM columns of accumulator w, behind the S regions.
+template <int D>
+__device__ __forceinline__ uint32_t col_o(int w) {
+  return 128u * Layout<D>::R + D * static_cast<uint32_t>(w);
+}
 
 // Instruction descriptor, kind::f16 with fp16 A and B (format code 0), both K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
@@ -127,6 +138,7 @@ constexpr __host__ __device__ int part_floats(int D) { return kRows * D + 3 * kR
 template <int D, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const CacheFwdParams p, const Geometry geo) {
   using L = Layout<D>;
+  constexpr int R = L::R, kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nseg = p.B * p.c.Hk * geo.RT;
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
     return;
   }
   const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
-  const Bars bar{smem_u32(smem + L::kBar)};
+  const Bars<R> bar{smem_u32(smem + L::kBar)};
   int* words = reinterpret_cast<int*>(smem + L::kWords);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   const int* meta_at = reinterpret_cast<const int*>(smem + L::kMeta);
@@ -150,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
     const int i = tid - 2 * kStages - kMetaRing;
     int n = 1;
     if (tid >= kStages && tid < 2 * kStages) n = 2;
-    if (i >= 0 && i < 4) n = 2;
-    if (i == 6 || i == 7 || i >= 10) n = 8;
+    if (i >= 0 && i < 2 * R) n = 2;
+    if ((i >= 3 * R && i < 4 * R) || i >= 5 * R) n = 8;
     mbar_init(bar.at(tid), n);
     fence_barrier_init();
   }
@@ -230,9 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           m[kParts] = parts;
           ok = slot_free(2 * done);
           if (ok) {
-            // entry J % 8 was last read for step J - 8, which every role has left: the K codes
-            // of step J - 2 are converted, so S of step J - 4 and P V of step J - 6 are done,
-            // and V of step J - 6 with them
+            // the entry was last read for step J - kMetaRing, which every role has left: the K
+            // codes of step J - R are converted, so S of step J - 2 R and P V of step J - 3 R
+            // are done, and V of step J - 3 R with them
             int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + (done % kMetaRing) * (kMetaInts / 4);
 #pragma unroll
             for (int i = 0; i < kMetaInts / 4; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
@@ -283,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       for (int J = 0;; ++J) {
         const int flags = step_flags(J);
         if (flags & kEnd) break;
-        const int g = J & 1;
-        // Q of the piece; the products of step J - 2, which read this region; K
+        const int g = J % R;
+        // Q of the piece; the products of step J - R, which read this region; K
         if ((flags & kFirstStep) && !cache_wait(bar.q_full(), pieces++ & 1, p.status)) break;
-        if (J >= 2 && !cache_wait(bar.pv_done(g), ((J >> 1) - 1) & 1, p.status)) break;
-        if (!cache_wait(bar.k_ready(g), (J >> 1) & 1, p.status)) break;
+        if (J >= R && !cache_wait(bar.pv_done(g), (J / R - 1) & 1, p.status)) break;
+        if (!cache_wait(bar.k_ready(g), (J / R) & 1, p.status)) break;
         tc_fence_after();
         const uint64_t kd = dk + static_cast<uint64_t>((g * L::kTile) >> 4);
 #pragma unroll
@@ -307,20 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       for (int J = 0;; ++J) {
         const int flags = step_flags(J);
         if (flags & kEnd) break;
-        const int g = J & 1;
+        const int g = J % R;
         const bool first = flags & kFirstStep;
-        if (!cache_wait(bar.v_ready(g), (J >> 1) & 1, p.status)) break;
+        if (!cache_wait(bar.v_ready(g), (J / R) & 1, p.status)) break;
         // the piece's first products overwrite the accumulators of the piece before
         if (first && pieces > 0 && !cache_wait(bar.o_free(), (pieces - 1) & 1, p.status)) break;
         pieces += first;
-        if (!cache_wait(bar.p_full(g), (J >> 1) & 1, p.status)) break;
+        if (!cache_wait(bar.p_full(g), (J / R) & 1, p.status)) break;
         tc_fence_after();
         const uint64_t vd = dv + static_cast<uint64_t>((g * L::kTile) >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + col_o(w), tmem + 128 * g + 64 * w + 8 * kk,
+            mma_ts(tmem + col_o<D>(w), tmem + 128 * g + 64 * w + 8 * kk,
                    vd + static_cast<uint64_t>((w * D * 128 + kk * 32) >> 4), idesc, !first || kk > 0);
         mma_commit(bar.pv_done(g));
       }
@@ -342,11 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       const int* m = meta_at + (J % kMetaRing) * kMetaInts;
       if (m[kFlags] & kEnd) break;
       const int valid[2] = {m[kPageWords + kValid], m[kPageWords + 4 + kValid]};
-      const int g = J & 1, slot = (2 * J + kv) % kStages;
-      // the operand slot is free once the products of step J - 2 have read it
+      const int g = J % R, slot = (2 * J + kv) % kStages;
+      // the operand slot is free once the products of step J - R have read it
       const uint32_t freed = kv ? bar.pv_done(g) : bar.s_full(g);
       ok = cache_wait(bar.stage_full(slot), ((2 * J + kv) / kStages) & 1, p.status) &&
-           (J < 2 || cache_wait(freed, ((J >> 1) - 1) & 1, p.status));
+           (J < R || cache_wait(freed, (J / R - 1) & 1, p.status));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint8_t* codes = smem + L::kStage + slot * L::kCodes + row0 * row_bytes + 16 * pc;
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           ok = __all_sync(0xffffffffu, cache_wait(bar.meta(J % kMetaRing), (J / kMetaRing) & 1, p.status));
           if (!ok) break;
         }
-        const int g = J & 1;
+        const int g = J % R;
         flags = meta_at[(J % kMetaRing) * kMetaInts + kFlags];
         const int4 pw = *reinterpret_cast<const int4*>(meta_at + (J % kMetaRing) * kMetaInts + kPageWords + 4 * w);
         const int j0 = pw.x;
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
         const float c = fmaxf(crow * __int_as_float(pw.y), 1.17549435e-38f);
         const float lvs = __int_as_float(pw.z);
         const bool masked = j0 < 0 || j0 + kPage > all_lim || (flags & (kCut << w));
-        ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J >> 1) & 1, p.status));
+        ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J / R) & 1, p.status));
         if (!ok) break;
         if (warp_live) {
           tc_fence_after();
@@ -524,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
           tmem_st32p(tmem + lane_base + 128 * g + 64 * w, pk);
           if (__builtin_expect(!first && __any_sync(0xffffffffu, rescale), 0)) {
             // O_w is rescaled once the products of step J - 1 have completed
-            ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g ^ 1), ((J - 1) >> 1) & 1, p.status));
+            ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done((J - 1) % R), ((J - 1) / R) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
             const float alpha = rescale ? ex2(mv_old - mv) : 1.f;
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) tmem_scale32(tmem + lane_base + col_o(w) + 32 * ch, alpha);
+            for (int ch = 0; ch < D / 32; ++ch) tmem_scale32(tmem + lane_base + col_o<D>(w) + 32 * ch, alpha);
           }
           tmem_st_wait();
         }
@@ -541,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       if (!ok) break;
 
       // ---- the piece's end: the two halves' states are merged
-      const int g = J & 1;
-      ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g), (J >> 1) & 1, p.status));
+      const int g = J % R;
+      ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done(g), (J / R) & 1, p.status));
       ++J;
       if (!ok) break;
       tc_fence_after();
@@ -565,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
         for (int ch = 0; ch < D / 64; ++ch) {
           uint32_t va[32], vb[32];
           const uint32_t col = w * (D / 2) + 32 * ch;
-          tmem_ld32(tmem + lane_base + col_o(0) + col, va);
-          tmem_ld32(tmem + lane_base + col_o(1) + col, vb);
+          tmem_ld32(tmem + lane_base + col_o<D>(0) + col, va);
+          tmem_ld32(tmem + lane_base + col_o<D>(1) + col, vb);
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(va[i]) * f0 + __uint_as_float(vb[i]) * f1;
