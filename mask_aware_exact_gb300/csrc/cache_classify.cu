@@ -3,11 +3,10 @@
 // row tile, the list of the pages that some row sees, in order, each with a bit that
 // says whether intervals hide some of its keys from some row, and their number.
 //
-// Latency-bound: 8 or 16 bytes of bounds per cached token. A cluster of eight CTAs
-// shares a row tile, each taking an eighth of the pages; the counts that place a CTA's
-// part of the list come from the others' shared memory. 8 sequences of 131072 tokens:
-// 8.7 us with cold caches, like one CTA for every 32 pages with a counter in global
-// memory, but without its scratch words.
+// Latency-bound: 8 or 16 bytes of bounds per cached token. A CTA of 1024 threads takes
+// 8192 keys a pass; longer tables are shared by a cluster of up to eight CTAs, whose
+// counts, which place a CTA's part of the list, come from the others' shared memory.
+// 8 sequences of 131072 tokens: 8.7 us with cold caches.
 #include "cache_common.cuh"
 #include "flashmask.h"
 
@@ -15,8 +14,9 @@ namespace fm {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8;
-constexpr int kWordsMost = FM_MAX_SEQLEN / kPage / 32 / kCluster;  // 32-page words of a CTA
+constexpr int kClusterMost = 8;
+constexpr int kWordsMost = FM_MAX_SEQLEN / kPage / 32 / kClusterMost;  // 32-page words of a CTA
+constexpr int kWordsPass = kThreads * 8 / (32 * kPage);                // words of one pass
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -38,15 +38,15 @@ __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
 // A key is hidden from the whole tile, positions [lo, hi], if the union of its
 // intervals (and of the rows above it, when causal) covers them. A thread takes 8 keys
 // at a time, so a page is 8 lanes and a warp takes groups of 4 pages.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    cache_classify(const CacheFwdParams p, const Geometry geo) {
+__global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams p, const Geometry geo,
+                                                            const int cluster) {
   __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
   __shared__ int before[kWordsMost];  // visible pages of this CTA before a word
   __shared__ int count;               // visible pages of this CTA
-  const int tile = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = blockIdx.y;
+  const int tile = blockIdx.x / cluster, rank = blockIdx.x - tile * cluster, b = blockIdx.y;
   const int cls = tile / geo.RT, rt = tile - cls * geo.RT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int each = (geo.words + kCluster - 1) / kCluster;
+  const int each = (geo.words + cluster - 1) / cluster;
   const int w0 = rank * each, words = max(0, min(each, geo.words - w0));  // words [w0, w0 + words)
   const RowTile r = row_tile(p, geo, b, rt, blockIdx.x == 0 && tid == 0);
   const int lo = r.shift + r.t_lo, hi = r.shift + r.t_hi;
@@ -134,8 +134,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   cluster_sync();
   // this CTA's place in the list, and the whole
   int mine = 0, total = 0;
-#pragma unroll
-  for (int k = 0; k < kCluster; ++k) {
+  for (int k = 0; k < cluster; ++k) {
     const int x = of_cta(&count, k);
     if (k < rank) mine += x;
     total += x;
@@ -156,10 +155,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(kCluster) * static_cast<unsigned>(geo.classes * geo.RT),
-                  static_cast<unsigned>(p.B));
-  cache_classify<<<grid, kThreads, 0, s>>>(p, geo);
-  return cudaGetLastError();
+  int cluster = 1;
+  while (cluster < kClusterMost && cluster * kWordsPass < geo.words) cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * static_cast<unsigned>(geo.classes * geo.RT),
+                     static_cast<unsigned>(p.B));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_classify, p, geo, cluster);
 }
 
 }  // namespace fm
