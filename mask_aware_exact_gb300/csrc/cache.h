@@ -70,13 +70,30 @@ struct CacheFwdParams {
                         // hide some key of the page from some row
   int32_t* listed;      // [row tiles]: their number
 };
+// n / d for 0 <= n < 2^31 by a multiplication: mul = ceil(2^(31 + s) / d) with 2^s >= d,
+// n / d = (n * mul) >> (31 + s) (the excess, below n * 2^-31-s, is less than 1 / d).
+struct Divisor {
+  uint32_t d, mul, shift;
+  __host__ void set(int divisor) {
+    d = static_cast<uint32_t>(divisor);
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    mul = static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d);
+    shift = s;
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> 31 >> shift);
+  }
+};
 // Rows of the attention's work. The G = H / Hk query heads of a cache head and a
 // sequence's query tokens form one list of rows, r = t * G + g, cut into RT tiles.
 struct Geometry {
   int G, rows, RT;  // query heads per cache head, rows of a tile, row tiles
   int classes;      // mask classes: cache heads whose rows see the same masks share one
   int words;        // 32-bit words of page bits
+  Divisor by_G, by_RT, by_Hk, by_class, by_mask;  // G, RT, Hk, Hk / classes, H / Hm
 };
+
 // Byte offsets of the workspace regions.
 struct CacheWs {
   size_t arrived, partial, list, listed, total;

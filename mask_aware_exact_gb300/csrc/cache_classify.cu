@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   __shared__ int before[kWordsMost];  // visible pages of this CTA before a word
   __shared__ int count;               // visible pages of this CTA
   const int tile = blockIdx.x / cluster, rank = blockIdx.x - tile * cluster, b = blockIdx.y;
-  const int cls = tile / geo.RT, rt = tile - cls * geo.RT;
+  const int cls = geo.by_RT.div(tile), rt = tile - cls * geo.RT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int each = (geo.words + cluster - 1) / cluster;
   const int w0 = rank * each, words = max(0, min(each, geo.words - w0));  // words [w0, w0 + words)

@@ -24,21 +24,22 @@ __device__ __forceinline__ RowTile row_tile(const CacheFwdParams& p, const Geome
     r.len = min(max(r.len, 0), most);
   }
   r.shift = r.len - r.live;
-  const uint32_t G = geo.G, rows = G * r.live, r0 = static_cast<uint32_t>(rt) * geo.rows;
-  r.t_lo = static_cast<int>(r0 / G);
-  r.t_hi = r0 < rows ? static_cast<int>(min(r0 + geo.rows - 1, rows - 1) / G) : r.t_lo - 1;
+  const int rows = geo.G * r.live, r0 = rt * geo.rows;
+  r.t_lo = geo.by_G.div(r0);
+  r.t_hi = r0 < rows ? geo.by_G.div(r0 + min(geo.rows, rows - r0) - 1) : r.t_lo - 1;
   return r;
 }
 
 __device__ __forceinline__ int mask_class(const CacheFwdParams& p, const Geometry& geo, int hk) {
-  return geo.classes == p.c.Hk ? hk : hk / (p.c.Hk / geo.classes);
+  return geo.by_class.div(hk);
 }
 
-// Pages on a segment's line.
+// Pages on a segment's line. (Not inline, like everything here that is not in a hot
+// loop: a run that is short spends much of its time on fetching instructions.)
 template <bool kVec>
-__device__ __forceinline__ int pages_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
-  const int bh = seg / geo.RT, rt = seg - bh * geo.RT;
-  const int b = bh / p.c.Hk;
+static __device__ __noinline__ int pages_of(const CacheFwdParams& p, const Geometry& geo, int seg) {
+  const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT;
+  const int b = geo.by_Hk.div(bh);
   if constexpr (kVec) {
     const int cls = mask_class(p, geo, bh - b * p.c.Hk);
     const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;

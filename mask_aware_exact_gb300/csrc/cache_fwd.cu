@@ -154,7 +154,7 @@ __device__ __forceinline__ void store_lse(const CacheFwdParams& p, const Geometr
                                           int rows, bool mine, const float (&m)[2], const float (&l)[2]) {
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int tok = (r0 + e) / geo.G, h = hk * geo.G + r0 + e - tok * geo.G;
+    const int tok = geo.by_G.div(r0 + e), h = hk * geo.G + r0 + e - tok * geo.G;
     if (mine && r0 + e < rows)
       p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(m[e], l[e]);
   }
@@ -255,7 +255,7 @@ struct FragmentSums {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const float f0 = out_factor(m[t][0], mv[t][0], l[t][0], kPShift), f1 = out_factor(m[t][1], mv[t][1], l[t][1], kPShift);
-      const int rr = r0 + 8 * t + g, tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+      const int rr = r0 + 8 * t + g, tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
       uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;
 #pragma unroll
       for (int q = 0; q < kMine; ++q) {
@@ -272,8 +272,9 @@ struct FragmentSums {
   }
 };
 
-// Bits of the keys at[i], at[i + 2], .. at[i + 14] (i = odd) with s <= pos < e.
-__device__ __forceinline__ uint32_t hidden8(const int32_t* s, const int32_t* e, int pos, int odd) {
+// Bits of the keys at[i], at[i + 2], .. at[i + 14] (i = odd) with s <= pos < e. (Not
+// inline: most pages need no look at the mask's words, and the loop stays small.)
+static __device__ __noinline__ uint32_t hidden8(const int32_t* s, const int32_t* e, int pos, int odd) {
   uint32_t hid = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -285,7 +286,8 @@ __device__ __forceinline__ uint32_t hidden8(const int32_t* s, const int32_t* e, 
 }
 
 template <int D, int NT, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdParams p, const Geometry geo) {
+__global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p,
+                                                                 const __grid_constant__ Geometry geo) {
   using S = Smem<D, NT>;
   constexpr int kRows = S::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       int page = -1, logical = 0, cut = 0;
       size_t ph = 0;
       if (live) {
-        const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+        const int bh = geo.by_RT.div(my_seg), rt = my_seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
         logical = page_on_line<kVec>(p, geo, b, hk, rt, my_k, cut);
         page = p.table[static_cast<size_t>(b) * p.max_pages + logical];
         if (page < 0 || page >= p.c.pages) {
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
     if (lane == 0) mbar_arrive(bar.piece_empty(e));
     if (count == 0) break;
 
-    const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
     const RowTile r = row_tile(p, geo, b, rt, lane == 0 && warp == 0);
     const int rows = geo.G * r.live;
     State<D, NT> st;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       // still on its way)
       const int rr = rt * kRows + 8 * t + g;
       const bool there = rr < geo.G * p.N, live = rr < rows;
-      const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+      const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
       uint4 x[D / 64][2];
       const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
 #pragma unroll
@@ -508,11 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
       for (int e = 0; e < 2; ++e) {
         crow[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
         const int r2 = rt * kRows + 8 * t + 2 * c + e;
-        const int tok2 = r2 / geo.G, h2 = hk * geo.G + r2 - tok2 * geo.G;
+        const int tok2 = geo.by_G.div(r2), h2 = hk * geo.G + r2 - tok2 * geo.G;
         pos[t][e] = r.shift + tok2;
         lim[t][e] = r2 < rows && p.mask.causal ? min(r.len, pos[t][e] + 1) : r.len;
         all_lim = min(all_lim, lim[t][e]);
-        mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + min(h2, p.H - 1) / (p.H / p.mask.Hm)) *
+        mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h2)) *
                                 static_cast<size_t>(p.max_pages * kPage)
                           : 0;
       }
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
         const float f0 = out_factor(st.m[t][0], st.mv[t][0], st.l[t][0], kPShift);
         const float f1 = out_factor(st.m[t][1], st.mv[t][1], st.l[t][1], kPShift);
         const int rr = rt * kRows + 8 * t + g;  // the row this lane holds after the transposes
-        const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+        const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
         uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;
 #pragma unroll
         for (int n = 0; n < D / 16; ++n)
@@ -810,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   for (int j = 0; ok && j < 2; ++j) {
     if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
     const int seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
-    const int bh = seg / geo.RT, rt = seg - bh * geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
     const int rows = geo.G * row_tile(p, geo, b, rt, false).live;
     FragmentSums<D, NT> f;
     f.clear();
@@ -831,11 +833,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const CacheFwdPa
   // segments without a visible page: O = 0, LSE = -inf
   for (int seg = blockIdx.x + gridDim.x * warp; ok && line.any_empty && seg < nseg; seg += gridDim.x * kConsumers) {
     if (pages_of<kVec>(p, geo, seg) != 0) continue;
-    const int rt = seg % geo.RT, bh = seg / geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+    const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
     const RowTile r = row_tile(p, geo, b, rt, lane == 0);
     const int row_hi = min(geo.G * r.live, (rt + 1) * kRows);
     for (int rr = rt * kRows; rr < row_hi; ++rr) {
-      const int t = rr / geo.G, h = hk * geo.G + rr % geo.G;
+      const int t = geo.by_G.div(rr), h = hk * geo.G + rr - t * geo.G;
       uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + t * p.os[2];
       for (int k = lane; k < D / 2; k += 32) *reinterpret_cast<uint32_t*>(o + 2 * k) = 0u;
       if (lane == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + t] = -INFINITY;
@@ -889,6 +891,11 @@ Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
   g.RT = (rows - 1) / g.rows + 1;
   g.classes = Hk % Hm == 0 ? Hm : Hk;
   g.words = (max_pages + 31) / 32;
+  g.by_G.set(g.G);
+  g.by_RT.set(g.RT);
+  g.by_Hk.set(Hk);
+  g.by_class.set(Hk / g.classes);
+  g.by_mask.set(H / Hm);
   return g;
 }
 

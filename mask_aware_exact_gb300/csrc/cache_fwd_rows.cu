@@ -136,7 +136,8 @@ __device__ __forceinline__ void tmem_scale32(uint32_t taddr, float f) {
 constexpr __host__ __device__ int part_floats(int D) { return kRows * D + 3 * kRows; }
 
 template <int D, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const CacheFwdParams p, const Geometry geo) {
+__global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __grid_constant__ CacheFwdParams p,
+                                                                     const __grid_constant__ Geometry geo) {
   using L = Layout<D>;
   constexpr int R = L::R, kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       int page[2] = {-1, -1}, j0[2] = {-1, -1}, valid[2] = {0, 0}, cut[2] = {0, 0};
       float ks[2] = {0.f, 0.f}, lvs[2] = {0.f, 0.f};
       if (lane < avail) {
-        const int bh = my_seg / geo.RT, rt = my_seg % geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+        const int bh = geo.by_RT.div(my_seg), rt = my_seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
         const int pages = pages_of<kVec>(p, geo, my_seg);
         const RowTile r = row_tile(p, geo, b, rt, true);
 #pragma unroll
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
             for (int i = 0; i < kMetaInts / 4; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
             mbar_arrive(bar.meta(done % kMetaRing));
           }
-          const int hk = (sg / geo.RT) % p.c.Hk;
+          const int bh = geo.by_RT.div(sg), hk = bh - geo.by_Hk.div(bh) * p.c.Hk;
           const uint32_t bytes = (pg[0] >= 0 ? L::kCodes / 2 : 0) + (pg[1] >= 0 ? L::kCodes / 2 : 0);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
@@ -421,18 +422,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
       const bool whole = head[kFlags] & kWhole;
       const int slot = head[kFlags] & kTailSlot ? 1 : 0;
       // this thread's row, and Q: columns [w D/2, w D/2 + D/2) of it
-      const int bh = seg / geo.RT, rt = seg - bh * geo.RT, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+      const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
       const RowTile r = row_tile(p, geo, b, rt, tid == 0);
       const int rows = geo.G * r.live;
       const int rr = rt * kRows + row;
       const bool live = rr < rows;
       const bool warp_live = __any_sync(0xffffffffu, live);
-      const int tok = rr / geo.G, h = hk * geo.G + rr - tok * geo.G;
+      const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
       const int pos = r.shift + tok;
       const int lim = live && p.mask.causal ? min(r.len, pos + 1) : r.len;
       const int all_lim = __reduce_min_sync(0xffffffffu, lim);  // keys that every row of the warp sees
       const size_t mrow =
-          kVec ? (static_cast<size_t>(b) * p.mask.Hm + h / (p.H / p.mask.Hm)) * static_cast<size_t>(p.max_pages * kPage) : 0;
+          kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h)) * static_cast<size_t>(p.max_pages * kPage) : 0;
       uint4 x[D / 16];
       const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + w * (D / 2);
       uint32_t top = 0;
@@ -668,11 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const Cache
     // segments without a visible page: O = 0, LSE = -inf
     for (int sg = blockIdx.x; ok && line.any_empty && sg < nseg; sg += gridDim.x) {
       if (steps_of<kVec>(p, geo, sg) != 0) continue;
-      const int rt2 = sg % geo.RT, bh = sg / geo.RT, b2 = bh / p.c.Hk, hk2 = bh - b2 * p.c.Hk;
+      const int bh = geo.by_RT.div(sg), rt2 = sg - bh * geo.RT, b2 = geo.by_Hk.div(bh), hk2 = bh - b2 * p.c.Hk;
       const RowTile r = row_tile(p, geo, b2, rt2, tid == 0);
       const int row_hi = min(geo.G * r.live, (rt2 + 1) * kRows);
       for (int rr = rt2 * kRows + warp; rr < row_hi; rr += 8) {
-        const int t = rr / geo.G, hh = hk2 * geo.G + rr - t * geo.G;
+        const int t = geo.by_G.div(rr), hh = hk2 * geo.G + rr - t * geo.G;
         uint16_t* o = p.o + b2 * p.os[0] + hh * p.os[1] + t * p.os[2];
         for (int i = lane; i < D / 2; i += 32) *reinterpret_cast<uint32_t*>(o + 2 * i) = 0u;
         if (lane == 0) p.lse[(static_cast<size_t>(b2) * p.H + hh) * p.N + t] = -INFINITY;
