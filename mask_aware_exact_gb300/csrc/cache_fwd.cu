@@ -48,14 +48,9 @@
 namespace fm {
 namespace {
 
-constexpr int kConsumers = 7;  // with the producer 8 warps: two for each scheduler, 255 registers a thread
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kSlots = 3;      // ring slots of a consumer warp
-constexpr int kPieceRing = 16;  // piece descriptors in flight: more than twice what a group can start
-constexpr int kBatch = 4 * kConsumers;  // tiles looked up at a time, one per lane
-// Pages a run has at least: one for each consumer warp. Shorter runs only
-// add partial results.
-constexpr int kMinRun = kConsumers;
+// Consumer warps and the ring slots of each.
+constexpr __host__ __device__ int consumers(int D, int NT) { return D == 64 || NT == 1 ? 11 : 7; }
+constexpr __host__ __device__ int slots(int D, int NT) { return D == 128 && NT == 1 ? 2 : 3; }
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 
 // ---------------------------------------------------------------- instructions
@@ -66,8 +61,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t* at, int x) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(x) : "memory");
+  return old;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 template <int D, int NT>
 struct Smem {
+  static constexpr int kConsumers = consumers(D, NT), kSlots = slots(D, NT);
+  static constexpr int kThreads = 32 * (kConsumers + 1);
+  static constexpr int kPieceRing = 2 * kConsumers + 2;  // piece descriptors: more than two groups start
+  static constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a time, one per lane
   static constexpr int kRows = 8 * NT;
   static constexpr int kFrags = D / 16 * NT;  // accumulator fragments (four floats a lane) of a warp
   static constexpr int kHalf = kPage * D;  // bytes of a page's K or V
@@ -82,8 +93,11 @@ struct Smem {
   static constexpr int kBytes = kScan + (kLineWords + 12) * 4;
 };
 static_assert(Smem<128, 2>::kBytes <= 227 * 1024 && Smem<64, 2>::kBytes <= 227 * 1024, "shared memory per CTA");
+static_assert(Smem<128, 1>::kBytes <= 227 * 1024 && Smem<64, 1>::kBytes <= 227 * 1024, "shared memory per CTA");
 
+template <typename S>
 struct Bars {
+  static constexpr int kConsumers = S::kConsumers, kSlots = S::kSlots, kPieceRing = S::kPieceRing;
   uint32_t base;
   __device__ uint32_t full(int w, int s) const { return base + 8 * (w * kSlots + s); }
   __device__ uint32_t empty(int w, int s) const { return base + 8 * ((kConsumers + w) * kSlots + s); }
@@ -149,88 +163,85 @@ struct State {
   }
 };
 
-// LSE of the rows r0 and r0 + 1 of a lane.
-__device__ __forceinline__ void store_lse(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0,
-                                          int rows, bool mine, const float (&m)[2], const float (&l)[2]) {
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int tok = geo.by_G.div(r0 + e), h = hk * geo.G + r0 + e - tok * geo.G;
-    if (mine && r0 + e < rows)
-      p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(m[e], l[e]);
-  }
-}
-
 // Sums of states, each warp its share of the fragments: warp, warp + kConsumers, ..
+// A lane looks after the statistics of row lane % kRows: of all states together in m,
+// mv and (a share of) l.
 template <int D, int NT>
 struct FragmentSums {
+  static constexpr int kConsumers = consumers(D, NT), kRows = 8 * NT;
   static constexpr int kFrags = D / 16 * NT, kMine = (kFrags + kConsumers - 1) / kConsumers;
+  static constexpr int kAtOnce = 32 / kRows, kSteps = (kConsumers + kAtOnce - 1) / kAtOnce;
   float acc[kMine][4];
-  float m[NT][2], mv[NT][2], l[NT][2];  // of all rows of the lane
+  float m, mv, l;
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int q = 0; q < kMine; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[t][e] = mv[t][e] = -INFINITY, l[t][e] = 0.f;
+    m = mv = -INFINITY;
+    l = 0.f;
   }
-  // Adds n (at most kMost) states in order: stats(k) points to m, mv, l [8 NT] of state
-  // k, frags(k) to this lane's part of its fragment 0. The loads of all of them are
-  // issued before the first is used.
-  template <int kMost, typename Stats, typename Frags, typename Load>
-  __device__ __forceinline__ void add(int n, int warp, Stats stats, Frags frags, int c, Load load) {
-    float x[kMost][NT][6];
-    float4 v[kMost][kMine];
+  // Row of element e of this lane in the warp's fragment q.
+  __device__ __forceinline__ static int row_of(int q, int e, int warp, int lane) {
+    return (NT == 2 ? 8 * ((warp + kConsumers * q) & 1) : 0) + 2 * (lane & 3) + e;
+  }
+  // Adds n states of the merge area in order, from + k modulo kConsumers.
+  __device__ __forceinline__ void add(int n, int from, const float4* merge, const float* stats, int warp, int lane) {
+    auto place = [&](int k) { return from + k < kConsumers ? from + k : from + k - kConsumers; };
+    // states lane / kRows, + kAtOnce, ..
+    float xm[kSteps], xv[kSteps], xl[kSteps];
+    float mm = m, mmv = mv;
 #pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-      const float* st = stats(min(k, n - 1)) + 2 * c;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int q = 0; q < 6; ++q) x[k][t][q] = load(st + 8 * t + (q >> 1) * 8 * NT + (q & 1));
-      const float4* fr = frags(min(k, n - 1));
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) v[k][q] = load(fr + min(warp + kConsumers * q, kFrags - 1) * 32);
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = lane / kRows + kAtOnce * i;
+      const float* x = stats + 3 * kRows * place(min(k, n - 1)) + lane % kRows;
+      xm[i] = x[0], xv[i] = x[kRows], xl[i] = k < n ? x[2 * kRows] : 0.f;
+      mm = fmaxf(mm, xm[i]);
+      mmv = fmaxf(mmv, xv[i]);
     }
-    float old[NT][2], f[kMost][NT][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int o = kRows; o < 32; o <<= 1) {
+      mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+      mmv = fmaxf(mmv, __shfl_xor_sync(0xffffffffu, mmv, o));
+    }
+    l *= ex2_diff(m, mm);
+    const float old = ex2_diff(mv, mmv);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mm = m[t][e], mmv = mv[t][e];
+    for (int i = 0; i < kSteps; ++i) {
+      l += xl[i] * ex2_diff(xm[i], mm);
+      xv[i] = lane / kRows + kAtOnce * i < n ? ex2_diff(xv[i], mmv) : 0.f;
+    }
+    m = mm;
+    mv = mmv;
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-          if (k < n) mm = fmaxf(mm, x[k][t][e]), mmv = fmaxf(mmv, x[k][t][2 + e]);
-        }
-        old[t][e] = ex2_diff(mv[t][e], mmv);
-        l[t][e] *= ex2_diff(m[t][e], mm);
+    for (int q = 0; q < kMine; ++q)
 #pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-          f[k][t][e] = ex2_diff(x[k][t][2 + e], mmv);
-          if (k < n) l[t][e] += x[k][t][4 + e] * ex2_diff(x[k][t][e], mm);
-        }
-        m[t][e] = mm;
-        mv[t][e] = mmv;
-      }
+      for (int i = 0; i < 4; ++i) acc[q][i] *= __shfl_sync(0xffffffffu, old, row_of(q, i & 1, warp, lane));
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      // kConsumers is odd: the rows of a warp's fragments alternate when NT is 2
-      const bool t1 = NT == 2 && ((warp + kConsumers * q) & 1);
+    for (int i = 0; i < kSteps; ++i) {
+      if (kAtOnce * i >= n) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[q][i] *= t1 ? old[NT - 1][i & 1] : old[0][i & 1];
+      for (int j = 0; j < kAtOnce; ++j) {
+        const float4* fr = merge + place(min(kAtOnce * i + j, n - 1)) * kFrags * 32 + lane;  // times 0 behind the last
 #pragma unroll
-      for (int k = 0; k < kMost; ++k) {
-        if (k < n) {
-          const float f0 = t1 ? f[k][NT - 1][0] : f[k][0][0], f1 = t1 ? f[k][NT - 1][1] : f[k][0][1];
-          acc[q][0] += v[k][q].x * f0;
-          acc[q][1] += v[k][q].y * f1;
-          acc[q][2] += v[k][q].z * f0;
-          acc[q][3] += v[k][q].w * f1;
+        for (int q = 0; q < kMine; ++q) {
+          const float f0 = __shfl_sync(0xffffffffu, xv[i], kRows * j + row_of(q, 0, warp, lane));
+          const float f1 = __shfl_sync(0xffffffffu, xv[i], kRows * j + row_of(q, 1, warp, lane));
+          const float4 v = fr[min(warp + kConsumers * q, kFrags - 1) * 32];
+          acc[q][0] += v.x * f0;
+          acc[q][1] += v.y * f1;
+          acc[q][2] += v.z * f0;
+          acc[q][3] += v.w * f1;
         }
       }
     }
+  }
+  // The whole sum of P of the lane's row.
+  __device__ __forceinline__ float sum() const {
+    float x = l;
+#pragma unroll
+    for (int o = kRows; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
   }
   // The sums as a state (see State::put).
   __device__ __forceinline__ void put(float4* frags, float* stats, int warp, int lane) const {
@@ -238,36 +249,30 @@ struct FragmentSums {
     for (int q = 0; q < kMine; ++q)
       if (warp + kConsumers * q < kFrags)
         frags[(warp + kConsumers * q) * 32 + lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
-    if (warp == 0 && lane < 4) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float* x = stats + 8 * t + 2 * lane + e;
-          x[0] = m[t][e], x[8 * NT] = mv[t][e], x[16 * NT] = l[t][e];
-        }
-    }
+    const float x = sum();
+    if (warp == 0 && lane < kRows) stats[lane] = m, stats[kRows + lane] = mv, stats[2 * kRows + lane] = x;
   }
   // O and LSE of the row tile that begins at row r0.
   __device__ __forceinline__ void store(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0, int rows,
                                         int warp, int lane) const {
     const int g = lane >> 2, c = lane & 3;
+    const float x = sum(), f = out_factor(m, mv, x, kPShift);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float f0 = out_factor(m[t][0], mv[t][0], l[t][0], kPShift), f1 = out_factor(m[t][1], mv[t][1], l[t][1], kPShift);
-      const int rr = r0 + 8 * t + g, tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
-      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;
+    for (int q = 0; q < kMine; ++q) {
+      const int fr = warp + kConsumers * q;
+      const float f0 = __shfl_sync(0xffffffffu, f, row_of(q, 0, warp, lane));
+      const float f1 = __shfl_sync(0xffffffffu, f, row_of(q, 1, warp, lane));
+      const int rr = r0 + 8 * (fr % NT) + g, tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
+      uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c + fr / NT * 16;
 #pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        const int fr = warp + kConsumers * q;
-        if (fr >= kFrags || fr % NT != t) continue;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t v = transpose8x8(pack_bf16x2(acc[q][2 * x] * f0, acc[q][2 * x + 1] * f1));
-          if (rr < rows) *reinterpret_cast<uint32_t*>(o + fr / NT * 16 + 8 * x) = v;
-        }
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t v = transpose8x8(pack_bf16x2(acc[q][2 * y] * f0, acc[q][2 * y + 1] * f1));
+        if (rr < rows && fr < kFrags) *reinterpret_cast<uint32_t*>(o + 8 * y) = v;
       }
-      if (warp == 0) store_lse(p, geo, b, hk, r0 + 8 * t + 2 * c, rows, g == 0, m[t], l[t]);
+    }
+    if (warp == 0 && lane < kRows && r0 + lane < rows) {
+      const int tok = geo.by_G.div(r0 + lane), h = hk * geo.G + r0 + lane - tok * geo.G;
+      p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(m, x);
     }
   }
 };
@@ -286,14 +291,18 @@ static __device__ __noinline__ uint32_t hidden8(const int32_t* s, const int32_t*
 }
 
 template <int D, int NT, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p,
+__global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p,
                                                                  const __grid_constant__ Geometry geo) {
   using S = Smem<D, NT>;
-  constexpr int kRows = S::kRows;
+  constexpr int kRows = S::kRows, kConsumers = S::kConsumers, kSlots = S::kSlots, kPieceRing = S::kPieceRing;
+  constexpr int kThreads = S::kThreads, kBatch = S::kBatch;
+  // Pages a run has at least: one for each consumer warp. Shorter runs only add
+  // partial results.
+  constexpr int kMinRun = kConsumers;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nseg = p.B * p.c.Hk * geo.RT;
-  const Bars bar{smem_u32(smem + S::kBars)};
+  const Bars<S> bar{smem_u32(smem + S::kBars)};
   int* scan = reinterpret_cast<int*>(smem + S::kScan);  // see the words below
   enum { kCount = kLineWords, kJobs, kMerged, kJob0 };
 
@@ -431,32 +440,34 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
     ++syncs;
     return ok;
   };
-  // a partial result is written: the last of its segment's notes the join, which all
-  // warps do at the end of the run
-  auto arrive = [&](int seg, int cta0, int parts, int slot_id) {
-    if (atomicAdd(&p.arrived[cta0], 1) != parts - 1) return;
+  // a partial result is written, by threads that this one has met since: the last of
+  // its segment's notes the join, which all warps do at the end of the run
+  auto arrive = [&](int seg, int cta0, int parts, int slot_id, int rows) {
+    if (atomic_add_acq_rel(&p.arrived[cta0], 1) != parts - 1) return;
     p.arrived[cta0] = 0;  // every part is there: ready for the next call
-    __threadfence();
     int* job = scan + kJob0 + 4 * slot_id;
-    job[0] = seg, job[1] = cta0, job[2] = parts;
+    job[0] = seg, job[1] = cta0, job[2] = parts, job[3] = rows;
     atomicOr(&scan[kJobs], 1 << slot_id);
   };
   int seq = 0;      // ring position of this warp
   int merges = 0;   // pieces so far whose states were merged in shared memory
 
+  int seg = 0, whole = 0, cta0 = 0, parts = 0, rows = 0;  // of the piece; its real rows from the sequence's start
+  int last_n = 0, last_from = 0;                // the run's last piece: states in shared memory, the first's place
   for (int piece = 0; ok; ++piece) {
     const int e = piece % kPieceRing;
     ok = __all_sync(0xffffffffu, cache_wait(bar.piece_full(e), (piece / kPieceRing) & 1, p.status));
     if (!ok) break;
     const int* d = reinterpret_cast<const int*>(smem + S::kPiece) + 8 * e;
-    const int seg = d[0], first = d[1], count = d[2], whole = d[3], slot_id = d[4], cta0 = d[5], parts = d[6];
+    const int first = d[1], count = d[2], slot_id = d[4];
+    seg = d[0], whole = d[3], cta0 = d[5], parts = d[6];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar.piece_empty(e));
     if (count == 0) break;
 
     const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
     const RowTile r = row_tile(p, geo, b, rt, lane == 0 && warp == 0);
-    const int rows = geo.G * r.live;
+    rows = geo.G * r.live;
     State<D, NT> st;
     st.clear();
     uint32_t qf[NT][D / 16][2];
@@ -696,28 +707,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
     const int writers = min(count, kConsumers);  // warps that had tiles, from first % 7 on
     const int mine = (warp - first % kConsumers + kConsumers) % kConsumers;
     if (first + count == run_hi - run_lo) {
-      // the run's last piece: nothing is left to overlap with, so all warps add up,
-      // each its fragments
+      // the run's last piece is added up below
       ok = __all_sync(0xffffffffu, count_wait(&scan[kMerged], merges, p.status));
-      if (!ok) break;
       if (mine < writers) st.put(merge + warp * S::kFrags * 32, stats + 3 * kRows * warp, lane);
-      if (!sync_warps()) break;
-      float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D, kRows);
-      FragmentSums<D, NT> f;
-      f.clear();
-      f.template add<kConsumers>(
-          writers, warp, [&](int k) { return stats + 3 * kRows * ((first + k) % kConsumers); },
-          [&](int k) { return merge + ((first + k) % kConsumers) * S::kFrags * 32 + lane; }, c,
-          [](auto* at) { return *at; });
-      if (whole)
-        f.store(p, geo, b, hk, rt * kRows, rows, warp, lane);
-      else
-        f.put(reinterpret_cast<float4*>(part), part + kRows * D, warp, lane);
-      if (!whole) {
-        __threadfence();
-        if (!sync_warps()) break;
-        if (tid == 0) arrive(seg, cta0, parts, slot_id);
-      }
+      last_n = writers;
+      last_from = first % kConsumers;
       break;
     }
     if (mine >= writers) {
@@ -792,42 +786,70 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
             const uint32_t v = transpose8x8(pack_bf16x2(st.acc[n][t][2 * x] * f0, st.acc[n][t][2 * x + 1] * f1));
             if (rr < rows) *reinterpret_cast<uint32_t*>(o + 16 * n + 8 * x) = v;
           }
-        store_lse(p, geo, b, hk, rt * kRows + 8 * t + 2 * c, rows, g == 0, st.m[t], st.l[t]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r2 = rt * kRows + 8 * t + 2 * c + e;
+          if (g == 0 && r2 < rows) {
+            const int tok2 = geo.by_G.div(r2), h2 = hk * geo.G + r2 - tok2 * geo.G;
+            p.lse[(static_cast<size_t>(b) * p.H + h2) * p.N + tok2] = out_lse(st.m[t][e], st.l[t][e]);
+          }
+        }
       }
     } else {
       float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D, kRows);
       st.put(reinterpret_cast<float4*>(out), out + kRows * D, lane);
-      __threadfence();
       __syncwarp();
-      if (lane == 0) arrive(seg, cta0, parts, slot_id);
+      if (lane == 0) arrive(seg, cta0, parts, slot_id, rows);
     }
   }
 
-  // segments of which this CTA's part came last: every part, in the order of the
-  // keys; a warp takes every seventh fragment
-  if (ok) {
-    __threadfence();
-    sync_warps();
-  }
-  for (int j = 0; ok && j < 2; ++j) {
-    if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
-    const int seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
+  // The end of the run. All warps add up the states of the last piece (nothing is left
+  // to overlap with), each its fragments, then the parts of the segments of which this
+  // CTA's came last. Both go through shared memory and one piece of code, in the order
+  // of the keys.
+  for (int j = -1; ok && last_n > 0 && j < 2; ++j) {
+    if (j >= 0) {
+      if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
+      seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
+      whole = 1;
+      last_n = parts;
+      last_from = 0;
+    }
     const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
-    const int rows = geo.G * row_tile(p, geo, b, rt, false).live;
+    if (j >= 0) rows = scan[kJob0 + 4 * j + 3];
+    constexpr int kPart = part_floats(D, kRows);
     FragmentSums<D, NT> f;
     f.clear();
-    for (int i0 = 0; i0 < parts; i0 += 4) {
-      // four parts on their way at a time
-      auto at = [&](int i) {
-        const int part = i0 + i;
-        return p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * part_floats(D, kRows);
-      };
-      f.template add<4>(
-          min(parts - i0, 4), warp, [&](int i) { return at(i) + kRows * D; },
-          [&](int i) { return reinterpret_cast<const float4*>(at(i)) + lane; }, c,
-          [](auto* at) { return __ldcg(at); });  // other CTAs wrote them: past L1
+    for (int k0 = 0; ok && k0 < last_n; k0 += kConsumers) {
+      const int n = min(last_n - k0, kConsumers);
+      if (j >= 0) {
+        if ((j > 0 || k0 > 0) && !sync_warps()) break;  // what was there has been read
+        constexpr int kUnits = kPart / 4;               // of 16 bytes
+#pragma unroll 1
+        for (int i = tid; i < n * kUnits; i += 32 * kConsumers) {
+          const int k = i / kUnits, u = i - k * kUnits, part = k0 + k;
+          const float* src = p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * kPart + 4 * u;
+          void* dst = u < S::kFrags * 32 ? static_cast<void*>(merge + k * S::kFrags * 32 + u)
+                                         : static_cast<void*>(stats + 3 * kRows * k + 4 * (u - S::kFrags * 32));
+          cp_async16(smem_u32(dst), src);  // past L1: other CTAs wrote them
+        }
+        cp_async_wait();
+      }
+      if (!sync_warps()) break;
+      f.add(n, last_from, merge, stats, warp, lane);
     }
-    f.store(p, geo, b, hk, rt * kRows, rows, warp, lane);
+    if (!ok) break;
+    if (whole) {
+      f.store(p, geo, b, hk, rt * kRows, rows, warp, lane);
+    } else {
+      // the part that continues from the CTA before, or the one that begins here
+      const int slot_id = cta0 == static_cast<int>(blockIdx.x) ? 1 : 0;
+      float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * kPart;
+      f.put(reinterpret_cast<float4*>(part), part + kRows * D, warp, lane);
+      if (!sync_warps()) break;
+      if (tid == 0) arrive(seg, cta0, parts, slot_id, rows);
+    }
+    if (j < 0) sync_warps();  // the joins are noted
   }
 
   // segments without a visible page: O = 0, LSE = -inf
@@ -869,7 +891,7 @@ cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, 
   const cudaError_t e = allow_smem<D, NT, kVec>();
   if (e != cudaSuccess) return e;
   const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
-  cache_fwd_kernel<D, NT, kVec><<<grid, kThreads, Smem<D, NT>::kBytes, s>>>(p, geo);
+  cache_fwd_kernel<D, NT, kVec><<<grid, Smem<D, NT>::kThreads, Smem<D, NT>::kBytes, s>>>(p, geo);
   return cudaGetLastError();
 }
 
