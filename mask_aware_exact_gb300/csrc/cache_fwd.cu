@@ -48,9 +48,17 @@
 namespace fm {
 namespace {
 
-// Consumer warps and the ring slots of each.
-constexpr __host__ __device__ int consumers(int D, int NT) { return D == 64 || NT == 1 ? 11 : 7; }
-constexpr __host__ __device__ int slots(int D, int NT) { return D == 128 && NT == 1 ? 2 : 3; }
+// With the producer 8 warps, two for each scheduler, 255 registers a thread. Eleven
+// consumer warps (two slots each for 8 rows of d = 128) gave the same times for long
+// sequences and up to 1.5 us more for short ones: what bounds long ones is not latency.
+constexpr int kConsumers = 7;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kSlots = 3;                           // ring slots of a consumer warp
+constexpr int kPieceRing = 2 * kConsumers + 2;      // piece descriptors: more than two groups start
+constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a time, one per lane
+// Pages a run has at least: one for each consumer warp. Shorter runs only add
+// partial results.
+constexpr int kMinRun = kConsumers;
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 
 // ---------------------------------------------------------------- instructions
@@ -75,10 +83,6 @@ __device__ __forceinline__ void cp_async_wait() {
 
 template <int D, int NT>
 struct Smem {
-  static constexpr int kConsumers = consumers(D, NT), kSlots = slots(D, NT);
-  static constexpr int kThreads = 32 * (kConsumers + 1);
-  static constexpr int kPieceRing = 2 * kConsumers + 2;  // piece descriptors: more than two groups start
-  static constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a time, one per lane
   static constexpr int kRows = 8 * NT;
   static constexpr int kFrags = D / 16 * NT;  // accumulator fragments (four floats a lane) of a warp
   static constexpr int kHalf = kPage * D;  // bytes of a page's K or V
@@ -93,11 +97,8 @@ struct Smem {
   static constexpr int kBytes = kScan + (kLineWords + 12) * 4;
 };
 static_assert(Smem<128, 2>::kBytes <= 227 * 1024 && Smem<64, 2>::kBytes <= 227 * 1024, "shared memory per CTA");
-static_assert(Smem<128, 1>::kBytes <= 227 * 1024 && Smem<64, 1>::kBytes <= 227 * 1024, "shared memory per CTA");
 
-template <typename S>
 struct Bars {
-  static constexpr int kConsumers = S::kConsumers, kSlots = S::kSlots, kPieceRing = S::kPieceRing;
   uint32_t base;
   __device__ uint32_t full(int w, int s) const { return base + 8 * (w * kSlots + s); }
   __device__ uint32_t empty(int w, int s) const { return base + 8 * ((kConsumers + w) * kSlots + s); }
@@ -168,7 +169,7 @@ struct State {
 // mv and (a share of) l.
 template <int D, int NT>
 struct FragmentSums {
-  static constexpr int kConsumers = consumers(D, NT), kRows = 8 * NT;
+  static constexpr int kRows = 8 * NT;
   static constexpr int kFrags = D / 16 * NT, kMine = (kFrags + kConsumers - 1) / kConsumers;
   static constexpr int kAtOnce = 32 / kRows, kSteps = (kConsumers + kAtOnce - 1) / kAtOnce;
   float acc[kMine][4];
@@ -291,18 +292,14 @@ static __device__ __noinline__ uint32_t hidden8(const int32_t* s, const int32_t*
 }
 
 template <int D, int NT, bool kVec>
-__global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p,
+__global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p,
                                                                  const __grid_constant__ Geometry geo) {
   using S = Smem<D, NT>;
-  constexpr int kRows = S::kRows, kConsumers = S::kConsumers, kSlots = S::kSlots, kPieceRing = S::kPieceRing;
-  constexpr int kThreads = S::kThreads, kBatch = S::kBatch;
-  // Pages a run has at least: one for each consumer warp. Shorter runs only add
-  // partial results.
-  constexpr int kMinRun = kConsumers;
+  constexpr int kRows = S::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nseg = p.B * p.c.Hk * geo.RT;
-  const Bars<S> bar{smem_u32(smem + S::kBars)};
+  const Bars bar{smem_u32(smem + S::kBars)};
   int* scan = reinterpret_cast<int*>(smem + S::kScan);  // see the words below
   enum { kCount = kLineWords, kJobs, kMerged, kJob0 };
 
@@ -427,7 +424,7 @@ __global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(c
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
-  const uint8_t* ring = smem + S::kRing + warp * kSlots * S::kHalf;
+  uint8_t* ring = smem + S::kRing + warp * kSlots * S::kHalf;
   float4* merge = reinterpret_cast<float4*>(smem + S::kMerge);
   float* stats = reinterpret_cast<float*>(smem + S::kStats);
   bool ok = true;
@@ -572,21 +569,17 @@ __global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.empty(warp, sk));
 
-      // scores in log2 units, masked; s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e
+      // s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e; ck times it is the score in
+      // log2 units (ck > 0 keeps masked scores at -inf)
       const float kscale = __int_as_float(meta.z);
       const bool tail = meta.x < 0 || j0 + kPage > all_lim;
-      // Each pass goes over all rows of the lane, so that their chains overlap.
+      // Each pass goes over all rows of the lane, so that their chains overlap; a row
+      // pair's elements go through packed instructions.
       float ck[NT][2], top[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ck[t][e] = crow[t][e] * kscale;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][t][i] *= ck[t][i & 1];
+        for (int e = 0; e < 2; ++e) ck[t][e] = fmaxf(crow[t][e] * kscale, 1.17549435e-38f);
       if (__builtin_expect(tail || meta.y, 0)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -614,7 +607,8 @@ __global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(c
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           top[t][e] = fmax3(fmax3(s[0][t][e], s[0][t][2 + e], s[1][t][e]), fmax3(s[1][t][2 + e], s[2][t][e], s[2][t][2 + e]),
-                            fmaxf(s[3][t][e], s[3][t][2 + e]));
+                            fmaxf(s[3][t][e], s[3][t][2 + e])) *
+                      ck[t][e];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -638,19 +632,22 @@ __global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(c
           fv[t][e] = ex2(fminf(mu[t][e] + lvs - (mv_new == -INFINITY ? 0.f : mv_new) + kPShift, 126.f));
         }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int t = 0; t < NT; ++t) {
+        const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-mu[t][0], -mu[t][1]), f2 = f2_make(fv[t][0], fv[t][1]);
+        uint64_t l2 = f2_make(st.l[t][0], st.l[t][1]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float pr[4];
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = ex2(s[u][t][i] - mu[t][i & 1]);
-            st.l[t][i & 1] += x;
-            pr[i] = x * fv[t][i & 1];
+          for (int x = 0; x < 2; ++x) {
+            float x0, x1, p0, p1;
+            f2_split(f2_fma(f2_make(s[u][t][2 * x], s[u][t][2 * x + 1]), c2, nm2), x0, x1);
+            const uint64_t pp = f2_make(ex2(x0), ex2(x1));
+            l2 = f2_add(l2, pp);
+            f2_split(f2_mul(pp, f2), p0, p1);
+            pf[u][t][x] = transpose8x8(pack_f16x2(p0, p1));
           }
-          pf[u][t][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
-          pf[u][t][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
-        }
+        f2_split(l2, st.l[t][0], st.l[t][1]);
+      }
       if (__builtin_expect(__any_sync(0xffffffffu, moved), 0)) {
 #pragma unroll
         for (int n = 0; n < D / 16; ++n)
@@ -662,16 +659,28 @@ __global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(c
 
       ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sv), ((seq + 1) / kSlots) & 1, p.status));
       if (!ok) break;
-      const uint8_t* vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
-      // codes behind the sequence's end may be anything, NaN too: they become 0
-      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-      if (tail) {
+      uint8_t* vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
+      if (__builtin_expect(tail, 0)) {
+        // codes behind the sequence's end may be anything, NaN too: they become 0, each
+        // lane's where it reads them
         const int n_ok = meta.x < 0 ? 0 : min(max(r.len - (j0 + 16 * c), 0), 16);
+        uint32_t keep[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int nb = min(max(n_ok - 4 * u, 0), 4);
           keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
         }
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / 8; i0 += 4) {
+          uint4* at = reinterpret_cast<uint4*>(vbase + 8 * i0 * kPage);
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = at[8 * i * kPage / 16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            at[8 * i * kPage / 16] = make_uint4(x[i].x & keep[0], x[i].y & keep[1], x[i].z & keep[2], x[i].w & keep[3]);
+        }
+        fence_proxy_async_smem();  // the next copy into the slot comes after
       }
 #pragma unroll
       for (int n0 = 0; n0 < D / 16; n0 += 4) {
@@ -686,8 +695,8 @@ __global__ void __launch_bounds__((Smem<D, NT>::kThreads), 1) cache_fwd_kernel(c
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             uint32_t a[4];
-            codes_to_f16(word(w[n][0], u) & keep[u], a[0], a[2]);
-            codes_to_f16(word(w[n][1], u) & keep[u], a[1], a[3]);
+            codes_to_f16(word(w[n][0], u) , a[0], a[2]);
+            codes_to_f16(word(w[n][1], u) , a[1], a[3]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) mma16816(st.acc[n0 + n][t], a, pf[u][t][0], pf[u][t][1]);
           }
@@ -891,7 +900,7 @@ cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, int num_sms, 
   const cudaError_t e = allow_smem<D, NT, kVec>();
   if (e != cudaSuccess) return e;
   const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
-  cache_fwd_kernel<D, NT, kVec><<<grid, Smem<D, NT>::kThreads, Smem<D, NT>::kBytes, s>>>(p, geo);
+  cache_fwd_kernel<D, NT, kVec><<<grid, kThreads, Smem<D, NT>::kBytes, s>>>(p, geo);
   return cudaGetLastError();
 }
 
