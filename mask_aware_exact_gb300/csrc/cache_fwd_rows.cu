@@ -347,6 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
     // instruction cache, which cost more than anything else here.
     const int kv = (warp - 12) >> 1, ct = tid & 63, pc = ct & 3, row0 = ct >> 2;
     const int blocks = kv ? 2 : D / 64, block_rows = kv ? D : 128, row_bytes = kv ? 64 : D;
+    // K, d = 128: odd rows begin with the other half, or the 64 bytes that eight lanes
+    // take of two rows would lie in the same banks
+    const int swap = !kv && D == 128 ? row0 & 1 : 0;
     const uint32_t u0 = ((2 * pc) ^ (row0 & 7)) << 4, u1 = ((2 * pc + 1) ^ (row0 & 7)) << 4;
     bool ok = true;
     for (int J = 0; ok; ++J) {
@@ -362,18 +365,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
            (J < R || cache_wait(freed, (J / R - 1) & 1, p.status));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint8_t* codes = smem + L::kStage + slot * L::kCodes + row0 * row_bytes + 16 * pc;
-      uint32_t dst = (kv ? sV : sK) + g * L::kTile + row0 * 128;
-      for (int x = 0; x < blocks; ++x) {
-        // V: codes behind the sequence's end (or of an absent page) become 0
-        const int left = kv == 0 ? 16 : (x == 0 ? valid[0] : valid[1]) - 16 * pc;
-        uint32_t keep[4];
+      uint8_t* codes = smem + L::kStage + slot * L::kCodes + row0 * row_bytes + 16 * pc;
+      if (kv && __builtin_expect((valid[0] & valid[1]) != kPage, 0)) {
+        // V: codes behind the sequence's end (or of an absent page) become 0, each
+        // thread's where it reads them
+        for (int x = 0; x < 2; ++x) {
+          const int left = valid[x] - 16 * pc;
+          uint32_t keep[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int nb = min(max(left - 4 * u, 0), 4);
-          keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
+          for (int u = 0; u < 4; ++u) {
+            const int nb = min(max(left - 4 * u, 0), 4);
+            keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
+          }
+#pragma unroll 1
+          for (int row = 0; row < D; row += 16) {
+            uint4* at = reinterpret_cast<uint4*>(codes + (x * D + row) * kPage);
+            const uint4 w = *at;
+            *at = make_uint4(w.x & keep[0], w.y & keep[1], w.z & keep[2], w.w & keep[3]);
+          }
         }
-        const uint8_t* src = codes + x * (kv ? kPage * D : 64);
+      }
+      const uint32_t dst = (kv ? sV : sK) + g * L::kTile + row0 * 128;
+      for (int x = 0; x < blocks; ++x) {
+        const int y = x ^ swap;
+        const uint8_t* src = codes + y * (kv ? kPage * D : 64);
+        const uint32_t to = dst + y * block_rows * 128;
 #pragma unroll 1
         for (int row = 0; row < block_rows; row += 64) {
           uint4 w[4];
@@ -383,13 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           for (int i = 0; i < 4; ++i) {
             uint32_t h[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) codes_to_f16(word(w[i], u) & keep[u], h[2 * u], h[2 * u + 1]);
-            const uint32_t at = dst + (row + 16 * i) * 128;
+            for (int u = 0; u < 4; ++u) codes_to_f16(word(w[i], u), h[2 * u], h[2 * u + 1]);
+            const uint32_t at = to + (row + 16 * i) * 128;
             st_shared_v4(at + u0, h[0], h[1], h[2], h[3]);
             st_shared_v4(at + u1, h[4], h[5], h[6], h[7]);
           }
         }
-        dst += block_rows * 128;
       }
       fence_proxy_async_smem();  // the operands are read by the tensor cores
       __syncwarp();
