@@ -25,11 +25,22 @@
 //   10     walks the run, looks pages up, issues the copies, publishes a step's
 //          description to all roles (ring of kMetaRing).
 //   12, 13 conversion of K; 14, 15 of V.
-// TMEM: R = 2 S regions of 128 columns (3 with d = 64), then O_0 and O_1; P over S.
+// TMEM: S (128 columns; two regions with d = 64), two P (64 columns each), O_0 and O_1.
+// P has columns of its own, so the next S is computed as soon as this one has been
+// read: with P over two regions of S, an S had to wait for the products of two steps
+// before, 553 us where this takes 545.
 //
-// What bounds it: shared memory. A step with d = 128 writes 32 KB of codes and 64 KB of
-// fp16 operands and reads 32 KB and 96 KB, 224 KB at 128 bytes a clock: 1 750 cycles,
-// about the softmax warps' latency chain (1 550).
+// Measured: 2 sequences of up to 32768 tokens, 512 query tokens, 32 / 8 heads of 128:
+// 545 us, 990 TFLOP/s, 52 % of the bf16 rate; 3 sequences up to 109407, 64 rows:
+// 172 us, 3.5 TB/s. A step of 128 keys takes 2 150 cycles. Its products need 1 024; shared
+// memory (d = 128: 32 KB of codes and 64 KB of operands written, 32 KB and 96 KB read)
+// 1 750 at 128 bytes a clock; each softmax warp is busy for about 1 900, waits included,
+// and the conversion warps for about 1 600. None of them alone is the bound: without
+// the conversion the call takes 466 us, without the exponentials 511, without any work
+// in the softmax 456. What did not help: Q in TMEM (shared memory reads - 14 %, 556
+// us), S and P signalled to each warpgroup by itself (products of 64 keys, 610), the
+// next codes loaded while some are converted (567), registers moved from the other
+// roles to the softmax (615).
 #include <atomic>
 
 #include "cache_common.cuh"
@@ -53,10 +64,8 @@ enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16,
 
 template <int D>
 struct Layout {
-  // S regions in TMEM, operand slots of K and of V: with d = 64 the accumulators leave
-  // room for a third region, and the way from a step's P over its products to the S
-  // that reuses its region is spread over three steps
-  static constexpr int R = D == 64 ? 3 : 2;
+  static constexpr int R = D == 64 ? 3 : 2;   // operand slots of K and of V in shared memory
+  static constexpr int kS = D == 64 ? 2 : 1;  // S regions in TMEM
   static constexpr int kStages = 2 * R;      // staged code tiles: K and V of R steps
   static constexpr int kTile = 128 * D * 2;  // fp16 operand tile
   static constexpr int kCodes = 128 * D;     // codes of a step, K or V
@@ -67,12 +76,12 @@ struct Layout {
   static constexpr int kMeta = kStage + kStages * kCodes;
   static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
   static constexpr int kBar = kWords + (kLineWords + 4) * 4;
-  static constexpr int kNumBars = 2 * kStages + kMetaRing + 5 * R + 3;
+  static constexpr int kNumBars = 2 * kStages + kMetaRing + 6 * R + 3;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kBytes = kTmemSlot + 16;
 };
 static_assert(Layout<128>::kBytes <= 227 * 1024 && Layout<64>::kBytes <= 227 * 1024, "shared memory per CTA");
-static_assert(kMetaRing > 3 * Layout<64>::R, "see where an entry is written");
+static_assert(kMetaRing > 2 * Layout<64>::R + Layout<64>::kS + 3, "see where an entry is written");
 static_assert(Layout<128>::kBar % 8 == 0 && Layout<64>::kBar % 8 == 0, "barriers are 8-byte aligned");
 
 template <int R>
@@ -88,15 +97,25 @@ struct Bars {
   __device__ uint32_t s_full(int g) const { return at(kFirst + 2 * R + g); }   // commit
   __device__ uint32_t p_full(int g) const { return at(kFirst + 3 * R + g); }   // 8
   __device__ uint32_t pv_done(int g) const { return at(kFirst + 4 * R + g); }  // commit
-  __device__ uint32_t q_full() const { return at(kFirst + 5 * R); }            // 8
-  __device__ uint32_t o_free() const { return at(kFirst + 5 * R + 1); }        // 8
-  __device__ uint32_t softmax() const { return at(kFirst + 5 * R + 2); }       // 8
+  __device__ uint32_t s_read(int g) const { return at(kFirst + 5 * R + g); }   // 8
+  __device__ uint32_t q_full() const { return at(kFirst + 6 * R); }            // 8
+  __device__ uint32_t o_free() const { return at(kFirst + 6 * R + 1); }        // 8
+  __device__ uint32_t softmax() const { return at(kFirst + 6 * R + 2); }       // 8
 };
 
-// TMEM columns of accumulator w, behind the S regions.
+// TMEM columns: S of step J, P of its page w (64 keys in 32 columns; two steps in
+// turn), accumulator w.
+template <int D>
+__device__ __forceinline__ uint32_t col_s(int J) {
+  return 128u * static_cast<uint32_t>(J % Layout<D>::kS);
+}
+template <int D>
+__device__ __forceinline__ uint32_t col_p(int J, int w) {
+  return 128u * Layout<D>::kS + 64u * static_cast<uint32_t>(J & 1) + 32u * static_cast<uint32_t>(w);
+}
 template <int D>
 __device__ __forceinline__ uint32_t col_o(int w) {
-  return 128u * Layout<D>::R + D * static_cast<uint32_t>(w);
+  return 128u * Layout<D>::kS + 128u + D * static_cast<uint32_t>(w);
 }
 
 // Instruction descriptor, kind::f16 with fp16 A and B (format code 0), both K-major.
@@ -159,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
   }
   if (tid < L::kNumBars) {
     // arrivals: stage_full 1, stage_empty 2, meta 1, k_ready and v_ready 2, s_full 1,
-    // p_full 8, pv_done 1, q_full, o_free and softmax 8
+    // p_full 8, pv_done 1, s_read, q_full, o_free and softmax 8
     const int i = tid - 2 * kStages - kMetaRing;
     int n = 1;
     if (tid >= kStages && tid < 2 * kStages) n = 2;
@@ -244,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           ok = slot_free(2 * done);
           if (ok) {
             // the entry was last read for step J - kMetaRing, which every role has left: the K
-            // codes of step J - R are converted, so S of step J - 2 R and P V of step J - 3 R
-            // are done, and V of step J - 3 R with them
+            // codes of step J - R are converted, so S of step J - 2 R is done, S of step
+            // x = J - 2 R - kS is read, and the products of step x - 3 are done, V with them
             int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + (done % kMetaRing) * (kMetaInts / 4);
 #pragma unroll
             for (int i = 0; i < kMetaInts / 4; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
@@ -297,16 +316,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         const int flags = step_flags(J);
         if (flags & kEnd) break;
         const int g = J % R;
-        // Q of the piece; the products of step J - R, which read this region; K
+        // Q of the piece; S of step J - kS, which lay here, has been read; K
         if ((flags & kFirstStep) && !cache_wait(bar.q_full(), pieces++ & 1, p.status)) break;
-        if (J >= R && !cache_wait(bar.pv_done(g), (J / R - 1) & 1, p.status)) break;
+        if (J >= L::kS && !cache_wait(bar.s_read((J - L::kS) % R), ((J - L::kS) / R) & 1, p.status)) break;
         if (!cache_wait(bar.k_ready(g), (J / R) & 1, p.status)) break;
         tc_fence_after();
         const uint64_t kd = dk + static_cast<uint64_t>((g * L::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-          mma_ss(tmem + 128 * g, dq + off, kd + off, idesc, kk > 0);
+          mma_ss(tmem + col_s<D>(J), dq + off, kd + off, idesc, kk > 0);
         }
         mma_commit(bar.s_full(g));
       }
@@ -333,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + col_o<D>(w), tmem + 128 * g + 64 * w + 8 * kk,
+            mma_ts(tmem + col_o<D>(w), tmem + col_p<D>(J, w) + 8 * kk,
                    vd + static_cast<uint64_t>((w * D * 128 + kk * 32) >> 4), idesc, !first || kk > 0);
         mma_commit(bar.pv_done(g));
       }
@@ -500,11 +519,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         const bool masked = j0 < 0 || j0 + kPage > all_lim || (flags & (kCut << w));
         ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J / R) & 1, p.status));
         if (!ok) break;
-        if (warp_live) {
+        if (!warp_live) {
+          if (lane == 0) mbar_arrive(bar.s_read(g));
+        } else {
           tc_fence_after();
           uint32_t sv[64];
-          const uint32_t s_addr = tmem + lane_base + 128 * g + 64 * w;
+          const uint32_t s_addr = tmem + lane_base + col_s<D>(J) + 64 * w;
           tmem_ld64(s_addr, s_addr + 32, sv);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.s_read(g));
           if (__builtin_expect(masked, 0)) {
             const int n = j0 < 0 ? 0 : min(max(lim - j0, 0), kPage);
             uint64_t hid = n == kPage ? 0ull : ~0ull << n;  // keys this row does not see
@@ -549,7 +573,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           float l0, l1;
           f2_split(l2, l0, l1);
           l += l0 + l1;
-          tmem_st32p(tmem + lane_base + 128 * g + 64 * w, pk);
+          if (J >= 2) {  // the products that read P of step J - 2 have completed
+            ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done((J - 2) % R), ((J - 2) / R) & 1, p.status));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_st32p(tmem + lane_base + col_p<D>(J, w), pk);
           if (__builtin_expect(!first && __any_sync(0xffffffffu, rescale), 0)) {
             // O_w is rescaled once the products of step J - 1 have completed
             ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done((J - 1) % R), ((J - 1) / R) & 1, p.status));
