@@ -74,9 +74,10 @@ struct Line {
 };
 constexpr int kLineWords = 40;  // ints of shared memory for find_run
 // Segments of up to this many pages (or an eighth of a run) are not cut: a join takes
-// about 4 us, as long as a CTA takes for some 30 pages. One sequence of 1000 tokens (16
-// pages, 8 cache heads): 11.4 us whole, 15.0 cut; 2000 tokens: 14.5, 15.7; 4000: 21.1,
-// 14.0. 64 sequences up to 2000: 46 us whole, 52 cut; up to 4000: 69, 66.
+// 3 to 4 us, about as long as a CTA takes for 30 pages. One sequence of 500 tokens (8
+// cache heads): 9.7 us whole, 13.8 cut; 1000 tokens (16 pages): 11.3, 13.8; 2000: 14.3,
+// 14.4; 4000: 20.5, 12.7. 64 sequences up to 2000: 44.8 us whole, 51.3 cut; up to 4000:
+// 68.2, 64.8.
 constexpr int kUncut = 32;
 
 // Called by all kThreads threads of every CTA; units(s) is the number of units of

@@ -910,8 +910,13 @@ cudaError_t launch_nt(const CacheFwdParams& p, const Geometry& geo, int num_sms,
                                                         : launch_t<D, NT, false>(p, geo, num_sms, s);
 }
 
-// Rows of a tile: as few as hold all rows, so that no columns of an instruction are
-// empty; above 16 rows the kernel for many rows takes over.
+// Rows of a tile: 8 or 16 as long as two tiles hold all rows, above that 128 on
+// tcgen05. Every tile reads and converts the codes again, which soon costs more than
+// rows of a tile that are empty. 16 sequences of 16384 tokens, 4 cache heads, tiles of
+// 16 rows / of 128, us:
+//   rows       16           24           32           40           64          128
+//   d = 64   40.4 / -    58.2 / 68.1  58.7 / 68.1  81.6 / 69.4   104 / 69.5   191 / 75.0
+//   d = 128  59.8 / -    83.1 / 86.6  84.9 / 87.0   133 / 89.4   172 / 90.2   325 / 96.7
 int rows_of_tile(int rows) { return rows <= 8 ? 8 : rows <= 32 ? 16 : kManyRows; }
 
 Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {

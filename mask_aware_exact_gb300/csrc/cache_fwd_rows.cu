@@ -25,10 +25,11 @@
 //   10     walks the run, looks pages up, issues the copies, publishes a step's
 //          description to all roles (ring of kMetaRing).
 //   12, 13 conversion of K; 14, 15 of V.
-// TMEM: S (128 columns; two regions with d = 64), two P (64 columns each), O_0 and O_1.
-// P has columns of its own, so the next S is computed as soon as this one has been
-// read: with P over two regions of S, an S had to wait for the products of two steps
-// before, 553 us where this takes 545.
+// TMEM, d = 128: S (128 columns), two P (64 columns each), O_0 and O_1. P has columns
+// of its own, so the next S is computed as soon as this one has been read; with P
+// over two regions of S, an S waited for the products of two steps before, 553 us
+// where this takes 545. With d = 64 there is room for three regions, P over its S:
+// 69.5 us for 16 sequences of 16384 with 64 rows; two regions and two P: 77.
 //
 // Measured: 2 sequences of up to 32768 tokens, 512 query tokens, 32 / 8 heads of 128:
 // 545 us, 990 TFLOP/s, 52 % of the bf16 rate; 3 sequences up to 109407, 64 rows:
@@ -65,7 +66,8 @@ enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16,
 template <int D>
 struct Layout {
   static constexpr int R = D == 64 ? 3 : 2;   // operand slots of K and of V in shared memory
-  static constexpr int kS = D == 64 ? 2 : 1;  // S regions in TMEM
+  static constexpr int kS = D == 64 ? 3 : 1;  // S regions in TMEM
+  static constexpr bool kOver = D == 64;      // P lies over its S
   static constexpr int kStages = 2 * R;      // staged code tiles: K and V of R steps
   static constexpr int kTile = 128 * D * 2;  // fp16 operand tile
   static constexpr int kCodes = 128 * D;     // codes of a step, K or V
@@ -103,19 +105,20 @@ struct Bars {
   __device__ uint32_t softmax() const { return at(kFirst + 6 * R + 2); }       // 8
 };
 
-// TMEM columns: S of step J, P of its page w (64 keys in 32 columns; two steps in
-// turn), accumulator w.
+// TMEM columns: S of step J, P of its page w (64 keys in 32 columns; with places of
+// their own two steps in turn), accumulator w.
 template <int D>
 __device__ __forceinline__ uint32_t col_s(int J) {
   return 128u * static_cast<uint32_t>(J % Layout<D>::kS);
 }
 template <int D>
 __device__ __forceinline__ uint32_t col_p(int J, int w) {
-  return 128u * Layout<D>::kS + 64u * static_cast<uint32_t>(J & 1) + 32u * static_cast<uint32_t>(w);
+  return Layout<D>::kOver ? col_s<D>(J) + 64u * static_cast<uint32_t>(w)
+                          : 128u * Layout<D>::kS + 64u * static_cast<uint32_t>(J & 1) + 32u * static_cast<uint32_t>(w);
 }
 template <int D>
 __device__ __forceinline__ uint32_t col_o(int w) {
-  return 128u * Layout<D>::kS + 128u + D * static_cast<uint32_t>(w);
+  return 128u * Layout<D>::kS + (Layout<D>::kOver ? 0u : 128u) + D * static_cast<uint32_t>(w);
 }
 
 // Instruction descriptor, kind::f16 with fp16 A and B (format code 0), both K-major.
@@ -264,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           if (ok) {
             // the entry was last read for step J - kMetaRing, which every role has left: the K
             // codes of step J - R are converted, so S of step J - 2 R is done, S of step
-            // x = J - 2 R - kS is read, and the products of step x - 3 are done, V with them
+            // x = J - 2 R - kS is read (or its products are done, if P lay over it), and the
+            // products of step x - 3 are done, V with them
             int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + (done % kMetaRing) * (kMetaInts / 4);
 #pragma unroll
             for (int i = 0; i < kMetaInts / 4; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
@@ -316,9 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         const int flags = step_flags(J);
         if (flags & kEnd) break;
         const int g = J % R;
-        // Q of the piece; S of step J - kS, which lay here, has been read; K
+        // Q of the piece; the region: S of step J - kS has been read, and if P lay over it
+        // its products are done; K
         if ((flags & kFirstStep) && !cache_wait(bar.q_full(), pieces++ & 1, p.status)) break;
-        if (J >= L::kS && !cache_wait(bar.s_read((J - L::kS) % R), ((J - L::kS) / R) & 1, p.status)) break;
+        if (J >= L::kS) {
+          const int x = J - L::kS;
+          if (!cache_wait(L::kOver ? bar.pv_done(x % R) : bar.s_read(x % R), (x / R) & 1, p.status)) break;
+        }
         if (!cache_wait(bar.k_ready(g), (J / R) & 1, p.status)) break;
         tc_fence_after();
         const uint64_t kd = dk + static_cast<uint64_t>((g * L::kTile) >> 4);
@@ -520,15 +528,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J / R) & 1, p.status));
         if (!ok) break;
         if (!warp_live) {
-          if (lane == 0) mbar_arrive(bar.s_read(g));
+          if (!L::kOver && lane == 0) mbar_arrive(bar.s_read(g));
         } else {
           tc_fence_after();
           uint32_t sv[64];
           const uint32_t s_addr = tmem + lane_base + col_s<D>(J) + 64 * w;
           tmem_ld64(s_addr, s_addr + 32, sv);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar.s_read(g));
+          if constexpr (!L::kOver) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.s_read(g));
+          }
           if (__builtin_expect(masked, 0)) {
             const int n = j0 < 0 ? 0 : min(max(lim - j0, 0), kPage);
             uint64_t hid = n == kPage ? 0ull : ~0ull << n;  // keys this row does not see
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           float l0, l1;
           f2_split(l2, l0, l1);
           l += l0 + l1;
-          if (J >= 2) {  // the products that read P of step J - 2 have completed
+          if (!L::kOver && J >= 2) {  // the products that read P of step J - 2 have completed
             ok = __all_sync(0xffffffffu, cache_wait(bar.pv_done((J - 2) % R), ((J - 2) / R) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
