@@ -31,6 +31,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kBlocksPerSm = 4;  // resident at once
 constexpr int kHeadsMost = 16;
 constexpr int kStages = 4;  // heads in flight per thread
+constexpr int kAtOnce = 8;  // heads loaded at a time when the elements are accessed one by one
 
 // f / (2 pi) modulo one turn as a 64-bit fraction, from the bits of the fp64
 // f: mantissa times the first 64 bits of 2 / pi, shifted by the exponent. The
@@ -163,18 +164,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     }
   }
 
-  int slot = 0;
-  for (int h = h0; h < h1; ++h) {
-    V x0, x1;
-    if constexpr (kAsync) {
-      copy_wait<kStages - 1>();
-      x0 = slots[slot][0][threadIdx.x];
-      if (two) x1 = slots[slot][1][threadIdx.x];
-    } else {
-      const T* src = source(h);
-      x0 = *reinterpret_cast<const V*>(src + e0);
-      if (two) x1 = *reinterpret_cast<const V*>(src + e1);
-    }
+  auto finish = [&](int h, V x0, V x1) {
     const bool first = h < p.t[0].H;
     const RopeTensor& r = p.t[first ? 0 : 1];
     T* dst = static_cast<T*>(r.y) + b * r.ys[0] + (first ? h : h - p.t[0].H) * r.ys[1] + t * r.ys[2];
@@ -206,8 +196,34 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     }
     *reinterpret_cast<V*>(dst + e0) = x0;
     if (two) *reinterpret_cast<V*>(dst + e1) = x1;
-    fetch(h + kStages, slot);
-    slot = slot + 1 == kStages ? 0 : slot + 1;
+  };
+  if constexpr (kAsync) {
+    int slot = 0;
+    for (int h = h0; h < h1; ++h) {
+      copy_wait<kStages - 1>();
+      const V x0 = slots[slot][0][threadIdx.x];
+      V x1 = x0;
+      if (two) x1 = slots[slot][1][threadIdx.x];
+      finish(h, x0, x1);
+      fetch(h + kStages, slot);
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+  } else {
+    for (int h = h0; h < h1; h += kAtOnce) {
+      V x0[kAtOnce], x1[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (h + i >= h1) break;
+        const T* src = source(h + i);
+        x0[i] = *reinterpret_cast<const V*>(src + e0);
+        if (two) x1[i] = *reinterpret_cast<const V*>(src + e1);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (h + i >= h1) break;
+        finish(h + i, x0[i], x1[i]);
+      }
+    }
   }
 }
 
