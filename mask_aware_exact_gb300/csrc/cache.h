@@ -65,6 +65,7 @@ struct CacheFwdParams {
   // workspace (see CacheWs)
   int32_t* arrived;     // [CTAs]: partial results that have arrived of the cut segment that begins
                         // in a CTA's run (0 between calls)
+  int32_t* groups;      // [CTAs][2]: the same for groups of parts, see Part (also 0 between calls)
   float* partial;       // [CTAs][2] partial results
   uint16_t* list;       // [row tiles][max_pages]: pages that some row sees, in order; bit 15: intervals
                         // hide some key of the page from some row
@@ -96,7 +97,7 @@ struct Geometry {
 
 // Byte offsets of the workspace regions.
 struct CacheWs {
-  size_t arrived, partial, list, listed, total;
+  size_t arrived, groups, partial, list, listed, total;
 };
 constexpr int kCacheMaxCtas = 256;  // partial results are kept for at most this many CTAs
 // Whether the pages of all row tiles can be counted in 32 bits.

@@ -221,6 +221,7 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   char* w = static_cast<char*>(ws);
   p.status = reinterpret_cast<int32_t*>(w);
   p.arrived = reinterpret_cast<int32_t*>(w + L.arrived);
+  p.groups = reinterpret_cast<int32_t*>(w + L.groups);
   p.partial = reinterpret_cast<float*>(w + L.partial);
   p.list = reinterpret_cast<uint16_t*>(w + L.list);
   p.listed = reinterpret_cast<int32_t*>(w + L.listed);

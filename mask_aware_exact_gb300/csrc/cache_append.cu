@@ -10,7 +10,11 @@
 // rounds where they become subnormal.
 //
 // HBM-bound for prompts: 4 bytes read and 2 written per (K, V) element pair.
-// All loads of a thread are issued before the first is used.
+// All loads of a thread are issued before the first is used; the page's two barriers
+// (its scale needs every row) are covered by the other three CTAs of the SM. 4 x 8192
+// tokens, 8 heads of 128: 32.4 us, 5.3 TB/s, 78 % of a copy; with registers held down
+// for five CTAs 32.6 us, for six 34.8, for eight 46.9. One token of each of 64
+// sequences: 5 us, the trip to the table between two others.
 #include "cache.h"
 #include "ptx_fp8.cuh"
 

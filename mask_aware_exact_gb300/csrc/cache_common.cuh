@@ -65,6 +65,12 @@ __device__ __forceinline__ int page_on_line(const CacheFwdParams& p, const Geome
   return v & 0x7fff;
 }
 
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t* at, int x) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(x) : "memory");
+  return old;
+}
+
 // A CTA's run on the line of units (pages, or pairs of them) of all segments.
 struct Line {
   int run;         // units of a full run
@@ -79,6 +85,34 @@ constexpr int kLineWords = 40;  // ints of shared memory for find_run
 // 14.4; 4000: 20.5, 12.7. 64 sequences up to 2000: 44.8 us whole, 51.3 cut; up to 4000:
 // 68.2, 64.8.
 constexpr int kUncut = 32;
+
+// Where there are at least two CTAs for each segment, the segments are cut one by one
+// into equal runs if these are not longer than the line's by more than kApart pages:
+// a second piece in a run costs a CTA about that much.
+constexpr int kApart = 14;
+
+// Sum of x over the threads before this one, and over all of them.
+template <int kWarps>
+static __device__ __noinline__ int block_before(int x, int* wsum, int& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int sum = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  __syncthreads();  // wsum may still be read
+  if (lane == 31) wsum[warp] = sum;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int y = wsum[w];
+    if (w < warp) sum += y;
+    total += y;
+  }
+  return sum - x;
+}
 
 // Called by all kThreads threads of every CTA; units(s) is the number of units of
 // segment s, `pages` the pages of a unit.
@@ -100,47 +134,52 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
     longest = max(longest, n);
     empty |= n == 0;
   }
-  int before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
-  }
   longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    wsum[warp] = before;
-    wmax[warp] = longest;
-  }
+  if (lane == 0) wmax[warp] = longest;
   Line r;
   r.any_empty = __syncthreads_or(empty);
-  int total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int x = wsum[w];
-    if (w < warp) before += x;
-    total += x;
-    longest = max(longest, wmax[w]);
-  }
-  before -= mine;
+  for (int w = 0; w < kWarps; ++w) longest = max(longest, wmax[w]);
+  int total;
+  int before = block_before<kWarps>(mine, wsum, total);
   const int even = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const bool uncut = longest <= max(kUncut / pages, even / 8);
   // the least run only keeps cut segments from falling into many parts
   r.run = max(uncut ? 1 : min_run, even);
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const long long x_wide = static_cast<long long>(r.run) * (blockIdx.x + side);
+  const int per = nseg > 0 ? static_cast<int>(gridDim.x) / nseg : 0;  // parts a segment may have
+  const int cut = per >= 2 ? max(min_run, (longest + per - 1) / per) : 0;
+  if (!uncut && per >= 2 && cut <= even + kApart / pages) {
+    // runs of one segment each: on this line every segment is filled up to whole runs
+    r.run = cut;
+    const int filled = (mine + cut - 1) / cut * cut;  // a thread has one segment at most
+    before = block_before<kWarps>(filled, wsum, total);
+    const long long x_wide = static_cast<long long>(cut) * blockIdx.x;
     const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
     if (x == total) {
-      if (tid == 0) found[side] = total;
-    } else if (before <= x && x < before + mine) {
-      int s = seg_lo, at = before, n;
-      // a thread with one segment knows its units
-      while (x >= at + (n = each == 1 ? mine : units(s))) at += n, ++s;
-      const bool next = uncut && x != at;  // on to the segment's end
-      found[side] = next ? at + n : x;
-      if (side == 0) {
-        found[2] = next ? s + 1 : s;
-        found[3] = uncut ? 0 : x - at;
+      if (tid == 0) found[0] = found[1] = total;
+    } else if (before <= x && x < before + filled) {
+      found[0] = x;
+      found[1] = min(x + cut, before + mine);
+      found[2] = seg_lo;
+      found[3] = x - before;
+    }
+  } else {
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const long long x_wide = static_cast<long long>(r.run) * (blockIdx.x + side);
+      const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
+      if (x == total) {
+        if (tid == 0) found[side] = total;
+      } else if (before <= x && x < before + mine) {
+        int s = seg_lo, at = before, n;
+        // a thread with one segment knows its units
+        while (x >= at + (n = each == 1 ? mine : units(s))) at += n, ++s;
+        const bool next = uncut && x != at;  // on to the segment's end
+        found[side] = next ? at + n : x;
+        if (side == 0) {
+          found[2] = next ? s + 1 : s;
+          found[3] = uncut ? 0 : x - at;
+        }
       }
     }
   }
@@ -150,6 +189,38 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
   r.seg = found[2];
   r.first = found[3];
   return r;
+}
+
+// Joins. The parts of a cut segment lie in consecutive CTAs from cta0 on. Up to kOnce
+// parts are added by the CTA whose part came last. Of more, every kFan are added up
+// first, by the last of those, into the place of the group's first, and the last
+// group's CTA adds the groups: one CTA alone takes 0.2 us for a part of 8 rows, 0.4 for
+// one of 128.
+struct Join {
+  int first, stride, n;  // parts first, first + stride, ..
+  bool last;             // the segment's result; else a group's
+};
+// A part (or group, `group` true) that begins at part `part` of `parts` is written, by
+// threads that the caller has met since. True if that was the last of a join.
+template <int kOnce, int kFan>
+static __device__ __noinline__ bool part_arrives(const CacheFwdParams& p, int cta0, int part, int parts, bool group,
+                                                 Join& join) {
+  if (parts > kOnce && !group) {
+    const int g = part / kFan, n = min(kFan, parts - g * kFan);
+    // (the group's first CTA may be the first of another segment's too)
+    int32_t* at = p.groups + 2 * (cta0 + g * kFan) + (g == 0 ? 1 : 0);
+    if (n > 1) {
+      if (atomic_add_acq_rel(at, 1) != n - 1) return false;
+      *at = 0;  // ready for the next call
+      join = {g * kFan, 1, n, false};
+      return true;
+    }
+  }
+  const int n = parts > kOnce ? (parts + kFan - 1) / kFan : parts;
+  if (atomic_add_acq_rel(&p.arrived[cta0], 1) != n - 1) return false;
+  p.arrived[cta0] = 0;
+  join = {0, parts > kOnce ? kFan : 1, n, true};
+  return true;
 }
 
 // Units run_at .. + 31 of a CTA's run, one per lane: unit k of segment seg is lane

@@ -20,7 +20,16 @@
 // each, contiguous) with bulk copies into a ring of three slots for each of seven
 // consumer warps; tile i of the run goes to warp i mod 7. The warps keep separate
 // softmax states. When a piece ends each leaves its state in shared memory and goes
-// on with the next piece; the last to arrive adds them up.
+// on with the next piece; the last to arrive adds them up. The run's last piece and
+// the joins are added up by all warps.
+//
+// What bounds it. 8 rows: memory, once the cache is long (8 sequences of 131072 tokens,
+// 32 / 8 heads of 128: 322 us, 6.7 TB/s, 98 % of a copy; 64 up to 8192: 115 us, 83 %, with
+// 12000 of 210000 cycles before the first page and 14000 behind the last). 16 rows and
+// two tiles: instruction issue, about 900 instructions for a page and tile of 16 rows,
+// 2 a clock (16 sequences up to 16384, 32 / 4 heads of 64, 4 tokens: 44.6 us; floor 12.4).
+// Short ones: latency (one sequence of 1000 tokens: 10.5 us, of which 4 are the way to the
+// first page: where the run begins, page table, page, query).
 //
 // Arithmetic. Codes become fp16 (exact) and enter m16n8k16 instructions with fp32
 // accumulators; tcgen05 would need 128 rows. The products are taken transposed,
@@ -29,7 +38,7 @@
 // and a code is converted once for all row groups of the tile. A query row is
 // scaled by a power of two so that its largest element lies in [2^14, 2^15): fp16
 // then holds every bf16 element down to 2^-30 of the largest exactly. P is rounded
-// to fp16 (2^-12 relative) after scaling by the page's V scale, relative to the
+// to fp16 (2^-11 relative) after scaling by the page's V scale, relative to the
 // row's largest such product: a second running maximum, mv of log2(P * scale),
 // beside m of the scores, so that neither the weights of pages with small values
 // (in l) nor the values of pages with small weights are lost. m, mv, l and O are
@@ -50,7 +59,7 @@ namespace {
 
 // With the producer 8 warps, two for each scheduler, 255 registers a thread. Eleven
 // consumer warps (two slots each for 8 rows of d = 128) gave the same times for long
-// sequences and up to 1.5 us more for short ones: what bounds long ones is not latency.
+// sequences and up to 1.5 us more for short ones.
 constexpr int kConsumers = 7;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kSlots = 3;                           // ring slots of a consumer warp
@@ -60,6 +69,7 @@ constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a ti
 // partial results.
 constexpr int kMinRun = kConsumers;
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
+constexpr int kOnce = 4 * kConsumers, kFan = 2 * kConsumers;  // see Join
 
 // ---------------------------------------------------------------- instructions
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -68,11 +78,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ int atomic_add_acq_rel(int32_t* at, int x) {
-  int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(x) : "memory");
-  return old;
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -93,8 +98,8 @@ struct Smem {
   static constexpr int kPiece = kMeta + kConsumers * kSlots * 16;    // int [ring][8], see below
   static constexpr int kBars = kPiece + kPieceRing * 32;
   static constexpr int kNumBars = 2 * kConsumers * kSlots + 2 * kPieceRing + 1;
-  static constexpr int kScan = kBars + kNumBars * 8;  // int [kLineWords + 12], see the kernel
-  static constexpr int kBytes = kScan + (kLineWords + 12) * 4;
+  static constexpr int kScan = kBars + kNumBars * 8;  // int [kLineWords + 20], see the kernel
+  static constexpr int kBytes = kScan + (kLineWords + 20) * 4;
 };
 static_assert(Smem<128, 2>::kBytes <= 227 * 1024 && Smem<64, 2>::kBytes <= 227 * 1024, "shared memory per CTA");
 
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
   const int nseg = p.B * p.c.Hk * geo.RT;
   const Bars bar{smem_u32(smem + S::kBars)};
   int* scan = reinterpret_cast<int*>(smem + S::kScan);  // see the words below
-  enum { kCount = kLineWords, kJobs, kMerged, kJob0 };
+  enum { kCount = kLineWords, kJobs, kMerged, kJob0, kJobInts = 8 };
 
   if (tid < S::kNumBars) {
     // one arrival each, but of piece_empty and done, where every consumer warp arrives
@@ -437,20 +442,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
     ++syncs;
     return ok;
   };
-  // a partial result is written, by threads that this one has met since: the last of
-  // its segment's notes the join, which all warps do at the end of the run
-  auto arrive = [&](int seg, int cta0, int parts, int slot_id, int rows) {
-    if (atomic_add_acq_rel(&p.arrived[cta0], 1) != parts - 1) return;
-    p.arrived[cta0] = 0;  // every part is there: ready for the next call
-    int* job = scan + kJob0 + 4 * slot_id;
+  // a partial result is written, by threads that this one has met since: the last of a
+  // join notes it for the end of the run, where all warps take part
+  auto arrive = [&](int seg, int cta0, int part, int parts, int slot_id, int rows, bool group) {
+    Join x;
+    if (!part_arrives<kOnce, kFan>(p, cta0, part, parts, group, x)) return;
+    int* job = scan + kJob0 + kJobInts * slot_id;
     job[0] = seg, job[1] = cta0, job[2] = parts, job[3] = rows;
+    job[4] = x.first, job[5] = x.stride, job[6] = x.n, job[7] = x.last;
     atomicOr(&scan[kJobs], 1 << slot_id);
   };
   int seq = 0;      // ring position of this warp
   int merges = 0;   // pieces so far whose states were merged in shared memory
 
   int seg = 0, whole = 0, cta0 = 0, parts = 0, rows = 0;  // of the piece; its real rows from the sequence's start
-  int last_n = 0, last_from = 0;                // the run's last piece: states in shared memory, the first's place
+  int last_n = 0, last_from = 0;  // the run's last piece: states in shared memory, place of the first
   for (int piece = 0; ok; ++piece) {
     const int e = piece % kPieceRing;
     ok = __all_sync(0xffffffffu, cache_wait(bar.piece_full(e), (piece / kPieceRing) & 1, p.status));
@@ -808,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
       float* out = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * part_floats(D, kRows);
       st.put(reinterpret_cast<float4*>(out), out + kRows * D, lane);
       __syncwarp();
-      if (lane == 0) arrive(seg, cta0, parts, slot_id, rows);
+      if (lane == 0) arrive(seg, cta0, blockIdx.x - cta0, parts, slot_id, rows, false);
     }
   }
 
@@ -816,31 +822,37 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
   // to overlap with), each its fragments, then the parts of the segments of which this
   // CTA's came last. Both go through shared memory and one piece of code, in the order
   // of the keys.
-  for (int j = -1; ok && last_n > 0 && j < 2; ++j) {
+  for (int j = -1; ok && last_n > 0 && j < 2;) {
+    Join join = {0, 1, last_n, whole != 0};
     if (j >= 0) {
-      if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) continue;
-      seg = scan[kJob0 + 4 * j], cta0 = scan[kJob0 + 4 * j + 1], parts = scan[kJob0 + 4 * j + 2];
-      whole = 1;
-      last_n = parts;
+      if (!((*reinterpret_cast<volatile int*>(&scan[kJobs]) >> j) & 1)) {
+        ++j;
+        continue;
+      }
+      const int* job = scan + kJob0 + kJobInts * j;
+      seg = job[0], cta0 = job[1], parts = job[2], rows = job[3];
+      join = {job[4], job[5], job[6], job[7] != 0};
       last_from = 0;
     }
     const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
-    if (j >= 0) rows = scan[kJob0 + 4 * j + 3];
     constexpr int kPart = part_floats(D, kRows);
+    // part 0 begins in its CTA's run and lies in its second place
+    auto place = [&](int part) {
+      return p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * kPart;
+    };
     FragmentSums<D, NT> f;
     f.clear();
-    for (int k0 = 0; ok && k0 < last_n; k0 += kConsumers) {
-      const int n = min(last_n - k0, kConsumers);
+    for (int k0 = 0; ok && k0 < join.n; k0 += kConsumers) {
+      const int n = min(join.n - k0, kConsumers);
       if (j >= 0) {
-        if ((j > 0 || k0 > 0) && !sync_warps()) break;  // what was there has been read
-        constexpr int kUnits = kPart / 4;               // of 16 bytes
+        if (k0 > 0 && !sync_warps()) break;  // what was there has been read
+        constexpr int kUnits = kPart / 4;    // of 16 bytes
 #pragma unroll 1
         for (int i = tid; i < n * kUnits; i += 32 * kConsumers) {
-          const int k = i / kUnits, u = i - k * kUnits, part = k0 + k;
-          const float* src = p.partial + (static_cast<size_t>(cta0 + part) * 2 + (part == 0 ? 1 : 0)) * kPart + 4 * u;
+          const int k = i / kUnits, u = i - k * kUnits;
           void* dst = u < S::kFrags * 32 ? static_cast<void*>(merge + k * S::kFrags * 32 + u)
                                          : static_cast<void*>(stats + 3 * kRows * k + 4 * (u - S::kFrags * 32));
-          cp_async16(smem_u32(dst), src);  // past L1: other CTAs wrote them
+          cp_async16(smem_u32(dst), place(join.first + (k0 + k) * join.stride) + 4 * u);  // past L1: other CTAs wrote them
         }
         cp_async_wait();
       }
@@ -848,17 +860,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
       f.add(n, last_from, merge, stats, warp, lane);
     }
     if (!ok) break;
-    if (whole) {
+    if (j >= 0 && tid == 0) atomicAnd(&scan[kJobs], ~(1 << j));
+    if (join.last) {
       f.store(p, geo, b, hk, rt * kRows, rows, warp, lane);
     } else {
-      // the part that continues from the CTA before, or the one that begins here
-      const int slot_id = cta0 == static_cast<int>(blockIdx.x) ? 1 : 0;
-      float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot_id) * kPart;
-      f.put(reinterpret_cast<float4*>(part), part + kRows * D, warp, lane);
+      const int part = j < 0 ? static_cast<int>(blockIdx.x) - cta0 : join.first;
+      float* out = place(part);
+      f.put(reinterpret_cast<float4*>(out), out + kRows * D, warp, lane);
       if (!sync_warps()) break;
-      if (tid == 0) arrive(seg, cta0, parts, slot_id, rows);
+      if (tid == 0) arrive(seg, cta0, part, parts, j < 0 ? (part == 0 ? 1 : 0) : j, rows, j >= 0);
     }
-    if (j < 0) sync_warps();  // the joins are noted
+    if (!sync_warps()) break;  // the joins are noted
+    if (j < 0) j = 0;
   }
 
   // segments without a visible page: O = 0, LSE = -inf
@@ -953,6 +966,8 @@ CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   size_t off = 256;
   w.arrived = off;
   off = up256(off + kCacheMaxCtas * 4);
+  w.groups = off;
+  off = up256(off + kCacheMaxCtas * 8);
   w.partial = off;
   off = up256(off + static_cast<size_t>(kCacheMaxCtas) * 2 *
                     (g.rows == kManyRows ? cache_fwd_rows_part_floats(d) : part_floats(d, g.rows)) * 4);

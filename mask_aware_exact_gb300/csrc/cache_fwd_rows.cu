@@ -55,6 +55,7 @@ constexpr int kRows = kManyRows;
 constexpr int kMetaRing = 16;
 constexpr int kMetaInts = 16;
 constexpr int kMinRun = 4;  // steps
+constexpr int kOnce = 16, kFan = 8;  // see Join
 constexpr float kPShift = 7.f;
 constexpr float kLag = 8.f;  // mv may lag the row's largest product by this much (log2)
 
@@ -77,7 +78,7 @@ struct Layout {
   static constexpr int kStage = kV + R * kTile;
   static constexpr int kMeta = kStage + kStages * kCodes;
   static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
-  static constexpr int kBar = kWords + (kLineWords + 4) * 4;
+  static constexpr int kBar = kWords + (kLineWords + 8) * 4;
   static constexpr int kNumBars = 2 * kStages + kMetaRing + 6 * R + 3;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kBytes = kTmemSlot + 16;
@@ -663,59 +664,86 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           float* x = part + kRows * D + row;
           x[0] = m, x[kRows] = mva, x[2 * kRows] = lsum;
         }
-        __threadfence();
-        if (!sync_softmax()) break;  // all of the partial result is written
-        if (tid == 0) {
-          const bool all = atomicAdd(&p.arrived[cta0], 1) == parts - 1;
-          if (all) p.arrived[cta0] = 0;  // ready for the next call
-          words[kLineWords] = all;
-          __threadfence();
-        }
-        if (!sync_softmax()) break;
-        if (words[kLineWords] && warp_live) {
-          // every part, in the order of the keys: this thread's row and half of its columns
-          __threadfence();
-          auto part_at = [&](int i) {
-            return p.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * part_floats(D);
-          };
+        int part_no = static_cast<int>(blockIdx.x) - cta0;
+        bool group = false;
+        while (true) {
+          if (!sync_softmax()) break;  // all of the partial result is written
+          int* word = words + kLineWords;
+          if (tid == 0) {
+            Join x;
+            word[0] = part_arrives<kOnce, kFan>(p, cta0, part_no, parts, group, x);
+            word[1] = x.first, word[2] = x.stride, word[3] = x.n, word[4] = x.last;
+          }
+          if (!sync_softmax()) break;
+          if (!word[0]) break;
+          const int n = word[3], last_join = word[4];
+          part_no = word[1];
+          group = true;
           float jm = -INFINITY, jmv = -INFINITY, jl = 0.f;
-          for (int i = 0; i < parts; ++i) {
-            const float* x = part_at(i) + kRows * D + row;
-            jm = fmaxf(jm, __ldcg(x));
-            jmv = fmaxf(jmv, __ldcg(x + kRows));
-          }
-          for (int i = 0; i < parts; ++i) {
-            const float* x = part_at(i) + kRows * D + row;
-            jl += __ldcg(x + 2 * kRows) * ex2_diff(__ldcg(x), jm);
-          }
-          const float fin = out_factor(jm, jmv, jl, kPShift);
+          if (warp_live) {
+            // the parts in the order of the keys: this thread's row and half of its columns
+            const int stride = word[2];
+            auto part_at = [&](int i) {
+              const int x = part_no + i * stride;
+              return p.partial + (static_cast<size_t>(cta0 + x) * 2 + (x == 0 ? 1 : 0)) * part_floats(D);
+            };
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+              const float* x = part_at(i) + kRows * D + row;
+              jm = fmaxf(jm, __ldcg(x));
+              jmv = fmaxf(jmv, __ldcg(x + kRows));
+            }
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+              const float* x = part_at(i) + kRows * D + row;
+              jl += __ldcg(x + 2 * kRows) * ex2_diff(__ldcg(x), jm);
+            }
+            const float fin = last_join ? out_factor(jm, jmv, jl, kPShift) : 1.f;
+            float* sum = p.partial + (static_cast<size_t>(cta0 + part_no) * 2 + (part_no == 0 ? 1 : 0)) * part_floats(D);
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              const int col = w * (D / 2) + 16 * ch;
+              float y[16];
 #pragma unroll
-          for (int ch = 0; ch < D / 64; ++ch) {
-            float y[32];
+              for (int i = 0; i < 16; ++i) y[i] = 0.f;
+#pragma unroll 4
+              for (int i = 0; i < n; ++i) {
+                const float* x = part_at(i);
+                const float fx = ex2_diff(__ldcg(x + kRows * D + kRows + row), jmv);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = 0.f;
-            for (int i = 0; i < parts; ++i) {
-              const float* x = part_at(i);
-              const float fx = ex2_diff(__ldcg(x + kRows * D + kRows + row), jmv);
+                for (int j = 0; j < 4; ++j) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(x) + (col / 4 + j) * kRows + row);
+                  y[4 * j] += v.x * fx;
+                  y[4 * j + 1] += v.y * fx;
+                  y[4 * j + 2] += v.z * fx;
+                  y[4 * j + 3] += v.w * fx;
+                }
+              }
+              if (!last_join) {
+                // (only this thread reads these places of the group's first part)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(x) + ((w * (D / 2) + 32 * ch) / 4 + j) * kRows + row);
-                y[4 * j] += v.x * fx;
-                y[4 * j + 1] += v.y * fx;
-                y[4 * j + 2] += v.z * fx;
-                y[4 * j + 3] += v.w * fx;
+                for (int j = 0; j < 4; ++j)
+                  reinterpret_cast<float4*>(sum)[(col / 4 + j) * kRows + row] =
+                      make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+              } else if (live) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  *reinterpret_cast<uint4*>(o + 16 * ch + 8 * i) = make_uint4(
+                      pack_bf16x2(y[8 * i] * fin, y[8 * i + 1] * fin), pack_bf16x2(y[8 * i + 2] * fin, y[8 * i + 3] * fin),
+                      pack_bf16x2(y[8 * i + 4] * fin, y[8 * i + 5] * fin), pack_bf16x2(y[8 * i + 6] * fin, y[8 * i + 7] * fin));
               }
             }
-            if (live) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(o + 32 * ch + 8 * i) = make_uint4(
-                    pack_bf16x2(y[8 * i] * fin, y[8 * i + 1] * fin), pack_bf16x2(y[8 * i + 2] * fin, y[8 * i + 3] * fin),
-                    pack_bf16x2(y[8 * i + 4] * fin, y[8 * i + 5] * fin), pack_bf16x2(y[8 * i + 6] * fin, y[8 * i + 7] * fin));
-            }
+            if (last_join && live && w == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(jm, jl);
           }
-          if (live && w == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] = out_lse(jm, jl);
+          if (last_join) break;
+          if (!sync_softmax()) break;  // the statistics of the group's first part have been read
+          if (warp_live && w == 0) {
+            float* x = p.partial + (static_cast<size_t>(cta0 + part_no) * 2 + (part_no == 0 ? 1 : 0)) * part_floats(D) +
+                       kRows * D + row;
+            x[0] = jm, x[kRows] = jmv, x[2 * kRows] = jl;
+          }
         }
+        if (!ok) break;
       }
       if (!sync_softmax()) break;  // red (Q's place) and the word have been read
     }

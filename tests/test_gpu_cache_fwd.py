@@ -317,6 +317,22 @@ def test_long_sequence(N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,N,d,lens", [
+    (4, 1, 64, [64 * 700]), (4, 1, 128, [64 * 230 + 5, 64 * 60]), (6, 3, 64, [30000, 100, 0]),
+    (2, 40, 64, [64 * 420]), (1, 140, 128, [64 * 330 + 1]), (3, 50, 128, [20000, 64 * 40, 9000])])
+def test_sequences_cut_into_many_parts(H, N, d, lens):
+    """Enough parts of one segment that they are added up in groups first; the counters
+    are back at zero afterwards, so that a second call gives the same bits."""
+    fm = need_gpu()
+    q, cache, table, _ = make(fm, len(lens), H, 1, N, d, lens, seed=7)
+    ws = fm.alloc_cache_workspace(len(lens), H, 1, N, d, table.shape[1])
+    o, lse = run(fm, q, cache, table, lens, ws=ws)
+    check(o, lse, q, cache, table, lens)
+    o2, lse2 = run(fm, q, cache, table, lens, ws=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
 def test_codes_behind_two_gigabytes():
     # pages whose offset passes 2^31 bytes
     fm = need_gpu()
