@@ -54,7 +54,9 @@ constexpr int kThreads = 512;
 constexpr int kRows = kManyRows;
 constexpr int kMetaRing = 16;
 constexpr int kMetaInts = 16;
-constexpr int kMinRun = 4;  // steps
+// Steps a run has at least. One sequence of 4000 tokens, 2 cache heads, 128 rows, at
+// least 2 / 4 / 8 steps: 29.7 / 26.3 / 27.1 us.
+constexpr int kMinRun = 4;
 constexpr int kOnce = 16, kFan = 8;  // see Join
 constexpr float kPShift = 7.f;
 constexpr float kLag = 8.f;  // mv may lag the row's largest product by this much (log2)
