@@ -355,7 +355,7 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
  * page_table is int32 [B, max_pages]: entry i of a row is the page holding the
  * sequence's tokens [64 i, 64 i + 64). Only the entries of pages that a call
  * needs are read; the rest may hold anything. d in {64, 128}; FM_PAGE *
- * max_pages <= FM_MAX_SEQLEN; B * H * N < 2^31, B < 2^16, and B * Hk * ceil(H / Hk *
+ * max_pages <= FM_MAX_SEQLEN; B * H * N < 2^31 - 255, B < 2^16, and B * Hk * ceil(H / Hk *
  * N / 128) * max_pages < 2^31. Entries, lengths and starts live on the device:
  * the kernels check each one they use, leave the access out when it is out of
  * range and record it, so that flashmask_check_status() returns FM_ERR_PAGE
@@ -422,7 +422,9 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * end, hold has no influence, NaN included. A query row with a value that is
  * not finite gives NaN.
  *   qs, os: strides of Q and O in elements for batch, head and token (multiples
- *   of 8; the last dimension contiguous, 16-byte aligned).
+ *   of 8; the last dimension contiguous, 16-byte aligned). O may be Q itself with
+ *   the same strides; otherwise O and LSE overlap neither each other nor an input.
+ *   scale: positive, scale / ln 2 finite.
  * Results do not depend on the order in which CTAs run (the same call gives the
  * same bits); how a sequence's sum is split depends on the whole batch, so its
  * last bits may differ beside other sequences. Asynchronous on `stream`. */

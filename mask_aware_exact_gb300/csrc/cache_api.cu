@@ -52,7 +52,8 @@ bool cache_shape_ok(int B, int H, int Hk, int N, int d, int max_pages) {
   if (d != 64 && d != 128) return false;
   if (H % Hk != 0 || Hk > 65535 || B > 65535) return false;
   if (max_pages > FM_MAX_SEQLEN / FM_PAGE || N > FM_MAX_SEQLEN) return false;
-  if (static_cast<long long>(B) * H > 0x7fffffffLL / N) return false;  // rows fit 32 bits
+  // rows fit 32 bits, with those that fill a tile up
+  if (static_cast<long long>(B) * H > (0x7fffffffLL - 255) / N) return false;
   return fm::cache_line_ok(B, H, Hk, N, max_pages);
 }
 
@@ -182,7 +183,8 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   if (!aligned16(q) || !aligned16(o) || !strides_ok(qs) || !strides_ok(os)) return FM_ERR_INVALID_ARG;
   if (!aligned4(page_table) || !aligned4(lens) || !aligned4(q_lens) || !aligned4(lse))
     return FM_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return FM_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2) || !(scale > 0.f)) return FM_ERR_INVALID_ARG;
   if (mask && !vectors_ok(mask)) return FM_ERR_INVALID_ARG;
   if (!cache_shape_ok(B, H, cache->Hk, N, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
   if (mask && (mask->Hm <= 0 || H % mask->Hm != 0)) return FM_ERR_UNSUPPORTED;
@@ -211,7 +213,7 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   p.B = B;
   p.H = H;
   p.N = N;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.o = static_cast<uint16_t*>(o);
   for (int i = 0; i < 3; ++i) {
     p.qs[i] = qs[i];

@@ -10,7 +10,6 @@ binding still works but the first call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import struct
@@ -622,8 +621,8 @@ def flashmask_rope_bwd(dq, dk, freqs, positions=None, interleaved=False, mscale=
 class KVCache:
     """Keys and values as e4m3 codes in pages of FM_PAGE tokens with one scale per
     page and head: k8 [pages, Hk, 64, d], v8 [pages, Hk, d, 64] (float8_e4m3fn,
-    V transposed), kscale, vscale fp32 [pages, Hk]. A handle: its tensors are
-    checked once, at its first use."""
+    V transposed), kscale, vscale fp32 [pages, Hk]. Its tensors are checked at
+    its first use, and again if one of them has moved since."""
 
     k8: torch.Tensor
     v8: torch.Tensor
@@ -641,9 +640,17 @@ class KVCache:
     def tensors(self):
         return self.k8, self.v8, self.kscale, self.vscale
 
-    @functools.cached_property
+    @property
     def _handle(self):
         """(C struct, Hk, d, device index)"""
+        at = (self.k8.data_ptr(), self.v8.data_ptr(), self.kscale.data_ptr(), self.vscale.data_ptr())
+        made = self.__dict__.get("_made")
+        if made is None or made[0] != at:
+            made = at, self._check()
+            object.__setattr__(self, "_made", made)
+        return made[1]
+
+    def _check(self):
         k8 = self.k8
         index = k8.get_device()
         if k8.dim() != 4 or k8.shape[2] != FM_PAGE or index < 0:

@@ -44,19 +44,23 @@ def cache_arrays(c):
             c.vscale.double().cpu().numpy())
 
 
-def attention_bounds(ref):
-    """Elementwise error bounds of O and LSE from the oracle's (O, LSE, PV, smag, top).
+def attention_bounds(ref, keys):
+    """Elementwise error bounds of O and LSE from the oracle's (O, LSE, PV, smag, top)
+    for at most `keys` keys.
 
-    delta bounds the error of a score: fp32 sums of d products in the tensor
-    cores (alignment to the largest loses up to 2^-22 of it a step, at most 8
-    steps of 32: 2^-19 of sum |q k|), the query as two or more parts of 4 bits
-    (2^-22 of its largest), and 2^-22 of the score in the exponent. P carries
-    2 delta + 2^-20 (the exponential's error) relative and 2^-8 for its own
-    rounding to two parts of 4 bits; parts below the smallest step lose up to
-    2^-22 of the row's largest P_j times value scale for each key (times a code
-    of at most 448). O is rounded to bf16 (2^-8)."""
+    delta bounds the error of a score: the products of fp16 query and codes are exact,
+    their fp32 sums lose up to 2^-22 of the largest term in each of at most 8 steps
+    (2^-19 of sum |q k|), and the exponent 2^-22 of the score. P carries 2 delta +
+    2^-20 (the exponential's error) relative and 2^-11 for its rounding to fp16; below
+    fp16's normal range half a step is 2^-32 of the row's largest P_j times value scale
+    or less (2^-25 of a P stored as 2^7 P or more), for each key, times a code of at
+    most 448. Sums over the keys add in chains of at most keys / 4 terms (l) or keys /
+    16 instructions (O), each a step of 2^-23: keys * 2^-25 covers either. O is rounded
+    to bf16 (2^-8)."""
     o, lse, pv, smag, top = ref
     delta = smag * 2.0 ** -18 + 2.0 ** -20
-    tol_o = pv * (2.0 ** -8 + 2 * delta[..., None]) + top[..., None] * 448 * 2.0 ** -22 + np.abs(o) * 2.0 ** -8 * 1.02 + 1e-30
-    tol_lse = delta + np.abs(np.where(np.isfinite(lse), lse, 0)) * 2.0 ** -22 + 2.0 ** -20
+    sums = keys * 2.0 ** -25
+    tol_o = pv * (2.0 ** -11 + 2.0 ** -19 + 2 * sums + 2 * delta[..., None]) + \
+        top[..., None] * 448 * 2.0 ** -32 * keys + np.abs(o) * 2.0 ** -8 * 1.02 + 1e-30
+    tol_lse = delta + np.abs(np.where(np.isfinite(lse), lse, 0)) * 2.0 ** -22 + 2.0 ** -20 + sums
     return tol_o, tol_lse

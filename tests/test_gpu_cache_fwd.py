@@ -39,7 +39,7 @@ def check(o, lse, q, cache, table, lens, q_lens=None, mask=None, scale=None, nan
     arrays = cache_arrays(cache)
     f = lambda t: t.double().cpu().numpy()
     ref = C.attend(f(q), *arrays, table.cpu().numpy(), lens, q_lens, scale, **vec)
-    tol_o, tol_l = attention_bounds(ref)
+    tol_o, tol_l = attention_bounds(ref, max(max(lens), 1))
     go, gl = f(o), f(lse)
     for b in range(B):
         live = N if q_lens is None else q_lens[b]
@@ -267,6 +267,31 @@ def test_strides_streams_and_repeatability():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 5, 70])
+def test_output_over_the_query(N):
+    fm = need_gpu()
+    lens = [700 + N, 64 * 90, N]
+    q, cache, table, _ = make(fm, 3, 8, 2, N, 128, lens, seed=3)
+    o, lse = run(fm, q, cache, table, lens)
+    ws = fm.alloc_cache_workspace(3, 8, 2, N, 128, table.shape[1])
+    o2, lse2 = fm.flashmask_fwd_cache(q, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), ws, o=q)
+    assert o2.data_ptr() == q.data_ptr() and torch.equal(o, q) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+def test_a_cache_whose_storage_has_moved():
+    """A handle made before its tensor got another storage reads the new one."""
+    fm = need_gpu()
+    lens = [200]
+    q, cache, table, gen = make(fm, 1, 4, 2, 1, 64, lens, seed=4)
+    run(fm, q, cache, table, lens)
+    other = random_cache(fm, cache.k8.shape[0], 2, 64, gen)
+    cache.k8.set_(other.k8)
+    o, lse = run(fm, q, cache, table, lens)
+    check(o, lse, q, cache, table, lens)
+
+
+@pytest.mark.gpu
 def test_one_workspace_serves_all_sizes_in_turn():
     fm = need_gpu()
     ws = fm.alloc_cache_workspace(8, 32, 4, 40, 128, 40)
@@ -412,7 +437,7 @@ def test_refusals(lib):
     upper = fm._FmMask(FAKE, FAKE, None, FAKE, 1, 1)
     for bad in (dict(q=None), dict(q=FAKE + 8), dict(qs=(0, 4, 64)), dict(k8=None), dict(pages=0),
                 dict(lens=None), dict(mask=half), dict(mask=upper), dict(scale=0.0),
-                dict(scale=float("inf")), dict(o=None), dict(o=FAKE + 2), dict(lens=FAKE + 2),
+                dict(scale=float("inf")), dict(scale=3e38), dict(o=None), dict(o=FAKE + 2), dict(lens=FAKE + 2),
                 dict(qs=(0, 0, 64)),  # as O's strides they let heads overlap
                 dict(mask=fm._FmMask(FAKE + 4, FAKE, None, None, 1, 1))):
         assert call(lib, **bad) == fm.FM_ERR_INVALID_ARG, bad

@@ -71,7 +71,7 @@ def test_prompt_in_chunks_then_tokens(d, masked):
             assert np.array_equal(got, ref)
         held = [h + n for h, n in zip(held, new)]
         ref = C.attend(f(q), *want, table.cpu().numpy(), held, new, 1 / math.sqrt(d), **vec)
-        tol_o, tol_l = attention_bounds(ref)
+        tol_o, tol_l = attention_bounds(ref, max(held))
         for b, n in enumerate(new):
             assert np.all(np.abs(f(o)[b, :, :n] - ref[0][b, :, :n]) <= tol_o[b, :, :n])
             assert np.all(np.abs(f(lse)[b, :, :n] - ref[1][b, :, :n]) <= tol_l[b, :, :n])
