@@ -77,6 +77,7 @@ struct Line {
   int lo, hi;      // this CTA's run
   int seg, first;  // segment of its first unit, and that unit's number in it
   bool any_empty;  // some segment has no unit
+  bool whole;      // no segment is cut
 };
 constexpr int kLineWords = 40;  // ints of shared memory for find_run
 // Segments of up to this many pages (or an eighth of a run) are not cut: a join takes
@@ -149,6 +150,7 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
   const bool uncut = longest <= max(kUncut / pages, even / 8);
   // the least run only keeps cut segments from falling into many parts
   r.run = max(uncut ? 1 : min_run, even);
+  r.whole = uncut;
   const int per = nseg > 0 ? static_cast<int>(gridDim.x) / nseg : 0;  // parts a segment may have
   const int cut = per >= 2 ? max(min_run, (longest + per - 1) / per) : 0;
   if (!uncut && per >= 2 && cut <= even + kApart / pages) {
@@ -159,7 +161,7 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
     const long long x_wide = static_cast<long long>(cut) * blockIdx.x;
     const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
     if (x == total) {
-      if (tid == 0) found[0] = found[1] = total;
+      if (tid == 0) found[0] = found[1] = total, found[2] = nseg, found[3] = 0;
     } else if (before <= x && x < before + filled) {
       found[0] = x;
       found[1] = min(x + cut, before + mine);
@@ -172,11 +174,14 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
       const long long x_wide = static_cast<long long>(r.run) * (blockIdx.x + side);
       const int x = static_cast<int>(min(x_wide, static_cast<long long>(total)));
       if (x == total) {
-        if (tid == 0) found[side] = total;
+        if (tid == 0) {
+          found[side] = total;
+          if (side == 0) found[2] = nseg, found[3] = 0;  // no unit, no segment
+        }
       } else if (before <= x && x < before + mine) {
         int s = seg_lo, at = before, n;
         // a thread with one segment knows its units
-        while (x >= at + (n = each == 1 ? mine : units(s))) at += n, ++s;
+        while (x >= at + (n = each == 1 ? mine : units(s)) && s + 1 < seg_hi) at += n, ++s;
         const bool next = uncut && x != at;  // on to the segment's end
         found[side] = next ? at + n : x;
         if (side == 0) {
@@ -292,7 +297,13 @@ static __device__ __noinline__ bool cache_wait_slow(uint32_t bar, uint32_t parit
 __device__ __forceinline__ bool cache_wait(uint32_t bar, uint32_t parity, int32_t* status) {
   return mbar_test_wait(bar, parity) || cache_wait_slow(bar, parity, status);
 }
-// The same for a counter in shared memory that only grows.
+// A CTA that does not find the units of its run, because a caller wrote lens or q_lens
+// while the call ran, gives up like a wait that ran out.
+static __device__ __noinline__ bool lengths_moved(int32_t* status) {
+  if ((threadIdx.x & 31) == 0) record_failure(status, kStatusTimeout, kSiteCacheWait);
+  return false;
+}
+// cache_wait_slow for a counter in shared memory that only grows.
 __device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* status) {
   const volatile int* at = count;
   const uint64_t t0 = global_timer_ns();

@@ -68,6 +68,8 @@ constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a ti
 // Pages a run has at least: one for each consumer warp. One sequence of 2500 tokens, 8
 // cache heads, at least 4 / 7 / 14 pages: 13.4 / 12.7 / 13.7 us; 6000: 16.1 / 14.4 / 13.9.
 constexpr int kMinRun = kConsumers;
+// Uncut segments, at least this many for each CTA: every segment is one warp's.
+constexpr int kAlone = 7;
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 constexpr int kOnce = 4 * kConsumers, kFan = 2 * kConsumers;  // see Join
 
@@ -318,15 +320,94 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 
   const Line line = find_run<kThreads>(nseg, kMinRun, 1, scan, [&](int seg) { return pages_of<kVec>(p, geo, seg); });
   const int run = line.run, run_lo = line.lo, run_hi = line.hi;
+  const bool alone = line.whole && nseg >= kAlone * static_cast<int>(gridDim.x);
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
     int seg = line.seg, k = line.first;
     const int tiles = run_hi - run_lo;
     bool ok = true;
+    // This lane's page to warp w, at positions q and q + 1 of its ring. K's copy is on its
+    // way before the scales are waited for: a barrier counts bytes that land before they
+    // are expected.
+    auto feed_k = [&](int w, int q, int logical, size_t off) {
+      const int slot = q % kSlots;
+      if (q >= kSlots && !cache_wait(bar.empty(w, slot), (q / kSlots - 1) & 1, p.status)) return false;
+      if (logical >= 0)
+        bulk_load(smem_u32(smem + S::kRing + (w * kSlots + slot) * S::kHalf), p.c.k8 + off, S::kHalf, bar.full(w, slot));
+      return true;
+    };
+    auto feed_v = [&](int w, int q, int logical, int cut, size_t off, float k_s, float v_s) {
+      const int slot_k = q % kSlots, slot = (q + 1) % kSlots;
+      *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot_k) =
+          make_int4(logical, cut, __float_as_int(k_s), __float_as_int(v_s));
+      mbar_arrive_expect_tx(bar.full(w, slot_k), logical >= 0 ? S::kHalf : 0);
+      if (q + 1 >= kSlots && !cache_wait(bar.empty(w, slot), ((q + 1) / kSlots - 1) & 1, p.status)) return false;
+      mbar_arrive_expect_tx(bar.full(w, slot), logical >= 0 ? S::kHalf : 0);
+      if (logical >= 0)
+        bulk_load(smem_u32(smem + S::kRing + (w * kSlots + slot) * S::kHalf), p.c.v8 + off, S::kHalf, bar.full(w, slot));
+      return true;
+    };
     int pieces = 0;  // published so far
     int done = 0;
-    while (ok && done < tiles) {
+    int issued = 0;  // tiles of warp `lane`, if segments are one warp's
+    if (alone) {
+      // lane w feeds warp w, whose piece entries are 2 w and 2 w + 1; a lane that has
+      // issued its segment takes the next of the run
+      auto units = [&](int sg) { return sg < nseg ? pages_of<kVec>(p, geo, sg) : 0; };
+      int left = tiles, next = 0, my_seg = 0, my_k = 0, my_n = 0;
+      int n_all = units(seg + lane);  // of segments seg .. seg + 31 (seg is nseg if the run is empty)
+      bool fed = lane < kConsumers;
+      while (ok && __any_sync(0xffffffffu, fed)) {
+        uint32_t need = __ballot_sync(0xffffffffu, fed && my_k == my_n);
+        while (need != 0 && left > 0 && seg < nseg) {
+          if (next == 32) {
+            seg += 32;
+            next = 0;
+            n_all = units(seg + lane);
+          }
+          const int n = __shfl_sync(0xffffffffu, n_all, next);
+          if (n > 0) {
+            if (lane == __ffs(need) - 1) my_seg = seg + next, my_k = 0, my_n = n;
+            need &= need - 1;
+            left -= n;
+          }
+          ++next;
+        }
+        if (fed) {
+          const bool end = (need >> lane) & 1u;  // nothing is left: an empty piece
+          if (end || my_k == 0) {
+            const int e = 2 * lane + (pieces & 1);
+            if (pieces >= 2) ok = cache_wait(bar.piece_empty(e), (pieces / 2 - 1) & 1, p.status);
+            if (ok) {
+              int* d = reinterpret_cast<int*>(smem + S::kPiece) + 8 * e;
+              d[0] = my_seg, d[1] = 0, d[2] = end ? 0 : my_n, d[3] = 1;
+              mbar_arrive(bar.piece_full(e));
+            }
+            ++pieces;
+          }
+          fed = !end;
+        }
+        if (ok && fed) {
+          const int bh = geo.by_RT.div(my_seg), rt = my_seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
+          int cut;
+          const int logical = page_on_line<kVec>(p, geo, b, hk, rt, my_k, cut);
+          int page = p.table[static_cast<size_t>(b) * p.max_pages + logical];
+          if (page < 0 || page >= p.c.pages) {
+            record_failure(p.status, kStatusPage, kSiteCachePage);
+            page = -1;
+          }
+          const size_t ph = static_cast<size_t>(max(page, 0)) * p.c.Hk + hk;
+          const float ks = p.c.kscale[ph], vs = p.c.vscale[ph];
+          const int there = page < 0 ? -1 : logical;
+          ok = feed_k(lane, 2 * issued, there, ph * S::kHalf) && feed_v(lane, 2 * issued, there, cut, ph * S::kHalf, ks, vs);
+          ++issued;
+          ++my_k;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+    while (!alone && ok && done < tiles) {
       // the next tiles of the run, one per lane, over the next 32 segments
       int my_seg, my_k, n_j;
       const int avail = next_units(
@@ -375,26 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
           }
         }
         pieces += __popc(who);
-        const int w = at % kConsumers, q = 2 * (at / kConsumers);
-        const int slot_k = q % kSlots, slot_v = (q + 1) % kSlots;
-        const uint32_t dst = smem_u32(smem + S::kRing + w * kSlots * S::kHalf);
-        // K's copy is on its way before the scales are waited for: a barrier counts
-        // bytes that land before they are expected
-        if (mine_too && ok) {
-          if (q >= kSlots) ok = cache_wait(bar.empty(w, slot_k), (q / kSlots - 1) & 1, p.status);
-          if (ok && pg >= 0) bulk_load(dst + slot_k * S::kHalf, p.c.k8 + off, S::kHalf, bar.full(w, slot_k));
-        }
+        const int w = at % kConsumers, q = 2 * (at / kConsumers), there = pg < 0 ? -1 : lg;
+        if (mine_too && ok) ok = feed_k(w, q, there, off);
         const float k_s = __shfl_sync(0xffffffffu, ks, src), v_s = __shfl_sync(0xffffffffu, vs, src);
-        if (mine_too && ok) {
-          *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot_k) =
-              make_int4(pg < 0 ? -1 : lg, ct, __float_as_int(k_s), __float_as_int(v_s));
-          mbar_arrive_expect_tx(bar.full(w, slot_k), pg >= 0 ? S::kHalf : 0);
-          if (q + 1 >= kSlots) ok = cache_wait(bar.empty(w, slot_v), ((q + 1) / kSlots - 1) & 1, p.status);
-          if (ok) {
-            mbar_arrive_expect_tx(bar.full(w, slot_v), pg >= 0 ? S::kHalf : 0);
-            if (pg >= 0) bulk_load(dst + slot_v * S::kHalf, p.c.v8 + off, S::kHalf, bar.full(w, slot_v));
-          }
-        }
+        if (mine_too && ok) ok = feed_v(w, q, there, ct, off, k_s, v_s);
         ok = __all_sync(0xffffffffu, ok);
         done += in_group;
       }
@@ -405,9 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
       } else {
         seg += 32;
         k = 0;
+        // the lengths are not those of the run's search any more
+        if (seg >= nseg) ok = lengths_moved(p.status);
       }
     }
-    if (ok && lane == 0) {  // the end: an empty piece
+    if (!alone && ok && lane == 0) {  // the end: an empty piece
       const int e = pieces % kPieceRing;
       if (pieces >= kPieceRing) ok = cache_wait(bar.piece_empty(e), (pieces / kPieceRing - 1) & 1, p.status);
       if (ok) {
@@ -415,14 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
         mbar_arrive(bar.piece_full(e));
       }
     }
-    if (!ok && lane == 0) {
+    if (!ok && lane < kConsumers) {
       // copies in flight land before the CTA's shared memory is given up
-      for (int w = 0; w < kConsumers; ++w)
-        for (int s = 0; s < kSlots; ++s) {
-          const int issued = (done + kConsumers - 1 - w) / kConsumers * 2;  // at most, of warp w
-          for (int seq = max(0, issued - kSlots); seq < issued; ++seq)
-            if (seq % kSlots == s) mbar_wait_for(bar.full(w, s), (seq / kSlots) & 1, nullptr, 1000000ull);
-        }
+      const int most = alone ? 2 * issued : (done + kConsumers - 1 - lane) / kConsumers * 2;
+      for (int seq = max(0, most - kSlots); seq < most; ++seq)
+        mbar_wait_for(bar.full(lane, seq % kSlots), (seq / kSlots) & 1, nullptr, 1000000ull);
     }
     return;
   }
@@ -458,280 +522,282 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
   int seg = 0, whole = 0, cta0 = 0, parts = 0, rows = 0;  // of the piece; its real rows from the sequence's start
   int last_n = 0, last_from = 0;  // the run's last piece: states in shared memory, place of the first
   for (int piece = 0; ok; ++piece) {
-    const int e = piece % kPieceRing;
-    ok = __all_sync(0xffffffffu, cache_wait(bar.piece_full(e), (piece / kPieceRing) & 1, p.status));
+    const int e = alone ? 2 * warp + (piece & 1) : piece % kPieceRing;
+    ok = __all_sync(0xffffffffu, cache_wait(bar.piece_full(e), (alone ? piece / 2 : piece / kPieceRing) & 1, p.status));
     if (!ok) break;
     const int* d = reinterpret_cast<const int*>(smem + S::kPiece) + 8 * e;
     const int first = d[1], count = d[2], slot_id = d[4];
     seg = d[0], whole = d[3], cta0 = d[5], parts = d[6];
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar.piece_empty(e));
+    if (lane < (alone ? kConsumers : 1)) mbar_arrive(bar.piece_empty(e));  // (one arrival for each warp)
     if (count == 0) break;
+    const int writers = alone ? 1 : min(count, kConsumers);  // warps that have tiles, from first % 7 on
+    const int mine = alone ? 0 : (warp - first % kConsumers + kConsumers) % kConsumers;
+    const bool last = !alone && first + count == run_hi - run_lo;
+    if (mine >= writers && !last) {  // on to the next piece, before the others
+      merges += writers > 1;
+      continue;
+    }
 
     const int bh = geo.by_RT.div(seg), rt = seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
-    const RowTile r = row_tile(p, geo, b, rt, lane == 0 && warp == 0);
+    const RowTile r = row_tile(p, geo, b, rt, lane == 0);
     rows = geo.G * r.live;
     State<D, NT> st;
     st.clear();
-    uint32_t qf[NT][D / 16][2];
-    float crow[NT][2];
-    int lim[NT][2], pos[NT][2];
-    size_t mrow[NT][2];
-    int all_lim = r.len;  // keys that every row of the tile sees as far as causality and length go
+    if (mine < writers) {
+      uint32_t qf[NT][D / 16][2];
+      float crow[NT][2];
+      int lim[NT][2], pos[NT][2];
+      size_t mrow[NT][2];
+      int all_lim = r.len;  // keys that every row of the tile sees as far as causality and length go
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // the query row that this lane brings in, 16 elements of each half: d = 64 half + 16 c ..
-      // (read whether real or not, as long as it exists: the number of real rows is
-      // still on its way)
-      const int rr = rt * kRows + 8 * t + g;
-      const bool there = rr < geo.G * p.N, live = rr < rows;
-      const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
-      uint4 x[D / 64][2];
-      const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
+      for (int t = 0; t < NT; ++t) {
+        // the query row that this lane brings in, 16 elements of each half: d = 64 half + 16 c ..
+        // (read whether real or not, as long as it exists: the number of real rows is
+        // still on its way)
+        const int rr = rt * kRows + 8 * t + g;
+        const bool there = rr < geo.G * p.N, live = rr < rows;
+        const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
+        uint4 x[D / 64][2];
+        const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
 #pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf)
+        for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          x[hf][u] = there ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t top = 0;
+          for (int u = 0; u < 2; ++u)
+            x[hf][u] = there ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t top = 0;
 #pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf)
+        for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (!live) x[hf][u] = make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t mk = 0x7fff7fffu;
-          const uint32_t a = __vmaxu2(__vmaxu2(x[hf][u].x & mk, x[hf][u].y & mk), __vmaxu2(x[hf][u].z & mk, x[hf][u].w & mk));
-          top = max(top, max(a & 0xffffu, a >> 16));
+          for (int u = 0; u < 2; ++u) {
+            if (!live) x[hf][u] = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t mk = 0x7fff7fffu;
+            const uint32_t a = __vmaxu2(__vmaxu2(x[hf][u].x & mk, x[hf][u].y & mk), __vmaxu2(x[hf][u].z & mk, x[hf][u].w & mk));
+            top = max(top, max(a & 0xffffu, a >> 16));
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest element's exponent becomes 14; rows that are not finite become NaN
+        const bool bad = top >= 0x7f80u;
+        const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+        const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
+        const float back = p.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4& v = x[hf][u >> 1];
+            const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
+            qf[t][4 * hf + u][0] = pack_f16x2(__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f);
+            qf[t][4 * hf + u][1] = pack_f16x2(__uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f);
+          }
+        // the rows whose scores this lane holds
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          crow[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
+          const int r2 = rt * kRows + 8 * t + 2 * c + e;
+          const int tok2 = geo.by_G.div(r2), h2 = hk * geo.G + r2 - tok2 * geo.G;
+          pos[t][e] = r.shift + tok2;
+          lim[t][e] = r2 < rows && p.mask.causal ? min(r.len, pos[t][e] + 1) : r.len;
+          all_lim = min(all_lim, lim[t][e]);
+          mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h2)) *
+                                  static_cast<size_t>(p.max_pages * kPage)
+                            : 0;
         }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the largest element's exponent becomes 14; rows that are not finite become NaN
-      const bool bad = top >= 0x7f80u;
-      const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
-      const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
-      const float back = p.scale_log2 * __int_as_float((127 - up) << 23);
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint4& v = x[hf][u >> 1];
-          const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
-          qf[t][4 * hf + u][0] = pack_f16x2(__uint_as_float(w0 << 16) * f, __uint_as_float(w0 & 0xffff0000u) * f);
-          qf[t][4 * hf + u][1] = pack_f16x2(__uint_as_float(w1 << 16) * f, __uint_as_float(w1 & 0xffff0000u) * f);
-        }
-      // the rows whose scores this lane holds
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        crow[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
-        const int r2 = rt * kRows + 8 * t + 2 * c + e;
-        const int tok2 = geo.by_G.div(r2), h2 = hk * geo.G + r2 - tok2 * geo.G;
-        pos[t][e] = r.shift + tok2;
-        lim[t][e] = r2 < rows && p.mask.causal ? min(r.len, pos[t][e] + 1) : r.len;
-        all_lim = min(all_lim, lim[t][e]);
-        mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h2)) *
-                                static_cast<size_t>(p.max_pages * kPage)
-                          : 0;
       }
-    }
-    all_lim = __reduce_min_sync(0xffffffffu, all_lim);
+      all_lim = __reduce_min_sync(0xffffffffu, all_lim);
 
-    const int t0 = first + ((warp - first) % kConsumers + kConsumers) % kConsumers;
-    for (int tile = t0; ok && tile < first + count; tile += kConsumers) {
-      const int sk = seq % kSlots, sv = (seq + 1) % kSlots;
-      ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sk), (seq / kSlots) & 1, p.status));
-      if (!ok) break;
-      const int4 meta = *(reinterpret_cast<const int4*>(smem + S::kMeta) + warp * kSlots + sk);
-      const float lvs = __log2f(__int_as_float(meta.w));
-      const int j0 = meta.x * kPage;
-      // S^T: instruction u holds the keys kb + 4 u and kb + 4 u + 2 of this lane
-      const int kb = 16 * (g >> 1) + (g & 1);
-      float s[4][NT][4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][t][i] = 0.f;
-      const uint8_t* kbase = ring + sk * S::kHalf + kb * D + 16 * c;
-#pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        uint4 w[4][2];
+      for (int left = alone ? count : (count - mine + kConsumers - 1) / kConsumers; ok && left > 0; --left) {
+        const int sk = seq % kSlots, sv = (seq + 1) % kSlots;
+        ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sk), (seq / kSlots) & 1, p.status));
+        if (!ok) break;
+        const int4 meta = *(reinterpret_cast<const int4*>(smem + S::kMeta) + warp * kSlots + sk);
+        const float lvs = __log2f(__int_as_float(meta.w));
+        const int j0 = meta.x * kPage;
+        // S^T: instruction u holds the keys kb + 4 u and kb + 4 u + 2 of this lane
+        const int kb = 16 * (g >> 1) + (g & 1);
+        float s[4][NT][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            w[u][x] = *reinterpret_cast<const uint4*>(kbase + (4 * u + 2 * x) * D + 64 * hf);
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+            for (int i = 0; i < 4; ++i) s[u][t][i] = 0.f;
+        const uint8_t* kbase = ring + sk * S::kHalf + kb * D + 16 * c;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t a[4];
-            codes_to_f16(word(w[u][0], k), a[0], a[2]);
-            codes_to_f16(word(w[u][1], k), a[1], a[3]);
+        for (int hf = 0; hf < D / 64; ++hf) {
+          uint4 w[4][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(s[u][t], a, qf[t][4 * hf + k][0], qf[t][4 * hf + k][1]);
-          }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.empty(warp, sk));
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              w[u][x] = *reinterpret_cast<const uint4*>(kbase + (4 * u + 2 * x) * D + 64 * hf);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t a[4];
+              codes_to_f16(word(w[u][0], k), a[0], a[2]);
+              codes_to_f16(word(w[u][1], k), a[1], a[3]);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816(s[u][t], a, qf[t][4 * hf + k][0], qf[t][4 * hf + k][1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.empty(warp, sk));
 
-      // s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e; ck times it is the score in
-      // log2 units (ck > 0 keeps masked scores at -inf)
-      const float kscale = __int_as_float(meta.z);
-      const bool tail = meta.x < 0 || j0 + kPage > all_lim;
-      // Each pass goes over all rows of the lane, so that their chains overlap; a row
-      // pair's elements go through packed instructions.
-      float ck[NT][2], top[NT][2];
+        // s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e; ck times it is the score in
+        // log2 units (ck > 0 keeps masked scores at -inf)
+        const float kscale = __int_as_float(meta.z);
+        const bool tail = meta.x < 0 || j0 + kPage > all_lim;
+        // Each pass goes over all rows of the lane, so that their chains overlap; a row
+        // pair's elements go through packed instructions.
+        float ck[NT][2], top[NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ck[t][e] = fmaxf(crow[t][e] * kscale, 1.17549435e-38f);
-      if (__builtin_expect(tail || meta.y, 0)) {
+          for (int e = 0; e < 2; ++e) ck[t][e] = fmaxf(crow[t][e] * kscale, 1.17549435e-38f);
+        if (__builtin_expect(tail || meta.y, 0)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // bit 2 u + x: key kb + 4 u + 2 x is visible
+              const int n = meta.x < 0 ? 0 : min(max(lim[t][e] - (j0 + kb), 0), 16);
+              uint32_t see = (1u << ((n + 1) >> 1)) - 1u;
+              if constexpr (kVec) {
+                if (meta.y && meta.x >= 0) {
+                  const size_t at = mrow[t][e] + j0 + (kb & ~1);
+                  if (p.mask.lts) see &= ~hidden8(p.mask.lts + at, p.mask.lte + at, pos[t][e], g & 1);
+                  if (p.mask.uts) see &= ~hidden8(p.mask.uts + at, p.mask.ute + at, pos[t][e], g & 1);
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  if (!((see >> (2 * u + x)) & 1u)) s[u][t][2 * x + e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            top[t][e] = fmax3(fmax3(s[0][t][e], s[0][t][2 + e], s[1][t][e]), fmax3(s[1][t][2 + e], s[2][t][e], s[2][t][2 + e]),
+                              fmaxf(s[3][t][e], s[3][t][2 + e])) *
+                        ck[t][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[t][e] = fmaxf(top[t][e], __shfl_xor_sync(0xffffffffu, top[t][e], o));
+        uint32_t pf[4][NT][2];
+        bool moved = false;
+        float av[NT][2], mu[NT][2], fv[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            // bit 2 u + x: key kb + 4 u + 2 x is visible
-            const int n = meta.x < 0 ? 0 : min(max(lim[t][e] - (j0 + kb), 0), 16);
-            uint32_t see = (1u << ((n + 1) >> 1)) - 1u;
-            if constexpr (kVec) {
-              if (meta.y && meta.x >= 0) {
-                const size_t at = mrow[t][e] + j0 + (kb & ~1);
-                if (p.mask.lts) see &= ~hidden8(p.mask.lts + at, p.mask.lte + at, pos[t][e], g & 1);
-                if (p.mask.uts) see &= ~hidden8(p.mask.uts + at, p.mask.ute + at, pos[t][e], g & 1);
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-                if (!((see >> (2 * u + x)) & 1u)) s[u][t][2 * x + e] = -INFINITY;
+            const float m_new = fmaxf(st.m[t][e], top[t][e]), mv_new = fmaxf(st.mv[t][e], top[t][e] + lvs);
+            st.l[t][e] *= ex2_diff(st.m[t][e], m_new);
+            av[t][e] = ex2_diff(st.mv[t][e], mv_new);
+            moved |= av[t][e] != 1.f;
+            st.m[t][e] = m_new;
+            st.mv[t][e] = mv_new;
+            mu[t][e] = m_new == -INFINITY ? 0.f : m_new;
+            fv[t][e] = ex2(fminf(mu[t][e] + lvs - (mv_new == -INFINITY ? 0.f : mv_new) + kPShift, 126.f));
           }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-mu[t][0], -mu[t][1]), f2 = f2_make(fv[t][0], fv[t][1]);
+          uint64_t l2 = f2_make(st.l[t][0], st.l[t][1]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float x0, x1, p0, p1;
+              f2_split(f2_fma(f2_make(s[u][t][2 * x], s[u][t][2 * x + 1]), c2, nm2), x0, x1);
+              const uint64_t pp = f2_make(ex2(x0), ex2(x1));
+              l2 = f2_add(l2, pp);
+              f2_split(f2_mul(pp, f2), p0, p1);
+              pf[u][t][x] = transpose8x8(pack_f16x2(p0, p1));
+            }
+          f2_split(l2, st.l[t][0], st.l[t][1]);
+        }
+        if (__builtin_expect(__any_sync(0xffffffffu, moved), 0)) {
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st.acc[n][t][i] *= av[t][i & 1];
+        }
+
+        ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sv), ((seq + 1) / kSlots) & 1, p.status));
+        if (!ok) break;
+        uint8_t* vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
+        if (__builtin_expect(tail, 0)) {
+          // codes behind the sequence's end may be anything, NaN too: they become 0, each
+          // lane's where it reads them
+          const int n_ok = meta.x < 0 ? 0 : min(max(r.len - (j0 + 16 * c), 0), 16);
+          uint32_t keep[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int nb = min(max(n_ok - 4 * u, 0), 4);
+            keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
+          }
+#pragma unroll 1
+          for (int i0 = 0; i0 < D / 8; i0 += 4) {
+            uint4* at = reinterpret_cast<uint4*>(vbase + 8 * i0 * kPage);
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = at[8 * i * kPage / 16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              at[8 * i * kPage / 16] = make_uint4(x[i].x & keep[0], x[i].y & keep[1], x[i].z & keep[2], x[i].w & keep[3]);
+          }
+          fence_proxy_async_smem();  // the next copy into the slot comes after
+        }
+#pragma unroll
+        for (int n0 = 0; n0 < D / 16; n0 += 4) {
+          uint4 w[4][2];
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              w[n][x] = *reinterpret_cast<const uint4*>(vbase + (16 * (n0 + n) + 8 * x) * kPage);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              uint32_t a[4];
+              codes_to_f16(word(w[n][0], u) , a[0], a[2]);
+              codes_to_f16(word(w[n][1], u) , a[1], a[3]);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816(st.acc[n0 + n][t], a, pf[u][t][0], pf[u][t][1]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.empty(warp, sv));
+        seq += 2;
       }
+      if (!ok) break;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          top[t][e] = fmax3(fmax3(s[0][t][e], s[0][t][2 + e], s[1][t][e]), fmax3(s[1][t][2 + e], s[2][t][e], s[2][t][2 + e]),
-                            fmaxf(s[3][t][e], s[3][t][2 + e])) *
-                      ck[t][e];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) top[t][e] = fmaxf(top[t][e], __shfl_xor_sync(0xffffffffu, top[t][e], o));
-      uint32_t pf[4][NT][2];
-      bool moved = false;
-      float av[NT][2], mu[NT][2], fv[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float m_new = fmaxf(st.m[t][e], top[t][e]), mv_new = fmaxf(st.mv[t][e], top[t][e] + lvs);
-          st.l[t][e] *= ex2_diff(st.m[t][e], m_new);
-          av[t][e] = ex2_diff(st.mv[t][e], mv_new);
-          moved |= av[t][e] != 1.f;
-          st.m[t][e] = m_new;
-          st.mv[t][e] = mv_new;
-          mu[t][e] = m_new == -INFINITY ? 0.f : m_new;
-          fv[t][e] = ex2(fminf(mu[t][e] + lvs - (mv_new == -INFINITY ? 0.f : mv_new) + kPShift, 126.f));
-        }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-mu[t][0], -mu[t][1]), f2 = f2_make(fv[t][0], fv[t][1]);
-        uint64_t l2 = f2_make(st.l[t][0], st.l[t][1]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float x0, x1, p0, p1;
-            f2_split(f2_fma(f2_make(s[u][t][2 * x], s[u][t][2 * x + 1]), c2, nm2), x0, x1);
-            const uint64_t pp = f2_make(ex2(x0), ex2(x1));
-            l2 = f2_add(l2, pp);
-            f2_split(f2_mul(pp, f2), p0, p1);
-            pf[u][t][x] = transpose8x8(pack_f16x2(p0, p1));
-          }
-        f2_split(l2, st.l[t][0], st.l[t][1]);
-      }
-      if (__builtin_expect(__any_sync(0xffffffffu, moved), 0)) {
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st.acc[n][t][i] *= av[t][i & 1];
-      }
-
-      ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sv), ((seq + 1) / kSlots) & 1, p.status));
-      if (!ok) break;
-      uint8_t* vbase = ring + sv * S::kHalf + g * kPage + 16 * c;
-      if (__builtin_expect(tail, 0)) {
-        // codes behind the sequence's end may be anything, NaN too: they become 0, each
-        // lane's where it reads them
-        const int n_ok = meta.x < 0 ? 0 : min(max(r.len - (j0 + 16 * c), 0), 16);
-        uint32_t keep[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int nb = min(max(n_ok - 4 * u, 0), 4);
-          keep[u] = nb == 4 ? ~0u : (1u << (8 * nb)) - 1u;
-        }
-#pragma unroll 1
-        for (int i0 = 0; i0 < D / 8; i0 += 4) {
-          uint4* at = reinterpret_cast<uint4*>(vbase + 8 * i0 * kPage);
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = at[8 * i * kPage / 16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            at[8 * i * kPage / 16] = make_uint4(x[i].x & keep[0], x[i].y & keep[1], x[i].z & keep[2], x[i].w & keep[3]);
-        }
-        fence_proxy_async_smem();  // the next copy into the slot comes after
-      }
-#pragma unroll
-      for (int n0 = 0; n0 < D / 16; n0 += 4) {
-        uint4 w[4][2];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            w[n][x] = *reinterpret_cast<const uint4*>(vbase + (16 * (n0 + n) + 8 * x) * kPage);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint32_t a[4];
-            codes_to_f16(word(w[n][0], u) , a[0], a[2]);
-            codes_to_f16(word(w[n][1], u) , a[1], a[3]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(st.acc[n0 + n][t], a, pf[u][t][0], pf[u][t][1]);
-          }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.empty(warp, sv));
-      seq += 2;
+          for (int o = 4; o < 32; o <<= 1) st.l[t][e] += __shfl_xor_sync(0xffffffffu, st.l[t][e], o);
     }
-    if (!ok) break;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) st.l[t][e] += __shfl_xor_sync(0xffffffffu, st.l[t][e], o);
 
-    const int writers = min(count, kConsumers);  // warps that had tiles, from first % 7 on
-    const int mine = (warp - first % kConsumers + kConsumers) % kConsumers;
-    if (first + count == run_hi - run_lo) {
+    if (last) {
       // the run's last piece is added up below
       ok = __all_sync(0xffffffffu, count_wait(&scan[kMerged], merges, p.status));
       if (mine < writers) st.put(merge + warp * S::kFrags * 32, stats + 3 * kRows * warp, lane);
       last_n = writers;
       last_from = first % kConsumers;
       break;
-    }
-    if (mine >= writers) {
-      merges += writers > 1;
-      continue;
     }
     if (writers > 1) {
       // leave the state, once the pieces before have been added up

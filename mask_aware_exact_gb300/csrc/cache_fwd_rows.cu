@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
       } else {
         seg += 32;
         k = 0;
+        if (seg >= nseg) ok = lengths_moved(p.status);
       }
     }
     if (lane == 0) {

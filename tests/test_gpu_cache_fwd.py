@@ -358,6 +358,47 @@ def test_sequences_cut_into_many_parts(H, N, d, lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Hk,N,d,kind,most", [
+    (280, 8, 4, 1, 64, None, 330), (140, 16, 8, 2, 128, "window_prefix", 330), (140, 16, 8, 1, 128, None, 330),
+    (600, 4, 2, 5, 64, "documents", 330), (140, 8, 8, 1, 64, None, 64), (1100, 1, 1, 3, 128, "documents", 100)])
+def test_many_short_sequences(B, H, Hk, N, d, kind, most):
+    """More segments than warps, among them empty ones and a page out of range: each
+    is one warp's. With a page or two for each segment the last CTAs have none."""
+    fm = need_gpu()
+    gen = torch.Generator().manual_seed(B)
+    lens = [0 if b % 17 == 3 else 1 + int(x) for b, x in enumerate(torch.randint(0, most, (B,), generator=gen))]
+    q_lens = [min(N, n) for n in lens]
+    q, cache, table, gen = make(fm, B, H, Hk, N, d, lens, seed=B)
+    mask = None
+    if kind is not None:
+        mask = mask_of(kind, B, H, Hk, N, table.shape[1] * PAGE, gen, fm)
+    ws = fm.alloc_cache_workspace(B, H, Hk, N, d, table.shape[1])
+    o, lse = run(fm, q, cache, table, lens, q_lens, mask, ws=ws)
+    check(o, lse, q, cache, table, lens, q_lens, mask)
+    o2, lse2 = run(fm, q, cache, table, lens, q_lens, mask, ws=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # a page out of range in one sequence is recorded if one of its keys is visible (no
+    # other entry is read); the others keep their results
+    bad = next(b for b, n in enumerate(lens) if n > most * 3 // 5)
+    at = 1 if most > 200 else 0
+    table[bad, at] = cache.k8.shape[0]
+    lens_d, q_d = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lens, q_lens))
+    o3, _ = fm.flashmask_fwd_cache(q, cache, table, lens_d, ws, mask=mask, q_lens=q_d,
+                                   o=torch.full_like(o, MARK))
+    i = np.arange(lens[bad] - q_lens[bad], lens[bad])[:, None]
+    j = np.arange(PAGE * at, PAGE * (at + 1))
+    see = np.repeat(j[None] < lens[bad], len(i), 0) if mask is not None and not mask.causal else j <= i  # (i < lens)
+    if mask is not None:
+        vec = lambda t: t[bad, 0, PAGE * at:PAGE * (at + 1)].cpu().numpy()
+        see &= ~((vec(mask.lts) <= i) & (i < vec(mask.lte)))
+        if mask.uts is not None:
+            see &= ~((vec(mask.uts) <= i) & (i < vec(mask.ute)))
+    assert fm.flashmask_check_status(ws)[0] == (fm.FM_ERR_PAGE if see.any() else fm.FM_OK)
+    keep = [b for b in range(B) if b != bad]
+    assert torch.equal(o3[keep], o[keep])
+
+
+@pytest.mark.gpu
 def test_codes_behind_two_gigabytes():
     # pages whose offset passes 2^31 bytes
     fm = need_gpu()
