@@ -77,7 +77,7 @@ struct Line {
   int lo, hi;      // this CTA's run
   int seg, first;  // segment of its first unit, and that unit's number in it
   bool any_empty;  // some segment has no unit
-  bool whole;      // no segment is cut
+  bool brief;      // no segment has more than kUncut pages
 };
 constexpr int kLineWords = 40;  // ints of shared memory for find_run
 // Segments of up to this many pages (or an eighth of a run) are not cut: a join takes
@@ -150,7 +150,7 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
   const bool uncut = longest <= max(kUncut / pages, even / 8);
   // the least run only keeps cut segments from falling into many parts
   r.run = max(uncut ? 1 : min_run, even);
-  r.whole = uncut;
+  r.brief = longest <= kUncut / pages;
   const int per = nseg > 0 ? static_cast<int>(gridDim.x) / nseg : 0;  // parts a segment may have
   const int cut = per >= 2 ? max(min_run, (longest + per - 1) / per) : 0;
   if (!uncut && per >= 2 && cut <= even + kApart / pages) {

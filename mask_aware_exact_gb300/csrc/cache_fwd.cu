@@ -68,7 +68,10 @@ constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a ti
 // Pages a run has at least: one for each consumer warp. One sequence of 2500 tokens, 8
 // cache heads, at least 4 / 7 / 14 pages: 13.4 / 12.7 / 13.7 us; 6000: 16.1 / 14.4 / 13.9.
 constexpr int kMinRun = kConsumers;
-// Uncut segments, at least this many for each CTA: every segment is one warp's.
+// Segments of at most kUncut pages, and at least this many for each CTA: every segment
+// is one warp's, without states to add up. 512 sequences up to 512 tokens, 8 cache heads:
+// 72.6 us so, 102 with a segment's pages spread over the warps; 1024 up to 100: 64, 81; 512
+// up to 512, 4 tokens: 87, 179. Segments of 62 pages spread better: 225, 208.
 constexpr int kAlone = 7;
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 constexpr int kOnce = 4 * kConsumers, kFan = 2 * kConsumers;  // see Join
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 
   const Line line = find_run<kThreads>(nseg, kMinRun, 1, scan, [&](int seg) { return pages_of<kVec>(p, geo, seg); });
   const int run = line.run, run_lo = line.lo, run_hi = line.hi;
-  const bool alone = line.whole && nseg >= kAlone * static_cast<int>(gridDim.x);
+  const bool alone = line.brief && nseg >= kAlone * static_cast<int>(gridDim.x);
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
