@@ -18,18 +18,20 @@
 //
 // One producer warp walks the run and loads pages (K codes, V codes: 64 * d bytes
 // each, contiguous) with bulk copies into a ring of three slots for each of seven
-// consumer warps; tile i of the run goes to warp i mod 7. The warps keep separate
-// softmax states. When a piece ends each leaves its state in shared memory and goes
+// consumer warps; tile i of the run goes to warp i mod 7 (or, with many short segments,
+// a segment to one warp). The warps keep separate softmax states. When a piece ends each leaves its state in shared memory and goes
 // on with the next piece; the last to arrive adds them up. The run's last piece and
 // the joins are added up by all warps.
 //
 // What bounds it. 8 rows: memory, once the cache is long (8 sequences of 131072 tokens,
 // 32 / 8 heads of 128: 322 us, 6.7 TB/s, 98 % of a copy; 64 up to 8192: 115 us, 83 %, with
-// 12000 of 210000 cycles before the first page and 14000 behind the last). 16 rows and
-// two tiles: instruction issue, about 900 instructions for a page and tile of 16 rows,
-// 2 a clock (16 sequences up to 16384, 32 / 4 heads of 64, 4 tokens: 44.6 us; floor 12.4).
-// Short ones: latency (one sequence of 1000 tokens: 10.5 us, of which 4 are the way to the
-// first page: where the run begins, page table, page, query).
+// 12000 of 210000 cycles before the first page and 14000 behind the last). 16 rows: the
+// loop's instructions, 900 for a page and tile, of which the seven warps issue 2.2 a
+// clock, eleven hardly more (16 sequences up to 16384, 32 / 4 heads of 64, 4 tokens, two
+// tiles of 16 rows: 45.6 us, floor 12.4; 50 of 85 thousand cycles in the loop, 9 before
+// the first page, the rest joins). Short ones: latency (one sequence of 1000 tokens: 10.8
+// us, of which 4 are the way to the first page: where the run begins, page table, page,
+// query).
 //
 // Arithmetic. Codes become fp16 (exact) and enter m16n8k16 instructions with fp32
 // accumulators; tcgen05 would need 128 rows. The products are taken transposed,
