@@ -81,12 +81,13 @@ struct Line {
 };
 constexpr int kLineWords = 40;  // ints of shared memory for find_run
 // Segments of up to this many pages (or an eighth of a run) are not cut: a join takes
-// 3 to 4 us, about as long as a CTA takes for 30 pages. One sequence of 500 tokens (8
-// cache heads): 9.7 us whole, 13.8 cut; 1000 tokens (16 pages): 11.3, 13.8; 2000: 14.3,
-// 14.4; 4000: 20.5, 12.7. 64 sequences up to 2000: 44.8 us whole, 51.3 cut; up to 4000:
-// 68.2, 64.8.
+// 3 to 4 us, about as long as a CTA takes for 30 pages. 128 segments of up to 32 pages:
+// 18.2 us whole, 21.5 cut; 512 of them 45.1, 51.0; of up to 64 pages 65.3 either way.
 constexpr int kUncut = 32;
-
+// The same where segments can be cut one by one (see below). One sequence of 1000 tokens,
+// 8 cache heads (16 pages): 11.7 us whole, 11.4 cut; 500: 10.1, 11.5; 1500: 13.2, 12.1;
+// 2000: 14.4, 12.0.
+constexpr int kUncutApart = 16;
 // Where there are at least two CTAs for each segment, the segments are cut one by one
 // into equal runs if these are not longer than the line's by more than kApart pages:
 // a second piece in a run costs a CTA about that much. Cut so / on the line: one
@@ -147,13 +148,14 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
   int total;
   int before = block_before<kWarps>(mine, wsum, total);
   const int even = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  const bool uncut = longest <= max(kUncut / pages, even / 8);
+  const int per = nseg > 0 ? static_cast<int>(gridDim.x) / nseg : 0;  // parts a segment may have
+  const int cut = per >= 2 ? max(min_run, (longest + per - 1) / per) : 0;
+  const bool one_by_one = per >= 2 && cut <= even + kApart / pages;
+  const bool uncut = longest <= max((one_by_one ? kUncutApart : kUncut) / pages, even / 8);
   // the least run only keeps cut segments from falling into many parts
   r.run = max(uncut ? 1 : min_run, even);
   r.brief = longest <= kUncut / pages;
-  const int per = nseg > 0 ? static_cast<int>(gridDim.x) / nseg : 0;  // parts a segment may have
-  const int cut = per >= 2 ? max(min_run, (longest + per - 1) / per) : 0;
-  if (!uncut && per >= 2 && cut <= even + kApart / pages) {
+  if (!uncut && one_by_one) {
     // runs of one segment each: on this line every segment is filled up to whole runs
     r.run = cut;
     const int filled = (mine + cut - 1) / cut * cut;  // a thread has one segment at most
