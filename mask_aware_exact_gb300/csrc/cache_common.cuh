@@ -139,23 +139,41 @@ __device__ __forceinline__ Line find_run(int nseg, int min_run, int pages, int* 
     longest = max(longest, n);
     empty |= n == 0;
   }
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
   longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) wmax[warp] = longest;
+  if (lane == 31) {
+    wsum[warp] = before;
+    wmax[warp] = longest;
+  }
   Line r;
   r.any_empty = __syncthreads_or(empty);
+  int total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) longest = max(longest, wmax[w]);
-  int total;
-  int before = block_before<kWarps>(mine, wsum, total);
+  for (int w = 0; w < kWarps; ++w) {
+    const int x = wsum[w];
+    if (w < warp) before += x;
+    total += x;
+    longest = max(longest, wmax[w]);
+  }
+  before -= mine;
   const int even = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  const int per = nseg > 0 ? static_cast<int>(gridDim.x) / nseg : 0;  // parts a segment may have
-  const int cut = per >= 2 ? max(min_run, (longest + per - 1) / per) : 0;
-  const bool one_by_one = per >= 2 && cut <= even + kApart / pages;
-  const bool uncut = longest <= max((one_by_one ? kUncutApart : kUncut) / pages, even / 8);
+  bool uncut = longest <= max(kUncutApart / pages, even / 8);
+  int cut = 0;  // the runs' length if segments are cut one by one
+  if (!uncut) {
+    const int per = static_cast<int>(gridDim.x) / nseg;  // parts a segment may have
+    if (per >= 2) cut = max(min_run, (longest + per - 1) / per);
+    if (cut > even + kApart / pages) cut = 0;
+    uncut = cut == 0 && longest <= kUncut / pages;
+  }
   // the least run only keeps cut segments from falling into many parts
   r.run = max(uncut ? 1 : min_run, even);
   r.brief = longest <= kUncut / pages;
-  if (!uncut && one_by_one) {
+  if (cut > 0) {
     // runs of one segment each: on this line every segment is filled up to whole runs
     r.run = cut;
     const int filled = (mine + cut - 1) / cut * cut;  // a thread has one segment at most

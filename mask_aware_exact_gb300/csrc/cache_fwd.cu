@@ -7,28 +7,28 @@
 // A segment is one (sequence, cache head, row tile); its work is the list of pages
 // that some row of it sees.
 //
-// Split. All pages of all segments form one line, cut into equal runs, one run
-// per CTA (one CTA per SM), whatever the lengths of the sequences. A run covers
-// pieces of one or more segments; a segment cut by a run border leaves partial
-// results in the workspace and the CTA that finishes last adds them in order, so
-// results do not depend on timing. Where every segment is short (32 pages or an
-// eighth of a run) the borders move to segment ends: nothing is cut, and the
-// imbalance costs less than the joins. With a column-wise mask a first kernel marks
+// Split. All pages of all segments form one line, cut into equal runs, one run per CTA
+// (one CTA per SM), whatever the lengths of the sequences; where there are CTAs enough
+// each segment is cut by itself instead. A segment cut by a run border leaves partial
+// results in the workspace and the CTA that finishes last adds them in order (in groups
+// first, if they are many), so results do not depend on timing. Where every segment is
+// short the borders move to segment ends: nothing is cut, and the imbalance costs less
+// than the joins. find_run has the rules. With a column-wise mask a first kernel lists
 // the pages that are visible to a row tile, and only those are on the line.
 //
 // One producer warp walks the run and loads pages (K codes, V codes: 64 * d bytes
 // each, contiguous) with bulk copies into a ring of three slots for each of seven
 // consumer warps; tile i of the run goes to warp i mod 7 (or, with many short segments,
-// a segment to one warp). The warps keep separate softmax states. When a piece ends each leaves its state in shared memory and goes
-// on with the next piece; the last to arrive adds them up. The run's last piece and
-// the joins are added up by all warps.
+// a segment to one warp). The warps keep separate softmax states. When a piece ends each
+// leaves its state in shared memory and goes on with the next piece; the last to arrive
+// adds them up. The run's last piece and the joins are added up by all warps.
 //
 // What bounds it. 8 rows: memory, once the cache is long (8 sequences of 131072 tokens,
 // 32 / 8 heads of 128: 322 us, 6.7 TB/s, 98 % of a copy; 64 up to 8192: 115 us, 83 %, with
 // 12000 of 210000 cycles before the first page and 14000 behind the last). 16 rows: the
 // loop's instructions, 900 for a page and tile, of which the seven warps issue 2.2 a
 // clock, eleven hardly more (16 sequences up to 16384, 32 / 4 heads of 64, 4 tokens, two
-// tiles of 16 rows: 45.6 us, floor 12.4; 50 of 85 thousand cycles in the loop, 9 before
+// tiles of 16 rows: 45.6 us, floor 12.4; 50 of 80 thousand cycles in the loop, 9 before
 // the first page, the rest joins). Short ones: latency (one sequence of 1000 tokens: 10.8
 // us, of which 4 are the way to the first page: where the run begins, page table, page,
 // query).
