@@ -418,9 +418,11 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * 0, H % Hm == 0. O, LSE and rows without a visible key are as at the top of
  * this file: O bf16 [B, H, N, d], LSE fp32 [B, H, N] (contiguous).
  * Keys and values count as their codes times their scales; scores, softmax
- * statistics and sums are fp32. What masked keys, and codes behind a sequence's
- * end, hold has no influence, NaN included. A query row with a value that is
- * not finite gives NaN.
+ * statistics and sums are fp32. What K holds for masked keys, what the slots behind
+ * a sequence's end hold and what pages hold of which no row sees a key has no
+ * influence, NaN included. V codes of the other slots must not be NaN, masked or not
+ * (flashmask_cache_append writes none: a NaN in V becomes one in K). A query row with a
+ * value that is not finite gives NaN.
  *   qs, os: strides of Q and O in elements for batch, head and token (multiples
  *   of 8; the last dimension contiguous, 16-byte aligned). O may be Q itself with
  *   the same strides; otherwise O and LSE overlap neither each other nor an input.
