@@ -13,10 +13,11 @@
 namespace fm {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreadsMost = 1024, kThreadsSmall = 256;
 constexpr int kClusterMost = 8;
 constexpr int kWordsMost = FM_MAX_SEQLEN / kPage / 32 / kClusterMost;  // 32-page words of a CTA
-constexpr int kWordsPass = kThreads * 8 / (32 * kPage);                // words of one pass
+constexpr int kWordsPass = kThreadsMost * 8 / (32 * kPage);            // words of one pass
+constexpr int kWordsSmall = kThreadsSmall * 8 / (32 * kPage);          // of a small table
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -38,6 +39,7 @@ __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
 // A key is hidden from the whole tile, positions [lo, hi], if the union of its
 // intervals (and of the rows above it, when causal) covers them. A thread takes 8 keys
 // at a time, so a page is 8 lanes and a warp takes groups of 4 pages.
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams p, const Geometry geo,
                                                             const int cluster) {
   __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
@@ -62,7 +64,8 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   for (int i = warp; i < 8 * words; i += kThreads / 32) {
     const int j0 = ((8 * w0 + i) * 32 + lane) * 8;  // this thread's keys j0 .. j0 + 7
     bool see = false, cut = false;
-    if (j0 < end) {
+    // (of a small table the bounds are on their way before the length is there)
+    if (kThreads == kThreadsSmall ? j0 < L : j0 < end) {
       for (int m = m0; m <= m1; ++m) {
         const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
         int s0[8] = {}, e0[8] = {};
@@ -131,13 +134,20 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
     }
     if (lane == 0) count = sum;
   }
-  cluster_sync();
+  if (kThreads == kThreadsSmall)
+    __syncthreads();
+  else
+    cluster_sync();
   // this CTA's place in the list, and the whole
   int mine = 0, total = 0;
-  for (int k = 0; k < cluster; ++k) {
-    const int x = of_cta(&count, k);
-    if (k < rank) mine += x;
-    total += x;
+  if (kThreads == kThreadsSmall) {
+    total = count;
+  } else {
+    for (int k = 0; k < cluster; ++k) {
+      const int x = of_cta(&count, k);
+      if (k < rank) mine += x;
+      total += x;
+    }
   }
   const size_t at = (static_cast<size_t>(b) * geo.classes + cls) * geo.RT + rt;
   uint16_t* list = p.list + at * p.max_pages + mine;
@@ -149,18 +159,23 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
           static_cast<uint16_t>((32 * (w0 + i) + bit) | (cuts[q >> 2] >> (q & 3) & 1u) << 15);
   }
   if (rank == 0 && tid == 0) p.listed[at] = total;
-  cluster_sync();  // no CTA leaves while its count may be read
+  if (kThreads != kThreadsSmall) cluster_sync();  // no CTA leaves while its count may be read
 }
 
 }  // namespace
 
 cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
+  if (geo.words <= kWordsSmall) {
+    const dim3 grid(static_cast<unsigned>(geo.classes * geo.RT), static_cast<unsigned>(p.B));
+    cache_classify<kThreadsSmall><<<grid, kThreadsSmall, 0, s>>>(p, geo, 1);
+    return cudaGetLastError();
+  }
   int cluster = 1;
   while (cluster < kClusterMost && cluster * kWordsPass < geo.words) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cluster) * static_cast<unsigned>(geo.classes * geo.RT),
                      static_cast<unsigned>(p.B));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreadsMost);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -168,7 +183,7 @@ cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, 
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_classify, p, geo, cluster);
+  return cudaLaunchKernelEx(&cfg, cache_classify<kThreadsMost>, p, geo, cluster);
 }
 
 }  // namespace fm
