@@ -13,11 +13,11 @@
 namespace fm {
 namespace {
 
-constexpr int kThreadsMost = 1024, kThreadsSmall = 256;
+constexpr int kThreadsMost = 1024;
 constexpr int kClusterMost = 8;
 constexpr int kWordsMost = FM_MAX_SEQLEN / kPage / 32 / kClusterMost;  // 32-page words of a CTA
-constexpr int kWordsPass = kThreadsMost * 8 / (32 * kPage);            // words of one pass
-constexpr int kWordsSmall = kThreadsSmall * 8 / (32 * kPage);          // of a small table
+// 32-page words that CTAs of kThreads take in one pass
+constexpr int words_pass(int threads) { return threads * 8 / (32 * kPage); }
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -39,7 +39,7 @@ __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
 // A key is hidden from the whole tile, positions [lo, hi], if the union of its
 // intervals (and of the rows above it, when causal) covers them. A thread takes 8 keys
 // at a time, so a page is 8 lanes and a warp takes groups of 4 pages.
-template <int kThreads>
+template <int kThreads, bool kOne>
 __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams p, const Geometry geo,
                                                             const int cluster) {
   __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
     const int j0 = ((8 * w0 + i) * 32 + lane) * 8;  // this thread's keys j0 .. j0 + 7
     bool see = false, cut = false;
     // (of a small table the bounds are on their way before the length is there)
-    if (kThreads == kThreadsSmall ? j0 < L : j0 < end) {
+    if (kOne ? j0 < L : j0 < end) {
       for (int m = m0; m <= m1; ++m) {
         const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
         int s0[8] = {}, e0[8] = {};
@@ -134,13 +134,13 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
     }
     if (lane == 0) count = sum;
   }
-  if (kThreads == kThreadsSmall)
+  if (kOne)
     __syncthreads();
   else
     cluster_sync();
   // this CTA's place in the list, and the whole
   int mine = 0, total = 0;
-  if (kThreads == kThreadsSmall) {
+  if (kOne) {
     total = count;
   } else {
     for (int k = 0; k < cluster; ++k) {
@@ -159,19 +159,23 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
           static_cast<uint16_t>((32 * (w0 + i) + bit) | (cuts[q >> 2] >> (q & 3) & 1u) << 15);
   }
   if (rank == 0 && tid == 0) p.listed[at] = total;
-  if (kThreads != kThreadsSmall) cluster_sync();  // no CTA leaves while its count may be read
+  if (!kOne) cluster_sync();  // no CTA leaves while its count may be read
 }
 
 }  // namespace
 
 cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
-  if (geo.words <= kWordsSmall) {
-    const dim3 grid(static_cast<unsigned>(geo.classes * geo.RT), static_cast<unsigned>(p.B));
-    cache_classify<kThreadsSmall><<<grid, kThreadsSmall, 0, s>>>(p, geo, 1);
+  const dim3 grid(static_cast<unsigned>(geo.classes * geo.RT), static_cast<unsigned>(p.B));
+  if (geo.words <= words_pass(256)) {
+    cache_classify<256, true><<<grid, 256, 0, s>>>(p, geo, 1);
+    return cudaGetLastError();
+  }
+  if (geo.words <= words_pass(512)) {
+    cache_classify<512, true><<<grid, 512, 0, s>>>(p, geo, 1);
     return cudaGetLastError();
   }
   int cluster = 1;
-  while (cluster < kClusterMost && cluster * kWordsPass < geo.words) cluster *= 2;
+  while (cluster < kClusterMost && cluster * words_pass(kThreadsMost) < geo.words) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cluster) * static_cast<unsigned>(geo.classes * geo.RT),
                      static_cast<unsigned>(p.B));
@@ -183,7 +187,7 @@ cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, 
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_classify<kThreadsMost>, p, geo, cluster);
+  return cudaLaunchKernelEx(&cfg, cache_classify<kThreadsMost, false>, p, geo, cluster);
 }
 
 }  // namespace fm
