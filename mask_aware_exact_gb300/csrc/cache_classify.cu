@@ -3,10 +3,12 @@
 // row tile, the list of the pages that some row sees, in order, each with a bit that
 // says whether intervals hide some of its keys from some row, and their number.
 //
-// Latency-bound: 8 or 16 bytes of bounds per cached token. A CTA of 1024 threads takes
-// 8192 keys a pass; longer tables are shared by a cluster of up to eight CTAs, whose
-// counts, which place a CTA's part of the list, come from the others' shared memory.
-// 8 sequences of 131072 tokens: 8.7 us with cold caches.
+// Latency-bound: 8 or 16 bytes of bounds per cached token. A table of up to 32, 64 or
+// 128 pages is one pass of a CTA of 256, 512 or 1024 threads (with 1024 threads and a
+// cluster of one for all of them, masked calls on up to 64 pages took 1.2 to 1.6 us more,
+// of 11 to 16); longer tables are shared by a cluster of up to eight CTAs, whose counts,
+// which place a CTA's part of the list, come from the others' shared memory. 8 sequences
+// of 131072 tokens: 8.7 us with cold caches.
 #include "cache_common.cuh"
 #include "flashmask.h"
 
@@ -45,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
   __shared__ int before[kWordsMost];  // visible pages of this CTA before a word
   __shared__ int count;               // visible pages of this CTA
-  const int tile = blockIdx.x / cluster, rank = blockIdx.x - tile * cluster, b = blockIdx.y;
+  const int tile = kOne ? blockIdx.x : blockIdx.x / cluster, rank = kOne ? 0 : blockIdx.x - tile * cluster, b = blockIdx.y;
   const int cls = geo.by_RT.div(tile), rt = tile - cls * geo.RT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int each = (geo.words + cluster - 1) / cluster;
@@ -64,8 +66,8 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   for (int i = warp; i < 8 * words; i += kThreads / 32) {
     const int j0 = ((8 * w0 + i) * 32 + lane) * 8;  // this thread's keys j0 .. j0 + 7
     bool see = false, cut = false;
-    // (of a small table the bounds are on their way before the length is there)
-    if (kOne ? j0 < L : j0 < end) {
+    // (the first pass's bounds are on their way before the length is there)
+    if (i < kThreads / 32 ? j0 < L : j0 < end) {
       for (int m = m0; m <= m1; ++m) {
         const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
         int s0[8] = {}, e0[8] = {};
@@ -174,7 +176,11 @@ cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, 
     cache_classify<512, true><<<grid, 512, 0, s>>>(p, geo, 1);
     return cudaGetLastError();
   }
-  int cluster = 1;
+  if (geo.words <= words_pass(kThreadsMost)) {
+    cache_classify<kThreadsMost, true><<<grid, kThreadsMost, 0, s>>>(p, geo, 1);
+    return cudaGetLastError();
+  }
+  int cluster = 2;
   while (cluster < kClusterMost && cluster * words_pass(kThreadsMost) < geo.words) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cluster) * static_cast<unsigned>(geo.classes * geo.RT),
