@@ -41,7 +41,8 @@ __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
 // A key is hidden from the whole tile, positions [lo, hi], if the union of its
 // intervals (and of the rows above it, when causal) covers them. A thread takes 8 keys
 // at a time, so a page is 8 lanes and a warp takes groups of 4 pages.
-template <int kThreads, bool kOne>
+// kOne: no cluster; kMany: a class has several mask heads.
+template <int kThreads, bool kOne, bool kMany>
 __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams p, const Geometry geo,
                                                             const int cluster) {
   __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   const RowTile r = row_tile(p, geo, b, rt, blockIdx.x == 0 && tid == 0);
   const int lo = r.shift + r.t_lo, hi = r.shift + r.t_hi;
   int m0 = cls, m1 = cls;  // mask heads of the class
-  if (geo.classes != p.mask.Hm) {
+  if constexpr (kMany) {
     const int per = p.H / p.mask.Hm;
     m0 = cls * geo.G / per;
     m1 = (cls * geo.G + geo.G - 1) / per;
@@ -68,7 +69,8 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
     bool see = false, cut = false;
     // (the first pass's bounds are on their way before the length is there)
     if (i < kThreads / 32 ? j0 < L : j0 < end) {
-      for (int m = m0; m <= m1; ++m) {
+#pragma unroll(kMany && kThreads <= 512 ? 4 : 1)
+      for (int m = m0; m <= (kMany ? m1 : m0); ++m) {
         const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
         int s0[8] = {}, e0[8] = {};
         if (p.mask.lts) {
@@ -164,27 +166,22 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   if (!kOne) cluster_sync();  // no CTA leaves while its count may be read
 }
 
-}  // namespace
-
-cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
+template <bool kMany>
+cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(geo.classes * geo.RT), static_cast<unsigned>(p.B));
-  if (geo.words <= words_pass(256)) {
-    cache_classify<256, true><<<grid, 256, 0, s>>>(p, geo, 1);
-    return cudaGetLastError();
-  }
-  if (geo.words <= words_pass(512)) {
-    cache_classify<512, true><<<grid, 512, 0, s>>>(p, geo, 1);
-    return cudaGetLastError();
-  }
   if (geo.words <= words_pass(kThreadsMost)) {
-    cache_classify<kThreadsMost, true><<<grid, kThreadsMost, 0, s>>>(p, geo, 1);
+    if (geo.words <= words_pass(256))
+      cache_classify<256, true, kMany><<<grid, 256, 0, s>>>(p, geo, 1);
+    else if (geo.words <= words_pass(512))
+      cache_classify<512, true, kMany><<<grid, 512, 0, s>>>(p, geo, 1);
+    else
+      cache_classify<kThreadsMost, true, kMany><<<grid, kThreadsMost, 0, s>>>(p, geo, 1);
     return cudaGetLastError();
   }
   int cluster = 2;
   while (cluster < kClusterMost && cluster * words_pass(kThreadsMost) < geo.words) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * static_cast<unsigned>(geo.classes * geo.RT),
-                     static_cast<unsigned>(p.B));
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * grid.x, grid.y);
   cfg.blockDim = dim3(kThreadsMost);
   cfg.stream = s;
   cudaLaunchAttribute attr;
@@ -193,7 +190,13 @@ cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, 
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_classify<kThreadsMost, false>, p, geo, cluster);
+  return cudaLaunchKernelEx(&cfg, cache_classify<kThreadsMost, false, kMany>, p, geo, cluster);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_classify(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
+  return geo.classes != p.mask.Hm ? launch_t<true>(p, geo, s) : launch_t<false>(p, geo, s);
 }
 
 }  // namespace fm
