@@ -6,7 +6,9 @@
 // Latency-bound: 8 or 16 bytes of bounds per cached token. A table of up to 32, 64 or
 // 128 pages is one pass of a CTA of 256, 512 or 1024 threads (with 1024 threads and a
 // cluster of one for all of them, masked calls on up to 64 pages took 1.2 to 1.6 us more,
-// of 11 to 16); longer tables are shared by a cluster of up to eight CTAs, whose counts,
+// of 11 to 16), of more if several mask heads share a class: its warps take the heads side
+// by side (16 heads, 10 sequences of up to 2500 tokens: 17 us one head after the other, 12
+// so); longer tables are shared by a cluster of up to eight CTAs, whose counts,
 // which place a CTA's part of the list, come from the others' shared memory. 8 sequences
 // of 131072 tokens: 8.7 us with cold caches.
 #include "cache_common.cuh"
@@ -45,7 +47,7 @@ __device__ __forceinline__ void load8(const int32_t* src, int (&v)[8]) {
 template <int kThreads, bool kOne, bool kMany>
 __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams p, const Geometry geo,
                                                             const int cluster) {
-  __shared__ uint8_t sees[kWordsMost * 8], cuts[kWordsMost * 8];  // of groups of 4 pages
+  __shared__ uint32_t bits[kWordsMost * 8];  // of groups of 4 pages: visible, and << 4 cut
   __shared__ int before[kWordsMost];  // visible pages of this CTA before a word
   __shared__ int count;               // visible pages of this CTA
   const int tile = kOne ? blockIdx.x : blockIdx.x / cluster, rank = kOne ? 0 : blockIdx.x - tile * cluster, b = blockIdx.y;
@@ -63,14 +65,23 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   }
   const int L = p.max_pages * kPage;
   const int end = hi < lo ? 0 : p.mask.causal ? min(r.len, hi + 1) : r.len;
+  // A warp takes a group of pages, and with several mask heads one of them: wm, wm +
+  // heads, .., where the other warps of the group have the others.
+  constexpr int kWarps = kThreads / 32;
+  const int heads = kMany ? min(m1 - m0 + 1, kWarps) : 1, wi = kMany ? warp / heads : warp, wm = warp - wi * heads;
+  const int step = kMany ? kWarps / heads : kWarps;
+  if constexpr (kMany) {
+    for (int i = tid; i < 8 * words; i += kThreads) bits[i] = 0;
+    __syncthreads();
+  }
 #pragma unroll 2
-  for (int i = warp; i < 8 * words; i += kThreads / 32) {
+  for (int i = wi < step ? wi : 8 * words; i < 8 * words; i += step) {
     const int j0 = ((8 * w0 + i) * 32 + lane) * 8;  // this thread's keys j0 .. j0 + 7
     bool see = false, cut = false;
     // (the first pass's bounds are on their way before the length is there)
-    if (i < kThreads / 32 ? j0 < L : j0 < end) {
-#pragma unroll(kMany && kThreads <= 512 ? 4 : 1)
-      for (int m = m0; m <= (kMany ? m1 : m0); ++m) {
+    if (i == wi ? j0 < L : j0 < end) {
+#pragma unroll 1
+      for (int m = m0 + wm; m <= (kMany ? m1 : m0); m += heads) {
         const size_t at = (static_cast<size_t>(b) * p.mask.Hm + m) * L + j0;
         int s0[8] = {}, e0[8] = {};
         if (p.mask.lts) {
@@ -112,15 +123,17 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
         v |= static_cast<uint32_t>((sb >> (8 * k) & 0xffu) != 0) << k;
         c |= static_cast<uint32_t>((cb >> (8 * k) & 0xffu) != 0) << k;
       }
-      sees[i] = static_cast<uint8_t>(v);
-      cuts[i] = static_cast<uint8_t>(c);
+      if (kMany)
+        atomicOr(&bits[i], v | c << 4);
+      else
+        bits[i] = v | c << 4;
     }
   }
   __syncthreads();
   auto word_of = [&](int i) {
     uint32_t v = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v |= static_cast<uint32_t>(sees[8 * i + k]) << (4 * k);
+    for (int k = 0; k < 8; ++k) v |= (bits[8 * i + k] & 15u) << (4 * k);
     return v;
   };
   if (warp == 0) {
@@ -160,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
     const uint32_t v = word_of(i);
     if (v >> bit & 1u)
       list[before[i] + __popc(v & ((1u << bit) - 1u))] =
-          static_cast<uint16_t>((32 * (w0 + i) + bit) | (cuts[q >> 2] >> (q & 3) & 1u) << 15);
+          static_cast<uint16_t>((32 * (w0 + i) + bit) | (bits[q >> 2] >> (4 + (q & 3)) & 1u) << 15);
   }
   if (rank == 0 && tid == 0) p.listed[at] = total;
   if (!kOne) cluster_sync();  // no CTA leaves while its count may be read
@@ -170,9 +183,11 @@ template <bool kMany>
 cudaError_t launch_t(const CacheFwdParams& p, const Geometry& geo, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(geo.classes * geo.RT), static_cast<unsigned>(p.B));
   if (geo.words <= words_pass(kThreadsMost)) {
-    if (geo.words <= words_pass(256))
+    // groups of pages, of each head: half as many warps at least
+    const int heads = (p.mask.Hm + geo.classes - 1) / geo.classes, warps = 4 * geo.words * heads;
+    if (geo.words <= words_pass(256) && warps <= 8)
       cache_classify<256, true, kMany><<<grid, 256, 0, s>>>(p, geo, 1);
-    else if (geo.words <= words_pass(512))
+    else if (geo.words <= words_pass(512) && warps <= 32)
       cache_classify<512, true, kMany><<<grid, 512, 0, s>>>(p, geo, 1);
     else
       cache_classify<kThreadsMost, true, kMany><<<grid, kThreadsMost, 0, s>>>(p, geo, 1);
