@@ -508,11 +508,13 @@ def _want(t, name, dtype, index, shape):
 
 
 def _rows(t, name, dtype, index):
-    """[B, H, N, d] with any strides but a contiguous last dimension."""
-    if t.dtype is not dtype or t.get_device() != index or index < 0 or t.dim() != 4 or \
-            (t.stride(3) != 1 and t.shape[3] != 1):
+    """Strides of a [B, H, N, d] tensor with any but a contiguous last dimension's."""
+    st = t.stride()
+    if t.dtype is not dtype or t.get_device() != index or index < 0 or len(st) != 4 or \
+            (st[3] != 1 and t.shape[3] != 1):
         raise ValueError(f"{name} must be a {dtype} CUDA tensor [B, H, N, d] with a contiguous last "
                          f"dimension, on the same device as the others")
+    return st
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -544,14 +546,15 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
 
 
 def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, where):
-    code = _ROPE_DTYPES.get(q.dtype)
+    dtype = q.dtype
+    code = _ROPE_DTYPES.get(dtype)
     if code is None:
         raise ValueError("q must be bf16, fp16 or fp32")
     index = q.get_device()
-    _rows(q, "q", q.dtype, index)
+    sq, sk = _rows(q, "q", dtype, index), None
     B, Hq, N, d = q.shape
     if k is not None:
-        _rows(k, "k", q.dtype, index)
+        sk = _rows(k, "k", dtype, index)
         Bk, Hk, Nk, dk = k.shape
         if Bk != B or Nk != N or dk != d:
             raise ValueError("q and k must share B, N and d")
@@ -561,32 +564,33 @@ def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, whe
         raise ValueError("freqs must be [rot_dim / 2] with rot_dim <= d")
     pos, pos_stride = None, 0
     if positions is not None:
+        sp, tp = positions.shape, positions.stride()
         if positions.dtype is not torch.int32 or positions.get_device() != index or \
-                positions.dim() != 2 or positions.shape[1] != N or \
-                positions.shape[0] not in (1, B) or (N > 1 and positions.stride(1) != 1):
+                len(sp) != 2 or sp[1] != N or (sp[0] != 1 and sp[0] != B) or (N > 1 and tp[1] != 1):
             raise ValueError(f"positions must be int32 [{B}, {N}] or [1, {N}] on cuda:{index}, rows "
                              "contiguous")
         pos = positions.data_ptr()
-        pos_stride = positions.stride(0) if positions.shape[0] > 1 else 0
-    yq = yk = None
+        pos_stride = tp[0] if sp[0] > 1 else 0
+    yq = yk = tq = tk = None
     if out is not None:
         yq, yk = out[0], (out[1] if k is not None else None)
-        for t, x in ((yq, q), (yk, k)):
-            if x is not None:
-                _rows(t, "out", q.dtype, index)
-                if t.shape != x.shape:
-                    raise ValueError("out must have the shapes of q and k")
+        tq = _rows(yq, "out", dtype, index)
+        if yk is not None:
+            tk = _rows(yk, "out", dtype, index)
+        if yq.shape != q.shape or (k is not None and yk.shape != k.shape):
+            raise ValueError("out must have the shapes of q and k")
 
     def call(raw):
-        oq, ok = yq, yk
+        oq, ok, uq, uk = yq, yk, tq, tk
         if oq is None:
-            oq = torch.empty((B, Hq, N, d), dtype=q.dtype, device=q.device)
+            device = q.device
+            oq, uq = torch.empty((B, Hq, N, d), dtype=dtype, device=device), (Hq * N * d, N * d, d)
             if k is not None:
-                ok = torch.empty((B, Hk, N, d), dtype=q.dtype, device=q.device)
+                ok, uk = torch.empty((B, Hk, N, d), dtype=dtype, device=device), (Hk * N * d, N * d, d)
         if B * N * d > 0:
-            heads = _HEADS.pack(q.data_ptr(), oq.data_ptr(), Hq, *q.stride()[:3], *oq.stride()[:3])
+            heads = _HEADS.pack(q.data_ptr(), oq.data_ptr(), Hq, *sq[:3], *uq[:3])
             if k is not None:
-                heads += _HEADS.pack(k.data_ptr(), ok.data_ptr(), Hk, *k.stride()[:3], *ok.stride()[:3])
+                heads += _HEADS.pack(k.data_ptr(), ok.data_ptr(), Hk, *sk[:3], *uk[:3])
             st = _lib.flashmask_rope(heads, 1 if k is None else 2, pos, pos_stride, freqs.data_ptr(), B, N,
                                      d, 2 * n, bool(interleaved), code, mscale, inverse, raw)
             if st:
@@ -701,8 +705,7 @@ def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=No
     page_table int32 [B, max_pages]; start, count int32 [B]. See
     include/flashmask.h for scales and rounding."""
     c, Hk, d, index = cache._handle
-    _rows(k, "k", torch.bfloat16, index)
-    _rows(v, "v", torch.bfloat16, index)
+    ks, vs = _rows(k, "k", torch.bfloat16, index), _rows(v, "v", torch.bfloat16, index)
     B, _, N, _ = k.shape
     if v.shape != k.shape or k.shape[1] != Hk or k.shape[3] != d:
         raise ValueError("k and v must be [B, Hk, N, d] with the cache's Hk and d")
@@ -712,8 +715,8 @@ def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=No
 
     def call(raw):
         code = load().flashmask_cache_append(c, page_table.data_ptr(), max_pages, k.data_ptr(),
-                                             _STRIDES.pack(*k.stride()[:3]), v.data_ptr(),
-                                             _STRIDES.pack(*v.stride()[:3]), st, ct, B, N, ws.data_ptr(),
+                                             _STRIDES.pack(*ks[:3]), v.data_ptr(),
+                                             _STRIDES.pack(*vs[:3]), st, ct, B, N, ws.data_ptr(),
                                              ws.numel(), raw)
         if code:
             raise FlashMaskError(code, "flashmask_cache_append")
@@ -730,7 +733,7 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
     be None). Returns (O bf16 like q, LSE fp32 [B, H, N]); rows behind q_lens[b]
     of `o` and `lse` are left as they were."""
     c, _, d, index = cache._handle
-    _rows(q, "q", torch.bfloat16, index)
+    qs = _rows(q, "q", torch.bfloat16, index)
     B, H, N, _ = q.shape
     if q.shape[3] != d:
         raise ValueError("q must have the cache's d")
@@ -761,7 +764,7 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
     def call(raw):
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
         norm = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
-        code = load().flashmask_fwd_cache(q.data_ptr(), _STRIDES.pack(*q.stride()[:3]), c,
+        code = load().flashmask_fwd_cache(q.data_ptr(), _STRIDES.pack(*qs[:3]), c,
                                           page_table.data_ptr(), max_pages, ln, ql, m, B, H, N, scale,
                                           out.data_ptr(), _STRIDES.pack(*out.stride()[:3]), norm.data_ptr(),
                                           ws.data_ptr(), ws.numel(), raw)
