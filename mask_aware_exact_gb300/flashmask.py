@@ -599,7 +599,7 @@ def _rope(q, k, freqs, positions, interleaved, mscale, out, stream, inverse, whe
 
     if _lib is None:
         load()
-    return _launch(index, stream, (q, k, freqs, positions, yq, yk), call)
+    return _launch(index, stream, () if stream is None else (q, k, freqs, positions, yq, yk), call)
 
 
 def flashmask_rope(q, k, freqs, positions=None, interleaved=False, mscale=1.0, out=None,
@@ -693,10 +693,11 @@ def _per_sequence(t, name, B, index):
 
 
 def _page_table(t, B, index):
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be int32 [B, max_pages]")
-    _want(t, "page_table", torch.int32, index, (B, t.shape[1]))
-    return t.shape[1]
+    _want(t, "page_table", torch.int32, index, (B, shape[1]))
+    return shape[1]
 
 
 def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=None, stream=None):
@@ -706,22 +707,25 @@ def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=No
     include/flashmask.h for scales and rounding."""
     c, Hk, d, index = cache._handle
     ks, vs = _rows(k, "k", torch.bfloat16, index), _rows(v, "v", torch.bfloat16, index)
-    B, _, N, _ = k.shape
-    if v.shape != k.shape or k.shape[1] != Hk or k.shape[3] != d:
+    shape = k.shape
+    B, heads, N, width = shape
+    if v.shape != shape or heads != Hk or width != d:
         raise ValueError("k and v must be [B, Hk, N, d] with the cache's Hk and d")
     max_pages = _page_table(page_table, B, index)
     st, ct = _per_sequence(start, "start", B, index), _per_sequence(count, "count", B, index)
-    _want(ws, "ws", torch.uint8, index, (ws.numel(),))
+    ws_bytes = ws.numel()
+    _want(ws, "ws", torch.uint8, index, (ws_bytes,))
 
     def call(raw):
         code = load().flashmask_cache_append(c, page_table.data_ptr(), max_pages, k.data_ptr(),
                                              _STRIDES.pack(*ks[:3]), v.data_ptr(),
                                              _STRIDES.pack(*vs[:3]), st, ct, B, N, ws.data_ptr(),
-                                             ws.numel(), raw)
+                                             ws_bytes, raw)
         if code:
             raise FlashMaskError(code, "flashmask_cache_append")
 
-    _launch(index, stream, (*cache.tensors, page_table, k, v, start, count, ws), call)
+    _launch(index, stream, () if stream is None else (*cache.tensors, page_table, k, v, start, count, ws),
+            call)
 
 
 def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMask | None = None,
@@ -734,12 +738,14 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
     of `o` and `lse` are left as they were."""
     c, _, d, index = cache._handle
     qs = _rows(q, "q", torch.bfloat16, index)
-    B, H, N, _ = q.shape
-    if q.shape[3] != d:
+    shape = q.shape
+    B, H, N, width = shape
+    if width != d:
         raise ValueError("q must have the cache's d")
     max_pages = _page_table(page_table, B, index)
     ln, ql = _per_sequence(lens, "lens", B, index), _per_sequence(q_lens, "q_lens", B, index)
-    _want(ws, "ws", torch.uint8, index, (ws.numel(),))
+    ws_bytes = ws.numel()
+    _want(ws, "ws", torch.uint8, index, (ws_bytes,))
     vectors, m = (), None
     if mask is not None:
         vectors = (mask.lts, mask.lte, mask.uts, mask.ute)
@@ -754,23 +760,24 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
         m = _FmMask(*ptrs, Hm, bool(mask.causal))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    os = (H * N * d, N * d, d)
     if o is not None:
-        _rows(o, "o", torch.bfloat16, index)
-        if o.shape != q.shape:
+        os = _rows(o, "o", torch.bfloat16, index)
+        if o.shape != shape:
             raise ValueError("o must have q's shape")
     if lse is not None:
         _want(lse, "lse", torch.float32, index, (B, H, N))
 
     def call(raw):
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device) if o is None else o
         norm = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
         code = load().flashmask_fwd_cache(q.data_ptr(), _STRIDES.pack(*qs[:3]), c,
                                           page_table.data_ptr(), max_pages, ln, ql, m, B, H, N, scale,
-                                          out.data_ptr(), _STRIDES.pack(*out.stride()[:3]), norm.data_ptr(),
-                                          ws.data_ptr(), ws.numel(), raw)
+                                          out.data_ptr(), _STRIDES.pack(*os[:3]), norm.data_ptr(),
+                                          ws.data_ptr(), ws_bytes, raw)
         if code:
             raise FlashMaskError(code, "flashmask_fwd_cache")
         return out, norm
 
-    return _launch(index, stream, (q, *cache.tensors, page_table, lens, q_lens, ws, o, lse, *vectors),
-                   call)
+    return _launch(index, stream, () if stream is None else
+                   (q, *cache.tensors, page_table, lens, q_lens, ws, o, lse, *vectors), call)
