@@ -211,7 +211,7 @@ def _cache(pages, Hk, d, gen, dev):
             codes[p:p + step] = (x * 96.0).clamp(-448, 448).to(torch.float8_e4m3fn)
         k = torch.randint(-8, -5, (pages, Hk), generator=gen, device=dev)
         s[name + "8"] = codes
-        s[name + "scale"] = _pow2(k).float()
+        s[name + "scale"] = torch.exp2(k.float())
     return s
 
 
@@ -298,11 +298,6 @@ def _rope_plain(s):
     return out
 
 
-def _pow2(k):
-    """2^k in fp64 from its bits (exp2 and ldexp may be a rounding off)."""
-    return ((k.to(torch.int64) + 1023) << 52).view(torch.float64)
-
-
 def _gather(codes, scale, table):
     """[B, M, Hk, ...] values of the pages in `table` (entries below 0 read page 0)."""
     t = table.clamp(min=0).long()
@@ -313,7 +308,7 @@ def _scale_of(absmax):
     m, e = torch.frexp(absmax)
     k = torch.where(m <= 0.875, e - 9, e - 8).clamp(min=-100)
     k = torch.where(absmax > 0, k, -100)
-    return _pow2(k).float()
+    return torch.ldexp(torch.ones_like(absmax), k)
 
 
 def _append_plain(s):
@@ -424,7 +419,7 @@ def _exact_rope(s):
 def _round_e4m3(x):
     """Nearest e4m3 value (ties to even) of 64-bit values of magnitude <= 448."""
     _, e = torch.frexp(x)
-    step = _pow2((e - 4).clamp(min=-9))
+    step = torch.ldexp(torch.ones_like(x), (e - 4).clamp(min=-9))
     return torch.round(x / step) * step
 
 
@@ -441,9 +436,9 @@ def _exact_append(s):
                 x = s[name][b, :, t - held[b]:t - held[b] + n].double()  # [Hk, n, d]
                 body = codes[page] if name == "k" else codes[page].transpose(-1, -2)
                 top = x.abs().amax((1, 2))
-                k = torch.ceil(torch.log2(top / 448.0)).clamp(-150, 150).to(torch.int64)
-                k = k + (top > 448.0 * _pow2(k)).long() - (top <= 224.0 * _pow2(k)).long()
-                scale = _pow2(k.clamp(min=-100))
+                k = torch.ceil(torch.log2(top / 448.0))
+                k = k + (top > 448.0 * torch.exp2(k)).double() - (top <= 224.0 * torch.exp2(k)).double()
+                scale = torch.exp2(k.clamp(min=-100.0))
                 if lo:
                     scale = torch.maximum(scale, scales[page])
                     body[:, :lo] = _round_e4m3(body[:, :lo] * (scales[page] / scale)[:, None, None])
