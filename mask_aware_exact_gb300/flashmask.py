@@ -626,7 +626,8 @@ class KVCache:
     """Keys and values as e4m3 codes in pages of FM_PAGE tokens with one scale per
     page and head: k8 [pages, Hk, 64, d], v8 [pages, Hk, d, 64] (float8_e4m3fn,
     V transposed, no NaN codes in it), kscale, vscale fp32 [pages, Hk]. Its tensors
-    are checked at its first use, and again if one of them has moved since."""
+    are checked at its first use, and again if one of them has changed its place,
+    shape, layout or type since (set_, resize_, .data)."""
 
     k8: torch.Tensor
     v8: torch.Tensor
@@ -647,7 +648,10 @@ class KVCache:
     @property
     def _handle(self):
         """(C struct, Hk, d, device index)"""
-        at = (self.k8.data_ptr(), self.v8.data_ptr(), self.kscale.data_ptr(), self.vscale.data_ptr())
+        k8, v8, ks, vs = self.k8, self.v8, self.kscale, self.vscale
+        at = (k8.data_ptr(), v8.data_ptr(), ks.data_ptr(), vs.data_ptr(), k8.shape, v8.shape, ks.shape,
+              vs.shape, k8.is_contiguous(), v8.is_contiguous(), ks.is_contiguous(), vs.is_contiguous(),
+              k8.dtype, v8.dtype, ks.dtype, vs.dtype)
         made = self.__dict__.get("_made")
         if made is None or made[0] != at:
             made = at, self._check()
