@@ -355,8 +355,9 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
  * page_table is int32 [B, max_pages]: entry i of a row is the page holding the
  * sequence's tokens [64 i, 64 i + 64). Only the entries of pages that a call
  * needs are read; the rest may hold anything. d in {64, 128}; FM_PAGE *
- * max_pages <= FM_MAX_SEQLEN; B * H * N < 2^31 - 255, B < 2^16, and B * Hk * ceil(H / Hk *
- * N / 128) * max_pages < 2^31. Entries, lengths and starts live on the device:
+ * max_pages <= FM_MAX_SEQLEN; B * H * N < 2^31 - 255, B < 2^16, and B * Hk * T * max_pages
+ * < 2^31 - 256, where T = ceil(R / 128) tiles hold the R = H / Hk * N rows of a cache head
+ * (T = 2 for 17 to 32 rows). Entries, lengths and starts live on the device:
  * the kernels check each one they use, leave the access out when it is out of
  * range and record it, so that flashmask_check_status() returns FM_ERR_PAGE
  * (the outputs of that sequence are then undefined). */

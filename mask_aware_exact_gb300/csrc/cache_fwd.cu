@@ -1026,7 +1026,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 bool cache_line_ok(int B, int H, int Hk, int N, int max_pages) {
   const Geometry g = geometry(H, Hk, Hk, N, max_pages);
-  return static_cast<double>(B) * Hk * g.RT * max_pages < 2147483648.0;
+  // (rounding up to whole runs adds less than a page for each CTA)
+  return static_cast<double>(B) * Hk * g.RT * max_pages < 2147483648.0 - kCacheMaxCtas;
 }
 
 CacheWs cache_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
