@@ -351,7 +351,8 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
  *   k8      e4m3 [pages, Hk, FM_PAGE, d]
  *   v8      e4m3 [pages, Hk, d, FM_PAGE]  (transposed: the tokens of one column
  *                                          lie together, as P V reads them)
- *   kscale, vscale  fp32 [pages, Hk]      a value is its code times the scale
+ *   kscale, vscale  fp32 [pages, Hk]      a value is its code times the scale, which is
+ *                                         finite and not negative
  * page_table is int32 [B, max_pages]: entry i of a row is the page holding the
  * sequence's tokens [64 i, 64 i + 64). Only the entries of pages that a call
  * needs are read; the rest may hold anything. d in {64, 128}; FM_PAGE *
@@ -423,7 +424,8 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * a sequence's end hold and what pages hold of which no row sees a key has no
  * influence, NaN included. V codes of the other slots must not be NaN, masked or not
  * (flashmask_cache_append writes none: a NaN in V becomes one in K). A query row with a
- * value that is not finite gives NaN.
+ * value that is not finite gives NaN, and so does a row that sees a key of a page whose K
+ * or V scale is negative, infinite or NaN.
  *   qs, os: strides of Q and O in elements for batch, head and token (multiples
  *   of 8; the last dimension contiguous, 16-byte aligned). O may be Q itself with
  *   the same strides; otherwise O and LSE overlap neither each other nor an input.

@@ -280,6 +280,13 @@ __device__ __forceinline__ int next_units(int seg, int k, int nseg, int most, F 
   return min(__shfl_sync(0xffffffffu, c, 31), most);
 }
 
+// Whether a page's scales are none (negative, infinite or NaN): rows that see a key of
+// it get NaN.
+__device__ __forceinline__ int no_scales(float k, float v) {
+  constexpr float kMost = 3.402823466e38f;
+  return !(k >= 0.f && k <= kMost && v >= 0.f && v <= kMost);
+}
+
 // Four codes -> two fp16 pairs.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"

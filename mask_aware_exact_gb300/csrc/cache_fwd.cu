@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
     auto feed_v = [&](int w, int q, int logical, int cut, size_t off, float k_s, float v_s) {
       const int slot_k = q % kSlots, slot = (q + 1) % kSlots;
       *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot_k) =
-          make_int4(logical, cut, __float_as_int(k_s), __float_as_int(v_s));
+          make_int4(logical, cut | no_scales(k_s, v_s) << 1, __float_as_int(k_s), __float_as_int(v_s));
       mbar_arrive_expect_tx(bar.full(w, slot_k), logical >= 0 ? S::kHalf : 0);
       if (q + 1 >= kSlots && !cache_wait(bar.empty(w, slot), ((q + 1) / kSlots - 1) & 1, p.status)) return false;
       mbar_arrive_expect_tx(bar.full(w, slot), logical >= 0 ? S::kHalf : 0);
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
               const int n = meta.x < 0 ? 0 : min(max(lim[t][e] - (j0 + kb), 0), 16);
               uint32_t see = (1u << ((n + 1) >> 1)) - 1u;
               if constexpr (kVec) {
-                if (meta.y && meta.x >= 0) {
+                if ((meta.y & 1) && meta.x >= 0) {
                   const size_t at = mrow[t][e] + j0 + (kb & ~1);
                   if (p.mask.lts) see &= ~hidden8(p.mask.lts + at, p.mask.lte + at, pos[t][e], g & 1);
                   if (p.mask.uts) see &= ~hidden8(p.mask.uts + at, p.mask.ute + at, pos[t][e], g & 1);
@@ -682,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                   if (!((see >> (2 * u + x)) & 1u)) s[u][t][2 * x + e] = -INFINITY;
+                  else if (meta.y & 2) s[u][t][2 * x + e] = __int_as_float(0x7fffffff);
             }
         }
 #pragma unroll

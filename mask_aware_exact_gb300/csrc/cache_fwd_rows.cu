@@ -64,7 +64,8 @@ constexpr float kLag = 8.f;  // mv may lag the row's largest product by this muc
 // A step's description, int[16]: the step, then four words for each of its two pages
 // (first key, or -1 for none; K scale; log2 of the V scale; keys before the end).
 enum MetaWord { kFlags, kSeg, kCta0, kParts, kPageWords, kJ0 = 0, kKs, kLvs, kValid };
-enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16, kCut = 32 };  // kCut << page
+// kCut and kNoScales << page
+enum Flag { kFirstStep = 1, kLastStep = 2, kEnd = 4, kWhole = 8, kTailSlot = 16, kCut = 32, kNoScales = 128 };
 
 template <int D>
 struct Layout {
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
       int my_seg, my_k, my_n;
       const int avail = next_units(
           seg, k, nseg, min(32, steps - done), [&](int s) { return steps_of<kVec>(p, geo, s); }, my_seg, my_k, my_n);
-      int page[2] = {-1, -1}, j0[2] = {-1, -1}, valid[2] = {0, 0}, cut[2] = {0, 0};
+      int page[2] = {-1, -1}, j0[2] = {-1, -1}, valid[2] = {0, 0}, cut[2] = {0, 0}, none[2] = {0, 0};
       float ks[2] = {0.f, 0.f}, lvs[2] = {0.f, 0.f};
       if (lane < avail) {
         const int bh = geo.by_RT.div(my_seg), rt = my_seg - bh * geo.RT, b = geo.by_Hk.div(bh), hk = bh - b * p.c.Hk;
@@ -235,8 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           page[x] = pg;
           j0[x] = logical * kPage;
           valid[x] = min(r.len - j0[x], kPage);
+          const float vs = p.c.vscale[ph];
           ks[x] = p.c.kscale[ph];
-          lvs[x] = __log2f(p.c.vscale[ph]);
+          none[x] = no_scales(ks[x], vs);
+          lvs[x] = __log2f(vs);
         }
       }
       for (int t = 0; ok && t < avail; ++t, ++done) {
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         int m[kMetaInts] = {};
         int pg[2];
         m[kSeg] = sg;
-        const int cuts = __shfl_sync(0xffffffffu, cut[0] | cut[1] << 1, t);
+        const int cuts = __shfl_sync(0xffffffffu, cut[0] | cut[1] << 1 | none[0] << 2 | none[1] << 3, t);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           pg[x] = __shfl_sync(0xffffffffu, page[x], t);
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         // a score is S times c; c > 0 keeps masked scores at -inf
         const float c = fmaxf(crow * __int_as_float(pw.y), 1.17549435e-38f);
         const float lvs = __int_as_float(pw.z);
-        const bool masked = j0 < 0 || j0 + kPage > all_lim || (flags & (kCut << w));
+        const bool masked = j0 < 0 || j0 + kPage > all_lim || (flags & ((kCut | kNoScales) << w));
         ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J / R) & 1, p.status));
         if (!ok) break;
         if (!warp_live) {
@@ -553,8 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
               }
             }
             const uint32_t hlo = static_cast<uint32_t>(hid), hhi = static_cast<uint32_t>(hid >> 32);
+            const bool none = flags & (kNoScales << w);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : sv[j];
+            for (int j = 0; j < 64; ++j)
+              sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : none ? 0x7fffffffu : sv[j];
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
