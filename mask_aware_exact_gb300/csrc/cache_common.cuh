@@ -344,15 +344,16 @@ __device__ __forceinline__ bool count_wait(const int* count, int want, int32_t* 
   __threadfence_block();
   return true;
 }
-// 2^(a - b) where either may be -inf (then a is, or both are).
-__device__ __forceinline__ float ex2_diff(float a, float b) { return a == b ? 1.f : ex2(a - b); }
-
-// O and LSE of a row from sums relative to m and mv.
-__device__ __forceinline__ float out_factor(float m, float mv, float l, float shift) {
-  // acc = 2^(shift - mv) sum P V and l = 2^-m sum P
-  const float f = mv == -INFINITY ? 0.f : ex2(mv - (m == -INFINITY ? 0.f : m) - shift);
-  return l == 0.f ? 0.f : f / l;
+// A row's sums: P = 2^(score - m), l = sum P and acc = 2^(shift - mv) sum P V, with m the
+// largest score so far and mv the log2 of the largest P * scale of V. mv counts from m: it
+// would lose the scale beside a large score. Before the first key they have the lowest
+// values, not -inf, so that differences are numbers.
+constexpr float kNoScore = -3.402823466e38f, kNoProduct = -1e30f;
+__device__ __forceinline__ float out_factor(float mv, float l, float shift) {
+  return l == 0.f ? 0.f : ex2(mv - shift) / l;
 }
+// log2 of a page's V scale; of 0, a value so low that nothing is left of its products.
+__device__ __forceinline__ float log2_scale(float scale) { return fmaxf(__log2f(scale), -300.f); }
 __device__ __forceinline__ float out_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }

@@ -42,7 +42,7 @@
 // then holds every bf16 element down to 2^-30 of the largest exactly. P is rounded
 // to fp16 (2^-11 relative) after scaling by the page's V scale, relative to the
 // row's largest such product: a second running maximum, mv of log2(P * scale),
-// beside m of the scores, so that neither the weights of pages with small values
+// beside m of the scores (mv counts from m), so that neither the weights of pages with small values
 // (in l) nor the values of pages with small weights are lost. m, mv, l and O are
 // fp32.
 //
@@ -153,7 +153,7 @@ struct State {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[t][e] = mv[t][e] = -INFINITY;
+        m[t][e] = kNoScore, mv[t][e] = kNoProduct;
         l[t][e] = 0.f;
       }
   }
@@ -191,7 +191,7 @@ struct FragmentSums {
     for (int q = 0; q < kMine; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
-    m = mv = -INFINITY;
+    m = kNoScore, mv = kNoProduct;
     l = 0.f;
   }
   // Row of element e of this lane in the warp's fragment q.
@@ -203,26 +203,33 @@ struct FragmentSums {
     auto place = [&](int k) { return from + k < kConsumers ? from + k : from + k - kConsumers; };
     // states lane / kRows, + kAtOnce, ..
     float xm[kSteps], xv[kSteps], xl[kSteps];
-    float mm = m, mmv = mv;
+    float mm = m;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int k = lane / kRows + kAtOnce * i;
       const float* x = stats + 3 * kRows * place(min(k, n - 1)) + lane % kRows;
       xm[i] = x[0], xv[i] = x[kRows], xl[i] = k < n ? x[2 * kRows] : 0.f;
       mm = fmaxf(mm, xm[i]);
+    }
+#pragma unroll
+    for (int o = kRows; o < 32; o <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    const float d = m - mm;
+    mv += d;
+    float mmv = mv;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      xm[i] -= mm;
+      xv[i] += xm[i];
       mmv = fmaxf(mmv, xv[i]);
     }
 #pragma unroll
-    for (int o = kRows; o < 32; o <<= 1) {
-      mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-      mmv = fmaxf(mmv, __shfl_xor_sync(0xffffffffu, mmv, o));
-    }
-    l *= ex2_diff(m, mm);
-    const float old = ex2_diff(mv, mmv);
+    for (int o = kRows; o < 32; o <<= 1) mmv = fmaxf(mmv, __shfl_xor_sync(0xffffffffu, mmv, o));
+    l *= ex2(d);
+    const float old = ex2(mv - mmv);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      l += xl[i] * ex2_diff(xm[i], mm);
-      xv[i] = lane / kRows + kAtOnce * i < n ? ex2_diff(xv[i], mmv) : 0.f;
+      l += xl[i] * ex2(xm[i]);
+      xv[i] = lane / kRows + kAtOnce * i < n ? ex2(xv[i] - mmv) : 0.f;
     }
     m = mm;
     mv = mmv;
@@ -269,7 +276,7 @@ struct FragmentSums {
   __device__ __forceinline__ void store(const CacheFwdParams& p, const Geometry& geo, int b, int hk, int r0, int rows,
                                         int warp, int lane) const {
     const int g = lane >> 2, c = lane & 3;
-    const float x = sum(), f = out_factor(m, mv, x, kPShift);
+    const float x = sum(), f = out_factor(mv, x, kPShift);
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
       const int fr = warp + kConsumers * q;
@@ -617,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
         ok = __all_sync(0xffffffffu, cache_wait(bar.full(warp, sk), (seq / kSlots) & 1, p.status));
         if (!ok) break;
         const int4 meta = *(reinterpret_cast<const int4*>(smem + S::kMeta) + warp * kSlots + sk);
-        const float lvs = __log2f(__int_as_float(meta.w));
+        const float lvs = log2_scale(__int_as_float(meta.w));
         const int j0 = meta.x * kPage;
         // S^T: instruction u holds the keys kb + 4 u and kb + 4 u + 2 of this lane
         const int kb = 16 * (g >> 1) + (g & 1);
@@ -700,23 +707,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
             for (int e = 0; e < 2; ++e) top[t][e] = fmaxf(top[t][e], __shfl_xor_sync(0xffffffffu, top[t][e], o));
         uint32_t pf[4][NT][2];
         bool moved = false;
-        float av[NT][2], mu[NT][2], fv[NT][2];
+        float av[NT][2], fv[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float m_new = fmaxf(st.m[t][e], top[t][e]), mv_new = fmaxf(st.mv[t][e], top[t][e] + lvs);
-            st.l[t][e] *= ex2_diff(st.m[t][e], m_new);
-            av[t][e] = ex2_diff(st.mv[t][e], mv_new);
+            const float m_new = fmaxf(st.m[t][e], top[t][e]), d = st.m[t][e] - m_new;
+            const float mv_old = st.mv[t][e] + d, mv_new = fmaxf(mv_old, top[t][e] - m_new + lvs);
+            st.l[t][e] *= ex2(d);
+            av[t][e] = ex2(mv_old - mv_new);
             moved |= av[t][e] != 1.f;
             st.m[t][e] = m_new;
             st.mv[t][e] = mv_new;
-            mu[t][e] = m_new == -INFINITY ? 0.f : m_new;
-            fv[t][e] = ex2(fminf(mu[t][e] + lvs - (mv_new == -INFINITY ? 0.f : mv_new) + kPShift, 126.f));
+            fv[t][e] = ex2(fminf(lvs - mv_new + kPShift, 126.f));
           }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-mu[t][0], -mu[t][1]), f2 = f2_make(fv[t][0], fv[t][1]);
+          const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-st.m[t][0], -st.m[t][1]), f2 = f2_make(fv[t][0], fv[t][1]);
           uint64_t l2 = f2_make(st.l[t][0], st.l[t][1]);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
@@ -824,10 +831,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            st.m[t][e] = fmaxf(st.m[t][e], x[8 * t + e]);
-            st.mv[t][e] = fmaxf(st.mv[t][e], x[kRows + 8 * t + e]);
-          }
+          for (int e = 0; e < 2; ++e) st.m[t][e] = fmaxf(st.m[t][e], x[8 * t + e]);
+      }
+      for (int k = 0; k < writers; ++k) {
+        const float* x = stats + 3 * kRows * ((first + k) % kConsumers) + 2 * c;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            st.mv[t][e] = fmaxf(st.mv[t][e], x[kRows + 8 * t + e] + (x[8 * t + e] - st.m[t][e]));
       }
       for (int k = 0; k < writers; ++k) {
         const int w = (first + k) % kConsumers;
@@ -837,8 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            st.l[t][e] += x[2 * kRows + 8 * t + e] * ex2_diff(x[8 * t + e], st.m[t][e]);
-            f[t][e] = ex2_diff(x[kRows + 8 * t + e], st.mv[t][e]);
+            const float d = x[8 * t + e] - st.m[t][e];
+            st.l[t][e] += x[2 * kRows + 8 * t + e] * ex2(d);
+            f[t][e] = ex2(x[kRows + 8 * t + e] + d - st.mv[t][e]);
           }
 #pragma unroll
         for (int n = 0; n < D / 16; ++n)
@@ -861,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
     if (whole) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float f0 = out_factor(st.m[t][0], st.mv[t][0], st.l[t][0], kPShift);
-        const float f1 = out_factor(st.m[t][1], st.mv[t][1], st.l[t][1], kPShift);
+        const float f0 = out_factor(st.mv[t][0], st.l[t][0], kPShift);
+        const float f1 = out_factor(st.mv[t][1], st.l[t][1], kPShift);
         const int rr = rt * kRows + 8 * t + g;  // the row this lane holds after the transposes
         const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
         uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + 2 * c;

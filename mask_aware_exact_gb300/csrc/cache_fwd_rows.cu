@@ -13,7 +13,7 @@
 // warpgroup w taking page w, with states and accumulators O_w of their own, merged
 // when a piece ends. So a warpgroup meets one K scale and one V scale a step: the
 // first goes into the exponent, the second into P, relative to the row's largest
-// P * scale so far (mv, beside m of the scores), so that neither the weights of
+// P * scale so far (mv, counted from m of the scores), so that neither the weights of
 // pages with small values nor the values of pages with small weights are lost. P is
 // stored as fp16(2^7 P * scale / 2^mv) and O_w rescaled only when mv grows by more
 // than 2^8.
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           const float vs = p.c.vscale[ph];
           ks[x] = p.c.kscale[ph];
           none[x] = no_scales(ks[x], vs);
-          lvs[x] = __log2f(vs);
+          lvs[x] = log2_scale(vs);
         }
       }
       for (int t = 0; ok && t < avail; ++t, ++done) {
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.q_full());
-      float m_ = -INFINITY, mv = -INFINITY, l = 0.f;
+      float m_ = kNoScore, mv = kNoProduct, l = 0.f;
 
       // ---- the piece's steps; what is rare is kept out of the loop's straight line
       int flags;
@@ -569,15 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
               mx[i] = fmax3(mx[i], __uint_as_float(sv[j + 2 * i]), __uint_as_float(sv[j + 2 * i + 1]));
           const float pm = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
           const float m_new = fmaxf(m_, pm);
-          l *= ex2_diff(m_, m_new);
+          const float dm = m_ - m_new;
+          l *= ex2(dm);
           m_ = m_new;
-          const float mv_new = fmaxf(mv, pm + lvs);
-          const bool rescale = mv_new > mv + kLag;
-          const float mv_old = mv;
-          if (rescale) mv = mv_new;
-          const float mu = m_ == -INFINITY ? 0.f : m_, mvu = mv == -INFINITY ? 0.f : mv;
-          const float f = ex2(fminf(mu + lvs - mvu + kPShift, 126.f));
-          const uint64_t c2 = f2_make(c, c), nm2 = f2_make(-mu, -mu), f2 = f2_make(f, f);
+          const float mv_old = mv + dm, mv_new = fmaxf(mv_old, pm - m_new + lvs);
+          const bool rescale = mv_new > mv_old + kLag;
+          mv = rescale ? mv_new : mv_old;
+          const float f = ex2(fminf(lvs - mv + kPShift, 126.f));
+          const uint64_t c2 = f2_make(c, c), nm2 = f2_make(-m_new, -m_new), f2 = f2_make(f, f);
           uint64_t l2 = f2_make(0.f, 0.f);
           uint32_t pk[32];
 #pragma unroll
@@ -627,12 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
       red[(w * 3 + 2) * kRows + row] = l;
       if (!sync_softmax()) break;
       const float* other = red + (w ^ 1) * 3 * kRows + row;
-      const float m = fmaxf(m_, other[0]), mva = fmaxf(mv, other[kRows]);
+      const float m = fmaxf(m_, other[0]), da = m_ - m, db = other[0] - m;
+      const float mvs = mv + da, mvo = other[kRows] + db, mva = fmaxf(mvs, mvo);
       // the sum in the same order in both warpgroups, so that they agree to the bit
-      const float la = l * ex2_diff(m_, m), lb = other[2 * kRows] * ex2_diff(other[0], m);
+      const float la = l * ex2(da), lb = other[2 * kRows] * ex2(db);
       const float lsum = w == 0 ? la + lb : lb + la;
-      const float fs = ex2_diff(mv, mva), fo = ex2_diff(other[kRows], mva);
-      const float out = whole ? out_factor(m, mva, lsum, kPShift) : 1.f;
+      const float fs = ex2(mvs - mva), fo = ex2(mvo - mva);
+      const float out = whole ? out_factor(mva, lsum, kPShift) : 1.f;
       const float f0 = (w == 0 ? fs : fo) * out, f1 = (w == 0 ? fo : fs) * out;
       float* part = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot) * part_floats(D);
       uint16_t* o = p.o + b * p.os[0] + h * p.os[1] + tok * p.os[2] + w * (D / 2);
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
           const int n = word[3], last_join = word[4];
           part_no = word[1];
           group = true;
-          float jm = -INFINITY, jmv = -INFINITY, jl = 0.f;
+          float jm = kNoScore, jmv = kNoProduct, jl = 0.f;
           if (warp_live) {
             // the parts in the order of the keys: this thread's row and half of its columns
             const int stride = word[2];
@@ -696,17 +696,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
               return p.partial + (static_cast<size_t>(cta0 + x) * 2 + (x == 0 ? 1 : 0)) * part_floats(D);
             };
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-              const float* x = part_at(i) + kRows * D + row;
-              jm = fmaxf(jm, __ldcg(x));
-              jmv = fmaxf(jmv, __ldcg(x + kRows));
-            }
+            for (int i = 0; i < n; ++i) jm = fmaxf(jm, __ldcg(part_at(i) + kRows * D + row));
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
               const float* x = part_at(i) + kRows * D + row;
-              jl += __ldcg(x + 2 * kRows) * ex2_diff(__ldcg(x), jm);
+              const float dm = __ldcg(x) - jm;
+              jmv = fmaxf(jmv, __ldcg(x + kRows) + dm);
+              jl += __ldcg(x + 2 * kRows) * ex2(dm);
             }
-            const float fin = last_join ? out_factor(jm, jmv, jl, kPShift) : 1.f;
+            const float fin = last_join ? out_factor(jmv, jl, kPShift) : 1.f;
             float* sum = p.partial + (static_cast<size_t>(cta0 + part_no) * 2 + (part_no == 0 ? 1 : 0)) * part_floats(D);
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
@@ -716,8 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
               for (int i = 0; i < 16; ++i) y[i] = 0.f;
 #pragma unroll 4
               for (int i = 0; i < n; ++i) {
-                const float* x = part_at(i);
-                const float fx = ex2_diff(__ldcg(x + kRows * D + kRows + row), jmv);
+                const float *x = part_at(i), *st = x + kRows * D + row;
+                const float fx = ex2(__ldcg(st + kRows) + (__ldcg(st) - jm) - jmv);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   const float4 v = __ldcg(reinterpret_cast<const float4*>(x) + (col / 4 + j) * kRows + row);
