@@ -286,6 +286,21 @@ __device__ __forceinline__ int no_scales(float k, float v) {
   constexpr float kMost = 3.402823466e38f;
   return !(k >= 0.f && k <= kMost && v >= 0.f && v <= kMost);
 }
+// A score is a sum of products of codes and scaled query times c, c = (row's factor) * (K
+// scale) kept above 0 so that masked scores stay at -inf. Where c would pass fp32 (a row's
+// factor above 1, that is queries of 10^4 and more, and keys near 10^38), 2^110 of it go
+// to the sum first: what overflows then is a score that does.
+constexpr float kLeast = 1.17549435e-38f;
+__device__ __forceinline__ float score_factor(float row, float k_scale) { return fmaxf(row * k_scale, kLeast); }
+// What such a row's sums are multiplied by before c; NaN for a page without scales.
+__device__ __forceinline__ float score_boost(float row, float k_scale, bool none, float& c) {
+  float boost = 1.f;
+  if (isinf(c)) {
+    boost = __int_as_float((110 + 127) << 23);
+    c = score_factor(row * __int_as_float((127 - 110) << 23), k_scale);
+  }
+  return none ? __int_as_float(0x7fffffff) : boost;
+}
 
 // Four codes -> two fp16 pairs.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {

@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
           const int tok2 = geo.by_G.div(r2), h2 = hk * geo.G + r2 - tok2 * geo.G;
           pos[t][e] = r.shift + tok2;
           lim[t][e] = r2 < rows && p.mask.causal ? min(r.len, pos[t][e] + 1) : r.len;
-          all_lim = min(all_lim, lim[t][e]);
+          all_lim = crow[t][e] > 1.f ? 0 : min(all_lim, lim[t][e]);  // (the row may need score_boost)
           mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h2)) *
                                   static_cast<size_t>(p.max_pages * kPage)
                             : 0;
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
         if (lane == 0) mbar_arrive(bar.empty(warp, sk));
 
         // s[u][t][2 x + e]: key kb + 4 u + 2 x, row 2 c + e; ck times it is the score in
-        // log2 units (ck > 0 keeps masked scores at -inf)
+        // log2 units
         const float kscale = __int_as_float(meta.z);
         const bool tail = meta.x < 0 || j0 + kPage > all_lim;
         // Each pass goes over all rows of the lane, so that their chains overlap; a row
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) ck[t][e] = fmaxf(crow[t][e] * kscale, 1.17549435e-38f);
+          for (int e = 0; e < 2; ++e) ck[t][e] = score_factor(crow[t][e], kscale);
         if (__builtin_expect(tail || meta.y, 0)) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -684,12 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
                   if (p.mask.uts) see &= ~hidden8(p.mask.uts + at, p.mask.ute + at, pos[t][e], g & 1);
                 }
               }
+              const float boost = score_boost(crow[t][e], kscale, meta.y & 2, ck[t][e]);
 #pragma unroll
               for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                  if (!((see >> (2 * u + x)) & 1u)) s[u][t][2 * x + e] = -INFINITY;
-                  else if (meta.y & 2) s[u][t][2 * x + e] = __int_as_float(0x7fffffff);
+                  s[u][t][2 * x + e] = (see >> (2 * u + x)) & 1u ? s[u][t][2 * x + e] * boost : -INFINITY;
             }
         }
 #pragma unroll

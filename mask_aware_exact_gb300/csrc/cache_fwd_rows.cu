@@ -480,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
       const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
       const int pos = r.shift + tok;
       const int lim = live && p.mask.causal ? min(r.len, pos + 1) : r.len;
-      const int all_lim = __reduce_min_sync(0xffffffffu, lim);  // keys that every row of the warp sees
       const size_t mrow =
           kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h)) * static_cast<size_t>(p.max_pages * kPage) : 0;
       uint4 x[D / 16];
@@ -502,6 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
       const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
       const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
       const float crow = p.scale_log2 * __int_as_float((127 - up) << 23);
+      // keys that every row of the warp sees (none if one may need score_boost)
+      const int all_lim = __reduce_min_sync(0xffffffffu, crow > 1.f ? 0 : lim);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -528,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
         flags = meta_at[(J % kMetaRing) * kMetaInts + kFlags];
         const int4 pw = *reinterpret_cast<const int4*>(meta_at + (J % kMetaRing) * kMetaInts + kPageWords + 4 * w);
         const int j0 = pw.x;
-        // a score is S times c; c > 0 keeps masked scores at -inf
-        const float c = fmaxf(crow * __int_as_float(pw.y), 1.17549435e-38f);
+        float c = score_factor(crow, __int_as_float(pw.y));  // a score is S times c
         const float lvs = __int_as_float(pw.z);
         const bool masked = j0 < 0 || j0 + kPage > all_lim || (flags & ((kCut | kNoScales) << w));
         ok = __all_sync(0xffffffffu, cache_wait(bar.s_full(g), (J / R) & 1, p.status));
@@ -556,10 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
               }
             }
             const uint32_t hlo = static_cast<uint32_t>(hid), hhi = static_cast<uint32_t>(hid >> 32);
-            const bool none = flags & (kNoScales << w);
+            const float boost = score_boost(crow, __int_as_float(pw.y), flags & (kNoScales << w), c);
 #pragma unroll
             for (int j = 0; j < 64; ++j)
-              sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : none ? 0x7fffffffu : sv[j];
+              sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : __float_as_uint(__uint_as_float(sv[j]) * boost);
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
