@@ -327,9 +327,10 @@ fm_status flashmask_localize(const fm_mask* mask, int B, int N, int row0, int ro
  *               one row for all), any value; NULL: token n sits at position n.
  *   freqs       fp64 [rot_dim / 2], radians per position, on the device. Any
  *               scaling for long contexts is in them and in mscale.
- * The angle is taken in turns modulo one with 64-bit integers, so its error
- * does not grow with the position; sums are fp32 and rounded once. A frequency
- * that is not finite gives NaN. d >= 1, 0 <= rot_dim <= d and even; B * N <
+ * The angle is taken in turns modulo one with 64-bit integers: its error is
+ * below 2^-31 turns at every position and frequency, and then 2^-26 for its
+ * rounding to fp32; sums are fp32 and rounded once. A frequency that is not
+ * finite, or of 2^129 or more, gives NaN. d >= 1, 0 <= rot_dim <= d and even; B * N <
  * 2^31. B, N or H zero is FM_ERR_UNSUPPORTED. Asynchronous on `stream`; needs
  * no workspace. */
 typedef enum { FM_BF16 = 0, FM_F16 = 1, FM_F32 = 2 } fm_dtype;

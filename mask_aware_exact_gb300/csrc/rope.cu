@@ -5,7 +5,7 @@
 // frequency has no correct digits left there. So the frequency is held in
 // turns per position as a 64-bit fraction, f = freqs[i] / (2 pi) mod 1, and t *
 // f is a 64-bit integer product whose overflow is the reduction modulo one
-// turn: exact up to |t| * 2^-64 turns, with no fp64 arithmetic (a few results
+// turn: right to |t| * 2^-63 turns, whatever f, with no fp64 arithmetic (a few results
 // per clock and SM on this GPU). The upper 32 bits, read as a signed fraction
 // of half turns, go to sincospif.
 //
@@ -38,24 +38,37 @@ constexpr int kHeadsMost = 16;
 constexpr int kStages = 4;  // heads in flight per thread
 constexpr int kAtOnce = 8;  // heads loaded at a time when the elements are accessed one by one
 
-// f / (2 pi) modulo one turn as a 64-bit fraction, from the bits of the fp64
-// f: mantissa times the first 64 bits of 2 / pi, shifted by the exponent. The
-// relative error is below 2^-62.
-__device__ __forceinline__ uint64_t turns_per_position(double f, bool& finite) {
+// The first 192 bits of 2 / pi.
+constexpr uint64_t kTwoOverPi0 = 0xa2f9836e4e441529ull, kTwoOverPi1 = 0xfc2757d1f534ddc0ull,
+                   kTwoOverPi2 = 0xdb6295993c439041ull;
+
+// f / (2 pi) modulo one turn as a 64-bit fraction, less than two units of it off, from the
+// bits of the fp64 f: mantissa times 2 / pi, shifted by the exponent. Up to |f| = 4 the
+// first word of 2 / pi has all the bits that stay. `high` is set for a frequency above:
+// that one is for turns_of_high.
+__device__ __forceinline__ uint64_t turns_per_position(double f, bool& high) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(f));
-  const int ex = static_cast<int>((u >> 52) & 0x7ffu);
-  finite = ex != 0x7ff;
-  if (ex == 0) return 0;  // zero and denormals: less than 2^-1000 turns
-  const uint64_t mant = (u & 0xfffffffffffffull) | (1ull << 52);
-  constexpr uint64_t kTwoOverPi = 0xA2F9836E4E441529ull;  // floor(2 / pi * 2^64)
-  // f = mant * 2^(ex - 1075); f / (2 pi) * 2^64 = hi * 2^(ex - 1024)
-  const uint64_t hi = __umul64hi(mant << 11, kTwoOverPi);
-  const int sh = ex - 1024;
-  uint64_t r;
-  if (sh <= 0)
-    r = sh > -64 ? hi >> -sh : 0;
-  else
-    r = sh < 64 ? hi << sh : 0;
+  const int ex = static_cast<int>((u >> 52) & 0x7ffu), sh = ex - 1024;
+  high |= sh > 0;
+  // f = m * 2^(ex - 1086); f / (2 pi) * 2^64 = m * (2 / pi) * 2^sh (zero and denormals
+  // vanish: sh is -1024)
+  const uint64_t m = ((u & 0xfffffffffffffull) | (1ull << 52)) << 11;
+  const uint64_t r = sh > -64 ? __umul64hi(m, kTwoOverPi0) >> (-sh & 63) : 0;
+  return (u >> 63) ? 0ull - r : r;
+}
+// The same for |f| >= 4, where the shift moves further bits of 2 / pi up and the first out
+// at the top. There are enough of them below kFreqLimit.
+constexpr double kFreqLimit = 0x1p129;
+__device__ __noinline__ uint64_t turns_of_high(double f) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(f));
+  const int sh = static_cast<int>((u >> 52) & 0x7ffu) - 1024;
+  const uint64_t m = ((u & 0xfffffffffffffull) | (1ull << 52)) << 11;
+  // m * (2 / pi) * 2^(sh / 64 * 64) as whole and fraction; the whole modulo 2^64
+  const bool far = sh >= 64;
+  const uint64_t before = far ? kTwoOverPi0 : 0, at = far ? kTwoOverPi1 : kTwoOverPi0;
+  const uint64_t low = m * at, fraction = low + __umul64hi(m, far ? kTwoOverPi2 : kTwoOverPi1);
+  const uint64_t whole = m * before + __umul64hi(m, at) + (fraction < low);
+  const uint64_t r = sh & 63 ? whole << (sh & 63) | fraction >> (64 - (sh & 63)) : whole;
   return (u >> 63) ? 0ull - r : r;
 }
 
@@ -151,19 +164,32 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
   for (int i = 0; i < kVec; ++i) cs[i] = 1.f, sn[i] = 0.f;
   if (rotated) {
     const int pos = p.positions ? p.positions[b * p.pos_stride + t] : t;
+    // interleaved: the first access holds pairs e0 / 2 .., the second pairs e1 / 2 ..
+    auto freq = [&](int i) {
+      return p.freqs[!kInterleaved || kVec == 1 ? kVec * chunk + i : (i < kVec / 2 ? e0 : e1 - kVec) / 2 + i];
+    };
+    uint64_t turns[kVec];
+    bool high = false;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) turns[i] = turns_per_position(freq(i), high);
+    uint32_t none = 0;  // bit i: no frequency
+    if (__builtin_expect(high, 0)) {
+      // (one branch behind the loop: one for each pair cost 1 % of the gradient's case)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const double f = freq(i);
+        if (!(fabs(f) < 4.)) turns[i] = turns_of_high(f);
+        if (!(fabs(f) < kFreqLimit)) none |= 1u << i;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      bool finite;
-      // interleaved: the first access holds pairs e0 / 2 .., the second pairs e1 / 2 ..
-      const int pair = !kInterleaved || kVec == 1 ? kVec * chunk + i
-                                                  : (i < kVec / 2 ? e0 : e1 - kVec) / 2 + i;
-      const uint64_t f = turns_per_position(p.freqs[pair], finite);
-      const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * f;
+      const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns[i];
       // the top 32 bits in units of half turns, in [-1, 1)
       const float half_turns =
           static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
       sincospif(half_turns, &sn[i], &cs[i]);
-      const float c = finite ? p.mscale : __int_as_float(0x7fffffff);
+      const float c = none >> i & 1u ? __int_as_float(0x7fffffff) : p.mscale;
       cs[i] *= c;
       sn[i] *= p.inverse ? -c : c;
     }
