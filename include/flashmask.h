@@ -331,8 +331,8 @@ fm_status flashmask_localize(const fm_mask* mask, int B, int N, int row0, int ro
  * below 2^-31 turns at every position and frequency, and then 2^-26 for its
  * rounding to fp32; sums are fp32 and rounded once. A frequency that is not
  * finite, or of 2^129 or more, gives NaN. d >= 1, 0 <= rot_dim <= d and even; B * N <
- * 2^31. B, N or H zero is FM_ERR_UNSUPPORTED. Asynchronous on `stream`; needs
- * no workspace. */
+ * 2^31, B * N * d <= 2^38, at most 65535 heads together. B, N or H zero is
+ * FM_ERR_UNSUPPORTED. Asynchronous on `stream`; needs no workspace. */
 typedef enum { FM_BF16 = 0, FM_F16 = 1, FM_F32 = 2 } fm_dtype;
 typedef struct {
   const void* x;
@@ -421,7 +421,9 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * 0, H % Hm == 0. O, LSE and rows without a visible key are as at the top of
  * this file: O bf16 [B, H, N, d], LSE fp32 [B, H, N] (contiguous).
  * Keys and values count as their codes times their scales; scores, softmax
- * statistics and sums are fp32. What K holds for masked keys, what the slots behind
+ * statistics and sums are fp32. For its product with V a weight P = exp(score - largest)
+ * is rounded to fp16: 2^-11 of it, or 2^-32 of the row's largest P * (scale of V) where
+ * that is more; LSE and the sum that O is divided by have it unrounded. What K holds for masked keys, what the slots behind
  * a sequence's end hold and what pages hold of which no row sees a key has no
  * influence, NaN included. V codes of the other slots must not be NaN, masked or not
  * (flashmask_cache_append writes none: a NaN in V becomes one in K). A query row with a
