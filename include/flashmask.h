@@ -423,9 +423,9 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
  * Keys and values count as their codes times their scales; scores, softmax
  * statistics and sums are fp32. For its product with V a weight P = exp(score - largest)
  * is rounded to fp16: 2^-11 of it, or 2^-32 of the row's largest P * (scale of V) where
- * that is more; LSE and the sum that O is divided by have it unrounded. What K holds for masked keys, what the slots behind
- * a sequence's end hold and what pages hold of which no row sees a key has no
- * influence, NaN included. V codes of the other slots must not be NaN, masked or not
+ * that is more; LSE and the sum that O is divided by have it unrounded. What K holds
+ * for masked keys, what the slots behind a sequence's end hold and what pages hold of
+ * which no row sees a key has no influence, NaN included. V codes of the other slots must not be NaN, masked or not
  * (flashmask_cache_append writes none: a NaN in V becomes one in K). A query row with a
  * value that is not finite gives NaN, and so does a row that sees a key of a page whose K
  * or V scale is negative, infinite or NaN.
