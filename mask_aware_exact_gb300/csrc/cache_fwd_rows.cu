@@ -5,9 +5,10 @@
 // for few rows; a unit of the line is a step of two pages, 128 keys. The codes of a
 // step arrive by bulk copies and four warps turn them into fp16 operands in shared
 // memory (exact), K as [key][d] and V as [d][key], both K-major and 128-byte
-// swizzled; S = Q K^T and O += P V then run as kind::f16 with P in TMEM. Taking Q and
-// P as several e4m3 parts would need no conversion, but four parts of Q and two of
-// P to keep their precision: more tensor work than fp16 and the same operand reads.
+// swizzled; S = Q K^T and O += P V then run as kind::f16 with P in TMEM. Taking Q and P
+// as sums of e4m3 parts would need no conversion; two parts hold an element of Q down to
+// 2^-10 of its row's largest, four what fp16 holds of it (2^-30), three what it holds of
+// P. That was not timed.
 //
 // As in the forward on bf16 tensors two softmax warpgroups split the keys of a step,
 // warpgroup w taking page w, with states and accumulators O_w of their own, merged
