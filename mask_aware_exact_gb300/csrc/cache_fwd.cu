@@ -203,33 +203,24 @@ struct FragmentSums {
     auto place = [&](int k) { return from + k < kConsumers ? from + k : from + k - kConsumers; };
     // states lane / kRows, + kAtOnce, ..
     float xm[kSteps], xv[kSteps], xl[kSteps];
-    float mm = m;
+    float mm = m, mmv = mv;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int k = lane / kRows + kAtOnce * i;
       const float* x = stats + 3 * kRows * place(min(k, n - 1)) + lane % kRows;
       xm[i] = x[0], xv[i] = x[kRows], xl[i] = k < n ? x[2 * kRows] : 0.f;
-      mm = fmaxf(mm, xm[i]);
+      join_maxima(mm, mmv, xm[i], xv[i]);
     }
 #pragma unroll
-    for (int o = kRows; o < 32; o <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    const float d = m - mm;
-    mv += d;
-    float mmv = mv;
+    for (int o = kRows; o < 32; o <<= 1)
+      join_maxima(mm, mmv, __shfl_xor_sync(0xffffffffu, mm, o), __shfl_xor_sync(0xffffffffu, mmv, o));
+    l *= ex2(m - mm);
+    const float old = ex2(mv + (m - mm) - mmv);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      xm[i] -= mm;
-      xv[i] += xm[i];
-      mmv = fmaxf(mmv, xv[i]);
-    }
-#pragma unroll
-    for (int o = kRows; o < 32; o <<= 1) mmv = fmaxf(mmv, __shfl_xor_sync(0xffffffffu, mmv, o));
-    l *= ex2(d);
-    const float old = ex2(mv - mmv);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      l += xl[i] * ex2(xm[i]);
-      xv[i] = lane / kRows + kAtOnce * i < n ? ex2(xv[i] - mmv) : 0.f;
+      const float d = xm[i] - mm;
+      l += xl[i] * ex2(d);
+      xv[i] = lane / kRows + kAtOnce * i < n ? ex2(xv[i] + d - mmv) : 0.f;
     }
     m = mm;
     mv = mmv;
@@ -352,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
     auto feed_v = [&](int w, int q, int logical, int cut, size_t off, float k_s, float v_s) {
       const int slot_k = q % kSlots, slot = (q + 1) % kSlots;
       *(reinterpret_cast<int4*>(smem + S::kMeta) + w * kSlots + slot_k) =
-          make_int4(logical, cut | no_scales(k_s, v_s) << 1, __float_as_int(k_s), __float_as_int(v_s));
+          make_int4(logical, cut | may_be_no_scales(k_s, v_s) << 1, __float_as_int(k_s), __float_as_int(v_s));
       mbar_arrive_expect_tx(bar.full(w, slot_k), logical >= 0 ? S::kHalf : 0);
       if (q + 1 >= kSlots && !cache_wait(bar.empty(w, slot), ((q + 1) / kSlots - 1) & 1, p.status)) return false;
       mbar_arrive_expect_tx(bar.full(w, slot), logical >= 0 ? S::kHalf : 0);
@@ -670,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < 2; ++e) ck[t][e] = score_factor(crow[t][e], kscale);
         if (__builtin_expect(tail || meta.y, 0)) {
+          const bool none = (meta.y & 2) && no_scales(kscale, __int_as_float(meta.w));
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -684,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
                   if (p.mask.uts) see &= ~hidden8(p.mask.uts + at, p.mask.ute + at, pos[t][e], g & 1);
                 }
               }
-              const float boost = score_boost(crow[t][e], kscale, meta.y & 2, ck[t][e]);
+              const float boost = score_boost(crow[t][e], kscale, none, ck[t][e]);
 #pragma unroll
               for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -831,15 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) st.m[t][e] = fmaxf(st.m[t][e], x[8 * t + e]);
-      }
-      for (int k = 0; k < writers; ++k) {
-        const float* x = stats + 3 * kRows * ((first + k) % kConsumers) + 2 * c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            st.mv[t][e] = fmaxf(st.mv[t][e], x[kRows + 8 * t + e] + (x[8 * t + e] - st.m[t][e]));
+          for (int e = 0; e < 2; ++e) join_maxima(st.m[t][e], st.mv[t][e], x[8 * t + e], x[kRows + 8 * t + e]);
       }
       for (int k = 0; k < writers; ++k) {
         const int w = (first + k) % kConsumers;

@@ -558,9 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_rows_kernel(const __gri
             }
             const uint32_t hlo = static_cast<uint32_t>(hid), hhi = static_cast<uint32_t>(hid >> 32);
             const float boost = score_boost(crow, __int_as_float(pw.y), flags & (kNoScales << w), c);
+            if (__builtin_expect(__any_sync(0xffffffffu, boost != 1.f), 0)) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : __float_as_uint(__uint_as_float(sv[j]) * boost);
+              for (int j = 0; j < 64; ++j) sv[j] = __float_as_uint(__uint_as_float(sv[j]) * boost);
+            }
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] = (((j < 32 ? hlo : hhi) >> (j & 31)) & 1u) ? 0xff800000u : sv[j];
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
