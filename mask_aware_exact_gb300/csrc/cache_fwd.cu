@@ -24,12 +24,12 @@
 // adds them up. The run's last piece and the joins are added up by all warps.
 //
 // What bounds it. 8 rows: memory, once the cache is long (8 sequences of 131072 tokens,
-// 32 / 8 heads of 128: 322 us, 6.7 TB/s, 98 % of a copy; 64 up to 8192: 115 us, 83 %, with
+// 32 / 8 heads of 128: 324 us, 6.6 TB/s, 98 % of a copy; 64 up to 8192: 115 us, 83 %, with
 // 12000 of 210000 cycles before the first page and 14000 behind the last). 16 rows: the
 // loop's instructions, 900 for a page and tile, of which the seven warps issue 2.2 a
 // clock, eleven hardly more (16 sequences up to 16384, 32 / 4 heads of 64, 4 tokens, two
-// tiles of 16 rows: 45.6 us, floor 12.4; 50 of 80 thousand cycles in the loop, 9 before
-// the first page, the rest joins). Short ones: latency (one sequence of 1000 tokens: 10.8
+// tiles of 16 rows: 44.8 us, floor 12.4; 50 of 80 thousand cycles in the loop, 9 before
+// the first page, the rest joins). Short ones: latency (one sequence of 1000 tokens: 10.9
 // us, of which 4 are the way to the first page: where the run begins, page table, page,
 // query).
 //
@@ -72,8 +72,8 @@ constexpr int kBatch = 32 / kConsumers * kConsumers;  // tiles looked up at a ti
 constexpr int kMinRun = kConsumers;
 // Segments of at most kUncut pages, and at least this many for each CTA: every segment
 // is one warp's, without states to add up. 512 sequences up to 512 tokens, 8 cache heads:
-// 72.6 us so, 102 with a segment's pages spread over the warps; 1024 up to 100: 64, 81; 512
-// up to 512, 4 tokens: 87, 179. Segments of 62 pages spread better: 225, 208.
+// 74 us so, 102 with a segment's pages spread over the warps; 1024 up to 100: 65, 81; 512
+// up to 512, 4 tokens: 88, 179. Segments of 62 pages spread better: 225, 209.
 constexpr int kAlone = 7;
 constexpr float kPShift = 14.f;  // P is stored as 2^14 P
 constexpr int kOnce = 4 * kConsumers, kFan = 2 * kConsumers;  // see Join
@@ -998,8 +998,8 @@ cudaError_t launch_nt(const CacheFwdParams& p, const Geometry& geo, int num_sms,
 // rows of a tile that are empty. 16 sequences of 16384 tokens, 4 cache heads, tiles of
 // 16 rows / of 128, us:
 //   rows       16           24           32           40           64          128
-//   d = 64   40.4 / -    58.2 / 68.1  58.7 / 68.1  81.6 / 69.4   104 / 69.5   191 / 75.0
-//   d = 128  59.8 / -    83.1 / 86.6  84.9 / 87.0   133 / 89.4   172 / 90.2   325 / 96.7
+//   d = 64   41.0 / -    58.2 / 68.1  59.0 / 68.1  81.6 / 72.1   104 / 72.8   191 / 76.5
+//   d = 128  60.3 / -    83.3 / 86.6  84.9 / 87.0   133 / 91.5   172 / 92.4   325 / 99.5
 int rows_of_tile(int rows) { return rows <= 8 ? 8 : rows <= 32 ? 16 : kManyRows; }
 
 Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {

@@ -29,12 +29,14 @@
 // TMEM, d = 128: S (128 columns), two P (64 columns each), O_0 and O_1. P has columns
 // of its own, so the next S is computed as soon as this one has been read; with P
 // over two regions of S, an S waited for the products of two steps before, 553 us
-// where this takes 545. With d = 64 there is room for three regions, P over its S:
+// where this took 545. With d = 64 there is room for three regions, P over its S:
 // 69.5 us for 16 sequences of 16384 with 64 rows; two regions and two P: 77.
 //
 // Measured: 2 sequences of up to 32768 tokens, 512 query tokens, 32 / 8 heads of 128:
-// 545 us, 990 TFLOP/s, 52 % of the bf16 rate; 3 sequences up to 109407, 64 rows:
-// 172 us, 3.5 TB/s. A step of 128 keys takes 2 150 cycles. Its products need 1 024; shared
+// 554 us, 971 TFLOP/s, 51 % of the bf16 rate (of d = 64: 440 us); 3 sequences up to 109407,
+// 64 rows: 172 us, 3.5 TB/s. A step of 128 keys takes 2 180 cycles. (It took 545 us with mv
+// as a number of its own; see out_factor. The figures that follow are from then.) Its
+// products need 1 024; shared
 // memory (d = 128: 32 KB of codes and 64 KB of operands written, 32 KB and 96 KB read)
 // 1 750 at 128 bytes a clock; each softmax warp is busy for about 1 900, waits included,
 // and the conversion warps for about 1 600. None of them alone is the bound: without
@@ -43,6 +45,8 @@
 // us), S and P signalled to each warpgroup by itself (products of 64 keys, 610), the
 // next codes loaded while some are converted (567), registers moved from the other
 // roles to the softmax (615).
+// The row's factor for scores past fp32 has a branch of its own: in the selection of masked
+// scores it cost 3 % with d = 64 (455 us). Updating mv behind a branch: 561 us, 446.
 #include <atomic>
 
 #include "cache_common.cuh"
