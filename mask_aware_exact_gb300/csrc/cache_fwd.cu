@@ -42,9 +42,9 @@
 // then holds every bf16 element down to 2^-30 of the largest exactly. P is rounded
 // to fp16 (2^-11 relative) after scaling by the page's V scale, relative to the
 // row's largest such product: a second running maximum, mv of log2(P * scale),
-// beside m of the scores (mv counts from m), so that neither the weights of pages with small values
-// (in l) nor the values of pages with small weights are lost. m, mv, l and O are
-// fp32.
+// beside m of the scores (mv counts from m), so that neither the weights of pages
+// with small values (in l) nor the values of pages with small weights are lost. m,
+// mv, l and O are fp32.
 //
 // Layout of a fragment. Lane = 4 g + c. The summed index of S^T is permuted so that
 // a lane reads 16 consecutive codes of a key (d = 64 half + 16 c ..), the query laid
@@ -715,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const __grid_con
           }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-st.m[t][0], -st.m[t][1]), f2 = f2_make(fv[t][0], fv[t][1]);
+          const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), nm2 = f2_make(-st.m[t][0], -st.m[t][1]);
+          const uint64_t f2 = f2_make(fv[t][0], fv[t][1]);
           uint64_t l2 = f2_make(st.l[t][0], st.l[t][1]);
 #pragma unroll
           for (int u = 0; u < 4; ++u)

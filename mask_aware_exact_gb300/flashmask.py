@@ -625,9 +625,9 @@ def flashmask_rope_bwd(dq, dk, freqs, positions=None, interleaved=False, mscale=
 class KVCache:
     """Keys and values as e4m3 codes in pages of FM_PAGE tokens with one scale per
     page and head: k8 [pages, Hk, 64, d], v8 [pages, Hk, d, 64] (float8_e4m3fn,
-    V transposed, no NaN codes in it), kscale, vscale fp32 [pages, Hk]. Its tensors
-    are checked at its first use, and again if one of them has changed its place,
-    shape, layout or type since (set_, resize_, .data)."""
+    V transposed, no NaN codes in it), kscale, vscale fp32 [pages, Hk] (finite, not
+    negative). Its tensors are checked at its first use, and again if one of them has
+    changed its place, shape, layout or type since (set_, resize_, .data)."""
 
     k8: torch.Tensor
     v8: torch.Tensor
