@@ -345,6 +345,52 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
                          int64_t pos_stride, const double* freqs, int B, int N, int d, int rot_dim,
                          int interleaved, int dtype, float mscale, int inverse, void* stream);
 
+/* Norm of every head of Q and K and the rotation above in one pass: a head x of d
+ * elements becomes x * r * w, r = 1 / sqrt(mean(x^2) + eps), and its leading
+ * `rot_dim` elements are then rotated as by flashmask_rope (times mscale; the
+ * others are not). rot_dim = 0 is the norm alone.
+ *   t[0], t[1]  as for flashmask_rope: x, y [B, H, N, d] of `dtype` with strides in
+ *               elements; y may be x with the same strides, otherwise they must not
+ *               overlap. w: the weights [d] of this tensor, of `weight_dtype` (FM_F32
+ *               or `dtype`); NULL: ones. dy, ds and dw are the backward's.
+ * d <= 256; eps >= 1e-30; other limits, positions and freqs as for flashmask_rope. Sums and
+ * everything before the one rounding at the end are fp32; a head whose squares would
+ * pass fp32 is scaled first. Asynchronous on `stream`; needs no workspace.
+ *
+ * The backward gives the gradients from dy, that of the rotated output, and x, the
+ * forward's input (nothing else is kept from the forward):
+ *     g = dy rotated back, times mscale where it is rotated
+ *     dw = sum of g * x * r over batch, heads and tokens
+ *     dx = r * (g * w - x * r * mean(g * w * x * r))
+ *   x, dy       [B, H, N, d] with strides xs and ds; y: dx, which may be dy or x with the
+ *               same strides and otherwise overlaps no input
+ *   dw          [d] of `weight_dtype`, written; NULL where it is not wanted
+ *   ws          flashmask_norm_workspace_bytes(d) bytes, 256-byte aligned, need not be
+ *               zeroed; not to be shared by calls that may run at the same time. May be
+ *               NULL when no dw is wanted.
+ * The sums for dw have a fixed order: the same call gives the same bits. */
+typedef struct {
+  const void* x;
+  void* y;
+  const void* dy;
+  const void* w;
+  void* dw;
+  int H;
+  int64_t xs[3]; /* strides of x: batch, head, token (elements) */
+  int64_t ys[3]; /* of y                                        */
+  int64_t ds[3]; /* of dy                                       */
+} fm_norm_heads;
+fm_status flashmask_norm_rope(const fm_norm_heads* t, int n_tensors, const int32_t* positions,
+                              int64_t pos_stride, const double* freqs, int B, int N, int d, int rot_dim,
+                              int interleaved, int dtype, int weight_dtype, float mscale, float eps,
+                              void* stream);
+/* 0 for an unsupported d. */
+size_t flashmask_norm_workspace_bytes(int d);
+fm_status flashmask_norm_rope_bwd(const fm_norm_heads* t, int n_tensors, const int32_t* positions,
+                                  int64_t pos_stride, const double* freqs, int B, int N, int d, int rot_dim,
+                                  int interleaved, int dtype, int weight_dtype, float mscale, float eps, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ 8-bit paged cache
  * Keys and values of running sequences as e4m3 codes in pages of FM_PAGE
  * tokens, one scale for each page and head (the block scaling of the FP8

@@ -26,6 +26,29 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_t s);
 
+struct NormTensor {
+  const void* x;
+  const void* dy;  // backward only, like ds and dw
+  void* y;
+  const void* w;  // weights, null: ones
+  void* dw;       // their gradient, null: not wanted
+  int H;
+  int64_t xs[3], ds[3], ys[3];  // batch, head, token
+};
+struct NormParams {
+  NormTensor t[2];  // t[1].H = 0 when there is one tensor
+  const int32_t* positions;
+  int64_t pos_stride;
+  const double* freqs;
+  int B, N, d, rot, interleaved;
+  int w_fp32;  // weights and their gradients are fp32 (else of the tensors' type)
+  float mscale, eps;
+  float* partial;  // workspace, backward only: [kNormPartials][d] sums of CTAs
+};
+constexpr int kNormWidest = 256;     // elements of a head
+constexpr int kNormPartials = 1024;  // CTAs that leave sums, at most
+cudaError_t launch_norm_rope(const NormParams& p, int dtype, bool backward, int num_sms, cudaStream_t s);
+
 struct CacheDev {
   uint8_t* k8;
   uint8_t* v8;

@@ -82,6 +82,70 @@ fm_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   return FM_OK;
 }
 
+// Arguments that the norm with rotary positions and its gradients share.
+fm_status norm_params(const fm_norm_heads* t, int n_tensors, const int32_t* positions, int64_t pos_stride,
+                      const double* freqs, int B, int N, int d, int rot_dim, int interleaved, int dtype,
+                      int weight_dtype, float mscale, float eps, bool backward, fm::NormParams& p) {
+  if (!t || n_tensors < 1 || n_tensors > 2) return FM_ERR_INVALID_ARG;
+  if (dtype != FM_BF16 && dtype != FM_F16 && dtype != FM_F32) return FM_ERR_INVALID_ARG;
+  if (weight_dtype != dtype && weight_dtype != FM_F32) return FM_ERR_INVALID_ARG;
+  if (!std::isfinite(mscale) || !std::isfinite(eps) || !(eps >= 1e-30f)) return FM_ERR_INVALID_ARG;
+  if (rot_dim > 0 && !freqs) return FM_ERR_INVALID_ARG;
+  if (!aligned4(positions) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0) return FM_ERR_INVALID_ARG;
+  if (B <= 0 || N <= 0 || d <= 0 || d > fm::kNormWidest || rot_dim < 0 || rot_dim > d || rot_dim % 2 != 0)
+    return FM_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * N > 0x7fffffffLL) return FM_ERR_UNSUPPORTED;
+  p = {};
+  long long heads = 0;
+  const uintptr_t esize = dtype == FM_F32 ? 4 : 2, wsize = weight_dtype == FM_F32 ? 4 : 2;
+  auto at = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
+  for (int i = 0; i < n_tensors; ++i) {
+    const fm_norm_heads& h = t[i];
+    if (!h.x || !h.y || (backward && !h.dy)) return FM_ERR_INVALID_ARG;
+    if (at(h.x) % esize || at(h.y) % esize || at(h.w) % wsize) return FM_ERR_INVALID_ARG;
+    if (backward && (at(h.dy) % esize || at(h.dw) % wsize)) return FM_ERR_INVALID_ARG;
+    if (h.H <= 0) return FM_ERR_UNSUPPORTED;
+    heads += h.H;
+    fm::NormTensor& o = p.t[i];
+    o.x = h.x;
+    o.y = h.y;
+    o.w = h.w;
+    o.H = h.H;
+    for (int k = 0; k < 3; ++k) {
+      o.xs[k] = h.xs[k];
+      o.ys[k] = h.ys[k];
+    }
+    if (backward) {
+      o.dy = h.dy;
+      o.dw = h.dw;
+      for (int k = 0; k < 3; ++k) o.ds[k] = h.ds[k];
+    }
+  }
+  if (heads > 65535 || static_cast<long long>(B) * N * d > (1LL << 38)) return FM_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_tensors; ++i)
+    if (!apart(t[i].ys, B, t[i].H, N)) return FM_ERR_INVALID_ARG;
+  p.positions = positions;
+  p.pos_stride = pos_stride;
+  p.freqs = freqs;
+  p.B = B;
+  p.N = N;
+  p.d = d;
+  p.rot = rot_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  p.w_fp32 = weight_dtype == FM_F32 ? 1 : 0;
+  p.mscale = mscale;
+  p.eps = eps;
+  return FM_OK;
+}
+
+fm_status launch_norm(const fm::NormParams& p, int dtype, bool backward, void* stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return FM_ERR_CUDA;
+  return fm::launch_norm_rope(p, dtype, backward, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FM_OK
+             : FM_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,6 +197,36 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
   return fm::launch_rope(p, dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FM_OK
              : FM_ERR_CUDA;
+}
+
+fm_status flashmask_norm_rope(const fm_norm_heads* t, int n_tensors, const int32_t* positions,
+                              int64_t pos_stride, const double* freqs, int B, int N, int d, int rot_dim,
+                              int interleaved, int dtype, int weight_dtype, float mscale, float eps,
+                              void* stream) {
+  fm::NormParams p;
+  const fm_status st = norm_params(t, n_tensors, positions, pos_stride, freqs, B, N, d, rot_dim, interleaved,
+                                   dtype, weight_dtype, mscale, eps, false, p);
+  return st != FM_OK ? st : launch_norm(p, dtype, false, stream);
+}
+
+size_t flashmask_norm_workspace_bytes(int d) {
+  return d <= 0 || d > fm::kNormWidest ? 0 : static_cast<size_t>(fm::kNormPartials) * d * sizeof(float);
+}
+
+fm_status flashmask_norm_rope_bwd(const fm_norm_heads* t, int n_tensors, const int32_t* positions,
+                                  int64_t pos_stride, const double* freqs, int B, int N, int d, int rot_dim,
+                                  int interleaved, int dtype, int weight_dtype, float mscale, float eps, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  fm::NormParams p;
+  fm_status st = norm_params(t, n_tensors, positions, pos_stride, freqs, B, N, d, rot_dim, interleaved, dtype,
+                             weight_dtype, mscale, eps, true, p);
+  if (st != FM_OK) return st;
+  if (p.t[0].dw || p.t[1].dw) {
+    st = check_ws(ws, ws_bytes, flashmask_norm_workspace_bytes(d));
+    if (st != FM_OK) return st;
+  }
+  p.partial = static_cast<float*>(ws);
+  return launch_norm(p, dtype, true, stream);
 }
 
 size_t flashmask_cache_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages) {

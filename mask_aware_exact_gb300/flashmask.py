@@ -51,6 +51,12 @@ class _FmHeads(ctypes.Structure):
                 ("xs", ctypes.c_int64 * 3), ("ys", ctypes.c_int64 * 3)]
 
 
+class _FmNormHeads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("dy", ctypes.c_void_p),
+                ("w", ctypes.c_void_p), ("dw", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("xs", ctypes.c_int64 * 3), ("ys", ctypes.c_int64 * 3), ("ds", ctypes.c_int64 * 3)]
+
+
 class _FmCache(ctypes.Structure):
     _fields_ = [("k8", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("kscale", ctypes.c_void_p),
                 ("vscale", ctypes.c_void_p), ("pages", ctypes.c_int), ("Hk", ctypes.c_int),
@@ -63,7 +69,8 @@ EXPORTED = ("flashmask_workspace_bytes", "flashmask_workspace_layout", "flashmas
             "flashmask_fwd_bwd_host", "flashmask_localize", "flashmask_selftest_timeout",
             "flashmask_fwd_fp8_workspace_bytes", "flashmask_fwd_fp8_layout", "flashmask_fwd_fp8",
             "flashmask_check_status", "flashmask_status_string", "flashmask_rope",
-            "flashmask_cache_workspace_bytes", "flashmask_cache_append", "flashmask_fwd_cache")
+            "flashmask_cache_workspace_bytes", "flashmask_cache_append", "flashmask_fwd_cache",
+            "flashmask_norm_rope", "flashmask_norm_workspace_bytes", "flashmask_norm_rope_bwd")
 
 _lib = None
 
@@ -129,6 +136,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.flashmask_fwd_cache.argtypes = [vp, vp, ctypes.POINTER(_FmCache), vp, i, vp, vp,
                                       ctypes.POINTER(_FmMask), i, i, i, f, vp, vp, vp, vp, sz, vp]
     L.flashmask_fwd_cache.restype = i
+    norm = [vp, i, vp, ctypes.c_int64, vp, i, i, i, i, i, i, i, f, f]
+    L.flashmask_norm_rope.argtypes = [*norm, vp]
+    L.flashmask_norm_rope.restype = i
+    L.flashmask_norm_workspace_bytes.argtypes = [i]
+    L.flashmask_norm_workspace_bytes.restype = sz
+    L.flashmask_norm_rope_bwd.argtypes = [*norm, vp, sz, vp]
+    L.flashmask_norm_rope_bwd.restype = i
     _lib = L
     return L
 
@@ -618,6 +632,141 @@ def flashmask_rope_bwd(dq, dk, freqs, positions=None, interleaved=False, mscale=
     """Gradients of flashmask_rope's inputs from those of its outputs, same arguments."""
     return _rope(dq, dk, freqs, positions, interleaved, mscale, out, stream, 1,
                  "flashmask_rope_bwd")
+
+
+# ---------------------------------------------------------------- norm and rotary positions
+_NORM_HEADS = struct.Struct("@5Pi9q")  # an _FmNormHeads
+assert _NORM_HEADS.size == ctypes.sizeof(_FmNormHeads)
+
+
+def flashmask_norm_workspace_bytes(d) -> int:
+    return int(load().flashmask_norm_workspace_bytes(d))
+
+
+def alloc_norm_workspace(d, device="cuda") -> torch.Tensor:
+    """Workspace of flashmask_norm_rope_bwd for heads of d elements."""
+    n = flashmask_norm_workspace_bytes(d)
+    if n == 0:
+        raise FlashMaskError(FM_ERR_UNSUPPORTED, "flashmask_norm_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+def _norm_rope(q, k, grads, weights, freqs, positions, interleaved, mscale, eps, ws, out, stream, where):
+    dtype = q.dtype
+    code = _ROPE_DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("q must be bf16, fp16 or fp32")
+    index = q.get_device()
+    sq, sk = _rows(q, "q", dtype, index), None
+    B, Hq, N, d = q.shape
+    if k is not None:
+        sk = _rows(k, "k", dtype, index)
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
+            raise ValueError("q and k must share B, N and d")
+    gq = gk = None
+    if grads is not None:
+        dq, dk = grads
+        gq = _rows(dq, "dq", dtype, index)
+        if (dk is None) != (k is None):
+            raise ValueError("dk and k must both be given or both be None")
+        if dk is not None:
+            gk = _rows(dk, "dk", dtype, index)
+        if dq.shape != q.shape or (k is not None and dk.shape != k.shape):
+            raise ValueError("dq and dk must have the shapes of q and k")
+    w_dtype = None
+    for w, name in zip(weights, ("q_weight", "k_weight")):
+        if w is None:
+            continue
+        if w_dtype is None:
+            w_dtype = w.dtype
+            if w_dtype is not dtype and w_dtype is not torch.float32:
+                raise ValueError(f"{name} must be fp32 or of q's type")
+        _want(w, name, w_dtype, index, (d,))
+    qw, kw = weights
+    if k is None and kw is not None:
+        raise ValueError("k_weight needs k")
+    n = freqs.numel()
+    _want(freqs, "freqs", torch.float64, index, (n,))
+    if 2 * n > d:
+        raise ValueError("freqs must be [rot_dim / 2] with rot_dim <= d")
+    pos, pos_stride = None, 0
+    if positions is not None:
+        sp, tp = positions.shape, positions.stride()
+        if positions.dtype is not torch.int32 or positions.get_device() != index or \
+                len(sp) != 2 or sp[1] != N or (sp[0] != 1 and sp[0] != B) or (N > 1 and tp[1] != 1):
+            raise ValueError(f"positions must be int32 [{B}, {N}] or [1, {N}] on cuda:{index}, rows "
+                             "contiguous")
+        pos = positions.data_ptr()
+        pos_stride = tp[0] if sp[0] > 1 else 0
+    ws_bytes = 0
+    if ws is not None:
+        ws_bytes = ws.numel()
+        _want(ws, "ws", torch.uint8, index, (ws_bytes,))
+    yq = yk = tq = tk = None
+    if out is not None:
+        yq, yk = out[0], (out[1] if k is not None else None)
+        tq = _rows(yq, "out", dtype, index)
+        if yk is not None:
+            tk = _rows(yk, "out", dtype, index)
+        if yq.shape != q.shape or (k is not None and yk.shape != k.shape):
+            raise ValueError("out must have the shapes of q and k")
+
+    def call(raw):
+        device = q.device
+        oq, ok, uq, uk = yq, yk, tq, tk
+        if oq is None:
+            oq, uq = torch.empty((B, Hq, N, d), dtype=dtype, device=device), (Hq * N * d, N * d, d)
+            if k is not None:
+                ok, uk = torch.empty((B, Hk, N, d), dtype=dtype, device=device), (Hk * N * d, N * d, d)
+        wq = wk = None
+        if grads is not None:
+            make = torch.zeros_like if B * N * d == 0 else torch.empty_like
+            wq, wk = (None if w is None else make(w) for w in weights)
+        if B * N * d > 0:
+            at = lambda t: 0 if t is None else t.data_ptr()
+            none = (0, 0, 0)
+            heads = _NORM_HEADS.pack(q.data_ptr(), oq.data_ptr(), 0 if grads is None else dq.data_ptr(), at(qw),
+                                     at(wq), Hq, *sq[:3], *uq[:3], *(none if gq is None else gq[:3]))
+            if k is not None:
+                heads += _NORM_HEADS.pack(k.data_ptr(), ok.data_ptr(), 0 if grads is None else dk.data_ptr(),
+                                          at(kw), at(wk), Hk, *sk[:3], *uk[:3], *(none if gk is None else gk[:3]))
+            how = (heads, 1 if k is None else 2, pos, pos_stride, freqs.data_ptr(), B, N, d, 2 * n,
+                   bool(interleaved), code, FM_F32 if w_dtype is torch.float32 else code, mscale, eps)
+            if grads is None:
+                st = _lib.flashmask_norm_rope(*how, raw)
+            else:
+                st = _lib.flashmask_norm_rope_bwd(*how, None if ws is None else ws.data_ptr(), ws_bytes, raw)
+            if st:
+                raise FlashMaskError(st, where)
+        return (oq, ok) if grads is None else (oq, ok, wq, wk)
+
+    if _lib is None:
+        load()
+    return _launch(index, stream, () if stream is None else
+                   (q, k, *(grads or ()), *weights, freqs, positions, ws, yq, yk), call)
+
+
+def flashmask_norm_rope(q, k, q_weight, k_weight, freqs, positions=None, interleaved=False, mscale=1.0,
+                        eps=1e-6, out=None, stream=None):
+    """flashmask_rope of Q and K whose heads are normed first: x / sqrt(mean(x^2) + eps)
+    times the weights [d] (fp32 or q's type, both the same; None: ones). d <= 256. No
+    frequencies (freqs of no elements): the norm alone. Returns (Q', K'); the other
+    arguments are flashmask_rope's."""
+    return _norm_rope(q, k, None, (q_weight, k_weight), freqs, positions, interleaved, mscale, eps, None, out,
+                      stream, "flashmask_norm_rope")
+
+
+def flashmask_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, freqs, ws, positions=None, interleaved=False,
+                            mscale=1.0, eps=1e-6, out=None, stream=None):
+    """Gradients of flashmask_norm_rope's q, k, q_weight and k_weight from those of its
+    outputs (dq, dk) and its inputs. ws comes from alloc_norm_workspace (may be None
+    without weights); out: a pair to write dQ and dK into, (dq, dk) itself or (q, k)
+    to overwrite them. Weights that are None have no gradient (None)."""
+    return _norm_rope(q, k, (dq, dk), (q_weight, k_weight), freqs, positions, interleaved, mscale, eps, ws,
+                      out, stream, "flashmask_norm_rope_bwd")
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
