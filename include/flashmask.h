@@ -488,6 +488,33 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
                               float scale, void* o, const int64_t os[3], float* lse, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* The attention weight that each cached key is given, for deciding which keys a cache
+ * keeps: for key j of cache head hk
+ *     sum over its query heads h and the query rows that see j of exp(scale q . k_j - LSE)
+ * is added to weights[page][hk][slot] (fp32 [pages, Hk, FM_PAGE], laid out like the
+ * scales), LSE [B, H, N] being what flashmask_fwd_cache gave for the same q, cache,
+ * lens, q_lens, mask and scale. Keys from position start[b] on are new: they have had
+ * nothing, so what their slots hold is replaced. start NULL: the query tokens' own
+ * keys, from lens[b] - q_lens[b] on. start 0 for a prompt whose last rows alone weigh
+ * all of its keys. A key that no row sees gets 0; slots from lens[b] on are left as they were.
+ *   q, cache, page_table, lens, q_lens, mask, scale and their limits as for
+ *   flashmask_fwd_cache; V takes no part. The pages of one call must be distinct. A row
+ *   whose LSE is -inf gives nothing; one whose LSE, query or visible K scale is NaN (or a
+ *   K scale that is negative or infinite) gives NaN to the keys that it sees. What K holds
+ *   for keys that no row sees has no influence.
+ *   ws: flashmask_cache_weights_workspace_bytes(...) bytes, 256-byte aligned and zeroed
+ *   before its first use; not to be shared by calls that may run at the same time; one
+ *   workspace serves all sizes that it is large enough for. Zero it again after another
+ *   entry point has used it. Its first 16 bytes are the status word.
+ * Scores, exponentials and sums are fp32 and a key's sum has a fixed order: the same call
+ * gives the same bits. Asynchronous on `stream`. */
+size_t flashmask_cache_weights_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages);
+fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_cache* cache,
+                                  const int32_t* page_table, int max_pages, const int32_t* lens,
+                                  const int32_t* q_lens, const fm_mask* mask, int B, int H, int N, float scale,
+                                  const float* lse, float* weights, const int32_t* start, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* Self-test of the failure path (no counterpart in the pages). Launches `ctas`
  * (1..1024) one-warp CTAs whose mbarrier wait can never complete, bounded the
  * way every wait of the library is: CTA 0 gives up after `limit_ns` (1e6..2e9)

@@ -134,4 +134,19 @@ cudaError_t launch_cache_fwd_rows(int d, const CacheFwdParams& p, const Geometry
                                   cudaStream_t s);
 cudaError_t launch_cache_fwd(int d, const CacheFwdParams& p, int num_sms, cudaStream_t s);
 
+
+// Sums of attention weight of the cached keys. `f` holds what the call shares with the
+// attention (v8, o and the partial results are not used).
+struct WeightsParams {
+  CacheFwdParams f;
+  const float* lse;      // [B, H, N]
+  float* weights;        // [pages, Hk, 64]
+  const int32_t* start;  // [B] or null: the query tokens are the new ones
+};
+struct WeightsWs {
+  size_t list, listed, total;
+};
+WeightsWs weights_ws_layout(int B, int H, int Hk, int N, int d, int max_pages);
+cudaError_t launch_cache_weights(int d, const WeightsParams& p, int num_sms, cudaStream_t s);
+
 }  // namespace fm

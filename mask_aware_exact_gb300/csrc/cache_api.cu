@@ -76,6 +76,22 @@ fm::CacheDev cache_dev(const fm_cache* c) {
   return r;
 }
 
+// null: causal, no intervals
+fm::MaskDev mask_dev(const fm_mask* m) {
+  fm::MaskDev r = {};
+  r.Hm = 1;
+  r.causal = 1;
+  if (m) {
+    r.lts = m->lts;
+    r.lte = m->lte;
+    r.uts = m->uts;
+    r.ute = m->ute;
+    r.Hm = m->Hm;
+    r.causal = m->causal ? 1 : 0;
+  }
+  return r;
+}
+
 fm_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < need)
     return FM_ERR_WORKSPACE;
@@ -266,6 +282,58 @@ fm_status flashmask_cache_append(const fm_cache* cache, const int32_t* page_tabl
              : FM_ERR_CUDA;
 }
 
+size_t flashmask_cache_weights_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages) {
+  if (!cache_shape_ok(B, H, Hk, N, d, max_pages)) return 0;
+  return fm::weights_ws_layout(B, H, Hk, N, d, max_pages).total;
+}
+
+fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_cache* cache,
+                                  const int32_t* page_table, int max_pages, const int32_t* lens,
+                                  const int32_t* q_lens, const fm_mask* mask, int B, int H, int N, float scale,
+                                  const float* lse, float* weights, const int32_t* start, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  const fm_status cs = cache_ok(cache);
+  if (cs != FM_OK) return cs;
+  if (!q || !qs || !page_table || !lens || !lse || !weights) return FM_ERR_INVALID_ARG;
+  if (!aligned16(q) || !strides_ok(qs)) return FM_ERR_INVALID_ARG;
+  if (!aligned4(page_table) || !aligned4(lens) || !aligned4(q_lens) || !aligned4(lse) || !aligned4(weights) ||
+      !aligned4(start))
+    return FM_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2) || !(scale > 0.f)) return FM_ERR_INVALID_ARG;
+  if (mask && !vectors_ok(mask)) return FM_ERR_INVALID_ARG;
+  if (!cache_shape_ok(B, H, cache->Hk, N, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
+  if (mask && (mask->Hm <= 0 || H % mask->Hm != 0)) return FM_ERR_UNSUPPORTED;
+  const fm::WeightsWs L = fm::weights_ws_layout(B, H, cache->Hk, N, cache->d, max_pages);
+  const fm_status st = check_ws(ws, ws_bytes, L.total);
+  if (st != FM_OK) return st;
+  fm::WeightsParams p = {};
+  p.f.q = static_cast<const uint16_t*>(q);
+  for (int i = 0; i < 3; ++i) p.f.qs[i] = qs[i];
+  p.f.c = cache_dev(cache);
+  p.f.table = page_table;
+  p.f.max_pages = max_pages;
+  p.f.lens = lens;
+  p.f.q_lens = q_lens;
+  p.f.mask = mask_dev(mask);
+  p.f.B = B;
+  p.f.H = H;
+  p.f.N = N;
+  p.f.scale_log2 = scale_log2;
+  p.lse = lse;
+  p.weights = weights;
+  p.start = start;
+  char* w = static_cast<char*>(ws);
+  p.f.status = reinterpret_cast<int32_t*>(w);
+  p.f.list = reinterpret_cast<uint16_t*>(w + L.list);
+  p.f.listed = reinterpret_cast<int32_t*>(w + L.listed);
+  const int sms = sm_count();
+  if (sms <= 0) return FM_ERR_CUDA;
+  return fm::launch_cache_weights(cache->d, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FM_OK
+             : FM_ERR_CUDA;
+}
+
 fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache* cache,
                               const int32_t* page_table, int max_pages, const int32_t* lens,
                               const int32_t* q_lens, const fm_mask* mask, int B, int H, int N,
@@ -293,17 +361,7 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
   p.max_pages = max_pages;
   p.lens = lens;
   p.q_lens = q_lens;
-  p.mask = {};
-  p.mask.Hm = 1;
-  p.mask.causal = 1;
-  if (mask) {
-    p.mask.lts = mask->lts;
-    p.mask.lte = mask->lte;
-    p.mask.uts = mask->uts;
-    p.mask.ute = mask->ute;
-    p.mask.Hm = mask->Hm;
-    p.mask.causal = mask->causal ? 1 : 0;
-  }
+  p.mask = mask_dev(mask);
   p.B = B;
   p.H = H;
   p.N = N;

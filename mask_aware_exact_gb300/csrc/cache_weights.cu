@@ -1,0 +1,376 @@
+// The attention weight that each cached key is given: for key j of a cache head the sum
+// of exp(scale q k_j - LSE) over the query heads that read it and the query rows that see
+// it, added to what the key had. Keys are independent of one another, so nothing is
+// joined: a warp has a page, takes the products S^T = K Q^T of its 64 keys with 8 rows at
+// a time (m16n8k16 with fp16 operands: codes are exact in fp16, queries scaled by a power
+// of two as in the attention) and adds each key's exponentials over the rows.
+//
+// The pages of all (sequence, cache head) segments form one line, cut into equal runs,
+// one for each warp. With a column-wise mask the line has only the pages that some row
+// sees (the attention's classification, all rows as one tile).
+#include "cache_common.cuh"
+#include "flashmask.h"
+
+namespace fm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Pages on the line of segment seg: those that some row sees, or all of them (where there
+// is no row, keys may still be new).
+template <bool kVec>
+static __device__ __noinline__ int line_pages(const CacheFwdParams& p, const Geometry& geo, int seg) {
+  if constexpr (kVec) return pages_of<true>(p, geo, seg);
+  return (row_tile(p, geo, geo.by_Hk.div(seg), 0, blockIdx.x == 0).len + kPage - 1) / kPage;
+}
+
+// Bit i: key at[8 i] has s <= pos < e.
+static __device__ __noinline__ uint32_t hidden_step8(const int32_t* s, const int32_t* e, int pos) {
+  uint32_t hid = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hid |= static_cast<uint32_t>(s[8 * i] <= pos && pos < e[8 * i]) << i;
+  return hid;
+}
+
+// A lane's part of a tile of 8 NT rows: the queries as second operands (row 8 t + lane /
+// 4, elements 64 half + 16 (lane % 4) .. + 15), and of the rows 8 t + 2 (lane % 4) + e what
+// turns S into weights.
+template <int D, int NT>
+struct Rows {
+  uint32_t q[NT][D / 16][2];
+  float crow[NT][2], lse2[NT][2];
+  int lim[NT][2], pos[NT][2];
+  size_t mrow[NT][2];
+  int all_lim;  // keys that every row sees as far as causality and length go (0 if one may need score_boost)
+};
+
+template <int D, int NT, bool kVec>
+__device__ __forceinline__ void load_rows(const WeightsParams& wp, const Geometry& geo, const RowTile& r, int b,
+                                          int hk, int tile, Rows<D, NT>& o) {
+  const CacheFwdParams& p = wp.f;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int rows = geo.G * r.live;
+  o.all_lim = r.len;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int rr = tile * 8 * NT + 8 * t + g;
+    const bool live = rr < rows;
+    const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
+    const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
+    uint4 x[D / 64][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        x[hf][u] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t mk = 0x7fff7fffu;
+        const uint32_t a = __vmaxu2(__vmaxu2(x[hf][u].x & mk, x[hf][u].y & mk), __vmaxu2(x[hf][u].z & mk, x[hf][u].w & mk));
+        top = max(top, max(a & 0xffffu, a >> 16));
+      }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the row's largest element goes to [2^14, 2^15): fp16 then holds every element down
+    // to 2^-30 of it
+    // rows that saw nothing, and those behind the last, give nothing; one whose LSE is NaN
+    // counts as one whose query is (a NaN in S is dropped where the key is masked)
+    float l = -INFINITY;
+    if (live) l = wp.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok];
+    const bool bad = top >= 0x7f80u || isnan(l);
+    l = isnan(l) ? 0.f : l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+    const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+    const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
+#pragma unroll
+    for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 w = x[hf][k >> 1];
+        const uint32_t lo = k & 1 ? w.z : w.x, hi = k & 1 ? w.w : w.y;
+        o.q[t][4 * hf + k][0] = pack_f16x2(__uint_as_float(lo << 16) * f, __uint_as_float(lo & 0xffff0000u) * f);
+        o.q[t][4 * hf + k][1] = pack_f16x2(__uint_as_float(hi << 16) * f, __uint_as_float(hi & 0xffff0000u) * f);
+      }
+    const float crow = p.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr2 = tile * 8 * NT + 8 * t + 2 * c + e;
+      const bool live2 = rr2 < rows;
+      const int tok2 = geo.by_G.div(rr2), h2 = hk * geo.G + rr2 - tok2 * geo.G;
+      o.crow[t][e] = __shfl_sync(0xffffffffu, crow, 4 * (2 * c + e));
+      o.pos[t][e] = r.shift + tok2;
+      o.lim[t][e] = live2 ? (p.mask.causal ? min(r.len, o.pos[t][e] + 1) : r.len) : 0;
+      o.lse2[t][e] = __shfl_sync(0xffffffffu, l, 4 * (2 * c + e));
+      o.mrow[t][e] = kVec ? (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h2)) *
+                                static_cast<size_t>(p.max_pages * kPage)
+                          : 0;
+      // (a row behind the last hides nothing: it adds 0 wherever the others see a key)
+      if (live2) o.all_lim = min(o.all_lim, o.crow[t][e] > 1.f ? 0 : o.lim[t][e]);
+    }
+  }
+  o.all_lim = __reduce_min_sync(0xffffffffu, o.all_lim);
+}
+
+template <int D, int NT, bool kVec>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+    cache_weights_kernel(const __grid_constant__ WeightsParams wp, const __grid_constant__ Geometry geo) {
+  const CacheFwdParams& p = wp.f;
+  __shared__ int wsum[kWarps], begin[kWarps][2];
+  __shared__ uint32_t bits[FM_MAX_SEQLEN / kPage / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int nseg = p.B * p.c.Hk;
+  auto units = [&](int s) { return line_pages<kVec>(p, geo, s); };
+
+  // this warp's run of the line
+  const int each = (nseg + kThreads - 1) / kThreads;
+  const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
+  int mine = 0;
+  for (int s = seg_lo; s < seg_hi; ++s) mine += units(s);
+  int total;
+  const int before = block_before<kWarps>(mine, wsum, total);
+  const int runs = static_cast<int>(gridDim.x) * kWarps, run = (total + runs - 1) / runs;
+  for (int w = 0; w < kWarps; ++w) {
+    const long long x = static_cast<long long>(run) * (w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x));
+    if (before <= x && x < before + mine) {
+      int s = seg_lo, at = before, n;
+      while (x >= at + (n = units(s)) && s + 1 < seg_hi) at += n, ++s;
+      begin[w][0] = s;
+      begin[w][1] = static_cast<int>(x) - at;
+    }
+  }
+  __syncthreads();
+  const long long lo = static_cast<long long>(run) * (warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x));
+  int left = static_cast<int>(max(0LL, min(static_cast<long long>(run), total - lo)));
+  int seg = left > 0 ? begin[warp][0] : 0, k = left > 0 ? begin[warp][1] : 0;
+
+  Rows<D, NT> rw;
+  RowTile r = {};
+  int cur = -1, cur_tile = -1;
+  while (left > 0) {
+    int my_seg, my_k, my_n;
+    const int avail = next_units(seg, k, nseg, min(32, left), units, my_seg, my_k, my_n);
+    int page = -1, logical = 0, cut = 0;
+    float ks = 0.f;
+    if (lane < avail) {
+      const int b = geo.by_Hk.div(my_seg), hk = my_seg - b * p.c.Hk;
+      logical = page_on_line<kVec>(p, geo, b, hk, 0, my_k, cut);
+      page = p.table[static_cast<size_t>(b) * p.max_pages + logical];
+      if (page < 0 || page >= p.c.pages) {
+        record_failure(p.status, kStatusPage, kSiteCachePage);
+        page = -1;
+      } else {
+        ks = p.c.kscale[static_cast<size_t>(page) * p.c.Hk + hk];
+      }
+    }
+    for (int i = 0; i < avail; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, page, i), sg = __shfl_sync(0xffffffffu, my_seg, i);
+      const int j0 = __shfl_sync(0xffffffffu, logical, i) * kPage, ct = __shfl_sync(0xffffffffu, cut, i);
+      const float kscale = __shfl_sync(0xffffffffu, ks, i);
+      if (pg < 0) continue;
+      const int b = geo.by_Hk.div(sg), hk = sg - b * p.c.Hk;
+      const size_t ph = static_cast<size_t>(pg) * p.c.Hk + hk;
+      // instruction u has the keys 16 u + g and 16 u + 8 + g of this lane
+      const uint8_t* src = p.c.k8 + ph * (kPage * D) + g * D + 16 * c;
+      uint4 w[4][2][D / 64];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            w[u][x][hf] = __ldcs(reinterpret_cast<const uint4*>(src + (16 * u + 8 * x) * D + 64 * hf));
+      float* const wt = wp.weights + ph * kPage + 16 * c + g;
+      const float old[2] = {wt[0], wt[8]};
+      if (sg != cur) r = row_tile(p, geo, b, 0, lane == 0);
+      const int rows = geo.G * r.live, tiles = (rows + 8 * NT - 1) / (8 * NT);
+      const bool none = no_scales(kscale, 0.f);
+      float sum[4][2] = {};
+      for (int tile = 0; tile < tiles; ++tile) {
+        if (p.mask.causal && r.shift + geo.by_G.div(min(rows, (tile + 1) * 8 * NT) - 1) < j0) continue;
+        if (sg != cur || tile != cur_tile) load_rows<D, NT, kVec>(wp, geo, r, b, hk, tile, rw);
+        cur = sg, cur_tile = tile;
+        float s[4][NT][4] = {};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t a[4];
+              codes_to_f16(word(w[u][0][hf], q), a[0], a[2]);
+              codes_to_f16(word(w[u][1][hf], q), a[1], a[3]);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816(s[u][t], a, rw.q[t][4 * hf + q][0], rw.q[t][4 * hf + q][1]);
+            }
+        // s[u][t][2 x + e]: key 16 u + 8 x + g, row 8 t + 2 c + e
+        float ck[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ck[t][e] = score_factor(rw.crow[t][e], kscale);
+        if (__builtin_expect(j0 + kPage > rw.all_lim || ct || none, 0)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int n = min(max(rw.lim[t][e] - (j0 + g), 0), kPage);
+              uint32_t see = (1u << ((n + 7) >> 3)) - 1u;  // bit i: key 8 i + g
+              if constexpr (kVec) {
+                if (ct) {
+                  const size_t at = rw.mrow[t][e] + j0 + g;
+                  if (p.mask.lts) see &= ~hidden_step8(p.mask.lts + at, p.mask.lte + at, rw.pos[t][e]);
+                  if (p.mask.uts) see &= ~hidden_step8(p.mask.uts + at, p.mask.ute + at, rw.pos[t][e]);
+                }
+              }
+              const float boost = score_boost(rw.crow[t][e], kscale, none, ck[t][e]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  s[u][t][2 * x + e] = (see >> (2 * u + x)) & 1u ? s[u][t][2 * x + e] * boost : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float a = ex2(fmaf(s[u][t][2 * x], ck[t][0], -rw.lse2[t][0]));
+              const float z = ex2(fmaf(s[u][t][2 * x + 1], ck[t][1], -rw.lse2[t][1]));
+              sum[u][x] += a + z;
+            }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          sum[u][x] += __shfl_xor_sync(0xffffffffu, sum[u][x], 1);
+          sum[u][x] += __shfl_xor_sync(0xffffffffu, sum[u][x], 2);
+        }
+      const int start = wp.start ? min(max(wp.start[b], 0), r.len) : r.shift;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = j0 + 16 * c + g + 8 * x;
+        const float v = c == 0 ? sum[0][x] : c == 1 ? sum[1][x] : c == 2 ? sum[2][x] : sum[3][x];
+        if (j < r.len) wt[8 * x] = j < start ? old[x] + v : v;
+      }
+    }
+    left -= avail;
+    if (avail > 0) {
+      seg = __shfl_sync(0xffffffffu, my_seg, avail - 1);
+      k = __shfl_sync(0xffffffffu, my_k, avail - 1) + 1;
+    } else {
+      seg += 32;
+      k = 0;
+      if (seg >= nseg) break;  // the lengths are not those of the run's search any more
+    }
+  }
+
+  if constexpr (kVec) {
+    // pages that no row sees and whose keys are new: they have had nothing
+    for (int sg = blockIdx.x; sg < nseg; sg += gridDim.x) {
+      const int b = geo.by_Hk.div(sg), hk = sg - b * p.c.Hk;
+      const RowTile rt = row_tile(p, geo, b, 0, tid == 0);
+      const int start = wp.start ? min(max(wp.start[b], 0), rt.len) : max(rt.shift, 0);
+      const int first = start / kPage, pages = (rt.len + kPage - 1) / kPage - first;
+      if (start >= rt.len) continue;
+      for (int i = tid; i < (pages + 31) / 32; i += kThreads) bits[i] = 0;
+      __syncthreads();
+      // the list is in order, so the new pages are among its last
+      const int cls = mask_class(p, geo, hk);
+      const size_t at = static_cast<size_t>(b) * geo.classes + cls;
+      const int n = p.listed[at];
+      for (int i = tid; i < min(pages, n); i += kThreads) {
+        const int q = (p.list[at * p.max_pages + n - 1 - i] & 0x7fff) - first;
+        if (q >= 0) atomicOr(&bits[q >> 5], 1u << (q & 31));
+      }
+      __syncthreads();
+      for (int i = warp; i < pages; i += kWarps) {
+        if (bits[i >> 5] >> (i & 31) & 1u) continue;
+        const int page = p.table[static_cast<size_t>(b) * p.max_pages + first + i];
+        if (page < 0 || page >= p.c.pages) {
+          record_failure(p.status, kStatusPage, kSiteCachePage);
+          continue;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int j = (first + i) * kPage + lane + 32 * x;
+          if (j >= start && j < rt.len)
+            wp.weights[(static_cast<size_t>(page) * p.c.Hk + hk) * kPage + lane + 32 * x] = 0.f;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_nt(const WeightsParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  const int grid = num_sms * (NT == 1 ? 2 : 1);
+  if (p.f.mask.lts != nullptr || p.f.mask.uts != nullptr) {
+    const cudaError_t e = launch_cache_classify(p.f, geo, s);
+    if (e != cudaSuccess) return e;
+    cache_weights_kernel<D, NT, true><<<grid, kThreads, 0, s>>>(p, geo);
+  } else {
+    cache_weights_kernel<D, NT, false><<<grid, kThreads, 0, s>>>(p, geo);
+  }
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const WeightsParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  if (geo.rows <= 8) return launch_nt<D, 1>(p, geo, num_sms, s);
+  return launch_nt<D, 2>(p, geo, num_sms, s);
+}
+
+// All rows of a cache head as one tile.
+Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
+  Geometry g;
+  g.G = H / Hk;
+  g.rows = g.G * N;  // below 2^31: B * H * N is
+  g.RT = 1;
+  g.classes = Hk % Hm == 0 ? Hm : Hk;
+  g.words = (max_pages + 31) / 32;
+  g.by_G.set(g.G);
+  g.by_RT.set(1);
+  g.by_Hk.set(Hk);
+  g.by_class.set(Hk / g.classes);
+  g.by_mask.set(H / Hm);
+  return g;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+WeightsWs weights_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
+  (void)H, (void)N, (void)d;
+  const size_t segs = static_cast<size_t>(B) * Hk;
+  WeightsWs w;
+  size_t off = 256;  // the status word
+  w.list = off;
+  off = up256(off + segs * max_pages * 2);
+  w.listed = off;
+  off = up256(off + segs * 4);
+  w.total = off;
+  return w;
+}
+
+cudaError_t launch_cache_weights(int d, const WeightsParams& p, int num_sms, cudaStream_t s) {
+  const Geometry geo = geometry(p.f.H, p.f.c.Hk, p.f.mask.Hm, p.f.N, p.f.max_pages);
+  return d == 64 ? launch_d<64>(p, geo, num_sms, s) : launch_d<128>(p, geo, num_sms, s);
+}
+
+}  // namespace fm

@@ -70,7 +70,8 @@ EXPORTED = ("flashmask_workspace_bytes", "flashmask_workspace_layout", "flashmas
             "flashmask_fwd_fp8_workspace_bytes", "flashmask_fwd_fp8_layout", "flashmask_fwd_fp8",
             "flashmask_check_status", "flashmask_status_string", "flashmask_rope",
             "flashmask_cache_workspace_bytes", "flashmask_cache_append", "flashmask_fwd_cache",
-            "flashmask_norm_rope", "flashmask_norm_workspace_bytes", "flashmask_norm_rope_bwd")
+            "flashmask_norm_rope", "flashmask_norm_workspace_bytes", "flashmask_norm_rope_bwd",
+            "flashmask_cache_weights_workspace_bytes", "flashmask_cache_weights")
 
 _lib = None
 
@@ -143,6 +144,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.flashmask_norm_workspace_bytes.restype = sz
     L.flashmask_norm_rope_bwd.argtypes = [*norm, vp, sz, vp]
     L.flashmask_norm_rope_bwd.restype = i
+    L.flashmask_cache_weights_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    L.flashmask_cache_weights_workspace_bytes.restype = sz
+    L.flashmask_cache_weights.argtypes = [vp, vp, ctypes.POINTER(_FmCache), vp, i, vp, vp,
+                                          ctypes.POINTER(_FmMask), i, i, i, f, vp, vp, vp, vp, sz, vp]
+    L.flashmask_cache_weights.restype = i
     _lib = L
     return L
 
@@ -853,6 +859,22 @@ def _page_table(t, B, index):
     return shape[1]
 
 
+def _cache_mask(mask, B, max_pages, index):
+    """A DeviceMask's vectors over cached keys, checked, and its C struct."""
+    if mask is None:
+        return (), None
+    vectors = (mask.lts, mask.lte, mask.uts, mask.ute)
+    Hm, ptrs = 1, []
+    for t in vectors:
+        if t is not None:
+            Hm = t.shape[1] if t.dim() == 3 else -1
+    for t in vectors:
+        if t is not None:
+            _want(t, "mask vectors", torch.int32, index, (B, Hm, max_pages * FM_PAGE))
+        ptrs.append(None if t is None else t.data_ptr())
+    return vectors, _FmMask(*ptrs, Hm, bool(mask.causal))
+
+
 def flashmask_cache_append(cache: KVCache, page_table, k, v, start, ws, count=None, stream=None):
     """Writes K and V (bf16 [B, Hk, N, d], last dimension contiguous) behind the
     start[b] tokens that sequence b holds; count[b] <= N of its rows are real.
@@ -899,18 +921,7 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
     ln, ql = _per_sequence(lens, "lens", B, index), _per_sequence(q_lens, "q_lens", B, index)
     ws_bytes = ws.numel()
     _want(ws, "ws", torch.uint8, index, (ws_bytes,))
-    vectors, m = (), None
-    if mask is not None:
-        vectors = (mask.lts, mask.lte, mask.uts, mask.ute)
-        Hm, ptrs = 1, []
-        for t in vectors:
-            if t is not None:
-                Hm = t.shape[1] if t.dim() == 3 else -1
-        for t in vectors:
-            if t is not None:
-                _want(t, "mask vectors", torch.int32, index, (B, Hm, max_pages * FM_PAGE))
-            ptrs.append(None if t is None else t.data_ptr())
-        m = _FmMask(*ptrs, Hm, bool(mask.causal))
+    vectors, m = _cache_mask(mask, B, max_pages, index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     os = (H * N * d, N * d, d)
@@ -934,3 +945,53 @@ def flashmask_fwd_cache(q, cache: KVCache, page_table, lens, ws, mask: DeviceMas
 
     return _launch(index, stream, () if stream is None else
                    (q, *cache.tensors, page_table, lens, q_lens, ws, o, lse, *vectors), call)
+
+
+# ---------------------------------------------------------------- a cache held to a size
+def flashmask_cache_weights_workspace_bytes(B, H, Hk, N, d, max_pages) -> int:
+    return int(load().flashmask_cache_weights_workspace_bytes(B, H, Hk, N, d, max_pages))
+
+
+def alloc_cache_weights_workspace(B, H, Hk, N, d, max_pages, device="cuda") -> torch.Tensor:
+    """Zeroed workspace of flashmask_cache_weights."""
+    n = flashmask_cache_weights_workspace_bytes(B, H, Hk, N, d, max_pages)
+    if n == 0:
+        raise FlashMaskError(FM_ERR_UNSUPPORTED, "flashmask_cache_weights_workspace_bytes")
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+def flashmask_cache_weights(q, cache: KVCache, page_table, lens, lse, weights, ws,
+                            mask: DeviceMask | None = None, q_lens=None, start=None, scale=None, stream=None):
+    """Adds the attention weight that flashmask_fwd_cache's query rows give each cached
+    key, summed over rows and query heads, to `weights` (fp32 [pages, Hk, 64]) and
+    returns it. q, cache, page_table, lens, mask, q_lens and scale as in that call, lse
+    its LSE. start (int32 [B]): keys from this position on are new and had nothing; None:
+    the query tokens' own. ws comes from alloc_cache_weights_workspace."""
+    c, Hk, d, index = cache._handle
+    qs = _rows(q, "q", torch.bfloat16, index)
+    B, H, N, width = q.shape
+    if width != d:
+        raise ValueError("q must have the cache's d")
+    max_pages = _page_table(page_table, B, index)
+    ln, ql = _per_sequence(lens, "lens", B, index), _per_sequence(q_lens, "q_lens", B, index)
+    st = _per_sequence(start, "start", B, index)
+    ws_bytes = ws.numel()
+    _want(ws, "ws", torch.uint8, index, (ws_bytes,))
+    _want(lse, "lse", torch.float32, index, (B, H, N))
+    _want(weights, "weights", torch.float32, index, (c.pages, Hk, FM_PAGE))
+    vectors, m = _cache_mask(mask, B, max_pages, index)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+
+    def call(raw):
+        code = load().flashmask_cache_weights(q.data_ptr(), _STRIDES.pack(*qs[:3]), c, page_table.data_ptr(),
+                                              max_pages, ln, ql, m, B, H, N, scale, lse.data_ptr(),
+                                              weights.data_ptr(), st, ws.data_ptr(), ws_bytes, raw)
+        if code:
+            raise FlashMaskError(code, "flashmask_cache_weights")
+
+    _launch(index, stream, () if stream is None else
+            (q, *cache.tensors, page_table, lens, q_lens, start, ws, lse, weights, *vectors), call)
+    return weights
