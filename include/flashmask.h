@@ -515,6 +515,44 @@ fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_c
                                   const float* lse, float* weights, const int32_t* start, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* Cuts sequences down: each cache head of sequence b keeps n = min(lens[b], keep[b]) of its
+ * tokens (keep NULL: `budget` for all; below 0 counts as 0): the first min(sink, n), the
+ * last min(recent, n - those), and of the others those of the largest weight (fp32 [pages,
+ * Hk, FM_PAGE], see flashmask_cache_weights; any values: -0 counts as 0, NaN as less than
+ * everything else; of equal ones the lower position is kept). Heads choose for themselves.
+ * The kept tokens move together in their order: K, V, scales and weights go to the
+ * positions 0 .. n - 1 of
+ *   out_table   int32 [B, out_pages], pages that neither repeat nor occur in page_table's
+ *               used entries, so that sequences which share pages can be cut down apart
+ *               and the old pages stay as they are; or
+ *   NULL (or page_table itself): in place, in the first ceil(n / 64) pages of page_table,
+ *               which must be distinct. Pages behind them are left as they were and free.
+ * new_lens (int32 [B], may be lens) gets n. index (int32 [B, Hk, index_width], may be NULL)
+ * gets the old positions of each head's kept tokens (the first index_width of them; entries
+ * behind n are left as they were): what a caller needs to cut down its own data for these
+ * keys, such as a mask's vectors. Afterwards positions count kept tokens: causality
+ * holds as before, intervals are the caller's to shorten.
+ *   Scales: a page whose tokens all stay where they are is left as it was. Any other gets, for
+ *   K and for V, the smallest 2^k, -100 <= k <= 127, with absmax <= 448 * 2^k over its
+ *   tokens, as flashmask_cache_append would give it, and codes are rounded to nearest even
+ *   for it (exact if the old scales are powers of two, unless a code falls into e4m3's
+ *   subnormal range). Its slots behind the last token are set to zero. NaN codes of K stay NaN and do not
+ *   count for the scale, nor does a token of a page whose K or V scale is negative, infinite
+ *   or NaN: its K codes become NaN, its V codes zero.
+ *   ws: flashmask_cache_evict_workspace_bytes(...) bytes, 256-byte aligned and zeroed
+ *   before its first use; not to be shared by calls that may run at the same time; one
+ *   workspace serves all sizes that it is large enough for. Zero it again after another
+ *   entry point has used it or after FM_ERR_TIMEOUT. Its first 16 bytes are the status word.
+ *   A page or length out of range, or n > 64 * out_pages, is recorded (see
+ *   flashmask_check_status) and the access left out.
+ * Limits as for flashmask_cache_append; out_pages <= FM_MAX_SEQLEN / FM_PAGE. The same call gives
+ * the same bits. Asynchronous on `stream`. */
+size_t flashmask_cache_evict_workspace_bytes(int B, int Hk, int max_pages);
+fm_status flashmask_cache_evict(const fm_cache* cache, const int32_t* page_table, int max_pages,
+                                const int32_t* out_table, int out_pages, const int32_t* lens, float* weights,
+                                const int32_t* keep, int budget, int sink, int recent, int32_t* new_lens,
+                                int32_t* index, int index_width, int B, void* ws, size_t ws_bytes, void* stream);
+
 /* Self-test of the failure path (no counterpart in the pages). Launches `ctas`
  * (1..1024) one-warp CTAs whose mbarrier wait can never complete, bounded the
  * way every wait of the library is: CTA 0 gives up after `limit_ns` (1e6..2e9)

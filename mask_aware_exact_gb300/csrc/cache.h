@@ -149,4 +149,34 @@ struct WeightsWs {
 WeightsWs weights_ws_layout(int B, int H, int Hk, int N, int d, int max_pages);
 cudaError_t launch_cache_weights(int d, const WeightsParams& p, int num_sms, cudaStream_t s);
 
+// Eviction: each cache head of a sequence keeps some of its tokens.
+struct EvictParams {
+  CacheDev c;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* out_table;  // null: in place
+  int out_pages;
+  const int32_t* lens;
+  float* weights;       // [pages, Hk, 64]
+  const int32_t* keep;  // [B] or null: budget for all
+  int budget, sink, recent;
+  int32_t* new_lens;  // [B], may be lens
+  int32_t* index;     // [B, Hk, index_width] or null
+  int index_width;
+  int B;
+  int32_t* status;
+  // workspace (see EvictWs); a segment is a (sequence, cache head)
+  int32_t* ticket;   // next page to be written
+  int32_t* info;     // [B][2]: tokens, tokens kept
+  uint64_t* mask;    // [segments][max_pages]: kept tokens of a page
+  int32_t* before;   // [segments][max_pages + 1]: tokens kept before a page
+  int32_t* first;    // [segments][max_pages]: page of the first token of a page to be written
+  int32_t* was_read; // [segments][max_pages]: whether the tokens of a page to be written are read
+};
+struct EvictWs {
+  size_t ticket, info, mask, before, first, was_read, total;
+};
+EvictWs evict_ws_layout(int B, int Hk, int max_pages);
+cudaError_t launch_cache_evict(int d, const EvictParams& p, int num_sms, cudaStream_t s);
+
 }  // namespace fm

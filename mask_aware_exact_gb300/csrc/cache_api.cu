@@ -334,6 +334,59 @@ fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_c
              : FM_ERR_CUDA;
 }
 
+size_t flashmask_cache_evict_workspace_bytes(int B, int Hk, int max_pages) {
+  if (!cache_shape_ok(B, Hk, Hk, 1, 64, max_pages)) return 0;
+  return fm::evict_ws_layout(B, Hk, max_pages).total;
+}
+
+fm_status flashmask_cache_evict(const fm_cache* cache, const int32_t* page_table, int max_pages,
+                                const int32_t* out_table, int out_pages, const int32_t* lens, float* weights,
+                                const int32_t* keep, int budget, int sink, int recent, int32_t* new_lens,
+                                int32_t* index, int index_width, int B, void* ws, size_t ws_bytes, void* stream) {
+  const fm_status cs = cache_ok(cache);
+  if (cs != FM_OK) return cs;
+  if (!page_table || !lens || !weights || !new_lens) return FM_ERR_INVALID_ARG;
+  if (!aligned4(page_table) || !aligned4(out_table) || !aligned4(lens) || !aligned4(weights) || !aligned4(keep) ||
+      !aligned4(new_lens) || !aligned4(index))
+    return FM_ERR_INVALID_ARG;
+  if (sink < 0 || recent < 0 || (!keep && budget < 0) || (index && index_width < 0)) return FM_ERR_INVALID_ARG;
+  if (!cache_shape_ok(B, cache->Hk, cache->Hk, 1, cache->d, max_pages)) return FM_ERR_UNSUPPORTED;
+  if (out_table && (out_pages <= 0 || out_pages > FM_MAX_SEQLEN / FM_PAGE)) return FM_ERR_UNSUPPORTED;
+  if (out_table == page_table && out_pages != max_pages) return FM_ERR_INVALID_ARG;
+  const fm::EvictWs L = fm::evict_ws_layout(B, cache->Hk, max_pages);
+  const fm_status st = check_ws(ws, ws_bytes, L.total);
+  if (st != FM_OK) return st;
+  fm::EvictParams p = {};
+  p.c = cache_dev(cache);
+  p.table = page_table;
+  p.max_pages = max_pages;
+  p.out_table = out_table == page_table ? nullptr : out_table;
+  p.out_pages = out_pages;
+  p.lens = lens;
+  p.weights = weights;
+  p.keep = keep;
+  p.budget = budget;
+  p.sink = sink;
+  p.recent = recent;
+  p.new_lens = new_lens;
+  p.index = index;
+  p.index_width = index_width;
+  p.B = B;
+  char* w = static_cast<char*>(ws);
+  p.status = reinterpret_cast<int32_t*>(w);
+  p.ticket = reinterpret_cast<int32_t*>(w + L.ticket);
+  p.info = reinterpret_cast<int32_t*>(w + L.info);
+  p.mask = reinterpret_cast<uint64_t*>(w + L.mask);
+  p.before = reinterpret_cast<int32_t*>(w + L.before);
+  p.first = reinterpret_cast<int32_t*>(w + L.first);
+  p.was_read = reinterpret_cast<int32_t*>(w + L.was_read);
+  const int sms = sm_count();
+  if (sms <= 0) return FM_ERR_CUDA;
+  return fm::launch_cache_evict(cache->d, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FM_OK
+             : FM_ERR_CUDA;
+}
+
 fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache* cache,
                               const int32_t* page_table, int max_pages, const int32_t* lens,
                               const int32_t* q_lens, const fm_mask* mask, int B, int H, int N,

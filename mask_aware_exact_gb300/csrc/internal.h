@@ -20,6 +20,7 @@ enum Site : int {
   kSiteBwdDV, kSiteBwdDQ, kSiteBwdDrained, kSiteBwdDone, kSiteBwdSmemAlign, kSiteBwdSplit,
   kSiteSelftest = 301,
   kSiteAppendRange = 401, kSiteAppendPage, kSiteCacheLen, kSiteCachePage, kSiteCacheWait,
+  kSiteEvictLen, kSiteEvictPage, kSiteEvictRange, kSiteEvictWait,
 };
 
 // Backward load balance: among the split_blocks(Tc) longest key blocks of

@@ -71,7 +71,8 @@ EXPORTED = ("flashmask_workspace_bytes", "flashmask_workspace_layout", "flashmas
             "flashmask_check_status", "flashmask_status_string", "flashmask_rope",
             "flashmask_cache_workspace_bytes", "flashmask_cache_append", "flashmask_fwd_cache",
             "flashmask_norm_rope", "flashmask_norm_workspace_bytes", "flashmask_norm_rope_bwd",
-            "flashmask_cache_weights_workspace_bytes", "flashmask_cache_weights")
+            "flashmask_cache_weights_workspace_bytes", "flashmask_cache_weights",
+            "flashmask_cache_evict_workspace_bytes", "flashmask_cache_evict")
 
 _lib = None
 
@@ -149,6 +150,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.flashmask_cache_weights.argtypes = [vp, vp, ctypes.POINTER(_FmCache), vp, i, vp, vp,
                                           ctypes.POINTER(_FmMask), i, i, i, f, vp, vp, vp, vp, sz, vp]
     L.flashmask_cache_weights.restype = i
+    L.flashmask_cache_evict_workspace_bytes.argtypes = [i, i, i]
+    L.flashmask_cache_evict_workspace_bytes.restype = sz
+    L.flashmask_cache_evict.argtypes = [ctypes.POINTER(_FmCache), vp, i, vp, i, vp, vp, vp, i, i, i, vp, vp, i, i,
+                                        vp, sz, vp]
+    L.flashmask_cache_evict.restype = i
     _lib = L
     return L
 
@@ -995,3 +1001,68 @@ def flashmask_cache_weights(q, cache: KVCache, page_table, lens, lse, weights, w
     _launch(index, stream, () if stream is None else
             (q, *cache.tensors, page_table, lens, q_lens, start, ws, lse, weights, *vectors), call)
     return weights
+
+
+def flashmask_cache_evict_workspace_bytes(B, Hk, max_pages) -> int:
+    return int(load().flashmask_cache_evict_workspace_bytes(B, Hk, max_pages))
+
+
+def alloc_cache_evict_workspace(B, Hk, max_pages, device="cuda") -> torch.Tensor:
+    """Zeroed workspace of flashmask_cache_evict."""
+    n = flashmask_cache_evict_workspace_bytes(B, Hk, max_pages)
+    if n == 0:
+        raise FlashMaskError(FM_ERR_UNSUPPORTED, "flashmask_cache_evict_workspace_bytes")
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+def flashmask_cache_evict(cache: KVCache, page_table, lens, weights, keep, ws, sink=0, recent=0, out_table=None,
+                          new_lens=None, index=None, stream=None):
+    """Cuts sequences down to keep[b] tokens (an int for all, or int32 [B]) of each cache
+    head: its first `sink`, its last `recent` and those of the largest weights between
+    (fp32 [pages, Hk, 64], moved along). They go together, in place or into the pages of
+    out_table (int32 [B, pages]). Returns the new lengths (int32 [B], written to
+    new_lens, which may be lens). index (int32 [B, Hk, width]) gets the old positions of
+    the kept tokens. See include/flashmask.h for scales and rounding. ws comes from
+    alloc_cache_evict_workspace."""
+    c, Hk, d, index_dev = cache._handle
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    B = page_table.shape[0]
+    max_pages = _page_table(page_table, B, index_dev)
+    ln = _per_sequence(lens, "lens", B, index_dev)
+    _want(weights, "weights", torch.float32, index_dev, (c.pages, Hk, FM_PAGE))
+    keep_ptr, budget = None, 0
+    if isinstance(keep, torch.Tensor):
+        keep_ptr = _per_sequence(keep, "keep", B, index_dev)
+    else:
+        budget = int(keep)
+    out_ptr, out_pages = None, 0
+    if out_table is not None:
+        out_pages = _page_table(out_table, B, index_dev)
+        out_ptr = out_table.data_ptr()
+    width, index_ptr = 0, None
+    if index is not None:
+        if index.dim() != 3:
+            raise ValueError("index must be int32 [B, Hk, width]")
+        width = index.shape[2]
+        _want(index, "index", torch.int32, index_dev, (B, Hk, width))
+        index_ptr = index.data_ptr()
+    if new_lens is not None:
+        _want(new_lens, "new_lens", torch.int32, index_dev, (B,))
+    ws_bytes = ws.numel()
+    _want(ws, "ws", torch.uint8, index_dev, (ws_bytes,))
+
+    def call(raw):
+        out = torch.empty((B,), dtype=torch.int32, device=lens.device) if new_lens is None else new_lens
+        code = load().flashmask_cache_evict(c, page_table.data_ptr(), max_pages, out_ptr, out_pages, ln,
+                                            weights.data_ptr(), keep_ptr, budget, int(sink), int(recent),
+                                            out.data_ptr(), index_ptr, width, B, ws.data_ptr(), ws_bytes, raw)
+        if code:
+            raise FlashMaskError(code, "flashmask_cache_evict")
+        return out
+
+    return _launch(index_dev, stream, () if stream is None else
+                   (*cache.tensors, page_table, lens, weights, keep if keep_ptr is not None else None, out_table,
+                    new_lens, index, ws), call)
