@@ -142,10 +142,20 @@ struct WeightsParams {
   const float* lse;      // [B, H, N]
   float* weights;        // [pages, Hk, 64]
   const int32_t* start;  // [B] or null: the query tokens are the new ones
+  // workspace (see WeightsWs); the last three only where there are many rows
+  uint8_t* tiles;    // [B * Hk][row tiles]: operands of 128 query rows and their factors
+  float* partial;    // [CTAs][2][256]: sums of the pieces of cut keys
+  int32_t* arrived;  // [CTAs]: pieces that have arrived (0 between calls)
 };
 struct WeightsWs {
-  size_t list, listed, total;
+  size_t arrived, partial, list, listed, tiles, total;
 };
+// Rows of a cache head from which on the products are taken on tcgen05.
+constexpr int kWeightsMany = 33;
+inline int weights_row_tiles(int H, int Hk, int N) { return (H / Hk * N + 127) / 128; }
+inline size_t weights_tile_bytes(int d) { return static_cast<size_t>(d) * 256 + 1024; }
+cudaError_t launch_cache_weights_rows(int d, const WeightsParams& p, const Geometry& geo, int num_sms,
+                                      cudaStream_t s);
 WeightsWs weights_ws_layout(int B, int H, int Hk, int N, int d, int max_pages);
 cudaError_t launch_cache_weights(int d, const WeightsParams& p, int num_sms, cudaStream_t s);
 

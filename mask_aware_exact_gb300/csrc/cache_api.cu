@@ -327,6 +327,9 @@ fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_c
   p.f.status = reinterpret_cast<int32_t*>(w);
   p.f.list = reinterpret_cast<uint16_t*>(w + L.list);
   p.f.listed = reinterpret_cast<int32_t*>(w + L.listed);
+  p.tiles = reinterpret_cast<uint8_t*>(w + L.tiles);
+  p.partial = reinterpret_cast<float*>(w + L.partial);
+  p.arrived = reinterpret_cast<int32_t*>(w + L.arrived);
   const int sms = sm_count();
   if (sms <= 0) return FM_ERR_CUDA;
   return fm::launch_cache_weights(cache->d, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess

@@ -8,7 +8,7 @@
 // The pages of all (sequence, cache head) segments form one line, cut into equal runs,
 // one for each warp. With a column-wise mask the line has only the pages that some row
 // sees (the attention's classification, all rows as one tile).
-#include "cache_common.cuh"
+#include "cache_weights.cuh"
 #include "flashmask.h"
 
 namespace fm {
@@ -23,14 +23,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Pages on the line of segment seg: those that some row sees, or all of them (where there
-// is no row, keys may still be new).
-template <bool kVec>
-static __device__ __noinline__ int line_pages(const CacheFwdParams& p, const Geometry& geo, int seg) {
-  if constexpr (kVec) return pages_of<true>(p, geo, seg);
-  return (row_tile(p, geo, geo.by_Hk.div(seg), 0, blockIdx.x == 0).len + kPage - 1) / kPage;
 }
 
 // Bit i: key at[8 i] has s <= pos < e.
@@ -127,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     cache_weights_kernel(const __grid_constant__ WeightsParams wp, const __grid_constant__ Geometry geo) {
   const CacheFwdParams& p = wp.f;
   __shared__ int wsum[kWarps], begin[kWarps][2];
-  __shared__ uint32_t bits[FM_MAX_SEQLEN / kPage / 32];
+  __shared__ uint32_t bits[kVec ? kUnseenWords : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int nseg = p.B * p.c.Hk;
   auto units = [&](int s) { return line_pages<kVec>(p, geo, s); };
@@ -278,42 +270,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     }
   }
 
-  if constexpr (kVec) {
-    // pages that no row sees and whose keys are new: they have had nothing
-    for (int sg = blockIdx.x; sg < nseg; sg += gridDim.x) {
-      const int b = geo.by_Hk.div(sg), hk = sg - b * p.c.Hk;
-      const RowTile rt = row_tile(p, geo, b, 0, tid == 0);
-      const int start = wp.start ? min(max(wp.start[b], 0), rt.len) : max(rt.shift, 0);
-      const int first = start / kPage, pages = (rt.len + kPage - 1) / kPage - first;
-      if (start >= rt.len) continue;
-      for (int i = tid; i < (pages + 31) / 32; i += kThreads) bits[i] = 0;
-      __syncthreads();
-      // the list is in order, so the new pages are among its last
-      const int cls = mask_class(p, geo, hk);
-      const size_t at = static_cast<size_t>(b) * geo.classes + cls;
-      const int n = p.listed[at];
-      for (int i = tid; i < min(pages, n); i += kThreads) {
-        const int q = (p.list[at * p.max_pages + n - 1 - i] & 0x7fff) - first;
-        if (q >= 0) atomicOr(&bits[q >> 5], 1u << (q & 31));
-      }
-      __syncthreads();
-      for (int i = warp; i < pages; i += kWarps) {
-        if (bits[i >> 5] >> (i & 31) & 1u) continue;
-        const int page = p.table[static_cast<size_t>(b) * p.max_pages + first + i];
-        if (page < 0 || page >= p.c.pages) {
-          record_failure(p.status, kStatusPage, kSiteCachePage);
-          continue;
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int j = (first + i) * kPage + lane + 32 * x;
-          if (j >= start && j < rt.len)
-            wp.weights[(static_cast<size_t>(page) * p.c.Hk + hk) * kPage + lane + 32 * x] = 0.f;
-        }
-      }
-      __syncthreads();
-    }
-  }
+  clear_unseen<kThreads, kVec>(wp, geo, bits);
 }
 
 template <int D, int NT>
@@ -335,41 +292,34 @@ cudaError_t launch_d(const WeightsParams& p, const Geometry& geo, int num_sms, c
   return launch_nt<D, 2>(p, geo, num_sms, s);
 }
 
-// All rows of a cache head as one tile.
-Geometry geometry(int H, int Hk, int Hm, int N, int max_pages) {
-  Geometry g;
-  g.G = H / Hk;
-  g.rows = g.G * N;  // below 2^31: B * H * N is
-  g.RT = 1;
-  g.classes = Hk % Hm == 0 ? Hm : Hk;
-  g.words = (max_pages + 31) / 32;
-  g.by_G.set(g.G);
-  g.by_RT.set(1);
-  g.by_Hk.set(Hk);
-  g.by_class.set(Hk / g.classes);
-  g.by_mask.set(H / Hm);
-  return g;
-}
-
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
 WeightsWs weights_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
-  (void)H, (void)N, (void)d;
   const size_t segs = static_cast<size_t>(B) * Hk;
+  const bool many = H / Hk * N >= kWeightsMany;
   WeightsWs w;
-  size_t off = 256;  // the status word
+  // the status word and the counters, which have to be zero, lie at the same place for
+  // all sizes, so that one workspace serves them in turn
+  size_t off = 256;
+  w.arrived = off;
+  off = up256(off + kCacheMaxCtas * 4);
+  w.partial = off;
+  off = up256(off + (many ? static_cast<size_t>(kCacheMaxCtas) * 2 * 256 * 4 : 0));
   w.list = off;
   off = up256(off + segs * max_pages * 2);
   w.listed = off;
   off = up256(off + segs * 4);
+  w.tiles = off;
+  off = up256(off + (many ? segs * weights_row_tiles(H, Hk, N) * weights_tile_bytes(d) : 0));
   w.total = off;
   return w;
 }
 
 cudaError_t launch_cache_weights(int d, const WeightsParams& p, int num_sms, cudaStream_t s) {
-  const Geometry geo = geometry(p.f.H, p.f.c.Hk, p.f.mask.Hm, p.f.N, p.f.max_pages);
+  const Geometry geo = weights_geometry(p.f.H, p.f.c.Hk, p.f.mask.Hm, p.f.N, p.f.max_pages);
+  if (geo.rows >= kWeightsMany) return launch_cache_weights_rows(d, p, geo, num_sms, s);
   return d == 64 ? launch_d<64>(p, geo, num_sms, s) : launch_d<128>(p, geo, num_sms, s);
 }
 

@@ -1,0 +1,681 @@
+// The attention weight of cached keys where a cache head has many query rows (the last
+// rows of a prompt, drafted tokens of large groups): products S^T = K Q^T on tcgen05.
+//
+// Keys stay, rows stream. An item is four pages, 256 keys, as two operands of 128 rows
+// in TMEM (fp16, exact for codes), converted once; tiles of 128 query rows pass by as the
+// other operand. A first kernel writes those as fp16 tiles in the layout that the tensor
+// cores read (128-byte swizzle), each row scaled by a power of two as in the attention,
+// with the row's factor and LSE behind them, so that a tile is one bulk copy. With 256 keys
+// on a CTA a tile of d = 128 is 32 KB for 1024 cycles of products.
+//
+// In S^T a thread owns a key (a TMEM lane) of each operand: the sum over rows is a sum in
+// its registers, and a row's factor and LSE, read from shared memory, serve two keys.
+// x = (S * K scale) * factor - LSE, weight 2^x.
+//
+// Items are cut into `parts` ranges of rows where there are few of them, on one line with
+// equal runs for the CTAs; the pieces of an item that a run's border cuts leave their
+// sums in the workspace, and the last to arrive adds them in order.
+//
+// Warp roles (448 threads):
+//   0-7    weights: warpgroup w takes units (64 rows) w, w + 2, ..
+//   8-11   conversion of K, one key of each operand a thread
+//   12     walks the run, looks pages up, brings row tiles in
+//   13     issues the products
+// TMEM: K 2 x d / 2 columns, then three units of S^T, 2 x 64 columns each.
+#include <atomic>
+
+#include "cache_weights.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kThreads = 448;
+constexpr int kMetaRing = 4;
+constexpr int kMetaInts = 32;
+constexpr int kKeys = 256;
+constexpr int kTileRows = 128;
+constexpr int kUnit = 64;
+constexpr int kUnits = 3;  // of S^T in TMEM
+constexpr int kScanWords = kThreads / 32 + 4;
+
+enum MetaWord { kFlags, kSeg, kTile0, kTiles, kCta0, kPieces, kLen, kLive, kPg = 8, kJ0 = 12, kKs = 16, kCutWord = 20 };
+enum Flag { kEnd = 1, kWhole = 2, kTail = 4 };
+
+template <int D>
+struct Layout {
+  static constexpr int kStages = D == 128 ? 5 : 9;   // row tiles in shared memory
+  static constexpr int kK = D == 128 ? 1 : 2;        // K operands in TMEM
+  static constexpr int kStageBytes = D * 256 + 1024;
+  static constexpr int kMeta = kStages * kStageBytes;
+  static constexpr int kRed = kMeta + kMetaRing * kMetaInts * 4;  // float [2][2][128]
+  static constexpr int kWords = kRed + 2 * kKeys * 4;
+  static constexpr int kUnseen = kWords + (kScanWords + 8) * 4;
+  static constexpr int kBar = (kUnseen + kUnseenWords * 4 + 7) / 8 * 8;
+  static constexpr int kNumBars = 2 * kStages + 2 * kMetaRing + 2 * kK + 2 * kUnits + 4 + 1;
+  static constexpr int kTmemSlot = kBar + kNumBars * 8;
+  static constexpr int kBytes = kTmemSlot + 16;
+};
+static_assert(Layout<128>::kBytes <= 227 * 1024 && Layout<64>::kBytes <= 227 * 1024, "shared memory per CTA");
+
+template <int D>
+struct Bars {
+  using L = Layout<D>;
+  uint32_t base;
+  __device__ uint32_t at(int i) const { return base + 8 * i; }
+  __device__ uint32_t q_full(int s) const { return at(s); }                                   // bytes
+  __device__ uint32_t q_empty(int s) const { return at(L::kStages + s); }                     // 8 warps, commit
+  __device__ uint32_t meta_full(int s) const { return at(2 * L::kStages + s); }               // 1
+  __device__ uint32_t meta_empty(int s) const { return at(2 * L::kStages + kMetaRing + s); }  // 13 warps
+  __device__ uint32_t k_full(int s) const { return at(2 * L::kStages + 2 * kMetaRing + s); }  // 4 warps
+  __device__ uint32_t k_empty(int s) const { return at(2 * L::kStages + 2 * kMetaRing + L::kK + s); }  // commit
+  __device__ uint32_t s_full(int u) const { return at(2 * L::kStages + 2 * kMetaRing + 2 * L::kK + u); }  // commit
+  __device__ uint32_t s_empty(int u) const { return s_full(u) + 8 * kUnits; }                 // 4 warps
+  __device__ uint32_t red_full(int x) const { return s_full(0) + 8 * (2 * kUnits + x); }      // 4 warps
+  __device__ uint32_t red_empty(int x) const { return s_full(0) + 8 * (2 * kUnits + 2 + x); } // 4 warps
+  __device__ uint32_t sums() const { return s_full(0) + 8 * (2 * kUnits + 4); }               // 4 warps
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- row tiles
+// One CTA a tile: 128 rows r = t G + g as fp16 in two (d = 128) or one blocks of 64
+// columns, swizzled, then the rows' factors and -LSE in log2 units. Rows behind the last are
+// zero with -LSE = -inf, and so are those that saw nothing; a row whose LSE is NaN counts
+// as one whose query is.
+template <int D>
+__global__ void __launch_bounds__(256) weights_tiles_kernel(const __grid_constant__ WeightsParams wp,
+                                                            const __grid_constant__ Geometry geo, const int RT) {
+  constexpr int kUnits16 = D / 8;               // 16-byte pieces of a row
+  constexpr int kPass = 256 / kUnits16;         // rows at a time
+  const CacheFwdParams& p = wp.f;
+  const int seg = blockIdx.x / RT, tile = blockIdx.x - seg * RT;
+  const int b = geo.by_Hk.div(seg), hk = seg - b * p.c.Hk;
+  const RowTile r = row_tile(p, geo, b, 0, false);
+  const int rows = geo.G * r.live;
+  if (tile * kTileRows >= rows) return;
+  const int u = threadIdx.x % kUnits16, r0 = threadIdx.x / kUnits16;
+  uint8_t* dst = wp.tiles + static_cast<size_t>(blockIdx.x) * (D * 256 + 1024);
+  float* factors = reinterpret_cast<float*>(dst + D * 256);
+  uint4 x[kTileRows / kPass];
+  float l[kTileRows / kPass];
+#pragma unroll
+  for (int i = 0; i < kTileRows / kPass; ++i) {
+    const int rr = tile * kTileRows + r0 + i * kPass;
+    const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    l[i] = -INFINITY;
+    if (rr < rows) {
+      x[i] = *reinterpret_cast<const uint4*>(p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 8 * u);
+      l[i] = wp.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTileRows / kPass; ++i) {
+    const int row = r0 + i * kPass;
+    const uint32_t mk = 0x7fff7fffu;
+    const uint32_t a = __vmaxu2(__vmaxu2(x[i].x & mk, x[i].y & mk), __vmaxu2(x[i].z & mk, x[i].w & mk));
+    uint32_t top = max(a & 0xffffu, a >> 16);
+#pragma unroll
+    for (int o = kUnits16 / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool bad = top >= 0x7f80u || isnan(l[i]);
+    const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+    const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
+    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      y[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
+    *reinterpret_cast<uint4*>(dst + (u >> 3) * 16384 + sw128_offset(row, u & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (u == 0) {
+      factors[row] = p.scale_log2 * __int_as_float((127 - up) << 23);
+      factors[kTileRows + row] = isnan(l[i]) ? 0.f : l[i] == -INFINITY ? -INFINITY : l[i] * -1.4426950408889634f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- keys
+// Bits [lo, hi) of 64, either outside [0, 64] too.
+__device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
+  lo = min(max(lo, 0), 64);
+  hi = min(max(hi, 0), 64);
+  const uint64_t below_hi = hi == 64 ? ~0ull : (1ull << hi) - 1ull, below_lo = lo == 64 ? ~0ull : (1ull << lo) - 1ull;
+  return below_hi & ~below_lo;
+}
+
+// A thread's key: which rows see it.
+struct Key {
+  int page, j;      // page -1: none
+  int lo, hi;       // rows [lo, hi), without
+  int a0, b0, a1, b1;  // [a0, b0) and [a1, b1)
+  float ks;
+  bool special;     // seen row by row, or of a scale beyond 2^90
+};
+
+// Rows whose position lies in [s, e), of the sequence's `live` tokens.
+__device__ __forceinline__ void row_range(int s, int e, const RowTile& r, int G, int& a, int& b) {
+  const long long lo = min(max(static_cast<long long>(s) - r.shift, 0LL), static_cast<long long>(r.live));
+  const long long hi = min(max(static_cast<long long>(e) - r.shift, 0LL), static_cast<long long>(r.live));
+  a = static_cast<int>(lo) * G;
+  b = static_cast<int>(hi) * G;
+}
+
+template <bool kVec>
+__device__ __forceinline__ Key key_of(const CacheFwdParams& p, const Geometry& geo, const RowTile& r, int b, int hk,
+                                      const int* m, int x, int slot) {
+  Key k;
+  k.page = m[kPg + x];
+  k.ks = __int_as_float(m[kKs + x]);
+  k.j = m[kJ0 + x] + slot;
+  const int cut = m[kCutWord + x];
+  const bool there = k.page >= 0 && k.j < r.len;
+  k.hi = there ? geo.G * r.live : 0;
+  k.lo = p.mask.causal ? max(k.j - r.shift, 0) * geo.G : 0;
+  if (k.j - r.shift >= r.live && p.mask.causal) k.lo = k.hi;  // (no product past 32 bits)
+  k.a0 = k.b0 = k.a1 = k.b1 = 0;
+  k.special = (cut & 2) != 0;
+  if constexpr (kVec) {
+    if ((cut & 1) && there) {
+      if (geo.classes != p.mask.Hm) {
+        k.special = true;
+      } else {
+        const size_t at = (static_cast<size_t>(b) * p.mask.Hm + mask_class(p, geo, hk)) *
+                              static_cast<size_t>(p.max_pages * kPage) + k.j;
+        if (p.mask.lts) row_range(p.mask.lts[at], p.mask.lte[at], r, geo.G, k.a0, k.b0);
+        if (p.mask.uts) row_range(p.mask.uts[at], p.mask.ute[at], r, geo.G, k.a1, k.b1);
+      }
+    }
+  }
+  return k;
+}
+// Whether all rows [u0, u1) see the key (rows behind the last may).
+__device__ __forceinline__ bool sees_all(const Key& k, int u0, int u1, int rows) {
+  return !k.special && k.lo <= u0 && k.hi >= min(u1, rows) && (k.b0 <= u0 || k.a0 >= u1 || k.a0 >= k.b0) &&
+         (k.b1 <= u0 || k.a1 >= u1 || k.a1 >= k.b1);
+}
+// Bit i: row u0 + i sees the key.
+template <bool kVec>
+__device__ __noinline__ uint64_t seen_bits(const CacheFwdParams& p, const Geometry& geo, const RowTile& r, int b,
+                                           int hk, const Key& k, int u0) {
+  uint64_t see = bit_range(k.lo - u0, k.hi - u0) & ~bit_range(k.a0 - u0, k.b0 - u0) & ~bit_range(k.a1 - u0, k.b1 - u0);
+  if constexpr (kVec) {
+    if (k.special && geo.classes != p.mask.Hm && see != 0) {
+      // heads of the group have masks of their own
+      for (int i = 0; i < kUnit; ++i) {
+        if (!(see >> i & 1ull)) continue;
+        const int rr = u0 + i, tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G, pos = r.shift + tok;
+        const size_t at = (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h)) *
+                              static_cast<size_t>(p.max_pages * kPage) + k.j;
+        bool hid = false;
+        if (p.mask.lts) hid |= p.mask.lts[at] <= pos && pos < p.mask.lte[at];
+        if (p.mask.uts) hid |= p.mask.uts[at] <= pos && pos < p.mask.ute[at];
+        if (hid) see &= ~(1ull << i);
+      }
+    }
+  }
+  return see;
+}
+
+template <int D, bool kVec>
+__global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const __grid_constant__ WeightsParams wp,
+                                                                         const __grid_constant__ Geometry geo,
+                                                                         const int RT) {
+  using L = Layout<D>;
+  const CacheFwdParams& p = wp.f;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nseg = p.B * p.c.Hk;
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) record_failure(p.status, kStatusLayout, kSiteCacheWait);
+    return;
+  }
+  const Bars<D> bar{smem_u32(smem + L::kBar)};
+  int* words = reinterpret_cast<int*>(smem + L::kWords);
+  int* found = words + kScanWords;  // segment, item of it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  const int* meta = reinterpret_cast<const int*>(smem + L::kMeta);
+  float* red = reinterpret_cast<float*>(smem + L::kRed);
+
+  if (warp == 13) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (tid < L::kNumBars) {
+    const int i = tid;
+    int n = 1;
+    if (i >= L::kStages && i < 2 * L::kStages) n = 9;
+    const int m = i - 2 * L::kStages;
+    if (m >= kMetaRing && m < 2 * kMetaRing) n = 13;
+    const int k = m - 2 * kMetaRing;
+    if (k >= 0 && k < L::kK) n = 4;
+    const int s = k - 2 * L::kK;
+    if (s >= kUnits) n = 4;
+    mbar_init(bar.at(i), n);
+    fence_barrier_init();
+  }
+  // the line: items of all segments, each `parts` long; this CTA's run
+  auto items = [&](int s) { return (line_pages<kVec>(p, geo, s) + 3) >> 2; };
+  const int each = (nseg + kThreads - 1) / kThreads;
+  const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
+  int mine = 0;
+  for (int s = seg_lo; s < seg_hi; ++s) mine += items(s);
+  int total;
+  const int before = block_before<kThreads / 32>(mine, words, total);
+  const int grid = static_cast<int>(gridDim.x);
+  // enough parts that a run is eight of them or more
+  const int parts = total == 0 || total >= 8 * grid ? 1 : min(RT, (8 * grid + total - 1) / total);
+  const long long line = static_cast<long long>(total) * parts;
+  const int run = static_cast<int>((line + grid - 1) / grid);
+  const long long run_lo = min(static_cast<long long>(run) * blockIdx.x, line), run_hi = min(run_lo + run, line);
+  const int item_lo = static_cast<int>(run_lo / parts);
+  const int item_hi = static_cast<int>((run_hi + parts - 1) / parts);
+  if (run_lo < run_hi && before <= item_lo && item_lo < before + mine) {
+    int s = seg_lo, at = before, n;
+    while (item_lo >= at + (n = items(s)) && s + 1 < seg_hi) at += n, ++s;
+    found[0] = s;
+    found[1] = item_lo - at;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto col_k = [&](int kb, int s) { return tmem + static_cast<uint32_t>(kb * D + s * (D / 2)); };
+  auto col_s = [&](int u, int s) { return tmem + 128u + 128u * static_cast<uint32_t>(u) + 64u * static_cast<uint32_t>(s); };
+
+  if (warp == 12) {
+    // ------------------------------------------------------------ run, pages, row tiles
+    int left = run_lo < run_hi ? item_hi - item_lo : 0, item = item_lo;
+    int seg = left > 0 ? found[0] : 0, k = left > 0 ? found[1] : 0;
+    int piece = 0, tq = 0;
+    bool ok = true;
+    while (ok && left > 0) {
+      int my_seg, my_k, my_n;
+      const int avail = next_units(seg, k, nseg, min(32, left), items, my_seg, my_k, my_n);
+      int m[kMetaInts];
+#pragma unroll
+      for (int i = 0; i < kMetaInts; ++i) m[i] = 0;
+      if (lane < avail) {
+        const int b = geo.by_Hk.div(my_seg), hk = my_seg - b * p.c.Hk;
+        const RowTile r = row_tile(p, geo, b, 0, true);
+        const int pages = line_pages<kVec>(p, geo, my_seg), rows = geo.G * r.live;
+        int first = r.len;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          m[kPg + x] = -1;
+          if (4 * my_k + x >= pages) continue;
+          int cut;
+          const int logical = page_on_line<kVec>(p, geo, b, hk, 0, 4 * my_k + x, cut);
+          const int pg = p.table[static_cast<size_t>(b) * p.max_pages + logical];
+          if (pg < 0 || pg >= p.c.pages) {
+            record_failure(p.status, kStatusPage, kSiteCachePage);
+            continue;
+          }
+          const float ks = p.c.kscale[static_cast<size_t>(pg) * p.c.Hk + hk];
+          m[kPg + x] = pg;
+          m[kJ0 + x] = logical * kPage;
+          m[kKs + x] = no_scales(ks, 0.f) ? 0x7fffffff : __float_as_int(ks);
+          m[kCutWord + x] = cut | (ks > 0x1p90f ? 2 : 0);
+          first = min(first, logical * kPage);
+        }
+        // row tiles that may see a key, cut into parts
+        const int tile_hi = (rows + kTileRows - 1) / kTileRows;
+        int tile_lo = 0;
+        if (p.mask.causal && first > r.shift) tile_lo = first - r.shift >= r.live ? tile_hi : (first - r.shift) * geo.G / kTileRows;
+        const long long lo = static_cast<long long>(item + lane) * parts;
+        const int pa = static_cast<int>(max(run_lo, lo) - lo), pb = static_cast<int>(min(run_hi, lo + parts) - lo);
+        const int n = tile_hi - tile_lo;
+        const int t0 = static_cast<int>(static_cast<long long>(n) * pa / parts), t1 = static_cast<int>(static_cast<long long>(n) * pb / parts);
+        m[kFlags] = (pa == 0 && pb == parts ? kWhole : 0) | (pa == 0 ? kTail : 0);
+        m[kSeg] = my_seg;
+        m[kLen] = r.len;
+        m[kLive] = r.live;
+        m[kTile0] = tile_lo + t0;
+        m[kTiles] = t1 - t0;
+        m[kCta0] = static_cast<int>(lo / run);
+        m[kPieces] = static_cast<int>((lo + parts - 1) / run) - m[kCta0] + 1;
+      }
+      for (int t = 0; ok && t < avail; ++t, ++piece) {
+        const int ring = piece % kMetaRing;
+        if (piece >= kMetaRing) ok = __all_sync(0xffffffffu, cache_wait(bar.meta_empty(ring), (piece / kMetaRing - 1) & 1, p.status));
+        if (!ok) break;
+        if (lane == t) {
+          int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + ring * (kMetaInts / 4);
+#pragma unroll
+          for (int i = 0; i < 6; ++i) at[i] = make_int4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+          mbar_arrive(bar.meta_full(ring));
+        }
+        const int sg = __shfl_sync(0xffffffffu, m[kSeg], t), tile0 = __shfl_sync(0xffffffffu, m[kTile0], t);
+        const int tiles = __shfl_sync(0xffffffffu, m[kTiles], t);
+        for (int i = 0; ok && i < tiles; ++i, ++tq) {
+          const int st = tq % L::kStages;
+          if (tq >= L::kStages) ok = __all_sync(0xffffffffu, cache_wait(bar.q_empty(st), (tq / L::kStages - 1) & 1, p.status));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar.q_full(st), L::kStageBytes);
+            bulk_load(smem_u32(smem + st * L::kStageBytes),
+                      wp.tiles + (static_cast<size_t>(sg) * RT + tile0 + i) * L::kStageBytes, L::kStageBytes, bar.q_full(st));
+          }
+        }
+      }
+      left -= avail;
+      item += avail;
+      if (avail > 0) {
+        seg = __shfl_sync(0xffffffffu, my_seg, avail - 1);
+        k = __shfl_sync(0xffffffffu, my_k, avail - 1) + 1;
+      } else {
+        seg += 32;
+        k = 0;
+        if (seg >= nseg) ok = lengths_moved(p.status);
+      }
+    }
+    if (ok && piece >= kMetaRing) ok = cache_wait(bar.meta_empty(piece % kMetaRing), (piece / kMetaRing - 1) & 1, p.status);
+    if (lane == 0) {
+      if (ok) {
+        (reinterpret_cast<int*>(smem + L::kMeta) + (piece % kMetaRing) * kMetaInts)[kFlags] = kEnd;
+        mbar_arrive(bar.meta_full(piece % kMetaRing));
+      } else {
+        // copies in flight land before the CTA's shared memory is given up
+        for (int i = max(0, tq - L::kStages); i < tq; ++i)
+          mbar_wait_for(bar.q_full(i % L::kStages), (i / L::kStages) & 1, nullptr, 1000000ull);
+      }
+    }
+  } else if (warp == 13) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16(128, kUnit);
+      const uint64_t dq = sdesc_sw128(smem_u32(smem), 16, 1024);
+      int tq = 0, unit = 0, kc = 0;
+      bool ok = true;
+      for (int piece = 0; ok; ++piece) {
+        const int ring = piece % kMetaRing;
+        if (!cache_wait(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status)) break;
+        const int* m = meta + ring * kMetaInts;
+        if (m[kFlags] & kEnd) break;
+        const int tile0 = m[kTile0], tiles = m[kTiles], rows = geo.G * m[kLive];
+        mbar_arrive(bar.meta_empty(ring));
+        if (tiles == 0) continue;
+        const int kb = kc % L::kK;
+        ok = cache_wait(bar.k_full(kb), (kc / L::kK) & 1, p.status);
+        tc_fence_after();
+        for (int i = 0; ok && i < tiles; ++i, ++tq) {
+          const int st = tq % L::kStages;
+          ok = cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status);
+          const int units = rows - (tile0 + i) * kTileRows > kUnit ? 2 : 1;
+          for (int h = 0; ok && h < units; ++h, ++unit) {
+            const int u = unit % kUnits;
+            if (unit >= kUnits) ok = cache_wait(bar.s_empty(u), (unit / kUnits - 1) & 1, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qd = dq + static_cast<uint64_t>((st * L::kStageBytes + h * kUnit * 128) >> 4);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(col_s(u, s), col_k(kb, s) + 8 * kk, qd + static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                       idesc, kk > 0);
+            mma_commit(bar.s_full(u));
+          }
+          if (ok) mma_commit(bar.q_empty(st));
+        }
+        if (ok) mma_commit(bar.k_empty(kb));
+        ++kc;
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ conversion
+    const int key = (warp - 8) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp - 8) * 32) << 16;
+    int kc = 0;
+    for (int piece = 0;; ++piece) {
+      const int ring = piece % kMetaRing;
+      if (!__all_sync(0xffffffffu, cache_wait(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status))) break;
+      const int* m = meta + ring * kMetaInts;
+      if (m[kFlags] & kEnd) break;
+      const int tiles = m[kTiles], seg = m[kSeg];
+      const int page[2] = {m[kPg + (key >> 6)], m[kPg + 2 + (key >> 6)]};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.meta_empty(ring));
+      if (tiles == 0) continue;
+      const int hk = seg - geo.by_Hk.div(seg) * p.c.Hk;
+      uint4 w[2][D / 16];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint8_t* src = p.c.k8 + (static_cast<size_t>(max(page[s], 0)) * p.c.Hk + hk) * (kPage * D) + (key & 63) * D;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          w[s][i] = page[s] < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 16 * i);
+      }
+      const int kb = kc % L::kK;
+      if (kc >= L::kK && !__all_sync(0xffffffffu, cache_wait(bar.k_empty(kb), (kc / L::kK - 1) & 1, p.status))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t h[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) codes_to_f16(word(w[s][4 * c + i], u), h[8 * i + 2 * u], h[8 * i + 2 * u + 1]);
+          tmem_st32p(col_k(kb, s) + lane_base + 32 * c, h);
+        }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.k_full(kb));
+      ++kc;
+    }
+  } else {
+    // ------------------------------------------------------------ weights
+    const int w = warp >> 2, key = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int tq = 0, unit = 0, syncs = 0;
+    bool ok = true;
+    for (int piece = 0; ok; ++piece) {
+      const int ring = piece % kMetaRing;
+      ok = __all_sync(0xffffffffu, cache_wait(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status));
+      if (!ok) break;
+      const int* m = meta + ring * kMetaInts;
+      const int flags = m[kFlags];
+      if (flags & kEnd) break;
+      const int tile0 = m[kTile0], tiles = m[kTiles], seg = m[kSeg], cta0 = m[kCta0], pieces = m[kPieces];
+      const int b = geo.by_Hk.div(seg), hk = seg - b * p.c.Hk;
+      RowTile r = {};
+      r.len = m[kLen], r.live = m[kLive], r.shift = r.len - r.live;
+      const int rows = geo.G * r.live;
+      const Key k0 = key_of<kVec>(p, geo, r, b, hk, m, key >> 6, key & 63);
+      const Key k1 = key_of<kVec>(p, geo, r, b, hk, m, 2 + (key >> 6), key & 63);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.meta_empty(ring));
+      float* const at0 = wp.weights + (static_cast<size_t>(max(k0.page, 0)) * p.c.Hk + hk) * kPage + (key & 63);
+      float* const at1 = wp.weights + (static_cast<size_t>(max(k1.page, 0)) * p.c.Hk + hk) * kPage + (key & 63);
+      const bool there0 = k0.page >= 0 && k0.j < r.len, there1 = k1.page >= 0 && k1.j < r.len;
+      float old0 = 0.f, old1 = 0.f;
+      if (w == 0) {
+        const int start = first_new(wp, b, r);
+        if (there0 && k0.j < start) old0 = *at0;
+        if (there1 && k1.j < start) old1 = *at1;
+      }
+      float sum0 = 0.f, sum1 = 0.f;
+      const uint64_t ks0 = f2_make(k0.ks, k0.ks), ks1 = f2_make(k1.ks, k1.ks);
+
+      for (int i = 0; ok && i < tiles; ++i, ++tq) {
+        const int st = tq % L::kStages, units = rows - (tile0 + i) * kTileRows > kUnit ? 2 : 1;
+        for (int h = 0; h < units; ++h, ++unit) {
+          if ((unit & 1) != w) continue;
+          const int u = unit % kUnits, u0 = (tile0 + i) * kTileRows + h * kUnit;
+          // the factors are read here, so their copy has to be waited for too
+          ok = __all_sync(0xffffffffu, cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status) &&
+                                           cache_wait(bar.s_full(u), (unit / kUnits) & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          const float* fac = reinterpret_cast<const float*>(smem + st * L::kStageBytes + D * 256) + h * kUnit;
+          const bool all = sees_all(k0, u0, u0 + kUnit, rows) && sees_all(k1, u0, u0 + kUnit, rows);
+          const bool plain = __all_sync(0xffffffffu, all);
+          uint64_t see0 = ~0ull, see1 = ~0ull;
+          if (!plain) {
+            see0 = seen_bits<kVec>(p, geo, r, b, hk, k0, u0);
+            see1 = seen_bits<kVec>(p, geo, r, b, hk, k1, u0);
+          }
+          uint64_t acc0 = f2_make(0.f, 0.f), acc1 = acc0;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t sv[64];
+            tmem_ld64(col_s(u, 0) + lane_base + 32 * c, col_s(u, 1) + lane_base + 32 * c, sv);
+            if (c == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar.s_empty(u));
+            }
+            const float4* cr = reinterpret_cast<const float4*>(fac + 32 * c);
+            const float4* nl = reinterpret_cast<const float4*>(fac + kTileRows + 32 * c);
+            if (plain) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float4 f = cr[q], n = nl[q];
+                const uint64_t fa = f2_make(f.x, f.y), fb = f2_make(f.z, f.w), na = f2_make(n.x, n.y), nb = f2_make(n.z, n.w);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                  const uint32_t* v = sv + 32 * s + 4 * q;
+                  const uint64_t ks = s ? ks1 : ks0;
+                  const uint64_t xa = f2_fma(f2_mul(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), ks), fa, na);
+                  const uint64_t xb = f2_fma(f2_mul(f2_make(__uint_as_float(v[2]), __uint_as_float(v[3])), ks), fb, nb);
+                  float x0, x1, x2, x3;
+                  f2_split(xa, x0, x1);
+                  f2_split(xb, x2, x3);
+                  uint64_t& acc = s ? acc1 : acc0;
+                  acc = f2_add(acc, f2_add(f2_make(ex2(x0), ex2(x1)), f2_make(ex2(x2), ex2(x3))));
+                }
+              }
+            } else {
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                const uint32_t see = static_cast<uint32_t>((s ? see1 : see0) >> (32 * c));
+                const float ks = s ? k1.ks : k0.ks;
+                float part = 0.f;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                  const float f = fac[32 * c + q], n = fac[kTileRows + 32 * c + q], v = __uint_as_float(sv[32 * s + q]);
+                  // (a factor past fp32: a product that overflows is a score that does)
+                  const float cc = f * ks;
+                  const float e = ex2((isinf(cc) ? (v * f) * ks : v * cc) + n);
+                  part += see >> q & 1u ? e : 0.f;
+                }
+                uint64_t& acc = s ? acc1 : acc0;
+                acc = f2_add(acc, f2_make(part, 0.f));
+              }
+            }
+          }
+          // the factors have been read: a tile of one unit counts for both warpgroups
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar.q_empty(st));
+            if (units == 1) mbar_arrive(bar.q_empty(st));
+          }
+          float x0, x1;
+          f2_split(acc0, x0, x1);
+          sum0 += x0 + x1;
+          f2_split(acc1, x0, x1);
+          sum1 += x0 + x1;
+        }
+      }
+      if (!ok) break;
+
+      // the two warpgroups' sums of the piece
+      const int x = piece & 1;
+      float* rd = red + x * kKeys;
+      if (w == 1) {
+        if (piece >= 2) ok = __all_sync(0xffffffffu, cache_wait(bar.red_empty(x), (piece / 2 - 1) & 1, p.status));
+        if (!ok) break;
+        rd[key] = sum0;
+        rd[128 + key] = sum1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.red_full(x));
+        continue;
+      }
+      ok = __all_sync(0xffffffffu, cache_wait(bar.red_full(x), (piece / 2) & 1, p.status));
+      if (!ok) break;
+      sum0 += rd[key];
+      sum1 += rd[128 + key];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.red_empty(x));
+      bool store = true;
+      if (!(flags & kWhole)) {
+        float* part = wp.partial + (static_cast<size_t>(blockIdx.x) * 2 + (flags & kTail ? 1 : 0)) * kKeys;
+        part[key] = sum0;
+        part[128 + key] = sum1;
+        auto meet = [&]() {  // the four warps
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.sums());
+          ok = __all_sync(0xffffffffu, cache_wait(bar.sums(), syncs & 1, p.status));
+          ++syncs;
+          return ok;
+        };
+        if (!meet()) break;
+        if (tid == 0) {
+          const bool last = atomic_add_acq_rel(&wp.arrived[cta0], 1) == pieces - 1;
+          if (last) wp.arrived[cta0] = 0;  // ready for the next call
+          found[2] = last;
+        }
+        if (!meet()) break;
+        store = found[2];
+        if (store) {
+          sum0 = sum1 = 0.f;
+          for (int i = 0; i < pieces; ++i) {
+            const float* q = wp.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * kKeys;
+            sum0 += __ldcg(q + key);
+            sum1 += __ldcg(q + 128 + key);
+          }
+        }
+        if (!meet()) break;  // found[2] has been read
+      }
+      if (store) {
+        if (there0) *at0 = old0 + sum0;
+        if (there1) *at1 = old1 + sum1;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  clear_unseen<kThreads, kVec>(wp, geo, reinterpret_cast<uint32_t*>(smem + L::kUnseen));
+}
+
+template <int D, bool kVec>
+cudaError_t launch_t(const WeightsParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> done[4];  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev > 255) return cudaErrorInvalidDevice;
+  if (!(done[dev >> 6].load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(cache_weights_rows_kernel<D, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    done[dev >> 6].fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  const int RT = weights_row_tiles(p.f.H, p.f.c.Hk, p.f.N);
+  weights_tiles_kernel<D><<<static_cast<unsigned>(p.f.B) * p.f.c.Hk * RT, 256, 0, s>>>(p, geo, RT);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && kVec) e = launch_cache_classify(p.f, geo, s);
+  if (e != cudaSuccess) return e;
+  const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
+  cache_weights_rows_kernel<D, kVec><<<grid, kThreads, Layout<D>::kBytes, s>>>(p, geo, RT);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weights_rows(int d, const WeightsParams& p, const Geometry& geo, int num_sms,
+                                      cudaStream_t s) {
+  const bool vec = p.f.mask.lts != nullptr || p.f.mask.uts != nullptr;
+  if (d == 64) return vec ? launch_t<64, true>(p, geo, num_sms, s) : launch_t<64, false>(p, geo, num_sms, s);
+  return vec ? launch_t<128, true>(p, geo, num_sms, s) : launch_t<128, false>(p, geo, num_sms, s);
+}
+
+}  // namespace fm
