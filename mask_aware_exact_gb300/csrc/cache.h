@@ -145,7 +145,7 @@ struct WeightsParams {
   // workspace (see WeightsWs); the last three only where there are many rows
   uint8_t* tiles;    // [B * Hk][row tiles]: operands of 128 query rows and their factors
   float* partial;    // [CTAs][2][256]: sums of the pieces of cut keys
-  int32_t* arrived;  // [CTAs]: pieces that have arrived (0 between calls)
+  int32_t* arrived;  // [CTAs][2]: pieces that have arrived (0 between calls)
 };
 struct WeightsWs {
   size_t arrived, partial, list, listed, tiles, total;

@@ -304,7 +304,7 @@ WeightsWs weights_ws_layout(int B, int H, int Hk, int N, int d, int max_pages) {
   // all sizes, so that one workspace serves them in turn
   size_t off = 256;
   w.arrived = off;
-  off = up256(off + kCacheMaxCtas * 4);
+  off = up256(off + kCacheMaxCtas * 8);
   w.partial = off;
   off = up256(off + (many ? static_cast<size_t>(kCacheMaxCtas) * 2 * 256 * 4 : 0));
   w.list = off;

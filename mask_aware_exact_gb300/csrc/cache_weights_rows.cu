@@ -8,20 +8,21 @@
 // with the row's factor and LSE behind them, so that a tile is one bulk copy. With 256 keys
 // on a CTA a tile of d = 128 is 32 KB for 1024 cycles of products.
 //
-// In S^T a thread owns a key (a TMEM lane) of each operand: the sum over rows is a sum in
-// its registers, and a row's factor and LSE, read from shared memory, serve two keys.
-// x = (S * K scale) * factor - LSE, weight 2^x.
+// In S^T a thread owns a key (a TMEM lane): the sum over rows is a sum in its registers. x =
+// (S * K scale) * factor - LSE, weight 2^x; a row's factor and LSE come from shared memory,
+// the factor only where the rows of a tile differ in it (see the row tiles).
 //
 // Items are cut into `parts` ranges of rows where there are few of them, on one line with
 // equal runs for the CTAs; the pieces of an item that a run's border cuts leave their
 // sums in the workspace, and the last to arrive adds them in order.
 //
 // Warp roles (448 threads):
-//   0-7    weights: warpgroup w takes units (64 rows) w, w + 2, ..
+//   0-7    weights: warpgroup w has operand w, a key a thread
 //   8-11   conversion of K, one key of each operand a thread
 //   12     walks the run, looks pages up, brings row tiles in
 //   13     issues the products
-// TMEM: K 2 x d / 2 columns, then three units of S^T, 2 x 64 columns each.
+// TMEM: K 2 x d / 2 columns, then three tiles of S^T, 128 columns each: a product of 128 keys
+// and 64 rows would run at 70 % of the rate of one with 128 rows.
 #include <atomic>
 
 #include "cache_weights.cuh"
@@ -34,8 +35,9 @@ constexpr int kMetaRing = 4;
 constexpr int kMetaInts = 32;
 constexpr int kKeys = 256;
 constexpr int kTileRows = 128;
-constexpr int kUnit = 64;
-constexpr int kUnits = 3;  // of S^T in TMEM
+constexpr int kHalf = 64;  // rows taken at a time
+constexpr int kUnits = 3;  // tiles of S^T in TMEM
+constexpr uint32_t kNear = 8;
 constexpr int kScanWords = kThreads / 32 + 4;
 
 enum MetaWord { kFlags, kSeg, kTile0, kTiles, kCta0, kPieces, kLen, kLive, kPg = 8, kJ0 = 12, kKs = 16, kCutWord = 20 };
@@ -47,11 +49,10 @@ struct Layout {
   static constexpr int kK = D == 128 ? 1 : 2;        // K operands in TMEM
   static constexpr int kStageBytes = D * 256 + 1024;
   static constexpr int kMeta = kStages * kStageBytes;
-  static constexpr int kRed = kMeta + kMetaRing * kMetaInts * 4;  // float [2][2][128]
-  static constexpr int kWords = kRed + 2 * kKeys * 4;
+  static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
   static constexpr int kUnseen = kWords + (kScanWords + 8) * 4;
   static constexpr int kBar = (kUnseen + kUnseenWords * 4 + 7) / 8 * 8;
-  static constexpr int kNumBars = 2 * kStages + 2 * kMetaRing + 2 * kK + 2 * kUnits + 4 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 * kMetaRing + 2 * kK + 2 * kUnits + 2;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kBytes = kTmemSlot + 16;
 };
@@ -70,9 +71,7 @@ struct Bars {
   __device__ uint32_t k_empty(int s) const { return at(2 * L::kStages + 2 * kMetaRing + L::kK + s); }  // commit
   __device__ uint32_t s_full(int u) const { return at(2 * L::kStages + 2 * kMetaRing + 2 * L::kK + u); }  // commit
   __device__ uint32_t s_empty(int u) const { return s_full(u) + 8 * kUnits; }                 // 4 warps
-  __device__ uint32_t red_full(int x) const { return s_full(0) + 8 * (2 * kUnits + x); }      // 4 warps
-  __device__ uint32_t red_empty(int x) const { return s_full(0) + 8 * (2 * kUnits + 2 + x); } // 4 warps
-  __device__ uint32_t sums() const { return s_full(0) + 8 * (2 * kUnits + 4); }               // 4 warps
+  __device__ uint32_t sums(int w) const { return s_full(0) + 8 * (2 * kUnits + w); }          // 4 warps
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
@@ -111,16 +110,40 @@ __global__ void __launch_bounds__(256) weights_tiles_kernel(const __grid_constan
       l[i] = wp.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok];
     }
   }
+  // exponents of the rows' largest elements; the tile's largest, and its smallest from 255 down
+  uint32_t top[kTileRows / kPass];
+  __shared__ uint32_t ends[2];
+  if (threadIdx.x < 2) ends[threadIdx.x] = 0;
+  __syncthreads();
+  uint32_t hi = 0, lo = 0;
+#pragma unroll
+  for (int i = 0; i < kTileRows / kPass; ++i) {
+    const uint32_t mk = 0x7fff7fffu;
+    const uint32_t a = __vmaxu2(__vmaxu2(x[i].x & mk, x[i].y & mk), __vmaxu2(x[i].z & mk, x[i].w & mk));
+    uint32_t t = max(a & 0xffffu, a >> 16);
+#pragma unroll
+    for (int o = kUnits16 / 2; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+    top[i] = t;
+    if (t != 0 && t < 0x7f80u) hi = max(hi, t >> 7), lo = max(lo, 255u - (t >> 7));
+  }
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_max_sync(0xffffffffu, lo);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&ends[0], hi);
+    atomicMax(&ends[1], lo);
+  }
+  __syncthreads();
+  // One power of two for all rows where they are within 2^kNear of the largest: fp16 then
+  // holds their elements down to 2^-(30 - kNear) of a row's largest to the bit, and smaller
+  // ones to 2^-(39 - kNear) of it.
+  const bool near = ends[0] != 0 && ends[0] + ends[1] <= 255u + kNear;
 #pragma unroll
   for (int i = 0; i < kTileRows / kPass; ++i) {
     const int row = r0 + i * kPass;
-    const uint32_t mk = 0x7fff7fffu;
-    const uint32_t a = __vmaxu2(__vmaxu2(x[i].x & mk, x[i].y & mk), __vmaxu2(x[i].z & mk, x[i].w & mk));
-    uint32_t top = max(a & 0xffffu, a >> 16);
-#pragma unroll
-    for (int o = kUnits16 / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool bad = top >= 0x7f80u || isnan(l[i]);
-    const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
+    const bool bad = top[i] >= 0x7f80u || isnan(l[i]);
+    // the largest element goes to [2^14, 2^15)
+    auto lift = [](uint32_t e) { return min(14 - (static_cast<int>(e) - 127), 126); };
+    const int up = near ? lift(ends[0]) : top[i] == 0 || bad ? 0 : lift(top[i] >> 7);
     const float f = bad ? __int_as_float(0x7fffffff) : __int_as_float((up + 127) << 23);
     const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t y[4];
@@ -202,7 +225,7 @@ __device__ __noinline__ uint64_t seen_bits(const CacheFwdParams& p, const Geomet
   if constexpr (kVec) {
     if (k.special && geo.classes != p.mask.Hm && see != 0) {
       // heads of the group have masks of their own
-      for (int i = 0; i < kUnit; ++i) {
+      for (int i = 0; i < kHalf; ++i) {
         if (!(see >> i & 1ull)) continue;
         const int rr = u0 + i, tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G, pos = r.shift + tok;
         const size_t at = (static_cast<size_t>(b) * p.mask.Hm + geo.by_mask.div(h)) *
@@ -235,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   int* found = words + kScanWords;  // segment, item of it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   const int* meta = reinterpret_cast<const int*>(smem + L::kMeta);
-  float* red = reinterpret_cast<float*>(smem + L::kRed);
 
   if (warp == 13) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -250,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     const int k = m - 2 * kMetaRing;
     if (k >= 0 && k < L::kK) n = 4;
     const int s = k - 2 * L::kK;
-    if (s >= kUnits) n = 4;
+    if (s >= kUnits) n = 4;  // and sums
     mbar_init(bar.at(i), n);
     fence_barrier_init();
   }
@@ -281,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto col_k = [&](int kb, int s) { return tmem + static_cast<uint32_t>(kb * D + s * (D / 2)); };
-  auto col_s = [&](int u, int s) { return tmem + 128u + 128u * static_cast<uint32_t>(u) + 64u * static_cast<uint32_t>(s); };
+  auto col_s = [&](int u) { return tmem + 128u + 128u * static_cast<uint32_t>(u); };
 
   if (warp == 12) {
     // ------------------------------------------------------------ run, pages, row tiles
@@ -383,9 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   } else if (warp == 13) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16(128, kUnit);
       const uint64_t dq = sdesc_sw128(smem_u32(smem), 16, 1024);
-      int tq = 0, unit = 0, kc = 0;
+      int tq = 0, kc = 0;
       bool ok = true;
       for (int piece = 0; ok; ++piece) {
         const int ring = piece % kMetaRing;
@@ -401,19 +422,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
         for (int i = 0; ok && i < tiles; ++i, ++tq) {
           const int st = tq % L::kStages;
           ok = cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status);
-          const int units = rows - (tile0 + i) * kTileRows > kUnit ? 2 : 1;
-          for (int h = 0; ok && h < units; ++h, ++unit) {
-            const int u = unit % kUnits;
+          const uint32_t idesc = idesc_f16(128, rows - (tile0 + i) * kTileRows > kHalf ? 128 : 64);
+          const uint64_t qd = dq + static_cast<uint64_t>((st * L::kStageBytes) >> 4);
+          for (int s = 0; ok && s < 2; ++s) {
+            const int unit = 2 * tq + s, u = unit % kUnits;
             if (unit >= kUnits) ok = cache_wait(bar.s_empty(u), (unit / kUnits - 1) & 1, p.status);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t qd = dq + static_cast<uint64_t>((st * L::kStageBytes + h * kUnit * 128) >> 4);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                mma_ts(col_s(u, s), col_k(kb, s) + 8 * kk, qd + static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                       idesc, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ts(col_s(u), col_k(kb, s) + 8 * kk, qd + static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                     idesc, kk > 0);
             mma_commit(bar.s_full(u));
           }
           if (ok) mma_commit(bar.q_empty(st));
@@ -470,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     // ------------------------------------------------------------ weights
     const int w = warp >> 2, key = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int tq = 0, unit = 0, syncs = 0;
+    int tq = 0, syncs = 0;
     bool ok = true;
     for (int piece = 0; ok; ++piece) {
       const int ring = piece % kMetaRing;
@@ -484,156 +503,123 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
       RowTile r = {};
       r.len = m[kLen], r.live = m[kLive], r.shift = r.len - r.live;
       const int rows = geo.G * r.live;
-      const Key k0 = key_of<kVec>(p, geo, r, b, hk, m, key >> 6, key & 63);
-      const Key k1 = key_of<kVec>(p, geo, r, b, hk, m, 2 + (key >> 6), key & 63);
+      const Key k = key_of<kVec>(p, geo, r, b, hk, m, 2 * w + (key >> 6), key & 63);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.meta_empty(ring));
-      float* const at0 = wp.weights + (static_cast<size_t>(max(k0.page, 0)) * p.c.Hk + hk) * kPage + (key & 63);
-      float* const at1 = wp.weights + (static_cast<size_t>(max(k1.page, 0)) * p.c.Hk + hk) * kPage + (key & 63);
-      const bool there0 = k0.page >= 0 && k0.j < r.len, there1 = k1.page >= 0 && k1.j < r.len;
-      float old0 = 0.f, old1 = 0.f;
-      if (w == 0) {
-        const int start = first_new(wp, b, r);
-        if (there0 && k0.j < start) old0 = *at0;
-        if (there1 && k1.j < start) old1 = *at1;
-      }
-      float sum0 = 0.f, sum1 = 0.f;
-      const uint64_t ks0 = f2_make(k0.ks, k0.ks), ks1 = f2_make(k1.ks, k1.ks);
+      const bool there = k.page >= 0 && k.j < r.len;
+      float* const at = wp.weights + (static_cast<size_t>(max(k.page, 0)) * p.c.Hk + hk) * kPage + (key & 63);
+      float old = 0.f;
+      if (there && k.j < first_new(wp, b, r)) old = *at;
+      float sum = 0.f;
 
-      for (int i = 0; ok && i < tiles; ++i, ++tq) {
-        const int st = tq % L::kStages, units = rows - (tile0 + i) * kTileRows > kUnit ? 2 : 1;
-        for (int h = 0; h < units; ++h, ++unit) {
-          if ((unit & 1) != w) continue;
-          const int u = unit % kUnits, u0 = (tile0 + i) * kTileRows + h * kUnit;
-          // the factors are read here, so their copy has to be waited for too
-          ok = __all_sync(0xffffffffu, cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status) &&
-                                           cache_wait(bar.s_full(u), (unit / kUnits) & 1, p.status));
-          if (!ok) break;
-          tc_fence_after();
-          const float* fac = reinterpret_cast<const float*>(smem + st * L::kStageBytes + D * 256) + h * kUnit;
-          const bool all = sees_all(k0, u0, u0 + kUnit, rows) && sees_all(k1, u0, u0 + kUnit, rows);
-          const bool plain = __all_sync(0xffffffffu, all);
-          uint64_t see0 = ~0ull, see1 = ~0ull;
-          if (!plain) {
-            see0 = seen_bits<kVec>(p, geo, r, b, hk, k0, u0);
-            see1 = seen_bits<kVec>(p, geo, r, b, hk, k1, u0);
-          }
-          uint64_t acc0 = f2_make(0.f, 0.f), acc1 = acc0;
+      for (int i = 0; i < tiles; ++i, ++tq) {
+        const int st = tq % L::kStages, unit = 2 * tq + w, u = unit % kUnits, row0 = (tile0 + i) * kTileRows;
+        const int halves = rows - row0 > kHalf ? 2 : 1;
+        // the factors are read here, so their copy has to be waited for too
+        ok = __all_sync(0xffffffffu, cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status) &&
+                                         cache_wait(bar.s_full(u), (unit / kUnits) & 1, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        const float* fac = reinterpret_cast<const float*>(smem + st * L::kStageBytes + D * 256);
+        const float f0 = fac[0];
+        const float4 mine4 = reinterpret_cast<const float4*>(fac)[lane];
+        // one factor for the tile, and no product of it with a scale past fp32
+        const bool one = __all_sync(0xffffffffu, mine4.x == f0 && mine4.y == f0 && mine4.z == f0 && mine4.w == f0 && f0 <= 1.f);
+        const float c1 = f0 * k.ks;
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t sv[64];
-            tmem_ld64(col_s(u, 0) + lane_base + 32 * c, col_s(u, 1) + lane_base + 32 * c, sv);
-            if (c == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar.s_empty(u));
-            }
-            const float4* cr = reinterpret_cast<const float4*>(fac + 32 * c);
-            const float4* nl = reinterpret_cast<const float4*>(fac + kTileRows + 32 * c);
-            if (plain) {
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 f = cr[q], n = nl[q];
-                const uint64_t fa = f2_make(f.x, f.y), fb = f2_make(f.z, f.w), na = f2_make(n.x, n.y), nb = f2_make(n.z, n.w);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                  const uint32_t* v = sv + 32 * s + 4 * q;
-                  const uint64_t ks = s ? ks1 : ks0;
-                  const uint64_t xa = f2_fma(f2_mul(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), ks), fa, na);
-                  const uint64_t xb = f2_fma(f2_mul(f2_make(__uint_as_float(v[2]), __uint_as_float(v[3])), ks), fb, nb);
-                  float x0, x1, x2, x3;
-                  f2_split(xa, x0, x1);
-                  f2_split(xb, x2, x3);
-                  uint64_t& acc = s ? acc1 : acc0;
-                  acc = f2_add(acc, f2_add(f2_make(ex2(x0), ex2(x1)), f2_make(ex2(x2), ex2(x3))));
-                }
-              }
-            } else {
-#pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                const uint32_t see = static_cast<uint32_t>((s ? see1 : see0) >> (32 * c));
-                const float ks = s ? k1.ks : k0.ks;
-                float part = 0.f;
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                  const float f = fac[32 * c + q], n = fac[kTileRows + 32 * c + q], v = __uint_as_float(sv[32 * s + q]);
-                  // (a factor past fp32: a product that overflows is a score that does)
-                  const float cc = f * ks;
-                  const float e = ex2((isinf(cc) ? (v * f) * ks : v * cc) + n);
-                  part += see >> q & 1u ? e : 0.f;
-                }
-                uint64_t& acc = s ? acc1 : acc0;
-                acc = f2_add(acc, f2_make(part, 0.f));
-              }
-            }
+        for (int h = 0; h < halves; ++h) {
+          const int u0 = row0 + h * kHalf;
+          uint32_t sv[64];
+          tmem_ld64(col_s(u) + lane_base + 64 * h, col_s(u) + lane_base + 64 * h + 32, sv);
+          if (h + 1 == halves) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.s_empty(u));
           }
-          // the factors have been read: a tile of one unit counts for both warpgroups
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar.q_empty(st));
-            if (units == 1) mbar_arrive(bar.q_empty(st));
+          const float4* cr = reinterpret_cast<const float4*>(fac + h * kHalf);
+          const float4* nl = reinterpret_cast<const float4*>(fac + kTileRows + h * kHalf);
+          const bool plain = __all_sync(0xffffffffu, sees_all(k, u0, u0 + kHalf, rows));
+          uint64_t acc0 = f2_make(0.f, 0.f), acc1 = acc0;
+          if (plain && one) {
+            const uint64_t c2 = f2_make(c1, c1);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float4 n = nl[q];
+              const uint32_t* v = sv + 4 * q;
+              float x0, x1, x2, x3;
+              f2_split(f2_fma(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, f2_make(n.x, n.y)), x0, x1);
+              f2_split(f2_fma(f2_make(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, f2_make(n.z, n.w)), x2, x3);
+              acc0 = f2_add(acc0, f2_make(ex2(x0), ex2(x1)));
+              acc1 = f2_add(acc1, f2_make(ex2(x2), ex2(x3)));
+            }
+          } else if (plain) {
+            const uint64_t ks = f2_make(k.ks, k.ks);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float4 f = cr[q], n = nl[q];
+              const uint32_t* v = sv + 4 * q;
+              float x0, x1, x2, x3;
+              f2_split(f2_fma(f2_mul(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), ks), f2_make(f.x, f.y),
+                              f2_make(n.x, n.y)), x0, x1);
+              f2_split(f2_fma(f2_mul(f2_make(__uint_as_float(v[2]), __uint_as_float(v[3])), ks), f2_make(f.z, f.w),
+                              f2_make(n.z, n.w)), x2, x3);
+              acc0 = f2_add(acc0, f2_make(ex2(x0), ex2(x1)));
+              acc1 = f2_add(acc1, f2_make(ex2(x2), ex2(x3)));
+            }
+          } else {
+            const uint64_t see = seen_bits<kVec>(p, geo, r, b, hk, k, u0);
+            if (__any_sync(0xffffffffu, see != 0)) {
+              float part[4] = {};
+#pragma unroll
+              for (int q = 0; q < 64; ++q) {
+                const float f = fac[h * kHalf + q], n = fac[kTileRows + h * kHalf + q], v = __uint_as_float(sv[q]);
+                // (a factor past fp32: a product that overflows is a score that does)
+                const float cc = f * k.ks;
+                const float e = ex2((isinf(cc) ? (v * f) * k.ks : v * cc) + n);
+                part[q & 3] += ((q < 32 ? static_cast<uint32_t>(see) : static_cast<uint32_t>(see >> 32)) >> (q & 31)) & 1u ? e : 0.f;
+              }
+              acc0 = f2_make(part[0], part[1]);
+              acc1 = f2_make(part[2], part[3]);
+            }
           }
           float x0, x1;
-          f2_split(acc0, x0, x1);
-          sum0 += x0 + x1;
-          f2_split(acc1, x0, x1);
-          sum1 += x0 + x1;
+          f2_split(f2_add(acc0, acc1), x0, x1);
+          sum += x0 + x1;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.q_empty(st));  // the factors have been read
       }
       if (!ok) break;
 
-      // the two warpgroups' sums of the piece
-      const int x = piece & 1;
-      float* rd = red + x * kKeys;
-      if (w == 1) {
-        if (piece >= 2) ok = __all_sync(0xffffffffu, cache_wait(bar.red_empty(x), (piece / 2 - 1) & 1, p.status));
-        if (!ok) break;
-        rd[key] = sum0;
-        rd[128 + key] = sum1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.red_full(x));
-        continue;
-      }
-      ok = __all_sync(0xffffffffu, cache_wait(bar.red_full(x), (piece / 2) & 1, p.status));
-      if (!ok) break;
-      sum0 += rd[key];
-      sum1 += rd[128 + key];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.red_empty(x));
       bool store = true;
       if (!(flags & kWhole)) {
-        float* part = wp.partial + (static_cast<size_t>(blockIdx.x) * 2 + (flags & kTail ? 1 : 0)) * kKeys;
-        part[key] = sum0;
-        part[128 + key] = sum1;
+        // this warpgroup's keys of the piece
+        float* part = wp.partial + (static_cast<size_t>(blockIdx.x) * 2 + (flags & kTail ? 1 : 0)) * kKeys + 128 * w;
+        part[key] = sum;
         auto meet = [&]() {  // the four warps
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar.sums());
-          ok = __all_sync(0xffffffffu, cache_wait(bar.sums(), syncs & 1, p.status));
+          if (lane == 0) mbar_arrive(bar.sums(w));
+          ok = __all_sync(0xffffffffu, cache_wait(bar.sums(w), syncs & 1, p.status));
           ++syncs;
           return ok;
         };
         if (!meet()) break;
-        if (tid == 0) {
-          const bool last = atomic_add_acq_rel(&wp.arrived[cta0], 1) == pieces - 1;
-          if (last) wp.arrived[cta0] = 0;  // ready for the next call
-          found[2] = last;
+        if (key == 0) {
+          int32_t* count = wp.arrived + 2 * cta0 + w;
+          const bool last = atomic_add_acq_rel(count, 1) == pieces - 1;
+          if (last) *count = 0;  // ready for the next call
+          found[2 + w] = last;
         }
         if (!meet()) break;
-        store = found[2];
+        store = found[2 + w];
         if (store) {
-          sum0 = sum1 = 0.f;
-          for (int i = 0; i < pieces; ++i) {
-            const float* q = wp.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * kKeys;
-            sum0 += __ldcg(q + key);
-            sum1 += __ldcg(q + 128 + key);
-          }
+          sum = 0.f;
+          for (int i = 0; i < pieces; ++i)
+            sum += __ldcg(wp.partial + (static_cast<size_t>(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * kKeys + 128 * w + key);
         }
-        if (!meet()) break;  // found[2] has been read
+        if (!meet()) break;  // found has been read
       }
-      if (store) {
-        if (there0) *at0 = old0 + sum0;
-        if (there1) *at1 = old1 + sum1;
-      }
+      if (store && there) *at = old + sum;
     }
   }
 
