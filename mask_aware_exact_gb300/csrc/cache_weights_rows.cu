@@ -2,8 +2,8 @@
 // rows of a prompt, drafted tokens of large groups): products S^T = K Q^T on tcgen05.
 //
 // Keys stay, rows stream. An item is four pages, 256 keys, as two operands of 128 rows
-// in TMEM (fp16, exact for codes), converted once; tiles of 128 query rows pass by as the
-// other operand. A first kernel writes those as fp16 tiles in the layout that the tensor
+// in shared memory (fp16, exact for codes), converted once; tiles of 128 query rows pass by
+// as the other operand. A first kernel writes those as fp16 tiles in the layout that the tensor
 // cores read (128-byte swizzle), each row scaled by a power of two as in the attention,
 // with the row's factor and LSE behind them, so that a tile is one bulk copy. With 256 keys
 // on a CTA a tile of d = 128 is 32 KB for 1024 cycles of products.
@@ -16,13 +16,14 @@
 // equal runs for the CTAs; the pieces of an item that a run's border cuts leave their
 // sums in the workspace, and the last to arrive adds them in order.
 //
-// Warp roles (448 threads):
+// Warp roles (480 threads):
 //   0-7    weights: warpgroup w has operand w, a key a thread
 //   8-11   conversion of K, one key of each operand a thread
 //   12     walks the run, looks pages up, brings row tiles in
-//   13     issues the products
-// TMEM: K 2 x d / 2 columns, then three tiles of S^T, 128 columns each: a product of 128 keys
-// and 64 rows would run at 70 % of the rate of one with 128 rows.
+//   13, 14 issue the products of an operand each: what one thread does between the products
+//          of two tiles (waits, commits) takes longer than the tensor cores have work queued
+// TMEM: two tiles of S^T for each operand, 128 columns each: a product of 128 keys and 64
+// rows would run at 70 % of the rate of one with 128 rows.
 #include <atomic>
 
 #include "cache_weights.cuh"
@@ -30,13 +31,15 @@
 namespace fm {
 namespace {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kMetaRing = 4;
 constexpr int kMetaInts = 32;
 constexpr int kKeys = 256;
 constexpr int kTileRows = 128;
+constexpr int kPartsRun = 32;
 constexpr int kHalf = 64;  // rows taken at a time
-constexpr int kUnits = 3;  // tiles of S^T in TMEM
+constexpr int kFactorRing = 8;       // of the row tiles' factors
+constexpr int kFactorBytes = 1024;
 constexpr uint32_t kNear = 8;
 constexpr int kScanWords = kThreads / 32 + 4;
 
@@ -45,14 +48,18 @@ enum Flag { kEnd = 1, kWhole = 2, kTail = 4 };
 
 template <int D>
 struct Layout {
-  static constexpr int kStages = D == 128 ? 5 : 9;   // row tiles in shared memory
-  static constexpr int kK = D == 128 ? 1 : 2;        // K operands in TMEM
-  static constexpr int kStageBytes = D * 256 + 1024;
-  static constexpr int kMeta = kStages * kStageBytes;
+  static constexpr int kStages = D == 128 ? 4 : 8;  // row tiles in shared memory
+  static constexpr int kK = D == 128 ? 1 : 2;       // pairs of K operands
+  static constexpr int kStageBytes = D * 256;
+  static constexpr int kTileBytes = kStageBytes + kFactorBytes;  // in the workspace
+  static constexpr int kKOperand = 128 * D * 2;
+  static constexpr int kKeysAt = kStages * kStageBytes;
+  static constexpr int kFactors = kKeysAt + 2 * kK * kKOperand;
+  static constexpr int kMeta = kFactors + kFactorRing * kFactorBytes;
   static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
   static constexpr int kUnseen = kWords + (kScanWords + 8) * 4;
   static constexpr int kBar = (kUnseen + kUnseenWords * 4 + 7) / 8 * 8;
-  static constexpr int kNumBars = 2 * kStages + 2 * kMetaRing + 2 * kK + 2 * kUnits + 2;
+  static constexpr int kNumBars = 2 * kStages + 2 * kMetaRing + 2 * kK + 10 + 2 * kFactorRing;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kBytes = kTmemSlot + 16;
 };
@@ -64,18 +71,26 @@ struct Bars {
   uint32_t base;
   __device__ uint32_t at(int i) const { return base + 8 * i; }
   __device__ uint32_t q_full(int s) const { return at(s); }                                   // bytes
-  __device__ uint32_t q_empty(int s) const { return at(L::kStages + s); }                     // 8 warps, commit
+  __device__ uint32_t q_empty(int s) const { return at(L::kStages + s); }                     // 2 commits
   __device__ uint32_t meta_full(int s) const { return at(2 * L::kStages + s); }               // 1
-  __device__ uint32_t meta_empty(int s) const { return at(2 * L::kStages + kMetaRing + s); }  // 13 warps
+  __device__ uint32_t meta_empty(int s) const { return at(2 * L::kStages + kMetaRing + s); }  // 14 warps
   __device__ uint32_t k_full(int s) const { return at(2 * L::kStages + 2 * kMetaRing + s); }  // 4 warps
-  __device__ uint32_t k_empty(int s) const { return at(2 * L::kStages + 2 * kMetaRing + L::kK + s); }  // commit
-  __device__ uint32_t s_full(int u) const { return at(2 * L::kStages + 2 * kMetaRing + 2 * L::kK + u); }  // commit
-  __device__ uint32_t s_empty(int u) const { return s_full(u) + 8 * kUnits; }                 // 4 warps
-  __device__ uint32_t sums(int w) const { return s_full(0) + 8 * (2 * kUnits + w); }          // 4 warps
+  __device__ uint32_t k_empty(int s) const { return at(2 * L::kStages + 2 * kMetaRing + L::kK + s); }  // 2 commits
+  // of operand w, tile i of S^T
+  __device__ uint32_t s_full(int w, int i) const { return at(2 * L::kStages + 2 * kMetaRing + 2 * L::kK + 2 * w + i); }  // commit
+  __device__ uint32_t s_empty(int w, int i) const { return s_full(w, i) + 32; }  // 4 warps
+  __device__ uint32_t sums(int w) const { return s_full(0, 0) + 64 + 8 * w; }    // 4 warps
+  __device__ uint32_t c_full(int i) const { return s_full(0, 0) + 80 + 8 * i; }                       // bytes
+  __device__ uint32_t c_empty(int i) const { return s_full(0, 0) + 80 + 8 * (kFactorRing + i); }  // 8 warps
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// cache_wait whose first tries do not read the clock.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* status) {
+  return mbar_test_wait(bar, parity) || mbar_try_wait(bar, parity) || cache_wait_slow(bar, parity, status);
 }
 
 // ---------------------------------------------------------------- row tiles
@@ -95,7 +110,7 @@ __global__ void __launch_bounds__(256) weights_tiles_kernel(const __grid_constan
   const int rows = geo.G * r.live;
   if (tile * kTileRows >= rows) return;
   const int u = threadIdx.x % kUnits16, r0 = threadIdx.x / kUnits16;
-  uint8_t* dst = wp.tiles + static_cast<size_t>(blockIdx.x) * (D * 256 + 1024);
+  uint8_t* dst = wp.tiles + static_cast<size_t>(blockIdx.x) * Layout<D>::kTileBytes;
   float* factors = reinterpret_cast<float*>(dst + D * 256);
   uint4 x[kTileRows / kPass];
   float l[kTileRows / kPass];
@@ -152,7 +167,8 @@ __global__ void __launch_bounds__(256) weights_tiles_kernel(const __grid_constan
       y[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
     *reinterpret_cast<uint4*>(dst + (u >> 3) * 16384 + sw128_offset(row, u & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
     if (u == 0) {
-      factors[row] = p.scale_log2 * __int_as_float((127 - up) << 23);
+      // (the second is below zero where the first is all rows')
+      factors[row] = near && row == 1 ? -1.f : p.scale_log2 * __int_as_float((127 - up) << 23);
       factors[kTileRows + row] = isnan(l[i]) ? 0.f : l[i] == -INFINITY ? -INFINITY : l[i] * -1.4426950408889634f;
     }
   }
@@ -212,6 +228,10 @@ __device__ __forceinline__ Key key_of(const CacheFwdParams& p, const Geometry& g
   }
   return k;
 }
+// Row from which on all see the key, as far as causality goes; INT_MAX where that is not all.
+__device__ __forceinline__ int seen_from(const Key& k) {
+  return k.special || k.b0 > k.a0 || k.b1 > k.a1 ? 0x7fffffff : k.lo;
+}
 // Whether all rows [u0, u1) see the key (rows behind the last may).
 __device__ __forceinline__ bool sees_all(const Key& k, int u0, int u1, int rows) {
   return !k.special && k.lo <= u0 && k.hi >= min(u1, rows) && (k.b0 <= u0 || k.a0 >= u1 || k.a0 >= k.b0) &&
@@ -220,7 +240,7 @@ __device__ __forceinline__ bool sees_all(const Key& k, int u0, int u1, int rows)
 // Bit i: row u0 + i sees the key.
 template <bool kVec>
 __device__ __noinline__ uint64_t seen_bits(const CacheFwdParams& p, const Geometry& geo, const RowTile& r, int b,
-                                           int hk, const Key& k, int u0) {
+                                           int hk, const Key k, int u0) {
   uint64_t see = bit_range(k.lo - u0, k.hi - u0) & ~bit_range(k.a0 - u0, k.b0 - u0) & ~bit_range(k.a1 - u0, k.b1 - u0);
   if constexpr (kVec) {
     if (k.special && geo.classes != p.mask.Hm && see != 0) {
@@ -266,13 +286,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   if (tid < L::kNumBars) {
     const int i = tid;
     int n = 1;
-    if (i >= L::kStages && i < 2 * L::kStages) n = 9;
+    if (i >= L::kStages && i < 2 * L::kStages) n = 2;
     const int m = i - 2 * L::kStages;
-    if (m >= kMetaRing && m < 2 * kMetaRing) n = 13;
+    if (m >= kMetaRing && m < 2 * kMetaRing) n = 14;
     const int k = m - 2 * kMetaRing;
-    if (k >= 0 && k < L::kK) n = 4;
-    const int s = k - 2 * L::kK;
-    if (s >= kUnits) n = 4;  // and sums
+    if (k >= 0 && k < 2 * L::kK) n = k < L::kK ? 4 : 2;
+    const int x = k - 2 * L::kK;
+    if (x >= 4 && x < 10) n = 4;
+    if (x >= 10 + kFactorRing) n = 8;
     mbar_init(bar.at(i), n);
     fence_barrier_init();
   }
@@ -285,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   int total;
   const int before = block_before<kThreads / 32>(mine, words, total);
   const int grid = static_cast<int>(gridDim.x);
-  // enough parts that a run is eight of them or more
-  const int parts = total == 0 || total >= 8 * grid ? 1 : min(RT, (8 * grid + total - 1) / total);
+  // enough parts that a run is 32 of them or more
+  const int parts = total == 0 || total >= kPartsRun * grid ? 1 : min(RT, (kPartsRun * grid + total - 1) / total);
   const long long line = static_cast<long long>(total) * parts;
   const int run = static_cast<int>((line + grid - 1) / grid);
   const long long run_lo = min(static_cast<long long>(run) * blockIdx.x, line), run_hi = min(run_lo + run, line);
@@ -302,8 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto col_k = [&](int kb, int s) { return tmem + static_cast<uint32_t>(kb * D + s * (D / 2)); };
-  auto col_s = [&](int u) { return tmem + 128u + 128u * static_cast<uint32_t>(u); };
+  auto col_s = [&](int w, int i) { return tmem + 256u * static_cast<uint32_t>(w) + 128u * static_cast<uint32_t>(i); };
 
   if (warp == 12) {
     // ------------------------------------------------------------ run, pages, row tiles
@@ -359,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
       }
       for (int t = 0; ok && t < avail; ++t, ++piece) {
         const int ring = piece % kMetaRing;
-        if (piece >= kMetaRing) ok = __all_sync(0xffffffffu, cache_wait(bar.meta_empty(ring), (piece / kMetaRing - 1) & 1, p.status));
+        if (piece >= kMetaRing) ok = __all_sync(0xffffffffu, wait_for(bar.meta_empty(ring), (piece / kMetaRing - 1) & 1, p.status));
         if (!ok) break;
         if (lane == t) {
           int4* at = reinterpret_cast<int4*>(smem + L::kMeta) + ring * (kMetaInts / 4);
@@ -371,12 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
         const int tiles = __shfl_sync(0xffffffffu, m[kTiles], t);
         for (int i = 0; ok && i < tiles; ++i, ++tq) {
           const int st = tq % L::kStages;
-          if (tq >= L::kStages) ok = __all_sync(0xffffffffu, cache_wait(bar.q_empty(st), (tq / L::kStages - 1) & 1, p.status));
+          const int ci = tq % kFactorRing;
+          if (tq >= L::kStages) ok = wait_for(bar.q_empty(st), (tq / L::kStages - 1) & 1, p.status);
+          if (ok && tq >= kFactorRing) ok = wait_for(bar.c_empty(ci), (tq / kFactorRing - 1) & 1, p.status);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
+            const uint8_t* src = wp.tiles + (static_cast<size_t>(sg) * RT + tile0 + i) * L::kTileBytes;
             mbar_arrive_expect_tx(bar.q_full(st), L::kStageBytes);
-            bulk_load(smem_u32(smem + st * L::kStageBytes),
-                      wp.tiles + (static_cast<size_t>(sg) * RT + tile0 + i) * L::kStageBytes, L::kStageBytes, bar.q_full(st));
+            bulk_load(smem_u32(smem + st * L::kStageBytes), src, L::kStageBytes, bar.q_full(st));
+            mbar_arrive_expect_tx(bar.c_full(ci), kFactorBytes);
+            bulk_load(smem_u32(smem + L::kFactors + ci * kFactorBytes), src + L::kStageBytes, kFactorBytes, bar.c_full(ci));
           }
         }
       }
@@ -391,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
         if (seg >= nseg) ok = lengths_moved(p.status);
       }
     }
-    if (ok && piece >= kMetaRing) ok = cache_wait(bar.meta_empty(piece % kMetaRing), (piece / kMetaRing - 1) & 1, p.status);
+    if (ok && piece >= kMetaRing) ok = wait_for(bar.meta_empty(piece % kMetaRing), (piece / kMetaRing - 1) & 1, p.status);
     if (lane == 0) {
       if (ok) {
         (reinterpret_cast<int*>(smem + L::kMeta) + (piece % kMetaRing) * kMetaInts)[kFlags] = kEnd;
@@ -400,55 +425,55 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
         // copies in flight land before the CTA's shared memory is given up
         for (int i = max(0, tq - L::kStages); i < tq; ++i)
           mbar_wait_for(bar.q_full(i % L::kStages), (i / L::kStages) & 1, nullptr, 1000000ull);
+        for (int i = max(0, tq - kFactorRing); i < tq; ++i)
+          mbar_wait_for(bar.c_full(i % kFactorRing), (i / kFactorRing) & 1, nullptr, 1000000ull);
       }
     }
-  } else if (warp == 13) {
-    // ------------------------------------------------------------ products
+  } else if (warp >= 13) {
+    // ------------------------------------------------------------ products of operand w
     if (lane == 0) {
+      const int w = warp - 13;
       const uint64_t dq = sdesc_sw128(smem_u32(smem), 16, 1024);
-      int tq = 0, kc = 0;
+      const uint64_t dk = sdesc_sw128(smem_u32(smem + L::kKeysAt + w * L::kKOperand), 16, 1024);
+      int st = 0, turn = 0, t = 0, kb = 0, kturn = 0;  // stage of the ring and its turns, tile, K
       bool ok = true;
       for (int piece = 0; ok; ++piece) {
         const int ring = piece % kMetaRing;
-        if (!cache_wait(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status)) break;
+        if (!wait_for(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status)) break;
         const int* m = meta + ring * kMetaInts;
         if (m[kFlags] & kEnd) break;
         const int tile0 = m[kTile0], tiles = m[kTiles], rows = geo.G * m[kLive];
         mbar_arrive(bar.meta_empty(ring));
         if (tiles == 0) continue;
-        const int kb = kc % L::kK;
-        ok = cache_wait(bar.k_full(kb), (kc / L::kK) & 1, p.status);
-        tc_fence_after();
-        for (int i = 0; ok && i < tiles; ++i, ++tq) {
-          const int st = tq % L::kStages;
-          ok = cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status);
+        ok = wait_for(bar.k_full(kb), kturn & 1, p.status);
+        const uint64_t kd = dk + static_cast<uint64_t>((2 * kb * L::kKOperand) >> 4);
+        for (int i = 0; ok && i < tiles; ++i, ++t) {
+          ok = wait_for(bar.q_full(st), turn & 1, p.status) &&
+               (t < 2 || wait_for(bar.s_empty(w, t & 1), ((t >> 1) - 1) & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
           const uint32_t idesc = idesc_f16(128, rows - (tile0 + i) * kTileRows > kHalf ? 128 : 64);
           const uint64_t qd = dq + static_cast<uint64_t>((st * L::kStageBytes) >> 4);
-          for (int s = 0; ok && s < 2; ++s) {
-            const int unit = 2 * tq + s, u = unit % kUnits;
-            if (unit >= kUnits) ok = cache_wait(bar.s_empty(u), (unit / kUnits - 1) & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ts(col_s(u), col_k(kb, s) + 8 * kk, qd + static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                     idesc, kk > 0);
-            mma_commit(bar.s_full(u));
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+            mma_ss(col_s(w, t & 1), kd + off, qd + off, idesc, kk > 0);
           }
-          if (ok) mma_commit(bar.q_empty(st));
+          mma_commit(bar.s_full(w, t & 1));
+          mma_commit(bar.q_empty(st));
+          if (++st == L::kStages) st = 0, ++turn;
         }
         if (ok) mma_commit(bar.k_empty(kb));
-        ++kc;
+        if (++kb == L::kK) kb = 0, ++kturn;
       }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ conversion
     const int key = (warp - 8) * 32 + lane;
-    const uint32_t lane_base = static_cast<uint32_t>((warp - 8) * 32) << 16;
     int kc = 0;
     for (int piece = 0;; ++piece) {
       const int ring = piece % kMetaRing;
-      if (!__all_sync(0xffffffffu, cache_wait(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status))) break;
+      if (!__all_sync(0xffffffffu, wait_for(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status))) break;
       const int* m = meta + ring * kMetaInts;
       if (m[kFlags] & kEnd) break;
       const int tiles = m[kTiles], seg = m[kSeg];
@@ -466,21 +491,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
           w[s][i] = page[s] < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 16 * i);
       }
       const int kb = kc % L::kK;
-      if (kc >= L::kK && !__all_sync(0xffffffffu, cache_wait(bar.k_empty(kb), (kc / L::kK - 1) & 1, p.status))) break;
-      tc_fence_after();
+      if (kc >= L::kK && !__all_sync(0xffffffffu, wait_for(bar.k_empty(kb), (kc / L::kK - 1) & 1, p.status))) break;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t to = smem_u32(smem + L::kKeysAt + (2 * kb + s) * L::kKOperand);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t h[32];
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t h[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) codes_to_f16(word(w[s][4 * c + i], u), h[8 * i + 2 * u], h[8 * i + 2 * u + 1]);
-          tmem_st32p(col_k(kb, s) + lane_base + 32 * c, h);
+          for (int u = 0; u < 4; ++u) codes_to_f16(word(w[s][i], u), h[2 * u], h[2 * u + 1]);
+          const uint32_t at = to + (i >> 2) * 16384;
+          st_shared_v4(at + sw128_offset(key, (2 * i) & 7), h[0], h[1], h[2], h[3]);
+          st_shared_v4(at + sw128_offset(key, (2 * i + 1) & 7), h[4], h[5], h[6], h[7]);
         }
-      tmem_st_wait();
-      tc_fence_before();
+      }
+      fence_proxy_async_smem();  // the operands are read by the tensor cores
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.k_full(kb));
       ++kc;
@@ -489,11 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     // ------------------------------------------------------------ weights
     const int w = warp >> 2, key = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int tq = 0, syncs = 0;
+    int ci = 0, cturn = 0, t = 0, syncs = 0;
     bool ok = true;
     for (int piece = 0; ok; ++piece) {
       const int ring = piece % kMetaRing;
-      ok = __all_sync(0xffffffffu, cache_wait(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status));
+      ok = __all_sync(0xffffffffu, wait_for(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status));
       if (!ok) break;
       const int* m = meta + ring * kMetaInts;
       const int flags = m[kFlags];
@@ -511,83 +536,75 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
       float old = 0.f;
       if (there && k.j < first_new(wp, b, r)) old = *at;
       float sum = 0.f;
+      // rows from which on nothing of this warp is masked (what keys that are not there get is
+      // dropped)
+      const int all_from = __reduce_max_sync(0xffffffffu, there ? seen_from(k) : 0);
 
-      for (int i = 0; i < tiles; ++i, ++tq) {
-        const int st = tq % L::kStages, unit = 2 * tq + w, u = unit % kUnits, row0 = (tile0 + i) * kTileRows;
-        const int halves = rows - row0 > kHalf ? 2 : 1;
-        // the factors are read here, so their copy has to be waited for too
-        ok = __all_sync(0xffffffffu, cache_wait(bar.q_full(st), (tq / L::kStages) & 1, p.status) &&
-                                         cache_wait(bar.s_full(u), (unit / kUnits) & 1, p.status));
-        if (!ok) break;
+      for (int i = 0; i < tiles; ++i, ++t) {
+        const int row0 = (tile0 + i) * kTileRows, halves = rows - row0 > kHalf ? 2 : 1;
+        // (both at once: a test that succeeds takes 100 cycles)
+        const bool now = mbar_test_wait(bar.c_full(ci), cturn & 1), done = mbar_test_wait(bar.s_full(w, t & 1), (t >> 1) & 1);
+        if (!__all_sync(0xffffffffu, now && done)) {
+          ok = __all_sync(0xffffffffu, wait_for(bar.c_full(ci), cturn & 1, p.status) &&
+                                           wait_for(bar.s_full(w, t & 1), (t >> 1) & 1, p.status));
+          if (!ok) break;
+        }
         tc_fence_after();
-        const float* fac = reinterpret_cast<const float*>(smem + st * L::kStageBytes + D * 256);
-        const float f0 = fac[0];
-        const float4 mine4 = reinterpret_cast<const float4*>(fac)[lane];
-        // one factor for the tile, and no product of it with a scale past fp32
-        const bool one = __all_sync(0xffffffffu, mine4.x == f0 && mine4.y == f0 && mine4.z == f0 && mine4.w == f0 && f0 <= 1.f);
-        const float c1 = f0 * k.ks;
-#pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-          const int u0 = row0 + h * kHalf;
+        const float* fac = reinterpret_cast<const float*>(smem + L::kFactors + ci * kFactorBytes);
+        const float2 first = *reinterpret_cast<const float2*>(fac);
+        const bool one = first.y < 0.f;
+        const float c1 = first.x * k.ks;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == halves) break;
+          const float4* nl = reinterpret_cast<const float4*>(fac + kTileRows + h * kHalf);
+          float4 ahead[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ahead[q] = nl[q];
           uint32_t sv[64];
-          tmem_ld64(col_s(u) + lane_base + 64 * h, col_s(u) + lane_base + 64 * h + 32, sv);
+          tmem_ld64(col_s(w, t & 1) + lane_base + 64 * h, col_s(w, t & 1) + lane_base + 64 * h + 32, sv);
           if (h + 1 == halves) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar.s_empty(u));
+            if (lane == 0) mbar_arrive(bar.s_empty(w, t & 1));
           }
-          const float4* cr = reinterpret_cast<const float4*>(fac + h * kHalf);
-          const float4* nl = reinterpret_cast<const float4*>(fac + kTileRows + h * kHalf);
-          const bool plain = __all_sync(0xffffffffu, sees_all(k, u0, u0 + kHalf, rows));
-          uint64_t acc0 = f2_make(0.f, 0.f), acc1 = acc0;
-          if (plain && one) {
+          const int u0 = row0 + h * kHalf;
+          const bool plain = u0 >= all_from || (kVec && __all_sync(0xffffffffu, !there || sees_all(k, u0, u0 + kHalf, rows)));
+          uint64_t acc = f2_make(0.f, 0.f);
+          if (plain && one && first.x <= 1.f) {
             const uint64_t c2 = f2_make(c1, c1);
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              const float4 n = nl[q];
+              const float4 n = q < 4 ? ahead[q] : nl[q];
               const uint32_t* v = sv + 4 * q;
               float x0, x1, x2, x3;
               f2_split(f2_fma(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, f2_make(n.x, n.y)), x0, x1);
               f2_split(f2_fma(f2_make(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, f2_make(n.z, n.w)), x2, x3);
-              acc0 = f2_add(acc0, f2_make(ex2(x0), ex2(x1)));
-              acc1 = f2_add(acc1, f2_make(ex2(x2), ex2(x3)));
-            }
-          } else if (plain) {
-            const uint64_t ks = f2_make(k.ks, k.ks);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const float4 f = cr[q], n = nl[q];
-              const uint32_t* v = sv + 4 * q;
-              float x0, x1, x2, x3;
-              f2_split(f2_fma(f2_mul(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), ks), f2_make(f.x, f.y),
-                              f2_make(n.x, n.y)), x0, x1);
-              f2_split(f2_fma(f2_mul(f2_make(__uint_as_float(v[2]), __uint_as_float(v[3])), ks), f2_make(f.z, f.w),
-                              f2_make(n.z, n.w)), x2, x3);
-              acc0 = f2_add(acc0, f2_make(ex2(x0), ex2(x1)));
-              acc1 = f2_add(acc1, f2_make(ex2(x2), ex2(x3)));
+              acc = f2_add(acc, f2_add(f2_make(ex2(x0), ex2(x1)), f2_make(ex2(x2), ex2(x3))));
             }
           } else {
-            const uint64_t see = seen_bits<kVec>(p, geo, r, b, hk, k, u0);
+            // a row at a time: masked, or with factors of their own
+            const uint64_t see = plain ? ~0ull : seen_bits<kVec>(p, geo, r, b, hk, k, u0);
             if (__any_sync(0xffffffffu, see != 0)) {
-              float part[4] = {};
+              float part[2] = {};
 #pragma unroll
               for (int q = 0; q < 64; ++q) {
-                const float f = fac[h * kHalf + q], n = fac[kTileRows + h * kHalf + q], v = __uint_as_float(sv[q]);
+                const float f = one ? first.x : fac[h * kHalf + q], v = __uint_as_float(sv[q]);
                 // (a factor past fp32: a product that overflows is a score that does)
                 const float cc = f * k.ks;
-                const float e = ex2((isinf(cc) ? (v * f) * k.ks : v * cc) + n);
-                part[q & 3] += ((q < 32 ? static_cast<uint32_t>(see) : static_cast<uint32_t>(see >> 32)) >> (q & 31)) & 1u ? e : 0.f;
+                const float e = ex2((isinf(cc) ? (v * f) * k.ks : v * cc) + fac[kTileRows + h * kHalf + q]);
+                part[q & 1] += ((q < 32 ? static_cast<uint32_t>(see) : static_cast<uint32_t>(see >> 32)) >> (q & 31)) & 1u ? e : 0.f;
               }
-              acc0 = f2_make(part[0], part[1]);
-              acc1 = f2_make(part[2], part[3]);
+              acc = f2_make(part[0], part[1]);
             }
           }
           float x0, x1;
-          f2_split(f2_add(acc0, acc1), x0, x1);
+          f2_split(acc, x0, x1);
           sum += x0 + x1;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar.q_empty(st));  // the factors have been read
+        if (lane == 0) mbar_arrive(bar.c_empty(ci));
+        if (++ci == kFactorRing) ci = 0, ++cturn;
       }
       if (!ok) break;
 
@@ -599,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
         auto meet = [&]() {  // the four warps
           __syncwarp();
           if (lane == 0) mbar_arrive(bar.sums(w));
-          ok = __all_sync(0xffffffffu, cache_wait(bar.sums(w), syncs & 1, p.status));
+          ok = __all_sync(0xffffffffu, wait_for(bar.sums(w), syncs & 1, p.status));
           ++syncs;
           return ok;
         };
