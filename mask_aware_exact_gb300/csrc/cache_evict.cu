@@ -25,8 +25,6 @@ namespace fm {
 namespace {
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kClusterMost = 8;
 constexpr int kBins = 2048;
 constexpr int kPagesCached = 256;                                     // of a CTA, with their keys
@@ -35,12 +33,24 @@ constexpr int kPagesMost = FM_MAX_SEQLEN / kPage / kClusterMost;      // of a CT
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The int at the same shared-memory address in CTA `rank`, written before the last
+// cluster_sync. (Several of these are on their way at once: one takes 800 cycles.)
 __device__ __forceinline__ int of_cta(const int* at, int rank) {
   uint32_t remote;
   int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote));
   return v;
+}
+// Sum of it over the first n CTAs of the cluster.
+__device__ __forceinline__ int of_ctas(const int* at, int n) {
+  int v[kClusterMost];
+#pragma unroll
+  for (int r = 0; r < kClusterMost; ++r) v[r] = r < n ? of_cta(at, r) : 0;
+  int sum = 0;
+#pragma unroll
+  for (int r = 0; r < kClusterMost; ++r) sum += v[r];
+  return sum;
 }
 
 // Weights in an order of unsigned numbers: NaN below all others, -0 as +0.
@@ -72,19 +82,21 @@ __device__ __forceinline__ Kept kept_of(const EvictParams& p, int b, bool record
 
 struct SelectSmem {
   int hist[2][kBins];
-  int wsum[kSelWarps + 4];
+  int wsum[32 + 4];
   int found[2];   // bin, keys wanted of it
   int totals[2];  // keys equal to the last one, tokens kept, of this CTA
 };
 
-template <bool kCached>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams p, const int cluster) {
+// `most`: pages of a CTA that there is shared memory for.
+template <int kThreads, bool kCached>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p, const int cluster, const int most) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint8_t smem[];
   SelectSmem& sh = *reinterpret_cast<SelectSmem*>(smem);
   uint64_t* masks = reinterpret_cast<uint64_t*>(smem + (sizeof(SelectSmem) + 15) / 16 * 16);  // [pages]
-  uint64_t* equals = masks + (kCached ? kPagesCached : kPagesMost);
-  int* counts = reinterpret_cast<int*>(equals + (kCached ? kPagesCached : kPagesMost));
-  uint32_t* keys = reinterpret_cast<uint32_t*>(counts + (kCached ? kPagesCached : kPagesMost));  // kCached
+  uint64_t* equals = masks + most;
+  int* counts = reinterpret_cast<int*>(equals + most);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(counts + most);  // kCached
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x / cluster, rank = blockIdx.x - seg * cluster;
   const int b = seg / p.c.Hk, hk = seg - b * p.c.Hk;
@@ -103,34 +115,43 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     if (b == 0) *p.ticket = 0;
   }
 
-  // keys of page p0 + i: this lane's tokens lane and lane + 32
-  auto load_keys = [&](int i, uint32_t (&k)[2]) {
-    const int page = p.table[static_cast<size_t>(b) * p.max_pages + p0 + i];
+  // keys of a page: this lane's tokens lane and lane + 32
+  auto load_keys = [&](int page, uint32_t (&k)[2]) {
     k[0] = k[1] = 0u;
-    if (page < 0 || page >= p.c.pages) {
-      if (lane == 0) record_failure(p.status, kStatusPage, kSiteEvictPage);
-    } else {
+    if (page >= 0) {
       const float* at = p.weights + (static_cast<size_t>(page) * p.c.Hk + hk) * kPage + lane;
       k[0] = order_key(at[0]);
       k[1] = order_key(at[32]);
     }
+  };
+  auto page_of = [&](int i) {
+    const int page = p.table[static_cast<size_t>(b) * p.max_pages + p0 + i];
+    if (page >= 0 && page < p.c.pages) return page;
+    record_failure(p.status, kStatusPage, kSiteEvictPage);
+    return -1;
   };
   auto keys_of = [&](int i, uint32_t (&k)[2]) {
     if constexpr (kCached) {
       k[0] = keys[i * kPage + lane];
       k[1] = keys[i * kPage + lane + 32];
     } else {
-      load_keys(i, k);
+      load_keys(page_of(i), k);
     }
   };
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) sh.hist[0][i] = 0;
+  for (int i = tid; i < 2 * kBins; i += kThreads) sh.hist[0][i] = 0;
   if constexpr (kCached) {
-#pragma unroll 4
-    for (int i = warp; i < np; i += kSelWarps) {
-      uint32_t k[2];
-      load_keys(i, k);
-      keys[i * kPage + lane] = k[0];
-      keys[i * kPage + lane + 32] = k[1];
+    // a warp's pages, each looked up by a lane
+    for (int i0 = warp; i0 < np; i0 += 32 * kWarps) {
+      const int mine = i0 + lane * kWarps < np ? page_of(i0 + lane * kWarps) : -1;
+      const int n = min((np - i0 + kWarps - 1) / kWarps, 32);
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        uint32_t k[2];
+        load_keys(__shfl_sync(0xffffffffu, mine, j), k);
+        uint32_t* to = keys + (i0 + j * kWarps) * kPage + lane;
+        to[0] = k[0];
+        to[32] = k[1];
+      }
     }
   }
   __syncthreads();
@@ -145,10 +166,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
       int* hist = sh.hist[pass & 1];
       if (pass == 2) {
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
         __syncthreads();
       }
-      for (int i = warp; i < np; i += kSelWarps) {
+      for (int i = warp; i < np; i += kWarps) {
         uint32_t k[2];
         keys_of(i, k);
 #pragma unroll
@@ -158,24 +179,24 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         }
       }
       sync_all();
-      // this thread's two bins, from the top
-      int c[2] = {0, 0};
-      const int top = bins - 1 - 2 * tid;
-      if (top >= 1) {
-        for (int r = 0; r < cluster; ++r) {
-          c[0] += cluster == 1 ? hist[top] : of_cta(&hist[top], r);
-          c[1] += cluster == 1 ? hist[top - 1] : of_cta(&hist[top - 1], r);
-        }
+      // this thread's bins, from the top
+      constexpr int kMine = kBins / kThreads;
+      int c[kMine], sum = 0;
+      const int top = bins - 1 - kMine * tid;
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        c[x] = top < x ? 0 : cluster == 1 ? hist[top - x] : of_ctas(&hist[top - x], cluster);
+        sum += c[x];
       }
       int all;
-      const int above = block_before<kSelWarps>(c[0] + c[1], sh.wsum, all);
+      int above = block_before<kWarps>(sum, sh.wsum, all);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int a = above + (x ? c[0] : 0);
-        if (a < want && want <= a + c[x]) {
+      for (int x = 0; x < kMine; ++x) {
+        if (above < want && want <= above + c[x]) {
           sh.found[0] = top - x;
-          sh.found[1] = want - a;
+          sh.found[1] = want - above;
         }
+        above += c[x];
       }
       __syncthreads();
       prefix |= static_cast<uint32_t>(sh.found[0]) << shift;
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   }
 
   // masks of the pages: what is kept anyway, and what is equal to the last key
-  for (int i = warp; i < np; i += kSelWarps) {
+  for (int i = warp; i < np; i += kWarps) {
     uint32_t k[2], keep[2], same[2];
     keys_of(i, k);
 #pragma unroll
@@ -205,14 +226,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   }
   __syncthreads();
   // a thread's pages in a row: sums before them, of this CTA and of those before it
-  const int per = (np + kSelThreads - 1) / kSelThreads, i0 = min(tid * per, np), i1 = min(i0 + per, np);
+  const int per = (np + kThreads - 1) / kThreads, i0 = min(tid * per, np), i1 = min(i0 + per, np);
   auto sums_before = [&](int mine, int which) {
     int all;
-    int x = block_before<kSelWarps>(mine, sh.wsum, all);
+    int x = block_before<kWarps>(mine, sh.wsum, all);
     if (cluster > 1) {
       if (tid == 0) sh.totals[which] = all;
       cluster_sync();
-      for (int r = 0; r < rank; ++r) x += of_cta(&sh.totals[which], r);
+      x += of_ctas(&sh.totals[which], rank);
     }
     return x;
   };
@@ -245,7 +266,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   if (p.index != nullptr) {
     __syncthreads();
     int32_t* index = p.index + static_cast<size_t>(seg) * p.index_width;
-    for (int i = warp; i < np; i += kSelWarps) {
+    for (int i = warp; i < np; i += kWarps) {
       const uint64_t m = masks[i];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -292,23 +313,33 @@ __device__ __forceinline__ int scale_exponent9(float x) {
   return min(max(((u & 0x7fffffu) <= 0x600000u ? e - 8 : e - 7) + 9, kMinExp), 127);
 }
 
+// Source pages of a page to be written, from the one of its first token on.
+struct Window {
+  int before[kWindow + 1];
+  int table[kWindow];
+  uint64_t mask[kWindow];
+};
 struct MoveSmem {
   int base[kMoveThreads + 1];  // pages to be written before a thread's sequences
   int wsum[kMoveWarps + 4];
-  int before[kWindow + 1];
-  uint64_t mask[kWindow];
+  Window window[2];
   int token[kPage];            // where each slot's token is now
   int page[kPage];             // its page, -1: none
-  float kscale[kPage], vscale[kPage];
+  float kscale[kPage], vscale[kPage], weight[kPage];
   uint32_t vmax[4][kPage];
   float top[2][kPage];         // of each slot, K and V, times 2^-9
-  float weight[kPage];
   int exps[2];
   int job;
 };
 
+// A page to be written: page dp of sequence b, head hk.
+struct Move {
+  int b, hk, dp, pages, cnt;  // pages of the sequence before, tokens of this page
+  size_t row;                 // segment * max_pages
+};
+
 template <int D, bool kInPlace>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p) {
   __shared__ MoveSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hk = p.c.Hk;
@@ -329,215 +360,264 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   }
   int total;
   sh.base[tid] = block_before<kMoveWarps>(mine, sh.wsum, total);
-  if (tid == 0) sh.base[kMoveThreads] = total;
+  if (tid == 0) {
+    sh.base[kMoveThreads] = total;
+    if (kInPlace) sh.job = atomicAdd(p.ticket, 1);
+  }
+  __syncthreads();
   const long long jobs = static_cast<long long>(total) * Hk;
 
-  for (long long job = blockIdx.x;; job += gridDim.x) {
-    __syncthreads();  // the shared words of the page before have been read
-    if constexpr (kInPlace) {
-      if (tid == 0) sh.job = atomicAdd(p.ticket, 1);
-      __syncthreads();
-      job = static_cast<uint32_t>(sh.job);
-    }
-    if (job >= jobs) break;
-    // which page: sequence, page of it, head
-    const int unit = static_cast<int>(job / Hk), hk = static_cast<int>(job - static_cast<long long>(unit) * Hk);
+  auto locate = [&](long long job) {
+    Move m;
+    const int unit = static_cast<int>(job / Hk);
+    m.hk = static_cast<int>(job - static_cast<long long>(unit) * Hk);
     int lo = 0, hi = kMoveThreads;  // base[lo] <= unit < base[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sh.base[mid] <= unit) lo = mid; else hi = mid;
     }
-    int b = lo * per, dp = unit - sh.base[lo];
-    for (int n; dp >= (n = pages_of_seq(b)); ++b) dp -= n;
-    const int seg = b * Hk + hk, len = p.info[2 * b], kept = p.info[2 * b + 1];
-    const int pages = (len + kPage - 1) / kPage, r0 = dp * kPage, cnt = min(kPage, kept - r0);
-    const size_t row = static_cast<size_t>(seg) * p.max_pages;
-    const int32_t* before = p.before + static_cast<size_t>(seg) * (p.max_pages + 1);
-    const int32_t* table = p.table + static_cast<size_t>(b) * p.max_pages;
-
-    // where the slots' tokens are
-    for (int s = p.first[row + dp];; s += kWindow) {
-      const int n = min(kWindow, pages - s);
-      if (tid < n) {
-        sh.before[tid] = before[s + tid];
-        sh.mask[tid] = p.mask[row + s + tid];
-      }
-      if (tid == 0) sh.before[n] = before[s + n];
-      __syncthreads();
-      const int have = sh.before[n];
-      if (tid < cnt) {
-        const int r = r0 + tid;
-        if (r >= sh.before[0] && r < have) {
-          int l = 0, h = n;  // before[l] <= r < before[h]
-          while (h - l > 1) {
-            const int mid = (l + h) >> 1;
-            if (sh.before[mid] <= r) l = mid; else h = mid;
-          }
-          // the k-th token kept of that page
-          int k = r - sh.before[l], bit = 0;
-          uint64_t m = sh.mask[l];
-#pragma unroll
-          for (int w = 32; w > 0; w >>= 1) {
-            const int c = __popcll(m & ((1ull << w) - 1ull));
-            if (k >= c) k -= c, bit += w, m >>= w;
-          }
-          sh.token[tid] = (s + l) * kPage + bit;
-        }
-      }
-      __syncthreads();
-      if (have >= r0 + cnt || s + n >= pages) break;
+    m.b = lo * per;
+    m.dp = unit - sh.base[lo];
+    for (int n; m.dp >= (n = pages_of_seq(m.b)); ++m.b) m.dp -= n;
+    m.pages = (p.info[2 * m.b] + kPage - 1) / kPage;
+    m.cnt = min(kPage, p.info[2 * m.b + 1] - m.dp * kPage);
+    m.row = (static_cast<size_t>(m.b) * Hk + m.hk) * p.max_pages;
+    return m;
+  };
+  auto before_of = [&](const Move& m) { return p.before + (m.row + static_cast<size_t>(m.b) * Hk + m.hk); };
+  // this thread's part of the window from page s on
+  struct Part {
+    int before, end, table;
+    uint64_t mask;
+  };
+  auto load_part = [&](const Move& m, int s) {
+    Part x = {};
+    const int n = min(kWindow, m.pages - s);
+    if (tid < n) {
+      x.before = before_of(m)[s + tid];
+      x.mask = p.mask[m.row + s + tid];
+      x.table = p.table[static_cast<size_t>(m.b) * p.max_pages + s + tid];
     }
-    bool moved = false;
-    if (tid < kPage) {
-      int page = -1;
-      float ks = 0.f, vs = 0.f;
-      if (tid < cnt) {
-        moved = !kInPlace || sh.token[tid] != r0 + tid;
-        page = table[sh.token[tid] / kPage];
+    if (tid == 0) x.end = before_of(m)[s + n];
+    return x;
+  };
+  auto store_part = [&](const Move& m, int s, const Part& x, Window& w) {
+    const int n = min(kWindow, m.pages - s);
+    if (tid < n) {
+      w.before[tid] = x.before;
+      w.mask[tid] = x.mask;
+      w.table[tid] = x.table;
+    }
+    if (tid == 0) w.before[n] = x.end;
+  };
+
+  long long job = kInPlace ? static_cast<long long>(static_cast<uint32_t>(sh.job)) : blockIdx.x;
+  if (job >= jobs) return;
+  Move m = locate(job);
+  int s = p.first[m.row + m.dp], cur = 0;
+  store_part(m, s, load_part(m, s), sh.window[0]);
+  while (true) {
+    __syncthreads();  // the window is there, and the shared words of the page before have been read
+    if (kInPlace && tid == 0) sh.job = atomicAdd(p.ticket, 1);
+    // where the slots' tokens are
+    const int r0 = m.dp * kPage;
+    int found = -1, page = -1;
+    while (true) {
+      const Window& w = sh.window[cur];
+      const int n = min(kWindow, m.pages - s), have = w.before[n];
+      if (tid < m.cnt && found < 0 && r0 + tid >= w.before[0] && r0 + tid < have) {
+        const int r = r0 + tid;
+        int l = 0, h = n;  // before[l] <= r < before[h]
+        while (h - l > 1) {
+          const int mid = (l + h) >> 1;
+          if (w.before[mid] <= r) l = mid; else h = mid;
+        }
+        // the k-th token kept of that page
+        int k = r - w.before[l], bit = 0;
+        uint64_t x = w.mask[l];
+#pragma unroll
+        for (int v = 32; v > 0; v >>= 1) {
+          const int c = __popcll(x & ((1ull << v) - 1ull));
+          if (k >= c) k -= c, bit += v, x >>= v;
+        }
+        found = (s + l) * kPage + bit;
+        page = w.table[l];
         if (page < 0 || page >= p.c.pages) {
           record_failure(p.status, kStatusPage, kSiteEvictPage);
           page = -1;
-        } else {
-          const size_t ph = static_cast<size_t>(page) * Hk + hk;
-          ks = p.c.kscale[ph];
-          vs = p.c.vscale[ph];
         }
+      }
+      if (have >= r0 + m.cnt || s + n >= m.pages) break;
+      s += n;  // few are kept: further pages
+      __syncthreads();
+      store_part(m, s, load_part(m, s), sh.window[cur]);
+      __syncthreads();
+    }
+    float slot_ks = 0.f, slot_vs = 0.f, slot_w = 0.f;
+    if (tid < kPage) {
+      if (page >= 0) {
+        const size_t ph = static_cast<size_t>(page) * Hk + m.hk;
+        slot_ks = p.c.kscale[ph];
+        slot_vs = p.c.vscale[ph];
+        slot_w = p.weights[ph * kPage + found % kPage];
       }
       sh.page[tid] = page;
-      sh.kscale[tid] = ks;
-      sh.vscale[tid] = vs;
+      sh.token[tid] = found;
     }
-    if (!__syncthreads_or(moved)) continue;  // every token stays where it is
+    // in place, a page whose tokens all stay is left alone
+    const bool moved = __syncthreads_or(tid < m.cnt && (!kInPlace || found != r0 + tid));
 
     // K: a thread has a quarter of a slot's row; V: a slot's rows q, q + 4, ..
-    uint4 kr[D / 64];
     const int ks_slot = tid >> 2, kq = tid & 3;
     const int vslot = lane + 32 * (warp & 1), vq = warp >> 1;
-    {
-      const int page = sh.page[ks_slot];
-      const uint8_t* src = p.c.k8 + (static_cast<size_t>(max(page, 0)) * Hk + hk) * (kPage * D) +
-                           (page < 0 ? 0 : sh.token[ks_slot] % kPage) * D + 16 * kq;
+    uint4 kr[D / 64];
+    uint32_t vr[D / 16];
+    if (moved) {
+      const int kp = sh.page[ks_slot], vp = sh.page[vslot];
+      const uint8_t* src = p.c.k8 + (static_cast<size_t>(max(kp, 0)) * Hk + m.hk) * (kPage * D) +
+                           (kp < 0 ? 0 : sh.token[ks_slot] % kPage) * D + 16 * kq;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
-        kr[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 64 * i);
+        kr[i] = kp < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 64 * i);
+      src = p.c.v8 + (static_cast<size_t>(max(vp, 0)) * Hk + m.hk) * (kPage * D) + (vp < 0 ? 0 : sh.token[vslot] % kPage) +
+            vq * kPage;
+      uint8_t v[D / 4];
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) v[i] = vp < 0 ? 0 : src[4 * i * kPage];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        vr[i] = v[4 * i] | static_cast<uint32_t>(v[4 * i + 1]) << 8 | static_cast<uint32_t>(v[4 * i + 2]) << 16 |
+                static_cast<uint32_t>(v[4 * i + 3]) << 24;
     }
-    uint32_t vr[D / 16];
-    {
-      const int page = sh.page[vslot];
-      const uint8_t* src = p.c.v8 + (static_cast<size_t>(max(page, 0)) * Hk + hk) * (kPage * D) +
-                           (page < 0 ? 0 : sh.token[vslot] % kPage) + vq * kPage;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        vr[i] = 0u;
-        if (page >= 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) vr[i] |= static_cast<uint32_t>(src[(16 * i + 4 * j) * kPage]) << (8 * j);
-        }
+    // the next page to be written: its first token's page is on its way, then its window
+    const long long next = kInPlace ? static_cast<long long>(static_cast<uint32_t>(sh.job)) : job + gridDim.x;
+    Move m2 = {};
+    int s2 = 0;
+    if (next < jobs) {
+      m2 = locate(next);
+      s2 = p.first[m2.row + m2.dp];
+    }
+    if (moved) {
+      if (tid < kPage) {
+        sh.kscale[tid] = slot_ks;
+        sh.vscale[tid] = slot_vs;
+        sh.weight[tid] = slot_w;
       }
+      // largest codes
+      uint32_t km = 0, vm = 0;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        km = __vmaxu4(km, __vmaxu4(__vmaxu4(magnitudes(kr[i].x), magnitudes(kr[i].y)),
+                                   __vmaxu4(magnitudes(kr[i].z), magnitudes(kr[i].w))));
+      km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 1));
+      km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 2));
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) vm = __vmaxu4(vm, magnitudes(vr[i]));
+      auto widest = [](uint32_t x) { return max(max(x & 0xffu, x >> 8 & 0xffu), max(x >> 16 & 0xffu, x >> 24)); };
+      if (kq == 0) sh.top[0][ks_slot] = code_value(widest(km));
+      sh.vmax[vq][vslot] = widest(vm);
     }
-    if (tid < kPage)
-      sh.weight[tid] = tid < cnt && sh.page[tid] >= 0
-                           ? p.weights[(static_cast<size_t>(sh.page[tid]) * Hk + hk) * kPage + sh.token[tid] % kPage]
-                           : 0.f;
-
-    // largest magnitudes
-    uint32_t km = 0, vm = 0;
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i)
-      km = __vmaxu4(km, __vmaxu4(__vmaxu4(magnitudes(kr[i].x), magnitudes(kr[i].y)),
-                                 __vmaxu4(magnitudes(kr[i].z), magnitudes(kr[i].w))));
-    km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 1));
-    km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 2));
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) vm = __vmaxu4(vm, magnitudes(vr[i]));
-    auto widest = [](uint32_t m) { return max(max(m & 0xffu, m >> 8 & 0xffu), max(m >> 16 & 0xffu, m >> 24)); };
-    const bool kbad = no_scales(sh.kscale[ks_slot], sh.vscale[ks_slot]), vbad = no_scales(sh.kscale[vslot], sh.vscale[vslot]);
-    if (kq == 0) sh.top[0][ks_slot] = kbad ? 0.f : code_value(widest(km)) * (sh.kscale[ks_slot] * 0x1p-9f);
-    sh.vmax[vq][vslot] = widest(vm);
+    Part part = {};
+    if (next < jobs) part = load_part(m2, s2);
     __syncthreads();  // all of the page's tokens have been read
-    if (kInPlace && tid == 0) {
-      asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p.was_read + row + dp), "r"(1)
-                   : "memory");
-    }
-    if (warp < 2) {
-      float top = 0.f;
+    if (moved) {
+      if (kInPlace && tid == 0)
+        asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p.was_read + m.row + m.dp), "r"(1)
+                     : "memory");
+      if (warp < 2) {
+        // the largest magnitudes, times 2^-9, of the slots whose scales are some
+        float top = 0.f;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int s = lane + 32 * x;
-        if (warp == 0) {
-          top = fmaxf(top, sh.top[0][s]);
-        } else if (!no_scales(sh.kscale[s], sh.vscale[s])) {
-          const uint32_t m = max(max(sh.vmax[0][s], sh.vmax[1][s]), max(sh.vmax[2][s], sh.vmax[3][s]));
-          top = fmaxf(top, code_value(m) * (sh.vscale[s] * 0x1p-9f));
+        for (int x = 0; x < 2; ++x) {
+          const int i = lane + 32 * x;
+          if (no_scales(sh.kscale[i], sh.vscale[i])) continue;
+          if (warp == 0) {
+            top = fmaxf(top, sh.top[0][i] * (sh.kscale[i] * 0x1p-9f));
+          } else {
+            const uint32_t c = max(max(sh.vmax[0][i], sh.vmax[1][i]), max(sh.vmax[2][i], sh.vmax[3][i]));
+            top = fmaxf(top, code_value(c) * (sh.vscale[i] * 0x1p-9f));
+          }
         }
+        // (not negative: ordered like their bits)
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (lane == 0) sh.exps[warp] = scale_exponent9(__uint_as_float(bits));
       }
-      // (not negative: ordered like their bits)
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) sh.exps[warp] = scale_exponent9(__uint_as_float(bits));
-    }
-    bool ok = true;
-    if constexpr (kInPlace) {
-      // tokens of the page to be overwritten go to at most two pages
-      if (tid >= 64 && tid < 66) {
-        const int a = before[min(dp, pages)], z = before[min(dp + 1, pages)];
-        const int reader = tid == 64 ? a / kPage : (z - 1) / kPage;
-        if (z > a && reader != dp) {
-          const int32_t* flag = p.was_read + row + reader;
-          const uint64_t t0 = global_timer_ns();
-          while (true) {
-            int v;
-            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-            if (v != 0) break;
-            if ((*reinterpret_cast<volatile int32_t*>(p.status) & kStatusTimeout) != 0 ||
-                global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
-              record_failure(p.status, kStatusTimeout, kSiteEvictWait);
-              ok = false;
-              break;
+      bool ok = true;
+      if constexpr (kInPlace) {
+        // tokens of the page to be overwritten go to at most two pages
+        if (tid >= 64 && tid < 66) {
+          const int a = before_of(m)[min(m.dp, m.pages)], z = before_of(m)[min(m.dp + 1, m.pages)];
+          const int reader = tid == 64 ? a / kPage : (z - 1) / kPage;
+          if (z > a && reader != m.dp) {
+            const int32_t* flag = p.was_read + m.row + reader;
+            const uint64_t t0 = global_timer_ns();
+            while (true) {
+              int v;
+              asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+              if (v != 0) break;
+              if ((*reinterpret_cast<volatile int32_t*>(p.status) & kStatusTimeout) != 0 ||
+                  global_timer_ns() - t0 > FM_WAIT_LIMIT_NS) {
+                record_failure(p.status, kStatusTimeout, kSiteEvictWait);
+                ok = false;
+                break;
+              }
             }
           }
         }
       }
-    }
-    ok = __syncthreads_and(ok);
-    if (!ok) return;
-    if (dp >= out_pages) continue;
-    const int to = out_table[static_cast<size_t>(b) * out_pages + dp];
-    if (to < 0 || to >= p.c.pages) {
-      if (tid == 0) record_failure(p.status, kStatusPage, kSiteEvictPage);
-      continue;
-    }
-    const size_t ph = static_cast<size_t>(to) * Hk + hk;
-    const float k_new = __int_as_float((sh.exps[0] + 127) << 23), v_new = __int_as_float((sh.exps[1] + 127) << 23);
-    {
-      const float f = sh.kscale[ks_slot] / k_new;
-      uint8_t* dst = p.c.k8 + ph * (kPage * D) + ks_slot * D + 16 * kq;
+      ok = __syncthreads_and(ok);
+      if (!ok) return;
+      int to = -1;
+      if (m.dp < out_pages) {
+        to = out_table[static_cast<size_t>(m.b) * out_pages + m.dp];
+        if (to < 0 || to >= p.c.pages) {
+          if (tid == 0) record_failure(p.status, kStatusPage, kSiteEvictPage);
+          to = -1;
+        }
+      }
+      if (to >= 0) {
+        const size_t ph = static_cast<size_t>(to) * Hk + m.hk;
+        const float k_new = __int_as_float((sh.exps[0] + 127) << 23), v_new = __int_as_float((sh.exps[1] + 127) << 23);
+        {
+          const float f = sh.kscale[ks_slot] / k_new;
+          const bool bad = no_scales(sh.kscale[ks_slot], sh.vscale[ks_slot]);
+          uint8_t* dst = p.c.k8 + ph * (kPage * D) + ks_slot * D + 16 * kq;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const uint32_t nan = 0x7f7f7f7fu;
-        uint4 o = kr[i];
-        if (kbad)
-          o = make_uint4(nan, nan, nan, nan);
-        else if (f != 1.f)
-          o = make_uint4(codes_times(o.x, f), codes_times(o.y, f), codes_times(o.z, f), codes_times(o.w, f));
-        *reinterpret_cast<uint4*>(dst + 64 * i) = o;
+          for (int i = 0; i < D / 64; ++i) {
+            const uint32_t nan = 0x7f7f7f7fu;
+            uint4 o = kr[i];
+            if (bad)
+              o = make_uint4(nan, nan, nan, nan);
+            else if (f != 1.f)
+              o = make_uint4(codes_times(o.x, f), codes_times(o.y, f), codes_times(o.z, f), codes_times(o.w, f));
+            *reinterpret_cast<uint4*>(dst + 64 * i) = o;
+          }
+        }
+        {
+          const float f = sh.vscale[vslot] / v_new;
+          const bool bad = no_scales(sh.kscale[vslot], sh.vscale[vslot]);
+          uint8_t* dst = p.c.v8 + ph * (kPage * D) + vslot + vq * kPage;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o = bad ? 0u : f != 1.f ? codes_times(vr[i], f) : vr[i];
+            o &= ~__vcmpeq4(o & 0x7f7f7f7fu, 0x7f7f7f7fu);  // V holds no NaN
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[(16 * i + 4 * j) * kPage] = static_cast<uint8_t>(o >> (8 * j));
+          }
+        }
+        if (tid < kPage) p.weights[ph * kPage + tid] = sh.weight[tid];
+        if (tid == 0) {
+          p.c.kscale[ph] = k_new;
+          p.c.vscale[ph] = v_new;
+        }
       }
     }
-    {
-      const float f = sh.vscale[vslot] / v_new;
-      uint8_t* dst = p.c.v8 + ph * (kPage * D) + vslot + vq * kPage;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t o = vbad ? 0u : f != 1.f ? codes_times(vr[i], f) : vr[i];
-        o &= ~__vcmpeq4(o & 0x7f7f7f7fu, 0x7f7f7f7fu);  // V holds no NaN
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dst[(16 * i + 4 * j) * kPage] = static_cast<uint8_t>(o >> (8 * j));
-      }
-    }
-    if (tid < kPage) p.weights[ph * kPage + tid] = sh.weight[tid];
-    if (tid == 0) {
-      p.c.kscale[ph] = k_new;
-      p.c.vscale[ph] = v_new;
-    }
+    if (next >= jobs) break;
+    cur ^= 1;
+    store_part(m2, s2, part, sh.window[cur]);
+    m = m2;
+    s = s2;
+    job = next;
   }
 }
 
@@ -553,18 +633,22 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>* done) {
   return e;
 }
 
-template <bool kCached>
+template <int kThreads, bool kCached>
 cudaError_t launch_select(const EvictParams& p, int cluster, cudaStream_t s) {
-  constexpr int kPages = kCached ? kPagesCached : kPagesMost;
-  constexpr int kBytes = (sizeof(SelectSmem) + 15) / 16 * 16 + kPages * (8 + 8 + 4) + (kCached ? kPages * kPage * 4 : 0);
-  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+  // shared memory for the pages that a CTA may have
+  const int most = ((p.max_pages + cluster - 1) / cluster + 1) / 2 * 2;
+  auto bytes = [](int pages) {
+    return static_cast<int>((sizeof(SelectSmem) + 15) / 16 * 16) + pages * (8 + 8 + 4) + (kCached ? pages * kPage * 4 : 0);
+  };
+  static_assert(sizeof(SelectSmem) + kPagesCached * (20 + kPage * 4) <= 227 * 1024 && sizeof(SelectSmem) + kPagesMost * 20 <= 227 * 1024,
+                "shared memory per CTA");
   static std::atomic<uint64_t> done[4];
-  const cudaError_t e = allow_smem(evict_select_kernel<kCached>, kBytes, done);
+  const cudaError_t e = allow_smem(evict_select_kernel<kThreads, kCached>, bytes(kCached ? kPagesCached : kPagesMost), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.c.Hk * cluster);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = kBytes;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes(most);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -572,7 +656,7 @@ cudaError_t launch_select(const EvictParams& p, int cluster, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kCached>, p, cluster);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads, kCached>, p, cluster, most);
 }
 
 template <int D>
@@ -613,8 +697,13 @@ EvictWs evict_ws_layout(int B, int Hk, int max_pages) {
 cudaError_t launch_cache_evict(int d, const EvictParams& p, int num_sms, cudaStream_t s) {
   int cluster = 1;
   while (cluster < kClusterMost && cluster * kPagesCached < p.max_pages) cluster *= 2;
-  const cudaError_t e = cluster * kPagesCached >= p.max_pages ? launch_select<true>(p, cluster, s)
-                                                              : launch_select<false>(p, cluster, s);
+  // small CTAs where there are several for each SM, which hide one another's barriers
+  const bool many = static_cast<long long>(p.B) * p.c.Hk * cluster > 2LL * num_sms;
+  cudaError_t e;
+  if (cluster * kPagesCached < p.max_pages)
+    e = launch_select<1024, false>(p, cluster, s);
+  else
+    e = many ? launch_select<256, true>(p, cluster, s) : launch_select<1024, true>(p, cluster, s);
   if (e != cudaSuccess) return e;
   return d == 64 ? launch_move<64>(p, num_sms, s) : launch_move<128>(p, num_sms, s);
 }
