@@ -176,17 +176,20 @@ struct EvictParams {
   int B;
   int32_t* status;
   // workspace (see EvictWs); a segment is a (sequence, cache head)
-  int32_t* ticket;   // next page to be written
+  int32_t* count;    // pages to be written (this and the next two are 0 between calls)
+  int32_t* ticket;   // next of them, in place
+  int32_t* done;     // CTAs that are through
   int32_t* info;     // [B][2]: tokens, tokens kept
   uint64_t* mask;    // [segments][max_pages]: kept tokens of a page
   int32_t* before;   // [segments][max_pages + 1]: tokens kept before a page
-  int32_t* first;    // [segments][max_pages]: page of the first token of a page to be written
+  int2* list;        // pages to be written: segment, page << 16 | page of its first token
   int32_t* was_read; // [segments][max_pages]: whether the tokens of a page to be written are read
+  Divisor by_Hk;
 };
 struct EvictWs {
-  size_t ticket, info, mask, before, first, was_read, total;
+  size_t counters, info, mask, before, list, was_read, total;
 };
 EvictWs evict_ws_layout(int B, int Hk, int max_pages);
-cudaError_t launch_cache_evict(int d, const EvictParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_cache_evict(int d, EvictParams p, int num_sms, cudaStream_t s);
 
 }  // namespace fm

@@ -377,11 +377,13 @@ fm_status flashmask_cache_evict(const fm_cache* cache, const int32_t* page_table
   p.B = B;
   char* w = static_cast<char*>(ws);
   p.status = reinterpret_cast<int32_t*>(w);
-  p.ticket = reinterpret_cast<int32_t*>(w + L.ticket);
+  p.count = reinterpret_cast<int32_t*>(w + L.counters);
+  p.ticket = p.count + 1;
+  p.done = p.count + 2;
   p.info = reinterpret_cast<int32_t*>(w + L.info);
   p.mask = reinterpret_cast<uint64_t*>(w + L.mask);
   p.before = reinterpret_cast<int32_t*>(w + L.before);
-  p.first = reinterpret_cast<int32_t*>(w + L.first);
+  p.list = reinterpret_cast<int2*>(w + L.list);
   p.was_read = reinterpret_cast<int32_t*>(w + L.was_read);
   const int sms = sm_count();
   if (sms <= 0) return FM_ERR_CUDA;

@@ -85,6 +85,7 @@ struct SelectSmem {
   int wsum[32 + 4];
   int found[2];   // bin, keys wanted of it
   int totals[2];  // keys equal to the last one, tokens kept, of this CTA
+  int place;      // of the segment's pages in the list of pages to be written (rank 0)
 };
 
 // `most`: pages of a CTA that there is shared memory for.
@@ -109,10 +110,12 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     else
       cluster_sync();
   };
-  if (tid == 0 && rank == 0 && hk == 0) {
-    p.info[2 * b] = kp.len;
-    p.info[2 * b + 1] = kp.n;
-    if (b == 0) *p.ticket = 0;
+  if (tid == 0 && rank == 0) {
+    sh.place = atomicAdd(p.count, (kp.n + kPage - 1) / kPage);
+    if (hk == 0) {
+      p.info[2 * b] = kp.len;
+      p.info[2 * b + 1] = kp.n;
+    }
   }
 
   // keys of a page: this lane's tokens lane and lane + 32
@@ -253,12 +256,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
   int at = sums_before(mine, 1);
   const size_t row = static_cast<size_t>(seg) * p.max_pages;
   int32_t* before = p.before + static_cast<size_t>(seg) * (p.max_pages + 1);
+  const int place = cluster == 1 ? sh.place : of_cta(&sh.place, 0);
   for (int i = i0; i < i1; ++i) {
     const int n = __popcll(masks[i]), to = (at + kPage - 1) / kPage;
     p.mask[row + p0 + i] = masks[i];
     before[p0 + i] = at;
     p.was_read[row + p0 + i] = 0;
-    if (n > 0 && to * kPage < at + n) p.first[row + to] = p0 + i;
+    if (n > 0 && to * kPage < at + n) p.list[place + to] = make_int2(seg, to << 16 | (p0 + i));
     counts[i] = at;
     at += n;
   }
@@ -284,13 +288,13 @@ constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kWindow = kMoveThreads;  // source pages looked at a time
 constexpr int kMinExp = -100;
 
-__device__ __forceinline__ uint32_t codes_times(uint32_t w, float f) {
+__device__ __forceinline__ uint32_t codes_times(uint32_t w, float f0, float f1, float f2, float f3) {
   uint32_t lo, hi;
   codes_to_f16(w, lo, hi);
   float v[4];
   asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[0]), "=f"(v[1]) : "r"(lo));
   asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[2]), "=f"(v[3]) : "r"(hi));
-  return pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+  return pack_e4m3x4(v[0] * f0, v[1] * f1, v[2] * f2, v[3] * f3);
 }
 // Magnitudes of four codes; 0 for a NaN.
 __device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
@@ -320,71 +324,53 @@ struct Window {
   uint64_t mask[kWindow];
 };
 struct MoveSmem {
-  int base[kMoveThreads + 1];  // pages to be written before a thread's sequences
-  int wsum[kMoveWarps + 4];
   Window window[2];
   int token[kPage];            // where each slot's token is now
   int page[kPage];             // its page, -1: none
   float kscale[kPage], vscale[kPage], weight[kPage];
-  uint32_t vmax[4][kPage];
-  float top[2][kPage];         // of each slot, K and V, times 2^-9
+  uint32_t vmax[kMoveWarps][kPage / 4];  // largest V codes of four slots each
+  float top[kPage];            // largest K code of each slot
   int exps[2];
   int job;
 };
 
-// A page to be written: page dp of sequence b, head hk.
+// A page to be written: page dp of sequence b, head hk; its first token is in page s.
 struct Move {
-  int b, hk, dp, pages, cnt;  // pages of the sequence before, tokens of this page
-  size_t row;                 // segment * max_pages
+  int b, hk, dp, s;
+  int pages, cnt;  // pages of the sequence before, tokens of this page
+  int seg;
 };
 
 template <int D, bool kInPlace>
-__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ MoveSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hk = p.c.Hk;
   const int32_t* out_table = kInPlace ? p.table : p.out_table;
   const int out_pages = kInPlace ? p.max_pages : p.out_pages;
-
-  // the line of pages to be written: a sequence's pages in order, its heads side by side
-  const int per = (p.B + kMoveThreads - 1) / kMoveThreads;
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  auto pages_of_seq = [&](int b) { return (p.info[2 * b + 1] + kPage - 1) / kPage; };
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    mine += pages_of_seq(b);
-    if (blockIdx.x == 0) {
-      p.new_lens[b] = p.info[2 * b + 1];
-      if (!kInPlace && pages_of_seq(b) > out_pages) record_failure(p.status, kStatusPage, kSiteEvictRange);
+  const uint32_t jobs = static_cast<uint32_t>(*p.count);  // (written by the kernel before)
+  if (blockIdx.x == 0) {
+    for (int b = tid; b < p.B; b += kMoveThreads) {
+      const int n = p.info[2 * b + 1];
+      p.new_lens[b] = n;
+      if (!kInPlace && (n + kPage - 1) / kPage > out_pages) record_failure(p.status, kStatusPage, kSiteEvictRange);
     }
   }
-  int total;
-  sh.base[tid] = block_before<kMoveWarps>(mine, sh.wsum, total);
-  if (tid == 0) {
-    sh.base[kMoveThreads] = total;
-    if (kInPlace) sh.job = atomicAdd(p.ticket, 1);
-  }
-  __syncthreads();
-  const long long jobs = static_cast<long long>(total) * Hk;
 
-  auto locate = [&](long long job) {
+  auto locate = [&](const int2& e) {
     Move m;
-    const int unit = static_cast<int>(job / Hk);
-    m.hk = static_cast<int>(job - static_cast<long long>(unit) * Hk);
-    int lo = 0, hi = kMoveThreads;  // base[lo] <= unit < base[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sh.base[mid] <= unit) lo = mid; else hi = mid;
-    }
-    m.b = lo * per;
-    m.dp = unit - sh.base[lo];
-    for (int n; m.dp >= (n = pages_of_seq(m.b)); ++m.b) m.dp -= n;
-    m.pages = (p.info[2 * m.b] + kPage - 1) / kPage;
-    m.cnt = min(kPage, p.info[2 * m.b + 1] - m.dp * kPage);
-    m.row = (static_cast<size_t>(m.b) * Hk + m.hk) * p.max_pages;
+    m.seg = e.x;
+    m.b = p.by_Hk.div(e.x);
+    m.hk = e.x - m.b * Hk;
+    m.dp = e.y >> 16;
+    m.s = e.y & 0xffff;
+    const int2 info = reinterpret_cast<const int2*>(p.info)[m.b];
+    m.pages = (info.x + kPage - 1) / kPage;
+    m.cnt = min(kPage, info.y - m.dp * kPage);
     return m;
   };
-  auto before_of = [&](const Move& m) { return p.before + (m.row + static_cast<size_t>(m.b) * Hk + m.hk); };
+  auto row_of = [&](const Move& m) { return static_cast<size_t>(m.seg) * p.max_pages; };
+  auto before_of = [&](const Move& m) { return p.before + static_cast<size_t>(m.seg) * (p.max_pages + 1); };
   // this thread's part of the window from page s on
   struct Part {
     int before, end, table;
@@ -395,7 +381,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     const int n = min(kWindow, m.pages - s);
     if (tid < n) {
       x.before = before_of(m)[s + tid];
-      x.mask = p.mask[m.row + s + tid];
+      x.mask = p.mask[row_of(m) + s + tid];
       x.table = p.table[static_cast<size_t>(m.b) * p.max_pages + s + tid];
     }
     if (tid == 0) x.end = before_of(m)[s + n];
@@ -411,12 +397,20 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     if (tid == 0) w.before[n] = x.end;
   };
 
-  long long job = kInPlace ? static_cast<long long>(static_cast<uint32_t>(sh.job)) : blockIdx.x;
-  if (job >= jobs) return;
-  Move m = locate(job);
-  int s = p.first[m.row + m.dp], cur = 0;
-  store_part(m, s, load_part(m, s), sh.window[0]);
-  while (true) {
+  uint32_t job = blockIdx.x;
+  if (kInPlace) {
+    if (tid == 0) sh.job = atomicAdd(p.ticket, 1);
+    __syncthreads();
+    job = static_cast<uint32_t>(sh.job);
+  }
+  Move m = {};
+  int s = 0, cur = 0;
+  if (job < jobs) {
+    m = locate(p.list[job]);
+    s = m.s;
+    store_part(m, s, load_part(m, s), sh.window[0]);
+  }
+  while (job < jobs) {
     __syncthreads();  // the window is there, and the shared words of the page before have been read
     if (kInPlace && tid == 0) sh.job = atomicAdd(p.ticket, 1);
     // where the slots' tokens are
@@ -459,7 +453,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
         const size_t ph = static_cast<size_t>(page) * Hk + m.hk;
         slot_ks = p.c.kscale[ph];
         slot_vs = p.c.vscale[ph];
-        slot_w = p.weights[ph * kPage + found % kPage];
+        slot_w = p.weights[ph * kPage + (found & (kPage - 1))];
       }
       sh.page[tid] = page;
       sh.token[tid] = found;
@@ -467,36 +461,36 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     // in place, a page whose tokens all stay is left alone
     const bool moved = __syncthreads_or(tid < m.cnt && (!kInPlace || found != r0 + tid));
 
-    // K: a thread has a quarter of a slot's row; V: a slot's rows q, q + 4, ..
+    // K: a thread has a quarter of a slot's row; V: four slots of the rows vrow, vrow + 16, ..
     const int ks_slot = tid >> 2, kq = tid & 3;
-    const int vslot = lane + 32 * (warp & 1), vq = warp >> 1;
+    const int vquad = tid & 15, vrow = tid >> 4;
     uint4 kr[D / 64];
     uint32_t vr[D / 16];
     if (moved) {
-      const int kp = sh.page[ks_slot], vp = sh.page[vslot];
+      const int kp = sh.page[ks_slot];
       const uint8_t* src = p.c.k8 + (static_cast<size_t>(max(kp, 0)) * Hk + m.hk) * (kPage * D) +
-                           (kp < 0 ? 0 : sh.token[ks_slot] % kPage) * D + 16 * kq;
+                           (sh.token[ks_slot] & (kPage - 1)) * D + 16 * kq;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
         kr[i] = kp < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 64 * i);
-      src = p.c.v8 + (static_cast<size_t>(max(vp, 0)) * Hk + m.hk) * (kPage * D) + (vp < 0 ? 0 : sh.token[vslot] % kPage) +
-            vq * kPage;
-      uint8_t v[D / 4];
 #pragma unroll
-      for (int i = 0; i < D / 4; ++i) v[i] = vp < 0 ? 0 : src[4 * i * kPage];
+      for (int i = 0; i < D / 16; ++i) vr[i] = 0u;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        vr[i] = v[4 * i] | static_cast<uint32_t>(v[4 * i + 1]) << 8 | static_cast<uint32_t>(v[4 * i + 2]) << 16 |
-                static_cast<uint32_t>(v[4 * i + 3]) << 24;
+      for (int j = 0; j < 4; ++j) {
+        const int vp = sh.page[4 * vquad + j];
+        if (vp < 0) continue;
+        src = p.c.v8 + (static_cast<size_t>(vp) * Hk + m.hk) * (kPage * D) + (sh.token[4 * vquad + j] & (kPage - 1)) + vrow * kPage;
+        uint8_t v[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) v[i] = src[16 * i * kPage];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) vr[i] |= static_cast<uint32_t>(v[i]) << (8 * j);
+      }
     }
     // the next page to be written: its first token's page is on its way, then its window
-    const long long next = kInPlace ? static_cast<long long>(static_cast<uint32_t>(sh.job)) : job + gridDim.x;
-    Move m2 = {};
-    int s2 = 0;
-    if (next < jobs) {
-      m2 = locate(next);
-      s2 = p.first[m2.row + m2.dp];
-    }
+    const uint32_t next = kInPlace ? static_cast<uint32_t>(sh.job) : job + gridDim.x;
+    int2 entry = make_int2(0, 0);
+    if (next < jobs) entry = p.list[next];
     if (moved) {
       if (tid < kPage) {
         sh.kscale[tid] = slot_ks;
@@ -513,16 +507,20 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
       km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 2));
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) vm = __vmaxu4(vm, magnitudes(vr[i]));
-      auto widest = [](uint32_t x) { return max(max(x & 0xffu, x >> 8 & 0xffu), max(x >> 16 & 0xffu, x >> 24)); };
-      if (kq == 0) sh.top[0][ks_slot] = code_value(widest(km));
-      sh.vmax[vq][vslot] = widest(vm);
+      vm = __vmaxu4(vm, __shfl_xor_sync(0xffffffffu, vm, 16));
+      if (kq == 0) sh.top[ks_slot] = code_value(max(max(km & 0xffu, km >> 8 & 0xffu), max(km >> 16 & 0xffu, km >> 24)));
+      if (lane < 16) sh.vmax[warp][vquad] = vm;
     }
+    Move m2 = {};
     Part part = {};
-    if (next < jobs) part = load_part(m2, s2);
+    if (next < jobs) {
+      m2 = locate(entry);
+      part = load_part(m2, m2.s);
+    }
     __syncthreads();  // all of the page's tokens have been read
     if (moved) {
       if (kInPlace && tid == 0)
-        asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p.was_read + m.row + m.dp), "r"(1)
+        asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p.was_read + row_of(m) + m.dp), "r"(1)
                      : "memory");
       if (warp < 2) {
         // the largest magnitudes, times 2^-9, of the slots whose scales are some
@@ -532,9 +530,11 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
           const int i = lane + 32 * x;
           if (no_scales(sh.kscale[i], sh.vscale[i])) continue;
           if (warp == 0) {
-            top = fmaxf(top, sh.top[0][i] * (sh.kscale[i] * 0x1p-9f));
+            top = fmaxf(top, sh.top[i] * (sh.kscale[i] * 0x1p-9f));
           } else {
-            const uint32_t c = max(max(sh.vmax[0][i], sh.vmax[1][i]), max(sh.vmax[2][i], sh.vmax[3][i]));
+            uint32_t c = 0;
+#pragma unroll
+            for (int k = 0; k < kMoveWarps; ++k) c = max(c, sh.vmax[k][i >> 2] >> (8 * (i & 3)) & 0xffu);
             top = fmaxf(top, code_value(c) * (sh.vscale[i] * 0x1p-9f));
           }
         }
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
           const int a = before_of(m)[min(m.dp, m.pages)], z = before_of(m)[min(m.dp + 1, m.pages)];
           const int reader = tid == 64 ? a / kPage : (z - 1) / kPage;
           if (z > a && reader != m.dp) {
-            const int32_t* flag = p.was_read + m.row + reader;
+            const int32_t* flag = p.was_read + row_of(m) + reader;
             const uint64_t t0 = global_timer_ns();
             while (true) {
               int v;
@@ -589,20 +589,28 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
             if (bad)
               o = make_uint4(nan, nan, nan, nan);
             else if (f != 1.f)
-              o = make_uint4(codes_times(o.x, f), codes_times(o.y, f), codes_times(o.z, f), codes_times(o.w, f));
+              o = make_uint4(codes_times(o.x, f, f, f, f), codes_times(o.y, f, f, f, f), codes_times(o.z, f, f, f, f),
+                             codes_times(o.w, f, f, f, f));
             *reinterpret_cast<uint4*>(dst + 64 * i) = o;
           }
         }
         {
-          const float f = sh.vscale[vslot] / v_new;
-          const bool bad = no_scales(sh.kscale[vslot], sh.vscale[vslot]);
-          uint8_t* dst = p.c.v8 + ph * (kPage * D) + vslot + vq * kPage;
+          float f[4];
+          uint32_t keep = 0;  // bytes of slots whose scales are some
+          bool same = true;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 4 * vquad + j;
+            f[j] = sh.vscale[i] / v_new;
+            keep |= no_scales(sh.kscale[i], sh.vscale[i]) ? 0u : 0xffu << (8 * j);
+            same = same && f[j] == 1.f;
+          }
+          uint8_t* dst = p.c.v8 + ph * (kPage * D) + 4 * vquad + vrow * kPage;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            uint32_t o = bad ? 0u : f != 1.f ? codes_times(vr[i], f) : vr[i];
-            o &= ~__vcmpeq4(o & 0x7f7f7f7fu, 0x7f7f7f7fu);  // V holds no NaN
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dst[(16 * i + 4 * j) * kPage] = static_cast<uint8_t>(o >> (8 * j));
+            uint32_t o = same ? vr[i] : codes_times(vr[i], f[0], f[1], f[2], f[3]);
+            o &= keep & ~__vcmpeq4(o & 0x7f7f7f7fu, 0x7f7f7f7fu);  // V holds no NaN
+            *reinterpret_cast<uint32_t*>(dst + 16 * i * kPage) = o;
           }
         }
         if (tid < kPage) p.weights[ph * kPage + tid] = sh.weight[tid];
@@ -612,12 +620,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
         }
       }
     }
+    job = next;
     if (next >= jobs) break;
     cur ^= 1;
-    store_part(m2, s2, part, sh.window[cur]);
     m = m2;
-    s = s2;
-    job = next;
+    s = m2.s;
+    store_part(m, s, part, sh.window[cur]);
+  }
+  // the last CTA leaves the counters as the next call wants them
+  if (tid == 0 && atomic_add_acq_rel(p.done, 1) == static_cast<int>(gridDim.x) - 1) {
+    *p.count = 0;
+    *p.ticket = 0;
+    *p.done = 0;
   }
 }
 
@@ -678,23 +692,24 @@ EvictWs evict_ws_layout(int B, int Hk, int max_pages) {
   const size_t segs = static_cast<size_t>(B) * Hk;
   EvictWs w;
   size_t off = 256;  // the status word
-  w.ticket = off;
-  off = up256(off + 4);
+  w.counters = off;  // (at the same place for all sizes: they have to be zero)
+  off = up256(off + 12);
   w.info = off;
   off = up256(off + static_cast<size_t>(B) * 8);
   w.mask = off;
   off = up256(off + segs * max_pages * 8);
   w.before = off;
   off = up256(off + segs * (max_pages + 1) * 4);
-  w.first = off;
-  off = up256(off + segs * max_pages * 4);
+  w.list = off;
+  off = up256(off + segs * max_pages * 8);
   w.was_read = off;
   off = up256(off + segs * max_pages * 4);
   w.total = off;
   return w;
 }
 
-cudaError_t launch_cache_evict(int d, const EvictParams& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_cache_evict(int d, EvictParams p, int num_sms, cudaStream_t s) {
+  p.by_Hk.set(p.c.Hk);
   int cluster = 1;
   while (cluster < kClusterMost && cluster * kPagesCached < p.max_pages) cluster *= 2;
   // small CTAs where there are several for each SM, which hide one another's barriers
