@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 
 // ---------------------------------------------------------------- pages
 constexpr int kMoveThreads = 256;
-constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kWindow = kMoveThreads;  // source pages looked at a time
 constexpr int kMinExp = -100;
 
@@ -296,11 +295,30 @@ __device__ __forceinline__ uint32_t codes_times(uint32_t w, float f0, float f1, 
   asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[2]), "=f"(v[3]) : "r"(hi));
   return pack_e4m3x4(v[0] * f0, v[1] * f1, v[2] * f2, v[3] * f3);
 }
-// Magnitudes of four codes; 0 for a NaN.
-__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
-  const uint32_t m = w & 0x7f7f7f7fu;
-  return m & ~__vcmpeq4(m, 0x7f7f7f7fu);
+// The same for powers of two from 2^-14 to 2^15, as fp16 pairs: the products are exact there.
+__device__ __forceinline__ uint32_t codes_times_f16(uint32_t w, uint32_t f01, uint32_t f23) {
+  uint32_t lo, hi, r;
+  codes_to_f16(w, lo, hi);
+  asm("{.reg .b32 x, y; .reg .b16 a, b; mul.rn.f16x2 x, %1, %3; mul.rn.f16x2 y, %2, %4; "
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, x; cvt.rn.satfinite.e4m3x2.f16x2 b, y; mov.b32 %0, {a, b};}"
+      : "=r"(r)
+      : "r"(lo), "r"(hi), "r"(f01), "r"(f23));
+  return r;
 }
+__device__ __forceinline__ bool plain_power(float f) {
+  return (__float_as_uint(f) & 0x7fffffu) == 0 && f >= 0x1p-14f && f <= 0x1p15f;
+}
+// Largest magnitudes of codes, kept as 16-bit pairs: the even bytes of words and the odd ones.
+struct Widest {
+  uint32_t even = 0, odd = 0;
+  __device__ __forceinline__ void add(uint32_t w) {
+    even = __vmaxu2(even, w & 0x007f007fu);
+    odd = __vmaxu2(odd, w >> 8 & 0x007f007fu);
+  }
+};
+constexpr uint32_t kNan = 0x7f;
+// Word without its NaN codes.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 __device__ __forceinline__ float code_value(uint32_t code) {
   uint32_t lo, hi;
   codes_to_f16(code & 0xffu, lo, hi);
@@ -328,7 +346,7 @@ struct MoveSmem {
   int token[kPage];            // where each slot's token is now
   int page[kPage];             // its page, -1: none
   float kscale[kPage], vscale[kPage], weight[kPage];
-  uint32_t vmax[kMoveWarps][kPage / 4];  // largest V codes of four slots each
+  uint32_t vmax[kMoveThreads / 16][kPage / 4];  // largest V codes of four slots each
   float top[kPage];            // largest K code of each slot
   int exps[2];
   int job;
@@ -484,7 +502,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) v[i] = src[16 * i * kPage];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) vr[i] |= static_cast<uint32_t>(v[i]) << (8 * j);
+        for (int i = 0; i < D / 16; ++i) vr[i] += static_cast<uint32_t>(v[i]) << (8 * j);
       }
     }
     // the next page to be written: its first token's page is on its way, then its window
@@ -497,19 +515,46 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
         sh.vscale[tid] = slot_vs;
         sh.weight[tid] = slot_w;
       }
-      // largest codes
-      uint32_t km = 0, vm = 0;
+      // largest codes: of K's slot over four threads, of V's four slots over two
+      Widest k, v;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-        km = __vmaxu4(km, __vmaxu4(__vmaxu4(magnitudes(kr[i].x), magnitudes(kr[i].y)),
-                                   __vmaxu4(magnitudes(kr[i].z), magnitudes(kr[i].w))));
-      km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 1));
-      km = __vmaxu4(km, __shfl_xor_sync(0xffffffffu, km, 2));
+      for (int i = 0; i < D / 64; ++i) {
+        k.add(kr[i].x);
+        k.add(kr[i].y);
+        k.add(kr[i].z);
+        k.add(kr[i].w);
+      }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) vm = __vmaxu4(vm, magnitudes(vr[i]));
-      vm = __vmaxu4(vm, __shfl_xor_sync(0xffffffffu, vm, 16));
-      if (kq == 0) sh.top[ks_slot] = code_value(max(max(km & 0xffu, km >> 8 & 0xffu), max(km >> 16 & 0xffu, km >> 24)));
-      if (lane < 16) sh.vmax[warp][vquad] = vm;
+      for (int i = 0; i < D / 16; ++i) v.add(vr[i]);
+      uint32_t kw = __vmaxu2(k.even, k.odd);
+      kw = max(kw & 0xffffu, kw >> 16);
+      // (rare: NaN codes do not count, and V keeps none)
+      if (__builtin_expect(__any_sync(0xffffffffu, kw == kNan), 0)) {
+        Widest x;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          x.add(without_nan(kr[i].x));
+          x.add(without_nan(kr[i].y));
+          x.add(without_nan(kr[i].z));
+          x.add(without_nan(kr[i].w));
+        }
+        kw = __vmaxu2(x.even, x.odd);
+        kw = max(kw & 0xffffu, kw >> 16);
+      }
+      uint32_t vw = v.even | v.odd << 8;
+      if (__builtin_expect(__any_sync(0xffffffffu, without_nan(vw) != vw), 0)) {
+        Widest x;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          vr[i] = without_nan(vr[i]);
+          x.add(vr[i]);
+        }
+        vw = x.even | x.odd << 8;
+      }
+      kw = max(kw, __shfl_xor_sync(0xffffffffu, kw, 1));
+      kw = max(kw, __shfl_xor_sync(0xffffffffu, kw, 2));
+      if (kq == 0) sh.top[ks_slot] = code_value(kw);
+      sh.vmax[vrow][vquad] = vw;
     }
     Move m2 = {};
     Part part = {};
@@ -534,7 +579,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
           } else {
             uint32_t c = 0;
 #pragma unroll
-            for (int k = 0; k < kMoveWarps; ++k) c = max(c, sh.vmax[k][i >> 2] >> (8 * (i & 3)) & 0xffu);
+            for (int k = 0; k < kMoveThreads / 16; ++k) c = max(c, sh.vmax[k][i >> 2] >> (8 * (i & 3)) & 0xffu);
             top = fmaxf(top, code_value(c) * (sh.vscale[i] * 0x1p-9f));
           }
         }
@@ -582,35 +627,45 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
           const float f = sh.kscale[ks_slot] / k_new;
           const bool bad = no_scales(sh.kscale[ks_slot], sh.vscale[ks_slot]);
           uint8_t* dst = p.c.k8 + ph * (kPage * D) + ks_slot * D + 16 * kq;
+          if (bad) {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const uint32_t nan = 0x7f7f7f7fu;
-            uint4 o = kr[i];
-            if (bad)
-              o = make_uint4(nan, nan, nan, nan);
-            else if (f != 1.f)
-              o = make_uint4(codes_times(o.x, f, f, f, f), codes_times(o.y, f, f, f, f), codes_times(o.z, f, f, f, f),
-                             codes_times(o.w, f, f, f, f));
-            *reinterpret_cast<uint4*>(dst + 64 * i) = o;
+            for (int i = 0; i < D / 64; ++i) kr[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+          } else if (f != 1.f) {
+            if (plain_power(f)) {
+              const uint32_t ff = pack_f16x2(f, f);
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i)
+                kr[i] = make_uint4(codes_times_f16(kr[i].x, ff, ff), codes_times_f16(kr[i].y, ff, ff),
+                                   codes_times_f16(kr[i].z, ff, ff), codes_times_f16(kr[i].w, ff, ff));
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i)
+                kr[i] = make_uint4(codes_times(kr[i].x, f, f, f, f), codes_times(kr[i].y, f, f, f, f),
+                                   codes_times(kr[i].z, f, f, f, f), codes_times(kr[i].w, f, f, f, f));
+            }
           }
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) *reinterpret_cast<uint4*>(dst + 64 * i) = kr[i];
         }
         {
           float f[4];
           uint32_t keep = 0;  // bytes of slots whose scales are some
-          bool same = true;
+          bool same = true, plain = true;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int i = 4 * vquad + j;
             f[j] = sh.vscale[i] / v_new;
             keep |= no_scales(sh.kscale[i], sh.vscale[i]) ? 0u : 0xffu << (8 * j);
             same = same && f[j] == 1.f;
+            plain = plain && plain_power(f[j]);
           }
           uint8_t* dst = p.c.v8 + ph * (kPage * D) + 4 * vquad + vrow * kPage;
+          const uint32_t f01 = pack_f16x2(f[0], f[1]), f23 = pack_f16x2(f[2], f[3]);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            uint32_t o = same ? vr[i] : codes_times(vr[i], f[0], f[1], f[2], f[3]);
-            o &= keep & ~__vcmpeq4(o & 0x7f7f7f7fu, 0x7f7f7f7fu);  // V holds no NaN
-            *reinterpret_cast<uint32_t*>(dst + 16 * i * kPage) = o;
+            uint32_t o = vr[i];
+            if (!same) o = plain ? codes_times_f16(o, f01, f23) : codes_times(o, f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint32_t*>(dst + 16 * i * kPage) = o & keep;
           }
         }
         if (tid < kPage) p.weights[ph * kPage + tid] = sh.weight[tid];
