@@ -287,22 +287,22 @@ constexpr int kMoveThreads = 256;
 constexpr int kWindow = kMoveThreads;  // source pages looked at a time
 constexpr int kMinExp = -100;
 
-__device__ __forceinline__ uint32_t codes_times(uint32_t w, float f0, float f1, float f2, float f3) {
+__device__ __forceinline__ uint32_t codes_times(uint32_t w, float f) {
   uint32_t lo, hi;
   codes_to_f16(w, lo, hi);
   float v[4];
   asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[0]), "=f"(v[1]) : "r"(lo));
   asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[2]), "=f"(v[3]) : "r"(hi));
-  return pack_e4m3x4(v[0] * f0, v[1] * f1, v[2] * f2, v[3] * f3);
+  return pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
 }
-// The same for powers of two from 2^-14 to 2^15, as fp16 pairs: the products are exact there.
-__device__ __forceinline__ uint32_t codes_times_f16(uint32_t w, uint32_t f01, uint32_t f23) {
+// The same for powers of two from 2^-14 to 2^15, as an fp16 pair ff: the products are exact there.
+__device__ __forceinline__ uint32_t codes_times_f16(uint32_t w, uint32_t ff) {
   uint32_t lo, hi, r;
   codes_to_f16(w, lo, hi);
-  asm("{.reg .b32 x, y; .reg .b16 a, b; mul.rn.f16x2 x, %1, %3; mul.rn.f16x2 y, %2, %4; "
+  asm("{.reg .b32 x, y; .reg .b16 a, b; mul.rn.f16x2 x, %1, %3; mul.rn.f16x2 y, %2, %3; "
       "cvt.rn.satfinite.e4m3x2.f16x2 a, x; cvt.rn.satfinite.e4m3x2.f16x2 b, y; mov.b32 %0, {a, b};}"
       : "=r"(r)
-      : "r"(lo), "r"(hi), "r"(f01), "r"(f23));
+      : "r"(lo), "r"(hi), "r"(ff));
   return r;
 }
 __device__ __forceinline__ bool plain_power(float f) {
@@ -346,7 +346,7 @@ struct MoveSmem {
   int token[kPage];            // where each slot's token is now
   int page[kPage];             // its page, -1: none
   float kscale[kPage], vscale[kPage], weight[kPage];
-  uint32_t vmax[kMoveThreads / 16][kPage / 4];  // largest V codes of four slots each
+  uint32_t vmax[4][kPage];     // largest V codes of a slot in a quarter of the rows
   float top[kPage];            // largest K code of each slot
   int exps[2];
   int job;
@@ -479,9 +479,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
     // in place, a page whose tokens all stay is left alone
     const bool moved = __syncthreads_or(tid < m.cnt && (!kInPlace || found != r0 + tid));
 
-    // K: a thread has a quarter of a slot's row; V: four slots of the rows vrow, vrow + 16, ..
+    // K: a thread has a quarter of a slot's row. V: the rows vq, vq + 4, .. of a slot, the
+    // slots side by side in the lanes, so that the bytes of a source page lie together (with
+    // a row's four neighbours in a thread a load touched 10 sectors in place of 4 and the
+    // lookups of them bound the kernel).
     const int ks_slot = tid >> 2, kq = tid & 3;
-    const int vquad = tid & 15, vrow = tid >> 4;
+    const int vslot = lane + 32 * (warp & 1), vq = warp >> 1;
     uint4 kr[D / 64];
     uint32_t vr[D / 16];
     if (moved) {
@@ -491,19 +494,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
         kr[i] = kp < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 64 * i);
+      const int vp = sh.page[vslot];
+      src = p.c.v8 + (static_cast<size_t>(max(vp, 0)) * Hk + m.hk) * (kPage * D) + (sh.token[vslot] & (kPage - 1)) + vq * kPage;
+      uint8_t v[D / 4];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) vr[i] = 0u;
+      for (int i = 0; i < D / 4; ++i) v[i] = vp < 0 ? 0 : src[4 * i * kPage];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int vp = sh.page[4 * vquad + j];
-        if (vp < 0) continue;
-        src = p.c.v8 + (static_cast<size_t>(vp) * Hk + m.hk) * (kPage * D) + (sh.token[4 * vquad + j] & (kPage - 1)) + vrow * kPage;
-        uint8_t v[D / 16];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) v[i] = src[16 * i * kPage];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) vr[i] += static_cast<uint32_t>(v[i]) << (8 * j);
-      }
+      for (int i = 0; i < D / 16; ++i)
+        vr[i] = v[4 * i] + (static_cast<uint32_t>(v[4 * i + 1]) << 8) + (static_cast<uint32_t>(v[4 * i + 2]) << 16) +
+                (static_cast<uint32_t>(v[4 * i + 3]) << 24);
     }
     // the next page to be written: its first token's page is on its way, then its window
     const uint32_t next = kInPlace ? static_cast<uint32_t>(sh.job) : job + gridDim.x;
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
         sh.vscale[tid] = slot_vs;
         sh.weight[tid] = slot_w;
       }
-      // largest codes: of K's slot over four threads, of V's four slots over two
+      // largest codes, K's over the slot's four threads
       Widest k, v;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
@@ -541,20 +540,22 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
         kw = __vmaxu2(x.even, x.odd);
         kw = max(kw & 0xffffu, kw >> 16);
       }
-      uint32_t vw = v.even | v.odd << 8;
-      if (__builtin_expect(__any_sync(0xffffffffu, without_nan(vw) != vw), 0)) {
+      uint32_t vw = __vmaxu2(v.even, v.odd);
+      vw = max(vw & 0xffffu, vw >> 16);
+      if (__builtin_expect(__any_sync(0xffffffffu, vw == kNan), 0)) {
         Widest x;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           vr[i] = without_nan(vr[i]);
           x.add(vr[i]);
         }
-        vw = x.even | x.odd << 8;
+        vw = __vmaxu2(x.even, x.odd);
+        vw = max(vw & 0xffffu, vw >> 16);
       }
       kw = max(kw, __shfl_xor_sync(0xffffffffu, kw, 1));
       kw = max(kw, __shfl_xor_sync(0xffffffffu, kw, 2));
       if (kq == 0) sh.top[ks_slot] = code_value(kw);
-      sh.vmax[vrow][vquad] = vw;
+      sh.vmax[vq][vslot] = vw;
     }
     Move m2 = {};
     Part part = {};
@@ -577,9 +578,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
           if (warp == 0) {
             top = fmaxf(top, sh.top[i] * (sh.kscale[i] * 0x1p-9f));
           } else {
-            uint32_t c = 0;
-#pragma unroll
-            for (int k = 0; k < kMoveThreads / 16; ++k) c = max(c, sh.vmax[k][i >> 2] >> (8 * (i & 3)) & 0xffu);
+            const uint32_t c = max(max(sh.vmax[0][i], sh.vmax[1][i]), max(sh.vmax[2][i], sh.vmax[3][i]));
             top = fmaxf(top, code_value(c) * (sh.vscale[i] * 0x1p-9f));
           }
         }
@@ -635,37 +634,43 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
               const uint32_t ff = pack_f16x2(f, f);
 #pragma unroll
               for (int i = 0; i < D / 64; ++i)
-                kr[i] = make_uint4(codes_times_f16(kr[i].x, ff, ff), codes_times_f16(kr[i].y, ff, ff),
-                                   codes_times_f16(kr[i].z, ff, ff), codes_times_f16(kr[i].w, ff, ff));
+                kr[i] = make_uint4(codes_times_f16(kr[i].x, ff), codes_times_f16(kr[i].y, ff),
+                                   codes_times_f16(kr[i].z, ff), codes_times_f16(kr[i].w, ff));
             } else {
 #pragma unroll
               for (int i = 0; i < D / 64; ++i)
-                kr[i] = make_uint4(codes_times(kr[i].x, f, f, f, f), codes_times(kr[i].y, f, f, f, f),
-                                   codes_times(kr[i].z, f, f, f, f), codes_times(kr[i].w, f, f, f, f));
+                kr[i] = make_uint4(codes_times(kr[i].x, f), codes_times(kr[i].y, f), codes_times(kr[i].z, f),
+                                   codes_times(kr[i].w, f));
             }
           }
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) *reinterpret_cast<uint4*>(dst + 64 * i) = kr[i];
         }
         {
-          float f[4];
-          uint32_t keep = 0;  // bytes of slots whose scales are some
-          bool same = true, plain = true;
+          const float f = sh.vscale[vslot] / v_new;
+          const bool bad = no_scales(sh.kscale[vslot], sh.vscale[vslot]);
+          if (bad) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = 4 * vquad + j;
-            f[j] = sh.vscale[i] / v_new;
-            keep |= no_scales(sh.kscale[i], sh.vscale[i]) ? 0u : 0xffu << (8 * j);
-            same = same && f[j] == 1.f;
-            plain = plain && plain_power(f[j]);
+            for (int i = 0; i < D / 16; ++i) vr[i] = 0u;
+          } else if (f != 1.f) {
+            if (plain_power(f)) {
+              const uint32_t ff = pack_f16x2(f, f);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) vr[i] = codes_times_f16(vr[i], ff);
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) vr[i] = codes_times(vr[i], f);
+            }
           }
-          uint8_t* dst = p.c.v8 + ph * (kPage * D) + 4 * vquad + vrow * kPage;
-          const uint32_t f01 = pack_f16x2(f[0], f[1]), f23 = pack_f16x2(f[2], f[3]);
+          __syncwarp();
+          // four rows of a slot in a thread -> four slots of row 16 i + 4 (lane % 4) + vq
+          uint8_t* dst = p.c.v8 + ph * (kPage * D) + (vslot & ~3) + (4 * (lane & 3) + vq) * kPage;
+          const uint32_t first = lane & 1 ? 0x3715u : 0x6240u, second = lane & 2 ? 0x3276u : 0x5410u;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            uint32_t o = vr[i];
-            if (!same) o = plain ? codes_times_f16(o, f01, f23) : codes_times(o, f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint32_t*>(dst + 16 * i * kPage) = o & keep;
+            uint32_t x = __byte_perm(vr[i], __shfl_xor_sync(0xffffffffu, vr[i], 1), first);
+            x = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 2), second);
+            *reinterpret_cast<uint32_t*>(dst + 16 * i * kPage) = x;
           }
         }
         if (tid < kPage) p.weights[ph * kPage + tid] = sh.weight[tid];
@@ -773,7 +778,9 @@ cudaError_t launch_cache_evict(int d, EvictParams p, int num_sms, cudaStream_t s
   if (cluster * kPagesCached < p.max_pages)
     e = launch_select<1024, false>(p, cluster, s);
   else
-    e = many ? launch_select<256, true>(p, cluster, s) : launch_select<1024, true>(p, cluster, s);
+    // (clusters of eight CTAs that fill an SM each do not all find a place at once)
+    e = many ? launch_select<256, true>(p, cluster, s)
+             : cluster > 1 ? launch_select<512, true>(p, cluster, s) : launch_select<1024, true>(p, cluster, s);
   if (e != cudaSuccess) return e;
   return d == 64 ? launch_move<64>(p, num_sms, s) : launch_move<128>(p, num_sms, s);
 }
