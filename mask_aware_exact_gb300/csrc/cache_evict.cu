@@ -42,6 +42,11 @@ __device__ __forceinline__ int of_cta(const int* at, int rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote));
   return v;
 }
+__device__ __forceinline__ void to_cta(int* at, int rank, int v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
 // Sum of it over the first n CTAs of the cluster.
 __device__ __forceinline__ int of_ctas(const int* at, int n) {
   int v[kClusterMost];
@@ -86,6 +91,8 @@ struct SelectSmem {
   int found[2];   // bin, keys wanted of it
   int totals[2];  // keys equal to the last one, tokens kept, of this CTA
   int place;      // of the segment's pages in the list of pages to be written (rank 0)
+  int sums[kBins / 2];        // cluster: of this CTA's bins, and
+  int ranges[kClusterMost];   // of all CTAs' bins
 };
 
 // `most`: pages of a CTA that there is shared memory for.
@@ -104,12 +111,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
   const Kept kp = kept_of(p, b, tid == 0 && rank == 0 && hk == 0);
   const int pages = (kp.len + kPage - 1) / kPage, each = (pages + cluster - 1) / cluster;
   const int p0 = min(rank * each, pages), np = min(each, pages - p0);
-  auto sync_all = [&]() {
-    if (cluster == 1)
-      __syncthreads();
-    else
-      cluster_sync();
-  };
   if (tid == 0 && rank == 0) {
     sh.place = atomicAdd(p.count, (kp.n + kPage - 1) / kPage);
     if (hk == 0) {
@@ -120,12 +121,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 
   // keys of a page: this lane's tokens lane and lane + 32
   auto load_keys = [&](int page, uint32_t (&k)[2]) {
-    k[0] = k[1] = 0u;
-    if (page >= 0) {
-      const float* at = p.weights + (static_cast<size_t>(page) * p.c.Hk + hk) * kPage + lane;
-      k[0] = order_key(at[0]);
-      k[1] = order_key(at[32]);
-    }
+    const float* at = p.weights + (static_cast<size_t>(max(page, 0)) * p.c.Hk + hk) * kPage + lane;
+    const float w0 = at[0], w1 = at[32];  // (without a branch: several pages are on their way)
+    k[0] = page < 0 ? 0u : order_key(w0);
+    k[1] = page < 0 ? 0u : order_key(w1);
   };
   auto page_of = [&](int i) {
     const int page = p.table[static_cast<size_t>(b) * p.max_pages + p0 + i];
@@ -147,13 +146,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     for (int i0 = warp; i0 < np; i0 += 32 * kWarps) {
       const int mine = i0 + lane * kWarps < np ? page_of(i0 + lane * kWarps) : -1;
       const int n = min((np - i0 + kWarps - 1) / kWarps, 32);
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
-        uint32_t k[2];
-        load_keys(__shfl_sync(0xffffffffu, mine, j), k);
-        uint32_t* to = keys + (i0 + j * kWarps) * kPage + lane;
-        to[0] = k[0];
-        to[32] = k[1];
+      for (int j0 = 0; j0 < n; j0 += 8) {
+        uint32_t k[8][2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) load_keys(__shfl_sync(0xffffffffu, mine, min(j0 + j, 31)), k[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j0 + j >= n) break;
+          uint32_t* to = keys + (i0 + (j0 + j) * kWarps) * kPage + lane;
+          to[0] = k[j][0];
+          to[32] = k[j][1];
+        }
       }
     }
   }
@@ -181,31 +184,64 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
           if (j >= kp.lo && j < kp.hi && (k[x] & known) == prefix) atomicAdd(&hist[k[x] >> shift & (bins - 1)], 1);
         }
       }
-      sync_all();
-      // this thread's bins, from the top
-      constexpr int kMine = kBins / kThreads;
-      int c[kMine], sum = 0;
-      const int top = bins - 1 - kMine * tid;
+      if (cluster == 1) {
+        __syncthreads();
+        // this thread's bins, from the top
+        constexpr int kMine = kBins / kThreads;
+        int c[kMine], sum = 0;
+        const int top = bins - 1 - kMine * tid;
 #pragma unroll
-      for (int x = 0; x < kMine; ++x) {
-        c[x] = top < x ? 0 : cluster == 1 ? hist[top - x] : of_ctas(&hist[top - x], cluster);
-        sum += c[x];
-      }
-      int all;
-      int above = block_before<kWarps>(sum, sh.wsum, all);
-#pragma unroll
-      for (int x = 0; x < kMine; ++x) {
-        if (above < want && want <= above + c[x]) {
-          sh.found[0] = top - x;
-          sh.found[1] = want - above;
+        for (int x = 0; x < kMine; ++x) {
+          c[x] = top < x ? 0 : hist[top - x];
+          sum += c[x];
         }
-        above += c[x];
+        int all;
+        int above = block_before<kWarps>(sum, sh.wsum, all);
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) {
+          if (above < want && want <= above + c[x]) {
+            sh.found[0] = top - x;
+            sh.found[1] = want - above;
+          }
+          above += c[x];
+        }
+        __syncthreads();
+      } else {
+        // each CTA adds up its share of the bins, the first the highest (a cluster's CTAs that
+        // all read all bins of one another took 20000 cycles a pass)
+        cluster_sync();
+        const int share = bins / cluster, base = bins - (rank + 1) * share;
+        for (int i = tid; i < share; i += kThreads) sh.sums[i] = of_ctas(&hist[base + i], cluster);
+        __syncthreads();
+        constexpr int kMine = (kBins / 2 + kThreads - 1) / kThreads;
+        int c[kMine], sum = 0;
+        const int top = share - 1 - kMine * tid;
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) {
+          c[x] = top < x ? 0 : sh.sums[top - x];
+          sum += c[x];
+        }
+        int all;
+        int above = block_before<kWarps>(sum, sh.wsum, all);
+        if (tid < cluster) to_cta(&sh.ranges[rank], tid, all);
+        cluster_sync();
+        for (int r = 0; r < rank; ++r) above += sh.ranges[r];
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) {
+          if (above < want && want <= above + c[x]) {
+            for (int r = 0; r < cluster; ++r) {
+              to_cta(&sh.found[0], r, base + top - x);
+              to_cta(&sh.found[1], r, want - above);
+            }
+          }
+          above += c[x];
+        }
+        cluster_sync();
       }
-      __syncthreads();
       prefix |= static_cast<uint32_t>(sh.found[0]) << shift;
       known |= static_cast<uint32_t>(bins - 1) << shift;
       want = sh.found[1];
-      __syncthreads();
+      if (cluster == 1) __syncthreads();
     }
     last = prefix;
     equal = want;
