@@ -7,15 +7,32 @@
 //
 // The pages of all (sequence, cache head) segments form one line, cut into equal runs,
 // one for each warp. With a column-wise mask the line has only the pages that some row
-// sees (the attention's classification, all rows as one tile).
+// sees (the attention's classification, all rows as one tile). A warp brings its pages in
+// by bulk copies, kSlots ahead, into slots of its own: no warp waits for another.
+#include <atomic>
+
 #include "cache_weights.cuh"
 #include "flashmask.h"
 
 namespace fm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Warps of a CTA: as many as registers allow, 12 or 8.
+template <int D, int NT>
+constexpr int kWarps = NT == 1 || (NT == 2 && D == 64) ? 12 : 8;
+// Pages of a warp on their way or being read.
+template <int D, int NT>
+constexpr int kSlots = (D == 128 ? 24 : 48) / kWarps<D, NT>;
+template <int D, int NT>
+constexpr int kSmem = kWarps<D, NT> * kSlots<D, NT> * (kPage * D + 8);
+
+// Up to 32 pages of a run, one per lane, and where the run goes on.
+struct Batch {
+  int n;                         // of all lanes
+  int seg, logical, page, cut;   // page -1: there is none
+  float kscale;
+  int next_seg, next_k;
+};
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -115,76 +132,108 @@ __device__ __forceinline__ void load_rows(const WeightsParams& wp, const Geometr
 }
 
 template <int D, int NT, bool kVec>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarps<D, NT>, 1)
     cache_weights_kernel(const __grid_constant__ WeightsParams wp, const __grid_constant__ Geometry geo) {
   const CacheFwdParams& p = wp.f;
-  __shared__ int wsum[kWarps], begin[kWarps][2];
-  __shared__ uint32_t bits[kVec ? kUnseenWords : 1];
+  constexpr int kW = kWarps<D, NT>, kThreads = 32 * kW, kRing = kSlots<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int wsum[kW], begin[kW][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int nseg = p.B * p.c.Hk;
+  const int nseg = p.B * p.c.Hk, grid = static_cast<int>(gridDim.x);
+  uint8_t* const ring = smem + warp * kRing * kPage * D;
+  const uint32_t bar = smem_u32(smem + kW * kRing * kPage * D) + 8 * kRing * warp;
+  if (lane < kRing) {
+    mbar_init(bar + 8 * lane, 1);
+    fence_barrier_init();
+  }
   auto units = [&](int s) { return line_pages<kVec>(p, geo, s); };
 
-  // this warp's run of the line
+  // this warp's run of the line (neighbouring runs go to different CTAs)
   const int each = (nseg + kThreads - 1) / kThreads;
   const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
   int mine = 0;
   for (int s = seg_lo; s < seg_hi; ++s) mine += units(s);
   int total;
-  const int before = block_before<kWarps>(mine, wsum, total);
-  const int runs = static_cast<int>(gridDim.x) * kWarps, run = (total + runs - 1) / runs;
-  for (int w = 0; w < kWarps; ++w) {
-    const long long x = static_cast<long long>(run) * (w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x));
+  const int before = block_before<kW>(mine, wsum, total);
+  const int runs = grid * kW, run = (total + runs - 1) / runs;
+  for (int w = 0; w < kW; ++w) {
+    const long long x = static_cast<long long>(run) * (w * grid + static_cast<int>(blockIdx.x));
     if (before <= x && x < before + mine) {
       int s = seg_lo, at = before, n;
-      while (x >= at + (n = units(s)) && s + 1 < seg_hi) at += n, ++s;
+      // a thread with one segment knows its units
+      while (x >= at + (n = each == 1 ? mine : units(s)) && s + 1 < seg_hi) at += n, ++s;
       begin[w][0] = s;
       begin[w][1] = static_cast<int>(x) - at;
     }
   }
   __syncthreads();
-  const long long lo = static_cast<long long>(run) * (warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x));
-  int left = static_cast<int>(max(0LL, min(static_cast<long long>(run), total - lo)));
-  int seg = left > 0 ? begin[warp][0] : 0, k = left > 0 ? begin[warp][1] : 0;
+  const long long lo = static_cast<long long>(run) * (warp * grid + static_cast<int>(blockIdx.x));
+  int left = static_cast<int>(max(0LL, min(static_cast<long long>(run), total - lo)));  // not in a batch yet
+
+  // the next pages of the run
+  auto next_batch = [&](int seg, int k) {
+    Batch q = {};
+    while (left > 0) {
+      int my_k, my_n;
+      q.n = next_units(seg, k, nseg, min(32, left), units, q.seg, my_k, my_n);
+      if (q.n == 0) {
+        seg += 32;
+        k = 0;
+        if (seg < nseg) continue;
+        left = 0;  // the lengths are not those of the run's search any more
+        break;
+      }
+      left -= q.n;
+      q.page = -1;
+      if (lane < q.n) {
+        const int b = geo.by_Hk.div(q.seg), hk = q.seg - b * p.c.Hk;
+        q.logical = page_on_line<kVec>(p, geo, b, hk, 0, my_k, q.cut);
+        q.page = p.table[static_cast<size_t>(b) * p.max_pages + q.logical];
+        if (q.page < 0 || q.page >= p.c.pages) {
+          record_failure(p.status, kStatusPage, kSiteCachePage);
+          q.page = -1;
+        } else {
+          q.kscale = p.c.kscale[static_cast<size_t>(q.page) * p.c.Hk + hk];
+        }
+      }
+      q.next_seg = __shfl_sync(0xffffffffu, q.seg, q.n - 1);
+      q.next_k = __shfl_sync(0xffffffffu, my_k, q.n - 1) + 1;
+      break;
+    }
+    return q;
+  };
+  // The page of lane i on its way to slot x (a page that is not there reads another's, and
+  // what comes of it is dropped).
+  auto fetch = [&](const Batch& q, int i, int x) {
+    if (lane == i) {
+      const int hk = q.seg - geo.by_Hk.div(q.seg) * p.c.Hk;
+      mbar_arrive_expect_tx(bar + 8 * x, kPage * D);
+      bulk_load(smem_u32(ring + x * kPage * D), p.c.k8 + (static_cast<size_t>(max(q.page, 0)) * p.c.Hk + hk) * (kPage * D),
+                kPage * D, bar + 8 * x);
+    }
+  };
 
   Rows<D, NT> rw;
   RowTile r = {};
-  int cur = -1, cur_tile = -1;
-  while (left > 0) {
-    int my_seg, my_k, my_n;
-    const int avail = next_units(seg, k, nseg, min(32, left), units, my_seg, my_k, my_n);
-    int page = -1, logical = 0, cut = 0;
-    float ks = 0.f;
-    if (lane < avail) {
-      const int b = geo.by_Hk.div(my_seg), hk = my_seg - b * p.c.Hk;
-      logical = page_on_line<kVec>(p, geo, b, hk, 0, my_k, cut);
-      page = p.table[static_cast<size_t>(b) * p.max_pages + logical];
-      if (page < 0 || page >= p.c.pages) {
-        record_failure(p.status, kStatusPage, kSiteCachePage);
-        page = -1;
-      } else {
-        ks = p.c.kscale[static_cast<size_t>(page) * p.c.Hk + hk];
-      }
-    }
-    for (int i = 0; i < avail; ++i) {
-      const int pg = __shfl_sync(0xffffffffu, page, i), sg = __shfl_sync(0xffffffffu, my_seg, i);
-      const int j0 = __shfl_sync(0xffffffffu, logical, i) * kPage, ct = __shfl_sync(0xffffffffu, cut, i);
-      const float kscale = __shfl_sync(0xffffffffu, ks, i);
-      if (pg < 0) continue;
+  int cur = -1, cur_tile = -1, start = 0;
+  int slot = 0, turn = 0, ahead = 0;  // of the ring; pages fetched that are not done
+  bool ok = true;
+  Batch now = left > 0 ? next_batch(begin[warp][0], begin[warp][1]) : Batch{};
+  for (; ahead < kRing && ahead < now.n; ++ahead) fetch(now, ahead, ahead);
+  while (ok && now.n > 0) {
+    // the batch behind this one is looked up while this one's pages are on their way
+    const Batch then = next_batch(now.next_seg, now.next_k);
+    for (int i = 0; ok && i < now.n; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, now.page, i), sg = __shfl_sync(0xffffffffu, now.seg, i);
+      const int j0 = __shfl_sync(0xffffffffu, now.logical, i) * kPage, ct = __shfl_sync(0xffffffffu, now.cut, i);
+      const float kscale = __shfl_sync(0xffffffffu, now.kscale, i);
       const int b = geo.by_Hk.div(sg), hk = sg - b * p.c.Hk;
-      const size_t ph = static_cast<size_t>(pg) * p.c.Hk + hk;
-      // instruction u has the keys 16 u + g and 16 u + 8 + g of this lane
-      const uint8_t* src = p.c.k8 + ph * (kPage * D) + g * D + 16 * c;
-      uint4 w[4][2][D / 64];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            w[u][x][hf] = __ldcs(reinterpret_cast<const uint4*>(src + (16 * u + 8 * x) * D + 64 * hf));
-      float* const wt = wp.weights + ph * kPage + 16 * c + g;
+      float* const wt = wp.weights + (static_cast<size_t>(max(pg, 0)) * p.c.Hk + hk) * kPage + 16 * c + g;
       const float old[2] = {wt[0], wt[8]};
-      if (sg != cur) r = row_tile(p, geo, b, 0, lane == 0);
+      if (sg != cur) {
+        r = row_tile(p, geo, b, 0, lane == 0);
+        start = wp.start ? min(max(wp.start[b], 0), r.len) : r.shift;
+      }
       const int rows = geo.G * r.live, tiles = (rows + 8 * NT - 1) / (8 * NT);
       const bool none = no_scales(kscale, 0.f);
       float sum[4][2] = {};
@@ -192,19 +241,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         if (p.mask.causal && r.shift + geo.by_G.div(min(rows, (tile + 1) * 8 * NT) - 1) < j0) continue;
         if (sg != cur || tile != cur_tile) load_rows<D, NT, kVec>(wp, geo, r, b, hk, tile, rw);
         cur = sg, cur_tile = tile;
+        ok = __all_sync(0xffffffffu, cache_wait(bar + 8 * slot, turn & 1, p.status));
+        if (!ok) break;
+        // instruction u has the keys 16 u + g and 16 u + 8 + g of this lane; halves of a row in
+        // another order for odd keys, so that the eight lanes of a phase are in different banks
+        const uint8_t* src = ring + slot * kPage * D + g * D + 16 * c;
         float s[4][NT][4] = {};
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
+          uint4 w[2][D / 64];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              w[x][hf] = *reinterpret_cast<const uint4*>(src + (16 * u + 8 * x) * D + (D == 128 ? 64 * (hf ^ (g & 1)) : 0));
+          if (D == 128 && (g & 1)) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint4 t = w[x][0];
+              w[x][0] = w[x][D / 64 - 1];
+              w[x][D / 64 - 1] = t;
+            }
+          }
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t a[4];
-              codes_to_f16(word(w[u][0][hf], q), a[0], a[2]);
-              codes_to_f16(word(w[u][1][hf], q), a[1], a[3]);
+              codes_to_f16(word(w[0][hf], q), a[0], a[2]);
+              codes_to_f16(word(w[1][hf], q), a[1], a[3]);
 #pragma unroll
               for (int t = 0; t < NT; ++t) mma16816(s[u][t], a, rw.q[t][4 * hf + q][0], rw.q[t][4 * hf + q][1]);
             }
+        }
         // s[u][t][2 x + e]: key 16 u + 8 x + g, row 8 t + 2 c + e
         float ck[NT][2];
 #pragma unroll
@@ -234,16 +303,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+          const uint64_t c2 = f2_make(ck[t][0], ck[t][1]), l2 = f2_make(-rw.lse2[t][0], -rw.lse2[t][1]);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const float a = ex2(fmaf(s[u][t][2 * x], ck[t][0], -rw.lse2[t][0]));
-              const float z = ex2(fmaf(s[u][t][2 * x + 1], ck[t][1], -rw.lse2[t][1]));
-              sum[u][x] += a + z;
+              float a, z;
+              f2_split(f2_fma(f2_make(s[u][t][2 * x], s[u][t][2 * x + 1]), c2, l2), a, z);
+              sum[u][x] += ex2(a) + ex2(z);
             }
+        }
       }
+      if (!ok) break;
+      // (a page that no tile of rows sees has to have arrived, too)
+      ok = __all_sync(0xffffffffu, cache_wait(bar + 8 * slot, turn & 1, p.status));
+      if (!ok) break;
+      __syncwarp();
+      // a page more, of this batch or the next
+      for (--ahead; ahead < kRing; ++ahead) {
+        const int q = i + 1 + ahead;
+        int x = slot + 1 + ahead;
+        if (x >= kRing) x -= kRing;
+        if (q < now.n)
+          fetch(now, q, x);
+        else if (q - now.n < then.n)
+          fetch(then, q - now.n, x);
+        else
+          break;
+      }
+      if (++slot == kRing) slot = 0, ++turn;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -251,45 +340,53 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           sum[u][x] += __shfl_xor_sync(0xffffffffu, sum[u][x], 1);
           sum[u][x] += __shfl_xor_sync(0xffffffffu, sum[u][x], 2);
         }
-      const int start = wp.start ? min(max(wp.start[b], 0), r.len) : r.shift;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int j = j0 + 16 * c + g + 8 * x;
         const float v = c == 0 ? sum[0][x] : c == 1 ? sum[1][x] : c == 2 ? sum[2][x] : sum[3][x];
-        if (j < r.len) wt[8 * x] = j < start ? old[x] + v : v;
+        if (pg >= 0 && j < r.len) wt[8 * x] = j < start ? old[x] + v : v;
       }
     }
-    left -= avail;
-    if (avail > 0) {
-      seg = __shfl_sync(0xffffffffu, my_seg, avail - 1);
-      k = __shfl_sync(0xffffffffu, my_k, avail - 1) + 1;
-    } else {
-      seg += 32;
-      k = 0;
-      if (seg >= nseg) break;  // the lengths are not those of the run's search any more
-    }
+    now = then;
   }
+  if (!ok) {
+    // copies in flight land before the CTA's shared memory is given up
+    for (int x = 0; x < ahead; ++x)
+      mbar_wait_for(bar + 8 * ((slot + x) % kRing), (slot + x >= kRing ? turn + 1 : turn) & 1, nullptr, 1000000ull);
+  }
+  clear_unseen<kVec>(wp, geo, static_cast<int>(blockIdx.x) * kW + warp, runs);
+}
 
-  clear_unseen<kThreads, kVec>(wp, geo, bits);
+template <int D, int NT, bool kVec>
+cudaError_t launch_t(const WeightsParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> done[4];  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev > 255) return cudaErrorInvalidDevice;
+  if (!(done[dev >> 6].load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(cache_weights_kernel<D, NT, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, NT>);
+    if (e != cudaSuccess) return e;
+    done[dev >> 6].fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  if (kVec) {
+    e = launch_cache_classify(p.f, geo, s);
+    if (e != cudaSuccess) return e;
+  }
+  cache_weights_kernel<D, NT, kVec><<<num_sms, 32 * kWarps<D, NT>, kSmem<D, NT>, s>>>(p, geo);
+  return cudaGetLastError();
 }
 
 template <int D, int NT>
 cudaError_t launch_nt(const WeightsParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
-  const int grid = num_sms * (NT == 1 ? 2 : 1);
-  if (p.f.mask.lts != nullptr || p.f.mask.uts != nullptr) {
-    const cudaError_t e = launch_cache_classify(p.f, geo, s);
-    if (e != cudaSuccess) return e;
-    cache_weights_kernel<D, NT, true><<<grid, kThreads, 0, s>>>(p, geo);
-  } else {
-    cache_weights_kernel<D, NT, false><<<grid, kThreads, 0, s>>>(p, geo);
-  }
-  return cudaGetLastError();
+  return p.f.mask.lts != nullptr || p.f.mask.uts != nullptr ? launch_t<D, NT, true>(p, geo, num_sms, s)
+                                                            : launch_t<D, NT, false>(p, geo, num_sms, s);
 }
 
 template <int D>
 cudaError_t launch_d(const WeightsParams& p, const Geometry& geo, int num_sms, cudaStream_t s) {
   if (geo.rows <= 8) return launch_nt<D, 1>(p, geo, num_sms, s);
-  return launch_nt<D, 2>(p, geo, num_sms, s);
+  return geo.rows <= 16 ? launch_nt<D, 2>(p, geo, num_sms, s) : launch_nt<D, 4>(p, geo, num_sms, s);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

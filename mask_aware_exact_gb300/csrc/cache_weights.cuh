@@ -29,49 +29,50 @@ static __device__ __noinline__ int line_pages(const CacheFwdParams& p, const Geo
   return (row_tile(p, geo, geo.by_Hk.div(seg), 0, blockIdx.x == 0).len + kPage - 1) / kPage;
 }
 
-constexpr int kUnseenWords = FM_MAX_SEQLEN / kPage / 32;
 // Position from which on the keys of a sequence are new.
 __device__ __forceinline__ int first_new(const WeightsParams& wp, int b, const RowTile& r) {
   return wp.start ? min(max(wp.start[b], 0), r.len) : max(r.shift, 0);
 }
 // With a column-wise mask: pages that no row sees and whose keys are new have had nothing.
-// Called by all kThreads threads of every CTA; `bits` is shared.
-template <int kThreads, bool kVec>
-__device__ __forceinline__ void clear_unseen(const WeightsParams& wp, const Geometry& geo, uint32_t* bits) {
+// Warp `warp` of `warps` takes its share of the segments.
+template <bool kVec>
+__device__ __forceinline__ void clear_unseen(const WeightsParams& wp, const Geometry& geo, int warp, int warps) {
   if constexpr (kVec) {
     const CacheFwdParams& p = wp.f;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nseg = p.B * p.c.Hk;
-    for (int sg = blockIdx.x; sg < nseg; sg += gridDim.x) {
+    const int lane = threadIdx.x & 31, nseg = p.B * p.c.Hk;
+    for (int sg = warp; sg < nseg; sg += warps) {
       const int b = geo.by_Hk.div(sg), hk = sg - b * p.c.Hk;
-      const RowTile rt = row_tile(p, geo, b, 0, tid == 0);
-      const int start = first_new(wp, b, rt);
-      const int first = start / kPage, pages = (rt.len + kPage - 1) / kPage - first;
-      if (start >= rt.len) continue;
-      for (int i = tid; i < (pages + 31) / 32; i += kThreads) bits[i] = 0;
-      __syncthreads();
-      // the list is in order, so the new pages are among its last
+      const RowTile r = row_tile(p, geo, b, 0, lane == 0);
+      const int start = first_new(wp, b, r);
+      if (start >= r.len) continue;
+      const int first = start / kPage, pages = (r.len + kPage - 1) / kPage;
       const size_t at = static_cast<size_t>(b) * geo.classes + mask_class(p, geo, hk);
-      const int n = p.listed[at];
-      for (int i = tid; i < min(pages, n); i += kThreads) {
-        const int q = (p.list[at * p.max_pages + n - 1 - i] & 0x7fff) - first;
-        if (q >= 0) atomicOr(&bits[q >> 5], 1u << (q & 31));
-      }
-      __syncthreads();
-      for (int i = warp; i < pages; i += kThreads / 32) {
-        if (bits[i >> 5] >> (i & 31) & 1u) continue;
-        const int page = p.table[static_cast<size_t>(b) * p.max_pages + first + i];
-        if (page < 0 || page >= p.c.pages) {
-          record_failure(p.status, kStatusPage, kSiteCachePage);
-          continue;
+      const uint16_t* list = p.list + at * p.max_pages;
+      int n = p.listed[at];
+      // 32 pages at a time from the last: those of them that are listed are the list's last
+      for (int hi = pages; hi > first; hi -= 32) {
+        const int lo = max(first, hi - 32);
+        const int q = lane < n ? (list[n - 1 - lane] & 0x7fff) - lo : -1;
+        const uint32_t seen = __reduce_or_sync(0xffffffffu, q >= 0 && q < 32 ? 1u << q : 0u);
+        n -= __popc(seen);
+        int page = -1;
+        if (lo + lane < hi && !(seen >> lane & 1u)) {
+          page = p.table[static_cast<size_t>(b) * p.max_pages + lo + lane];
+          if (page < 0 || page >= p.c.pages) {
+            record_failure(p.status, kStatusPage, kSiteCachePage);
+            page = -1;
+          }
         }
+        for (uint32_t todo = __ballot_sync(0xffffffffu, page >= 0); todo != 0; todo &= todo - 1) {
+          const int i = __ffs(todo) - 1, pg = __shfl_sync(0xffffffffu, page, i);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int j = (first + i) * kPage + lane + 32 * x;
-          if (j >= start && j < rt.len)
-            wp.weights[(static_cast<size_t>(page) * p.c.Hk + hk) * kPage + lane + 32 * x] = 0.f;
+          for (int x = 0; x < 2; ++x) {
+            const int j = (lo + i) * kPage + lane + 32 * x;
+            if (j >= start && j < r.len)
+              wp.weights[(static_cast<size_t>(pg) * p.c.Hk + hk) * kPage + lane + 32 * x] = 0.f;
+          }
         }
       }
-      __syncthreads();
     }
   }
 }

@@ -57,8 +57,7 @@ struct Layout {
   static constexpr int kFactors = kKeysAt + 2 * kK * kKOperand;
   static constexpr int kMeta = kFactors + kFactorRing * kFactorBytes;
   static constexpr int kWords = kMeta + kMetaRing * kMetaInts * 4;
-  static constexpr int kUnseen = kWords + (kScanWords + 8) * 4;
-  static constexpr int kBar = (kUnseen + kUnseenWords * 4 + 7) / 8 * 8;
+  static constexpr int kBar = (kWords + (kScanWords + 8) * 4 + 7) / 8 * 8;
   static constexpr int kNumBars = 2 * kStages + 2 * kMetaRing + 2 * kK + 10 + 2 * kFactorRing;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kBytes = kTmemSlot + 16;
@@ -646,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  clear_unseen<kThreads, kVec>(wp, geo, reinterpret_cast<uint32_t*>(smem + L::kUnseen));
+  clear_unseen<kVec>(wp, geo, static_cast<int>(blockIdx.x) * (kThreads / 32) + warp, grid * (kThreads / 32));
 }
 
 template <int D, bool kVec>
