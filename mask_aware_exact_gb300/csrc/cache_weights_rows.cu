@@ -48,8 +48,8 @@ enum Flag { kEnd = 1, kWhole = 2, kTail = 4 };
 
 template <int D>
 struct Layout {
-  static constexpr int kStages = D == 128 ? 4 : 8;  // row tiles in shared memory
-  static constexpr int kK = D == 128 ? 1 : 2;       // pairs of K operands
+  static constexpr int kStages = D == 128 ? 2 : 8;  // row tiles in shared memory
+  static constexpr int kK = 2;                      // pairs of K operands
   static constexpr int kStageBytes = D * 256;
   static constexpr int kTileBytes = kStageBytes + kFactorBytes;  // in the workspace
   static constexpr int kKOperand = 128 * D * 2;
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(256) weights_tiles_kernel(const __grid_constan
   const RowTile r = row_tile(p, geo, b, 0, false);
   const int rows = geo.G * r.live;
   if (tile * kTileRows >= rows) return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int u = threadIdx.x % kUnits16, r0 = threadIdx.x / kUnits16;
   uint8_t* dst = wp.tiles + static_cast<size_t>(blockIdx.x) * Layout<D>::kTileBytes;
   float* factors = reinterpret_cast<float*>(dst + D * 256);
@@ -296,6 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     mbar_init(bar.at(i), n);
     fence_barrier_init();
   }
+  // The kernel before (with a mask: the classification) may still run up to here. Its results
+  // are the lists of pages with a mask, the row tiles without one.
+  if (kVec) asm volatile("griddepcontrol.wait;" ::: "memory");
   // the line: items of all segments, each `parts` long; this CTA's run
   auto items = [&](int s) { return (line_pages<kVec>(p, geo, s) + 3) >> 2; };
   const int each = (nseg + kThreads - 1) / kThreads;
@@ -329,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     int left = run_lo < run_hi ? item_hi - item_lo : 0, item = item_lo;
     int seg = left > 0 ? found[0] : 0, k = left > 0 ? found[1] : 0;
     int piece = 0, tq = 0;
+    if (!kVec) asm volatile("griddepcontrol.wait;" ::: "memory");
     bool ok = true;
     while (ok && left > 0) {
       int my_seg, my_k, my_n;
@@ -468,46 +473,82 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ conversion
-    const int key = (warp - 8) * 32 + lane;
-    int kc = 0;
-    for (int piece = 0;; ++piece) {
-      const int ring = piece % kMetaRing;
-      if (!__all_sync(0xffffffffu, wait_for(bar.meta_full(ring), (piece / kMetaRing) & 1, p.status))) break;
-      const int* m = meta + ring * kMetaInts;
-      if (m[kFlags] & kEnd) break;
-      const int tiles = m[kTiles], seg = m[kSeg];
-      const int page[2] = {m[kPg + (key >> 6)], m[kPg + 2 + (key >> 6)]};
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.meta_empty(ring));
-      if (tiles == 0) continue;
-      const int hk = seg - geo.by_Hk.div(seg) * p.c.Hk;
-      uint4 w[2][D / 16];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint8_t* src = p.c.k8 + (static_cast<size_t>(max(page[s], 0)) * p.c.Hk + hk) * (kPage * D) + (key & 63) * D;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          w[s][i] = page[s] < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + 16 * i);
+    // A warp has 32 keys of each operand, a thread 16 codes of every kRows-th of them: whole
+    // rows side by side (with a key a thread a load touched 32 of them, and the lookups
+    // bound calls with few rows: 40 rows at 16 x 16384, 4 heads of 128, took 45.6 us and take 37.6).
+    constexpr int kRows = 512 / D, kLanes = 32 / kRows;
+    const int key0 = (warp - 8) * 32 + lane / kLanes, chunk = lane % kLanes;
+    int piece = 0, kc = 0;
+    bool ok = true;
+    struct Item {
+      int page[2], hk;
+      bool some;  // not the end
+    };
+    // The next piece that has row tiles. `wait` false: if it is there already.
+    auto next_item = [&](bool wait) {
+      Item x = {};
+      while (ok) {
+        const int ring = piece % kMetaRing, phase = (piece / kMetaRing) & 1;
+        if (!wait && !__all_sync(0xffffffffu, mbar_test_wait(bar.meta_full(ring), phase))) break;
+        ok = __all_sync(0xffffffffu, wait_for(bar.meta_full(ring), phase, p.status));
+        if (!ok) break;
+        const int* m = meta + ring * kMetaInts;
+        if (m[kFlags] & kEnd) break;
+        const int tiles = m[kTiles], seg = m[kSeg];
+        x.page[0] = m[kPg + ((warp - 8) >> 1)];
+        x.page[1] = m[kPg + 2 + ((warp - 8) >> 1)];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.meta_empty(ring));
+        ++piece;
+        if (tiles == 0) continue;
+        x.hk = seg - geo.by_Hk.div(seg) * p.c.Hk;
+        x.some = true;
+        break;
       }
+      return x;
+    };
+    auto load = [&](const Item& x, int s, uint4 (&w)[D / 16]) {
+      const uint8_t* src = p.c.k8 + (static_cast<size_t>(max(x.page[s], 0)) * p.c.Hk + x.hk) * (kPage * D) + (key0 & 63) * D + 16 * chunk;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        w[i] = x.page[s] < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + i * kRows * D);
+    };
+    auto convert = [&](int kb, int s, const uint4 (&w)[D / 16]) {
+      const uint32_t to = smem_u32(smem + L::kKeysAt + (2 * kb + s) * L::kKOperand) + (chunk >> 2) * 16384;
+      // (the upper half's units in another order, for the banks)
+      const uint32_t first = (2 * chunk + (chunk >> 2)) & 7, second = first ^ 1;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t h[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) codes_to_f16(word(w[i], u), h[2 * u], h[2 * u + 1]);
+        const uint32_t row = key0 + i * kRows;
+        const bool up = chunk >= 4;
+        st_shared_v4(to + sw128_offset(row, first), up ? h[4] : h[0], up ? h[5] : h[1], up ? h[6] : h[2], up ? h[7] : h[3]);
+        st_shared_v4(to + sw128_offset(row, second), up ? h[0] : h[4], up ? h[1] : h[5], up ? h[2] : h[6], up ? h[3] : h[7]);
+      }
+    };
+    uint4 w0[D / 16], w1[D / 16];
+    Item now = next_item(true);
+    if (now.some) load(now, 0, w0);
+    for (; ok && now.some; ++kc) {
       const int kb = kc % L::kK;
-      if (kc >= L::kK && !__all_sync(0xffffffffu, wait_for(bar.k_empty(kb), (kc / L::kK - 1) & 1, p.status))) break;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t to = smem_u32(smem + L::kKeysAt + (2 * kb + s) * L::kKOperand);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t h[8];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) codes_to_f16(word(w[s][i], u), h[2 * u], h[2 * u + 1]);
-          const uint32_t at = to + (i >> 2) * 16384;
-          st_shared_v4(at + sw128_offset(key, (2 * i) & 7), h[0], h[1], h[2], h[3]);
-          st_shared_v4(at + sw128_offset(key, (2 * i + 1) & 7), h[4], h[5], h[6], h[7]);
-        }
-      }
+      load(now, 1, w1);
+      if (kc >= L::kK) ok = __all_sync(0xffffffffu, wait_for(bar.k_empty(kb), (kc / L::kK - 1) & 1, p.status));
+      if (!ok) break;
+      convert(kb, 0, w0);
+      // the next item's codes are on their way while these are converted, if it is known
+      Item then = next_item(false);
+      if (then.some) load(then, 0, w0);
+      convert(kb, 1, w1);
       fence_proxy_async_smem();  // the operands are read by the tensor cores
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.k_full(kb));
-      ++kc;
+      if (!then.some) {
+        then = next_item(true);
+        if (then.some) load(then, 0, w0);
+      }
+      now = then;
     }
   } else {
     // ------------------------------------------------------------ weights
@@ -667,8 +708,17 @@ cudaError_t launch_t(const WeightsParams& p, const Geometry& geo, int num_sms, c
   if (e == cudaSuccess && kVec) e = launch_cache_classify(p.f, geo, s);
   if (e != cudaSuccess) return e;
   const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
-  cache_weights_rows_kernel<D, kVec><<<grid, kThreads, Layout<D>::kBytes, s>>>(p, geo, RT);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_weights_rows_kernel<D, kVec>, p, geo, RT);
 }
 
 }  // namespace
