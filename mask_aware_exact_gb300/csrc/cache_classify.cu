@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) cache_classify(const CacheFwdParams 
   __shared__ uint32_t bits[kWordsMost * 8];  // of groups of 4 pages: visible, and << 4 cut
   __shared__ int before[kWordsMost];  // visible pages of this CTA before a word
   __shared__ int count;               // visible pages of this CTA
+  allow_next();
   const int tile = kOne ? blockIdx.x : blockIdx.x / cluster, rank = kOne ? 0 : blockIdx.x - tile * cluster, b = blockIdx.y;
   const int cls = geo.by_RT.div(tile), rt = tile - cls * geo.RT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -2,6 +2,7 @@
 // pages, the cut of the line of pages into runs, waits and conversions.
 #pragma once
 #include "cache.h"
+#include "overlap.cuh"
 #include "ptx_fp8.cuh"
 
 namespace fm {

@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT>, 1)
   }
   auto units = [&](int s) { return line_pages<kVec>(p, geo, s); };
 
+  if (kVec) wait_for_previous();  // its results are the lists of pages
   // this warp's run of the line (neighbouring runs go to different CTAs)
   const int each = (nseg + kThreads - 1) / kThreads;
   const int seg_lo = min(tid * each, nseg), seg_hi = min(seg_lo + each, nseg);
@@ -373,6 +374,9 @@ cudaError_t launch_t(const WeightsParams& p, const Geometry& geo, int num_sms, c
     e = launch_cache_classify(p.f, geo, s);
     if (e != cudaSuccess) return e;
   }
+  if (kVec)
+    return launch_overlapped(cache_weights_kernel<D, NT, kVec>, dim3(static_cast<unsigned>(num_sms)),
+                             32 * kWarps<D, NT>, kSmem<D, NT>, s, p, geo);
   cache_weights_kernel<D, NT, kVec><<<num_sms, 32 * kWarps<D, NT>, kSmem<D, NT>, s>>>(p, geo);
   return cudaGetLastError();
 }

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(256) weights_tiles_kernel(const __grid_constan
   const RowTile r = row_tile(p, geo, b, 0, false);
   const int rows = geo.G * r.live;
   if (tile * kTileRows >= rows) return;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  allow_next();
   const int u = threadIdx.x % kUnits16, r0 = threadIdx.x / kUnits16;
   uint8_t* dst = wp.tiles + static_cast<size_t>(blockIdx.x) * Layout<D>::kTileBytes;
   float* factors = reinterpret_cast<float*>(dst + D * 256);
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
   }
   // The kernel before (with a mask: the classification) may still run up to here. Its results
   // are the lists of pages with a mask, the row tiles without one.
-  if (kVec) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kVec) wait_for_previous();
   // the line: items of all segments, each `parts` long; this CTA's run
   auto items = [&](int s) { return (line_pages<kVec>(p, geo, s) + 3) >> 2; };
   const int each = (nseg + kThreads - 1) / kThreads;
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_weights_rows_kernel(const _
     int left = run_lo < run_hi ? item_hi - item_lo : 0, item = item_lo;
     int seg = left > 0 ? found[0] : 0, k = left > 0 ? found[1] : 0;
     int piece = 0, tq = 0;
-    if (!kVec) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!kVec) wait_for_previous();
     bool ok = true;
     while (ok && left > 0) {
       int my_seg, my_k, my_n;
@@ -708,17 +708,8 @@ cudaError_t launch_t(const WeightsParams& p, const Geometry& geo, int num_sms, c
   if (e == cudaSuccess && kVec) e = launch_cache_classify(p.f, geo, s);
   if (e != cudaSuccess) return e;
   const int grid = num_sms < kCacheMaxCtas ? num_sms : kCacheMaxCtas;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D>::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_weights_rows_kernel<D, kVec>, p, geo, RT);
+  return launch_overlapped(cache_weights_rows_kernel<D, kVec>, dim3(static_cast<unsigned>(grid)), kThreads,
+                           Layout<D>::kBytes, s, p, geo, RT);
 }
 
 }  // namespace
