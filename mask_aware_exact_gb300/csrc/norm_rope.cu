@@ -17,9 +17,12 @@
 // threads' sums in a fixed order and leaves them in the workspace, and a second kernel
 // adds the CTAs' in order. No atomics: the same call gives the same bits.
 #include <algorithm>
+#include <atomic>
 
 #include "cache.h"
 #include "flashmask.h"
+#include "overlap.cuh"
+#include "ptx.cuh"
 #include "rope_common.cuh"
 
 namespace fm {
@@ -27,6 +30,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeadsMost = 16;
+// Heads in flight per thread, and the bytes of their slots.
+__host__ __device__ constexpr int stages(bool backward) { return backward ? 3 : 4; }
+__host__ __device__ constexpr int slot_bytes(bool backward) { return stages(backward) * (backward ? 4 : 2) * kThreads * 16; }
 
 // The sum of a head's squares beyond which it is taken again of values scaled by 2^-70.
 constexpr float kSquaresMost = 1e38f;
@@ -59,6 +65,16 @@ __device__ __forceinline__ Chunk chunk_at(int c, int d, int rot) {
 // Turns kVec pairs held as two accesses in a row, v[0 .. kVec) and v[kVec .. 2 kVec).
 template <int kVec, bool kInterleaved>
 __device__ __forceinline__ void turn(float* v, const float (&cs)[kVec], const float (&sn)[kVec]) {
+  if constexpr (!kInterleaved && kVec > 1) {
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+      const uint64_t x = f2_make(v[i], v[i + 1]), y = f2_make(v[kVec + i], v[kVec + i + 1]);
+      const uint64_t c = f2_make(cs[i], cs[i + 1]), s = f2_make(sn[i], sn[i + 1]);
+      f2_split(f2_sub(f2_mul(x, c), f2_mul(y, s)), v[i], v[i + 1]);
+      f2_split(f2_fma(x, s, f2_mul(y, c)), v[kVec + i], v[kVec + i + 1]);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int a = kInterleaved ? 2 * i : i, b = kInterleaved ? 2 * i + 1 : kVec + i;
@@ -89,10 +105,11 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
   using V = Vec<T, kVec>;
   constexpr bool kAsync = sizeof(V) == 16;
   constexpr int kIn = kBackward ? 2 : 1;
-  constexpr int kStages = kBackward ? 3 : 4;  // heads in flight per thread
+  constexpr int kStages = stages(kBackward);  // heads in flight per thread
   constexpr int kOwn = 2 * kVec * kPer;       // elements of a head that a thread has
   static_assert(!kAsync || kPer == 1, "one chunk a thread in the slots");
-  __shared__ V slots[kAsync ? kStages : 1][2 * kIn][kAsync ? kThreads : 1];
+  extern __shared__ __align__(16) uint8_t dynamic_smem[];
+  auto& slots = *reinterpret_cast<V(*)[kStages][2 * kIn][kThreads]>(dynamic_smem);  // (without kAsync there are none)
 
   const int lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1);
   const bool second = static_cast<int>(blockIdx.y) >= groups0;
@@ -117,9 +134,24 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
       w[c * 2 * kVec + i] = x;
     }
   }
-  float dw[kBackward ? kOwn : 1];
+  uint64_t w2[kOwn / 2], dw2[kBackward ? kOwn / 2 : 1];
 #pragma unroll
-  for (int i = 0; i < (kBackward ? kOwn : 1); ++i) dw[i] = 0.f;
+  for (int i = 0; i < kOwn / 2; ++i) {
+    w2[i] = f2_make(w[2 * i], w[2 * i + 1]);
+    if constexpr (kBackward) dw2[i] = f2_make(0.f, 0.f);
+  }
+
+  // what the sines need of each frequency
+  __shared__ __align__(16) uint64_t turns[kNormWidest / 2];
+  __shared__ __align__(16) float factor[kNormWidest / 2];
+  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
+    const double f = p.freqs[i];
+    bool high = false;
+    turns[i] = turns_per_position(f, high);
+    if (high && !(fabs(f) < 4.)) turns[i] = turns_of_high(f);
+    factor[i] = fabs(f) < kFreqLimit ? p.mscale : __int_as_float(0x7fffffff);
+  }
+  __syncthreads();
 
   for (int tile = blockIdx.x; static_cast<long long>(tile) * tile_tokens < tokens; tile += gridDim.x) {
     const long long token_wide = static_cast<long long>(tile) * tile_tokens + (threadIdx.x >> lanes_log2);
@@ -157,11 +189,12 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
       if (ck[c].rotated) {
         const int first = lane + c * lanes;
         // interleaved: the first access holds pairs e0 / 2 .., the second pairs e1 / 2 ..
-        auto freq = [&](int i) {
-          return p.freqs[!kInterleaved || kVec == 1 ? kVec * first + i
-                                                    : (i < kVec / 2 ? ck[c].e0 : ck[c].e1 - kVec) / 2 + i];
-        };
-        sines_of(pos, p.mscale, kBackward, freq, cs[c], sn[c]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const int pair = !kInterleaved || kVec == 1 ? kVec * first + i
+                                                      : (i < kVec / 2 ? ck[c].e0 : ck[c].e1 - kVec) / 2 + i;
+          sines_at(pos, turns[pair], factor[pair], kBackward, cs[c][i], sn[c][i]);
+        }
       }
     }
 
@@ -201,14 +234,23 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
         for (int c = 0; c < kPer; ++c)
           if (ck[c].rotated) turn<kVec, kInterleaved>(g + 2 * kVec * c, cs[c], sn[c]);
       }
+      // from here on two elements at a time
+      uint64_t x2[kOwn / 2], gw[kBackward ? kOwn / 2 : 1];
+#pragma unroll
+      for (int i = 0; i < kOwn / 2; ++i) {
+        x2[i] = f2_make(x[2 * i], x[2 * i + 1]);
+        if constexpr (kBackward) gw[i] = f2_mul(f2_make(g[2 * i], g[2 * i + 1]), w2[i]);
+      }
       float s1 = 0.f, s2 = 0.f, f = 1.f;
       auto sums = [&]() {
-        s1 = s2 = 0.f;
+        uint64_t a = f2_make(0.f, 0.f), z = a;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          s1 += x[i] * x[i];
-          if constexpr (kBackward) s2 += g[i] * w[i] * x[i];
+        for (int i = 0; i < kOwn / 2; ++i) {
+          a = f2_fma(x2[i], x2[i], a);
+          if constexpr (kBackward) z = f2_fma(gw[i], x2[i], z);
         }
+        s1 = f2_sum(a);
+        s2 = f2_sum(z);
         for (int o = 1; o < lanes; o <<= 1) {
           s1 += __shfl_xor_sync(0xffffffffu, s1, o);
           if constexpr (kBackward) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
@@ -218,26 +260,28 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
       if (__builtin_expect(__any_sync(0xffffffffu, !(s1 <= kSquaresMost)), 0)) {
         f = s1 <= kSquaresMost ? 1.f : 0x1p-70f;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) x[i] *= f;
+        for (int i = 0; i < kOwn / 2; ++i) x2[i] = f2_mul(x2[i], f2_make(f, f));
         sums();
       }
       // r f of the definition is that of the values as they are
       const float r = rsqrtf(s1 * inv_d + p.eps * f * f);
       float y[kOwn];
       if constexpr (!kBackward) {
+        const uint64_t r2 = f2_make(r, r);
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) y[i] = x[i] * r * w[i];
+        for (int i = 0; i < kOwn / 2; ++i) f2_split(f2_mul(f2_mul(x2[i], r2), w2[i]), y[2 * i], y[2 * i + 1]);
 #pragma unroll
         for (int c = 0; c < kPer; ++c) {
           if (ck[c].rotated) turn<kVec, kInterleaved>(y + 2 * kVec * c, cs[c], sn[c]);
         }
       } else {
-        const float along = r * s2 * inv_d, rf = r * f;
+        const float rf = r * f, along = -rf * (r * s2 * inv_d);
+        const uint64_t r2 = f2_make(r, r), rf2 = f2_make(rf, rf), along2 = f2_make(along, along);
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const float u = x[i] * r;
-          dw[i] += g[i] * u;
-          y[i] = rf * (g[i] * w[i] - u * along);
+        for (int i = 0; i < kOwn / 2; ++i) {
+          const uint64_t u = f2_mul(x2[i], r2);
+          dw2[i] = f2_fma(f2_make(g[2 * i], g[2 * i + 1]), u, dw2[i]);
+          f2_split(f2_fma(u, along2, f2_mul(gw[i], rf2)), y[2 * i], y[2 * i + 1]);
         }
       }
       if (live) {
@@ -256,14 +300,18 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
   }
 
   if constexpr (kBackward) {
+    allow_next();
     if (t.dw == nullptr) return;
     // the CTA's sums: tokens of a warp by shuffles, then the warps in order
     constexpr int kWarps = kThreads / 32;
     __shared__ float sums_small[kAsync ? 1 : kWarps][kAsync ? 1 : kNormWidest];
-    float* sums = kAsync ? reinterpret_cast<float*>(slots) : &sums_small[0][0];
-    static_assert(!kAsync || sizeof(slots) >= kWarps * kNormWidest * sizeof(float), "sums fit the slots");
+    float* sums = kAsync ? reinterpret_cast<float*>(dynamic_smem) : &sums_small[0][0];
+    static_assert(!kAsync || slot_bytes(true) >= kWarps * kNormWidest * sizeof(float), "sums fit the slots");
     __syncthreads();
     const int warp = threadIdx.x >> 5;
+    float dw[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn / 2; ++i) f2_split(dw2[i], dw[2 * i], dw[2 * i + 1]);
 #pragma unroll
     for (int c = 0; c < kPer; ++c) {
 #pragma unroll
@@ -290,6 +338,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024) norm_weights_kernel(const NormParams p, const int rows_x, const int groups0,
                                                            const int groups1) {
   __shared__ float sums[32][33];
+  wait_for_previous();
   const NormTensor& t = p.t[blockIdx.y];
   if (t.dw == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -314,6 +363,27 @@ __global__ void __launch_bounds__(1024) norm_weights_kernel(const NormParams p, 
   }
 }
 
+template <typename T, int kVec, int kPer>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done[4];  // devices whose kernels have their shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev > 255) return cudaErrorInvalidDevice;
+  if (done[dev >> 6].load(std::memory_order_relaxed) >> (dev & 63) & 1) return cudaSuccess;
+  for (auto* k : {norm_rope_kernel<T, kVec, kPer, true, true>, norm_rope_kernel<T, kVec, kPer, false, true>}) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  done[dev >> 6].fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+// CTAs of a group of heads in the backward pass.
+long long backward_blocks(long long tiles, long long want, long long groups) {
+  return std::max(1LL, std::min({tiles, want / groups, kNormPartials / groups}));
+}
+
 template <typename T, int kVec, int kPer, bool kBackward>
 cudaError_t launch_t(const NormParams& p, int num_sms, cudaStream_t s) {
   const int chunks = p.rot / 2 / kVec + (p.d - p.rot + 2 * kVec - 1) / (2 * kVec);
@@ -324,26 +394,44 @@ cudaError_t launch_t(const NormParams& p, int num_sms, cudaStream_t s) {
   const int tile = kThreads >> lanes_log2;
   const long long tiles = (static_cast<long long>(p.B) * p.N + tile - 1) / tile;
   const int H = p.t[0].H + p.t[1].H;
-  // Heads per thread: as many as leave all SMs full, at most kHeadsMost.
   const long long want = (kBackward ? 2LL : 3LL) * num_sms;
-  int each = static_cast<int>(std::min<long long>(kHeadsMost, std::max(1LL, H * tiles / want)));
-  if (kBackward) each = std::max(each, (H + kNormPartials / 2 - 1) / (kNormPartials / 2));
+  int each;  // heads per thread
+  if constexpr (kBackward) {
+    // All CTAs run at once, each over its share of the tiles: the heads that give the
+    // shortest longest share, a tile's sines counted as one head more. (32 + 8 heads of 1024
+    // tiles: 16 at a time leave the CTAs of the last 8 waiting, 185 us; 8 at a time 169, 4 at a time 190.)
+    const int least = (H + kNormPartials / 2 - 1) / (kNormPartials / 2);
+    long long best = 0;
+    each = least;
+    for (int e = std::max(1, least); e <= std::max(kHeadsMost, least); ++e) {
+      const long long g = (p.t[0].H + e - 1) / e + (p.t[1].H + e - 1) / e;
+      const long long share = (tiles - 1) / backward_blocks(tiles, want, g) + 1;
+      if (best == 0 || share * (e + 1) < best) best = share * (e + 1), each = e;
+    }
+  } else {
+    // as many as leave all SMs full, at most kHeadsMost
+    each = static_cast<int>(std::min<long long>(kHeadsMost, std::max(1LL, H * tiles / want)));
+  }
   const int groups0 = (p.t[0].H + each - 1) / each, groups1 = (p.t[1].H + each - 1) / each;
   const int groups = groups0 + groups1;
   if (groups > 65535) return cudaErrorInvalidValue;
   long long blocks = tiles;
-  if (kBackward) blocks = std::max(1LL, std::min({tiles, want / groups, static_cast<long long>(kNormPartials) / groups}));
+  if (kBackward) blocks = backward_blocks(tiles, want, groups);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
-  if (p.interleaved)
-    norm_rope_kernel<T, kVec, kPer, true, kBackward><<<grid, kThreads, 0, s>>>(p, each, groups0, lanes_log2);
-  else
-    norm_rope_kernel<T, kVec, kPer, false, kBackward><<<grid, kThreads, 0, s>>>(p, each, groups0, lanes_log2);
-  if (kBackward && (p.t[0].dw != nullptr || p.t[1].dw != nullptr)) {
-    const cudaError_t e = cudaGetLastError();
+  constexpr int kSmem = kVec > 1 ? slot_bytes(kBackward) : 0;
+  auto* kernel = p.interleaved ? norm_rope_kernel<T, kVec, kPer, true, kBackward>
+                               : norm_rope_kernel<T, kVec, kPer, false, kBackward>;
+  if constexpr (kSmem + 2048 > 48 * 1024) {
+    const cudaError_t e = allow_smem<T, kVec, kPer>(kSmem);
     if (e != cudaSuccess) return e;
-    norm_weights_kernel<T><<<dim3((p.d + 31) / 32, p.t[1].H ? 2 : 1), 1024, 0, s>>>(
-        p, static_cast<int>(blocks), groups0, groups1);
+  }
+  kernel<<<grid, kThreads, kSmem, s>>>(p, each, groups0, lanes_log2);
+  if (kBackward && (p.t[0].dw != nullptr || p.t[1].dw != nullptr)) {
+    const cudaError_t st = cudaGetLastError();
+    if (st != cudaSuccess) return st;
+    return launch_overlapped(norm_weights_kernel<T>, dim3((p.d + 31) / 32, p.t[1].H ? 2 : 1), 1024, 0, s, p,
+                             static_cast<int>(blocks), groups0, groups1);
   }
   return cudaGetLastError();
 }

@@ -41,6 +41,16 @@ static __device__ __noinline__ uint64_t turns_of_high(double f) {
   return (u >> 63) ? 0ull - r : r;
 }
 
+// c times cosine and sine (negated for `inverse`) at position pos of `turns` a position.
+__device__ __forceinline__ void sines_at(int pos, uint64_t turns, float c, bool inverse, float& cs, float& sn) {
+  const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
+  // the top 32 bits in units of half turns, in [-1, 1)
+  const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
+  sincospif(half_turns, &sn, &cs);
+  cs *= c;
+  sn *= inverse ? -c : c;
+}
+
 // mscale times cosine and sine (negated for `inverse`) of kVec pairs at position pos;
 // freq(i) is the frequency of pair i.
 template <int kVec, typename F>
@@ -62,13 +72,7 @@ __device__ __forceinline__ void sines_of(int pos, float mscale, bool inverse, F 
   }
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns[i];
-    // the top 32 bits in units of half turns, in [-1, 1)
-    const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    sincospif(half_turns, &sn[i], &cs[i]);
-    const float c = none >> i & 1u ? __int_as_float(0x7fffffff) : mscale;
-    cs[i] *= c;
-    sn[i] *= inverse ? -c : c;
+    sines_at(pos, turns[i], none >> i & 1u ? __int_as_float(0x7fffffff) : mscale, inverse, cs[i], sn[i]);
   }
 }
 
