@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 constexpr int kMoveThreads = 256;
 constexpr int kWindow = kMoveThreads;  // source pages looked at a time
 constexpr int kMinExp = -100;
+constexpr int kAheadKept = 4;
 
 __device__ __forceinline__ uint32_t codes_times(uint32_t w, float f) {
   uint32_t lo, hi;
@@ -647,6 +648,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
       }
       ok = __syncthreads_and(ok);
       if (!ok) return;
+      // V of the next page's source pages on its way to L2 (64 x 8192 tokens cut to a quarter:
+      // 199 -> 186 us; K's kept rows, or whole pages of K, as well: 236, 198). Where a page
+      // keeps fewer than kAheadKept tokens, half of it may be what no slot asks for.
+      if (next < jobs && tid < min(kWindow, m2.pages - m2.s)) {
+        const int kept = __popcll(part.mask), r2 = m2.dp * kPage;
+        if (kept >= kAheadKept && part.before < r2 + m2.cnt && part.before + kept > r2 && part.table >= 0 &&
+            part.table < p.c.pages)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           p.c.v8 + (static_cast<size_t>(part.table) * Hk + m2.hk) * (kPage * D)),
+                       "r"(kPage * D)
+                       : "memory");
+      }
       int to = -1;
       if (m.dp < out_pages) {
         to = out_table[static_cast<size_t>(m.b) * out_pages + m.dp];
