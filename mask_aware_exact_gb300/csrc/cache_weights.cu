@@ -50,7 +50,7 @@ static __device__ __noinline__ uint32_t hidden_step8(const int32_t* s, const int
   return hid;
 }
 
-// A lane's part of a tile of 8 NT rows: the queries as second operands (row 8 t + lane /
+// A lane's part of the 8 NT rows: the queries as second operands (row 8 t + lane /
 // 4, elements 64 half + 16 (lane % 4) .. + 15), and of the rows 8 t + 2 (lane % 4) + e what
 // turns S into weights.
 template <int D, int NT>
@@ -64,14 +64,14 @@ struct Rows {
 
 template <int D, int NT, bool kVec>
 __device__ __forceinline__ void load_rows(const WeightsParams& wp, const Geometry& geo, const RowTile& r, int b,
-                                          int hk, int tile, Rows<D, NT>& o) {
+                                          int hk, Rows<D, NT>& o) {
   const CacheFwdParams& p = wp.f;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rows = geo.G * r.live;
   o.all_lim = r.len;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int rr = tile * 8 * NT + 8 * t + g;
+    const int rr = 8 * t + g;
     const bool live = rr < rows;
     const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
     const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
@@ -114,7 +114,7 @@ __device__ __forceinline__ void load_rows(const WeightsParams& wp, const Geometr
     const float crow = p.scale_log2 * __int_as_float((127 - up) << 23);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int rr2 = tile * 8 * NT + 8 * t + 2 * c + e;
+      const int rr2 = 8 * t + 2 * c + e;
       const bool live2 = rr2 < rows;
       const int tok2 = geo.by_G.div(rr2), h2 = hk * geo.G + rr2 - tok2 * geo.G;
       o.crow[t][e] = __shfl_sync(0xffffffffu, crow, 4 * (2 * c + e));
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT>, 1)
 
   Rows<D, NT> rw;
   RowTile r = {};
-  int cur = -1, cur_tile = -1, start = 0;
+  int cur = -1, start = 0;
   int slot = 0, turn = 0, ahead = 0;  // of the ring; pages fetched that are not done
   bool ok = true;
   Batch now = left > 0 ? next_batch(begin[warp][0], begin[warp][1]) : Batch{};
@@ -233,17 +233,16 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT>, 1)
       const float old[2] = {wt[0], wt[8]};
       if (sg != cur) {
         r = row_tile(p, geo, b, 0, lane == 0);
-        start = wp.start ? min(max(wp.start[b], 0), r.len) : r.shift;
+        start = first_new(wp, b, r);
+        load_rows<D, NT, kVec>(wp, geo, r, b, hk, rw);
+        cur = sg;
       }
-      const int rows = geo.G * r.live, tiles = (rows + 8 * NT - 1) / (8 * NT);
       const bool none = no_scales(kscale, 0.f);
       float sum[4][2] = {};
-      for (int tile = 0; tile < tiles; ++tile) {
-        if (p.mask.causal && r.shift + geo.by_G.div(min(rows, (tile + 1) * 8 * NT) - 1) < j0) continue;
-        if (sg != cur || tile != cur_tile) load_rows<D, NT, kVec>(wp, geo, r, b, hk, tile, rw);
-        cur = sg, cur_tile = tile;
-        ok = __all_sync(0xffffffffu, cache_wait(bar + 8 * slot, turn & 1, p.status));
-        if (!ok) break;
+      ok = __all_sync(0xffffffffu, cache_wait(bar + 8 * slot, turn & 1, p.status));
+      if (!ok) break;
+      // (keys behind the last row's are seen by none)
+      if (r.live > 0 && !(p.mask.causal && r.shift + r.live - 1 < j0)) {
         // instruction u has the keys 16 u + g and 16 u + 8 + g of this lane; halves of a row in
         // another order for odd keys, so that the eight lanes of a phase are in different banks
         const uint8_t* src = ring + slot * kPage * D + g * D + 16 * c;
@@ -316,10 +315,6 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT>, 1)
             }
         }
       }
-      if (!ok) break;
-      // (a page that no tile of rows sees has to have arrived, too)
-      ok = __all_sync(0xffffffffu, cache_wait(bar + 8 * slot, turn & 1, p.status));
-      if (!ok) break;
       __syncwarp();
       // a page more, of this batch or the next
       for (--ahead; ahead < kRing; ++ahead) {
