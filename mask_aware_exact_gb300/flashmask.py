@@ -1037,7 +1037,8 @@ def flashmask_cache_evict(cache: KVCache, page_table, lens, weights, keep, ws, s
     if isinstance(keep, torch.Tensor):
         keep_ptr = _per_sequence(keep, "keep", B, index_dev)
     else:
-        budget = int(keep)
+        budget = max(min(int(keep), 0x7fffffff), -1)
+    most = [max(min(int(x), 0x7fffffff), -1) for x in (sink, recent)]  # (ctypes drops bits past 32)
     out_ptr, out_pages = None, 0
     if out_table is not None:
         out_pages = _page_table(out_table, B, index_dev)
@@ -1057,7 +1058,7 @@ def flashmask_cache_evict(cache: KVCache, page_table, lens, weights, keep, ws, s
     def call(raw):
         out = torch.empty((B,), dtype=torch.int32, device=lens.device) if new_lens is None else new_lens
         code = load().flashmask_cache_evict(c, page_table.data_ptr(), max_pages, out_ptr, out_pages, ln,
-                                            weights.data_ptr(), keep_ptr, budget, int(sink), int(recent),
+                                            weights.data_ptr(), keep_ptr, budget, *most,
                                             out.data_ptr(), index_ptr, width, B, ws.data_ptr(), ws_bytes, raw)
         if code:
             raise FlashMaskError(code, "flashmask_cache_evict")

@@ -194,6 +194,54 @@ def test_budget_for_all_and_a_larger_workspace():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("apart", [False, True])
+def test_pages_past_four_gigabytes(apart):
+    fm = need_gpu()
+    far, lens, keep = 70000, [500, 333], [200, 333]  # 64 KB of K a page
+    cache, table, out_table, w, _ = make(fm, lens, 8, 128, out=keep if apart else None)
+    ws = fm.alloc_cache_evict_workspace(2, 8, table.shape[1])
+    n = cache.k8.shape[0]
+    big = fm.KVCache.empty(far + n, 8, 128)
+    wide = torch.zeros((far + n, 8, PAGE), device="cuda")
+    for x, y in zip((*big.tensors, wide), (*cache.tensors, w)):
+        x[far:].view(torch.uint8).copy_(y.view(torch.uint8))
+    move = lambda t: None if t is None else torch.where((t >= 0) & (t < n), t + far, t)
+    fm.flashmask_cache_evict(cache, table, ints(lens), w, ints(keep), ws, sink=3, recent=9, out_table=out_table)
+    ln = ints(lens)
+    new = fm.flashmask_cache_evict(big, move(table), ln, wide, ints(keep), ws, sink=3, recent=9,
+                                   out_table=move(out_table), new_lens=ln)
+    assert new is ln and new.tolist() == keep and fm.flashmask_check_status(ws) == (fm.FM_OK, 0)
+    for x, y in zip((*big.tensors, wide), (*cache.tensors, w)):
+        assert torch.equal(x[far:].view(torch.uint8), y.view(torch.uint8))
+    assert not wide[:far].any()
+
+
+@pytest.mark.gpu
+def test_an_index_of_no_width_and_sizes_past_32_bits():
+    fm = need_gpu()
+    lens = [300, 64]
+    a = check(fm, lens, [100, 64], width=0, sink=5, recent=7)
+    cache, table, _, w, _ = make(fm, lens, 2, 64)
+    ws = fm.alloc_cache_evict_workspace(2, 2, table.shape[1])
+    new = fm.flashmask_cache_evict(cache, table, ints(lens), w, ints([100, 64]), ws, sink=5, recent=7)
+    assert new.tolist() == [100, 64] and torch.equal(w, a[2])
+    # more than all of it, whatever the number
+    for keep, kw in ((2 ** 32 + 5, {}), (50, dict(sink=2 ** 32 + 1)), (50, dict(recent=2 ** 40))):
+        cache, table, _, w, _ = make(fm, lens, 2, 64)
+        old = w.clone()
+        new = fm.flashmask_cache_evict(cache, table, ints(lens), w, keep, ws, **kw)
+        assert new.tolist() == [min(n, keep) for n in lens]
+        if keep > 300:
+            assert torch.equal(w, old)
+        else:
+            first = table[0, 0].long()
+            got = w[first, :, :50]
+            pages = table[0, :5].long()
+            line = old[pages].transpose(0, 1).flatten(1)[:, :300]
+            assert torch.equal(got, line[:, :50] if "sink" in kw else line[:, -50:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [False, True])
 def test_streams_and_graphs(apart):
     fm = need_gpu()
     lens, keep = [900, 400, 77], [500, 399, 10]
