@@ -243,6 +243,120 @@ def test_bad_pages_are_left_out():
     assert torch.equal(fm.flashmask_cache_weights(q, cache, table, ints(lens), lse, w.clone(), ws), good)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [None, "window_prefix", "documents", "random", "random_kv", "random_head"])
+@pytest.mark.parametrize("H,Hk,N,d", [(8, 2, 300, 64), (3, 3, 260, 128), (33, 1, 1, 128)])
+def test_many_rows(kind, H, Hk, N, d):
+    # few keys for all CTAs: a group of pages is shared out by its rows
+    fm = need_gpu()
+    lens = [N, 1500 + N, 640]
+    q, cache, table, gen = make(fm, 3, H, Hk, N, d, lens, seed=4)
+    q_lens = [N, N, max(N - 135, 1)]
+    mask = None if kind is None else mask_of(kind, 3, H, Hk, N, table.shape[1] * PAGE, gen, fm)
+    check(fm, q, cache, table, lens, q_lens, mask)
+    check(fm, q, cache, table, lens, q_lens, mask, start=[0, 70, 600])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [None, "window"])
+@pytest.mark.parametrize("Hk,N", [(4, 1), (4, 11), (2, 35)])
+def test_many_sequences(kind, Hk, N):
+    # more segments than a CTA has threads, most of them short, some without keys
+    fm = need_gpu()
+    B, d = 300, 64
+    gen = torch.Generator().manual_seed(N)
+    lens = (torch.randint(0, 130, (B,), generator=gen) * torch.randint(0, 2, (B,), generator=gen)).tolist()
+    q_lens = [min(n, N) for n in lens]
+    q, cache, table, gen = make(fm, B, Hk, Hk, N, d, lens, seed=N)
+    mask = None if kind is None else mask_of(kind, B, Hk, Hk, N, table.shape[1] * PAGE, gen, fm)
+    check(fm, q, cache, table, lens, q_lens, mask)
+    check(fm, q, cache, table, [0] * B, [0] * B, mask)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 30])
+def test_masked_on_streams_and_in_graphs(N):
+    # the kernel starts beside the classification and must not read its lists too early:
+    # calls whose masks differ follow one another without a pause
+    fm = need_gpu()
+    H, Hk, d = 8, 2, 64
+    lens = [5000, 9000]
+    q, cache, table, gen = make(fm, 2, H, Hk, N, d, lens)
+    masks = [mask_of(k, 2, H, Hk, N, table.shape[1] * PAGE, gen, fm) for k in ("window", "random", "nothing", "documents")]
+    lse = [forward(fm, q, cache, table, lens, None, m) for m in masks]
+    ws = fm.alloc_cache_weights_workspace(2, H, Hk, N, d, table.shape[1])
+    ln, w0 = ints(lens), torch.rand((cache.k8.shape[0], Hk, PAGE), device="cuda")
+    call = lambda i, w, **kw: fm.flashmask_cache_weights(q, cache, table, ln, lse[i], w, ws, mask=masks[i], **kw)
+    want = []
+    for i in range(4):
+        want.append(call(i, w0.clone()))
+        torch.cuda.synchronize()
+    outs = [w0.clone() for _ in range(40)]
+    for i, w in enumerate(outs):
+        call(i % 4, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    more = [w0.clone() for _ in range(4)]
+    s.wait_stream(torch.cuda.current_stream())
+    for i, w in enumerate(more):
+        call(i, w, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    g, held = torch.cuda.CUDAGraph(), [w0.clone() for _ in range(4)]
+    with torch.cuda.graph(g):
+        for i, w in enumerate(held):
+            call(i, w)
+    g.replay()
+    for i in range(4):
+        assert all(torch.equal(w, want[i]) for w in (*outs[i::4], more[i], held[i]))
+    assert fm.flashmask_check_status(ws) == (fm.FM_OK, 0)
+
+
+@pytest.mark.gpu
+def test_bad_pages_are_left_out_with_many_rows():
+    fm = need_gpu()
+    H, Hk, N, d = 4, 2, 40, 64
+    lens = [200, 130]
+    q, cache, table, _ = make(fm, 2, H, Hk, N, d, lens)
+    ws = fm.alloc_cache_weights_workspace(2, H, Hk, N, d, table.shape[1])
+    lse = forward(fm, q, cache, table, lens, None, None)
+    w = torch.rand((cache.k8.shape[0], Hk, PAGE), device="cuda")
+    good = fm.flashmask_cache_weights(q, cache, table, ints(lens), lse, w.clone(), ws)
+    for bad in (-1, cache.k8.shape[0], 2 ** 31 - 1, -2 ** 31):
+        t = table.clone()
+        t[0, 1] = bad
+        got = fm.flashmask_cache_weights(q, cache, t, ints(lens), lse, w.clone(), ws)
+        assert fm.flashmask_check_status(ws)[0] == fm.FM_ERR_PAGE
+        for p in [*table[1, :3].tolist(), int(table[0, 0]), int(table[0, 2])]:
+            assert torch.equal(got[p], good[p])
+        assert torch.equal(got[int(table[0, 1])], w[int(table[0, 1])])
+    for n in (-1, table.shape[1] * PAGE + 1):
+        fm.flashmask_cache_weights(q, cache, table.clamp(max=cache.k8.shape[0] - 1), ints([n, 130]), lse, w.clone(), ws)
+        assert fm.flashmask_check_status(ws)[0] == fm.FM_ERR_PAGE
+    assert torch.equal(fm.flashmask_cache_weights(q, cache, table, ints(lens), lse, w.clone(), ws), good)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 30])
+def test_pages_past_four_gigabytes(N):
+    fm = need_gpu()
+    H, Hk, d, far = 8, 8, 128, 70000  # 64 KB of K a page
+    lens = [150, 333]
+    q, cache, table, _ = make(fm, 2, H, Hk, N, d, lens)
+    lse = forward(fm, q, cache, table, lens, None, None)
+    ws = fm.alloc_cache_weights_workspace(2, H, Hk, N, d, table.shape[1])
+    n = cache.k8.shape[0]
+    w = torch.rand((n, Hk, PAGE), device="cuda")
+    big = fm.KVCache.empty(far + n, Hk, d)
+    for x, y in zip(big.tensors, cache.tensors):
+        x[far:].view(torch.uint8).copy_(y.view(torch.uint8))
+    wide = torch.zeros((far + n, Hk, PAGE), device="cuda")
+    wide[far:] = w
+    fm.flashmask_cache_weights(q, cache, table, ints(lens), lse, w, ws)
+    fm.flashmask_cache_weights(q, big, torch.where(table < n, table + far, table), ints(lens), lse, wide, ws)
+    assert torch.equal(wide[far:], w) and not wide[:far].any()
+    assert fm.flashmask_check_status(ws) == (fm.FM_OK, 0)
+
+
 @pytest.fixture(scope="module")
 def lib():
     from mask_aware_exact_gb300 import build
