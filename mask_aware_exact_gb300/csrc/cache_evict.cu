@@ -16,6 +16,14 @@
 // pages, none behind it. Pages are taken in order from a counter, each CTA reads all of
 // its page's tokens first and says so; before it writes it waits for the one or two pages
 // that read from it, which were taken before and wait for nothing until they have read.
+//
+// Measured (whole calls, L2 flushed): 64 sequences up to 8192 of 8 heads of 128 cut to a
+// quarter, in place, 186 us: 26 for the first kernel (latency: barriers and the weights' way in;
+// its histograms stay in shared memory) and 158 for the second (705 MB, 4.5 TB/s, 66 % of a
+// copy: the kept bytes of V lie apart, so that its source pages are read whole). Two
+// sequences of 131072 cut to an eighth, into other pages, 112 us: 40 and 68 (361 MB, 5.3 TB/s). A
+// page to be written is a chain of look-ups, loads, largest codes and stores behind two or
+// three barriers; four CTAs an SM hide most of it, registers allow no more.
 #include <atomic>
 
 #include "cache_common.cuh"
@@ -28,6 +36,7 @@ namespace {
 constexpr int kClusterMost = 8;
 constexpr int kBins = 2048;
 constexpr int kPagesCached = 256;                                     // of a CTA, with their keys
+constexpr int kPagesFew = 64;
 constexpr int kPagesMost = FM_MAX_SEQLEN / kPage / kClusterMost;      // of a CTA
 
 __device__ __forceinline__ void cluster_sync() {
@@ -819,17 +828,24 @@ EvictWs evict_ws_layout(int B, int Hk, int max_pages) {
 
 cudaError_t launch_cache_evict(int d, EvictParams p, int num_sms, cudaStream_t s) {
   p.by_Hk.set(p.c.Hk);
+  // CTAs of a segment: as many as hold its keys, and more down to kPagesFew pages each while
+  // they leave SMs free (one segment of 16384 tokens, whole call: 29.0 -> 25.6 us; shares of 32
+  // pages take 4000 tokens from 17.6 to 22.8)
   int cluster = 1;
-  while (cluster < kClusterMost && cluster * kPagesCached < p.max_pages) cluster *= 2;
-  // small CTAs where there are several for each SM, which hide one another's barriers
+  while (cluster < kClusterMost &&
+         (cluster * kPagesCached < p.max_pages ||
+          (cluster * kPagesFew < p.max_pages && 2LL * p.B * p.c.Hk * cluster <= num_sms)))
+    cluster *= 2;
+  // CTAs of 256 threads where there are several for each SM, which hide one another's
+  // barriers: 64 x 8 segments of 8192, whole calls, 187 us; of 512, 195. Otherwise of 512: 20 x
+  // 8 segments 86 us (256: 89, 1024: 97), 8 of 16384 31.6 (34.2, 35.2), 16 of 131072 112 (120,
+  // 134: clusters of eight CTAs that fill an SM each do not all find a place at once).
   const bool many = static_cast<long long>(p.B) * p.c.Hk * cluster > 2LL * num_sms;
   cudaError_t e;
   if (cluster * kPagesCached < p.max_pages)
     e = launch_select<1024, false>(p, cluster, s);
   else
-    // (clusters of eight CTAs that fill an SM each do not all find a place at once)
-    e = many ? launch_select<256, true>(p, cluster, s)
-             : cluster > 1 ? launch_select<512, true>(p, cluster, s) : launch_select<1024, true>(p, cluster, s);
+    e = many ? launch_select<256, true>(p, cluster, s) : launch_select<512, true>(p, cluster, s);
   if (e != cudaSuccess) return e;
   return d == 64 ? launch_move<64>(p, num_sms, s) : launch_move<128>(p, num_sms, s);
 }
