@@ -505,7 +505,8 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
  *   ws: flashmask_cache_weights_workspace_bytes(...) bytes, 256-byte aligned and zeroed
  *   before its first use; not to be shared by calls that may run at the same time; one
  *   workspace serves all sizes that it is large enough for. Zero it again after another
- *   entry point has used it. Its first 16 bytes are the status word.
+ *   entry point has used it and after FM_ERR_TIMEOUT or FM_ERR_CUDA. Its first 16 bytes are
+ *   the status word.
  * Scores, exponentials and sums are fp32 and a key's sum has a fixed order: the same call
  * gives the same bits. Asynchronous on `stream`. */
 size_t flashmask_cache_weights_workspace_bytes(int B, int H, int Hk, int N, int d, int max_pages);
@@ -542,7 +543,8 @@ fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_c
  *   ws: flashmask_cache_evict_workspace_bytes(...) bytes, 256-byte aligned and zeroed
  *   before its first use; not to be shared by calls that may run at the same time; one
  *   workspace serves all sizes that it is large enough for. Zero it again after another
- *   entry point has used it or after FM_ERR_TIMEOUT. Its first 16 bytes are the status word.
+ *   entry point has used it and after FM_ERR_TIMEOUT or FM_ERR_CUDA. Its first 16 bytes are
+ *   the status word.
  *   A page or length out of range, or n > 64 * out_pages, is recorded (see
  *   flashmask_check_status) and the access left out.
  * Limits as for flashmask_cache_append; out_pages <= FM_MAX_SEQLEN / FM_PAGE. The same call gives

@@ -9,6 +9,18 @@
 // one for each warp. With a column-wise mask the line has only the pages that some row
 // sees (the attention's classification, all rows as one tile). A warp brings its pages in
 // by bulk copies, kSlots ahead, into slots of its own: no warp waits for another.
+//
+// Up to 32 rows, as 1, 2 or 4 groups of 8 (kWeightsMany says why not more). K is read
+// once: 8 rows are bound by HBM, 32 by instructions (600 a page of d = 64) and their
+// latencies, with two warps a scheduler: registers allow no more (9, 10 warps: 33, 31 us for
+// the drafted tokens below, 28 with 8). Measured, calls with L2 flushed: 64 sequences up to 8192,
+// 32 / 8 heads of 128: 63 us (342 MB, 5.4 TB/s); 8 sequences of 131072, window of 4096 and
+// prefix of 2048, 8 / 8 heads: 25 us, 9 of them the classification of 131072 columns; 16
+// sequences up to 16384, 4 tokens, 32 / 4 heads of 64: 28 us (42 MB); one sequence of 1000:
+// 5.9 us on the GPU. 16 sequences of 16384, 4 heads, by rows (us; L2 warm):
+//   rows        4      8     16     24     32
+//   d = 64    14.6   14.7   16.8   23.1   23.1
+//   d = 128   16.8   16.9   22.3   29.3   30.5
 #include <atomic>
 
 #include "cache_weights.cuh"
@@ -17,10 +29,12 @@
 namespace fm {
 namespace {
 
-// Warps of a CTA: as many as registers allow, 12 or 8.
+// Warps of a CTA: as many as registers allow, 12 or 8 (16 of 128 registers for 8 rows: 63.0 us
+// for the 64 sequences, 63.7 with 12, but 26.8 for the window where 12 take 25.2).
 template <int D, int NT>
 constexpr int kWarps = NT == 1 || (NT == 2 && D == 64) ? 12 : 8;
-// Pages of a warp on their way or being read.
+// Pages of a warp on their way or being read. (A third less: 64.3 us for the 64 sequences, 63.7
+// so; the drafted tokens 27.0, 28.0 so.)
 template <int D, int NT>
 constexpr int kSlots = (D == 128 ? 24 : 48) / kWarps<D, NT>;
 template <int D, int NT>

@@ -12,13 +12,30 @@
 // (S * K scale) * factor - LSE, weight 2^x; a row's factor and LSE come from shared memory,
 // the factor only where the rows of a tile differ in it (see the row tiles).
 //
+// K's codes are loaded an item ahead and converted while the products of the item before
+// run, into the other of two pairs of operands. The main kernel starts while the row tiles
+// are still being written and finds its run meanwhile (238 -> 230 us for the prompt below).
+//
+// Measured: the last 512 rows of 2 prompts up to 32768, 32 / 8 heads of 128 (2.7e11
+// operations, 2.1e9 exponentials): 218 us, 1240 TFLOP/s, 65 % of the measured bf16 rate. The
+// tensor cores are busy for 51 % of the cycles and the exponential unit, which gives 26 a
+// cycle and SM, would need 145 us; what is left is the two warps a scheduler of the weights,
+// each load of a tile, its 64 x 2 exponentials and their sums one chain. Not kept: P's
+// warps with two keys a thread and tiles of 96 rows, 16 weights warps, keys in TMEM as the
+// first operand, units of 64 rows (a product of 128 x 64 takes 45 cycles, ideally 32).
+// 16 sequences of 16384, 4 heads, by rows (us; L2 warm), with the kernel for few rows beside
+// it where that takes them:
+//   rows            24           32        40     64    128
+//   d = 64    29.1 / 23.1  29.2 / 23.1   29.1   29.1   35.5
+//   d = 128   37.7 / 29.3  37.7 / 30.5   37.6   38.2   41.5
+//
 // Items are cut into `parts` ranges of rows where there are few of them, on one line with
 // equal runs for the CTAs; the pieces of an item that a run's border cuts leave their
 // sums in the workspace, and the last to arrive adds them in order.
 //
 // Warp roles (480 threads):
 //   0-7    weights: warpgroup w has operand w, a key a thread
-//   8-11   conversion of K, one key of each operand a thread
+//   8-11   conversion of K, 32 keys of each operand a warp
 //   12     walks the run, looks pages up, brings row tiles in
 //   13, 14 issue the products of an operand each: what one thread does between the products
 //          of two tiles (waits, commits) takes longer than the tensor cores have work queued
@@ -36,11 +53,11 @@ constexpr int kMetaRing = 4;
 constexpr int kMetaInts = 32;
 constexpr int kKeys = 256;
 constexpr int kTileRows = 128;
-constexpr int kPartsRun = 32;
+constexpr int kPartsRun = 32;  // (2 prompts up to 32768: 222 us; with 8 229, with 128 224)
 constexpr int kHalf = 64;  // rows taken at a time
 constexpr int kFactorRing = 8;       // of the row tiles' factors
 constexpr int kFactorBytes = 1024;
-constexpr uint32_t kNear = 8;
+constexpr uint32_t kNear = 8;  // (factors of their own for all rows: 521 us for the same prompts)
 constexpr int kScanWords = kThreads / 32 + 4;
 
 enum MetaWord { kFlags, kSeg, kTile0, kTiles, kCta0, kPieces, kLen, kLive, kPg = 8, kJ0 = 12, kKs = 16, kCutWord = 20 };
