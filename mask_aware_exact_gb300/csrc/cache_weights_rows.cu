@@ -17,11 +17,11 @@
 // are still being written and finds its run meanwhile (238 -> 230 us for the prompt below).
 //
 // Measured: the last 512 rows of 2 prompts up to 32768, 32 / 8 heads of 128 (2.7e11
-// operations, 2.1e9 exponentials): 218 us, 1240 TFLOP/s, 65 % of the measured bf16 rate. The
+// operations, 1.05e9 exponentials): 218 us, 1240 TFLOP/s, 65 % of the measured bf16 rate. The
 // tensor cores are busy for 51 % of the cycles and the exponential unit, which gives 26 a
 // cycle and SM, would need 145 us; what is left is the two warps a scheduler of the weights,
-// each load of a tile, its 64 x 2 exponentials and their sums one chain. Not kept: P's
-// warps with two keys a thread and tiles of 96 rows, 16 weights warps, keys in TMEM as the
+// each load of a tile, its 64 x 2 exponentials and their sums one chain. Not kept: weights'
+// warps with two keys a thread and tiles of 96 rows, 16 of them, keys in TMEM as the
 // first operand, units of 64 rows (a product of 128 x 64 takes 45 cycles, ideally 32).
 // 16 sequences of 16384, 4 heads, by rows (us; L2 warm), with the kernel for few rows beside
 // it where that takes them:
