@@ -98,10 +98,8 @@ struct SelectSmem {
   int hist[2][kBins];
   int wsum[32 + 4];
   int found[2];   // bin, keys wanted of it
-  int totals[2];  // keys equal to the last one, tokens kept, of this CTA
+  int totals[2];  // of this CTA: keys equal to the last one, tokens kept beside these
   int place;      // of the segment's pages in the list of pages to be written (rank 0)
-  int sums[kBins / 2];        // cluster: of this CTA's bins, and
-  int ranges[kClusterMost];   // of all CTAs' bins
 };
 
 // `most`: pages of a CTA that there is shared memory for.
@@ -114,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
   uint64_t* equals = masks + most;
   int* counts = reinterpret_cast<int*>(equals + most);
   uint32_t* keys = reinterpret_cast<uint32_t*>(counts + most);  // kCached
+  int* sums = reinterpret_cast<int*>(keys) + (kCached ? most * kPage : 0);  // of a cluster: the bins of all CTAs
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x / cluster, rank = blockIdx.x - seg * cluster;
   const int b = seg / p.c.Hk, hk = seg - b * p.c.Hk;
@@ -193,64 +192,45 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
           if (j >= kp.lo && j < kp.hi && (k[x] & known) == prefix) atomicAdd(&hist[k[x] >> shift & (bins - 1)], 1);
         }
       }
+      const int* bin = hist;
       if (cluster == 1) {
         __syncthreads();
-        // this thread's bins, from the top
-        constexpr int kMine = kBins / kThreads;
-        int c[kMine], sum = 0;
-        const int top = bins - 1 - kMine * tid;
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-          c[x] = top < x ? 0 : hist[top - x];
-          sum += c[x];
-        }
-        int all;
-        int above = block_before<kWarps>(sum, sh.wsum, all);
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-          if (above < want && want <= above + c[x]) {
-            sh.found[0] = top - x;
-            sh.found[1] = want - above;
-          }
-          above += c[x];
-        }
-        __syncthreads();
       } else {
-        // each CTA adds up its share of the bins, the first the highest (a cluster's CTAs that
-        // all read all bins of one another took 20000 cycles a pass)
+        // each CTA adds up its share of the bins for all (a cluster's CTAs that all read all bins
+        // of one another took 20000 cycles a pass)
+        bin = sums;
         cluster_sync();
-        const int share = bins / cluster, base = bins - (rank + 1) * share;
-        for (int i = tid; i < share; i += kThreads) sh.sums[i] = of_ctas(&hist[base + i], cluster);
-        __syncthreads();
-        constexpr int kMine = (kBins / 2 + kThreads - 1) / kThreads;
-        int c[kMine], sum = 0;
-        const int top = share - 1 - kMine * tid;
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-          c[x] = top < x ? 0 : sh.sums[top - x];
-          sum += c[x];
-        }
-        int all;
-        int above = block_before<kWarps>(sum, sh.wsum, all);
-        if (tid < cluster) to_cta(&sh.ranges[rank], tid, all);
-        cluster_sync();
-        for (int r = 0; r < rank; ++r) above += sh.ranges[r];
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-          if (above < want && want <= above + c[x]) {
-            for (int r = 0; r < cluster; ++r) {
-              to_cta(&sh.found[0], r, base + top - x);
-              to_cta(&sh.found[1], r, want - above);
-            }
-          }
-          above += c[x];
+        const int share = bins / cluster;
+        for (int i = rank * share + tid; i < (rank + 1) * share; i += kThreads) {
+          const int v = of_ctas(&hist[i], cluster);
+          for (int r = 0; r < cluster; ++r) to_cta(&sums[i], r, v);
         }
         cluster_sync();
       }
+      // this thread's bins, from the top
+      constexpr int kMine = kBins / kThreads;
+      int c[kMine], sum = 0;
+      const int top = bins - 1 - kMine * tid;
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        c[x] = top < x ? 0 : bin[top - x];
+        sum += c[x];
+      }
+      int all;
+      int above = block_before<kWarps>(sum, sh.wsum, all);
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        if (above < want && want <= above + c[x]) {
+          sh.found[0] = top - x;
+          sh.found[1] = want - above;
+        }
+        above += c[x];
+      }
+      __syncthreads();
       prefix |= static_cast<uint32_t>(sh.found[0]) << shift;
       known |= static_cast<uint32_t>(bins - 1) << shift;
       want = sh.found[1];
-      if (cluster == 1) __syncthreads();
+      __syncthreads();
     }
     last = prefix;
     equal = want;
@@ -273,36 +253,29 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     }
   }
   __syncthreads();
-  // a thread's pages in a row: sums before them, of this CTA and of those before it
+  // a thread's pages in a row: what is equal and what is kept beside it before them, in this
+  // CTA and in those before it. Of the equal ones the lowest positions stay.
   const int per = (np + kThreads - 1) / kThreads, i0 = min(tid * per, np), i1 = min(i0 + per, np);
-  auto sums_before = [&](int mine, int which) {
-    int all;
-    int x = block_before<kWarps>(mine, sh.wsum, all);
-    if (cluster > 1) {
-      if (tid == 0) sh.totals[which] = all;
-      cluster_sync();
-      x += of_ctas(&sh.totals[which], rank);
-    }
-    return x;
-  };
-  int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += __popcll(equals[i]);
-  int left = equal - sums_before(mine, 0);
-  mine = 0;
-  for (int i = i0; i < i1; ++i) {
-    uint64_t e = equals[i];
-    const int n = __popcll(e);
-    // the lowest positions first
-    for (int drop = n - min(max(left, 0), n); drop > 0; --drop) e &= ~(1ull << (63 - __clzll(static_cast<long long>(e))));
-    left -= n;
-    masks[i] |= e;
-    mine += __popcll(masks[i]);
+  int same_mine = 0, kept_mine = 0, same_all, kept_all;
+  for (int i = i0; i < i1; ++i) same_mine += __popcll(equals[i]), kept_mine += __popcll(masks[i]);
+  int same = block_before<kWarps>(same_mine, sh.wsum, same_all), at = block_before<kWarps>(kept_mine, sh.wsum, kept_all);
+  if (cluster > 1) {
+    if (tid == 0) sh.totals[0] = same_all, sh.totals[1] = kept_all;
+    cluster_sync();
+    same += of_ctas(&sh.totals[0], rank);
+    at += of_ctas(&sh.totals[1], rank);
   }
-  int at = sums_before(mine, 1);
+  at += min(equal, same);
   const size_t row = static_cast<size_t>(seg) * p.max_pages;
   int32_t* before = p.before + static_cast<size_t>(seg) * (p.max_pages + 1);
   const int place = cluster == 1 ? sh.place : of_cta(&sh.place, 0);
   for (int i = i0; i < i1; ++i) {
+    uint64_t e = equals[i];
+    const int some = __popcll(e);
+    for (int drop = some - min(max(equal - same, 0), some); drop > 0; --drop)
+      e &= ~(1ull << (63 - __clzll(static_cast<long long>(e))));
+    same += some;
+    masks[i] |= e;
     const int n = __popcll(masks[i]), to = (at + kPage - 1) / kPage;
     p.mask[row + p0 + i] = masks[i];
     before[p0 + i] = at;
@@ -769,18 +742,20 @@ template <int kThreads, bool kCached>
 cudaError_t launch_select(const EvictParams& p, int cluster, cudaStream_t s) {
   // shared memory for the pages that a CTA may have
   const int most = ((p.max_pages + cluster - 1) / cluster + 1) / 2 * 2;
-  auto bytes = [](int pages) {
-    return static_cast<int>((sizeof(SelectSmem) + 15) / 16 * 16) + pages * (8 + 8 + 4) + (kCached ? pages * kPage * 4 : 0);
+  auto bytes = [](int pages, bool clusters) {
+    return static_cast<int>((sizeof(SelectSmem) + 15) / 16 * 16) + pages * (8 + 8 + 4) + (kCached ? pages * kPage * 4 : 0) +
+           (clusters ? kBins * 4 : 0);
   };
-  static_assert(sizeof(SelectSmem) + kPagesCached * (20 + kPage * 4) <= 227 * 1024 && sizeof(SelectSmem) + kPagesMost * 20 <= 227 * 1024,
+  static_assert(sizeof(SelectSmem) + 16 + kPagesCached * (20 + kPage * 4) + kBins * 4 <= 227 * 1024 &&
+                    sizeof(SelectSmem) + 16 + kPagesMost * 20 + kBins * 4 <= 227 * 1024,
                 "shared memory per CTA");
   static std::atomic<uint64_t> done[4];
-  const cudaError_t e = allow_smem(evict_select_kernel<kThreads, kCached>, bytes(kCached ? kPagesCached : kPagesMost), done);
+  const cudaError_t e = allow_smem(evict_select_kernel<kThreads, kCached>, bytes(kCached ? kPagesCached : kPagesMost, true), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.c.Hk * cluster);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes(most);
+  cfg.dynamicSmemBytes = bytes(most, cluster > 1);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
