@@ -35,7 +35,10 @@ namespace {
 // ---------------------------------------------------------------- selection
 constexpr int kClusterMost = 8;
 constexpr int kBins = 2048;
-constexpr int kPagesCached = 256;                                     // of a CTA, with their keys
+constexpr int kPagesShare = 256;                                      // of a CTA while its cluster may grow
+// whose keys fit its shared memory (8 segments of 131072 in a table of one page more, whole call:
+// 61 us; with the weights read again in each pass 71)
+constexpr int kPagesCached = 704;
 constexpr int kPagesFew = 64;
 constexpr int kPagesMost = FM_MAX_SEQLEN / kPage / kClusterMost;      // of a CTA
 
@@ -808,7 +811,7 @@ cudaError_t launch_cache_evict(int d, EvictParams p, int num_sms, cudaStream_t s
   // pages take 4000 tokens from 17.6 to 22.8)
   int cluster = 1;
   while (cluster < kClusterMost &&
-         (cluster * kPagesCached < p.max_pages ||
+         (cluster * kPagesShare < p.max_pages ||
           (cluster * kPagesFew < p.max_pages && 2LL * p.B * p.c.Hk * cluster <= num_sms)))
     cluster *= 2;
   // CTAs of 256 threads where there are several for each SM, which hide one another's

@@ -104,6 +104,15 @@ def test_clusters(slack, apart):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("slack", [4000, 6000])
+def test_tables_far_wider_than_their_sequences(slack, apart):
+    fm = need_gpu()
+    check(fm, [5000, 0, 64, 1], [1200, 3, 63, 0], Hk=2, slack=slack, sink=5, recent=70, apart=apart, weights="ties")
+    check(fm, [20000], [15000], Hk=1, slack=slack, sink=5, recent=700, apart=apart)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,keep", [(40000, 9000), (150000, 140000)])
 def test_long(n, keep):
     fm = need_gpu()
