@@ -116,3 +116,55 @@ def test_a_training_step_with_normed_heads():
                  np.sqrt(np.mean(f64(x) ** 2, -1, keepdims=True))).sum((0, 1, 2))
         assert np.all(np.abs(f64(gw) - dw) <= terms * 2.0 ** -14)
     assert fm.flashmask_check_status(ws) == (fm.FM_OK, 0)
+
+
+@pytest.mark.gpu
+def test_two_servers_at_once():
+    # the same calls on two streams, each with workspaces of its own, give what they give
+    # one after the other
+    fm = need_gpu()
+    H, Hk, d, N, lens, keep = 8, 2, 128, 40, [3000, 1000, 77], 500
+
+    def server(seed):
+        gen = torch.Generator().manual_seed(seed)
+        rn = lambda *s: torch.randn(s, generator=gen)
+        table = random_table(lens, 47, gen)
+        out = torch.arange(3 * 8, dtype=torch.int32).view(3, 8) + 65
+        cache = fm.KVCache.empty(65 + 24, Hk, d)
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        k, v = (rn(3, Hk, max(lens), d).bfloat16().cuda() for _ in range(2))
+        ws = fm.alloc_cache_workspace(3, H, Hk, N, d, 47)
+        fm.flashmask_cache_append(cache, table, k, v, ints([0] * 3), ws, count=ints(lens))
+        return dict(q=rn(3, H, N, d).bfloat16().cuda(), qw=rn(d).cuda(), cache=cache, table=table, out=out.cuda(),
+                    lens=ints(lens), ws=ws, wws=fm.alloc_cache_weights_workspace(3, H, Hk, N, d, 47),
+                    ews=fm.alloc_cache_evict_workspace(3, Hk, 47), nws=fm.alloc_norm_workspace(d))
+
+    freqs, mscale = fm.rope_frequencies(d)
+
+    def turn(s):
+        q, _ = fm.flashmask_norm_rope(s["q"], None, s["qw"], None, freqs, mscale=mscale)
+        o, lse = fm.flashmask_fwd_cache(q, s["cache"], s["table"], s["lens"], s["ws"])
+        w = torch.zeros((89, Hk, PAGE), device="cuda")
+        start = torch.zeros(3, dtype=torch.int32, device="cuda")
+        fm.flashmask_cache_weights(q, s["cache"], s["table"], s["lens"], lse, w, s["wws"], start=start)
+        new = fm.flashmask_cache_evict(s["cache"], s["table"], s["lens"], w, keep, s["ews"], sink=4, recent=16,
+                                       out_table=s["out"])
+        dq, _, dw, _ = fm.flashmask_norm_rope_bwd(o, None, s["q"], None, s["qw"], None, freqs, s["nws"], mscale=mscale)
+        codes = [t[s["out"].flatten().long()].clone().view(torch.uint8) for t in (*s["cache"].tensors, w)]
+        return [q, o, lse, w, new, dq, dw, *codes]
+
+    servers = [server(1), server(2)]
+    want = [turn(s) for s in servers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in servers]
+    got = [[], []]
+    for _ in range(6):
+        for i, (s, stream) in enumerate(zip(servers, streams)):
+            with torch.cuda.stream(stream):
+                got[i].append(turn(s))
+    torch.cuda.synchronize()
+    for i, s in enumerate(servers):
+        for x in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(x, want[i]))
+        for name in ("ws", "wws", "ews"):
+            assert fm.flashmask_check_status(s[name]) == (fm.FM_OK, 0)
