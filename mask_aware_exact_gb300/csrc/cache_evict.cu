@@ -72,9 +72,8 @@ __device__ __forceinline__ int of_ctas(const int* at, int n) {
 
 // Weights in an order of unsigned numbers: NaN below all others, -0 as +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
-  if (isnan(w)) return 0u;
-  const uint32_t u = __float_as_uint(w + 0.f);
-  return u >> 31 ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.f), key = u >> 31 ? ~u : u | 0x80000000u;
+  return isnan(w) ? 0u : key;
 }
 
 // What a sequence has and keeps.
@@ -130,12 +129,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     }
   }
 
-  // keys of a page: this lane's tokens lane and lane + 32
-  auto load_keys = [&](int page, uint32_t (&k)[2]) {
+  // weights of a page: this lane's tokens lane and lane + 32
+  auto load_weights = [&](int page, float (&w)[2]) {
     const float* at = p.weights + (static_cast<size_t>(max(page, 0)) * p.c.Hk + hk) * kPage + lane;
-    const float w0 = at[0], w1 = at[32];  // (without a branch: several pages are on their way)
-    k[0] = page < 0 ? 0u : order_key(w0);
-    k[1] = page < 0 ? 0u : order_key(w1);
+    w[0] = at[0], w[1] = at[32];
   };
   auto page_of = [&](int i) {
     const int page = p.table[static_cast<size_t>(b) * p.max_pages + p0 + i];
@@ -148,7 +145,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
       k[0] = keys[i * kPage + lane];
       k[1] = keys[i * kPage + lane + 32];
     } else {
-      load_keys(page_of(i), k);
+      const int page = page_of(i);
+      float w[2];
+      load_weights(page, w);
+      k[0] = page < 0 ? 0u : order_key(w[0]);
+      k[1] = page < 0 ? 0u : order_key(w[1]);
     }
   };
   for (int i = tid; i < 2 * kBins; i += kThreads) sh.hist[0][i] = 0;
@@ -158,15 +159,20 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
       const int mine = i0 + lane * kWarps < np ? page_of(i0 + lane * kWarps) : -1;
       const int n = min((np - i0 + kWarps - 1) / kWarps, 32);
       for (int j0 = 0; j0 < n; j0 += 8) {
-        uint32_t k[8][2];
+        // (nothing between the loads: with each page's keys taken behind its loads they went
+        // one after the other, and eight pages took 8000 cycles)
+        int page[8];
+        float w[8][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) load_keys(__shfl_sync(0xffffffffu, mine, min(j0 + j, 31)), k[j]);
+        for (int j = 0; j < 8; ++j) page[j] = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) load_weights(page[j], w[j]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (j0 + j >= n) break;
           uint32_t* to = keys + (i0 + (j0 + j) * kWarps) * kPage + lane;
-          to[0] = k[j][0];
-          to[32] = k[j][1];
+          to[0] = page[j] < 0 ? 0u : order_key(w[j][0]);
+          to[32] = page[j] < 0 ? 0u : order_key(w[j][1]);
         }
       }
     }
