@@ -70,6 +70,11 @@ __device__ __forceinline__ int of_ctas(const int* at, int n) {
   return sum;
 }
 
+// Four bytes on their way into shared memory.
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // Weights in an order of unsigned numbers: NaN below all others, -0 as +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.f), key = u >> 31 ? ~u : u | 0x80000000u;
@@ -129,27 +134,23 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     }
   }
 
-  // weights of a page: this lane's tokens lane and lane + 32
-  auto load_weights = [&](int page, float (&w)[2]) {
-    const float* at = p.weights + (static_cast<size_t>(max(page, 0)) * p.c.Hk + hk) * kPage + lane;
-    w[0] = at[0], w[1] = at[32];
-  };
   auto page_of = [&](int i) {
     const int page = p.table[static_cast<size_t>(b) * p.max_pages + p0 + i];
     if (page >= 0 && page < p.c.pages) return page;
     record_failure(p.status, kStatusPage, kSiteEvictPage);
     return -1;
   };
+  // keys of a page: this lane's tokens lane and lane + 32
   auto keys_of = [&](int i, uint32_t (&k)[2]) {
     if constexpr (kCached) {
       k[0] = keys[i * kPage + lane];
       k[1] = keys[i * kPage + lane + 32];
     } else {
       const int page = page_of(i);
-      float w[2];
-      load_weights(page, w);
-      k[0] = page < 0 ? 0u : order_key(w[0]);
-      k[1] = page < 0 ? 0u : order_key(w[1]);
+      const float* at = p.weights + (static_cast<size_t>(max(page, 0)) * p.c.Hk + hk) * kPage + lane;
+      const float w0 = at[0], w1 = at[32];
+      k[0] = page < 0 ? 0u : order_key(w0);
+      k[1] = page < 0 ? 0u : order_key(w1);
     }
   };
   for (int i = tid; i < 2 * kBins; i += kThreads) sh.hist[0][i] = 0;
@@ -158,22 +159,26 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     for (int i0 = warp; i0 < np; i0 += 32 * kWarps) {
       const int mine = i0 + lane * kWarps < np ? page_of(i0 + lane * kWarps) : -1;
       const int n = min((np - i0 + kWarps - 1) / kWarps, 32);
-      for (int j0 = 0; j0 < n; j0 += 8) {
-        // (nothing between the loads: with each page's keys taken behind its loads they went
-        // one after the other, and eight pages took 8000 cycles)
-        int page[8];
-        float w[8][2];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) page[j] = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) load_weights(page[j], w[j]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j0 + j >= n) break;
-          uint32_t* to = keys + (i0 + (j0 + j) * kWarps) * kPage + lane;
-          to[0] = page[j] < 0 ? 0u : order_key(w[j][0]);
-          to[32] = page[j] < 0 ? 0u : order_key(w[j][1]);
+      // (all on their way at once: by way of registers they came a few at a time; 2 segments of
+      // 300000 tokens, whole call: 162 us, so 140)
+      for (int j = 0; j < n; ++j) {
+        const int page = __shfl_sync(0xffffffffu, mine, j);
+        uint32_t* to = keys + (i0 + j * kWarps) * kPage + lane;
+        if (page >= 0) {
+          const float* at = p.weights + (static_cast<size_t>(page) * p.c.Hk + hk) * kPage + lane;
+          copy4(to, at);
+          copy4(to + 32, at + 32);
+        } else {
+          to[0] = to[32] = 0x7fffffffu;
         }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int i = warp; i < np; i += kWarps) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t& k = keys[i * kPage + lane + 32 * x];  // (copied by this thread)
+        k = order_key(__uint_as_float(k));
       }
     }
   }
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int j = (p0 + i) * kPage + lane + 32 * x;
-          if (j >= kp.lo && j < kp.hi && (k[x] & known) == prefix) atomicAdd(&hist[k[x] >> shift & (bins - 1)], 1);
+          if ((j >= kp.lo) & (j < kp.hi) & ((k[x] & known) == prefix)) atomicAdd(&hist[k[x] >> shift & (bins - 1)], 1);
         }
       }
       const int* bin = hist;
@@ -252,9 +257,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int j = (p0 + i) * kPage + lane + 32 * x;
-      const bool choice = j >= kp.lo && j < kp.hi;
-      keep[x] = __ballot_sync(0xffffffffu, choice ? k[x] > last : j < kp.len);
-      same[x] = __ballot_sync(0xffffffffu, choice && k[x] == last && equal > 0);
+      const bool choice = (j >= kp.lo) & (j < kp.hi);
+      keep[x] = __ballot_sync(0xffffffffu, (choice & (k[x] > last)) | (!choice & (j < kp.len)));
+      same[x] = __ballot_sync(0xffffffffu, choice & (k[x] == last) & (equal > 0));
     }
     if (lane == 0) {
       masks[i] = static_cast<uint64_t>(keep[1]) << 32 | keep[0];
