@@ -17,13 +17,14 @@
 // its page's tokens first and says so; before it writes it waits for the one or two pages
 // that read from it, which were taken before and wait for nothing until they have read.
 //
-// Measured (whole calls, L2 flushed): 64 sequences up to 8192 of 8 heads of 128 cut to a
-// quarter, in place, 186 us: 26 for the first kernel (latency: barriers and the weights' way in;
-// its histograms stay in shared memory) and 158 for the second (705 MB, 4.5 TB/s, 66 % of a
-// copy: the kept bytes of V lie apart, so that its source pages are read whole). Two
-// sequences of 131072 cut to an eighth, into other pages, 112 us: 40 and 68 (361 MB, 5.3 TB/s). A
-// page to be written is a chain of look-ups, loads, largest codes and stores behind two or
-// three barriers; four CTAs an SM hide most of it, registers allow no more.
+// Measured (whole calls, L2 flushed, into other pages with an index): 64 sequences up to 8192
+// of 8 heads of 128 cut to a quarter 184 us: 24 for the first kernel (latency: barriers and the
+// weights' way in; its histograms stay in shared memory) and 158 for the second (704 MB, 4.5
+// TB/s, 66 % of a copy: the kept bytes of V lie apart, so that its source pages are read
+// whole). Two sequences of 131072 cut to an eighth 107 us: 35 and 71 (361 MB, 5.1 TB/s). In
+// place, 40 sequences of 8192 150 us. A page to be written is a chain of look-ups, loads,
+// largest codes and stores behind two or three barriers; four CTAs an SM hide most of it (three
+// 201 us, five with fewer registers 193, where four took 186).
 #include <atomic>
 
 #include "cache_common.cuh"
