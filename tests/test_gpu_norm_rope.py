@@ -189,6 +189,51 @@ def test_extreme_heads(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d", [64, 62])
+def test_frequencies_of_all_sizes(d, interleaved):
+    # the positions' turns are those of flashmask_rope for every frequency; one that is none
+    # spoils its pair. In fp32 the two ways differ by the roundings of a turn's two products and
+    # their sum, 4 u of the pair's magnitudes, and by r: which elements a thread adds up depends on
+    # how many are turned, so each way's r is within 15 u of the exact one (half of 22 u, and 4 u)
+    # and they within 30 u of one another: 34 u < 2^-18 in all
+    fm = need_gpu()
+    n, N = d // 2, 70
+    gen = torch.Generator().manual_seed(d)
+    f = 10.0 ** torch.linspace(-9, 38, n, dtype=torch.float64)
+    f[1::3] *= -1
+    f[2], f[3], f[4], f[5] = 0.0, 4.0, 2.0 ** 128, -5.0
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (2, N), generator=gen, dtype=torch.int64).int().cuda()
+    x, g = (torch.randn((2, 3, N, d), generator=gen).cuda() for _ in range(2))
+    w = (torch.rand(d, generator=gen) + 0.5).cuda()
+    none = torch.empty(0, dtype=torch.float64, device="cuda")
+    how = dict(positions=pos, interleaved=interleaved, mscale=1.5)
+    flat, _ = fm.flashmask_norm_rope(x, None, w, None, none)
+    for last in (None, float("nan"), float("inf"), 2.0 ** 129):
+        if last is not None:
+            f[7] = last
+        freqs = f.cuda()
+        want, _ = fm.flashmask_rope(flat, None, freqs, **how)
+        got, _ = fm.flashmask_norm_rope(x, None, w, None, freqs, **how)
+        spoilt = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), spoilt) and spoilt.any() == (last is not None)
+        mag = torch.from_numpy(O.pair_magnitudes(f64(flat), n, interleaved)).cuda() * 1.5
+        off = ((got.double() - want.double()).abs() / mag)[~spoilt].max()
+        assert off <= 2.0 ** -18, off * 2.0 ** 24
+        if last is None:
+            turned, _ = fm.flashmask_rope_bwd(g, None, freqs, **how)
+            ws = fm.alloc_norm_workspace(d)
+            a = fm.flashmask_norm_rope_bwd(turned, None, x, None, w, None, none, ws)
+            b = fm.flashmask_norm_rope_bwd(g, None, x, None, w, None, freqs, ws, **how)
+            r = 1.0 / (x.double().square().mean(-1, keepdim=True) + 1e-6).sqrt()
+            u = x.double().abs() * r
+            gw = torch.from_numpy(O.pair_magnitudes(f64(g), n, interleaved)).cuda() * 1.5 * w.double()
+            bound = 2.0 ** -17 * r * (gw + u * (gw * u).mean(-1, keepdim=True))
+            assert torch.all((a[0].double() - b[0].double()).abs() <= bound)
+            assert torch.all((a[2].double() - b[2].double()).abs() <= 2.0 ** -17 * (gw / w.double() * u).sum((0, 1, 2)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
 def test_gradients_against_differences(interleaved):
     # central differences with step h in fp32: the error is h^2 / 6 of the third derivative
     # (below 8 |g| here, since r <= 4 and its derivatives are of the order of r^3) and 2^-19
