@@ -258,6 +258,17 @@ def test_many_rows(kind, H, Hk, N, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", [None, "window_prefix", "random"])
+def test_a_prompt_of_its_own_keys(kind):
+    # 12000 rows of one cache head, all of the sequence's tokens, and the last but one
+    fm = need_gpu()
+    H, N, d = 8, 1500, 64
+    q, cache, table, gen = make(fm, 2, H, 1, N, d, [N, N - 1], seed=6)
+    mask = None if kind is None else mask_of(kind, 2, H, 1, N, table.shape[1] * PAGE, gen, fm)
+    check(fm, q, cache, table, [N, N - 1], [N, N - 1], mask)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", [None, "window"])
 @pytest.mark.parametrize("Hk,N", [(4, 1), (4, 11), (2, 35)])
 def test_many_sequences(kind, Hk, N):

@@ -233,6 +233,27 @@ def test_frequencies_of_all_sizes(d, interleaved):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float32, 30)])
+def test_weights_that_are_not_there(dtype, d):
+    # none, and then no workspace either; Q's alone; K's alone
+    fm = need_gpu()
+    B, Hq, Hk, N = 2, 4, 2, 50
+    t, w, _ = inputs(B, Hq, Hk, N, d, dtype, torch.float32)
+    freqs, _ = fm.rope_frequencies(d)
+    ws, ones = fm.alloc_norm_workspace(d), torch.ones(d, device="cuda")
+    args = (t["dq"], t["dk"], t["q"], t["k"])
+    for qw, kw in ((None, None), (w[0], None), (None, w[1])):
+        full = [ones if x is None else x for x in (qw, kw)]
+        for a, b in zip(fm.flashmask_norm_rope(t["q"], t["k"], qw, kw, freqs),
+                        fm.flashmask_norm_rope(t["q"], t["k"], *full, freqs)):
+            assert torch.equal(a, b)
+        got = fm.flashmask_norm_rope_bwd(*args, qw, kw, freqs, None if qw is kw else ws)
+        want = fm.flashmask_norm_rope_bwd(*args, *full, freqs, ws)
+        for x, a, b in zip((1, 1, qw, kw), got, want):
+            assert a is None if x is None else torch.equal(a, b)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_gradients_against_differences(interleaved):
     # central differences with step h in fp32: the error is h^2 / 6 of the third derivative
