@@ -13,7 +13,7 @@
 // Up to 32 rows, as 1, 2 or 4 groups of 8 (kWeightsMany says why not more). K is read
 // once: 8 rows are bound by HBM, 32 by instructions (600 a page of d = 64) and their
 // latencies, with two warps a scheduler: registers allow no more (9, 10 warps: 33, 31 us for
-// the drafted tokens below, 28 with 8). Measured, calls with L2 flushed: 64 sequences up to 8192,
+// the drafted tokens below where 8 took 28). Measured, calls with L2 flushed: 64 sequences up to 8192,
 // 32 / 8 heads of 128: 63 us (342 MB, 5.4 TB/s); 8 sequences of 131072, window of 4096 and
 // prefix of 2048, 8 / 8 heads: 25 us, 9 of them the classification of 131072 columns; 16
 // sequences up to 16384, 4 tokens, 32 / 4 heads of 64: 28 us (42 MB); one sequence of 1000:
@@ -83,35 +83,41 @@ __device__ __forceinline__ void load_rows(const WeightsParams& wp, const Geometr
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rows = geo.G * r.live;
   o.all_lim = r.len;
+  // (all loads before the first use: group by group they would wait for one another)
+  uint4 x[NT][D / 64][2];
+  float lse[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int rr = 8 * t + g;
     const bool live = rr < rows;
     const int tok = geo.by_G.div(rr), h = hk * geo.G + rr - tok * geo.G;
     const uint16_t* src = p.q + b * p.qs[0] + h * p.qs[1] + tok * p.qs[2] + 16 * c;
-    uint4 x[D / 64][2];
-    uint32_t top = 0;
 #pragma unroll
     for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        x[hf][u] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
+        x[t][hf][u] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * u) : make_uint4(0u, 0u, 0u, 0u);
+    // rows that saw nothing, and those behind the last, give nothing; one whose LSE is NaN
+    // counts as one whose query is (a NaN in S is dropped where the key is masked)
+    lse[t] = live ? wp.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok] : -INFINITY;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    uint32_t top = 0;
 #pragma unroll
     for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t mk = 0x7fff7fffu;
-        const uint32_t a = __vmaxu2(__vmaxu2(x[hf][u].x & mk, x[hf][u].y & mk), __vmaxu2(x[hf][u].z & mk, x[hf][u].w & mk));
+        const uint4 v = x[t][hf][u];
+        const uint32_t a = __vmaxu2(__vmaxu2(v.x & mk, v.y & mk), __vmaxu2(v.z & mk, v.w & mk));
         top = max(top, max(a & 0xffffu, a >> 16));
       }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // the row's largest element goes to [2^14, 2^15): fp16 then holds every element down
     // to 2^-30 of it
-    // rows that saw nothing, and those behind the last, give nothing; one whose LSE is NaN
-    // counts as one whose query is (a NaN in S is dropped where the key is masked)
-    float l = -INFINITY;
-    if (live) l = wp.lse[(static_cast<size_t>(b) * p.H + h) * p.N + tok];
+    float l = lse[t];
     const bool bad = top >= 0x7f80u || isnan(l);
     l = isnan(l) ? 0.f : l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
     const int up = top == 0 || bad ? 0 : min(14 - (static_cast<int>(top >> 7) - 127), 126);
@@ -120,7 +126,7 @@ __device__ __forceinline__ void load_rows(const WeightsParams& wp, const Geometr
     for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 w = x[hf][k >> 1];
+        const uint4 w = x[t][hf][k >> 1];
         const uint32_t lo = k & 1 ? w.z : w.x, hi = k & 1 ? w.w : w.y;
         o.q[t][4 * hf + k][0] = pack_f16x2(__uint_as_float(lo << 16) * f, __uint_as_float(lo & 0xffff0000u) * f);
         o.q[t][4 * hf + k][1] = pack_f16x2(__uint_as_float(hi << 16) * f, __uint_as_float(hi & 0xffff0000u) * f);
