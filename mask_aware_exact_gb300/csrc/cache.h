@@ -150,8 +150,8 @@ struct WeightsParams {
 struct WeightsWs {
   size_t arrived, partial, list, listed, tiles, total;
 };
-// Rows of a cache head from which on the products are taken on tcgen05: 32 rows take 23.1 us
-// without, 29.2 with (16 sequences of 16384, 4 heads of 64; of 128: 30.5, 37.7), and more
+// Rows of a cache head from which on the products are taken on tcgen05: 32 rows take 22.9 us
+// without, 29.2 with (16 sequences of 16384, 4 heads of 64; of 128: 29.2, 37.7), and more
 // rows than 32 would have to read and convert K again for each 32, where tcgen05 takes 64
 // in the time of 33.
 constexpr int kWeightsMany = 33;

@@ -16,11 +16,11 @@
 // the drafted tokens below where 8 took 28). Measured, calls with L2 flushed: 64 sequences up to 8192,
 // 32 / 8 heads of 128: 63 us (342 MB, 5.4 TB/s); 8 sequences of 131072, window of 4096 and
 // prefix of 2048, 8 / 8 heads: 25 us, 9 of them the classification of 131072 columns; 16
-// sequences up to 16384, 4 tokens, 32 / 4 heads of 64: 28 us (42 MB); one sequence of 1000:
+// sequences up to 16384, 4 tokens, 32 / 4 heads of 64: 25 us (42 MB); one sequence of 1000:
 // 5.9 us on the GPU. 16 sequences of 16384, 4 heads, by rows (us; L2 warm):
 //   rows        4      8     16     24     32
-//   d = 64    14.6   14.7   16.8   23.1   23.1
-//   d = 128   16.8   16.9   22.3   29.3   30.5
+//   d = 64    14.7   14.7   16.8   22.9   22.9
+//   d = 128   16.8   16.9   21.1   29.2   29.2
 #include <atomic>
 
 #include "cache_weights.cuh"

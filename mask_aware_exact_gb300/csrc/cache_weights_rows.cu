@@ -27,8 +27,8 @@
 // 16 sequences of 16384, 4 heads, by rows (us; L2 warm), with the kernel for few rows beside
 // it where that takes them:
 //   rows            24           32        40     64    128
-//   d = 64    29.1 / 23.1  29.2 / 23.1   29.1   29.1   35.5
-//   d = 128   37.7 / 29.3  37.7 / 30.5   37.6   38.2   41.5
+//   d = 64    29.1 / 22.9  29.2 / 22.9   29.1   29.1   35.5
+//   d = 128   37.7 / 29.2  37.7 / 29.2   37.6   38.2   41.5
 //
 // Items are cut into `parts` ranges of rows where there are few of them, on one line with
 // equal runs for the CTAs; the pieces of an item that a run's border cuts leave their
