@@ -688,16 +688,21 @@ def _norm_rope(q, k, grads, weights, freqs, positions, interleaved, mscale, eps,
             gk = _rows(dk, "dk", dtype, index)
         if dq.shape != q.shape or (k is not None and dk.shape != k.shape):
             raise ValueError("dq and dk must have the shapes of q and k")
-    w_dtype = None
-    for w, name in zip(weights, ("q_weight", "k_weight")):
-        if w is None:
-            continue
-        if w_dtype is None:
-            w_dtype = w.dtype
-            if w_dtype is not dtype and w_dtype is not torch.float32:
-                raise ValueError(f"{name} must be fp32 or of q's type")
-        _want(w, name, w_dtype, index, (d,))
     qw, kw = weights
+    w_dtype, w_size, qw_ptr, kw_ptr = None, (d,), 0, 0
+    if qw is not None:
+        w_dtype = qw.dtype
+        if w_dtype is not dtype and w_dtype is not torch.float32:
+            raise ValueError("q_weight must be fp32 or of q's type")
+        _want(qw, "q_weight", w_dtype, index, w_size)
+        qw_ptr = qw.data_ptr()
+    if kw is not None:
+        if w_dtype is None:
+            w_dtype = kw.dtype
+            if w_dtype is not dtype and w_dtype is not torch.float32:
+                raise ValueError("k_weight must be fp32 or of q's type")
+        _want(kw, "k_weight", w_dtype, index, w_size)
+        kw_ptr = kw.data_ptr()
     if k is None and kw is not None:
         raise ValueError("k_weight needs k")
     n = freqs.numel()
@@ -734,17 +739,26 @@ def _norm_rope(q, k, grads, weights, freqs, positions, interleaved, mscale, eps,
             if k is not None:
                 ok, uk = torch.empty((B, Hk, N, d), dtype=dtype, device=device), (Hk * N * d, N * d, d)
         wq = wk = None
+        some = B * N * d > 0
         if grads is not None:
-            make = torch.zeros_like if B * N * d == 0 else torch.empty_like
-            wq, wk = (None if w is None else make(w) for w in weights)
-        if B * N * d > 0:
-            at = lambda t: 0 if t is None else t.data_ptr()
-            none = (0, 0, 0)
-            heads = _NORM_HEADS.pack(q.data_ptr(), oq.data_ptr(), 0 if grads is None else dq.data_ptr(), at(qw),
-                                     at(wq), Hq, *sq[:3], *uq[:3], *(none if gq is None else gq[:3]))
-            if k is not None:
-                heads += _NORM_HEADS.pack(k.data_ptr(), ok.data_ptr(), 0 if grads is None else dk.data_ptr(),
-                                          at(kw), at(wk), Hk, *sk[:3], *uk[:3], *(none if gk is None else gk[:3]))
+            make = torch.empty if some else torch.zeros
+            if qw is not None:
+                wq = make(w_size, dtype=w_dtype, device=device)
+            if kw is not None:
+                wk = make(w_size, dtype=w_dtype, device=device)
+        if some:
+            if grads is None:
+                heads = _NORM_HEADS.pack(q.data_ptr(), oq.data_ptr(), 0, qw_ptr, 0, Hq, sq[0], sq[1], sq[2],
+                                         uq[0], uq[1], uq[2], 0, 0, 0)
+                if k is not None:
+                    heads += _NORM_HEADS.pack(k.data_ptr(), ok.data_ptr(), 0, kw_ptr, 0, Hk, sk[0], sk[1], sk[2],
+                                              uk[0], uk[1], uk[2], 0, 0, 0)
+            else:
+                heads = _NORM_HEADS.pack(q.data_ptr(), oq.data_ptr(), dq.data_ptr(), qw_ptr,
+                                         0 if wq is None else wq.data_ptr(), Hq, *sq[:3], *uq[:3], *gq[:3])
+                if k is not None:
+                    heads += _NORM_HEADS.pack(k.data_ptr(), ok.data_ptr(), dk.data_ptr(), kw_ptr,
+                                              0 if wk is None else wk.data_ptr(), Hk, *sk[:3], *uk[:3], *gk[:3])
             how = (heads, 1 if k is None else 2, pos, pos_stride, freqs.data_ptr(), B, N, d, 2 * n,
                    bool(interleaved), code, FM_F32 if w_dtype is torch.float32 else code, mscale, eps)
             if grads is None:
