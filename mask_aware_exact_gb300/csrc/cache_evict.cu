@@ -339,6 +339,10 @@ __device__ __forceinline__ uint32_t codes_times_f16(uint32_t w, uint32_t ff) {
       : "r"(lo), "r"(hi), "r"(ff));
   return r;
 }
+// What codes of a page of scale `was` are multiplied by for one of scale `now`. Codes that are
+// all zero do not count for `now`, so that the quotient may pass fp32 for them (others leave
+// it below 2^19), and zero times infinity would be NaN.
+__device__ __forceinline__ float scale_ratio(float was, float now) { return fminf(was / now, 0x1p100f); }
 __device__ __forceinline__ bool plain_power(float f) {
   return (__float_as_uint(f) & 0x7fffffu) == 0 && f >= 0x1p-14f && f <= 0x1p15f;
 }
@@ -669,7 +673,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
         const size_t ph = static_cast<size_t>(to) * Hk + m.hk;
         const float k_new = __int_as_float((sh.exps[0] + 127) << 23), v_new = __int_as_float((sh.exps[1] + 127) << 23);
         {
-          const float f = sh.kscale[ks_slot] / k_new;
+          const float f = scale_ratio(sh.kscale[ks_slot], k_new);
           const bool bad = no_scales(sh.kscale[ks_slot], sh.vscale[ks_slot]);
           uint8_t* dst = p.c.k8 + ph * (kPage * D) + ks_slot * D + 16 * kq;
           if (bad) {
@@ -693,7 +697,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
           for (int i = 0; i < D / 64; ++i) *reinterpret_cast<uint4*>(dst + 64 * i) = kr[i];
         }
         {
-          const float f = sh.vscale[vslot] / v_new;
+          const float f = scale_ratio(sh.vscale[vslot], v_new);
           const bool bad = no_scales(sh.kscale[vslot], sh.vscale[vslot]);
           if (bad) {
 #pragma unroll

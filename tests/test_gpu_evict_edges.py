@@ -1,0 +1,51 @@
+"""Eviction at its edges, against the same definition as in test_gpu_cache_evict (results
+are compared for equality)."""
+import pytest
+import torch
+
+from test_gpu_cache_evict import check
+from gpu_common import need_gpu
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [2.0 ** 27, 2.0 ** 28, 1.5 * 2.0 ** 100, 3.4e38])
+@pytest.mark.parametrize("beside", [None, 2.0 ** -60, 2.0 ** -100])
+def test_tokens_of_zeros_from_pages_of_large_scales(beside, scale, d, apart):
+    # They do not count for the new page's scale, so that the old one may be more than 2^128
+    # times the new: they stay zero, beside pages of small scales and where all is zero.
+    fm = need_gpu()
+
+    def edit(cache, table, gen):
+        pages = table[0, :12].tolist()
+        for i, page in enumerate(pages):
+            if i % 3 == 1 or beside is None:
+                cache.k8[page] = 0.0
+                cache.v8[page] = 0.0
+            if i % 3 == 1:
+                cache.kscale[page] = scale
+                cache.vscale[page] = scale
+            elif beside is not None:
+                cache.kscale[page] = beside
+                cache.vscale[page] = beside
+        cache.k8.view(torch.uint8)[pages[4], :, ::2] = 0x80  # of either sign
+    check(fm, [760, 100], [380, 90], 2, d, 2, 10, apart, edit=edit)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [False, True])
+def test_zeros_beside_a_large_token_that_is_given_up(apart):
+    # equal weights: positions 0 .. 49 stay and the last 100, so that the token of page 3 which
+    # set its scale goes and zeros of that page move to another
+    fm = need_gpu()
+
+    def edit(cache, table, gen):
+        cache.k8.zero_()
+        cache.v8.zero_()
+        page = int(table[0, 3])
+        cache.k8[page, :, 0, 5] = 300.0
+        cache.v8[page, :, 7, 1] = -300.0
+        cache.kscale[page] = 2.0 ** 40
+        cache.vscale[page] = 2.0 ** 28
+    check(fm, [300], [150], 2, 64, 0, 100, apart, "equal", edit=edit)
