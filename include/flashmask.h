@@ -354,8 +354,9 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
  *               overlap. w: the weights [d] of this tensor, of `weight_dtype` (FM_F32
  *               or `dtype`); NULL: ones. dy, ds and dw are the backward's.
  * d <= 256; eps >= 1e-30; other limits, positions and freqs as for flashmask_rope. Sums and
- * everything before the one rounding at the end are fp32; a head whose squares would
- * pass fp32 is scaled first. Asynchronous on `stream`; needs no workspace.
+ * everything before the one rounding at the end are fp32; a head whose squares (backward:
+ * or whose sum of g * w * x) would pass fp32 is scaled first. Asynchronous on `stream`;
+ * needs no workspace.
  *
  * The backward gives the gradients from dy, that of the rotated output, and x, the
  * forward's input (nothing else is kept from the forward):

@@ -46,8 +46,9 @@ constexpr int kHeadsMost = 16;
 __host__ __device__ constexpr int stages(bool backward) { return backward ? 3 : 4; }
 __host__ __device__ constexpr int slot_bytes(bool backward) { return stages(backward) * (backward ? 4 : 2) * kThreads * 16; }
 
-// The sum of a head's squares beyond which it is taken again of values scaled by 2^-70.
-constexpr float kSquaresMost = 1e38f;
+// The sum of a head's squares, or the magnitude of sum g w x, beyond which they are taken again
+// of scaled values.
+constexpr float kSumMost = 1e38f;
 
 // Where a thread's chunk c (pairs, or elements that are not turned) lies in a head:
 // accesses of kVec elements at e0 and, if `two`, at e1.
@@ -269,11 +270,19 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
         }
       };
       sums();
-      if (__builtin_expect(__any_sync(0xffffffffu, !(s1 <= kSquaresMost)), 0)) {
-        f = s1 <= kSquaresMost ? 1.f : 0x1p-70f;
+      if (__builtin_expect(__any_sync(0xffffffffu, !(s1 + fabsf(s2) <= kSumMost)), 0)) {
+        auto scale = [&](float by) {
+          f *= by;
 #pragma unroll
-        for (int i = 0; i < kOwn / 2; ++i) x2[i] = f2_mul(x2[i], f2_make(f, f));
-        sums();
+          for (int i = 0; i < kOwn / 2; ++i) x2[i] = f2_mul(x2[i], f2_make(by, by));
+          sums();
+        };
+        scale(s1 <= kSumMost ? 1.f : 0x1p-70f);
+        if constexpr (kBackward) {
+          // a norm of 2^-10 at most: s2 is then below 2^-10 * 2^128 * sqrt(256)
+          const int down = max(((__float_as_int(s1) >> 23) - 127) / 2 + 11, 0);
+          scale(fabsf(s2) <= kSumMost ? 1.f : __int_as_float((127 - down) << 23));
+        }
       }
       // r f of the definition is that of the values as they are
       const float r = rsqrtf(s1 * inv_d + p.eps * f * f);
