@@ -518,10 +518,11 @@ fm_status flashmask_cache_weights(const void* q, const int64_t qs[3], const fm_c
                                   size_t ws_bytes, void* stream);
 
 /* Cuts sequences down: each cache head of sequence b keeps n = min(lens[b], keep[b]) of its
- * tokens (keep NULL: `budget` for all; below 0 counts as 0): the first min(sink, n), the
- * last min(recent, n - those), and of the others those of the largest weight (fp32 [pages,
- * Hk, FM_PAGE], see flashmask_cache_weights; any values: -0 counts as 0, NaN as less than
- * everything else; of equal ones the lower position is kept). Heads choose for themselves.
+ * tokens (a keep[b] below 0 counts as 0; keep NULL: `budget` for all, which is refused
+ * below 0, as sink and recent are): the first min(sink, n), the last min(recent, n -
+ * those), and of the others those of the largest weight (fp32 [pages, Hk, FM_PAGE], see
+ * flashmask_cache_weights; any values: -0 counts as 0, NaN as less than everything else;
+ * of equal ones the lower position is kept). Heads choose for themselves.
  * The kept tokens move together in their order: K, V, scales and weights go to the
  * positions 0 .. n - 1 of
  *   out_table   int32 [B, out_pages], pages that neither repeat nor occur in page_table's

@@ -1033,13 +1033,13 @@ def alloc_cache_evict_workspace(B, Hk, max_pages, device="cuda") -> torch.Tensor
 
 def flashmask_cache_evict(cache: KVCache, page_table, lens, weights, keep, ws, sink=0, recent=0, out_table=None,
                           new_lens=None, index=None, stream=None):
-    """Cuts sequences down to keep[b] tokens (an int for all, or int32 [B]) of each cache
-    head: its first `sink`, its last `recent` and those of the largest weights between
-    (fp32 [pages, Hk, 64], moved along). They go together, in place or into the pages of
-    out_table (int32 [B, pages]). Returns the new lengths (int32 [B], written to
-    new_lens, which may be lens). index (int32 [B, Hk, width]) gets the old positions of
-    the kept tokens. See include/flashmask.h for scales and rounding. ws comes from
-    alloc_cache_evict_workspace."""
+    """Cuts sequences down to keep[b] tokens (an int for all, not negative, or int32 [B],
+    where one below 0 counts as 0) of each cache head: its first `sink`, its last `recent`
+    and those of the largest weights between (fp32 [pages, Hk, 64], moved along). They go
+    together, in place or into the pages of out_table (int32 [B, pages]). Returns the new
+    lengths (int32 [B], written to new_lens, which may be lens). index (int32 [B, Hk,
+    width]) gets the old positions of the kept tokens. See include/flashmask.h for scales
+    and rounding. ws comes from alloc_cache_evict_workspace."""
     c, Hk, d, index_dev = cache._handle
     if page_table.dim() != 2:
         raise ValueError("page_table must be int32 [B, max_pages]")

@@ -3,7 +3,7 @@ are compared for equality)."""
 import pytest
 import torch
 
-from test_gpu_cache_evict import check
+from test_gpu_cache_evict import check, ints, make
 from gpu_common import need_gpu
 
 
@@ -49,3 +49,21 @@ def test_zeros_beside_a_large_token_that_is_given_up(apart):
         cache.kscale[page] = 2.0 ** 40
         cache.vscale[page] = 2.0 ** 28
     check(fm, [300], [150], 2, 64, 0, 100, apart, "equal", edit=edit)
+
+
+@pytest.mark.gpu
+def test_sizes_below_zero():
+    # of one sequence they count as zero; for all of them they are refused, as the header says
+    fm = need_gpu()
+    cache, table, _, w, _ = make(fm, [100, 64], 2, 64)
+    ws = fm.alloc_cache_evict_workspace(2, 2, table.shape[1])
+    first = [t.clone() for t in (*cache.tensors, w)]
+    for keep in (-1, -5, -2 ** 40):
+        with pytest.raises(fm.FlashMaskError):
+            fm.flashmask_cache_evict(cache, table, ints([100, 64]), w, keep, ws)
+    for kw in (dict(sink=-1), dict(recent=-2 ** 33)):
+        with pytest.raises(fm.FlashMaskError):
+            fm.flashmask_cache_evict(cache, table, ints([100, 64]), w, 10, ws, **kw)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip((*cache.tensors, w), first))
+    assert fm.flashmask_cache_evict(cache, table, ints([100, 64]), w, ints([-5, 64]), ws).tolist() == [0, 64]
+    assert fm.flashmask_cache_evict(cache, table, ints([0, 64]), w, 0, ws).tolist() == [0, 0]
