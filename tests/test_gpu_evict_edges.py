@@ -67,3 +67,52 @@ def test_sizes_below_zero():
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip((*cache.tensors, w), first))
     assert fm.flashmask_cache_evict(cache, table, ints([100, 64]), w, ints([-5, 64]), ws).tolist() == [0, 64]
     assert fm.flashmask_cache_evict(cache, table, ints([0, 64]), w, 0, ws).tolist() == [0, 0]
+
+
+# Tables of more than 8 x 704 pages: the selection reads the weights again in each pass.
+WIDE = 6000
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("weights", ["odd", "equal", "tails"])
+def test_weights_of_any_value_in_tables_that_are_not_held(weights, apart):
+    fm = need_gpu()
+    check(fm, [3000, 70, 0, 1], [1111, 3, 3, 3], 2, 64, 5, 50, apart, weights, slack=WIDE)
+    check(fm, [3000, 65], [17, 64], 1, 128, 0, 0, apart, weights, slack=WIDE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1, 2 ** 31 - 1])
+def test_a_page_that_is_not_there_in_wide_tables(bad):
+    # its keys count as NaN, so that they are the first to go, as in a table whose keys are held;
+    # the other sequence is cut down as ever
+    fm = need_gpu()
+    lens, keep = [3000, 700], [1500, 100]
+    cache, table, out_table, w, _ = make(fm, lens, 2, 64, out=keep, weights="odd")
+    first = [t.clone() for t in (*cache.tensors, w)]
+    got = []
+    for width in (table.shape[1], WIDE):
+        for missing in (False, True):
+            t = torch.full((2, width), 1 << 30, dtype=torch.int32, device="cuda")
+            t[:, :table.shape[1]] = table
+            if missing:
+                t[0, 20] = bad
+            ws = fm.alloc_cache_evict_workspace(2, 2, width)
+            for x, y in zip((*cache.tensors, w), first):
+                x.copy_(y)
+            index = torch.full((2, 2, keep[0]), -7, dtype=torch.int32, device="cuda")
+            new = fm.flashmask_cache_evict(cache, t, ints(lens), w, ints(keep), ws, sink=3, recent=9,
+                                           out_table=out_table, index=index)
+            assert new.tolist() == keep
+            # none of the missing page's tokens is kept, so that nothing of it is moved, but it
+            # was looked at
+            assert fm.flashmask_check_status(ws)[0] == (fm.FM_ERR_PAGE if missing else fm.FM_OK)
+            gone = ((index[0] >= 20 * 64) & (index[0] < 21 * 64)).sum()
+            assert (int(gone) == 0) == missing
+            got.append([x.clone().view(torch.uint8) for x in (*cache.tensors, w, index)])
+    for x, y in zip(got[:2], got[2:]):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+    for a, b in zip(got[0][:5], got[1][:5]):  # the other sequence's pages
+        at = out_table[1, :2].long()
+        assert torch.equal(a[at], b[at])
