@@ -363,6 +363,7 @@ fm_status flashmask_rope(const fm_heads* t, int n_tensors, const int32_t* positi
  *     g = dy rotated back, times mscale where it is rotated
  *     dw = sum of g * x * r over batch, heads and tokens
  *     dx = r * (g * w - x * r * mean(g * w * x * r))
+ * (a term g * w * x of the mean loses bits where it falls below fp32's normal range).
  *   x, dy       [B, H, N, d] with strides xs and ds; y: dx, which may be dy or x with the
  *               same strides and otherwise overlaps no input
  *   dw          [d] of `weight_dtype`, written; NULL where it is not wanted
@@ -499,10 +500,12 @@ fm_status flashmask_fwd_cache(const void* q, const int64_t qs[3], const fm_cache
  * keys, from lens[b] - q_lens[b] on. start 0 for a prompt whose last rows alone weigh
  * all of its keys. A key that no row sees gets 0; slots from lens[b] on are left as they were.
  *   q, cache, page_table, lens, q_lens, mask, scale and their limits as for
- *   flashmask_fwd_cache; V takes no part. The pages of one call must be distinct. A row
- *   whose LSE is -inf gives nothing; one whose LSE, query or visible K scale is NaN (or a
- *   K scale that is negative or infinite) gives NaN to the keys that it sees. What K holds
- *   for keys that no row sees has no influence.
+ *   flashmask_fwd_cache; V takes no part. The pages of one call must be distinct: two
+ *   sequences that share some (of a common beginning) would both add to the same slots at
+ *   once, so they take a call each, one after the other, and start lies behind the shared
+ *   keys in all but the first. A row whose LSE is -inf gives nothing; one whose LSE, query
+ *   or visible K scale is NaN (or a K scale that is negative or infinite) gives NaN to the
+ *   keys that it sees. What K holds for keys that no row sees has no influence.
  *   ws: flashmask_cache_weights_workspace_bytes(...) bytes, 256-byte aligned and zeroed
  *   before its first use; not to be shared by calls that may run at the same time; one
  *   workspace serves all sizes that it is large enough for. Zero it again after another
