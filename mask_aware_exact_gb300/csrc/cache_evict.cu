@@ -21,10 +21,15 @@
 // of 8 heads of 128 cut to a quarter 184 us: 24 for the first kernel (latency: barriers and the
 // weights' way in; its histograms stay in shared memory) and 158 for the second (704 MB, 4.5
 // TB/s, 66 % of a copy: the kept bytes of V lie apart, so that its source pages are read
-// whole). Two sequences of 131072 cut to an eighth 107 us: 35 and 71 (361 MB, 5.1 TB/s). In
-// place, 40 sequences of 8192 150 us. A page to be written is a chain of look-ups, loads,
-// largest codes and stores behind two or three barriers; four CTAs an SM hide most of it (three
-// 201 us, five with fewer registers 193, where four took 186).
+// whole). Two sequences of 131072 cut to an eighth 107 us: 35 and 71 (361 MB, 5.1 TB/s). A page
+// to be written is a chain of look-ups, loads, largest codes and stores behind two or three
+// barriers; four CTAs an SM hide most of it (three 201 us, five with fewer registers 193, where
+// four took 186). In place, caches of 8 heads of 128 that no call has cut before, and their
+// floors (the weights, and the kept tokens read and written): 40 sequences of 8192 cut to 2048
+// 163 us (52), 64 of them 242 (83); 64 of 2112 that give up 64 tokens 200 (81), of 2049 that give
+// up one 157 (81; the pages before its place stay). Equal weights cost no more: with all of
+// them zero, 64 sequences of 8192 into other pages take 176 us where spread ones take 210, since
+// the tokens that stay lie together.
 #include <atomic>
 
 #include "cache_common.cuh"
@@ -823,15 +828,16 @@ EvictWs evict_ws_layout(int B, int Hk, int max_pages) {
 cudaError_t launch_cache_evict(int d, EvictParams p, int num_sms, cudaStream_t s) {
   p.by_Hk.set(p.c.Hk);
   // CTAs of a segment: as many as hold its keys, and more down to kPagesFew pages each while
-  // they leave SMs free (one segment of 16384 tokens, whole call: 29.0 -> 25.6 us; shares of 32
-  // pages take 4000 tokens from 17.6 to 22.8)
+  // they leave SMs free (one segment of 16384 tokens, whole call, measured as below: 29.0 -> 25.6
+  // us; shares of 32 pages take 4000 tokens from 17.6 to 22.8)
   int cluster = 1;
   while (cluster < kClusterMost &&
          (cluster * kPagesShare < p.max_pages ||
           (cluster * kPagesFew < p.max_pages && 2LL * p.B * p.c.Hk * cluster <= num_sms)))
     cluster *= 2;
   // CTAs of 256 threads where there are several for each SM, which hide one another's
-  // barriers: 64 x 8 segments of 8192, whole calls, 187 us; of 512, 195. Otherwise of 512: 20 x
+  // barriers: 64 x 8 segments of 8192, whole calls, 187 us; of 512, 195. Otherwise of 512 (in
+  // place, a cache cut the same way again, so that most of it lies in front): 20 x
   // 8 segments 86 us (256: 89, 1024: 97), 8 of 16384 31.6 (34.2, 35.2), 16 of 131072 112 (120,
   // 134: clusters of eight CTAs that fill an SM each do not all find a place at once).
   const bool many = static_cast<long long>(p.B) * p.c.Hk * cluster > 2LL * num_sms;

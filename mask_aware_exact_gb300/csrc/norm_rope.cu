@@ -23,7 +23,7 @@
 //
 // Measured (bf16 forward, 32768 tokens, 32 + 32 heads of 128, 1.07 GB): 160 us, 6.7 TB/s,
 // 98 % of a copy. Backward (fp16, 2 x 16384 tokens, 32 + 8 heads of 128, half of each turned,
-// interleaved, 1.01 GB): 166 us, 6.1 TB/s, 89 % of a copy; a scheduler issues in 61 % of the
+// interleaved, 1.01 GB): 167 us, 6.0 TB/s, 89 % of a copy; a scheduler issues in 61 % of the
 // cycles and the two CTAs that fit an SM hide no more (three CTAs spill: 248 us; rings of 2,
 // 3, 4, 5 heads: 174, 169, 171, 174; a ring that runs on into the next tile: 185 against 182
 // then). One token of 64 sequences: 3.8 us on the GPU, two trips to memory; a call is the
